@@ -64,6 +64,8 @@ typedef struct CUstream_st *moe_stream_t; /* == cudaStream_t */
 #define MOE_WS_TIMEOUT 1   /* a bounded wait inside a kernel gave up           */
 #define MOE_WS_PLAN 2      /* a plan exceeded a kernel's capacity; work skipped */
 #define MOE_WS_TRIPLE 4    /* moe_slot_table_set met a triple outside the table */
+#define MOE_WS_INDEX 8     /* a slot, page, length or token read on the device lay outside its table */
+#define MOE_WS_NONFINITE 16 /* a value to be quantised or a logit was NaN or infinite                */
 
 /* Layer configuration ([moe_v41] struct MoeV41Cfg). norm_topk_prob is 0/1. */
 typedef struct {
@@ -453,6 +455,134 @@ int moe_fetch_host_images(void *source, int layer, int expert, void *slot_dev, u
  * headers; *layers_rerun (may be NULL) = layers run again. */
 int moe_graph_step_cached(void *graph, void *cache, int32_t *headers_host, int *layers_rerun,
                           moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Speculative decoding around the layer step: a quantised paged cache of keys
+ * and values, attention of drafted tokens over it, and their verification.
+ * The pages have no counterpart of these calls: a layer step of several tokens
+ * of one sequence (m > 1) needs tokens drafted ahead, and these judge them.
+ * All calls only enqueue on `stream`; bf16 as raw 16-bit patterns. */
+
+/* Formats of the cache: per 32 consecutive values of a row (one token, one kv
+ * head), clamped to +-60000 (NaN is held as 0 and sets MOE_WS_NONFINITE, as
+ * do infinities),
+ *   Q8: d = f16(max|x| / 127) rounded up, code = rint(x / d) + 128 in 8 bits,
+ *       value d * (code - 128);
+ *   Q4: m = f16(min x) rounded down, d = f16((max x - m) / 15) rounded up,
+ *       code = rint((x - m) / d) in 4 bits, value d * code + m
+ * (quotients in f32, rint to even, code 0 of the quotient where d = 0), so
+ * |x - value| <= d / 2. */
+#define MOE_KV_Q8 0
+#define MOE_KV_Q4 1
+
+#define MOE_MAX_DRAFT 64 /* query rows of one sequence in one call: the last token and 63 drafted */
+
+/* A cache of one layer: n_pages pages of page_size tokens, of which slot s is
+ * token s % page_size of page s / page_size. Per page, kv head and 16 tokens
+ * one block, blocks in that order (page, head, 16 tokens):
+ *   K codes [16 RB] | K scales | V codes [16 RB] | V scales,
+ * RB = head_dim (Q8) or head_dim / 2 (Q4) bytes. With t the token in the
+ * block, i a byte of its row and x a count of bytes, a code byte lies at
+ * x / 16 * 512 + lane * 16 + x % 16:
+ *   K: lane = t % 8 * 4 + i / (RB / 4), x = t / 8 * (RB / 4) + i % (RB / 4)
+ *   V: lane = i / (RB / 8) * 4 + t % 8 / 2,
+ *      x = (t / 8 * 2 + t % 2) * (RB / 8) + i % (RB / 8)
+ * Four bytes hold eight Q4 codes (a little-endian word), code c of them at bit
+ * c / 2 * 4 + c % 2 * 16. Scales are f16: K [t][group][d or d, m], V [d or
+ * d, m][group][t]. pages: device memory, 16-byte aligned, n_pages *
+ * moe_kv_page_bytes bytes. head_dim 64, 128 or 256; page_size a multiple of 16
+ * up to 1024; n_kv_heads 1 .. 256; n_pages * page_size below 2^31. */
+typedef struct {
+    void *pages;
+    int64_t n_pages;
+    int32_t head_dim, n_kv_heads, page_size, format;
+} moe_kv_cache;
+
+/* Bytes of one page (pages and n_pages of the struct are not looked at). */
+int moe_kv_page_bytes(const moe_kv_cache *cache, size_t *bytes);
+
+/* Quantises n_tokens rows of keys and values into the cache: token t's row of
+ * head h is k_dev + t * k_token_stride + h * k_head_stride (bf16, strides in
+ * elements, so views of a fused projection's output can be passed), written
+ * to slot slots_dev[t] (i32; -1: the token is skipped; the caller passes a
+ * slot at most once). Rows that start on 16-byte boundaries with strides that
+ * are multiples of 8 take the wider loads. *status_dev (NULL, or a device
+ * word) receives MOE_WS_INDEX for a slot outside the cache (skipped) and
+ * MOE_WS_NONFINITE. */
+int moe_kv_append(const moe_kv_cache *cache, const void *k_dev, int64_t k_token_stride, int64_t k_head_stride,
+                  const void *v_dev, int64_t v_token_stride, int64_t v_head_stride, const int32_t *slots_dev,
+                  int n_tokens, uint32_t *status_dev, moe_stream_t stream);
+
+/* Types of a call's floating-point argument. */
+#define MOE_BF16 0
+#define MOE_F32 1
+
+/* Reads rows back: k_out_dev, v_out_dev [n_tokens, n_kv_heads, head_dim] of
+ * out_type (MOE_BF16: rounded once; MOE_F32), 16-byte aligned; slot -1 (or one
+ * outside the cache, which sets MOE_WS_INDEX) gives zeros. */
+int moe_kv_read(const moe_kv_cache *cache, const int32_t *slots_dev, int n_tokens, void *k_out_dev,
+                void *v_out_dev, int out_type, uint32_t *status_dev, moe_stream_t stream);
+
+/* Attention of drafted tokens. Sequence b has the query rows (tokens)
+ * q_start_dev[b] .. q_start_dev[b + 1] - 1 (i32 [batch + 1], at most
+ * MOE_MAX_DRAFT rows each, n_tokens in all) and kv_len_dev[b] (i32) tokens in
+ * the cache, its query rows' own keys and values among them as the last ones;
+ * token j of it is in slot j % page_size of page
+ * table_dev[b * table_stride + j / page_size] (i32, table_pages entries a
+ * sequence). Query row i of the sequence sees the tokens before the sequence's
+ * query rows, and of those row j when bit j of mask_dev[q_start + i] (u64) is
+ * set; mask_dev NULL: rows 0 .. i (a chain). A single token: one row, mask_dev
+ * NULL. Per query head h, kv head h / (n_q_heads / n_kv_heads):
+ *   out = sum_j softmax_j(scale q . K_j | j seen) V_j,
+ * a row that sees nothing gives 0. Products of f16 roundings of the cache's
+ * values (2^-12 relative) and of the query's bf16 values scaled by a power of
+ * two, f32 sums; the softmax in f32, its weights rounded to f16 for the second
+ * product. q, out bf16, row stride *_token_stride and head stride
+ * *_head_stride in elements, dimensions contiguous. n_q_heads a multiple of
+ * n_kv_heads, at most 64 a kv head. ws_dev: moe_tree_attention_workspace_bytes
+ * bytes, initialised once (moe_workspace_init); moe_read_status gives
+ * MOE_WS_INDEX where lengths (the sequence's rows are 0), or a page (its
+ * tokens are not seen) lay outside. batch 0 .. 1024. */
+int moe_tree_attention_workspace_bytes(const moe_kv_cache *cache, int n_q_heads, int batch, int n_tokens,
+                                       size_t *bytes);
+int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_token_stride, int64_t q_head_stride,
+                       void *out_dev, int64_t out_token_stride, int64_t out_head_stride, int n_q_heads,
+                       const int32_t *q_start_dev, const int32_t *kv_len_dev, const int32_t *table_dev,
+                       int64_t table_stride, int table_pages, const uint64_t *mask_dev, int batch, int n_tokens,
+                       float scale, void *ws_dev, size_t ws_bytes, moe_stream_t stream);
+
+/* Verification of drafted tokens from given random numbers. Sequence b has
+ * rows q_start_dev[b] .. q_start_dev[b + 1] - 1 of logits (logits_type;
+ * n_rows rows of vocab values, row stride logits_stride elements): row 0 of
+ * its last accepted token, row j of drafted node j (at most MOE_MAX_DRAFT
+ * rows). tokens_dev i32 [n_rows]: node j's token (row 0's is not read);
+ * parents_dev i32 [n_rows]: node j's parent, an earlier row of the sequence
+ * (NULL: j - 1, a chain); draft_dev f32 [n_rows, vocab], row stride
+ * draft_stride: the probabilities that node j's token was drawn from (NULL:
+ * the token was chosen, not drawn). Let p_j = softmax(logits_j /
+ * temperature_dev[b]) (NULL: 1; not above 0: all on the largest logit, the
+ * lowest index of equals). From cur = 0, r = p_0, Z = 1, for j = 1 .. in order
+ * where parent_j = cur: with x = token_j and q = draft row j (NULL: 1 at x),
+ *   uniforms_dev[row j] * Z * q(x) < r(x): accepted, cur = j, r = p_j, Z = 1;
+ *   else r = max(r - Z q, 0), Z = sum r.
+ * next_token = the index of the largest r(i) / noise_dev[b * noise_stride + i]
+ * (lowest of equals; r = p_cur where Z = 0): with noise from the exponential
+ * distribution a sample of r / Z, so that the tokens follow the target's
+ * distribution whatever the draft's. uniforms_dev f32 [n_rows] in [0, 1),
+ * noise_dev f32 [batch, vocab] > 0; both NULL: every sequence greedy.
+ * Outputs: n_accepted_dev i32 [batch]; path_dev i32 [n_rows], the accepted
+ * nodes of sequence b from q_start[b] on, then -1; next_token_dev i32 [batch]
+ * (-1 where the last row has no finite logit, or no rows). A logit of NaN or
+ * +infinity counts as -infinity and sets MOE_WS_NONFINITE, a token outside the
+ * vocabulary is passed over and sets MOE_WS_INDEX. ws_dev: initialised once.
+ * batch 0 .. 65535, vocab 1 .. 2^24. */
+int moe_spec_verify_workspace_bytes(int batch, int n_rows, size_t *bytes);
+int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stride, const int32_t *q_start_dev,
+                    const int32_t *tokens_dev, const int32_t *parents_dev, const float *draft_dev,
+                    int64_t draft_stride, const float *temperature_dev, const float *uniforms_dev,
+                    const float *noise_dev, int64_t noise_stride, int batch, int n_rows, int vocab,
+                    int32_t *n_accepted_dev, int32_t *path_dev, int32_t *next_token_dev, void *ws_dev,
+                    size_t ws_bytes, moe_stream_t stream);
 
 /* Last error message of the calling thread ("" if none). */
 const char *moe_last_error(void);

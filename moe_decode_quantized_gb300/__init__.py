@@ -21,6 +21,13 @@ MOE_HDR_NONFINITE = 2
 MOE_WS_TIMEOUT = 1
 MOE_WS_PLAN = 2
 MOE_WS_TRIPLE = 4
+MOE_WS_INDEX = 8
+MOE_WS_NONFINITE = 16
+MOE_KV_Q8 = 0
+MOE_KV_Q4 = 1
+MOE_MAX_DRAFT = 64
+MOE_BF16 = 0
+MOE_F32 = 1
 MOE_SHARED_BF16 = 0
 MOE_SHARED_KQUANT = 1
 MOE_GRAPH_SNAPSHOTS = 1
@@ -33,7 +40,9 @@ __all__ = ["Config", "Arena", "Layer", "MoeError", "header_words", "workspace_by
            "swiglu_q8", "layer_step", "host_io_bytes", "layer_step_host", "workspace_view",
            "read_status", "layer_step_profiled", "layer_step_static", "route_scores", "set_wait_limit_ns",
            "expert_step_unreleased", "gemm_bf16", "prefill_workspace_bytes", "prefill_step", "prefill_step_profiled", "prefill_status", "graph_snapshot_bytes", "HostSource",
-           "ExpertCache", "slot_table_set", "dedupe_triples", "parse_header", "Graph"]
+           "ExpertCache", "slot_table_set", "dedupe_triples", "parse_header", "Graph",
+           "KvCache", "kv_page_bytes", "kv_append", "kv_read", "tree_attention_workspace_bytes", "tree_attention",
+           "spec_verify_workspace_bytes", "spec_verify"]
 
 
 class MoeError(RuntimeError):
@@ -422,3 +431,152 @@ class Graph:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------------------------ speculative decoding
+
+def _strided(t, name, dims):
+    """Device address of a tensor whose last dimension alone must be contiguous."""
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return C.c_void_p(t.data_ptr())
+
+
+def _typed(t, name, *dtypes):
+    if t is not None and hasattr(t, "dtype") and str(t.dtype).replace("torch.", "") not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(dtypes)}, not {t.dtype}")
+    return t
+
+
+def _count(t, name, n):
+    if t is not None and hasattr(t, "numel") and t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} values, {n} are needed")
+    return t
+
+
+@dataclass
+class KvCache:
+    """A paged cache of quantised keys and values (include/moe.h, moe_kv_cache).
+    pages: uint8 device tensor of whole pages (kv_page_bytes each)."""
+    pages: object
+    head_dim: int
+    n_kv_heads: int
+    page_size: int = 64
+    format: int = MOE_KV_Q8
+
+    def __post_init__(self):
+        self.n_pages = 0
+        per = kv_page_bytes(self)
+        if self.pages is not None:
+            size = self.pages.numel() * self.pages.element_size()
+            if size % per:
+                raise ValueError(f"pages holds {size} bytes, not a multiple of a page's {per}")
+            self.n_pages = size // per
+
+    def c(self) -> _lib.MoeKvCache:
+        return _lib.MoeKvCache(_ptr(self.pages), self.n_pages, self.head_dim, self.n_kv_heads, self.page_size,
+                               self.format)
+
+
+def kv_page_bytes(cache: KvCache) -> int:
+    b = C.c_size_t(0)
+    c = _lib.MoeKvCache(None, 0, cache.head_dim, cache.n_kv_heads, cache.page_size, cache.format)
+    _check(_lib.moe().moe_kv_page_bytes(C.byref(c), C.byref(b)))
+    return b.value
+
+
+def _rows(cache: KvCache, t, name, heads):
+    _typed(t, name, "bfloat16", "int16", "uint16")
+    p = _strided(t, name, 3)
+    if t.shape[1] != heads or t.shape[2] != cache.head_dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {cache.head_dim}], not {list(t.shape)}")
+    return p, t.stride(0), t.stride(1)
+
+
+def kv_append(cache: KvCache, k, v, slots, status=None, stream=None):
+    """Quantise rows k, v (bf16 [tokens, n_kv_heads, head_dim], any strides of the
+    first two) into slots (int32 [tokens], -1: skipped). status: None, or a
+    device word that receives MOE_WS_* bits."""
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have the same number of tokens")
+    _count(_typed(slots, "slots", "int32"), "slots", k.shape[0])
+    _check(_lib.moe().moe_kv_append(C.byref(cache.c()), *_rows(cache, k, "k", cache.n_kv_heads),
+                                    *_rows(cache, v, "v", cache.n_kv_heads), _ptr(slots), k.shape[0],
+                                    _ptr(status), _stream(stream)))
+
+
+def kv_read(cache: KvCache, slots, k_out, v_out, status=None, stream=None):
+    """Rows of the cache as numbers: k_out, v_out bf16 or f32 [tokens, n_kv_heads, head_dim]."""
+    n = slots.numel()
+    _typed(slots, "slots", "int32")
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        _count(_typed(t, name, "bfloat16", "float32"), name, n * cache.n_kv_heads * cache.head_dim)
+    if k_out.dtype != v_out.dtype:
+        raise ValueError("k_out and v_out must have the same type")
+    kind = MOE_F32 if "float32" in str(k_out.dtype) else MOE_BF16
+    _check(_lib.moe().moe_kv_read(C.byref(cache.c()), _ptr(slots), n, _ptr(k_out), _ptr(v_out), kind, _ptr(status),
+                                  _stream(stream)))
+
+
+def tree_attention_workspace_bytes(cache: KvCache, n_q_heads: int, batch: int, n_tokens: int) -> int:
+    b = C.c_size_t(0)
+    _check(_lib.moe().moe_tree_attention_workspace_bytes(C.byref(cache.c()), n_q_heads, batch, n_tokens,
+                                                         C.byref(b)))
+    return b.value
+
+
+def tree_attention(cache: KvCache, q, out, q_start, kv_len, table, mask, scale: float, ws, stream=None):
+    """Attention of each sequence's drafted tokens over the cache (include/moe.h,
+    moe_tree_attention): q, out bf16 [tokens, n_q_heads, head_dim], q_start int32
+    [batch + 1], kv_len int32 [batch], table int32 [batch, pages], mask int64
+    [tokens] of bits, or None for chains and single tokens."""
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    heads, n, batch = q.shape[1], q.shape[0], kv_len.numel()
+    for t, name in ((q_start, "q_start"), (kv_len, "kv_len"), (table, "table")):
+        _typed(t, name, "int32")
+    _count(q_start, "q_start", batch + 1)
+    _count(_typed(mask, "mask", "int64", "uint64"), "mask", n)
+    tp = _strided(table, "table", 2)
+    if table.shape[0] < batch:
+        raise ValueError(f"table has {table.shape[0]} rows for {batch} sequences")
+    _check(_lib.moe().moe_tree_attention(C.byref(cache.c()), *_rows(cache, q, "q", heads),
+                                         *_rows(cache, out, "out", heads), heads, _ptr(q_start), _ptr(kv_len), tp,
+                                         table.stride(0), table.shape[1], _ptr(mask), batch, n, float(scale),
+                                         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def spec_verify_workspace_bytes(batch: int, n_rows: int) -> int:
+    b = C.c_size_t(0)
+    _check(_lib.moe().moe_spec_verify_workspace_bytes(batch, n_rows, C.byref(b)))
+    return b.value
+
+
+def spec_verify(logits, q_start, tokens, parents, draft, temperature, uniforms, noise, n_accepted, path, next_token,
+                ws, stream=None):
+    """Verify drafted tokens from given random numbers (include/moe.h, moe_spec_verify):
+    logits bf16 or f32 [rows, vocab], draft f32 [rows, vocab] or None, noise f32
+    [batch, vocab]; the other inputs as there. Outputs int32: n_accepted [batch],
+    path [rows], next_token [batch]."""
+    _typed(logits, "logits", "bfloat16", "float32")
+    lp = _strided(logits, "logits", 2)
+    rows, vocab = logits.shape
+    batch = next_token.numel()
+    for t, name, n in ((q_start, "q_start", batch + 1), (tokens, "tokens", rows), (parents, "parents", rows),
+                       (n_accepted, "n_accepted", batch), (path, "path", rows), (next_token, "next_token", batch)):
+        _count(_typed(t, name, "int32"), name, n)
+    for t, name, n in ((temperature, "temperature", batch), (uniforms, "uniforms", rows)):
+        _count(_typed(t, name, "float32"), name, n)
+    for t, name, n in ((draft, "draft", rows), (noise, "noise", batch)):
+        if _typed(t, name, "float32") is not None and (t.dim() != 2 or t.shape[0] < n or t.shape[1] != vocab):
+            raise ValueError(f"{name} must be [{n}, {vocab}], not {list(t.shape)}")
+    dp = None if draft is None else _strided(draft, "draft", 2)
+    np_ = None if noise is None else _strided(noise, "noise", 2)
+    _check(_lib.moe().moe_spec_verify(lp, MOE_F32 if "float32" in str(logits.dtype) else MOE_BF16,
+                                      logits.stride(0), _ptr(q_start), _ptr(tokens), _ptr(parents), dp,
+                                      0 if draft is None else draft.stride(0), _ptr(temperature), _ptr(uniforms),
+                                      np_, 0 if noise is None else noise.stride(0), batch, rows, vocab,
+                                      _ptr(n_accepted), _ptr(path), _ptr(next_token), _ptr(ws),
+                                      ws.numel() * ws.element_size(), _stream(stream)))

@@ -15,6 +15,7 @@ _synth = None
 
 P = C.c_void_p
 I32 = C.c_int32
+I64 = C.c_int64
 U64 = C.c_uint64
 SZ = C.c_size_t
 
@@ -33,6 +34,11 @@ class MoeArena(C.Structure):
 class MoeLayer(C.Structure):
     _fields_ = [("router_w", P), ("bias", P), ("slot_row", P), ("sh_w1", P), ("sh_w3", P),
                 ("sh_w2", P), ("sh_format", C.c_int32)]
+
+
+class MoeKvCache(C.Structure):
+    _fields_ = [("pages", P), ("n_pages", C.c_int64), ("head_dim", I32), ("n_kv_heads", I32),
+                ("page_size", I32), ("format", I32)]
 
 
 class MoeWsView(C.Structure):
@@ -95,6 +101,16 @@ MOE_SYMBOLS = {
     "moe_prefill_step_profiled": (C.c_int, [C.POINTER(MoeCfg), C.POINTER(MoeLayer), C.POINTER(MoeArena),
                                             C.c_int64, P, P, P, P, P, C.c_int, P, SZ, P, P]),
     "moe_prefill_status": (C.c_int, [C.POINTER(MoeCfg), C.c_int, P, C.POINTER(C.c_uint32), P]),
+    "moe_kv_page_bytes": (C.c_int, [C.POINTER(MoeKvCache), C.POINTER(SZ)]),
+    "moe_kv_append": (C.c_int, [C.POINTER(MoeKvCache), P, I64, I64, P, I64, I64, P, C.c_int, P, P]),
+    "moe_kv_read": (C.c_int, [C.POINTER(MoeKvCache), P, C.c_int, P, P, C.c_int, P, P]),
+    "moe_tree_attention_workspace_bytes": (C.c_int, [C.POINTER(MoeKvCache), C.c_int, C.c_int, C.c_int,
+                                                     C.POINTER(SZ)]),
+    "moe_tree_attention": (C.c_int, [C.POINTER(MoeKvCache), P, I64, I64, P, I64, I64, C.c_int, P, P, P, I64,
+                                     C.c_int, P, C.c_int, C.c_int, C.c_float, P, SZ, P]),
+    "moe_spec_verify_workspace_bytes": (C.c_int, [C.c_int, C.c_int, C.POINTER(SZ)]),
+    "moe_spec_verify": (C.c_int, [P, C.c_int, I64, P, P, P, P, I64, P, P, P, I64, C.c_int, C.c_int, C.c_int, P, P,
+                                  P, P, SZ, P]),
     "moe_last_error": (C.c_char_p, []),
 }
 

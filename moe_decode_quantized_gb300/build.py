@@ -1,11 +1,12 @@
 """Builds the in-tree CUDA libraries for sm_103a with nvcc.
 
-libmoe.so        the engine (csrc/moe_abi.cu and the kernels it includes)
+libmoe.so        the engine (csrc/moe_abi.cu, csrc/moe_spec.cu and the kernels
+                 they include)
 libmoe_synth.so  the device twin of the synthetic-input generator
 
-Both are compiled in parallel, one -gencode (compute_103a / sm_103a), -O3,
--lineinfo, no fast-math; a library is rebuilt when a source or header is
-newer than it.
+The sources are compiled in parallel, one -gencode (compute_103a / sm_103a),
+-O3, -lineinfo, no fast-math, and each library linked from its objects; a
+library is rebuilt when a source or header is newer than it.
 """
 from __future__ import annotations
 
@@ -22,7 +23,8 @@ LIBMOE = os.path.join(PKG, "libmoe.so")
 LIBSYNTH = os.path.join(PKG, "libmoe_synth.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared", "-cudart", "static"]
+FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC"]
+LINK = ["-shared", "-Xcompiler", "-fPIC", "-cudart", "static"]
 
 
 def _nvcc() -> str:
@@ -42,29 +44,40 @@ def _stale(out: str, deps) -> bool:
 def targets():
     hdrs = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     return [
-        (LIBMOE, os.path.join(CSRC, "moe_abi.cu"), hdrs),
-        (LIBSYNTH, os.path.join(CSRC, "moe_synth.cu"), [os.path.join(INCLUDE, "moe_synth.h")]),
+        (LIBMOE, [os.path.join(CSRC, f) for f in ("moe_abi.cu", "moe_spec.cu")], hdrs),
+        (LIBSYNTH, [os.path.join(CSRC, "moe_synth.cu")], [os.path.join(INCLUDE, "moe_synth.h")]),
     ]
+
+
+def _run(cmds):
+    """Runs the commands in parallel; the failed ones' output."""
+    procs = [(c, subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)) for c in cmds]
+    logs = [(c, p.communicate()[0], p.returncode) for c, p in procs]
+    return [f"{' '.join(c)}\n{log}" for c, log, rc in logs if rc != 0]
 
 
 def build(force: bool = False, extra_flags=()) -> list:
     """Compile every stale library; returns the list of library paths."""
-    procs = []
-    for out, src, hdrs in targets():
-        if force or _stale(out, [src] + hdrs):
-            tmp = out + f".tmp{os.getpid()}"
-            cmd = [_nvcc()] + ARCH + FLAGS + list(extra_flags) + ["-o", tmp, src]
-            procs.append((out, tmp, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE,
-                                                          stderr=subprocess.STDOUT, text=True)))
-    errors = []
-    for out, tmp, cmd, p in procs:
-        log, _ = p.communicate()
-        if p.returncode != 0:
-            errors.append(f"{' '.join(cmd)}\n{log}")
-        else:
+    stale = [t for t in targets() if force or _stale(t[0], t[1] + t[2])]
+    nvcc, pid = _nvcc(), os.getpid()
+    compiles, links, objects, moves = [], [], [], []
+    for out, srcs, _ in stale:
+        objs = [f"{out}.{os.path.basename(s)}.tmp{pid}.o" for s in srcs]
+        objects += objs
+        compiles += [[nvcc] + ARCH + FLAGS + list(extra_flags) + ["-c", "-o", o, s] for s, o in zip(srcs, objs)]
+        tmp = out + f".tmp{pid}"
+        links.append([nvcc] + ARCH + LINK + ["-o", tmp] + objs)
+        moves.append((tmp, out))
+    try:
+        errors = _run(compiles) or _run(links)
+        if errors:
+            raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
+        for tmp, out in moves:
             os.replace(tmp, out)
-    if errors:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
+    finally:
+        for o in objects:
+            if os.path.exists(o):
+                os.unlink(o)
     return [t[0] for t in targets()]
 
 

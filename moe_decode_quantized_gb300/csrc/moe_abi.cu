@@ -16,6 +16,7 @@
 #include "moe_slot.cuh"
 #include "moe_prefill.cuh"
 #include "moe_runtime.cuh"
+#include "moe_host.cuh"
 
 using namespace moe;
 
@@ -804,6 +805,18 @@ struct HostSource {
 };
 
 }  // namespace
+
+// the message and the wait bound for the library's other translation units
+int moe::host_fail(int code, const char *fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return code;
+}
+
+unsigned long long moe::host_wait_ns() { return g_wait_ns.load(); }
 
 // ==================================================================== C ABI
 

@@ -1,0 +1,293 @@
+// moe_spec.cu -- the entry points of libmoe.so for speculative decoding
+// (declared and documented in include/moe.h): the quantised cache, attention
+// of drafted tokens over it and their verification. Argument checks,
+// workspace layout and launches.
+#include <algorithm>
+
+#include "moe_common.cuh"
+#include "moe_host.cuh"
+#include "moe_kv.cuh"
+#include "moe_tree_attn.cuh"
+#include "moe_verify.cuh"
+
+using namespace moe;
+
+namespace {
+
+#define SPEC_CUDA_OK(expr)                                                                              \
+    do {                                                                                                \
+        cudaError_t e_ = (expr);                                                                        \
+        if (e_ != cudaSuccess)                                                                          \
+            return host_fail(MOE_ECUDA, "%s: %s (%s)", #expr, cudaGetErrorString(e_), cudaGetErrorName(e_)); \
+    } while (0)
+
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+#define SPEC_CTRL_BYTES 256  // control words: the status is word MOE_CTRL_STATUS
+
+int check_shape(const moe_kv_cache *c, KvDims &k)
+{
+    if (!c)
+        return host_fail(MOE_EINVAL, "cache is NULL");
+    if (c->format != MOE_KV_Q8 && c->format != MOE_KV_Q4)
+        return host_fail(MOE_EINVAL, "cache format %d", c->format);
+    if (c->head_dim < 1 || c->n_kv_heads < 1 || c->page_size < 1)
+        return host_fail(MOE_EINVAL, "head_dim (%d), n_kv_heads (%d) and page_size (%d) must be positive", c->head_dim,
+                         c->n_kv_heads, c->page_size);
+    if ((c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) || c->n_kv_heads > 256 ||
+        c->page_size % MOE_KV_BLOCK || c->page_size > 1024)
+        return host_fail(MOE_EUNSUPPORTED, "head_dim (%d) of 64, 128 or 256, n_kv_heads (%d) <= 256, page_size (%d) a "
+                         "multiple of 16 up to 1024", c->head_dim, c->n_kv_heads, c->page_size);
+    k.dim = c->head_dim;
+    k.heads = c->n_kv_heads;
+    k.page = c->page_size;
+    k.fmt = c->format;
+    return MOE_OK;
+}
+
+int check_cache(const moe_kv_cache *c, KvDims &k)
+{
+    const int rc = check_shape(c, k);
+    if (rc)
+        return rc;
+    if (!c->pages || !aligned(c->pages, 16))
+        return host_fail(MOE_EINVAL, "the cache's pages are NULL or not 16-byte aligned");
+    if (c->n_pages < 1 || c->n_pages > 0x7FFFFFFFll / c->page_size)
+        return host_fail(MOE_EINVAL, "n_pages (%lld) must be positive and n_pages * page_size below 2^31",
+                         (long long)c->n_pages);
+    return MOE_OK;
+}
+
+// one thread per eight values of the K and V rows of n tokens
+int row_grid(const KvDims &k, int n, unsigned &grid)
+{
+    const long long blocks = (2ll * n * k.heads * (k.dim / 8) + 255) / 256;
+    if (blocks > 0x7FFFFFFFll)
+        return host_fail(MOE_EUNSUPPORTED, "%d tokens in one call", n);
+    grid = (unsigned)blocks;
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_kv_page_bytes(const moe_kv_cache *cache, size_t *bytes)
+{
+    KvDims k;
+    const int rc = check_shape(cache, k);
+    if (rc)
+        return rc;
+    if (!bytes)
+        return host_fail(MOE_EINVAL, "bytes is NULL");
+    *bytes = k.page_bytes();
+    return MOE_OK;
+}
+
+int moe_kv_append(const moe_kv_cache *cache, const void *k_dev, int64_t k_token_stride, int64_t k_head_stride,
+                  const void *v_dev, int64_t v_token_stride, int64_t v_head_stride, const int32_t *slots_dev,
+                  int n_tokens, uint32_t *status_dev, moe_stream_t stream)
+{
+    KvArgs a{};
+    int rc = check_cache(cache, a.k);
+    if (rc)
+        return rc;
+    if (n_tokens < 0 || (n_tokens > 0 && (!k_dev || !v_dev || !slots_dev)))
+        return host_fail(MOE_EINVAL, "moe_kv_append: NULL argument or n_tokens (%d) < 0", n_tokens);
+    if (!aligned(k_dev, 2) || !aligned(v_dev, 2) || !aligned(slots_dev, 4) || !aligned(status_dev, 4))
+        return host_fail(MOE_EINVAL, "moe_kv_append: an argument is not aligned to its type");
+    if (n_tokens == 0)
+        return MOE_OK;
+    unsigned grid;
+    if ((rc = row_grid(a.k, n_tokens, grid)))
+        return rc;
+    a.pages = static_cast<uint8_t *>(cache->pages);
+    a.n_slots = cache->n_pages * cache->page_size;
+    a.src[0] = static_cast<const uint16_t *>(k_dev);
+    a.src[1] = static_cast<const uint16_t *>(v_dev);
+    a.tok_stride[0] = k_token_stride;
+    a.tok_stride[1] = v_token_stride;
+    a.head_stride[0] = k_head_stride;
+    a.head_stride[1] = v_head_stride;
+    a.slots = slots_dev;
+    a.tokens = n_tokens;
+    a.status = status_dev;
+    const bool wide = aligned(k_dev, 16) && aligned(v_dev, 16) &&
+                      (k_token_stride | k_head_stride | v_token_stride | v_head_stride) % 8 == 0;
+    (wide ? moe_kv_append_kernel<true> : moe_kv_append_kernel<false>)<<<grid, 256, 0, (cudaStream_t)stream>>>(a);
+    SPEC_CUDA_OK(cudaGetLastError());
+    return MOE_OK;
+}
+
+int moe_kv_read(const moe_kv_cache *cache, const int32_t *slots_dev, int n_tokens, void *k_out_dev, void *v_out_dev,
+                int out_type, uint32_t *status_dev, moe_stream_t stream)
+{
+    KvArgs a{};
+    int rc = check_cache(cache, a.k);
+    if (rc)
+        return rc;
+    if (n_tokens < 0 || (n_tokens > 0 && (!k_out_dev || !v_out_dev || !slots_dev)))
+        return host_fail(MOE_EINVAL, "moe_kv_read: NULL argument or n_tokens (%d) < 0", n_tokens);
+    if (out_type != MOE_BF16 && out_type != MOE_F32)
+        return host_fail(MOE_EINVAL, "moe_kv_read: out_type %d", out_type);
+    if (!aligned(k_out_dev, 16) || !aligned(v_out_dev, 16) || !aligned(slots_dev, 4) || !aligned(status_dev, 4))
+        return host_fail(MOE_EINVAL, "moe_kv_read: outputs must be 16-byte aligned, slots and status 4-byte");
+    if (n_tokens == 0)
+        return MOE_OK;
+    unsigned grid;
+    if ((rc = row_grid(a.k, n_tokens, grid)))
+        return rc;
+    a.pages = static_cast<uint8_t *>(cache->pages);
+    a.n_slots = cache->n_pages * cache->page_size;
+    a.slots = slots_dev;
+    a.out[0] = k_out_dev;
+    a.out[1] = v_out_dev;
+    a.out_f32 = out_type == MOE_F32;
+    a.tokens = n_tokens;
+    a.status = status_dev;
+    moe_kv_read_kernel<<<grid, 256, 0, (cudaStream_t)stream>>>(a);
+    SPEC_CUDA_OK(cudaGetLastError());
+    return MOE_OK;
+}
+
+static int tree_ws(const moe_kv_cache *cache, int n_q_heads, int batch, int n_tokens, KvDims &k, size_t &bytes)
+{
+    const int rc = check_shape(cache, k);
+    if (rc)
+        return rc;
+    if (n_q_heads < 1 || n_q_heads % k.heads || batch < 0 || n_tokens < 0)
+        return host_fail(MOE_EINVAL, "n_q_heads (%d) must be a positive multiple of n_kv_heads (%d), batch (%d) and "
+                         "n_tokens (%d) not negative", n_q_heads, k.heads, batch, n_tokens);
+    if (n_q_heads / k.heads > 64 || batch > 1024 || n_tokens > batch * MOE_MAX_DRAFT)
+        return host_fail(MOE_EUNSUPPORTED, "n_q_heads / n_kv_heads (%d) <= 64, batch (%d) <= 1024, n_tokens (%d) <= "
+                         "%d a sequence", n_q_heads / k.heads, batch, n_tokens, MOE_MAX_DRAFT);
+    bytes = SPEC_CTRL_BYTES;
+    return MOE_OK;
+}
+
+int moe_tree_attention_workspace_bytes(const moe_kv_cache *cache, int n_q_heads, int batch, int n_tokens,
+                                       size_t *bytes)
+{
+    if (!bytes)
+        return host_fail(MOE_EINVAL, "bytes is NULL");
+    KvDims k;
+    return tree_ws(cache, n_q_heads, batch, n_tokens, k, *bytes);
+}
+
+int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_token_stride, int64_t q_head_stride,
+                       void *out_dev, int64_t out_token_stride, int64_t out_head_stride, int n_q_heads,
+                       const int32_t *q_start_dev, const int32_t *kv_len_dev, const int32_t *table_dev,
+                       int64_t table_stride, int table_pages, const uint64_t *mask_dev, int batch, int n_tokens,
+                       float scale, void *ws_dev, size_t ws_bytes, moe_stream_t stream)
+{
+    TreeArgs a{};
+    int rc = check_cache(cache, a.k);
+    if (rc)
+        return rc;
+    size_t need;
+    if ((rc = tree_ws(cache, n_q_heads, batch, n_tokens, a.k, need)))
+        return rc;
+    if (batch == 0 || n_tokens == 0)
+        return MOE_OK;
+    if (!q_dev || !out_dev || !q_start_dev || !kv_len_dev || !table_dev || !ws_dev)
+        return host_fail(MOE_EINVAL, "moe_tree_attention: NULL argument");
+    if (!aligned(q_dev, 2) || !aligned(out_dev, 2) || !aligned(q_start_dev, 4) || !aligned(kv_len_dev, 4) ||
+        !aligned(table_dev, 4) || !aligned(mask_dev, 8) || !aligned(ws_dev, 256))
+        return host_fail(MOE_EINVAL, "moe_tree_attention: an argument is not aligned to its type, or ws_dev not to 256 "
+                         "bytes");
+    if (ws_bytes < need)
+        return host_fail(MOE_EINVAL, "moe_tree_attention: the workspace holds %zu bytes, %zu are needed", ws_bytes, need);
+    if (table_pages < 1 || (batch > 1 && table_stride < table_pages) || !(scale >= -3.0e38f && scale <= 3.0e38f))
+        return host_fail(MOE_EINVAL, "moe_tree_attention: table_pages (%d) must be positive and at most table_stride "
+                         "(%lld), scale finite", table_pages, (long long)table_stride);
+    a.pages = static_cast<const uint8_t *>(cache->pages);
+    a.n_pages = (int)cache->n_pages;
+    a.q = static_cast<const uint16_t *>(q_dev);
+    a.q_tok = q_token_stride;
+    a.q_head = q_head_stride;
+    a.out = static_cast<uint16_t *>(out_dev);
+    a.o_tok = out_token_stride;
+    a.o_head = out_head_stride;
+    a.q_start = q_start_dev;
+    a.kv_len = kv_len_dev;
+    a.table = table_dev;
+    a.table_stride = table_stride;
+    a.table_pages = table_pages;
+    a.mask = reinterpret_cast<const unsigned long long *>(mask_dev);
+    a.batch = batch;
+    a.tokens = n_tokens;
+    a.q_heads = n_q_heads;
+    a.scale = scale;
+    a.ctrl = static_cast<uint32_t *>(ws_dev);
+    const int rows = n_tokens * n_q_heads;
+    moe_tree_attn_kernel<<<(rows + 3) / 4, 128, 0, (cudaStream_t)stream>>>(a);
+    SPEC_CUDA_OK(cudaGetLastError());
+    return MOE_OK;
+}
+
+int moe_spec_verify_workspace_bytes(int batch, int n_rows, size_t *bytes)
+{
+    if (!bytes || batch < 0 || n_rows < 0)
+        return host_fail(MOE_EINVAL, "moe_spec_verify_workspace_bytes: bad arguments");
+    if (batch > 65535)
+        return host_fail(MOE_EUNSUPPORTED, "batch (%d) <= 65535", batch);
+    *bytes = SPEC_CTRL_BYTES;
+    return MOE_OK;
+}
+
+int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stride, const int32_t *q_start_dev,
+                    const int32_t *tokens_dev, const int32_t *parents_dev, const float *draft_dev, int64_t draft_stride,
+                    const float *temperature_dev, const float *uniforms_dev, const float *noise_dev, int64_t noise_stride,
+                    int batch, int n_rows, int vocab, int32_t *n_accepted_dev, int32_t *path_dev,
+                    int32_t *next_token_dev, void *ws_dev, size_t ws_bytes, moe_stream_t stream)
+{
+    size_t need;
+    int rc = moe_spec_verify_workspace_bytes(batch, n_rows, &need);
+    if (rc)
+        return rc;
+    if (logits_type != MOE_BF16 && logits_type != MOE_F32)
+        return host_fail(MOE_EINVAL, "moe_spec_verify: logits_type %d", logits_type);
+    if (vocab < 1 || vocab > (1 << 24))
+        return host_fail(vocab < 1 ? MOE_EINVAL : MOE_EUNSUPPORTED, "moe_spec_verify: vocab (%d) of 1 .. 2^24", vocab);
+    if (batch == 0)
+        return MOE_OK;
+    if (!logits_dev || !q_start_dev || !tokens_dev || !n_accepted_dev || !path_dev || !next_token_dev || !ws_dev)
+        return host_fail(MOE_EINVAL, "moe_spec_verify: NULL argument");
+    if ((uniforms_dev == nullptr) != (noise_dev == nullptr))
+        return host_fail(MOE_EINVAL, "moe_spec_verify: uniforms and noise go together");
+    if (!aligned(logits_dev, logits_type == MOE_F32 ? 4 : 2) || !aligned(q_start_dev, 4) || !aligned(tokens_dev, 4) ||
+        !aligned(parents_dev, 4) || !aligned(draft_dev, 4) || !aligned(temperature_dev, 4) || !aligned(uniforms_dev, 4) ||
+        !aligned(noise_dev, 4) || !aligned(n_accepted_dev, 4) || !aligned(path_dev, 4) || !aligned(next_token_dev, 4) ||
+        !aligned(ws_dev, 256))
+        return host_fail(MOE_EINVAL, "moe_spec_verify: an argument is not aligned to its type, or ws_dev not to 256 bytes");
+    if ((n_rows > 1 && (logits_stride < vocab || (draft_dev && draft_stride < vocab))) ||
+        (batch > 1 && noise_dev && noise_stride < vocab))
+        return host_fail(MOE_EINVAL, "moe_spec_verify: a row stride is below vocab (%d)", vocab);
+    if (ws_bytes < need)
+        return host_fail(MOE_EINVAL, "moe_spec_verify: the workspace holds %zu bytes, %zu are needed", ws_bytes, need);
+    VerifyArgs a{};
+    a.logits = logits_dev;
+    a.f32 = logits_type == MOE_F32;
+    a.stride = logits_stride;
+    a.q_start = q_start_dev;
+    a.tokens = tokens_dev;
+    a.parents = parents_dev;
+    a.draft = draft_dev;
+    a.draft_stride = draft_stride;
+    a.temperature = temperature_dev;
+    a.uniforms = uniforms_dev;
+    a.noise = noise_dev;
+    a.noise_stride = noise_stride;
+    a.batch = batch;
+    a.rows = n_rows;
+    a.vocab = vocab;
+    a.n_accepted = n_accepted_dev;
+    a.path = path_dev;
+    a.next = next_token_dev;
+    a.ctrl = static_cast<uint32_t *>(ws_dev);
+    moe_verify_kernel<<<batch, MOE_VERIFY_THREADS, 0, (cudaStream_t)stream>>>(a);
+    SPEC_CUDA_OK(cudaGetLastError());
+    return MOE_OK;
+}
+
+}  // extern "C"
