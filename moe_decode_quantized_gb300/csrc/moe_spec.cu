@@ -3,6 +3,7 @@
 // of drafted tokens over it and their verification. Argument checks,
 // workspace layout and launches.
 #include <algorithm>
+#include <mutex>
 
 #include "moe_common.cuh"
 #include "moe_host.cuh"
@@ -65,6 +66,80 @@ int row_grid(const KvDims &k, int n, unsigned &grid)
     if (blocks > 0x7FFFFFFFll)
         return host_fail(MOE_EUNSUPPORTED, "%d tokens in one call", n);
     grid = (unsigned)blocks;
+    return MOE_OK;
+}
+
+// ---- tree attention: instances and their launch shape
+
+using TreeKernel = void (*)(TreeArgs, int);
+
+struct TreeInstance {
+    TreeKernel kernel;
+    int rows;         // rows of a row block
+    size_t fixed, stage, part;  // bytes of shared memory (beside the ring, a stage of all warps); floats of a partial
+    int stages, ctas;  // found at the first use on a device
+};
+
+template <int FMT, int D, int MT>
+TreeInstance tree_instance()
+{
+    using T = TreeShape<FMT, D, MT>;
+    return {moe_tree_attn_kernel<FMT, D, MT>, T::ROWS, (size_t)T::fixed(), (size_t)MOE_TREE_WARPS * T::BLOCK, T::PART, 0, 0};
+}
+
+#define MOE_TREE_MAX_GRID 640  // runs; the workspace holds two partials each
+#define MOE_TREE_MAX_DEVICES 64
+
+std::mutex g_tree_mu;
+
+// the instance for (format, head size) with at least `rows` rows a block where there is one, else the largest
+int tree_choose(int fmt, int dim, int rows)
+{
+    const int mt = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;
+    const int first = dim == 64 ? 0 : dim == 128 ? 3 : 5, most = dim == 64 ? 2 : dim == 128 ? 1 : 0;
+    return (fmt == MOE_KV_Q8 ? 0 : 6) + first + std::min(mt, most);
+}
+
+int tree_get(int index, int &sms, TreeInstance &out)
+{
+    static TreeInstance inst[MOE_TREE_MAX_DEVICES][12];
+    static int sm_count[MOE_TREE_MAX_DEVICES];
+    int d = 0;
+    SPEC_CUDA_OK(cudaGetDevice(&d));
+    if (d < 0 || d >= MOE_TREE_MAX_DEVICES)
+        return host_fail(MOE_EUNSUPPORTED, "device ordinal %d", d);
+    std::lock_guard<std::mutex> lk(g_tree_mu);
+    if (!sm_count[d]) {
+        const TreeInstance all[12] = {
+            tree_instance<MOE_KV_Q8, 64, 1>(),  tree_instance<MOE_KV_Q8, 64, 2>(),  tree_instance<MOE_KV_Q8, 64, 4>(),
+            tree_instance<MOE_KV_Q8, 128, 1>(), tree_instance<MOE_KV_Q8, 128, 2>(), tree_instance<MOE_KV_Q8, 256, 1>(),
+            tree_instance<MOE_KV_Q4, 64, 1>(),  tree_instance<MOE_KV_Q4, 64, 2>(),  tree_instance<MOE_KV_Q4, 64, 4>(),
+            tree_instance<MOE_KV_Q4, 128, 1>(), tree_instance<MOE_KV_Q4, 128, 2>(), tree_instance<MOE_KV_Q4, 256, 1>()};
+        int n = 0, per_sm = 0, optin = 0;
+        SPEC_CUDA_OK(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d));
+        SPEC_CUDA_OK(cudaDeviceGetAttribute(&per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, d));
+        SPEC_CUDA_OK(cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, d));
+        for (int i = 0; i < 12; ++i) {
+            TreeInstance t = all[i];
+            cudaFuncAttributes fa;
+            SPEC_CUDA_OK(cudaFuncGetAttributes(&fa, t.kernel));
+            SPEC_CUDA_OK(cudaFuncSetAttribute(t.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
+            // as many CTAs an SM as the registers allow (at most 3) while each ring keeps 3 stages
+            const int by_regs = 65536 / ((fa.numRegs + 7) / 8 * 8 * MOE_TREE_THREADS);
+            for (t.ctas = std::max(1, std::min(by_regs, 3));; --t.ctas) {
+                const size_t room = std::min<size_t>(optin, per_sm / t.ctas - 1024);
+                t.stages = room > t.fixed ? (int)std::min<size_t>(8, (room - t.fixed) / t.stage) : 0;
+                if (t.stages >= 3 || t.ctas == 1)
+                    break;
+            }
+            if (t.stages < 2)
+                return host_fail(MOE_EUNSUPPORTED, "tree attention: %zu bytes of shared memory do not fit", t.fixed);
+            inst[d][i] = t;
+        }
+        sm_count[d] = n;
+    }
+    sms = sm_count[d];
+    out = inst[d][index];
     return MOE_OK;
 }
 
@@ -161,7 +236,9 @@ static int tree_ws(const moe_kv_cache *cache, int n_q_heads, int batch, int n_to
     if (n_q_heads / k.heads > 64 || batch > 1024 || n_tokens > batch * MOE_MAX_DRAFT)
         return host_fail(MOE_EUNSUPPORTED, "n_q_heads / n_kv_heads (%d) <= 64, batch (%d) <= 1024, n_tokens (%d) <= "
                          "%d a sequence", n_q_heads / k.heads, batch, n_tokens, MOE_MAX_DRAFT);
-    bytes = SPEC_CTRL_BYTES;
+    // control words, arrivals, and two partials of the largest row block a run
+    const size_t rows = k.dim == 64 ? 64 : k.dim == 128 ? 32 : 16;
+    bytes = SPEC_CTRL_BYTES + 4 * MOE_TREE_MAX_GRID + (size_t)MOE_TREE_MAX_GRID * 2 * 4 * rows * (k.dim + 2);
     return MOE_OK;
 }
 
@@ -216,11 +293,22 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     a.mask = reinterpret_cast<const unsigned long long *>(mask_dev);
     a.batch = batch;
     a.tokens = n_tokens;
-    a.q_heads = n_q_heads;
+    a.group = n_q_heads / a.k.heads;
     a.scale = scale;
+    a.q_wide = aligned(q_dev, 16) && (q_token_stride | q_head_stride) % 8 == 0;
+    a.o_wide = aligned(out_dev, 16) && (out_token_stride | out_head_stride) % 8 == 0;
+    a.min_units = 2 * MOE_TREE_WARPS;
     a.ctrl = static_cast<uint32_t *>(ws_dev);
-    const int rows = n_tokens * n_q_heads;
-    moe_tree_attn_kernel<<<(rows + 3) / 4, 128, 0, (cudaStream_t)stream>>>(a);
+    a.count = a.ctrl + SPEC_CTRL_BYTES / 4;
+    a.part = reinterpret_cast<float *>(a.count + MOE_TREE_MAX_GRID);
+    a.wait_ns = host_wait_ns();
+    // the row block from the mean rows of a sequence (the lengths themselves are on the device)
+    TreeInstance t;
+    int sms;
+    if ((rc = tree_get(tree_choose(a.k.fmt, a.k.dim, (n_tokens + batch - 1) / batch * a.group), sms, t)))
+        return rc;
+    const int grid = std::min(sms * t.ctas, MOE_TREE_MAX_GRID);
+    t.kernel<<<grid, MOE_TREE_THREADS, t.fixed + t.stages * t.stage, (cudaStream_t)stream>>>(a, t.stages);
     SPEC_CUDA_OK(cudaGetLastError());
     return MOE_OK;
 }

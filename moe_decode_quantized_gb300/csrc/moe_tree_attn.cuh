@@ -2,14 +2,37 @@
 // token, a chain, or a tree) over the quantised paged cache.
 //
 //   o = sum_j softmax_j(scale q . K_j | j seen) V_j
-// in one pass over the cache: a running maximum m and sum l of each row,
-// o and l scaled by e^(m - m') when the maximum rises.
+// in one pass over the cache: a running reference m of each row's scores, the
+// sum l of its weights and o, both scaled by 2^(m - m') when m moves.
+//
+// The rows of one kv head are its query rows times the heads of its group,
+// row r = token r / G, head r % G; 16 MT of them (a row block) are worked on
+// together. An item is (sequence, kv head, row block), a unit of it one block
+// of 16 tokens of the cache. The units of all items form one list that is cut
+// into equal runs, one a CTA, so ragged lengths cost nothing; a run that cuts
+// an item leaves a partial (o, m, l) in the workspace, and the CTA that
+// finishes an item last joins its partials in the order of the runs (no CTA
+// waits for another; the result does not depend on who is last).
+//
+// A warp takes every fourth unit of its CTA's run through a ring of its own
+// (one bulk copy a unit), and everything stays in registers: codes to f16 B
+// fragments (the cache's byte order is the fragments'), S = Q K^T by 16x8x16
+// products, the weights as the A fragments of o += P V. Bound by the copies
+// while the rows are few; 16 rows cost 32 products a unit of 128 dimensions.
 #pragma once
 #include <cuda_bf16.h>
 
 #include "moe_kv.cuh"
 
 namespace moe {
+
+#define MOE_TREE_WARPS 4
+#define MOE_TREE_THREADS (MOE_TREE_WARPS * 32)
+#define MOE_TREE_MAX_BATCH 1024
+// the weights are 2^(s - m + 7): m moves when a score passes it by 8, so a
+// weight stays below 2^15, and f16 holds weights of 2^-31 of the largest
+#define MOE_TREE_SLACK 8.0f
+#define MOE_TREE_LIFT 7.0f
 
 struct TreeArgs {
     KvDims k;
@@ -25,74 +48,710 @@ struct TreeArgs {
     long long table_stride;
     int table_pages;          // pages a sequence can have
     const unsigned long long *mask;  // [tokens] or NULL: causal
-    int batch, tokens, q_heads;
+    int batch, tokens, group;
     float scale;
-    uint32_t *ctrl;
+    int q_wide, o_wide;       // rows of q (out) can be read (written) 16 bytes at a time
+    int min_units;            // fewest units of a run
+    uint32_t *ctrl, *count;   // control words; [grid] arrivals at the item that leaves a run at its end
+    float *part;              // [grid][2] partials of part_floats
+    unsigned long long wait_ns;
 };
 
-// rows and length of a sequence, checked; n = 0 where they do not hold
-__device__ __forceinline__ void tree_sequence(const TreeArgs &a, int b, int &first, int &n, int &len)
+// geometry of an instance: FMT, head size, 16-row tiles
+template <int FMT, int D, int MT>
+struct TreeShape {
+    static constexpr int RB = FMT == MOE_KV_Q8 ? D : D / 2;
+    static constexpr int GR = D / MOE_KV_GROUP;
+    static constexpr int SCALES = 16 * GR * (FMT == MOE_KV_Q8 ? 2 : 4);
+    static constexpr int HALF = 16 * RB + SCALES;
+    static constexpr int BLOCK = 2 * HALF;
+    static constexpr int KS = D / 16;       // steps of the contraction over the dimensions
+    static constexpr int NB = D / 8;        // column blocks of the output
+    static constexpr int WK = RB / 16;      // words of a lane's quarter of a K row
+    static constexpr int WV = RB / 32;      // words of a lane's eighth of a V row
+    static constexpr int ROWS = 16 * MT;
+    static constexpr int OREGS = MT * NB * 4;
+    static constexpr bool QREG = OREGS + MT * KS * 4 <= 96;  // query fragments kept in registers
+    static constexpr int PART = ROWS * D + 2 * ROWS;         // floats of a partial
+    static constexpr int BARS = 8 * 8 * MOE_TREE_WARPS;      // room for 8 stages' barriers
+    static constexpr int SEQ = 8 * (MOE_TREE_MAX_BATCH + 2);
+    static constexpr int HEAD = BARS + 8 * ROWS + 12 * ROWS * MOE_TREE_WARPS + 64;
+    static constexpr int QBYTES = MT * KS * 512;
+    static constexpr int MERGE = 2 * OREGS * 128;
+    __host__ __device__ static constexpr int fixed() { return (HEAD + SEQ + QBYTES + MERGE + 127) / 128 * 128; }
+    static size_t smem(int stages) { return fixed() + (size_t)stages * MOE_TREE_WARPS * BLOCK; }
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// D (+)= A B: 16x8x16, f16 operands, f32 sums
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<uint32_t *>(&v); }
+__device__ __forceinline__ __half2 h2(uint32_t v) { return *reinterpret_cast<__half2 *>(&v); }
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) { return h2(__floats2half2_rn(a, b)); }
+__device__ __forceinline__ uint32_t dup_lo(uint32_t v) { return __byte_perm(v, v, 0x1010); }
+__device__ __forceinline__ uint32_t dup_hi(uint32_t v) { return __byte_perm(v, v, 0x3232); }
+
+// two code bytes (bytes i and j of w) as f16: 0x6400 | u is 1024 + u, less
+// 1024 + 128 the code, exactly; times the scale, rounded once
+__device__ __forceinline__ uint32_t q8_pair(uint32_t w, uint32_t sel, __half2 d)
+{
+    const __half2 u = h2(__byte_perm(w, 0x64646464u, sel));
+    return h2(__hmul2(__hsub2(u, h2(0x64806480u)), d));
+}
+
+// two 4-bit codes at bits 0 and 16 of w (already 0x6400 | code) as code d + m
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w, __half2 d, __half2 m)
+{
+    return h2(__hfma2(__hsub2(h2(w), h2(0x64006400u)), d, m));
+}
+
+// rows and length of a sequence, checked; n = 0 where they do not hold (rows:
+// the query rows that are then written as zeros)
+__device__ __forceinline__ void tree_sequence(const TreeArgs &a, int b, int &first, int &n, int &len, int &rows)
 {
     first = a.q_start[b];
     n = a.q_start[b + 1] - first;
     len = a.kv_len[b];
-    const bool ok = first >= 0 && n >= 0 && n <= MOE_MAX_DRAFT && first + n <= a.tokens && len >= n &&
-                    len <= (long long)a.table_pages * a.k.page;
-    if (!ok) {
-        atomicOr(a.ctrl + MOE_CTRL_STATUS, (uint32_t)MOE_WS_INDEX);
+    const bool held = first >= 0 && n >= 0 && n <= MOE_MAX_DRAFT && first <= a.tokens - n;
+    rows = held ? n : 0;
+    if (!held || len < n || len > (long long)a.table_pages * a.k.page) {
+        if (!held || n > 0)
+            atomicOr(a.ctrl + MOE_CTRL_STATUS, (uint32_t)MOE_WS_INDEX);
         n = 0;
     }
 }
 
-// One warp a query row (token and head), lanes over the dimensions.
-__global__ void __launch_bounds__(128) moe_tree_attn_kernel(const TreeArgs a)
+// one item: the units [lo, lo + units) of the list
+struct TreeItem {
+    int b, head, block, first, n, len, units;
+    long long lo;
+};
+
+template <int ROWS>
+__device__ __forceinline__ int tree_blocks(int n, int group) { return (n * group + ROWS - 1) / ROWS; }
+
+// the item that holds unit u: cum [batch + 1] is the list's units before each sequence
+template <int ROWS>
+__device__ __forceinline__ TreeItem tree_item(const TreeArgs &a, const long long *cum, long long u)
 {
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= a.tokens * a.q_heads)
-        return;
-    const int token = row / a.q_heads, head = row % a.q_heads, kvh = head / (a.q_heads / a.k.heads);
-    int first = 0, n = 0, len = 0, b = 0;
-    for (; b < a.batch; ++b) {
-        tree_sequence(a, b, first, n, len);
-        if (token >= first && token < first + n)
-            break;
+    int x = 0, y = a.batch;  // cum[x] <= u < cum[y]
+    while (y - x > 1) {
+        const int z = (x + y) / 2;
+        if (cum[z] <= u)
+            x = z;
+        else
+            y = z;
     }
-    if (b == a.batch)  // a row of no sequence, or of one whose length does not hold
-        n = len = 0;
-    const int i = max(0, min(token - first, MOE_MAX_DRAFT - 1)), per = a.k.dim / 32, d0 = lane * per;
-    const unsigned long long mask = a.mask ? a.mask[token] : (2ull << i) - 1;
-    float q[8], o[8], top = -INFINITY, sum = 0.0f;
-    for (int e = 0; e < per; ++e) {
-        q[e] = bf16_to_f32(a.q[token * a.q_tok + head * a.q_head + d0 + e]) * a.scale;
-        o[e] = 0.0f;
-    }
-    for (int j = 0; j < len; ++j) {
-        const int place = j - (len - n);
-        if (place >= 0 && !(mask >> place & 1))
-            continue;
-        const int page = a.table[b * a.table_stride + j / a.k.page];
-        if (page < 0 || page >= a.n_pages) {
-            atomicOr(a.ctrl + MOE_CTRL_STATUS, (uint32_t)MOE_WS_INDEX);
-            continue;
+    TreeItem it;
+    it.b = x;
+    it.first = a.q_start[x];
+    it.n = a.q_start[x + 1] - it.first;
+    it.len = a.kv_len[x];
+    it.units = (it.len + 15) / 16;
+    const int at = (int)((u - cum[x]) / it.units), blocks = tree_blocks<ROWS>(it.n, a.group);
+    it.head = at / blocks;
+    it.block = at % blocks;
+    it.lo = cum[x] + (long long)at * it.units;
+    return it;
+}
+
+// writes a row block: o[mt][j] of this lane divided by the rows' sums
+template <int D, int MT>
+__device__ __forceinline__ void tree_store(const TreeArgs &a, const TreeItem &it, float (&o)[MT][D / 8][4],
+                                           const float (&l)[MT][2], int lane)
+{
+    constexpr int Q = D / 4;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int r = it.block * 16 * MT + mt * 16 + s * 8 + lane / 4;
+            if (r >= it.n * a.group)
+                continue;
+            uint16_t *p = a.out + (it.first + r / a.group) * a.o_tok + (it.head * a.group + r % a.group) * a.o_head +
+                          (lane & 3) * Q;
+            const float inv = l[mt][s] == 0.0f ? 0.0f : 1.0f / l[mt][s];
+#pragma unroll
+            for (int x = 0; x < Q; x += 8) {  // column 2 tid of block j is dimension 2 tid D / 8 + j
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = x + 2 * i, c = s * 2 + e / (D / 8), j = e % (D / 8);
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(o[mt][j][c] * inv, o[mt][j + 1][c] * inv);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+                if (a.o_wide) {
+                    *reinterpret_cast<uint4 *>(p + x) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        p[x + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+                }
+            }
         }
-        const int in = j % a.k.page, t = in % 16;
-        const uint8_t *blk = a.pages + (((size_t)page * a.k.heads + kvh) * (a.k.page / 16) + in / 16) * a.k.block_bytes();
-        float v[8], s = 0.0f;
-        kv_values8(a.k, blk, false, t, d0 / 8, v);
-        for (int e = 0; e < per; ++e)
-            s = fmaf(q[e], v[d0 % 8 + e], s);
-        for (int m = 16; m; m /= 2)
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
-        const float up = fmaxf(top, s), keep = expf(top - up), p = expf(s - up);
-        top = up;
-        sum = sum * keep + p;
-        kv_values8(a.k, blk + a.k.half_bytes(), true, t, d0 / 8, v);
-        for (int e = 0; e < per; ++e)
-            o[e] = fmaf(p, v[d0 % 8 + e], o[e] * keep);
+}
+
+template <int FMT, int D, int MT>
+__global__ void __launch_bounds__(MOE_TREE_THREADS) moe_tree_attn_kernel(const __grid_constant__ TreeArgs a, const int stages)
+{
+    using T = TreeShape<FMT, D, MT>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem);                           // [warps][8]
+    unsigned long long *masks = reinterpret_cast<unsigned long long *>(smem + T::BARS);  // [rows]
+    float *cmul = reinterpret_cast<float *>(smem + T::BARS + 8 * T::ROWS);         // [rows]
+    float *wm = cmul + T::ROWS, *wl = wm + MOE_TREE_WARPS * T::ROWS;               // [warps][rows]
+    long long *scan = reinterpret_cast<long long *>(smem + T::HEAD - 48);          // [warps]
+    long long *cum = reinterpret_cast<long long *>(smem + T::HEAD);                // [batch + 1]
+    uint4 *qf = reinterpret_cast<uint4 *>(smem + T::HEAD + T::SEQ);                // [mt][ks][lane]
+    float4 *merge = reinterpret_cast<float4 *>(smem + T::HEAD + T::SEQ + T::QBYTES);  // [2][regs / 4][lane]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+    uint8_t *ring = smem + T::fixed() + (size_t)warp * stages * T::BLOCK;
+    uint64_t *bar = bars + warp * 8;
+    if (lane == 0) {
+        for (int s = 0; s < stages; ++s)
+            mbar_init(bar + s, 1);
+        fence_barrier_init();
     }
-    for (int e = 0; e < per; ++e)
-        a.out[token * a.o_tok + head * a.o_head + d0 + e] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.0f ? 0.0f : o[e] / sum));
+    // the list: units before each sequence
+    {
+        const int per = (a.batch + MOE_TREE_THREADS - 1) / MOE_TREE_THREADS;
+        long long mine = 0;
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b >= a.batch)
+                break;
+            int first, n, len, rows;
+            tree_sequence(a, b, first, n, len, rows);
+            cum[b] = mine;
+            mine += (long long)((len + 15) / 16) * (n > 0 ? tree_blocks<T::ROWS>(n, a.group) * a.k.heads : 0);
+            if (n == 0 && rows > 0 && blockIdx.x == (unsigned)(b % gridDim.x))  // what does not hold gives zeros
+                for (int r = 0; r < rows * a.k.heads * a.group; ++r) {
+                    uint16_t *p = a.out + (first + r / (a.k.heads * a.group)) * a.o_tok + r % (a.k.heads * a.group) * a.o_head;
+                    for (int d = 0; d < D; ++d)
+                        p[d] = 0;
+                }
+        }
+        long long incl = mine;
+        for (int m = 1; m < 32; m *= 2) {
+            const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+            if (lane >= m)
+                incl += v;
+        }
+        if (lane == 31)
+            scan[warp] = incl;
+        __syncthreads();
+        long long before = incl - mine;
+        for (int w = 0; w < warp; ++w)
+            before += scan[w];
+        for (int i = 0; i < per; ++i)
+            if (tid * per + i < a.batch)
+                cum[tid * per + i] += before;
+        if (tid == MOE_TREE_THREADS - 1)
+            cum[a.batch] = before + mine;
+        __syncthreads();
+    }
+    const long long total = cum[a.batch];
+    const long long run = max((total + gridDim.x - 1) / (long long)gridDim.x, (long long)a.min_units);
+    const long long lo = run * blockIdx.x, hi = min(lo + run, total);
+    if (lo >= hi)
+        return;
+    const int mine = (int)((hi - lo - warp + MOE_TREE_WARPS - 1) / MOE_TREE_WARPS);  // this warp's units
+    const uint64_t policy = policy_evict_first();
+    bool ok = true;
+
+    // the copies' side: lane i holds the place of this warp's unit batch + i
+    int asked = 0, batch = 0;
+    const uint8_t *place = nullptr;
+    uint32_t bad = 0, bad_before = 0;  // units of this batch (the one before) whose page lay outside
+    auto look = [&](int at) {
+        batch = at;
+        bool out = false;
+        place = a.pages;
+        if (at + lane < mine) {
+            const long long u = lo + warp + (long long)(at + lane) * MOE_TREE_WARPS;
+            const TreeItem it = tree_item<T::ROWS>(a, cum, u);
+            const int blk = (int)(u - it.lo), per_page = a.k.page / 16;
+            const int page = a.table[it.b * a.table_stride + blk / per_page];
+            out = page < 0 || page >= a.n_pages;
+            if (out)
+                atomicOr(a.ctrl + MOE_CTRL_STATUS, (uint32_t)MOE_WS_INDEX);
+            else
+                place = a.pages + (((size_t)page * a.k.heads + it.head) * per_page + blk % per_page) * T::BLOCK;
+        }
+        bad_before = bad;
+        bad = __ballot_sync(0xFFFFFFFFu, out);
+    };
+    auto ask = [&]() {  // the copy of the next unit into its stage
+        if (asked - batch == 32)
+            look(asked);
+        const uint8_t *src = reinterpret_cast<const uint8_t *>(
+            __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(place), asked - batch));
+        const int s = asked % stages;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar + s, T::BLOCK);
+            bulk_g2s(ring + s * T::BLOCK, src, T::BLOCK, bar + s, policy);
+        }
+        ++asked;
+    };
+    if (mine > 0)
+        look(0);
+    for (int s = 0; s < stages && asked < mine; ++s)
+        ask();
+
+    int done = 0, stage = 0;
+    uint32_t phase = 0;
+    for (long long u = lo; u < hi;) {
+        const TreeItem it = tree_item<T::ROWS>(a, cum, u);
+        const long long end = min(hi, it.lo + it.units);
+        // query fragments: k step ks of lane (g, t4) is dimensions t4 D / 4 + 4 ks .. + 3 of rows g and g + 8,
+        // each row scaled by a power of two to below 2^14 (f16 then holds bf16's values exactly)
+        for (int mt = warp; mt < MT; mt += MOE_TREE_WARPS) {
+            uint32_t x[2][D / 8];
+            float mul[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int r = it.block * T::ROWS + mt * 16 + s * 8 + g;
+                const bool live = r < it.n * a.group;
+                const int i = live ? r / a.group : 0;
+                const uint16_t *p = a.q + (it.first + i) * a.q_tok +
+                                    (it.head * a.group + (live ? r % a.group : 0)) * a.q_head + t4 * (D / 4);
+                float top = 0.0f;
+                bool odd = false;
+#pragma unroll
+                for (int e = 0; e < D / 8; e += 4) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (live && a.q_wide) {
+                        v = *reinterpret_cast<const uint4 *>(p + 2 * e);
+                    } else if (live) {
+                        v.x = p[2 * e] | (uint32_t)p[2 * e + 1] << 16;
+                        v.y = p[2 * e + 2] | (uint32_t)p[2 * e + 3] << 16;
+                        v.z = p[2 * e + 4] | (uint32_t)p[2 * e + 5] << 16;
+                        v.w = p[2 * e + 6] | (uint32_t)p[2 * e + 7] << 16;
+                    }
+                    x[s][e] = v.x;
+                    x[s][e + 1] = v.y;
+                    x[s][e + 2] = v.z;
+                    x[s][e + 3] = v.w;
+#pragma unroll
+                    for (int i2 = 0; i2 < 4; ++i2) {
+                        const float f0 = fabsf(bf16_lo(x[s][e + i2])), f1 = fabsf(bf16_hi(x[s][e + i2]));
+                        odd |= !(f0 < INFINITY) || !(f1 < INFINITY);
+                        top = fmaxf(top, fmaxf(f0, f1));
+                    }
+                }
+#pragma unroll
+                for (int m = 1; m < 4; m *= 2) {
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+                    odd |= __shfl_xor_sync(0xFFFFFFFFu, (int)odd, m) != 0;
+                }
+                // 2^e with top 2^e in [2^13, 2^14): two factors, as e can pass f32's exponents
+                const int e = top > 0.0f ? 13 - ilogbf(top) : 0;
+                const float up0 = exp2f((float)(e / 2)), up1 = exp2f((float)(e - e / 2));
+                const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+                for (int i2 = 0; i2 < D / 8; ++i2) {
+                    float f0 = bf16_lo(x[s][i2]) * up0 * up1 * sign, f1 = bf16_hi(x[s][i2]) * up0 * up1 * sign;
+                    if (odd)  // a row with a NaN or an infinity is a row of NaN
+                        f0 = f1 = __int_as_float(0x7FC00000);
+                    if (a.scale == 0.0f && !odd)
+                        f0 = f1 = 0.0f;
+                    x[s][i2] = pack_h2(f0, f1);
+                }
+                mul[s] = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f / up0 / up1;
+                if (t4 == 0) {
+                    cmul[mt * 16 + s * 8 + g] = mul[s];
+                    masks[mt * 16 + s * 8 + g] = !live ? 0 : a.mask ? a.mask[it.first + i] : (2ull << i) - 1;
+                }
+            }
+#pragma unroll
+            for (int ks = 0; ks < T::KS; ++ks)
+                qf[(mt * T::KS + ks) * 32 + lane] = make_uint4(x[0][2 * ks], x[1][2 * ks], x[0][2 * ks + 1],
+                                                               x[1][2 * ks + 1]);
+        }
+        __syncthreads();
+        uint4 qr[T::QREG ? MT : 1][T::QREG ? T::KS : 1];
+        if constexpr (T::QREG)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int ks = 0; ks < T::KS; ++ks)
+                    qr[mt][ks] = qf[(mt * T::KS + ks) * 32 + lane];
+        float c[MT][2], m[MT][2], l[MT][2], o[MT][T::NB][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                c[mt][s] = cmul[mt * 16 + s * 8 + g];
+                m[mt][s] = -INFINITY;
+                l[mt][s] = 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < T::NB; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[mt][j][i] = 0.0f;
+        }
+        const int prefix = it.len - it.n;
+        for (; done < mine; ++done) {
+            const long long at = lo + warp + (long long)done * MOE_TREE_WARPS;
+            if (at >= end)
+                break;
+            const int first = (int)(at - it.lo) * 16;  // the unit's first token
+            if (ok)
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar + stage, phase, a.ctrl + MOE_CTRL_STATUS, a.wait_ns));
+            const uint8_t *blk = ring + stage * T::BLOCK;
+            const bool gone = (done >= batch ? bad >> (done - batch) : bad_before >> (done - batch + 32)) & 1;
+            const bool masked = gone || first + 16 > prefix;
+
+            // ---- scores: columns 2 t4, 2 t4 + 1 of two blocks of eight tokens
+            float s[MT][2][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[mt][nb][i] = 0.0f;
+            {
+                uint32_t kw[2 * T::WK];
+#pragma unroll
+                for (int i = 0; i < 2 * T::WK; i += 4)
+                    *reinterpret_cast<uint4 *>(kw + i) = *reinterpret_cast<const uint4 *>(blk + i * 128 + lane * 16);
+                constexpr int GL = D == 256 ? 2 : 1;  // groups of a lane's quarter
+                __half2 kd[2][GL], km[2][GL];
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                    for (int x = 0; x < GL; ++x) {
+                        const int at2 = (nb * 8 + g) * T::GR + (D == 64 ? t4 / 2 : t4 * GL + x);
+                        if (FMT == MOE_KV_Q8) {
+                            kd[nb][x] = __half2half2(reinterpret_cast<const __half *>(blk + 16 * T::RB)[at2]);
+                        } else {
+                            const uint32_t w = reinterpret_cast<const uint32_t *>(blk + 16 * T::RB)[at2];
+                            kd[nb][x] = h2(dup_lo(w));
+                            km[nb][x] = h2(dup_hi(w));
+                        }
+                    }
+#pragma unroll
+                for (int ks = 0; ks < T::KS; ++ks) {
+                    const int x = GL == 1 ? 0 : ks / (T::KS / 2);
+                    uint32_t b[2][2];
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb) {
+                        if (FMT == MOE_KV_Q8) {
+                            const uint32_t w = kw[nb * T::WK + ks];
+                            b[nb][0] = q8_pair(w, 0x5140, kd[nb][x]);
+                            b[nb][1] = q8_pair(w, 0x5342, kd[nb][x]);
+                        } else {
+                            const uint32_t w = kw[nb * T::WK + ks / 2] >> (8 * (ks & 1));
+                            b[nb][0] = q4_pair((w & 0x000F000Fu) | 0x64006400u, kd[nb][x], km[nb][x]);
+                            b[nb][1] = q4_pair((w >> 4 & 0x000F000Fu) | 0x64006400u, kd[nb][x], km[nb][x]);
+                        }
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint4 q = T::QREG ? qr[T::QREG ? mt : 0][T::QREG ? ks : 0] : qf[(mt * T::KS + ks) * 32 + lane];
+                        mma16816(s[mt][0], q, b[0][0], b[0][1]);
+                        mma16816(s[mt][1], q, b[1][0], b[1][1]);
+                    }
+                }
+            }
+            if (masked) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int j = first + (i / 4) * 8 + t4 * 2 + (i & 1), row = mt * 16 + (i & 2) * 4 + g;
+                        const bool sees = !gone && j < it.len && (j < prefix || masks[row] >> (j - prefix) & 1);
+                        if (!sees)
+                            s[mt][i / 4][i & 3] = -INFINITY;
+                    }
+            }
+            // ---- weights
+            uint4 p[MT];
+            bool moves = false;
+            float top[MT][2];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float v = fmaxf(fmaxf(s[mt][0][2 * r], s[mt][0][2 * r + 1]), fmaxf(s[mt][1][2 * r], s[mt][1][2 * r + 1]));
+                    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+                    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+                    top[mt][r] = v * c[mt][r];
+                    moves |= top[mt][r] > m[mt][r] + MOE_TREE_SLACK;
+                }
+            if (__any_sync(0xFFFFFFFFu, moves)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    float keep[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const bool up = top[mt][r] > m[mt][r] + MOE_TREE_SLACK;
+                        keep[r] = up ? ex2(m[mt][r] - top[mt][r]) : 1.0f;
+                        m[mt][r] = up ? top[mt][r] : m[mt][r];
+                        l[mt][r] *= keep[r];
+                    }
+#pragma unroll
+                    for (int j = 0; j < T::NB; ++j) {
+                        o[mt][j][0] *= keep[0];
+                        o[mt][j][1] *= keep[0];
+                        o[mt][j][2] *= keep[1];
+                        o[mt][j][3] *= keep[1];
+                    }
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float e[2][4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float off = m[mt][r] == -INFINITY ? 0.0f : MOE_TREE_LIFT - m[mt][r];
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                        for (int i = 2 * r; i < 2 * r + 2; ++i)
+                            e[nb][i] = ex2(fmaf(s[mt][nb][i], c[mt][r], off));
+                    l[mt][r] += (e[0][2 * r] + e[0][2 * r + 1]) + (e[1][2 * r] + e[1][2 * r + 1]);
+                }
+                p[mt] = make_uint4(pack_h2(e[0][0], e[0][1]), pack_h2(e[0][2], e[0][3]), pack_h2(e[1][0], e[1][1]),
+                                   pack_h2(e[1][2], e[1][3]));
+            }
+            // ---- o += P V: a lane's words of tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9
+            {
+                const uint8_t *vb = blk + T::HALF;
+                uint32_t vw[4 * T::WV];
+#pragma unroll
+                for (int i = 0; i < 4 * T::WV; i += 4)
+                    *reinterpret_cast<uint4 *>(vw + i) = *reinterpret_cast<const uint4 *>(vb + i * 128 + lane * 16);
+                const uint32_t *vs = reinterpret_cast<const uint32_t *>(vb + 16 * T::RB);  // pairs of tokens
+                const int at2 = g * T::GR / 8 * 8 + t4;
+                __half2 vd[2], vm[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    vd[x] = h2(vs[at2 + 4 * x]);
+                    if (FMT == MOE_KV_Q4)
+                        vm[x] = h2(vs[T::GR * 8 + at2 + 4 * x]);
+                }
+                if (masked) {  // bytes past the length (of no page) are anything: as values they are 0
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int j = first + 8 * x + 2 * t4;
+                        const uint32_t keep = gone ? 0u : (j < it.len ? 0xFFFFu : 0u) | (j + 1 < it.len ? 0xFFFF0000u : 0u);
+                        vd[x] = h2(h2(vd[x]) & keep);
+                        if (FMT == MOE_KV_Q4)
+                            vm[x] = h2(h2(vm[x]) & keep);
+                    }
+                }
+                if (FMT == MOE_KV_Q8) {
+#pragma unroll
+                    for (int w = 0; w < T::WV; ++w) {
+                        uint32_t b[2][4];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t w0 = vw[(2 * x) * T::WV + w], w1 = vw[(2 * x + 1) * T::WV + w];
+                            const uint32_t a0 = __byte_perm(w0, w1, 0x5140), a1 = __byte_perm(w0, w1, 0x7362);
+                            b[x][0] = q8_pair(a0, 0x5140, vd[x]);
+                            b[x][1] = q8_pair(a0, 0x5342, vd[x]);
+                            b[x][2] = q8_pair(a1, 0x5140, vd[x]);
+                            b[x][3] = q8_pair(a1, 0x5342, vd[x]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt)
+                                mma16816(o[mt][4 * w + i], p[mt], b[0][i], b[1][i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int w = 0; w < T::WV; ++w)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {  // codes 2 i, 2 i + 1 of the word
+                            uint32_t b[2][2];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const uint32_t w0 = (vw[(2 * x) * T::WV + w] >> (4 * i) & 0x000F000Fu) | 0x64006400u;
+                                const uint32_t w1 = (vw[(2 * x + 1) * T::WV + w] >> (4 * i) & 0x000F000Fu) | 0x64006400u;
+                                b[x][0] = q4_pair(__byte_perm(w0, w1, 0x5410), vd[x], vm[x]);
+                                b[x][1] = q4_pair(__byte_perm(w0, w1, 0x7632), vd[x], vm[x]);
+                            }
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                mma16816(o[mt][8 * w + 2 * i], p[mt], b[0][0], b[1][0]);
+                                mma16816(o[mt][8 * w + 2 * i + 1], p[mt], b[0][1], b[1][1]);
+                            }
+                        }
+                }
+            }
+            __syncwarp();  // the stage has been read
+            if (ok && asked < mine)
+                ask();
+            if (++stage == stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+
+        // ---- join the warps: rows' references and sums, then o of warps 2, 3 into 0, 1 and 1 into 0
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                l[mt][r] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][r], 1);
+                l[mt][r] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][r], 2);
+                if (t4 == 0) {
+                    wm[warp * T::ROWS + mt * 16 + r * 8 + g] = m[mt][r];
+                    wl[warp * T::ROWS + mt * 16 + r * 8 + g] = l[mt][r];
+                }
+            }
+        __syncthreads();
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = mt * 16 + r * 8 + g;
+                float up = -INFINITY, sum = 0.0f;
+                for (int w = 0; w < MOE_TREE_WARPS; ++w)
+                    up = fmaxf(up, wm[w * T::ROWS + row]);
+                for (int w = 0; w < MOE_TREE_WARPS; ++w) {
+                    const float v = wm[w * T::ROWS + row];
+                    sum += wl[w * T::ROWS + row] * (v == -INFINITY ? 1.0f : ex2(v - up));  // a NaN sum stays
+                }
+                const float keep = m[mt][r] == -INFINITY ? 1.0f : ex2(m[mt][r] - up);
+                m[mt][r] = up;
+                l[mt][r] = sum;
+#pragma unroll
+                for (int j = 0; j < T::NB; ++j) {
+                    o[mt][j][2 * r] *= keep;
+                    o[mt][j][2 * r + 1] *= keep;
+                }
+            }
+        auto give = [&](int slot) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int j = 0; j < T::NB; ++j)
+                    merge[(slot * MT * T::NB + mt * T::NB + j) * 32 + lane] =
+                        make_float4(o[mt][j][0], o[mt][j][1], o[mt][j][2], o[mt][j][3]);
+        };
+        auto take = [&](int slot) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int j = 0; j < T::NB; ++j) {
+                    const float4 v = merge[(slot * MT * T::NB + mt * T::NB + j) * 32 + lane];
+                    o[mt][j][0] += v.x;
+                    o[mt][j][1] += v.y;
+                    o[mt][j][2] += v.z;
+                    o[mt][j][3] += v.w;
+                }
+        };
+        if (warp >= 2)
+            give(warp - 2);
+        __syncthreads();
+        if (warp < 2)
+            take(warp);
+        __syncthreads();
+        if (warp == 1)
+            give(0);
+        __syncthreads();
+        const long long item_end = it.lo + it.units;
+        const bool whole = u == it.lo && end == item_end;
+        if (warp == 0) {
+            take(0);
+            if (whole) {
+                tree_store<D, MT>(a, it, o, l, lane);
+            } else {  // a partial: slot 0 is the run's first item, 1 its last
+                float *part = a.part + ((size_t)blockIdx.x * 2 + (u == lo ? 0 : 1)) * T::PART;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                    for (int j = 0; j < T::NB; ++j)
+                        reinterpret_cast<float4 *>(part)[(mt * T::NB + j) * 32 + lane] =
+                            make_float4(o[mt][j][0], o[mt][j][1], o[mt][j][2], o[mt][j][3]);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        if (t4 == 0) {
+                            part[T::ROWS * D + mt * 16 + r * 8 + g] = m[mt][r];
+                            part[T::ROWS * D + T::ROWS + mt * 16 + r * 8 + g] = l[mt][r];
+                        }
+                }
+                __threadfence();
+                __syncwarp();
+                const int c0 = (int)(it.lo / run), c1 = (int)((item_end - 1) / run);  // the item's runs
+                unsigned old = 0;
+                if (lane == 0)
+                    old = atom_add_acq_rel_gpu(a.count + c0, 1);
+                old = __shfl_sync(0xFFFFFFFFu, old, 0);
+                if (old == (unsigned)(c1 - c0)) {  // the last: join
+                    __threadfence();
+                    if (lane == 0)
+                        st_relaxed_gpu(a.count + c0, 0);
+                    auto slot = [&](int cta) { return a.part + ((size_t)cta * 2 + (it.lo <= cta * run ? 0 : 1)) * T::PART; };
+                    float up[MT][2];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            up[mt][r] = -INFINITY;
+                            l[mt][r] = 0.0f;
+                        }
+                    for (int cta = c0; cta <= c1; ++cta)
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                up[mt][r] = fmaxf(up[mt][r], __ldcg(slot(cta) + T::ROWS * D + mt * 16 + r * 8 + g));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int j = 0; j < T::NB; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                o[mt][j][i] = 0.0f;
+                    for (int cta = c0; cta <= c1; ++cta) {
+                        const float *src = slot(cta);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            float f[2];
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const float v = __ldcg(src + T::ROWS * D + mt * 16 + r * 8 + g);
+                                f[r] = v == -INFINITY ? 1.0f : ex2(v - up[mt][r]);
+                                l[mt][r] += __ldcg(src + T::ROWS * D + T::ROWS + mt * 16 + r * 8 + g) * f[r];
+                            }
+#pragma unroll
+                            for (int j = 0; j < T::NB; ++j) {
+                                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src) + (mt * T::NB + j) * 32 + lane);
+                                o[mt][j][0] = fmaf(v.x, f[0], o[mt][j][0]);
+                                o[mt][j][1] = fmaf(v.y, f[0], o[mt][j][1]);
+                                o[mt][j][2] = fmaf(v.z, f[1], o[mt][j][2]);
+                                o[mt][j][3] = fmaf(v.w, f[1], o[mt][j][3]);
+                            }
+                        }
+                    }
+                    tree_store<D, MT>(a, it, o, l, lane);
+                }
+            }
+        }
+        u = end;
+    }
+    if (!ok)  // a copy did not arrive in time: wait for those in flight (bounded) before the memory is given back
+        for (int k = max(0, asked - stages); k < asked; ++k)
+            mbar_wait(bar + k % stages, (uint32_t)(k / stages) & 1u, a.ctrl + MOE_CTRL_STATUS, a.wait_ns);
 }
 
 }  // namespace moe
