@@ -434,26 +434,75 @@ class Graph:
 
 
 # ------------------------------------------------------------------ speculative decoding
+#
+# These calls run between others of a few microseconds each, so their host side
+# is kept short: library and torch looked up once, addresses passed as integers.
 
-def _strided(t, name, dims):
-    """Device address of a tensor whose last dimension alone must be contiguous."""
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    return C.c_void_p(t.data_ptr())
+_rt = None
 
 
-def _typed(t, name, *dtypes):
-    if t is not None and hasattr(t, "dtype") and str(t.dtype).replace("torch.", "") not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(dtypes)}, not {t.dtype}")
-    return t
+class _Runtime:
+    def __init__(self):
+        import torch
+        self.lib = _lib.moe()
+        self.bf16, self.f32, self.i32 = torch.bfloat16, torch.float32, torch.int32
+        self.rows = (torch.bfloat16, torch.int16, torch.uint16)  # bf16 or its bit patterns
+        self.bits = (torch.int64, torch.uint64)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device, current = torch.cuda.current_device, torch.cuda.current_stream
+        self.stream = (lambda: raw(device())) if raw is not None else (lambda: current().cuda_stream)
 
 
-def _count(t, name, n):
-    if t is not None and hasattr(t, "numel") and t.numel() < n:
+def _runtime():
+    global _rt
+    if _rt is None:
+        _rt = _Runtime()
+    return _rt
+
+
+def _on(rt, stream):
+    if stream is None:
+        return rt.stream()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _dev(t, name, dtype, n):
+    """Device address of a contiguous tensor of at least n values; None stays NULL."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.numel() < n:
         raise ValueError(f"{name} holds {t.numel()} values, {n} are needed")
-    return t
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _matrix(t, name, dtype, rows, columns):
+    """Address and row stride of a [rows, columns] tensor whose rows are contiguous; None: NULL."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != columns:
+        raise ValueError(f"{name} must be [{rows}, {columns}], not {list(t.shape)}")
+    if columns > 1 and t.stride(1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr(), t.stride(0)
+
+
+def _heads(rt, cache, t, name, heads):
+    """Address, token stride and head stride of bf16 rows [tokens, heads, head_dim]."""
+    if t.dtype not in rt.rows:
+        raise ValueError(f"{name} must be bfloat16, not {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != cache.head_dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {cache.head_dim}], not {list(shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr(), st, sh
 
 
 @dataclass
@@ -466,6 +515,10 @@ class KvCache:
     page_size: int = 64
     format: int = MOE_KV_Q8
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_ref", None)
+
     def __post_init__(self):
         self.n_pages = 0
         per = kv_page_bytes(self)
@@ -475,9 +528,13 @@ class KvCache:
                 raise ValueError(f"pages holds {size} bytes, not a multiple of a page's {per}")
             self.n_pages = size // per
 
-    def c(self) -> _lib.MoeKvCache:
-        return _lib.MoeKvCache(_ptr(self.pages), self.n_pages, self.head_dim, self.n_kv_heads, self.page_size,
-                               self.format)
+    def ref(self):
+        """The C struct by reference, made again after a field was set."""
+        if self._ref is None:
+            c = _lib.MoeKvCache(_ptr(self.pages), self.n_pages, self.head_dim, self.n_kv_heads, self.page_size,
+                                self.format)
+            object.__setattr__(self, "_ref", C.byref(c))
+        return self._ref
 
 
 def kv_page_bytes(cache: KvCache) -> int:
@@ -487,43 +544,37 @@ def kv_page_bytes(cache: KvCache) -> int:
     return b.value
 
 
-def _rows(cache: KvCache, t, name, heads):
-    _typed(t, name, "bfloat16", "int16", "uint16")
-    p = _strided(t, name, 3)
-    if t.shape[1] != heads or t.shape[2] != cache.head_dim:
-        raise ValueError(f"{name} must be [tokens, {heads}, {cache.head_dim}], not {list(t.shape)}")
-    return p, t.stride(0), t.stride(1)
-
-
 def kv_append(cache: KvCache, k, v, slots, status=None, stream=None):
     """Quantise rows k, v (bf16 [tokens, n_kv_heads, head_dim], any strides of the
     first two) into slots (int32 [tokens], -1: skipped). status: None, or a
-    device word that receives MOE_WS_* bits."""
-    if k.shape[0] != v.shape[0]:
+    device word (int32) that receives MOE_WS_* bits."""
+    rt = _runtime()
+    n, heads = k.shape[0], cache.n_kv_heads
+    if n != v.shape[0]:
         raise ValueError("k and v must have the same number of tokens")
-    _count(_typed(slots, "slots", "int32"), "slots", k.shape[0])
-    _check(_lib.moe().moe_kv_append(C.byref(cache.c()), *_rows(cache, k, "k", cache.n_kv_heads),
-                                    *_rows(cache, v, "v", cache.n_kv_heads), _ptr(slots), k.shape[0],
-                                    _ptr(status), _stream(stream)))
+    rc = rt.lib.moe_kv_append(cache.ref(), *_heads(rt, cache, k, "k", heads), *_heads(rt, cache, v, "v", heads),
+                              _dev(slots, "slots", rt.i32, n), n, _dev(status, "status", rt.i32, 1), _on(rt, stream))
+    if rc:
+        _check(rc)
 
 
 def kv_read(cache: KvCache, slots, k_out, v_out, status=None, stream=None):
     """Rows of the cache as numbers: k_out, v_out bf16 or f32 [tokens, n_kv_heads, head_dim]."""
-    n = slots.numel()
-    _typed(slots, "slots", "int32")
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        _count(_typed(t, name, "bfloat16", "float32"), name, n * cache.n_kv_heads * cache.head_dim)
-    if k_out.dtype != v_out.dtype:
-        raise ValueError("k_out and v_out must have the same type")
-    kind = MOE_F32 if "float32" in str(k_out.dtype) else MOE_BF16
-    _check(_lib.moe().moe_kv_read(C.byref(cache.c()), _ptr(slots), n, _ptr(k_out), _ptr(v_out), kind, _ptr(status),
-                                  _stream(stream)))
+    rt = _runtime()
+    n, kind = slots.numel(), k_out.dtype
+    if kind is not rt.bf16 and kind is not rt.f32:
+        raise ValueError(f"k_out must be bfloat16 or float32, not {kind}")
+    size = n * cache.n_kv_heads * cache.head_dim
+    rc = rt.lib.moe_kv_read(cache.ref(), _dev(slots, "slots", rt.i32, n), n, _dev(k_out, "k_out", kind, size),
+                            _dev(v_out, "v_out", kind, size), MOE_F32 if kind is rt.f32 else MOE_BF16,
+                            _dev(status, "status", rt.i32, 1), _on(rt, stream))
+    if rc:
+        _check(rc)
 
 
 def tree_attention_workspace_bytes(cache: KvCache, n_q_heads: int, batch: int, n_tokens: int) -> int:
     b = C.c_size_t(0)
-    _check(_lib.moe().moe_tree_attention_workspace_bytes(C.byref(cache.c()), n_q_heads, batch, n_tokens,
-                                                         C.byref(b)))
+    _check(_lib.moe().moe_tree_attention_workspace_bytes(cache.ref(), n_q_heads, batch, n_tokens, C.byref(b)))
     return b.value
 
 
@@ -532,20 +583,21 @@ def tree_attention(cache: KvCache, q, out, q_start, kv_len, table, mask, scale: 
     moe_tree_attention): q, out bf16 [tokens, n_q_heads, head_dim], q_start int32
     [batch + 1], kv_len int32 [batch], table int32 [batch, pages], mask int64
     [tokens] of bits, or None for chains and single tokens."""
+    rt = _runtime()
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    heads, n, batch = q.shape[1], q.shape[0], kv_len.numel()
-    for t, name in ((q_start, "q_start"), (kv_len, "kv_len"), (table, "table")):
-        _typed(t, name, "int32")
-    _count(q_start, "q_start", batch + 1)
-    _count(_typed(mask, "mask", "int64", "uint64"), "mask", n)
-    tp = _strided(table, "table", 2)
-    if table.shape[0] < batch:
-        raise ValueError(f"table has {table.shape[0]} rows for {batch} sequences")
-    _check(_lib.moe().moe_tree_attention(C.byref(cache.c()), *_rows(cache, q, "q", heads),
-                                         *_rows(cache, out, "out", heads), heads, _ptr(q_start), _ptr(kv_len), tp,
-                                         table.stride(0), table.shape[1], _ptr(mask), batch, n, float(scale),
-                                         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    n, heads = q.shape[:2]
+    batch = kv_len.numel()
+    if mask is not None and mask.dtype not in rt.bits:
+        raise ValueError(f"mask must be int64, not {mask.dtype}")
+    tp, ts = _matrix(table, "table", rt.i32, batch, table.shape[-1])
+    rc = rt.lib.moe_tree_attention(cache.ref(), *_heads(rt, cache, q, "q", heads), *_heads(rt, cache, out, "out", heads),
+                                   heads, _dev(q_start, "q_start", rt.i32, batch + 1),
+                                   _dev(kv_len, "kv_len", rt.i32, batch), tp, ts, table.shape[1],
+                                   None if mask is None else _dev(mask, "mask", mask.dtype, n), batch, n, scale,
+                                   ws.data_ptr(), ws.numel() * ws.element_size(), _on(rt, stream))
+    if rc:
+        _check(rc)
 
 
 def spec_verify_workspace_bytes(batch: int, n_rows: int) -> int:
@@ -560,23 +612,20 @@ def spec_verify(logits, q_start, tokens, parents, draft, temperature, uniforms, 
     logits bf16 or f32 [rows, vocab], draft f32 [rows, vocab] or None, noise f32
     [batch, vocab]; the other inputs as there. Outputs int32: n_accepted [batch],
     path [rows], next_token [batch]."""
-    _typed(logits, "logits", "bfloat16", "float32")
-    lp = _strided(logits, "logits", 2)
+    rt = _runtime()
+    kind = logits.dtype
+    if kind is not rt.bf16 and kind is not rt.f32:
+        raise ValueError(f"logits must be bfloat16 or float32, not {kind}")
     rows, vocab = logits.shape
-    batch = next_token.numel()
-    for t, name, n in ((q_start, "q_start", batch + 1), (tokens, "tokens", rows), (parents, "parents", rows),
-                       (n_accepted, "n_accepted", batch), (path, "path", rows), (next_token, "next_token", batch)):
-        _count(_typed(t, name, "int32"), name, n)
-    for t, name, n in ((temperature, "temperature", batch), (uniforms, "uniforms", rows)):
-        _count(_typed(t, name, "float32"), name, n)
-    for t, name, n in ((draft, "draft", rows), (noise, "noise", batch)):
-        if _typed(t, name, "float32") is not None and (t.dim() != 2 or t.shape[0] < n or t.shape[1] != vocab):
-            raise ValueError(f"{name} must be [{n}, {vocab}], not {list(t.shape)}")
-    dp = None if draft is None else _strided(draft, "draft", 2)
-    np_ = None if noise is None else _strided(noise, "noise", 2)
-    _check(_lib.moe().moe_spec_verify(lp, MOE_F32 if "float32" in str(logits.dtype) else MOE_BF16,
-                                      logits.stride(0), _ptr(q_start), _ptr(tokens), _ptr(parents), dp,
-                                      0 if draft is None else draft.stride(0), _ptr(temperature), _ptr(uniforms),
-                                      np_, 0 if noise is None else noise.stride(0), batch, rows, vocab,
-                                      _ptr(n_accepted), _ptr(path), _ptr(next_token), _ptr(ws),
-                                      ws.numel() * ws.element_size(), _stream(stream)))
+    batch, i32, f32 = next_token.numel(), rt.i32, rt.f32
+    lp, ls = _matrix(logits, "logits", kind, rows, vocab)
+    dp, ds = _matrix(draft, "draft", f32, rows, vocab)
+    np_, ns = _matrix(noise, "noise", f32, batch, vocab)
+    rc = rt.lib.moe_spec_verify(lp, MOE_F32 if kind is f32 else MOE_BF16, ls, _dev(q_start, "q_start", i32, batch + 1),
+                                _dev(tokens, "tokens", i32, rows), _dev(parents, "parents", i32, rows), dp, ds,
+                                _dev(temperature, "temperature", f32, batch), _dev(uniforms, "uniforms", f32, rows),
+                                np_, ns, batch, rows, vocab, _dev(n_accepted, "n_accepted", i32, batch),
+                                _dev(path, "path", i32, rows), _dev(next_token, "next_token", i32, batch),
+                                ws.data_ptr(), ws.numel() * ws.element_size(), _on(rt, stream))
+    if rc:
+        _check(rc)

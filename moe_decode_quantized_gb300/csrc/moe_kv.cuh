@@ -22,6 +22,8 @@
 // Scales are f16, one (Q8) or a scale and a minimum (Q4) per 32 values:
 // K [token][group][1 or 2], V [1 or 2][group][token].
 #pragma once
+#include <cuda_bf16.h>
+
 #include "moe_common.cuh"
 
 #define MOE_KV_GROUP 32
@@ -41,21 +43,6 @@ struct KvDims {
     __host__ __device__ size_t page_bytes() const { return (size_t)heads * (page / 16) * block_bytes(); }
 };
 
-// byte offset in a block's K (V) codes of code byte i (0 <= i < RB) of token t
-__device__ __forceinline__ int kv_code_at(const KvDims &k, bool value, int t, int i)
-{
-    const int rb = k.row_bytes(), piece = value ? rb / 8 : rb / 4;
-    const int lane = value ? i / piece * 4 + (t & 7) / 2 : (t & 7) * 4 + i / piece;
-    const int x = (value ? (t / 8) * 2 + (t & 1) : t / 8) * piece + i % piece;
-    return (x >> 4) * 512 + lane * 16 + (x & 15);
-}
-
-// index of the f16 word z (0: scale, 1: minimum) of group g of token t
-__device__ __forceinline__ int kv_scale_at(const KvDims &k, bool value, int t, int g, int z)
-{
-    return value ? (z * k.groups() + g) * 16 + t : (t * k.groups() + g) * k.per() + z;
-}
-
 struct KvArgs {
     KvDims k;
     uint8_t *pages;
@@ -64,173 +51,291 @@ struct KvArgs {
     long long tok_stride[2], head_stride[2];  // elements
     const int32_t *slots;
     void *out[2];
-    int out_f32;
     int tokens;
     uint32_t *status;
 };
 
-__device__ __forceinline__ uint8_t *kv_half(const KvArgs &a, int slot, int head, int value)
+// The threads of both kernels take a tile of eight consecutive tokens of one
+// head the way the cache stores a half block: a warp's lanes are (token,
+// quarter of the row) for K and (eighth of the row, pair of tokens) for V, so
+// that where the tokens' slots are consecutive and aligned -- a prompt, a
+// long context -- a warp's accesses to the cache are whole lines. Any slots
+// are right.
+
+// the token of a tile that this lane works on; which: V's token of the pair
+__device__ __forceinline__ int kv_tile_token(bool value, int lane, int which)
 {
-    const int page = slot / a.k.page, in = slot % a.k.page;
-    const size_t block = ((size_t)page * a.k.heads + head) * (a.k.page / 16) + in / 16;
-    return a.pages + block * a.k.block_bytes() + (value ? a.k.half_bytes() : 0);
+    return value ? (lane & 3) * 2 + which : lane >> 2;
 }
 
-// Quantises and writes rows. Eight values a thread, D / 8 threads a row (a
-// row: K or V of one token and head), four neighbouring lanes a group. The
-// scale is rounded up and the minimum down to f16, so that no code is
-// clipped: |x - value| <= scale / 2 for the whole range. VEC: rows that a
-// 16-byte load can take (16-byte aligned with strides of 8 elements).
-template <bool VEC>
-__global__ void __launch_bounds__(256) moe_kv_append_kernel(const KvArgs a)
+// checked slot of a token of the call: -1 where there is nothing to do
+__device__ __forceinline__ int kv_slot(const KvArgs &a, int token)
 {
-    const int per_row = a.k.dim / 8;
-    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-    const long long row = id / per_row;
-    const int part = (int)(id % per_row);
-    const bool live = row < 2ll * a.tokens * a.k.heads;
-    int slot = -1, head = 0, value = 0;
-    long long token = 0;
-    if (live) {
-        head = (int)(row % a.k.heads);
-        token = row / a.k.heads;
-        value = token >= a.tokens;
-        token -= value ? a.tokens : 0;
-        slot = a.slots[token];
-        if (slot >= a.n_slots || slot < -1) {
-            if (a.status)
-                atomicOr(a.status, (uint32_t)MOE_WS_INDEX);
-            slot = -1;
-        }
-    }
-    float v[8];
-    bool odd = false;
-    if (slot >= 0) {
-        const uint16_t *p = a.src[value] + token * a.tok_stride[value] + head * a.head_stride[value] + part * 8;
-        uint32_t w[4];
-        if (VEC) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(p);
-            w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float f = i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-            odd |= !(fabsf(f) <= 3.402823466e38f);
-            f = f == f ? f : 0.0f;
-            v[i] = fminf(fmaxf(f, -MOE_KV_LIMIT), MOE_KV_LIMIT);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = 0.0f;
-    }
-    if (odd && a.status)
-        atomicOr(a.status, (uint32_t)MOE_WS_NONFINITE);
-    float lo = v[0], hi = v[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        lo = fminf(lo, v[i]);
-        hi = fmaxf(hi, v[i]);
-    }
-#pragma unroll
-    for (int m = 1; m < 4; m *= 2) {  // all 32 lanes take part: rows are whole groups of four lanes
-        lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, m));
-        hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, m));
-    }
-    if (slot < 0)
-        return;
-    uint8_t *half = kv_half(a, slot, head, value);
-    const int t = slot % 16, g = part / 4;
-    __half *scales = reinterpret_cast<__half *>(half + 16 * a.k.row_bytes());
-    if (a.k.fmt == MOE_KV_Q8) {
-        const __half d = __float2half_ru(__fdiv_rn(fmaxf(hi, -lo), 127.0f));
-        const float f = __half2float(d);
-        uint32_t c[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float r = f > 0.0f ? rintf(__fdiv_rn(v[i], f)) : 0.0f;
-            c[i >> 2] |= (uint32_t)((int)fminf(fmaxf(r, -127.0f), 127.0f) + 128) << (8 * (i & 3));
-        }
-        *reinterpret_cast<uint2 *>(half + kv_code_at(a.k, value, t, part * 8)) = make_uint2(c[0], c[1]);
-        if ((part & 3) == 0)
-            scales[kv_scale_at(a.k, value, t, g, 0)] = d;
-    } else {
-        const __half m = __float2half_rd(lo);
-        const float fm = __half2float(m);
-        const __half d = __float2half_ru(__fdiv_rn(__fsub_rn(hi, fm), 15.0f));
-        const float f = __half2float(d);
-        uint32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float r = f > 0.0f ? rintf(__fdiv_rn(__fsub_rn(v[i], fm), f)) : 0.0f;
-            c |= (uint32_t)(int)fminf(fmaxf(r, 0.0f), 15.0f) << (4 * (i >> 1) + 16 * (i & 1));
-        }
-        *reinterpret_cast<uint32_t *>(half + kv_code_at(a.k, value, t, part * 4)) = c;
-        if ((part & 3) == 0) {
-            scales[kv_scale_at(a.k, value, t, g, 0)] = d;
-            scales[kv_scale_at(a.k, value, t, g, 1)] = m;
-        }
-    }
-}
-
-// Eight values of a row of the cache in f32. c + 128 (Q8) and the 4-bit codes
-// times the scale are exact in f32; Q4's sum is rounded once.
-__device__ __forceinline__ void kv_values8(const KvDims &k, const uint8_t *half, bool value, int t, int part, float (&v)[8])
-{
-    const __half *scales = reinterpret_cast<const __half *>(half + 16 * k.row_bytes());
-    const int g = part / 4;
-    const float d = __half2float(scales[kv_scale_at(k, value, t, g, 0)]);
-    if (k.fmt == MOE_KV_Q8) {
-        const uint2 c = *reinterpret_cast<const uint2 *>(half + kv_code_at(k, value, t, part * 8));
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = (float)((int)((i < 4 ? c.x : c.y) >> (8 * (i & 3)) & 255u) - 128) * d;
-    } else {
-        const float m = __half2float(scales[kv_scale_at(k, value, t, g, 1)]);
-        const uint32_t c = *reinterpret_cast<const uint32_t *>(half + kv_code_at(k, value, t, part * 4));
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = fmaf((float)(c >> (4 * (i >> 1) + 16 * (i & 1)) & 15u), d, m);
-    }
-}
-
-// Reads rows back: eight values a thread, rounded once to bf16 or kept in f32.
-__global__ void __launch_bounds__(256) moe_kv_read_kernel(const KvArgs a)
-{
-    const int per_row = a.k.dim / 8;
-    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-    const long long row = id / per_row;
-    const int part = (int)(id % per_row);
-    if (row >= 2ll * a.tokens * a.k.heads)
-        return;
-    const int head = (int)(row % a.k.heads);
-    long long token = row / a.k.heads;
-    const int value = token >= a.tokens;
-    token -= value ? a.tokens : 0;
-    int slot = a.slots[token];
+    if (token >= a.tokens)
+        return -1;
+    const int slot = a.slots[token];
     if (slot >= a.n_slots || slot < -1) {
         if (a.status)
             atomicOr(a.status, (uint32_t)MOE_WS_INDEX);
-        slot = -1;
+        return -1;
     }
-    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (slot >= 0)
-        kv_values8(a.k, kv_half(a, slot, head, value), value, slot % 16, part, v);
-    const long long at = (token * a.k.heads + head) * a.k.dim + part * 8;
-    if (a.out_f32) {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out[value]) + at);
-        o[0] = make_float4(v[0], v[1], v[2], v[3]);
-        o[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        uint32_t w[4];
+    return slot;
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ uint8_t *kv_half(const KvArgs &a, int slot, int head, int value)
+{
+    constexpr int RB = FMT == MOE_KV_Q8 ? D : D / 2;
+    constexpr int HALF = 16 * RB + 16 * (D / MOE_KV_GROUP) * (FMT == MOE_KV_Q8 ? 2 : 4);
+    const unsigned page = (unsigned)slot / (unsigned)a.k.page, in = (unsigned)slot - page * a.k.page;
+    const size_t block = ((size_t)page * a.k.heads + head) * (a.k.page / 16) + in / 16;
+    return a.pages + block * (2 * HALF) + (value ? HALF : 0);
+}
+
+// Quantises one lane's values of a row (N of them: a quarter of a K row, an
+// eighth of a V row) and writes their codes and scales. A group of 32 is
+// within the lane (N >= 32) or over the lanes that hold the row's next
+// pieces (`step` lanes apart). The scale is rounded up and the minimum down to
+// f16, so that no code is clipped: |x - value| <= scale / 2 over the whole
+// range.
+template <int FMT, int D, int N, bool VALUE>
+__device__ __forceinline__ void kv_quantise(const KvArgs &a, uint8_t *half, int t, int lane, float (&v)[N])
+{
+    constexpr int RB = FMT == MOE_KV_Q8 ? D : D / 2, GR = D / MOE_KV_GROUP;
+    constexpr int NG = N >= 32 ? N / 32 : 1, PER = N / NG, STEP = VALUE ? 4 : 1;
+    constexpr int BYTES = N * RB / D, WORDS = BYTES / 4;
+    const int piece = VALUE ? lane >> 2 : lane & 3;
+    uint32_t w[WORDS];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = f32_to_bf16(v[2 * i]) | (uint32_t)f32_to_bf16(v[2 * i + 1]) << 16;
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out[value]) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < WORDS; ++i)
+        w[i] = 0;
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+        float lo = v[q * PER], hi = lo;
+#pragma unroll
+        for (int i = 1; i < PER; ++i) {
+            lo = fminf(lo, v[q * PER + i]);
+            hi = fmaxf(hi, v[q * PER + i]);
+        }
+#pragma unroll
+        for (int m = 1; m < MOE_KV_GROUP / PER; m *= 2) {
+            lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, m * STEP));
+            hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, m * STEP));
+        }
+        const int g = (piece * N + q * PER) / MOE_KV_GROUP;
+        const bool first = (piece * N + q * PER) % MOE_KV_GROUP == 0;  // of the group's lanes
+        if (FMT == MOE_KV_Q8) {
+            const __half d = __float2half_ru(__fdiv_rn(fmaxf(hi, -lo), 127.0f));
+            const float f = __half2float(d);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const float r = f > 0.0f ? rintf(__fdiv_rn(v[q * PER + i], f)) : 0.0f;
+                const int c = (int)fminf(fmaxf(r, -127.0f), 127.0f) + 128, e = q * PER + i;
+                w[e / 4] |= (uint32_t)c << (8 * (e & 3));
+            }
+            if (half && first)
+                reinterpret_cast<__half *>(half + 16 * RB)[VALUE ? g * 16 + t : t * GR + g] = d;
+        } else {
+            const __half m = __float2half_rd(lo);
+            const float fm = __half2float(m);
+            const __half d = __float2half_ru(__fdiv_rn(__fsub_rn(hi, fm), 15.0f));
+            const float f = __half2float(d);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const float r = f > 0.0f ? rintf(__fdiv_rn(__fsub_rn(v[q * PER + i], fm), f)) : 0.0f;
+                const int c = (int)fminf(fmaxf(r, 0.0f), 15.0f), e = q * PER + i;
+                w[e / 8] |= (uint32_t)c << (4 * (e % 8 / 2) + 16 * (e & 1));
+            }
+            if (half && first) {
+                __half *s = reinterpret_cast<__half *>(half + 16 * RB);
+                s[VALUE ? g * 16 + t : (t * GR + g) * 2] = d;
+                s[VALUE ? (GR + g) * 16 + t : (t * GR + g) * 2 + 1] = m;
+            }
+        }
+    }
+    if (!half)
+        return;
+    const int x = VALUE ? ((t >> 3) * 2 + (t & 1)) * BYTES : (t >> 3) * BYTES;
+    const int at = VALUE ? piece * 4 + ((t & 7) >> 1) : (t & 7) * 4 + piece;  // the slot's lane
+    uint8_t *p = half + (x >> 4) * 512 + at * 16 + (x & 15);
+    if constexpr (BYTES >= 16) {
+#pragma unroll
+        for (int i = 0; i < BYTES / 16; ++i)
+            *reinterpret_cast<uint4 *>(p + i * 512) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else if constexpr (BYTES == 8) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    } else {
+        *reinterpret_cast<uint32_t *>(p) = w[0];
+    }
+}
+
+template <int FMT, int D, int N, bool VALUE, bool WIDE>
+__device__ __forceinline__ void kv_append_row(const KvArgs &a, int token, int head, int lane)
+{
+    const int slot = kv_slot(a, token), piece = VALUE ? lane >> 2 : lane & 3;
+    float v[N];
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = 0.0f;
+    if (slot >= 0) {
+        const uint16_t *p = a.src[VALUE] + token * a.tok_stride[VALUE] + head * a.head_stride[VALUE] + piece * N;
+#pragma unroll
+        for (int i = 0; i < N; i += 8) {
+            uint32_t w[4];
+            if (WIDE) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(p + i);
+                w[0] = q.x;
+                w[1] = q.y;
+                w[2] = q.z;
+                w[3] = q.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = p[i + 2 * j] | (uint32_t)p[i + 2 * j + 1] << 16;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float f = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+                odd |= !(fabsf(f) <= 3.402823466e38f);
+                f = f == f ? f : 0.0f;
+                v[i + j] = fminf(fmaxf(f, -MOE_KV_LIMIT), MOE_KV_LIMIT);
+            }
+        }
+    }
+    if (odd && a.status)
+        atomicOr(a.status, (uint32_t)MOE_WS_NONFINITE);
+    kv_quantise<FMT, D, N, VALUE>(a, slot >= 0 ? kv_half<FMT, D>(a, slot, head, VALUE) : nullptr, slot & 15, lane, v);
+}
+
+#define MOE_KV_THREADS 256
+#define MOE_KV_APPEND_TILES (MOE_KV_THREADS / 32)  // 8 tokens x a head of K, or half of them of V, a warp
+
+// Quantises and writes rows: blockIdx.y = head x 3 + {K, V's even tokens, V's
+// odd tokens}, a warp a tile of eight tokens (four of V). WIDE: rows that
+// 16-byte loads can take. Bound by the reads and writes for a prompt, by
+// latency for a decode step.
+template <int FMT, int D, bool WIDE>
+__global__ void __launch_bounds__(MOE_KV_THREADS) moe_kv_append_kernel(const KvArgs a)
+{
+    const int lane = threadIdx.x & 31, part = blockIdx.y % 3, head = blockIdx.y / 3;
+    const int tile = (blockIdx.x * MOE_KV_APPEND_TILES + (threadIdx.x >> 5)) * 8;
+    if (tile >= a.tokens)
+        return;
+    if (part == 0)
+        kv_append_row<FMT, D, D / 4, false, WIDE>(a, tile + kv_tile_token(false, lane, 0), head, lane);
+    else
+        kv_append_row<FMT, D, D / 8, true, WIDE>(a, tile + kv_tile_token(true, lane, part - 1), head, lane);
+}
+
+// 32 bytes at once (8 words); p 32-byte aligned
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t *w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// one thread's piece of a row (BYTES of codes) as numbers
+template <int FMT, int D, bool VALUE, bool F32, bool WIDE>
+__device__ __forceinline__ void kv_read_piece(const KvArgs &a, int token, int head, int lane, int chunk)
+{
+    constexpr int RB = FMT == MOE_KV_Q8 ? D : D / 2, GR = D / MOE_KV_GROUP;
+    constexpr int PIECE = VALUE ? RB / 8 : RB / 4, BYTES = PIECE < 16 ? PIECE : 16;
+    constexpr int N = BYTES * D / RB, WORDS = BYTES / 4;
+    if (token >= a.tokens)
+        return;
+    const int slot = kv_slot(a, token);
+    const int d0 = (VALUE ? lane >> 2 : lane & 3) * (PIECE * D / RB) + chunk * N;  // first dimension
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = 0.0f;
+    if (slot >= 0) {
+        const uint8_t *half = kv_half<FMT, D>(a, slot, head, VALUE);
+        const int t = slot & 15, g = d0 / MOE_KV_GROUP;
+        const int x = (VALUE ? (t >> 3) * 2 + (t & 1) : t >> 3) * PIECE + chunk * 16;
+        const int at = VALUE ? (lane & ~3) + ((t & 7) >> 1) : (t & 7) * 4 + (lane & 3);  // the slot's lane
+        const uint8_t *p = half + (x >> 4) * 512 + at * 16 + (x & 15);
+        uint32_t w[WORDS];
+        if constexpr (BYTES == 16) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(p);
+            w[0] = q.x;
+            w[1] = q.y;
+            w[2] = q.z;
+            w[3] = q.w;
+        } else if constexpr (BYTES == 8) {
+            const uint2 q = *reinterpret_cast<const uint2 *>(p);
+            w[0] = q.x;
+            w[1] = q.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        }
+        const __half *s = reinterpret_cast<const __half *>(half + 16 * RB);
+        // a code in the low bits of 2^23 is 2^23 + code: exact, as is its product with the f16 scale
+        if (FMT == MOE_KV_Q8) {
+            const float d = __half2float(s[VALUE ? g * 16 + t : t * GR + g]);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] = (__uint_as_float(__byte_perm(w[i / 4], 0x4B000000u, 0x7440 | (i & 3))) - 8388736.0f) * d;
+        } else {
+            const float d = __half2float(s[VALUE ? g * 16 + t : (t * GR + g) * 2]);
+            const float m = __half2float(s[VALUE ? (GR + g) * 16 + t : (t * GR + g) * 2 + 1]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t c = w[i / 8] >> (4 * (i % 8 / 2) + 16 * (i & 1)) & 15u;
+                v[i] = fmaf(__uint_as_float(c | 0x4B000000u) - 8388608.0f, d, m);
+            }
+        }
+    }
+    constexpr int OUT = F32 ? N : N / 2;  // words
+    uint32_t o[OUT];
+#pragma unroll
+    for (int i = 0; i < OUT; ++i) {
+        if (F32) {
+            o[i] = __float_as_uint(v[i]);
+        } else {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            o[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+    }
+    uint8_t *q = static_cast<uint8_t *>(a.out[VALUE]) + (((size_t)token * a.k.heads + head) * D + d0) * (F32 ? 4 : 2);
+    if constexpr (OUT >= 8 && WIDE) {
+#pragma unroll
+        for (int i = 0; i < OUT; i += 8)
+            st_global_32(q + 4 * i, o + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < OUT; i += 4)
+            *reinterpret_cast<uint4 *>(q + 4 * i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    }
+}
+
+// threads of a tile of eight tokens of one head: 16-byte (or smaller) pieces of codes
+template <int FMT, int D, bool VALUE>
+__host__ __device__ constexpr int kv_read_threads()
+{
+    constexpr int RB = FMT == MOE_KV_Q8 ? D : D / 2, PIECE = VALUE ? RB / 8 : RB / 4;
+    return 8 * RB / (PIECE < 16 ? PIECE : 16);
+}
+
+// Reads rows back: blockIdx.y = head x 2 + {K, V}; a thread one piece of codes
+// as 8, 16 or 32 numbers, rounded once to bf16 or kept in f32. WIDE: outputs
+// on 32-byte boundaries (the stores are then whole sectors). Bound by the
+// reads and writes.
+template <int FMT, int D, bool F32, bool WIDE>
+__global__ void __launch_bounds__(MOE_KV_THREADS) moe_kv_read_kernel(const KvArgs a)
+{
+    constexpr int NK = kv_read_threads<FMT, D, false>(), NV = kv_read_threads<FMT, D, true>();
+    const int head = blockIdx.y >> 1;
+    const int lane = threadIdx.x & 31;
+    if ((blockIdx.y & 1) == 0) {
+        const int tile = blockIdx.x * (MOE_KV_THREADS / NK) + threadIdx.x / NK;
+        kv_read_piece<FMT, D, false, F32, WIDE>(a, tile * 8 + kv_tile_token(false, lane, 0), head, lane,
+                                                threadIdx.x % NK / 32);
+    } else {
+        const int tile = blockIdx.x * (MOE_KV_THREADS / NV) + threadIdx.x / NV, x = threadIdx.x % NV / 32;
+        kv_read_piece<FMT, D, true, F32, WIDE>(a, tile * 8 + kv_tile_token(true, lane, x & 1), head, lane, x >> 1);
     }
 }
 

@@ -59,14 +59,33 @@ int check_cache(const moe_kv_cache *c, KvDims &k)
     return MOE_OK;
 }
 
-// one thread per eight values of the K and V rows of n tokens
-int row_grid(const KvDims &k, int n, unsigned &grid)
+// ---- the cache's kernels
+
+using KvKernel = void (*)(KvArgs);
+
+template <int FMT, int D>
+KvKernel kv_append_kernel(bool wide)
 {
-    const long long blocks = (2ll * n * k.heads * (k.dim / 8) + 255) / 256;
-    if (blocks > 0x7FFFFFFFll)
-        return host_fail(MOE_EUNSUPPORTED, "%d tokens in one call", n);
-    grid = (unsigned)blocks;
-    return MOE_OK;
+    return wide ? moe_kv_append_kernel<FMT, D, true> : moe_kv_append_kernel<FMT, D, false>;
+}
+
+template <int FMT, int D>
+KvKernel kv_read_kernel(bool f32, bool wide)
+{
+    if (f32)
+        return wide ? moe_kv_read_kernel<FMT, D, true, true> : moe_kv_read_kernel<FMT, D, true, false>;
+    return wide ? moe_kv_read_kernel<FMT, D, false, true> : moe_kv_read_kernel<FMT, D, false, false>;
+}
+
+// f<format, head size>() of the cache's
+template <typename F>
+auto with_kv(const KvDims &k, F &&f)
+{
+    if (k.fmt == MOE_KV_Q8)
+        return k.dim == 64 ? f(IntC<MOE_KV_Q8>{}, IntC<64>{}) : k.dim == 128 ? f(IntC<MOE_KV_Q8>{}, IntC<128>{})
+                                                                              : f(IntC<MOE_KV_Q8>{}, IntC<256>{});
+    return k.dim == 64 ? f(IntC<MOE_KV_Q4>{}, IntC<64>{}) : k.dim == 128 ? f(IntC<MOE_KV_Q4>{}, IntC<128>{})
+                                                                          : f(IntC<MOE_KV_Q4>{}, IntC<256>{});
 }
 
 // ---- tree attention: instances and their launch shape
@@ -164,7 +183,7 @@ int moe_kv_append(const moe_kv_cache *cache, const void *k_dev, int64_t k_token_
                   int n_tokens, uint32_t *status_dev, moe_stream_t stream)
 {
     KvArgs a{};
-    int rc = check_cache(cache, a.k);
+    const int rc = check_cache(cache, a.k);
     if (rc)
         return rc;
     if (n_tokens < 0 || (n_tokens > 0 && (!k_dev || !v_dev || !slots_dev)))
@@ -173,9 +192,6 @@ int moe_kv_append(const moe_kv_cache *cache, const void *k_dev, int64_t k_token_
         return host_fail(MOE_EINVAL, "moe_kv_append: an argument is not aligned to its type");
     if (n_tokens == 0)
         return MOE_OK;
-    unsigned grid;
-    if ((rc = row_grid(a.k, n_tokens, grid)))
-        return rc;
     a.pages = static_cast<uint8_t *>(cache->pages);
     a.n_slots = cache->n_pages * cache->page_size;
     a.src[0] = static_cast<const uint16_t *>(k_dev);
@@ -189,7 +205,12 @@ int moe_kv_append(const moe_kv_cache *cache, const void *k_dev, int64_t k_token_
     a.status = status_dev;
     const bool wide = aligned(k_dev, 16) && aligned(v_dev, 16) &&
                       (k_token_stride | k_head_stride | v_token_stride | v_head_stride) % 8 == 0;
-    (wide ? moe_kv_append_kernel<true> : moe_kv_append_kernel<false>)<<<grid, 256, 0, (cudaStream_t)stream>>>(a);
+    const KvKernel kernel =
+        with_kv(a.k, [&](auto f, auto d) { return kv_append_kernel<decltype(f)::value, decltype(d)::value>(wide); });
+    const int tiles = (n_tokens + 7) / 8;
+    const int warps = std::min(MOE_KV_APPEND_TILES, tiles);
+    const dim3 grid((tiles + warps - 1) / warps, 3 * a.k.heads);
+    kernel<<<grid, warps * 32, 0, (cudaStream_t)stream>>>(a);
     SPEC_CUDA_OK(cudaGetLastError());
     return MOE_OK;
 }
@@ -198,7 +219,7 @@ int moe_kv_read(const moe_kv_cache *cache, const int32_t *slots_dev, int n_token
                 int out_type, uint32_t *status_dev, moe_stream_t stream)
 {
     KvArgs a{};
-    int rc = check_cache(cache, a.k);
+    const int rc = check_cache(cache, a.k);
     if (rc)
         return rc;
     if (n_tokens < 0 || (n_tokens > 0 && (!k_out_dev || !v_out_dev || !slots_dev)))
@@ -209,18 +230,25 @@ int moe_kv_read(const moe_kv_cache *cache, const int32_t *slots_dev, int n_token
         return host_fail(MOE_EINVAL, "moe_kv_read: outputs must be 16-byte aligned, slots and status 4-byte");
     if (n_tokens == 0)
         return MOE_OK;
-    unsigned grid;
-    if ((rc = row_grid(a.k, n_tokens, grid)))
-        return rc;
     a.pages = static_cast<uint8_t *>(cache->pages);
     a.n_slots = cache->n_pages * cache->page_size;
     a.slots = slots_dev;
     a.out[0] = k_out_dev;
     a.out[1] = v_out_dev;
-    a.out_f32 = out_type == MOE_F32;
     a.tokens = n_tokens;
     a.status = status_dev;
-    moe_kv_read_kernel<<<grid, 256, 0, (cudaStream_t)stream>>>(a);
+    const bool f32 = out_type == MOE_F32, wide = aligned(k_out_dev, 32) && aligned(v_out_dev, 32);
+    KvKernel kernel = nullptr;
+    int per = 0;  // the more threads that K's or V's tile of eight tokens takes
+    with_kv(a.k, [&](auto f, auto d) {
+        constexpr int F = decltype(f)::value, D = decltype(d)::value;
+        kernel = kv_read_kernel<F, D>(f32, wide);
+        per = std::max(kv_read_threads<F, D, false>(), kv_read_threads<F, D, true>());
+        return 0;
+    });
+    const long long threads = (n_tokens + 7) / 8 * (long long)per;
+    const dim3 grid((unsigned)((threads + MOE_KV_THREADS - 1) / MOE_KV_THREADS), 2 * a.k.heads);
+    kernel<<<grid, MOE_KV_THREADS, 0, (cudaStream_t)stream>>>(a);
     SPEC_CUDA_OK(cudaGetLastError());
     return MOE_OK;
 }

@@ -20,8 +20,6 @@
 // products, the weights as the A fragments of o += P V. Bound by the copies
 // while the rows are few; 16 rows cost 32 products a unit of 128 dimensions.
 #pragma once
-#include <cuda_bf16.h>
-
 #include "moe_kv.cuh"
 
 namespace moe {
