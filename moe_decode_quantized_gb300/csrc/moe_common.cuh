@@ -306,6 +306,14 @@ __device__ __forceinline__ float fma_bf16x8(const uint4 &w, const uint4 &x, floa
     return s;
 }
 
+// 2^x by the special-function unit (2 ulp; 0 below 2^-126)
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // clamped SwiGLU in f32: silu(min(g, L)) * clamp(u, -L, L); L <= 0: no clamp
 __device__ __forceinline__ float swiglu_f32(float g, float u, float limit)
 {

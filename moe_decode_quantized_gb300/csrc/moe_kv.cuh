@@ -55,14 +55,13 @@ struct KvArgs {
     uint32_t *status;
 };
 
-// The threads of both kernels take a tile of eight consecutive tokens of one
-// head the way the cache stores a half block: a warp's lanes are (token,
-// quarter of the row) for K and (eighth of the row, pair of tokens) for V, so
-// that where the tokens' slots are consecutive and aligned -- a prompt, a
-// long context -- a warp's accesses to the cache are whole lines. Any slots
-// are right.
+// A warp of both kernels works on consecutive tokens of one head the way the
+// cache stores them, so that where the tokens' slots are consecutive and
+// aligned -- a prompt, a long context -- its accesses are whole lines: lanes
+// are (token, piece of the row) for K, (eighth of the row, pair of tokens)
+// for V. Any slots are right.
 
-// the token of a tile that this lane works on; which: V's token of the pair
+// the token of eight that this lane works on; which: V's token of the pair
 __device__ __forceinline__ int kv_tile_token(bool value, int lane, int which)
 {
     return value ? (lane & 3) * 2 + which : lane >> 2;
@@ -92,76 +91,161 @@ __device__ __forceinline__ uint8_t *kv_half(const KvArgs &a, int slot, int head,
     return a.pages + block * (2 * HALF) + (value ? HALF : 0);
 }
 
-// Quantises one lane's values of a row (N of them: a quarter of a K row, an
-// eighth of a V row) and writes their codes and scales. A group of 32 is
-// within the lane (N >= 32) or over the lanes that hold the row's next
-// pieces (`step` lanes apart). The scale is rounded up and the minimum down to
-// f16, so that no code is clipped: |x - value| <= scale / 2 over the whole
-// range.
-template <int FMT, int D, int N, bool VALUE>
-__device__ __forceinline__ void kv_quantise(const KvArgs &a, uint8_t *half, int t, int lane, float (&v)[N])
+// rint(y / f) of a lane's group values, f > 0 (inv = 1 / f, or both 0), as
+// 1.5 2^23 + code: the product with the reciprocal is within 2^-16 of the
+// quotient (codes up to 127), so its rounding is the quotient's unless it
+// lies within 2^-15 of the middle between two codes; `near` then says that
+// the quotients have to be divided out (ties, and what rounds to one).
+__device__ __forceinline__ float kv_round(float y, float inv, bool &near)
 {
-    constexpr int RB = FMT == MOE_KV_Q8 ? D : D / 2, GR = D / MOE_KV_GROUP;
-    constexpr int NG = N >= 32 ? N / 32 : 1, PER = N / NG, STEP = VALUE ? 4 : 1;
-    constexpr int BYTES = N * RB / D, WORDS = BYTES / 4;
-    const int piece = VALUE ? lane >> 2 : lane & 3;
-    uint32_t w[WORDS];
+    const float q = __fmul_rn(y, inv), t = __fadd_rn(q, 12582912.0f);
+    near |= fabsf(__fsub_rn(q, __fadd_rn(t, -12582912.0f))) >= 0.5f - 3.0517578e-5f;
+    return t;
+}
+
+// the same by the division itself
+__device__ __forceinline__ float kv_divide(float y, float f)
+{
+    return __fadd_rn(f > 0.0f ? rintf(__fdiv_rn(y, f)) : 0.0f, 12582912.0f);
+}
+
+__device__ __forceinline__ __nv_bfloat162 bf2(uint32_t v) { return *reinterpret_cast<__nv_bfloat162 *>(&v); }
+
+// 32 bytes at once (8 words); p 32-byte aligned
+__device__ __forceinline__ void ld_global_32(const void *p, uint32_t *w)
+{
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+
+// Quantises and writes one lane's piece of a row: N values from dimension
+// piece N. A group of 32 is the lane's own (N = 32) or shared with the lanes
+// of the row's neighbouring pieces, 1 (K) or 4 (V) apart. The scale is rounded
+// up and the minimum down to f16, so that no code is clipped: |x - value| <=
+// scale / 2 over the whole range. ALIGN: 32, 16 or 2, what rows and strides
+// are multiples of in bytes.
+template <int FMT, int D, int N, bool VALUE, int ALIGN>
+__device__ __forceinline__ void kv_append_piece(const KvArgs &a, int token, int head, int lane, int piece)
+{
+    constexpr int RB = FMT == MOE_KV_Q8 ? D : D / 2, GR = D / MOE_KV_GROUP, BYTES = N * RB / D;
+    uint32_t in[N / 2];
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i)
-        w[i] = 0;
+    for (int i = 0; i < N / 2; ++i)
+        in[i] = 0;
+    if (token < a.tokens) {  // also a skipped token's: the load does not wait for the slot
+        const uint16_t *p = a.src[VALUE] + token * a.tok_stride[VALUE] + head * a.head_stride[VALUE] + piece * N;
+        if constexpr (ALIGN == 32 && N >= 16) {
 #pragma unroll
-    for (int q = 0; q < NG; ++q) {
-        float lo = v[q * PER], hi = lo;
+            for (int i = 0; i < N / 2; i += 8)
+                ld_global_32(p + 2 * i, in + i);
+        } else if constexpr (ALIGN >= 16) {
 #pragma unroll
-        for (int i = 1; i < PER; ++i) {
-            lo = fminf(lo, v[q * PER + i]);
-            hi = fmaxf(hi, v[q * PER + i]);
-        }
-#pragma unroll
-        for (int m = 1; m < MOE_KV_GROUP / PER; m *= 2) {
-            lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, m * STEP));
-            hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, m * STEP));
-        }
-        const int g = (piece * N + q * PER) / MOE_KV_GROUP;
-        const bool first = (piece * N + q * PER) % MOE_KV_GROUP == 0;  // of the group's lanes
-        if (FMT == MOE_KV_Q8) {
-            const __half d = __float2half_ru(__fdiv_rn(fmaxf(hi, -lo), 127.0f));
-            const float f = __half2float(d);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const float r = f > 0.0f ? rintf(__fdiv_rn(v[q * PER + i], f)) : 0.0f;
-                const int c = (int)fminf(fmaxf(r, -127.0f), 127.0f) + 128, e = q * PER + i;
-                w[e / 4] |= (uint32_t)c << (8 * (e & 3));
+            for (int i = 0; i < N / 2; i += 4) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(p + 2 * i);
+                in[i] = q.x;
+                in[i + 1] = q.y;
+                in[i + 2] = q.z;
+                in[i + 3] = q.w;
             }
-            if (half && first)
-                reinterpret_cast<__half *>(half + 16 * RB)[VALUE ? g * 16 + t : t * GR + g] = d;
         } else {
-            const __half m = __float2half_rd(lo);
-            const float fm = __half2float(m);
-            const __half d = __float2half_ru(__fdiv_rn(__fsub_rn(hi, fm), 15.0f));
-            const float f = __half2float(d);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const float r = f > 0.0f ? rintf(__fdiv_rn(__fsub_rn(v[q * PER + i], fm), f)) : 0.0f;
-                const int c = (int)fminf(fmaxf(r, 0.0f), 15.0f), e = q * PER + i;
-                w[e / 8] |= (uint32_t)c << (4 * (e % 8 / 2) + 16 * (e & 1));
-            }
-            if (half && first) {
-                __half *s = reinterpret_cast<__half *>(half + 16 * RB);
-                s[VALUE ? g * 16 + t : (t * GR + g) * 2] = d;
-                s[VALUE ? (GR + g) * 16 + t : (t * GR + g) * 2 + 1] = m;
-            }
+            for (int i = 0; i < N / 2; ++i)
+                in[i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
         }
     }
-    if (!half)
+    const int slot = kv_slot(a, token);
+    // the extremes, two values at a time; NaN stays, and with what is out of range leads to the slow way
+    __nv_bfloat162 least = bf2(in[0]), most = least;
+#pragma unroll
+    for (int i = 1; i < N / 2; ++i) {
+        least = __hmin2_nan(least, bf2(in[i]));
+        most = __hmax2_nan(most, bf2(in[i]));
+    }
+    float lo = __low2float(__hmin2_nan(least, __lowhigh2highlow(least)));
+    float hi = __low2float(__hmax2_nan(most, __lowhigh2highlow(most)));
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = i & 1 ? bf16_hi(in[i >> 1]) : bf16_lo(in[i >> 1]);
+    if (!(lo >= -MOE_KV_LIMIT && hi <= MOE_KV_LIMIT)) {
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            odd |= !(fabsf(v[i]) <= 3.402823466e38f);
+            v[i] = fminf(fmaxf(v[i] == v[i] ? v[i] : 0.0f, -MOE_KV_LIMIT), MOE_KV_LIMIT);
+            lo = i ? fminf(lo, v[i]) : v[i];
+            hi = i ? fmaxf(hi, v[i]) : v[i];
+        }
+        if (odd && slot >= 0 && a.status)
+            atomicOr(a.status, (uint32_t)MOE_WS_NONFINITE);
+    }
+#pragma unroll
+    for (int m = 1; m < MOE_KV_GROUP / N; m *= 2) {  // every lane of the warp is here
+        lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, m * (VALUE ? 4 : 1)));
+        hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, m * (VALUE ? 4 : 1)));
+    }
+    if (slot < 0)
         return;
-    const int x = VALUE ? ((t >> 3) * 2 + (t & 1)) * BYTES : (t >> 3) * BYTES;
-    const int at = VALUE ? piece * 4 + ((t & 7) >> 1) : (t & 7) * 4 + piece;  // the slot's lane
+    uint8_t *half = kv_half<FMT, D>(a, slot, head, VALUE);
+    const int t = slot & 15, g = piece * N / MOE_KV_GROUP;
+    const bool first = piece * N % MOE_KV_GROUP == 0;  // of the group's lanes
+    __half *s = reinterpret_cast<__half *>(half + 16 * RB);
+    uint32_t w[BYTES / 4];
+    float code[N];
+    bool near = false;
+    if (FMT == MOE_KV_Q8) {
+        const __half d = __float2half_ru(__fdiv_rn(fmaxf(hi, -lo), 127.0f));
+        const float f = __half2float(d), inv = f > 0.0f ? __fdiv_rn(1.0f, f) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            code[i] = kv_round(v[i], inv, near);
+        if (near) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                code[i] = kv_divide(v[i], f);
+        }
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {  // the codes' low bytes, and 128 added
+            const uint32_t x = __byte_perm(__float_as_uint(code[i]), __float_as_uint(code[i + 1]), 0x0040);
+            const uint32_t y = __byte_perm(__float_as_uint(code[i + 2]), __float_as_uint(code[i + 3]), 0x0040);
+            w[i / 4] = __byte_perm(x, y, 0x5410) ^ 0x80808080u;
+        }
+        if (first)
+            s[VALUE ? g * 16 + t : t * GR + g] = d;
+    } else {
+        const __half m = __float2half_rd(lo);
+        const float fm = __half2float(m);
+        const __half d = __float2half_ru(__fdiv_rn(__fsub_rn(hi, fm), 15.0f));
+        const float f = __half2float(d), inv = f > 0.0f ? __fdiv_rn(1.0f, f) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            code[i] = kv_round(__fsub_rn(v[i], fm), inv, near);
+        if (near) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                code[i] = kv_divide(__fsub_rn(v[i], fm), f);
+        }
+#pragma unroll
+        for (int i = 0; i < N; i += 8) {
+            w[i / 8] = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                w[i / 8] |= (__float_as_uint(code[i + k]) & 15u) << (4 * (k / 2) + 16 * (k & 1));
+        }
+        if (first) {
+            s[VALUE ? g * 16 + t : (t * GR + g) * 2] = d;
+            s[VALUE ? (GR + g) * 16 + t : (t * GR + g) * 2 + 1] = m;
+        }
+    }
+    constexpr int PIECE = VALUE ? RB / 8 : RB / 4;  // bytes of a lane of the layout
+    const int i = piece * BYTES, x = (VALUE ? (t >> 3) * 2 + (t & 1) : t >> 3) * PIECE + i % PIECE;
+    const int at = VALUE ? i / PIECE * 4 + ((t & 7) >> 1) : (t & 7) * 4 + i / PIECE;
     uint8_t *p = half + (x >> 4) * 512 + at * 16 + (x & 15);
     if constexpr (BYTES >= 16) {
 #pragma unroll
-        for (int i = 0; i < BYTES / 16; ++i)
-            *reinterpret_cast<uint4 *>(p + i * 512) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int k = 0; k < BYTES / 16; ++k)
+            *reinterpret_cast<uint4 *>(p + k * 512) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
     } else if constexpr (BYTES == 8) {
         *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     } else {
@@ -169,63 +253,29 @@ __device__ __forceinline__ void kv_quantise(const KvArgs &a, uint8_t *half, int 
     }
 }
 
-template <int FMT, int D, int N, bool VALUE, bool WIDE>
-__device__ __forceinline__ void kv_append_row(const KvArgs &a, int token, int head, int lane)
-{
-    const int slot = kv_slot(a, token), piece = VALUE ? lane >> 2 : lane & 3;
-    float v[N];
-    bool odd = false;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        v[i] = 0.0f;
-    if (slot >= 0) {
-        const uint16_t *p = a.src[VALUE] + token * a.tok_stride[VALUE] + head * a.head_stride[VALUE] + piece * N;
-#pragma unroll
-        for (int i = 0; i < N; i += 8) {
-            uint32_t w[4];
-            if (WIDE) {
-                const uint4 q = *reinterpret_cast<const uint4 *>(p + i);
-                w[0] = q.x;
-                w[1] = q.y;
-                w[2] = q.z;
-                w[3] = q.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = p[i + 2 * j] | (uint32_t)p[i + 2 * j + 1] << 16;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float f = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
-                odd |= !(fabsf(f) <= 3.402823466e38f);
-                f = f == f ? f : 0.0f;
-                v[i + j] = fminf(fmaxf(f, -MOE_KV_LIMIT), MOE_KV_LIMIT);
-            }
-        }
-    }
-    if (odd && a.status)
-        atomicOr(a.status, (uint32_t)MOE_WS_NONFINITE);
-    kv_quantise<FMT, D, N, VALUE>(a, slot >= 0 ? kv_half<FMT, D>(a, slot, head, VALUE) : nullptr, slot & 15, lane, v);
-}
-
 #define MOE_KV_THREADS 256
-#define MOE_KV_APPEND_TILES (MOE_KV_THREADS / 32)  // 8 tokens x a head of K, or half of them of V, a warp
 
-// Quantises and writes rows: blockIdx.y = head x 3 + {K, V's even tokens, V's
-// odd tokens}, a warp a tile of eight tokens (four of V). WIDE: rows that
-// 16-byte loads can take. Bound by the reads and writes for a prompt, by
-// latency for a decode step.
-template <int FMT, int D, bool WIDE>
+// tokens of a warp: K's pieces are 16 values, V's an eighth of a row
+template <int D, bool VALUE>
+__host__ __device__ constexpr int kv_append_tokens() { return VALUE ? 4 : 512 / D; }
+
+// Quantises and writes rows: blockIdx.y = head x 2 + {K, V}. Bound by the
+// reads and writes for a prompt, by latency for a decode step.
+template <int FMT, int D, int ALIGN>
 __global__ void __launch_bounds__(MOE_KV_THREADS) moe_kv_append_kernel(const KvArgs a)
 {
-    const int lane = threadIdx.x & 31, part = blockIdx.y % 3, head = blockIdx.y / 3;
-    const int tile = (blockIdx.x * MOE_KV_APPEND_TILES + (threadIdx.x >> 5)) * 8;
-    if (tile >= a.tokens)
-        return;
-    if (part == 0)
-        kv_append_row<FMT, D, D / 4, false, WIDE>(a, tile + kv_tile_token(false, lane, 0), head, lane);
-    else
-        kv_append_row<FMT, D, D / 8, true, WIDE>(a, tile + kv_tile_token(true, lane, part - 1), head, lane);
+    const int lane = threadIdx.x & 31, head = blockIdx.y >> 1;
+    const int warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if ((blockIdx.y & 1) == 0) {
+        const int token = warp * kv_append_tokens<D, false>();
+        if (token < a.tokens)
+            kv_append_piece<FMT, D, 16, false, ALIGN>(a, token + lane / (D / 16), head, lane, lane % (D / 16));
+    } else {
+        const int token = (warp >> 1) * 8;  // two warps eight tokens
+        if (token < a.tokens)
+            kv_append_piece<FMT, D, D / 8, true, ALIGN>(a, token + kv_tile_token(true, lane, warp & 1), head, lane,
+                                                        lane >> 2);
+    }
 }
 
 // 32 bytes at once (8 words); p 32-byte aligned

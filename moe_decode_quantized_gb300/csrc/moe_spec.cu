@@ -64,9 +64,11 @@ int check_cache(const moe_kv_cache *c, KvDims &k)
 using KvKernel = void (*)(KvArgs);
 
 template <int FMT, int D>
-KvKernel kv_append_kernel(bool wide)
+KvKernel kv_append_kernel(int align)
 {
-    return wide ? moe_kv_append_kernel<FMT, D, true> : moe_kv_append_kernel<FMT, D, false>;
+    return align >= 32   ? moe_kv_append_kernel<FMT, D, 32>
+           : align >= 16 ? moe_kv_append_kernel<FMT, D, 16>
+                         : moe_kv_append_kernel<FMT, D, 2>;
 }
 
 template <int FMT, int D>
@@ -87,6 +89,24 @@ auto with_kv(const KvDims &k, F &&f)
     return k.dim == 64 ? f(IntC<MOE_KV_Q4>{}, IntC<64>{}) : k.dim == 128 ? f(IntC<MOE_KV_Q4>{}, IntC<128>{})
                                                                           : f(IntC<MOE_KV_Q4>{}, IntC<256>{});
 }
+
+// ---- verification
+
+using VerifyKernel = void (*)(VerifyArgs);
+
+template <bool AHEAD>
+VerifyKernel verify_kernel(bool f32, bool wide)
+{
+    return f32 ? (wide ? moe_verify_kernel<true, true, AHEAD> : moe_verify_kernel<true, false, AHEAD>)
+               : (wide ? moe_verify_kernel<false, true, AHEAD> : moe_verify_kernel<false, false, AHEAD>);
+}
+
+VerifyKernel verify_kernel(bool f32, bool wide, bool ahead)
+{
+    return ahead ? verify_kernel<true>(f32, wide) : verify_kernel<false>(f32, wide);
+}
+
+#define MOE_VERIFY_AHEAD_BYTES (48u << 20)
 
 // ---- tree attention: instances and their launch shape
 
@@ -203,14 +223,20 @@ int moe_kv_append(const moe_kv_cache *cache, const void *k_dev, int64_t k_token_
     a.slots = slots_dev;
     a.tokens = n_tokens;
     a.status = status_dev;
-    const bool wide = aligned(k_dev, 16) && aligned(v_dev, 16) &&
-                      (k_token_stride | k_head_stride | v_token_stride | v_head_stride) % 8 == 0;
-    const KvKernel kernel =
-        with_kv(a.k, [&](auto f, auto d) { return kv_append_kernel<decltype(f)::value, decltype(d)::value>(wide); });
-    const int tiles = (n_tokens + 7) / 8;
-    const int warps = std::min(MOE_KV_APPEND_TILES, tiles);
-    const dim3 grid((tiles + warps - 1) / warps, 3 * a.k.heads);
-    kernel<<<grid, warps * 32, 0, (cudaStream_t)stream>>>(a);
+    int align = 32;  // bytes that every row starts at a multiple of, 32, 16 or 2
+    while (align > 2 && !(aligned(k_dev, align) && aligned(v_dev, align) &&
+                          (k_token_stride | k_head_stride | v_token_stride | v_head_stride) * 2 % align == 0))
+        align = align == 32 ? 16 : 2;
+    KvKernel kernel = nullptr;
+    int most = 0;  // warps a head: the more of K's and V's
+    with_kv(a.k, [&](auto f, auto d) {
+        constexpr int D = decltype(d)::value, TK = kv_append_tokens<D, false>();
+        kernel = kv_append_kernel<decltype(f)::value, D>(align);
+        most = std::max((n_tokens + TK - 1) / TK, (n_tokens + 7) / 8 * 2);
+        return 0;
+    });
+    const int warps = std::min(MOE_KV_THREADS / 32, most);
+    kernel<<<dim3((most + warps - 1) / warps, 2 * a.k.heads), warps * 32, 0, (cudaStream_t)stream>>>(a);
     SPEC_CUDA_OK(cudaGetLastError());
     return MOE_OK;
 }
@@ -347,7 +373,7 @@ int moe_spec_verify_workspace_bytes(int batch, int n_rows, size_t *bytes)
         return host_fail(MOE_EINVAL, "moe_spec_verify_workspace_bytes: bad arguments");
     if (batch > 65535)
         return host_fail(MOE_EUNSUPPORTED, "batch (%d) <= 65535", batch);
-    *bytes = SPEC_CTRL_BYTES;
+    *bytes = SPEC_CTRL_BYTES + (size_t)n_rows * MOE_VERIFY_MAX_SPLITS * sizeof(VerifySlice);
     return MOE_OK;
 }
 
@@ -383,7 +409,6 @@ int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stri
         return host_fail(MOE_EINVAL, "moe_spec_verify: the workspace holds %zu bytes, %zu are needed", ws_bytes, need);
     VerifyArgs a{};
     a.logits = logits_dev;
-    a.f32 = logits_type == MOE_F32;
     a.stride = logits_stride;
     a.q_start = q_start_dev;
     a.tokens = tokens_dev;
@@ -394,15 +419,47 @@ int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stri
     a.uniforms = uniforms_dev;
     a.noise = noise_dev;
     a.noise_stride = noise_stride;
-    a.batch = batch;
     a.rows = n_rows;
     a.vocab = vocab;
     a.n_accepted = n_accepted_dev;
     a.path = path_dev;
     a.next = next_token_dev;
     a.ctrl = static_cast<uint32_t *>(ws_dev);
-    moe_verify_kernel<<<batch, MOE_VERIFY_THREADS, 0, (cudaStream_t)stream>>>(a);
-    SPEC_CUDA_OK(cudaGetLastError());
+    const bool f32 = logits_type == MOE_F32;
+    const bool wide = aligned(logits_dev, 16) && logits_stride % (f32 ? 4 : 8) == 0 &&
+                      (!draft_dev || (aligned(draft_dev, 16) && draft_stride % 4 == 0)) &&
+                      (!noise_dev || (aligned(noise_dev, 16) && noise_stride % 4 == 0));
+    // a cluster of CTAs a sequence: as many as are on the GPU together (two an SM), with 2048 values a CTA at least
+    const int ranks = std::max(1, std::min({MOE_VERIFY_MAX_CLUSTER, 304 / batch, vocab / 2048}));
+    a.slice = ((vocab + ranks - 1) / ranks + 7) / 8 * 8;
+    // all rows ahead where that is little, else as the walk reaches them
+    const size_t all = (size_t)n_rows * vocab * (f32 ? 4 : 2);
+    const bool ahead = n_rows > 0 && (all <= MOE_VERIFY_AHEAD_BYTES || !parents_dev);
+    if (ahead) {
+        a.batch = batch;
+        // parts of 16384 values, of 2048 where the rows are few
+        a.splits = std::max(1, std::min({MOE_VERIFY_MAX_SPLITS, vocab / 2048, std::max(1216 / n_rows, vocab / 16384)}));
+        a.split = ((vocab + a.splits - 1) / a.splits + 7) / 8 * 8;
+        a.stats = reinterpret_cast<VerifySlice *>(static_cast<char *>(ws_dev) + SPEC_CTRL_BYTES);
+        const auto rows = f32 ? (wide ? moe_verify_rows_kernel<true, true> : moe_verify_rows_kernel<true, false>)
+                              : (wide ? moe_verify_rows_kernel<false, true> : moe_verify_rows_kernel<false, false>);
+        rows<<<(unsigned)n_rows * a.splits, MOE_VERIFY_STAT_THREADS, 0, (cudaStream_t)stream>>>(a);
+        SPEC_CUDA_OK(cudaGetLastError());
+    }
+    const auto kernel = verify_kernel(f32, wide, ahead);
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3((unsigned)batch * ranks);
+    lc.blockDim = dim3(MOE_VERIFY_THREADS);
+    lc.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ranks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = ahead ? 2 : 1;
+    SPEC_CUDA_OK(cudaLaunchKernelEx(&lc, kernel, a));
     return MOE_OK;
 }
 

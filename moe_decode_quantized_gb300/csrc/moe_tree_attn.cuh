@@ -80,13 +80,6 @@ struct TreeShape {
     static size_t smem(int stages) { return fixed() + (size_t)stages * MOE_TREE_WARPS * BLOCK; }
 };
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // D (+)= A B: 16x8x16, f16 operands, f32 sums
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1)
 {
