@@ -429,8 +429,8 @@ int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stri
     const bool wide = aligned(logits_dev, 16) && logits_stride % (f32 ? 4 : 8) == 0 &&
                       (!draft_dev || (aligned(draft_dev, 16) && draft_stride % 4 == 0)) &&
                       (!noise_dev || (aligned(noise_dev, 16) && noise_stride % 4 == 0));
-    // a cluster of CTAs a sequence: as many as are on the GPU together (two an SM), with 2048 values a CTA at least
-    const int ranks = std::max(1, std::min({MOE_VERIFY_MAX_CLUSTER, 304 / batch, vocab / 2048}));
+    // a cluster of CTAs a sequence: as many as are on the GPU together (three an SM), with 2048 values a CTA at least
+    const int ranks = std::max(1, std::min({MOE_VERIFY_MAX_CLUSTER, 456 / batch, vocab / 2048}));
     a.slice = ((vocab + ranks - 1) / ranks + 7) / 8 * 8;
     // all rows ahead where that is little, else as the walk reaches them
     const size_t all = (size_t)n_rows * vocab * (f32 ? 4 : 2);

@@ -26,7 +26,7 @@
 
 namespace moe {
 
-#define MOE_VERIFY_THREADS 512
+#define MOE_VERIFY_THREADS 256
 #define MOE_VERIFY_MAX_CLUSTER 8
 #define MOE_VERIFY_STAT_THREADS 256
 #define MOE_VERIFY_MAX_SPLITS 64
@@ -72,6 +72,13 @@ __device__ __forceinline__ void warp_larger(float &v, int &i)
     const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, key);
     i = (int)__reduce_min_sync(0xFFFFFFFFu, key == top ? (uint32_t)i : 0x7FFFFFFFu);
     v = __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
+}
+
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ float max_nan(float x, float y)
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(MOE_VERIFY_STAT_THREADS) moe_verify_rows_kerne
 }
 
 template <bool F32, bool WIDE, bool AHEAD>
-__global__ void __launch_bounds__(MOE_VERIFY_THREADS, 2) moe_verify_kernel(const VerifyArgs a)
+__global__ void __launch_bounds__(MOE_VERIFY_THREADS, 3) moe_verify_kernel(const VerifyArgs a)
 {
     constexpr int NT = MOE_VERIFY_THREADS, NW = NT / 32;
     __shared__ VerifySlice slices[2][MOE_VERIFY_MAX_CLUSTER];
@@ -460,7 +467,7 @@ __global__ void __launch_bounds__(MOE_VERIFY_THREADS, 2) moe_verify_kernel(const
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 sum += l[k];
-                const float s = __fdividef(l[k], fmaxf(e[k], 1.17549435e-38f));
+                const float s = l[k] * rcp(fmaxf(e[k], 1.17549435e-38f));
                 if (s > best && (FULL || view.place(at, k) < hi)) {  // ascending indexes: the first of equals
                     best = s;
                     where = view.place(at, k);
