@@ -114,16 +114,15 @@ using TreeKernel = void (*)(TreeArgs, int);
 
 struct TreeInstance {
     TreeKernel kernel;
-    int rows;         // rows of a row block
-    size_t fixed, stage, part;  // bytes of shared memory (beside the ring, a stage of all warps); floats of a partial
-    int stages, ctas;  // found at the first use on a device
+    size_t fixed, stage;  // bytes of shared memory: beside the ring and the list; of a stage of all warps
+    int ctas;             // an SM, by registers
 };
 
 template <int FMT, int D, int MT>
 TreeInstance tree_instance()
 {
     using T = TreeShape<FMT, D, MT>;
-    return {moe_tree_attn_kernel<FMT, D, MT>, T::ROWS, (size_t)T::fixed(), (size_t)MOE_TREE_WARPS * T::BLOCK, T::PART, 0, 0};
+    return {moe_tree_attn_kernel<FMT, D, MT>, (size_t)T::FIXED, (size_t)MOE_TREE_WARPS * T::BLOCK, T::CTAS};
 }
 
 #define MOE_TREE_MAX_GRID 640  // runs; the workspace holds two partials each
@@ -139,16 +138,22 @@ int tree_choose(int fmt, int dim, int rows)
     return (fmt == MOE_KV_Q8 ? 0 : 6) + first + std::min(mt, most);
 }
 
-int tree_get(int index, int &sms, TreeInstance &out)
+struct TreeDevice {
+    int sms = 0;
+    size_t per_sm = 0, optin = 0;  // shared memory
+    TreeInstance inst[12];
+};
+
+int tree_device(TreeDevice **out)
 {
-    static TreeInstance inst[MOE_TREE_MAX_DEVICES][12];
-    static int sm_count[MOE_TREE_MAX_DEVICES];
+    static TreeDevice dev[MOE_TREE_MAX_DEVICES];
     int d = 0;
     SPEC_CUDA_OK(cudaGetDevice(&d));
     if (d < 0 || d >= MOE_TREE_MAX_DEVICES)
         return host_fail(MOE_EUNSUPPORTED, "device ordinal %d", d);
     std::lock_guard<std::mutex> lk(g_tree_mu);
-    if (!sm_count[d]) {
+    TreeDevice &D = dev[d];
+    if (!D.sms) {
         const TreeInstance all[12] = {
             tree_instance<MOE_KV_Q8, 64, 1>(),  tree_instance<MOE_KV_Q8, 64, 2>(),  tree_instance<MOE_KV_Q8, 64, 4>(),
             tree_instance<MOE_KV_Q8, 128, 1>(), tree_instance<MOE_KV_Q8, 128, 2>(), tree_instance<MOE_KV_Q8, 256, 1>(),
@@ -159,26 +164,14 @@ int tree_get(int index, int &sms, TreeInstance &out)
         SPEC_CUDA_OK(cudaDeviceGetAttribute(&per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, d));
         SPEC_CUDA_OK(cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, d));
         for (int i = 0; i < 12; ++i) {
-            TreeInstance t = all[i];
-            cudaFuncAttributes fa;
-            SPEC_CUDA_OK(cudaFuncGetAttributes(&fa, t.kernel));
-            SPEC_CUDA_OK(cudaFuncSetAttribute(t.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
-            // as many CTAs an SM as the registers allow (at most 3) while each ring keeps 3 stages
-            const int by_regs = 65536 / ((fa.numRegs + 7) / 8 * 8 * MOE_TREE_THREADS);
-            for (t.ctas = std::max(1, std::min(by_regs, 3));; --t.ctas) {
-                const size_t room = std::min<size_t>(optin, per_sm / t.ctas - 1024);
-                t.stages = room > t.fixed ? (int)std::min<size_t>(8, (room - t.fixed) / t.stage) : 0;
-                if (t.stages >= 3 || t.ctas == 1)
-                    break;
-            }
-            if (t.stages < 2)
-                return host_fail(MOE_EUNSUPPORTED, "tree attention: %zu bytes of shared memory do not fit", t.fixed);
-            inst[d][i] = t;
+            SPEC_CUDA_OK(cudaFuncSetAttribute(all[i].kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
+            D.inst[i] = all[i];
         }
-        sm_count[d] = n;
+        D.per_sm = per_sm;
+        D.optin = optin;
+        D.sms = n;
     }
-    sms = sm_count[d];
-    out = inst[d][index];
+    *out = &D;
     return MOE_OK;
 }
 
@@ -357,12 +350,23 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     a.part = reinterpret_cast<float *>(a.count + MOE_TREE_MAX_GRID);
     a.wait_ns = host_wait_ns();
     // the row block from the mean rows of a sequence (the lengths themselves are on the device)
-    TreeInstance t;
-    int sms;
-    if ((rc = tree_get(tree_choose(a.k.fmt, a.k.dim, (n_tokens + batch - 1) / batch * a.group), sms, t)))
+    TreeDevice *dev;
+    if ((rc = tree_device(&dev)))
         return rc;
-    const int grid = std::min(sms * t.ctas, MOE_TREE_MAX_GRID);
-    t.kernel<<<grid, MOE_TREE_THREADS, t.fixed + t.stages * t.stage, (cudaStream_t)stream>>>(a, t.stages);
+    const TreeInstance &t = dev->inst[tree_choose(a.k.fmt, a.k.dim, (n_tokens + batch - 1) / batch * a.group)];
+    // as many CTAs an SM as the registers allow while each ring keeps three stages
+    const size_t list = 8 * ((size_t)batch + 1), used = t.fixed + list;
+    int ctas = t.ctas, stages;
+    for (;; --ctas) {
+        const size_t room = std::min(dev->optin, dev->per_sm / ctas - 1024);
+        stages = room > used ? (int)std::min<size_t>(8, (room - used) / t.stage) : 0;
+        if (stages >= 3 || ctas == 1)
+            break;
+    }
+    if (stages < 2)
+        return host_fail(MOE_EUNSUPPORTED, "moe_tree_attention: %zu bytes of shared memory do not fit", used + 2 * t.stage);
+    const int grid = std::min(dev->sms * ctas, MOE_TREE_MAX_GRID);
+    t.kernel<<<grid, MOE_TREE_THREADS, used + stages * t.stage, (cudaStream_t)stream>>>(a, stages);
     SPEC_CUDA_OK(cudaGetLastError());
     return MOE_OK;
 }

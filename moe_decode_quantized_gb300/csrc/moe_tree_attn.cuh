@@ -69,15 +69,14 @@ struct TreeShape {
     static constexpr int WV = RB / 32;      // words of a lane's eighth of a V row
     static constexpr int ROWS = 16 * MT;
     static constexpr int OREGS = MT * NB * 4;
+    static constexpr int CTAS = OREGS <= 32 ? 4 : OREGS <= 64 ? 3 : 2;  // an SM, by registers
     static constexpr bool QREG = OREGS + MT * KS * 4 <= 96;  // query fragments kept in registers
     static constexpr int PART = ROWS * D + 2 * ROWS;         // floats of a partial
     static constexpr int BARS = 8 * 8 * MOE_TREE_WARPS;      // room for 8 stages' barriers
-    static constexpr int SEQ = 8 * (MOE_TREE_MAX_BATCH + 2);
     static constexpr int HEAD = BARS + 8 * ROWS + 12 * ROWS * MOE_TREE_WARPS + 64;
     static constexpr int QBYTES = MT * KS * 512;
     static constexpr int MERGE = 2 * OREGS * 128;
-    __host__ __device__ static constexpr int fixed() { return (HEAD + SEQ + QBYTES + MERGE + 127) / 128 * 128; }
-    static size_t smem(int stages) { return fixed() + (size_t)stages * MOE_TREE_WARPS * BLOCK; }
+    static constexpr int FIXED = (HEAD + QBYTES + MERGE + 127) / 128 * 128;  // then the ring, then the list
 };
 
 // D (+)= A B: 16x8x16, f16 operands, f32 sums
@@ -196,7 +195,7 @@ __device__ __forceinline__ void tree_store(const TreeArgs &a, const TreeItem &it
 }
 
 template <int FMT, int D, int MT>
-__global__ void __launch_bounds__(MOE_TREE_THREADS) moe_tree_attn_kernel(const __grid_constant__ TreeArgs a, const int stages)
+__global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS) moe_tree_attn_kernel(const __grid_constant__ TreeArgs a, const int stages)
 {
     using T = TreeShape<FMT, D, MT>;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -205,11 +204,11 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS) moe_tree_attn_kernel(const _
     float *cmul = reinterpret_cast<float *>(smem + T::BARS + 8 * T::ROWS);         // [rows]
     float *wm = cmul + T::ROWS, *wl = wm + MOE_TREE_WARPS * T::ROWS;               // [warps][rows]
     long long *scan = reinterpret_cast<long long *>(smem + T::HEAD - 48);          // [warps]
-    long long *cum = reinterpret_cast<long long *>(smem + T::HEAD);                // [batch + 1]
-    uint4 *qf = reinterpret_cast<uint4 *>(smem + T::HEAD + T::SEQ);                // [mt][ks][lane]
-    float4 *merge = reinterpret_cast<float4 *>(smem + T::HEAD + T::SEQ + T::QBYTES);  // [2][regs / 4][lane]
+    uint4 *qf = reinterpret_cast<uint4 *>(smem + T::HEAD);                         // [mt][ks][lane]
+    float4 *merge = reinterpret_cast<float4 *>(smem + T::HEAD + T::QBYTES);        // [2][regs / 4][lane]
+    long long *cum = reinterpret_cast<long long *>(smem + T::FIXED + (size_t)MOE_TREE_WARPS * stages * T::BLOCK);  // [batch + 1]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-    uint8_t *ring = smem + T::fixed() + (size_t)warp * stages * T::BLOCK;
+    uint8_t *ring = smem + T::FIXED + (size_t)warp * stages * T::BLOCK;
     uint64_t *bar = bars + warp * 8;
     if (lane == 0) {
         for (int s = 0; s < stages; ++s)
@@ -285,12 +284,11 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS) moe_tree_attn_kernel(const _
         bad_before = bad;
         bad = __ballot_sync(0xFFFFFFFFu, out);
     };
-    auto ask = [&]() {  // the copy of the next unit into its stage
+    auto ask = [&](int s) {  // the copy of the next unit, into stage s
         if (asked - batch == 32)
             look(asked);
         const uint8_t *src = reinterpret_cast<const uint8_t *>(
             __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(place), asked - batch));
-        const int s = asked % stages;
         if (lane == 0) {
             mbar_arrive_expect_tx(bar + s, T::BLOCK);
             bulk_g2s(ring + s * T::BLOCK, src, T::BLOCK, bar + s, policy);
@@ -300,7 +298,7 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS) moe_tree_attn_kernel(const _
     if (mine > 0)
         look(0);
     for (int s = 0; s < stages && asked < mine; ++s)
-        ask();
+        ask(s);
 
     int done = 0, stage = 0;
     uint32_t phase = 0;
@@ -396,11 +394,10 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS) moe_tree_attn_kernel(const _
                     o[mt][j][i] = 0.0f;
         }
         const int prefix = it.len - it.n;
-        for (; done < mine; ++done) {
-            const long long at = lo + warp + (long long)done * MOE_TREE_WARPS;
-            if (at >= end)
-                break;
-            const int first = (int)(at - it.lo) * 16;  // the unit's first token
+        // this warp's units below `last` belong to the item; the first token of unit `done`
+        const int last = min(mine, (int)((end - lo - warp + MOE_TREE_WARPS - 1) / MOE_TREE_WARPS));
+        int first = (int)(lo + warp + (long long)done * MOE_TREE_WARPS - it.lo) * 16;
+        for (; done < last; ++done, first += 16 * MOE_TREE_WARPS) {
             if (ok)
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar + stage, phase, a.ctrl + MOE_CTRL_STATUS, a.wait_ns));
             const uint8_t *blk = ring + stage * T::BLOCK;
@@ -589,7 +586,7 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS) moe_tree_attn_kernel(const _
             }
             __syncwarp();  // the stage has been read
             if (ok && asked < mine)
-                ask();
+                ask(stage);
             if (++stage == stages) {
                 stage = 0;
                 phase ^= 1;
