@@ -314,6 +314,14 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int m = 16; m; m /= 2)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+    return v;
+}
+
 // clamped SwiGLU in f32: silu(min(g, L)) * clamp(u, -L, L); L <= 0: no clamp
 __device__ __forceinline__ float swiglu_f32(float g, float u, float limit)
 {

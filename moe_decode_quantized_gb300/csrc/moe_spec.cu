@@ -9,6 +9,7 @@
 #include "moe_host.cuh"
 #include "moe_kv.cuh"
 #include "moe_tree_attn.cuh"
+#include "moe_tree_tc.cuh"
 #include "moe_verify.cuh"
 
 using namespace moe;
@@ -138,10 +139,25 @@ int tree_choose(int fmt, int dim, int rows)
     return (fmt == MOE_KV_Q8 ? 0 : 6) + first + std::min(mt, most);
 }
 
+// the tensor-core kernels' instances, by format and columns (32, 64, 128)
+struct TtcInstance {
+    TreeKernel kernel;
+    size_t fixed, stage;
+    int columns;
+};
+
+template <int FMT, int N>
+TtcInstance ttc_instance()
+{
+    using T = TtcShape<FMT, N>;
+    return {moe_tree_tc_kernel<FMT, N>, 1024 + (size_t)T::RAW_AT + T::SMALL, (size_t)T::STAGE, N};
+}
+
 struct TreeDevice {
     int sms = 0;
     size_t per_sm = 0, optin = 0;  // shared memory
     TreeInstance inst[12];
+    TtcInstance tc[6];
 };
 
 int tree_device(TreeDevice **out)
@@ -166,6 +182,13 @@ int tree_device(TreeDevice **out)
         for (int i = 0; i < 12; ++i) {
             SPEC_CUDA_OK(cudaFuncSetAttribute(all[i].kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
             D.inst[i] = all[i];
+        }
+        const TtcInstance tc[6] = {ttc_instance<MOE_KV_Q8, 32>(), ttc_instance<MOE_KV_Q8, 64>(),
+                                   ttc_instance<MOE_KV_Q8, 128>(), ttc_instance<MOE_KV_Q4, 32>(),
+                                   ttc_instance<MOE_KV_Q4, 64>(), ttc_instance<MOE_KV_Q4, 128>()};
+        for (int i = 0; i < 6; ++i) {
+            SPEC_CUDA_OK(cudaFuncSetAttribute(tc[i].kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
+            D.tc[i] = tc[i];
         }
         D.per_sm = per_sm;
         D.optin = optin;
@@ -353,7 +376,20 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     TreeDevice *dev;
     if ((rc = tree_device(&dev)))
         return rc;
-    const TreeInstance &t = dev->inst[tree_choose(a.k.fmt, a.k.dim, (n_tokens + batch - 1) / batch * a.group)];
+    const int rows = (n_tokens + batch - 1) / batch * a.group;
+    if (a.k.dim == 128 && rows > 16) {
+        const TtcInstance &t = dev->tc[(a.k.fmt == MOE_KV_Q8 ? 0 : 3) + (rows <= 32 ? 0 : rows <= 64 ? 1 : 2)];
+        const size_t used = t.fixed + 8 * ((size_t)batch + 1);
+        const int stages = (int)std::min<size_t>(4, (dev->optin - used) / t.stage);
+        if (stages < 2)
+            return host_fail(MOE_EUNSUPPORTED, "moe_tree_attention: %zu bytes of shared memory do not fit", used + 2 * t.stage);
+        a.min_units = 2;
+        const int grid = std::min(dev->sms, MOE_TREE_MAX_GRID * 32 / t.columns);  // what the partials' room holds
+        t.kernel<<<grid, MOE_TTC_THREADS, used + stages * t.stage, (cudaStream_t)stream>>>(a, stages);
+        SPEC_CUDA_OK(cudaGetLastError());
+        return MOE_OK;
+    }
+    const TreeInstance &t = dev->inst[tree_choose(a.k.fmt, a.k.dim, rows)];
     // as many CTAs an SM as the registers allow while each ring keeps three stages
     const size_t list = 8 * ((size_t)batch + 1), used = t.fixed + list;
     int ctas = t.ctas, stages;

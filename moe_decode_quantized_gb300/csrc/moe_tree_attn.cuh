@@ -134,7 +134,8 @@ template <int ROWS>
 __device__ __forceinline__ int tree_blocks(int n, int group) { return (n * group + ROWS - 1) / ROWS; }
 
 // the item that holds unit u: cum [batch + 1] is the list's units before each sequence
-template <int ROWS>
+// of TOKENS tokens
+template <int ROWS, int TOKENS>
 __device__ __forceinline__ TreeItem tree_item(const TreeArgs &a, const long long *cum, long long u)
 {
     int x = 0, y = a.batch;  // cum[x] <= u < cum[y]
@@ -150,12 +151,75 @@ __device__ __forceinline__ TreeItem tree_item(const TreeArgs &a, const long long
     it.first = a.q_start[x];
     it.n = a.q_start[x + 1] - it.first;
     it.len = a.kv_len[x];
-    it.units = (it.len + 15) / 16;
+    it.units = (it.len + TOKENS - 1) / TOKENS;
     const int at = (int)((u - cum[x]) / it.units), blocks = tree_blocks<ROWS>(it.n, a.group);
     it.head = at / blocks;
     it.block = at % blocks;
     it.lo = cum[x] + (long long)at * it.units;
     return it;
+}
+
+// zeros for the query rows of a sequence that does not hold
+template <int D>
+__device__ __forceinline__ void tree_zero(const TreeArgs &a, int first, int rows)
+{
+    const int heads = a.k.heads * a.group;
+    for (int r = 0; r < rows * heads; ++r) {
+        uint16_t *p = a.out + (first + r / heads) * a.o_tok + r % heads * a.o_head;
+        for (int d = 0; d < D; ++d)
+            p[d] = 0;
+    }
+}
+
+// COUNT values (from dimension d0) of a query row that LANES neighbouring
+// lanes hold between them, as f16 pairs: the row times the power of two that
+// brings its largest magnitude below 2^14, so that f16 holds bf16's values
+// exactly (and the scale's sign). Returns what turns the row's scores into
+// exponents of 2. A row with a NaN or an infinity becomes a row of NaN; a row
+// that is not live (and every row for scale 0) one of zeros.
+template <int COUNT, int LANES>
+__device__ __forceinline__ float tree_row(const TreeArgs &a, bool live, int token, int head, int d0, uint32_t (&x)[COUNT / 2])
+{
+    const uint16_t *p = a.q + token * a.q_tok + head * a.q_head + d0;
+    float top = 0.0f;
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < COUNT / 2; e += 4) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (live && a.q_wide) {
+            v = *reinterpret_cast<const uint4 *>(p + 2 * e);
+        } else if (live) {
+            v.x = p[2 * e] | (uint32_t)p[2 * e + 1] << 16;
+            v.y = p[2 * e + 2] | (uint32_t)p[2 * e + 3] << 16;
+            v.z = p[2 * e + 4] | (uint32_t)p[2 * e + 5] << 16;
+            v.w = p[2 * e + 6] | (uint32_t)p[2 * e + 7] << 16;
+        }
+        x[e] = v.x;
+        x[e + 1] = v.y;
+        x[e + 2] = v.z;
+        x[e + 3] = v.w;
+#pragma unroll
+        for (int i = e; i < e + 4; ++i) {
+            const float f0 = fabsf(bf16_lo(x[i])), f1 = fabsf(bf16_hi(x[i]));
+            odd |= !(f0 < INFINITY) || !(f1 < INFINITY);
+            top = fmaxf(top, fmaxf(f0, f1));
+        }
+    }
+#pragma unroll
+    for (int m = 1; m < LANES; m *= 2) {
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+        odd |= __shfl_xor_sync(0xFFFFFFFFu, (int)odd, m) != 0;
+    }
+    // 2^e with top 2^e in [2^13, 2^14): two factors, as e can pass f32's exponents
+    const int e = top > 0.0f && !odd ? 13 - ilogbf(top) : 0;
+    const float up0 = exp2f((float)(e / 2)), up1 = exp2f((float)(e - e / 2));
+    const float sign = a.scale < 0.0f ? -1.0f : a.scale > 0.0f ? 1.0f : 0.0f;
+#pragma unroll
+    for (int i = 0; i < COUNT / 2; ++i) {
+        const float f0 = bf16_lo(x[i]) * up0 * up1 * sign, f1 = bf16_hi(x[i]) * up0 * up1 * sign;
+        x[i] = odd ? 0x7E007E00u : pack_h2(f0, f1);
+    }
+    return sign == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f / up0 / up1;
 }
 
 // writes a row block: o[mt][j] of this lane divided by the rows' sums
@@ -228,11 +292,7 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
             cum[b] = mine;
             mine += (long long)((len + 15) / 16) * (n > 0 ? tree_blocks<T::ROWS>(n, a.group) * a.k.heads : 0);
             if (n == 0 && rows > 0 && blockIdx.x == (unsigned)(b % gridDim.x))  // what does not hold gives zeros
-                for (int r = 0; r < rows * a.k.heads * a.group; ++r) {
-                    uint16_t *p = a.out + (first + r / (a.k.heads * a.group)) * a.o_tok + r % (a.k.heads * a.group) * a.o_head;
-                    for (int d = 0; d < D; ++d)
-                        p[d] = 0;
-                }
+                tree_zero<D>(a, first, rows);
         }
         long long incl = mine;
         for (int m = 1; m < 32; m *= 2) {
@@ -272,7 +332,7 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
         place = a.pages;
         if (at + lane < mine) {
             const long long u = lo + warp + (long long)(at + lane) * MOE_TREE_WARPS;
-            const TreeItem it = tree_item<T::ROWS>(a, cum, u);
+            const TreeItem it = tree_item<T::ROWS, MOE_KV_BLOCK>(a, cum, u);
             const int blk = (int)(u - it.lo), per_page = a.k.page / 16;
             const int page = a.table[it.b * a.table_stride + blk / per_page];
             out = page < 0 || page >= a.n_pages;
@@ -303,66 +363,21 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
     int done = 0, stage = 0;
     uint32_t phase = 0;
     for (long long u = lo; u < hi;) {
-        const TreeItem it = tree_item<T::ROWS>(a, cum, u);
+        const TreeItem it = tree_item<T::ROWS, MOE_KV_BLOCK>(a, cum, u);
         const long long end = min(hi, it.lo + it.units);
-        // query fragments: k step ks of lane (g, t4) is dimensions t4 D / 4 + 4 ks .. + 3 of rows g and g + 8,
-        // each row scaled by a power of two to below 2^14 (f16 then holds bf16's values exactly)
+        // query fragments: k step ks of lane (g, t4) is dimensions t4 D / 4 + 4 ks .. + 3 of rows g and g + 8
         for (int mt = warp; mt < MT; mt += MOE_TREE_WARPS) {
             uint32_t x[2][D / 8];
-            float mul[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const int r = it.block * T::ROWS + mt * 16 + s * 8 + g;
+                const int at = mt * 16 + s * 8 + g, r = it.block * T::ROWS + at;
                 const bool live = r < it.n * a.group;
                 const int i = live ? r / a.group : 0;
-                const uint16_t *p = a.q + (it.first + i) * a.q_tok +
-                                    (it.head * a.group + (live ? r % a.group : 0)) * a.q_head + t4 * (D / 4);
-                float top = 0.0f;
-                bool odd = false;
-#pragma unroll
-                for (int e = 0; e < D / 8; e += 4) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (live && a.q_wide) {
-                        v = *reinterpret_cast<const uint4 *>(p + 2 * e);
-                    } else if (live) {
-                        v.x = p[2 * e] | (uint32_t)p[2 * e + 1] << 16;
-                        v.y = p[2 * e + 2] | (uint32_t)p[2 * e + 3] << 16;
-                        v.z = p[2 * e + 4] | (uint32_t)p[2 * e + 5] << 16;
-                        v.w = p[2 * e + 6] | (uint32_t)p[2 * e + 7] << 16;
-                    }
-                    x[s][e] = v.x;
-                    x[s][e + 1] = v.y;
-                    x[s][e + 2] = v.z;
-                    x[s][e + 3] = v.w;
-#pragma unroll
-                    for (int i2 = 0; i2 < 4; ++i2) {
-                        const float f0 = fabsf(bf16_lo(x[s][e + i2])), f1 = fabsf(bf16_hi(x[s][e + i2]));
-                        odd |= !(f0 < INFINITY) || !(f1 < INFINITY);
-                        top = fmaxf(top, fmaxf(f0, f1));
-                    }
-                }
-#pragma unroll
-                for (int m = 1; m < 4; m *= 2) {
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-                    odd |= __shfl_xor_sync(0xFFFFFFFFu, (int)odd, m) != 0;
-                }
-                // 2^e with top 2^e in [2^13, 2^14): two factors, as e can pass f32's exponents
-                const int e = top > 0.0f ? 13 - ilogbf(top) : 0;
-                const float up0 = exp2f((float)(e / 2)), up1 = exp2f((float)(e - e / 2));
-                const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
-#pragma unroll
-                for (int i2 = 0; i2 < D / 8; ++i2) {
-                    float f0 = bf16_lo(x[s][i2]) * up0 * up1 * sign, f1 = bf16_hi(x[s][i2]) * up0 * up1 * sign;
-                    if (odd)  // a row with a NaN or an infinity is a row of NaN
-                        f0 = f1 = __int_as_float(0x7FC00000);
-                    if (a.scale == 0.0f && !odd)
-                        f0 = f1 = 0.0f;
-                    x[s][i2] = pack_h2(f0, f1);
-                }
-                mul[s] = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f / up0 / up1;
+                const float mul = tree_row<D / 4, 4>(a, live, it.first + i, it.head * a.group + (live ? r % a.group : 0),
+                                                     t4 * (D / 4), x[s]);
                 if (t4 == 0) {
-                    cmul[mt * 16 + s * 8 + g] = mul[s];
-                    masks[mt * 16 + s * 8 + g] = !live ? 0 : a.mask ? a.mask[it.first + i] : (2ull << i) - 1;
+                    cmul[at] = mul;
+                    masks[at] = !live ? 0 : a.mask ? a.mask[it.first + i] : (2ull << i) - 1;
                 }
             }
 #pragma unroll

@@ -88,14 +88,6 @@ __device__ __forceinline__ float max_nan(float x, float y)
     return z;
 }
 
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int m = 16; m; m /= 2)
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
-    return v;
-}
-
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
