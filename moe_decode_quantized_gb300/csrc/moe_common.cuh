@@ -322,6 +322,28 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// two f32 operations at once
+struct F2 {
+    unsigned long long v;
+    __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+    __device__ __forceinline__ void get(float &x, float &y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+};
+__device__ __forceinline__ F2 add2(F2 x, const F2 &y)
+{
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x.v) : "l"(x.v), "l"(y.v));
+    return x;
+}
+__device__ __forceinline__ F2 mul2(F2 x, const F2 &y)
+{
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x.v) : "l"(x.v), "l"(y.v));
+    return x;
+}
+__device__ __forceinline__ F2 fma2(F2 x, const F2 &y, const F2 &z)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x.v) : "l"(x.v), "l"(y.v), "l"(z.v));
+    return x;
+}
+
 // clamped SwiGLU in f32: silu(min(g, L)) * clamp(u, -L, L); L <= 0: no clamp
 __device__ __forceinline__ float swiglu_f32(float g, float u, float limit)
 {

@@ -115,6 +115,7 @@ using TreeKernel = void (*)(TreeArgs, int);
 
 struct TreeInstance {
     TreeKernel kernel;
+    int rows;
     size_t fixed, stage;  // bytes of shared memory: beside the ring and the list; of a stage of all warps
     int ctas;             // an SM, by registers
 };
@@ -123,10 +124,11 @@ template <int FMT, int D, int MT>
 TreeInstance tree_instance()
 {
     using T = TreeShape<FMT, D, MT>;
-    return {moe_tree_attn_kernel<FMT, D, MT>, (size_t)T::FIXED, (size_t)MOE_TREE_WARPS * T::BLOCK, T::CTAS};
+    return {moe_tree_attn_kernel<FMT, D, MT>, T::ROWS, (size_t)T::FIXED, (size_t)MOE_TREE_WARPS * T::BLOCK, T::CTAS};
 }
 
 #define MOE_TREE_MAX_GRID 640  // runs; the workspace holds two partials each
+#define MOE_TTC_MAX_GRID 160   // of the tensor-core kernel
 #define MOE_TREE_MAX_DEVICES 64
 
 std::mutex g_tree_mu;
@@ -139,25 +141,24 @@ int tree_choose(int fmt, int dim, int rows)
     return (fmt == MOE_KV_Q8 ? 0 : 6) + first + std::min(mt, most);
 }
 
-// the tensor-core kernels' instances, by format and columns (32, 64, 128)
+// the tensor-core kernels' instances, by format
 struct TtcInstance {
     TreeKernel kernel;
     size_t fixed, stage;
-    int columns;
 };
 
-template <int FMT, int N>
+template <int FMT>
 TtcInstance ttc_instance()
 {
-    using T = TtcShape<FMT, N>;
-    return {moe_tree_tc_kernel<FMT, N>, 1024 + (size_t)T::RAW_AT + T::SMALL, (size_t)T::STAGE, N};
+    using T = TtcShape<FMT>;
+    return {moe_tree_tc_kernel<FMT>, 1024 + (size_t)T::RAW_AT + T::SMALL, (size_t)T::STAGE};
 }
 
 struct TreeDevice {
     int sms = 0;
     size_t per_sm = 0, optin = 0;  // shared memory
     TreeInstance inst[12];
-    TtcInstance tc[6];
+    TtcInstance tc[2];
 };
 
 int tree_device(TreeDevice **out)
@@ -183,10 +184,8 @@ int tree_device(TreeDevice **out)
             SPEC_CUDA_OK(cudaFuncSetAttribute(all[i].kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
             D.inst[i] = all[i];
         }
-        const TtcInstance tc[6] = {ttc_instance<MOE_KV_Q8, 32>(), ttc_instance<MOE_KV_Q8, 64>(),
-                                   ttc_instance<MOE_KV_Q8, 128>(), ttc_instance<MOE_KV_Q4, 32>(),
-                                   ttc_instance<MOE_KV_Q4, 64>(), ttc_instance<MOE_KV_Q4, 128>()};
-        for (int i = 0; i < 6; ++i) {
+        const TtcInstance tc[2] = {ttc_instance<MOE_KV_Q8>(), ttc_instance<MOE_KV_Q4>()};
+        for (int i = 0; i < 2; ++i) {
             SPEC_CUDA_OK(cudaFuncSetAttribute(tc[i].kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
             D.tc[i] = tc[i];
         }
@@ -195,6 +194,25 @@ int tree_device(TreeDevice **out)
         D.sms = n;
     }
     *out = &D;
+    return MOE_OK;
+}
+
+// the second kernel of a call: a CTA a run and 16 rows of its row block
+int tree_join(const TreeArgs &a, int grid, int rows, cudaStream_t s)
+{
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(grid, rows / MOE_TREE_JOIN_ROWS);
+    lc.blockDim = dim3(MOE_TREE_JOIN_THREADS);
+    lc.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    const TreeKernel kernel = a.k.dim == 64    ? moe_tree_join_kernel<64>
+                              : a.k.dim == 128 ? moe_tree_join_kernel<128>
+                                               : moe_tree_join_kernel<256>;
+    SPEC_CUDA_OK(cudaLaunchKernelEx(&lc, kernel, a, rows));
     return MOE_OK;
 }
 
@@ -306,9 +324,10 @@ static int tree_ws(const moe_kv_cache *cache, int n_q_heads, int batch, int n_to
     if (n_q_heads / k.heads > 64 || batch > 1024 || n_tokens > batch * MOE_MAX_DRAFT)
         return host_fail(MOE_EUNSUPPORTED, "n_q_heads / n_kv_heads (%d) <= 64, batch (%d) <= 1024, n_tokens (%d) <= "
                          "%d a sequence", n_q_heads / k.heads, batch, n_tokens, MOE_MAX_DRAFT);
-    // control words, arrivals, and two partials of the largest row block a run
-    const size_t rows = k.dim == 64 ? 64 : k.dim == 128 ? 32 : 16;
-    bytes = SPEC_CTRL_BYTES + 4 * MOE_TREE_MAX_GRID + (size_t)MOE_TREE_MAX_GRID * 2 * 4 * rows * (k.dim + 2);
+    // control words, cuts, and two partials of the largest row block a run
+    const size_t rows = k.dim == 64 ? (size_t)MOE_TREE_MAX_GRID * 64
+                        : k.dim == 128 ? (size_t)MOE_TTC_MAX_GRID * MOE_TTC_ROWS : (size_t)MOE_TREE_MAX_GRID * 16;
+    bytes = SPEC_CTRL_BYTES + sizeof(TreeCut) * MOE_TREE_MAX_GRID + rows * 2 * 4 * (k.dim + 2);
     return MOE_OK;
 }
 
@@ -369,8 +388,8 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     a.o_wide = aligned(out_dev, 16) && (out_token_stride | out_head_stride) % 8 == 0;
     a.min_units = 2 * MOE_TREE_WARPS;
     a.ctrl = static_cast<uint32_t *>(ws_dev);
-    a.count = a.ctrl + SPEC_CTRL_BYTES / 4;
-    a.part = reinterpret_cast<float *>(a.count + MOE_TREE_MAX_GRID);
+    a.cuts = reinterpret_cast<TreeCut *>(a.ctrl + SPEC_CTRL_BYTES / 4);
+    a.part = reinterpret_cast<float *>(a.cuts + MOE_TREE_MAX_GRID);
     a.wait_ns = host_wait_ns();
     // the row block from the mean rows of a sequence (the lengths themselves are on the device)
     TreeDevice *dev;
@@ -378,16 +397,14 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
         return rc;
     const int rows = (n_tokens + batch - 1) / batch * a.group;
     if (a.k.dim == 128 && rows > 16) {
-        const TtcInstance &t = dev->tc[(a.k.fmt == MOE_KV_Q8 ? 0 : 3) + (rows <= 32 ? 0 : rows <= 64 ? 1 : 2)];
+        const TtcInstance &t = dev->tc[a.k.fmt == MOE_KV_Q8 ? 0 : 1];
         const size_t used = t.fixed + 8 * ((size_t)batch + 1);
         const int stages = (int)std::min<size_t>(4, (dev->optin - used) / t.stage);
-        if (stages < 2)
-            return host_fail(MOE_EUNSUPPORTED, "moe_tree_attention: %zu bytes of shared memory do not fit", used + 2 * t.stage);
         a.min_units = 2;
-        const int grid = std::min(dev->sms, MOE_TREE_MAX_GRID * 32 / t.columns);  // what the partials' room holds
+        const int grid = std::min(dev->sms, MOE_TTC_MAX_GRID);
         t.kernel<<<grid, MOE_TTC_THREADS, used + stages * t.stage, (cudaStream_t)stream>>>(a, stages);
         SPEC_CUDA_OK(cudaGetLastError());
-        return MOE_OK;
+        return tree_join(a, grid, MOE_TTC_ROWS, (cudaStream_t)stream);
     }
     const TreeInstance &t = dev->inst[tree_choose(a.k.fmt, a.k.dim, rows)];
     // as many CTAs an SM as the registers allow while each ring keeps three stages
@@ -404,7 +421,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     const int grid = std::min(dev->sms * ctas, MOE_TREE_MAX_GRID);
     t.kernel<<<grid, MOE_TREE_THREADS, used + stages * t.stage, (cudaStream_t)stream>>>(a, stages);
     SPEC_CUDA_OK(cudaGetLastError());
-    return MOE_OK;
+    return tree_join(a, grid, t.rows, (cudaStream_t)stream);
 }
 
 int moe_spec_verify_workspace_bytes(int batch, int n_rows, size_t *bytes)

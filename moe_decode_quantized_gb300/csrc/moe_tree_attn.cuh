@@ -10,9 +10,9 @@
 // together. An item is (sequence, kv head, row block), a unit of it one block
 // of 16 tokens of the cache. The units of all items form one list that is cut
 // into equal runs, one a CTA, so ragged lengths cost nothing; a run that cuts
-// an item leaves a partial (o, m, l) in the workspace, and the CTA that
-// finishes an item last joins its partials in the order of the runs (no CTA
-// waits for another; the result does not depend on who is last).
+// an item leaves a partial (o, m, l) in the workspace, and a second kernel,
+// launched behind the first so that it starts the moment that one ends, joins
+// the partials of each cut item in the order of the runs.
 //
 // A warp takes every fourth unit of its CTA's run through a ring of its own
 // (one bulk copy a unit), and everything stays in registers: codes to f16 B
@@ -32,6 +32,12 @@ namespace moe {
 #define MOE_TREE_SLACK 8.0f
 #define MOE_TREE_LIFT 7.0f
 
+// an item that more than one run works on: its query rows, and the runs after
+// the one it starts in (0: there is no such item)
+struct TreeCut {
+    int first, n, head, block, runs, whole_run;  // whole_run: it begins where its first run does
+};
+
 struct TreeArgs {
     KvDims k;
     const uint8_t *pages;
@@ -50,8 +56,9 @@ struct TreeArgs {
     float scale;
     int q_wide, o_wide;       // rows of q (out) can be read (written) 16 bytes at a time
     int min_units;            // fewest units of a run
-    uint32_t *ctrl, *count;   // control words; [grid] arrivals at the item that leaves a run at its end
-    float *part;              // [grid][2] partials of part_floats
+    uint32_t *ctrl;
+    TreeCut *cuts;     // [grid] the item that starts in the run and leaves it
+    float *part;              // [grid][2] partials: rows of head size, then references, then sums
     unsigned long long wait_ns;
 };
 
@@ -258,6 +265,76 @@ __device__ __forceinline__ void tree_store(const TreeArgs &a, const TreeItem &it
         }
 }
 
+// the run's last item, if it starts in the run and goes on after it
+__device__ __forceinline__ void tree_cut(const TreeArgs &a, const TreeItem &it, long long lo, long long run)
+{
+    const long long p0 = it.lo / run, p1 = (it.lo + it.units - 1) / run;
+    a.cuts[blockIdx.x] = {it.first, it.n, it.head, it.block, p0 == blockIdx.x ? (int)(p1 - p0) : 0, it.lo == lo};
+}
+
+#define MOE_TREE_JOIN_ROWS 16
+#define MOE_TREE_JOIN_THREADS 256
+
+// Joins the partials of cut items: CTA (run, 16 rows of the row block). Bound
+// by latency: a round of loads for the weights, then one for each few parts.
+template <int D>
+__global__ void __launch_bounds__(MOE_TREE_JOIN_THREADS) moe_tree_join_kernel(const __grid_constant__ TreeArgs a, const int rows)
+{
+    constexpr int NT = MOE_TREE_JOIN_THREADS, PER = MOE_TREE_JOIN_ROWS * D / NT, STEP = NT / D > 0 ? NT / D : 1;
+    __shared__ float top[MOE_TREE_JOIN_ROWS], sum[MOE_TREE_JOIN_ROWS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const size_t size = (size_t)rows * (D + 2);
+    pdl_wait();
+    const TreeCut c = a.cuts[blockIdx.x];
+    const int r0 = blockIdx.y * MOE_TREE_JOIN_ROWS, live = min(MOE_TREE_JOIN_ROWS, c.n * a.group - c.block * rows - r0);
+    if (c.runs == 0 || live <= 0)
+        return;
+    // part i: of the first run the second slot, unless the item begins with the run
+    auto part = [&](int i) { return a.part + ((size_t)(blockIdx.x + i) * 2 + (i == 0 && !c.whole_run ? 1 : 0)) * size; };
+    for (int r = warp; r < live; r += NT / 32) {
+        float m = -INFINITY, l = 0.0f;
+        for (int i = lane; i <= c.runs; i += 32)
+            m = fmaxf(m, part(i)[rows * D + r0 + r]);
+#pragma unroll
+        for (int x = 16; x; x /= 2)
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+        for (int i = lane; i <= c.runs; i += 32) {
+            const float v = part(i)[rows * D + r0 + r];
+            l += part(i)[rows * (D + 1) + r0 + r] * (v == -INFINITY ? 1.0f : ex2(v - m));  // a NaN sum stays
+        }
+        l = warp_sum(l);
+        if (lane == 0) {
+            top[r] = m;
+            sum[r] = l;
+        }
+    }
+    __syncthreads();
+    float o[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+        o[k] = 0.0f;
+    const int d = tid % D, r1 = tid / D;  // rows r1, r1 + STEP, ..
+#pragma unroll 2
+    for (int i = 0; i <= c.runs; ++i) {
+        const float *p = part(i) + r0 * D;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int r = r1 + k * STEP;
+            if (r < live) {
+                const float v = part(i)[rows * D + r0 + r];
+                o[k] = fmaf(p[r * D + d], v == -INFINITY ? 1.0f : ex2(v - top[r]), o[k]);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int r = r1 + k * STEP, rr = c.block * rows + r0 + r;
+        if (r < live)
+            a.out[(c.first + rr / a.group) * a.o_tok + (c.head * a.group + rr % a.group) * a.o_head + d] =
+                __bfloat16_as_ushort(__float2bfloat16_rn(sum[r] == 0.0f ? 0.0f : o[k] / sum[r]));
+    }
+}
+
 template <int FMT, int D, int MT>
 __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS) moe_tree_attn_kernel(const __grid_constant__ TreeArgs a, const int stages)
 {
@@ -316,8 +393,12 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
     const long long total = cum[a.batch];
     const long long run = max((total + gridDim.x - 1) / (long long)gridDim.x, (long long)a.min_units);
     const long long lo = run * blockIdx.x, hi = min(lo + run, total);
-    if (lo >= hi)
+    pdl_launch_dependents();
+    if (lo >= hi) {
+        if (tid == 0)
+            a.cuts[blockIdx.x].runs = 0;
         return;
+    }
     const int mine = (int)((hi - lo - warp + MOE_TREE_WARPS - 1) / MOE_TREE_WARPS);  // this warp's units
     const uint64_t policy = policy_evict_first();
     bool ok = true;
@@ -680,76 +761,26 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
             } else {  // a partial: slot 0 is the run's first item, 1 its last
                 float *part = a.part + ((size_t)blockIdx.x * 2 + (u == lo ? 0 : 1)) * T::PART;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int j = 0; j < T::NB; ++j)
-                        reinterpret_cast<float4 *>(part)[(mt * T::NB + j) * 32 + lane] =
-                            make_float4(o[mt][j][0], o[mt][j][1], o[mt][j][2], o[mt][j][3]);
+                    for (int r = 0; r < 2; ++r) {
+                        const int row = mt * 16 + r * 8 + g;
+                        float *p = part + row * D + t4 * (D / 4);
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
+                        for (int e = 0; e < D / 4; e += 4) {  // column 2 t4 of block j is dimension 2 t4 D / 8 + j
+                            const int c = 2 * r + e / (D / 8), j = e % (D / 8);
+                            *reinterpret_cast<float4 *>(p + e) =
+                                make_float4(o[mt][j][c], o[mt][j + 1][c], o[mt][j + 2][c], o[mt][j + 3][c]);
+                        }
                         if (t4 == 0) {
-                            part[T::ROWS * D + mt * 16 + r * 8 + g] = m[mt][r];
-                            part[T::ROWS * D + T::ROWS + mt * 16 + r * 8 + g] = l[mt][r];
-                        }
-                }
-                __threadfence();
-                __syncwarp();
-                const int c0 = (int)(it.lo / run), c1 = (int)((item_end - 1) / run);  // the item's runs
-                unsigned old = 0;
-                if (lane == 0)
-                    old = atom_add_acq_rel_gpu(a.count + c0, 1);
-                old = __shfl_sync(0xFFFFFFFFu, old, 0);
-                if (old == (unsigned)(c1 - c0)) {  // the last: join
-                    __threadfence();
-                    if (lane == 0)
-                        st_relaxed_gpu(a.count + c0, 0);
-                    auto slot = [&](int cta) { return a.part + ((size_t)cta * 2 + (it.lo <= cta * run ? 0 : 1)) * T::PART; };
-                    float up[MT][2];
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            up[mt][r] = -INFINITY;
-                            l[mt][r] = 0.0f;
-                        }
-                    for (int cta = c0; cta <= c1; ++cta)
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                            for (int r = 0; r < 2; ++r)
-                                up[mt][r] = fmaxf(up[mt][r], __ldcg(slot(cta) + T::ROWS * D + mt * 16 + r * 8 + g));
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int j = 0; j < T::NB; ++j)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                o[mt][j][i] = 0.0f;
-                    for (int cta = c0; cta <= c1; ++cta) {
-                        const float *src = slot(cta);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            float f[2];
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const float v = __ldcg(src + T::ROWS * D + mt * 16 + r * 8 + g);
-                                f[r] = v == -INFINITY ? 1.0f : ex2(v - up[mt][r]);
-                                l[mt][r] += __ldcg(src + T::ROWS * D + T::ROWS + mt * 16 + r * 8 + g) * f[r];
-                            }
-#pragma unroll
-                            for (int j = 0; j < T::NB; ++j) {
-                                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src) + (mt * T::NB + j) * 32 + lane);
-                                o[mt][j][0] = fmaf(v.x, f[0], o[mt][j][0]);
-                                o[mt][j][1] = fmaf(v.y, f[0], o[mt][j][1]);
-                                o[mt][j][2] = fmaf(v.z, f[1], o[mt][j][2]);
-                                o[mt][j][3] = fmaf(v.w, f[1], o[mt][j][3]);
-                            }
+                            part[T::ROWS * D + row] = m[mt][r];
+                            part[T::ROWS * D + T::ROWS + row] = l[mt][r];
                         }
                     }
-                    tree_store<D, MT>(a, it, o, l, lane);
-                }
             }
         }
+        if (end == hi && tid == 0)
+            tree_cut(a, it, lo, run);
         u = end;
     }
     if (!ok)  // a copy did not arrive in time: wait for those in flight (bounded) before the memory is given back

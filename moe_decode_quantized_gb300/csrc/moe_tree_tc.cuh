@@ -1,24 +1,23 @@
 // moe_tree_tc.cuh -- tree attention for more than 16 query rows a kv head, on
 // the 5th-generation tensor cores: the same sums, list of work and partials
-// as moe_tree_attn.cuh, in tiles of 128 tokens.
+// as moe_tree_attn.cuh, in tiles of 128 tokens and up to 128 rows an M tile.
 //
-// Tokens are the M side, so that any number of rows costs what it is:
-//   S^T [128 tokens x N rows] = K [tokens x 128] Q^T,
-//   O^T [128 dims x N rows] += V^T [dims x tokens] P^T [tokens x rows],
-// both accumulators in tensor memory, a token (a dimension) a lane. V lies in
-// shared memory as K does, 128-byte rows of 64 dimensions a token in the
-// 128-byte swizzle: read with M contiguous it is V^T; P^T likewise, a token's
-// row of 64 weights, read with N contiguous. The maximum of a row runs across
-// lanes, so the weights are taken against a reference that only moves when a
-// score passes it by 2^8 (one vote a tile; the exact maxima are then found,
-// and o and the sums scaled).
+//   S [128 rows x 128 tokens] = Q [rows x 128] K^T,
+//   O [128 rows x 128 dims] += P [rows x tokens] V,
+// S, P and O in tensor memory, a row a lane, so that a row's maximum and sum
+// are one thread's. P takes the place of its S, as f16, and is the second
+// product's A operand from there; K and V lie in shared memory as 128-byte
+// rows of 64 dimensions in the 128-byte swizzle (V read with the dimensions
+// contiguous). Two groups of four softmax warps, each with an S and an O:
+//  - a row block of more than 128 rows: a group an M tile, every token tile
+//    for both, so that one's softmax runs under the other's products;
+//  - up to 128 rows: the groups take the token tiles in turn, each keeping its
+//    own maximum, sum and O, and are joined at the item's end.
+// A reference m moves only when a score passes it by 2^8 (O is then scaled).
 //
-// One CTA an SM: a warp copies the cache's blocks, four turn codes into f16
-// tiles, eight (two column halves of the four lane quarters) do the softmax,
-// one thread issues the products. K of tile t + 1 is made while the softmax
-// of tile t runs. What bounds it: shared memory, which a tile's codes and f16
-// values cross five times (128 tokens of Q8: 35 KB in, out, 64 KB in, out,
-// and Q, P in proportion to N), about 1800 cycles a tile for any N <= 64.
+// One CTA an SM: a warp copies the cache's blocks, eight turn codes into f16
+// tiles (K of the next tile while this one's softmax runs, V once the last
+// tile's second product is done), one thread issues the products.
 #pragma once
 #include "moe_tc.cuh"
 #include "moe_tree_attn.cuh"
@@ -26,13 +25,12 @@
 namespace moe {
 
 #define MOE_TTC_TOKENS 128
-#define MOE_TTC_SOFT 8   // softmax warps
-#define MOE_TTC_CODE 4   // warps that turn codes into f16
-// the offset of a row without a reference: every finite score then asks for one
-#define MOE_TTC_NONE 3.0e38f
+#define MOE_TTC_ROWS 256  // of a row block: two M tiles
+#define MOE_TTC_SOFT 8    // softmax warps
+#define MOE_TTC_CODE 8    // warps that turn codes into f16
 #define MOE_TTC_THREADS ((MOE_TTC_SOFT + MOE_TTC_CODE + 2) * 32)
 
-template <int FMT, int N>
+template <int FMT>
 struct TtcShape {
     static constexpr int D = 128;
     static constexpr int RB = FMT == MOE_KV_Q8 ? D : D / 2;
@@ -40,33 +38,12 @@ struct TtcShape {
     static constexpr int HALF = 16 * RB + 16 * GR * (FMT == MOE_KV_Q8 ? 2 : 4);
     static constexpr int BLOCK = 2 * HALF;
     static constexpr int STAGE = 8 * BLOCK;                // a tile's blocks
-    static constexpr int PANEL = MOE_TTC_TOKENS * 128;     // 64 columns of 128 tokens
-    static constexpr int PP = (N + 63) / 64;               // panels of P
-    static constexpr int K_AT = 0, V_AT = 2 * PANEL, P_AT = 4 * PANEL, Q_AT = P_AT + PP * PANEL;
-    static constexpr int RAW_AT = Q_AT + 2 * N * 128;
-    static constexpr int COLS = N <= 32 ? 128 : N <= 64 ? 256 : 512;  // of tensor memory: S, S, O
-    static constexpr int CPT = N / 2;                      // columns of a softmax thread
-    // small arrays, after the raw stages: barriers, (multiplier, offset), factors, per-quarter maxima and sums,
-    // masks, places of the output rows, stage flags, the scan and the list
-    static constexpr int BARS = 256;
-    static constexpr int SMALL = BARS + N * (8 + 4 + 4 * 4 + 4 * 4 + 4 + 8 + 8) + 128;
-    static constexpr int PART = N * D + 2 * N;             // floats of a partial: [row][dim], references, sums
+    static constexpr int PANEL = MOE_TTC_TOKENS * 128;     // 64 dimensions of 128 tokens (rows)
+    static constexpr int K_AT = 0, V_AT = 2 * PANEL, Q_AT = 4 * PANEL;  // Q: [M tile][2 panels]
+    static constexpr int RAW_AT = Q_AT + 4 * PANEL;
+    // after the raw stages: barriers, rows' multipliers, the second group's references and sums, the scan and the list
+    static constexpr int SMALL = 256 + 4 * 256 + 2 * 4 * 128 + 32 * 8;
 };
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
-{
-    uint32_t r[16];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-                 "%14, %15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr)
-                 : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        v[i] = __uint_as_float(r[i]);
-}
 
 // descriptor of a tile whose M (N) side is contiguous: 128-byte rows of 64
 // elements, one row a k, in the 128-byte swizzle; 8 rows are 1024 bytes apart
@@ -80,23 +57,6 @@ __device__ __forceinline__ uint64_t mn_desc(const void *tile)
 
 // the softmax warps' own barrier
 __device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(MOE_TTC_SOFT * 32) : "memory"); }
-__device__ __forceinline__ bool soft_any(bool p)
-{
-    uint32_t r;
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n"
-                 " selp.u32 %0, 1, 0, q;\n}\n"
-                 : "=r"(r)
-                 : "r"((uint32_t)p), "n"(MOE_TTC_SOFT * 32)
-                 : "memory");
-    return r != 0;
-}
-
-__device__ __forceinline__ float warp_max(float v)  // no NaN
-{
-    const uint32_t u = __float_as_uint(v), key = u & 0x80000000u ? ~u : u | 0x80000000u;
-    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, key);
-    return __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
-}
 
 // 16 codes (four words) of a 16-byte piece of Q8 as f16 pairs
 __device__ __forceinline__ void q8_sixteen(const uint4 &w, __half2 d, uint32_t (&h)[8])
@@ -121,39 +81,31 @@ __device__ __forceinline__ void q4_sixteen(uint32_t w0, uint32_t w1, __half2 d, 
     }
 }
 
-// 16 consecutive dimensions (from 16 x) of a token's row of an f16 tile: two
-// 16-byte pieces, the `second` one first in half of the lanes (bank conflicts)
-__device__ __forceinline__ void put_sixteen(uint8_t *tile, int token, int x, const uint32_t (&h)[8], bool swap)
+// stores 16 consecutive dimensions of a token: pieces of 16 bytes at off and off ^ 16
+__device__ __forceinline__ void put_sixteen(uint8_t *tile, uint32_t off, const uint32_t (&h)[8])
 {
-    uint8_t *row = tile + (x >> 2) * (MOE_TTC_TOKENS * 128) + token * 128;
-    const int c = (x & 3) * 2;
-    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-    *reinterpret_cast<uint4 *>(row + (((c + (swap ? 1 : 0)) ^ (token & 7)) << 4)) = swap ? hi : lo;
-    *reinterpret_cast<uint4 *>(row + (((c + (swap ? 0 : 1)) ^ (token & 7)) << 4)) = swap ? lo : hi;
+    *reinterpret_cast<uint4 *>(tile + off) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4 *>(tile + (off ^ 16u)) = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
-template <int FMT, int N>
+template <int FMT>
 __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const __grid_constant__ TreeArgs a, const int stages)
 {
-    using T = TtcShape<FMT, N>;
-    constexpr int D = T::D, CPT = T::CPT;
+    using T = TtcShape<FMT>;
+    constexpr int D = T::D, ROWS = MOE_TTC_ROWS;
+    constexpr uint32_t S_COL = 0, O_COL = 256;  // of tensor memory: S (and P) of the two groups, O of the two
     extern __shared__ __align__(1024) uint8_t smem_any[];
     uint8_t *smem = smem_any + (-smem_u32(smem_any) & 1023u);  // the swizzle goes by address bits
-    uint8_t *sk = smem + T::K_AT, *sv = smem + T::V_AT, *sp = smem + T::P_AT, *sq = smem + T::Q_AT;
+    uint8_t *sk = smem + T::K_AT, *sv = smem + T::V_AT, *sq = smem + T::Q_AT;
     uint8_t *raw = smem + T::RAW_AT, *small = raw + (size_t)stages * T::STAGE;
     uint64_t *bars = reinterpret_cast<uint64_t *>(small);
-    uint64_t *raw_full = bars, *raw_free = bars + 4, *k_full = bars + 8, *v_full = bars + 9, *p_full = bars + 10,
-             *q_full = bars + 11, *pv_done = bars + 12, *s_full = bars + 13;  // s_full[2]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 16);
+    uint64_t *raw_full = bars, *raw_free = bars + 4, *k_full = bars + 8, *v_full = bars + 9, *k_done = bars + 10,
+             *v_done = bars + 11, *q_full = bars + 12, *s_full = bars + 13, *p_full = bars + 15, *o_done = bars + 17;  // s_full, p_full [2]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
     uint32_t *gone = tmem_slot + 1;  // [8] blocks of tile t that are not there, at t % 8: kept longer than its stage
-    int *last = reinterpret_cast<int *>(gone + 8);
-    float2 *mul = reinterpret_cast<float2 *>(small + T::BARS);                // [N] (c, 7 - m)
-    float *ref = reinterpret_cast<float *>(mul + N);                          // [N] m
-    float *qmax = ref + N, *qsum = qmax + 4 * N;                              // [4][N]
-    float *factor = qsum + 4 * N;                                             // [N]
-    unsigned long long *masks = reinterpret_cast<unsigned long long *>(factor + N);  // [N]
-    long long *rowat = reinterpret_cast<long long *>(masks + N);              // [N]
-    long long *scan = rowat + N, *cum = scan + 16;                            // [batch + 1]
+    float *mul = reinterpret_cast<float *>(small + 256);  // [256] rows' multipliers
+    float *ref2 = mul + 256, *sum2 = ref2 + 128;          // the second group's
+    long long *scan = reinterpret_cast<long long *>(sum2 + 128), *cum = scan + 32;  // cum [batch + 1]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t *status = a.ctrl + MOE_CTRL_STATUS;
 
@@ -164,15 +116,18 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
         }
         mbar_init(k_full, MOE_TTC_CODE);
         mbar_init(v_full, MOE_TTC_CODE);
-        mbar_init(p_full, MOE_TTC_SOFT);
+        mbar_init(k_done, 1);
+        mbar_init(v_done, 1);
         mbar_init(q_full, MOE_TTC_SOFT);
-        mbar_init(pv_done, 1);
-        mbar_init(s_full, 1);
-        mbar_init(s_full + 1, 1);
+        mbar_init(o_done, 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(s_full + x, 1);
+            mbar_init(p_full + x, MOE_TTC_SOFT / 2);
+        }
         fence_barrier_init();
     }
     if (warp == 0)
-        tmem_alloc(tmem_slot, T::COLS);
+        tmem_alloc(tmem_slot, 512);
     // the list: tiles before each sequence
     {
         constexpr int NT = MOE_TTC_THREADS;
@@ -186,7 +141,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
             tree_sequence(a, b, first, n, len, rows);
             cum[b] = mine;
             mine += (long long)((len + MOE_TTC_TOKENS - 1) / MOE_TTC_TOKENS) *
-                    (n > 0 ? tree_blocks<N>(n, a.group) * a.k.heads : 0);
+                    (n > 0 ? tree_blocks<ROWS>(n, a.group) * a.k.heads : 0);
             if (n == 0 && rows > 0 && blockIdx.x == (unsigned)(b % gridDim.x))
                 tree_zero<D>(a, first, rows);
         }
@@ -216,20 +171,29 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
     const long long run = max((total + gridDim.x - 1) / (long long)gridDim.x, (long long)a.min_units);
     const long long lo = min(run * blockIdx.x, total), hi = min(lo + run, total);
     const int tiles = (int)(hi - lo);
-    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, status, a.wait_ns); };
-    auto item_at = [&](long long u) { return tree_item<N, MOE_TTC_TOKENS>(a, cum, u); };
+    pdl_launch_dependents();
+    if (tiles == 0 && tid == 0)
+        a.cuts[blockIdx.x].runs = 0;
+    auto wait = [&](uint64_t *bar, int phase) { return mbar_wait(bar, (uint32_t)phase & 1u, status, a.wait_ns); };
+    auto item_at = [&](int t) { return tree_item<ROWS, MOE_TTC_TOKENS>(a, cum, lo + t); };
+    // the item's tiles of this run end before tile:
+    auto item_end = [&](const TreeItem &it) { return (int)(min(hi, it.lo + it.units) - lo); };
+    auto wide = [&](const TreeItem &it) { return it.n * a.group - it.block * ROWS > 128; };  // a group an M tile
 
     if (warp == MOE_TTC_SOFT + MOE_TTC_CODE) {
         // ---------------- the copies: lane i the i-th block of a tile
         const uint64_t policy = policy_evict_first();
         bool ok = true;
-        int t = 0;
-        for (; t < tiles && ok; ++t) {
-            const TreeItem it = item_at(lo + t);
+        int t = 0, end = 0;
+        TreeItem it{};
+        for (; t < tiles; ++t) {
+            if (t == end) {
+                it = item_at(t);
+                end = item_end(it);
+            }
             const int blk = (int)(lo + t - it.lo) * 8 + lane, per_page = a.k.page / 16;
-            const bool there = lane < 8 && blk * 16 < it.len;
             const uint8_t *src = nullptr;
-            if (there) {
+            if (lane < 8 && blk * 16 < it.len) {
                 const int page = a.table[it.b * a.table_stride + blk / per_page];
                 if (page < 0 || page >= a.n_pages)
                     atomicOr(status, (uint32_t)MOE_WS_INDEX);
@@ -239,7 +203,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
             const uint32_t got = __ballot_sync(0xFFFFFFFFu, src != nullptr);
             const int s = t % stages;
             if (t >= stages)
-                ok = __all_sync(0xFFFFFFFFu, wait(raw_free + s, (uint32_t)(t / stages - 1) & 1u));
+                ok = __all_sync(0xFFFFFFFFu, wait(raw_free + s, t / stages - 1));
             if (!ok)
                 break;
             if (lane == 0) {
@@ -251,356 +215,398 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 bulk_g2s(raw + (size_t)s * T::STAGE + lane * T::BLOCK, src, T::BLOCK, raw_full + s, policy);
         }
         for (int k = max(0, t - stages); k < t; ++k)  // nothing in flight when the memory is given back
-            wait(raw_full + k % stages, (uint32_t)(k / stages) & 1u);
+            wait(raw_full + k % stages, k / stages);
     } else if (warp == MOE_TTC_SOFT + MOE_TTC_CODE + 1) {
         // ---------------- the products
         if (lane == 0) {
-            constexpr uint32_t id_s = mma_idesc(128, N, false), id_o = id_s | (1u << 15) | (1u << 16);
-            bool ok = true, open = false;  // open: tile t - 1's second product is still to come
-            uint32_t items = 0;
-            bool fresh = false;  // that tile is its item's first
-            long long end = lo;
-            auto second = [&](int t) {
-                ok = ok && wait(v_full, (uint32_t)t & 1u) && wait(p_full, (uint32_t)t & 1u);
+            constexpr uint32_t id_s = mma_idesc(128, 128, false), id_o = id_s | (1u << 16);
+            const uint64_t kd = sw128_desc(sk), vd = mn_desc(sv);
+            bool ok = true;
+            // by group, a bit each: parity of the products S begun; whether O of the last is still to come; whether
+            // that is the item's first
+            uint32_t jobs = 0, open = 0, fresh = 0;
+            int open_tile = -1, begin = 0, end = 0, items = 0;
+            bool two = false;
+            auto first = [&](int x, int m) {  // S of group x from M tile m
+                const uint64_t qd = sw128_desc(sq + m * 2 * T::PANEL);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)  // 16 dimensions: 32 bytes, then the next panel
+                    mma_f16(tmem + S_COL + x * 128, qd + (k / 4) * (T::PANEL / 16) + (k % 4) * 2,
+                            kd + (k / 4) * (T::PANEL / 16) + (k % 4) * 2, id_s, k > 0);
+                mma_commit(s_full + x);
+                jobs ^= 1u << x;
+                open |= 1u << x;
+            };
+            auto second = [&](int x) {  // O of group x += P V of the open tile
+                if (!(open >> x & 1) || !ok)
+                    return;
+                ok = wait(v_full, open_tile) && wait(p_full + x, (int)(jobs >> x & 1) - 1);
                 if (!ok)
                     return;
                 tc_fence_after();
-                const uint64_t ad = mn_desc(sv), bd = mn_desc(sp);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)  // 16 tokens: 2048 bytes
-                    mma_f16(tmem + 2 * N, ad + k * 128, bd + k * 128, id_o, !fresh || k > 0);
-                mma_commit(pv_done);
+                for (int k = 0; k < 8; ++k)  // 16 tokens: 8 columns of P, 2048 bytes of V
+                    mma_f16_ts(tmem + O_COL + x * 128, tmem + S_COL + x * 128 + k * 8, vd + k * 128, id_o, !(fresh >> x & 1) || k > 0);
+                fresh &= ~(1u << x);
+                open &= ~(1u << x);
             };
             for (int t = 0; t < tiles && ok; ++t) {
-                const bool starts = lo + t == end;
-                if (starts) {  // the softmax warps finish the last item before they bring the next one's queries
-                    if (open)
-                        second(t - 1);
-                    open = false;
-                    const TreeItem it = item_at(lo + t);
-                    end = min(hi, it.lo + it.units);
-                    ok = ok && wait(q_full, items & 1u);
-                    ++items;
+                if (t == end) {  // a new item: the softmax warps finish the last before they bring its queries
+                    second(0);
+                    second(1);
+                    if (t > 0) {
+                        mma_commit(v_done);
+                        mma_commit(o_done);
+                    }
+                    open_tile = -1;
+                    begin = t;
+                    const TreeItem it = item_at(t);
+                    end = item_end(it);
+                    two = wide(it);
+                    fresh = 3;
+                    ok = ok && wait(q_full, items++);
                 }
-                ok = ok && wait(k_full, (uint32_t)t & 1u);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                const uint64_t ad = sw128_desc(sk), bd = sw128_desc(sq);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)  // 16 dimensions: 32 bytes, then the next panel
-                    mma_f16(tmem + (t & 1) * N, ad + (k / 4) * (T::PANEL / 16) + (k % 4) * 2,
-                            bd + (k / 4) * (N * 128 / 16) + (k % 4) * 2, id_s, k > 0);
-                mma_commit(s_full + (t & 1));
-                if (open)
-                    second(t - 1);
-                open = true;
-                fresh = starts;
-            }
-            if (open && ok)
-                second(tiles - 1);
-            if (tiles > 0 && ok)
-                wait(pv_done, (uint32_t)(tiles - 1) & 1u);
-        }
-    } else if (warp >= MOE_TTC_SOFT) {
-        // ---------------- codes to f16: warp w the blocks w, w + 4 of a tile
-        const int w = warp - MOE_TTC_SOFT, g = lane >> 2, t4 = lane & 3;
-        bool ok = true;
-        for (int t = 0; t < tiles; ++t) {
-            const TreeItem it = item_at(lo + t);
-            const int s = t % stages, left = it.len - (int)(lo + t - it.lo) * MOE_TTC_TOKENS;  // tokens from the tile on
-            ok = ok && wait(raw_full + s, (uint32_t)(t / stages) & 1u);
-            if (t > 0)  // K has been read
-                ok = ok && wait(s_full + ((t - 1) & 1), (uint32_t)((t - 1) >> 1) & 1u);
-            if (!__all_sync(0xFFFFFFFFu, ok))
-                break;
-            const uint32_t out = *reinterpret_cast<volatile uint32_t *>(gone + (t & 7));
-            const uint8_t *stage = raw + (size_t)s * T::STAGE;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int blk = w + 4 * x;
-                const uint8_t *b = stage + blk * T::BLOCK;
-#pragma unroll
-                for (int nb = 0; nb < 2; ++nb) {
-                    const int tok = nb * 8 + g, at = blk * 16 + tok;
-                    uint32_t h[8];
-                    if (FMT == MOE_KV_Q8) {
-                        const __half2 d = __half2half2(reinterpret_cast<const __half *>(b + 16 * T::RB)[tok * 4 + t4]);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int c = i ^ (g & 1);
-                            const uint4 v = *reinterpret_cast<const uint4 *>(b + (nb * 2 + c) * 512 + lane * 16);
-                            q8_sixteen(v, d, h);
-                            put_sixteen(sk, at, t4 * 2 + c, h, t4 >= 2);
-                        }
-                    } else {
-                        const uint32_t dm = reinterpret_cast<const uint32_t *>(b + 16 * T::RB)[tok * 4 + t4];
-                        const __half2 d = h2(dup_lo(dm)), m = h2(dup_hi(dm));
-                        const uint4 v = *reinterpret_cast<const uint4 *>(b + nb * 512 + lane * 16);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int c = i ^ (g & 1);
-                            q4_sixteen(c ? v.z : v.x, c ? v.w : v.y, d, m, h);
-                            put_sixteen(sk, at, t4 * 2 + c, h, t4 >= 2);
-                        }
+                // two M tiles: O of the last tile frees the S that the next product writes; else the groups' S are
+                // taken in turn, and O of the last tile comes after S of this one
+                if (two) {
+                    for (int x = 0; x < 2; ++x) {
+                        second(x);
+                        if (x == 1 && open_tile >= 0)
+                            mma_commit(v_done);
+                        ok = ok && wait(k_full, t);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        first(x, x);
+                    }
+                    mma_commit(k_done);
+                } else {
+                    ok = ok && wait(k_full, t);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const int x = (t - begin) & 1;
+                    first(x, 0);
+                    mma_commit(k_done);
+                    if (open_tile >= 0) {
+                        second(x ^ 1);
+                        mma_commit(v_done);
                     }
                 }
+                open_tile = t;
             }
+            second(0);
+            second(1);
+            if (tiles > 0 && ok) {
+                mma_commit(v_done);
+                mma_commit(o_done);
+                wait(o_done, items - 1);
+            }
+        }
+    } else if (warp >= MOE_TTC_SOFT) {
+        // ---------------- codes to f16: warp w the block w of a tile. The lanes of eight that a store serves at once
+        // take pieces (tokens) that the swizzle puts in different banks.
+        const int w = warp - MOE_TTC_SOFT, g = lane >> 2, t4 = lane & 3, turn = t4 >> 1;
+        // K, first piece: 16 dimensions from 32 t4 + 16 turn of token g; the other piece is 32 bytes off (xor)
+        const uint32_t k_off = (uint32_t)(turn * T::PANEL + (w * 16 + g) * 128 + ((((t4 & 1) * 4 + turn * 2) ^ g) << 4));
+        // V, 16 dimensions from 16 g of token 2 t4 + (g & 1), and of 2 t4 + 1 - (g & 1)
+        const int odd = g & 1;
+        const uint32_t v_row = (uint32_t)((g >> 2) * T::PANEL + (w * 16 + 2 * t4) * 128);
+        const uint32_t v_off[2] = {v_row + odd * 128 + ((((g & 3) * 2) ^ (2 * t4) ^ odd) << 4),
+                                   v_row + (1 - odd) * 128 + ((((g & 3) * 2) ^ (2 * t4) ^ (1 - odd)) << 4)};
+        constexpr int KP = FMT == MOE_KV_Q8 ? 4 : 2;  // 16-byte pieces of a block's K (V) codes a lane
+        bool ok = true;
+        int end = 0;
+        TreeItem it{};
+        for (int t = 0; t < tiles; ++t) {
+            if (t == end) {
+                it = item_at(t);
+                end = item_end(it);
+            }
+            const int s = t % stages, left = it.len - (int)(lo + t - it.lo) * MOE_TTC_TOKENS - w * 16;  // of this block
+            ok = ok && wait(raw_full + s, t / stages);
+            const uint8_t *b = raw + (size_t)s * T::STAGE + w * T::BLOCK;
+            uint4 v[KP];
+            uint32_t sc[4], mn[4];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < KP; ++i)
+                v[i] = *reinterpret_cast<const uint4 *>(b + (FMT == MOE_KV_Q8 ? i ^ turn : i) * 512 + lane * 16);
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb) {
+                const int at = (nb * 8 + g) * 4 + t4;
+                if (FMT == MOE_KV_Q8) {
+                    sc[nb] = h2(__half2half2(reinterpret_cast<const __half *>(b + 16 * T::RB)[at]));
+                } else {
+                    const uint32_t dm = reinterpret_cast<const uint32_t *>(b + 16 * T::RB)[at];
+                    sc[nb] = dup_lo(dm);
+                    mn[nb] = dup_hi(dm);
+                }
+            }
+            if (t > 0)
+                ok = ok && wait(k_done, t - 1);
+            if (!__all_sync(0xFFFFFFFFu, ok))
+                break;
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t h[8];
+                    if (FMT == MOE_KV_Q8) {
+                        q8_sixteen(v[(nb * 2 + i) % KP], h2(sc[nb]), h);
+                    } else {
+                        const uint4 u = v[nb];
+                        const bool hi2 = (i ^ turn) != 0;
+                        q4_sixteen(hi2 ? u.z : u.x, hi2 ? u.w : u.y, h2(sc[nb]), h2(mn[nb]), h);
+                    }
+                    put_sixteen(sk, (k_off ^ (uint32_t)(i * 32)) + nb * 1024, h);
+                }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(k_full);
-            if (t > 0)  // V has been read
-                ok = wait(pv_done, (uint32_t)(t - 1) & 1u);
+            const bool there = !(*reinterpret_cast<volatile uint32_t *>(gone + (t & 7)) >> w & 1);
+            const uint8_t *vb = b + T::HALF;
+            const __half *p = reinterpret_cast<const __half *>(vb + 16 * T::RB) + (g >> 1) * 16;
+#pragma unroll
+            for (int i = 0; i < KP; ++i)
+                v[i] = *reinterpret_cast<const uint4 *>(vb + (FMT == MOE_KV_Q8 ? i ^ odd : i) * 512 + lane * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tok = (i >> 1) * 8 + 2 * t4 + ((i & 1) ^ odd);
+                const bool in = there && tok < left;  // else the bytes are anything: values of 0
+                sc[i] = in ? h2(__half2half2(p[tok])) : 0u;
+                if (FMT == MOE_KV_Q4)
+                    mn[i] = in ? h2(__half2half2(p[T::GR * 16 + tok])) : 0u;
+            }
+            __syncwarp();
+            if (lane == 0)  // the stage is in registers
+                mbar_arrive(raw_free + s);
+            if (t > 0)
+                ok = wait(v_done, t - 1);
             if (!__all_sync(0xFFFFFFFFu, ok))
                 break;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int blk = w + 4 * x;
-                const uint8_t *b = stage + blk * T::BLOCK + T::HALF;
-                const __half *sc = reinterpret_cast<const __half *>(b + 16 * T::RB);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int tok = (r >> 1) * 8 + t4 * 2 + (r & 1), at = blk * 16 + tok;
-                    const bool in = at < left && !(out >> blk & 1);  // else the bytes are anything: 0
-                    const __half2 d = __half2half2(in ? sc[(g >> 1) * 16 + tok] : __ushort_as_half(0));
-                    uint32_t h[8];
-                    if (FMT == MOE_KV_Q8) {
-                        q8_sixteen(*reinterpret_cast<const uint4 *>(b + r * 512 + lane * 16), d, h);
-                    } else {
-                        const __half2 m = __half2half2(in ? sc[(T::GR + (g >> 1)) * 16 + tok] : __ushort_as_half(0));
-                        const uint2 v = *reinterpret_cast<const uint2 *>(b + (r >> 1) * 512 + lane * 16 + (r & 1) * 8);
-                        q4_sixteen(v.x, v.y, d, m, h);
-                    }
-                    put_sixteen(sv, at, g, h, g & 1);
+            for (int i = 0; i < 4; ++i) {
+                uint32_t h[8];
+                if (FMT == MOE_KV_Q8) {
+                    q8_sixteen(v[i % KP], h2(sc[i]), h);
+                } else {
+                    const uint4 u = v[i >> 1];
+                    const bool hi2 = ((i & 1) ^ odd) != 0;
+                    q4_sixteen(hi2 ? u.z : u.x, hi2 ? u.w : u.y, h2(sc[i]), h2(mn[i]), h);
                 }
+                put_sixteen(sv, v_off[i & 1] + (i >> 1) * 1024, h);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
+            if (lane == 0)
                 mbar_arrive(v_full);
-                mbar_arrive(raw_free + s);
-            }
         }
     } else {
-        // ---------------- softmax: quarter q's lanes (tokens; dimensions of O), columns from c0
-        const int quarter = warp & 3, half = warp >> 2, c0 = half * CPT, row = quarter * 32 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        // ---------------- softmax: group x, row `row` of its M tile
+        const int x = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_at = lanes + S_COL + x * 128, o_at = lanes + O_COL + x * 128;
         bool ok = true;
-        int t = 0;
-        while (t < tiles && ok) {
-            const long long u = lo + t;
-            const TreeItem it = item_at(u);
-            const long long end = min(hi, it.lo + it.units);
-            // ---- the item's queries: a row a pair of threads (64 dimensions each)
-            for (int r = tid >> 1; r < N; r += MOE_TTC_SOFT * 16) {
-                const int rr = it.block * N + r;
-                const bool live = rr < it.n * a.group;
-                const int i = live ? rr / a.group : 0, h = it.head * a.group + (live ? rr % a.group : 0);
-                uint32_t x[32];
-                const float c = tree_row<64, 2>(a, live, it.first + i, h, (tid & 1) * 64, x);
-                if ((tid & 1) == 0) {
-                    mul[r] = make_float2(c, MOE_TTC_NONE);
-                    ref[r] = -INFINITY;
-                    masks[r] = !live ? 0 : a.mask ? a.mask[it.first + i] : (2ull << i) - 1;
-                    rowat[r] = live ? (it.first + i) * a.o_tok + h * a.o_head : -1;
-                }
-                uint8_t *p = sq + (tid & 1) * (N * 128) + r * 128;
+        int jobs = 0, items = 0;
+        for (int t = 0; t < tiles;) {
+            // every warp goes through every item's barriers, a failed wait or not
+            const TreeItem it = item_at(t);
+            const int end = item_end(it), rows = it.n * a.group - it.block * ROWS;
+            const bool two = wide(it);
+            for (int r = tid >> 1; r < (two ? ROWS : 128); r += MOE_TTC_SOFT * 16) {  // the queries: a row a pair of threads
+                const bool live = r < rows;
+                const int rr = it.block * ROWS + (live ? r : 0);
+                uint32_t q[32];
+                const float c = tree_row<64, 2>(a, live, it.first + rr / a.group, it.head * a.group + rr % a.group,
+                                                (tid & 1) * 64, q);
+                if ((tid & 1) == 0)
+                    mul[r] = c;
+                uint8_t *p = sq + ((r >> 7) * 2 + (tid & 1)) * T::PANEL + (r & 127) * 128;
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    *reinterpret_cast<uint4 *>(p + ((c ^ (r & 7)) << 4)) =
-                        make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<uint4 *>(p + ((k ^ (r & 7)) << 4)) =
+                        make_uint4(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]);
             }
             fence_proxy_async_smem();
             soft_sync();
             if (lane == 0)
                 mbar_arrive(q_full);
-            float sum[CPT];
-#pragma unroll
-            for (int i = 0; i < CPT; ++i)
-                sum[i] = 0.0f;
-            const int prefix = it.len - it.n, t0 = t;
-            for (; lo + t < end; ++t) {
-                ok = ok && wait(s_full + (t & 1), (uint32_t)(t >> 1) & 1u);
-                if (soft_any(!ok)) {
+            const int local = two ? x * 128 + row : row, at = it.block * ROWS + local;  // this thread's row
+            const bool live = local < rows;
+            const int node = live ? at / a.group : 0;
+            const float c = mul[local];
+            // the drafted tokens that it sees
+            const unsigned long long mask = !live ? 0 : (a.mask ? a.mask[it.first + node] : (2ull << node) - 1) &
+                                                         (it.n < 64 ? (1ull << it.n) - 1 : ~0ull);
+            const int prefix = it.len - it.n;
+            float m = -INFINITY, l = 0.0f;
+            bool fresh = true;
+            for (int u = t + (two ? 0 : x); u < end; u += two ? 1 : 2) {
+                ok = ok && wait(s_full + x, jobs++);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const int first = (int)(lo + t - it.lo) * MOE_TTC_TOKENS, j = first + row;  // this lane's token
-                const uint32_t out = *reinterpret_cast<volatile uint32_t *>(gone + (t & 7));
+                const int first = (int)(lo + u - it.lo) * MOE_TTC_TOKENS;
+                const uint32_t out = *reinterpret_cast<volatile uint32_t *>(gone + (u & 7));
                 const bool masked = first + MOE_TTC_TOKENS > prefix || out;
-                const bool in = j < it.len && !(out >> (row >> 4) & 1);
-                auto scores = [&](int c, float (&s)[16]) {
-                    tmem_ld16(lanes + (t & 1) * N + c0 + c, s);
-                    if (masked)
+                auto scores = [&](int k, float (&s)[32]) {
+                    tmem_ld32(s_at + k, s);
+                    if (masked) {  // bit i: token first + k + i is seen
+                        const int off = prefix - (first + k);
+                        uint32_t vis = off >= 32  ? 0xFFFFFFFFu
+                                       : off >= 0 ? ((1u << off) - 1) | (uint32_t)(mask << off)
+                                       : off > -64 ? (uint32_t)(mask >> -off) : 0u;
+                        vis &= (out >> (k / 16) & 1 ? 0u : 0xFFFFu) | (out >> (k / 16 + 1) & 1 ? 0u : 0xFFFF0000u);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (!in || (j >= prefix && !(masks[c0 + c + i] >> (j - prefix) & 1)))
-                                s[i] = -INFINITY;
+                        for (int i = 0; i < 32; ++i)
+                            s[i] = vis >> i & 1 ? s[i] : -INFINITY;
+                    }
                 };
-                // does a score pass its reference? (no reference yet: every finite one)
-                bool up = t == t0;
-                if (!up) {
+                float top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < CPT; c += 16) {
-                        float s[16];
-                        scores(c, s);
+                for (int k = 0; k < 128; k += 32) {
+                    float s[32];
+                    scores(k, s);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 m = mul[c0 + c + i];
-                            up |= fmaf(s[i], m.x, m.y) > MOE_TREE_LIFT + MOE_TREE_SLACK;
-                        }
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        top = fmaxf(top, s[i]);
                 }
-                if (soft_any(up)) {
+                top *= c;
+                const bool moves = top > m + MOE_TREE_SLACK;
+                if (__any_sync(0xFFFFFFFFu, moves)) {
+                    const float f = moves ? ex2(m - top) : 1.0f;
+                    m = moves ? top : m;
+                    l *= f;
+                    if (!fresh) {  // S is there, so the last tile's O is too
 #pragma unroll
-                    for (int c = 0; c < CPT; c += 16) {
-                        float s[16];
-                        scores(c, s);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float v = warp_max(fmaxf(s[i], -INFINITY) * mul[c0 + c + i].x);
-                            if (lane == 0)
-                                qmax[quarter * N + c0 + c + i] = v;
-                        }
-                    }
-                    soft_sync();
-                    for (int r = tid; r < N; r += MOE_TTC_SOFT * 32) {
-                        const float v = fmaxf(fmaxf(qmax[r], qmax[N + r]), fmaxf(qmax[2 * N + r], qmax[3 * N + r]));
-                        const float m = ref[r], to = v > m + MOE_TREE_SLACK ? v : m;
-                        factor[r] = to == m ? 1.0f : ex2(m - to);
-                        ref[r] = to;
-                        mul[r].y = to == -INFINITY ? MOE_TTC_NONE : MOE_TREE_LIFT - to;
-                    }
-                    soft_sync();
-#pragma unroll
-                    for (int i = 0; i < CPT; ++i)
-                        sum[i] *= factor[c0 + i];
-                    if (t > t0) {  // O, once the last tile's product is in
-                        ok = ok && wait(pv_done, (uint32_t)(t - 1) & 1u);
-                        __syncwarp();
-                        tc_fence_after();
-#pragma unroll
-                        for (int c = 0; c < CPT; c += 16) {
+                        for (int k = 0; k < 128; k += 16) {
                             float o[16];
                             uint32_t w[16];
-                            tmem_ld16(lanes + 2 * N + c0 + c, o);
+                            tmem_ld16(o_at + k, o);
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                w[i] = __float_as_uint(o[i] * factor[c0 + c + i]);
-                            tmem_st16(lanes + 2 * N + c0 + c, w);
+                                w[i] = __float_as_uint(o[i] * f);
+                            tmem_st16(o_at + k, w);
                         }
-                        tmem_st_wait();
                     }
                 }
-                if (t > 0 && ok)  // P has been read
-                    ok = wait(pv_done, (uint32_t)(t - 1) & 1u);
-                __syncwarp();
+                const float off = m == -INFINITY ? 0.0f : MOE_TREE_LIFT - m;
+                const F2 c2(c, c), off2(off, off);
+                F2 sum(0.0f, 0.0f);
 #pragma unroll
-                for (int c = 0; c < CPT; c += 16) {
-                    float s[16];
-                    scores(c, s);
-                    uint32_t w[8];
+                for (int k = 0; k < 128; k += 32) {
+                    float s[32];
+                    scores(k, s);
+                    uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float4 m = *reinterpret_cast<const float4 *>(mul + c0 + c + i);
-                        const float e0 = ex2(fmaf(s[i], m.x, m.y)), e1 = ex2(fmaf(s[i + 1], m.z, m.w));
-                        sum[c + i] += e0;
-                        sum[c + i + 1] += e1;
+                    for (int i = 0; i < 32; i += 2) {
+                        float e0, e1;
+                        fma2(F2(s[i], s[i + 1]), c2, off2).get(e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        sum = add2(sum, F2(e0, e1));
                         w[i / 2] = pack_h2(e0, e1);
                     }
-                    const int col = c0 + c;
-                    uint8_t *p = sp + (col >> 6) * T::PANEL + row * 128;
-                    const int k = (col & 63) >> 3;
-                    *reinterpret_cast<uint4 *>(p + ((k ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4 *>(p + (((k + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+                    tmem_st16(s_at + k / 2, w);
                 }
-                fence_proxy_async_smem();
+                float s0, s1;
+                sum.get(s0, s1);
+                l += s0 + s1;
+                fresh = false;
+                tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(p_full);
+                    mbar_arrive(p_full + x);
             }
-            if (soft_any(!ok)) {
-                ok = false;
-                break;
-            }
-            // ---- the rows' sums over the lanes and quarters
+            // ---- the item's end: all its products are in
+            ok = ok && wait(o_done, items++);
+            __syncwarp();
+            tc_fence_after();
+            // piece k of row `row` of the second group's O, in the queries' place
+            auto spot = [&](int k) { return reinterpret_cast<float4 *>(sq + row * 512 + ((k ^ (row & 31)) << 4)); };
+            if (!two && x == 1) {
+                ref2[row] = m;
+                sum2[row] = l;
+                if (!fresh)
 #pragma unroll
-            for (int i = 0; i < CPT; ++i) {
-                const float v = warp_sum(sum[i]);
-                if (lane == 0)
-                    qsum[quarter * N + c0 + i] = v;
+                    for (int k = 0; k < 128; k += 16) {
+                        float o[16];
+                        tmem_ld16(o_at + k, o);
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            *spot((k + i) / 4) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    }
             }
             soft_sync();
-            for (int r = tid; r < N; r += MOE_TTC_SOFT * 32)
-                factor[r] = (qsum[r] + qsum[N + r]) + (qsum[2 * N + r] + qsum[3 * N + r]);
-            ok = wait(pv_done, (uint32_t)(t - 1) & 1u);
-            if (soft_any(!ok)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const long long item_end = it.lo + it.units;
-            const bool whole = u == it.lo && end == item_end;
-            float *part = a.part + ((size_t)blockIdx.x * 2 + (u == lo ? 0 : 1)) * T::PART;
+            const bool whole = lo + t == it.lo && lo + end == it.lo + it.units;
+            if (two || x == 0) {
+                const bool join = !two && end - t > 1;
+                float f0 = 1.0f, f1 = 0.0f;
+                if (join) {
+                    const float m1 = ref2[row], up = fmaxf(m, m1);
+                    f0 = m == -INFINITY ? 1.0f : ex2(m - up);  // sums of NaN stay
+                    f1 = m1 == -INFINITY ? 1.0f : ex2(m1 - up);
+                    l = l * f0 + sum2[row] * f1;
+                    m = up;
+                }
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                float *part = a.part + ((size_t)blockIdx.x * 2 + (t == 0 ? 0 : 1)) * ROWS * (D + 2);
+                uint16_t *to = a.out + (it.first + node) * a.o_tok + (it.head * a.group + (live ? at % a.group : 0)) * a.o_head;
 #pragma unroll
-            for (int c = 0; c < CPT; c += 16) {
-                float o[16];
-                tmem_ld16(lanes + 2 * N + c0 + c, o);
+                for (int k = 0; k < 128; k += 16) {
+                    float o[16];
+                    tmem_ld16(o_at + k, o);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int r = c0 + c + i;
-                    if (!whole)
-                        part[r * D + row] = o[i];
-                    else if (rowat[r] >= 0)
-                        a.out[rowat[r] + row] = __bfloat16_as_ushort(
-                            __float2bfloat16_rn(factor[r] == 0.0f ? 0.0f : o[i] / factor[r]));
-                }
-            }
-            tc_fence_before();
-            if (!whole) {
-                for (int r = tid; r < N; r += MOE_TTC_SOFT * 32) {
-                    part[N * D + r] = ref[r];
-                    part[N * D + N + r] = factor[r];
-                }
-                __threadfence();
-                soft_sync();
-                const int p0 = (int)(it.lo / run), p1 = (int)((item_end - 1) / run);  // the item's runs
-                if (tid == 0) {
-                    const bool end_of_it = atom_add_acq_rel_gpu(a.count + p0, 1) == (unsigned)(p1 - p0);
-                    if (end_of_it)
-                        st_relaxed_gpu(a.count + p0, 0);
-                    *last = end_of_it;
-                }
-                soft_sync();
-                if (*reinterpret_cast<volatile int *>(last)) {  // join the parts in the order of the runs
-                    __threadfence();
-                    auto slot = [&](int cta) { return a.part + ((size_t)cta * 2 + (it.lo <= cta * run ? 0 : 1)) * T::PART; };
-                    for (int r = c0; r < c0 + CPT; ++r) {
-                        if (rowat[r] < 0)
-                            continue;
-                        float m = -INFINITY, l = 0.0f, o = 0.0f;
-                        for (int cta = p0; cta <= p1; ++cta)
-                            m = fmaxf(m, __ldcg(slot(cta) + N * D + r));
-                        for (int cta = p0; cta <= p1; ++cta) {
-                            const float *src = slot(cta);
-                            const float v = __ldcg(src + N * D + r), f = v == -INFINITY ? 1.0f : ex2(v - m);
-                            l = fmaf(__ldcg(src + N * D + N + r), f, l);
-                            o = fmaf(__ldcg(src + r * D + row), f, o);
+                    for (int i = 0; i < 16; i += 4) {
+                        if (join) {
+                            const float4 v = *spot((k + i) / 4);
+                            o[i] = fmaf(v.x, f1, o[i] * f0);
+                            o[i + 1] = fmaf(v.y, f1, o[i + 1] * f0);
+                            o[i + 2] = fmaf(v.z, f1, o[i + 2] * f0);
+                            o[i + 3] = fmaf(v.w, f1, o[i + 3] * f0);
                         }
-                        a.out[rowat[r] + row] = __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.0f ? 0.0f : o / l));
+                        if (live && !whole)
+                            *reinterpret_cast<float4 *>(part + local * D + k + i) =
+                                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    }
+                    if (live && whole) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(o[i] * inv, o[i + 1] * inv);
+                            w[i / 2] = *reinterpret_cast<const uint32_t *>(&v);
+                        }
+                        if (a.o_wide) {
+                            *reinterpret_cast<uint4 *>(to + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4 *>(to + k + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                to[k + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+                        }
                     }
                 }
+                if (live && !whole) {
+                    part[ROWS * D + local] = m;
+                    part[ROWS * D + ROWS + local] = l;
+                }
             }
-            soft_sync();  // factor, rowat and the queries' arrays are free
+            if (end == tiles && tid == 0)
+                tree_cut(a, it, lo, run);
+            tc_fence_before();
+            soft_sync();  // the queries' place and the small arrays are free
+            t = end;
         }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 0)
-        tmem_dealloc(tmem, T::COLS);
+        tmem_dealloc(tmem, 512);
 }
 
 }  // namespace moe

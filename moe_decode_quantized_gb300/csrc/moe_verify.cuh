@@ -111,23 +111,6 @@ __device__ __forceinline__ void st_cluster(const void *p, uint32_t rank, uint32_
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
-// two f32 operations at once
-struct F2 {
-    unsigned long long v;
-    __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
-    __device__ __forceinline__ void get(float &x, float &y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
-};
-__device__ __forceinline__ F2 add2(F2 x, const F2 &y)
-{
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x.v) : "l"(x.v), "l"(y.v));
-    return x;
-}
-__device__ __forceinline__ F2 mul2(F2 x, const F2 &y)
-{
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x.v) : "l"(x.v), "l"(y.v));
-    return x;
-}
-
 // A thread's view of [lo, hi) of rows of vocab values, eight values at a time
 // (a step of the CTA is 8 NT): where rows can be read 16 bytes at a time
 // (WIDE) eight consecutive ones, else every NT-th. F32: logits' type. FULL:
