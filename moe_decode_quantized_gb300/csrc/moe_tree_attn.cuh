@@ -274,23 +274,26 @@ __device__ __forceinline__ void tree_cut(const TreeArgs &a, const TreeItem &it, 
 
 #define MOE_TREE_JOIN_ROWS 16
 #define MOE_TREE_JOIN_THREADS 256
+#define MOE_TREE_JOIN_PARTS 64  // whose weights are held at once
 
 // Joins the partials of cut items: CTA (run, 16 rows of the row block). Bound
-// by latency: a round of loads for the weights, then one for each few parts.
+// by latency: a round of loads for the weights, then one for every four parts.
 template <int D>
 __global__ void __launch_bounds__(MOE_TREE_JOIN_THREADS) moe_tree_join_kernel(const __grid_constant__ TreeArgs a, const int rows)
 {
-    constexpr int NT = MOE_TREE_JOIN_THREADS, PER = MOE_TREE_JOIN_ROWS * D / NT, STEP = NT / D > 0 ? NT / D : 1;
-    __shared__ float top[MOE_TREE_JOIN_ROWS], sum[MOE_TREE_JOIN_ROWS];
+    constexpr int NT = MOE_TREE_JOIN_THREADS, R = MOE_TREE_JOIN_ROWS, P = MOE_TREE_JOIN_PARTS;
+    constexpr int COLS = D / 4, STEP = NT / COLS, PER = R / STEP;  // a thread: four dimensions of PER rows
+    __shared__ float weight[P][R], top[R], sum[R];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const size_t size = (size_t)rows * (D + 2);
     pdl_wait();
     const TreeCut c = a.cuts[blockIdx.x];
-    const int r0 = blockIdx.y * MOE_TREE_JOIN_ROWS, live = min(MOE_TREE_JOIN_ROWS, c.n * a.group - c.block * rows - r0);
+    const int r0 = blockIdx.y * R, live = min(R, c.n * a.group - c.block * rows - r0);
     if (c.runs == 0 || live <= 0)
         return;
     // part i: of the first run the second slot, unless the item begins with the run
-    auto part = [&](int i) { return a.part + ((size_t)(blockIdx.x + i) * 2 + (i == 0 && !c.whole_run ? 1 : 0)) * size; };
+    const size_t size = (size_t)rows * (D + 2);
+    const float *base = a.part + (size_t)blockIdx.x * 2 * size;
+    auto part = [&](int i) { return base + (i == 0 && !c.whole_run ? size : 2 * i * size); };
     for (int r = warp; r < live; r += NT / 32) {
         float m = -INFINITY, l = 0.0f;
         for (int i = lane; i <= c.runs; i += 32)
@@ -299,8 +302,10 @@ __global__ void __launch_bounds__(MOE_TREE_JOIN_THREADS) moe_tree_join_kernel(co
         for (int x = 16; x; x /= 2)
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
         for (int i = lane; i <= c.runs; i += 32) {
-            const float v = part(i)[rows * D + r0 + r];
-            l += part(i)[rows * (D + 1) + r0 + r] * (v == -INFINITY ? 1.0f : ex2(v - m));  // a NaN sum stays
+            const float v = part(i)[rows * D + r0 + r], f = v == -INFINITY ? 1.0f : ex2(v - m);  // a NaN sum stays
+            l += part(i)[rows * (D + 1) + r0 + r] * f;
+            if (i < P)
+                weight[i][r] = f;
         }
         l = warp_sum(l);
         if (lane == 0) {
@@ -309,29 +314,57 @@ __global__ void __launch_bounds__(MOE_TREE_JOIN_THREADS) moe_tree_join_kernel(co
         }
     }
     __syncthreads();
-    float o[PER];
+    float4 o[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k)
-        o[k] = 0.0f;
-    const int d = tid % D, r1 = tid / D;  // rows r1, r1 + STEP, ..
-#pragma unroll 2
-    for (int i = 0; i <= c.runs; ++i) {
-        const float *p = part(i) + r0 * D;
+        o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int d = tid % COLS * 4, r1 = tid / COLS;  // rows r1, r1 + STEP, ..
+    for (int p0 = 0; p0 <= c.runs; p0 += P) {
+        const int n = min(P, c.runs + 1 - p0);
+        if (p0 > 0) {  // the next weights
+            __syncthreads();
+            for (int x = tid; x < n * R; x += NT)
+                if (x % R < live) {
+                    const float v = part(p0 + x / R)[rows * D + r0 + x % R];
+                    weight[x / R][x % R] = v == -INFINITY ? 1.0f : ex2(v - top[x % R]);
+                }
+            __syncthreads();
+        }
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float *src = part(p0 + i) + r0 * D + d;
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            const int r = r1 + k * STEP;
-            if (r < live) {
-                const float v = part(i)[rows * D + r0 + r];
-                o[k] = fmaf(p[r * D + d], v == -INFINITY ? 1.0f : ex2(v - top[r]), o[k]);
+            for (int k = 0; k < PER; ++k) {
+                const int r = r1 + k * STEP;
+                if (r < live) {
+                    const float4 v = *reinterpret_cast<const float4 *>(src + r * D);
+                    const float f = weight[i][r];
+                    o[k].x = fmaf(v.x, f, o[k].x);
+                    o[k].y = fmaf(v.y, f, o[k].y);
+                    o[k].z = fmaf(v.z, f, o[k].z);
+                    o[k].w = fmaf(v.w, f, o[k].w);
+                }
             }
         }
     }
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int r = r1 + k * STEP, rr = c.block * rows + r0 + r;
-        if (r < live)
-            a.out[(c.first + rr / a.group) * a.o_tok + (c.head * a.group + rr % a.group) * a.o_head + d] =
-                __bfloat16_as_ushort(__float2bfloat16_rn(sum[r] == 0.0f ? 0.0f : o[k] / sum[r]));
+        if (r >= live)
+            continue;
+        const float inv = sum[r] == 0.0f ? 0.0f : 1.0f / sum[r];
+        uint16_t *to = a.out + (c.first + rr / a.group) * a.o_tok + (c.head * a.group + rr % a.group) * a.o_head + d;
+        const __nv_bfloat162 x = __floats2bfloat162_rn(o[k].x * inv, o[k].y * inv);
+        const __nv_bfloat162 y = __floats2bfloat162_rn(o[k].z * inv, o[k].w * inv);
+        const uint32_t w0 = *reinterpret_cast<const uint32_t *>(&x), w1 = *reinterpret_cast<const uint32_t *>(&y);
+        if (a.o_wide) {
+            *reinterpret_cast<uint2 *>(to) = make_uint2(w0, w1);
+        } else {
+            to[0] = (uint16_t)w0;
+            to[1] = (uint16_t)(w0 >> 16);
+            to[2] = (uint16_t)w1;
+            to[3] = (uint16_t)(w1 >> 16);
+        }
     }
 }
 

@@ -404,7 +404,8 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 mbar_arrive(v_full);
         }
     } else {
-        // ---------------- softmax: group x, row `row` of its M tile
+        // ---------------- softmax: group x, row `row` of its M tile. Loops over columns stay loops: the four roles
+        // share the instruction cache.
         const int x = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t s_at = lanes + S_COL + x * 128, o_at = lanes + O_COL + x * 128;
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                     }
                 };
                 float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 128; k += 32) {
                     float s[32];
                     scores(k, s);
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                     m = moves ? top : m;
                     l *= f;
                     if (!fresh) {  // S is there, so the last tile's O is too
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < 128; k += 16) {
                             float o[16];
                             uint32_t w[16];
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 const float off = m == -INFINITY ? 0.0f : MOE_TREE_LIFT - m;
                 const F2 c2(c, c), off2(off, off);
                 F2 sum(0.0f, 0.0f);
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 128; k += 32) {
                     float s[32];
                     scores(k, s);
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 ref2[row] = m;
                 sum2[row] = l;
                 if (!fresh)
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < 128; k += 16) {
                         float o[16];
                         tmem_ld16(o_at + k, o);
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 float *part = a.part + ((size_t)blockIdx.x * 2 + (t == 0 ? 0 : 1)) * ROWS * (D + 2);
                 uint16_t *to = a.out + (it.first + node) * a.o_tok + (it.head * a.group + (live ? at % a.group : 0)) * a.o_head;
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 128; k += 16) {
                     float o[16];
                     tmem_ld16(o_at + k, o);
