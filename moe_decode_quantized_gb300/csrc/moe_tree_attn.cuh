@@ -101,6 +101,39 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) { return h2(__floa
 __device__ __forceinline__ uint32_t dup_lo(uint32_t v) { return __byte_perm(v, v, 0x1010); }
 __device__ __forceinline__ uint32_t dup_hi(uint32_t v) { return __byte_perm(v, v, 0x3232); }
 
+// mbar_wait for waits that are short and many: each poll lets the hardware
+// hold the warp until the phase completes (10 us at most), so that waiting
+// warps leave the issue slots to those that work; the clock that bounds the
+// wait is read only after the first poll that fails; what follows the first
+// poll is out of line.
+__device__ __forceinline__ bool tree_poll(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __noinline__ bool tree_wait_on(uint64_t *bar, uint32_t parity, uint32_t *status, unsigned long long wait_ns)
+{
+    const uint64_t t0 = globaltimer();
+    do {
+        if (tree_poll(bar, parity))
+            return true;
+    } while (globaltimer() - t0 <= wait_ns);
+    atomicOr(status, (uint32_t)MOE_WS_TIMEOUT);
+    return false;
+}
+
+__device__ __forceinline__ bool tree_wait(uint64_t *bar, uint32_t parity, uint32_t *status, unsigned long long wait_ns)
+{
+    return tree_poll(bar, parity) || tree_wait_on(bar, parity, status, wait_ns);
+}
+
 // two code bytes (bytes i and j of w) as f16: 0x6400 | u is 1024 + u, less
 // 1024 + 128 the code, exactly; times the scale, rounded once
 __device__ __forceinline__ uint32_t q8_pair(uint32_t w, uint32_t sel, __half2 d)
@@ -164,6 +197,26 @@ __device__ __forceinline__ TreeItem tree_item(const TreeArgs &a, const long long
     it.block = at % blocks;
     it.lo = cum[x] + (long long)at * it.units;
     return it;
+}
+
+// the item after `it` in the list (there is one)
+template <int ROWS, int TOKENS>
+__device__ __forceinline__ void tree_next(const TreeArgs &a, const long long *cum, TreeItem &it)
+{
+    it.lo += it.units;
+    if (++it.block < tree_blocks<ROWS>(it.n, a.group))
+        return;
+    it.block = 0;
+    if (++it.head < a.k.heads)
+        return;
+    it.head = 0;
+    do
+        ++it.b;
+    while (it.b + 1 < a.batch && cum[it.b + 1] == it.lo);  // sequences without units
+    it.first = a.q_start[it.b];
+    it.n = a.q_start[it.b + 1] - it.first;
+    it.len = a.kv_len[it.b];
+    it.units = (it.len + TOKENS - 1) / TOKENS;
 }
 
 // zeros for the query rows of a sequence that does not hold
@@ -528,7 +581,7 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
         int first = (int)(lo + warp + (long long)done * MOE_TREE_WARPS - it.lo) * 16;
         for (; done < last; ++done, first += 16 * MOE_TREE_WARPS) {
             if (ok)
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar + stage, phase, a.ctrl + MOE_CTRL_STATUS, a.wait_ns));
+                ok = __all_sync(0xFFFFFFFFu, tree_wait(bar + stage, phase, a.ctrl + MOE_CTRL_STATUS, a.wait_ns));
             const uint8_t *blk = ring + stage * T::BLOCK;
             const bool gone = (done >= batch ? bad >> (done - batch) : bad_before >> (done - batch + 32)) & 1;
             const bool masked = gone || first + 16 > prefix;

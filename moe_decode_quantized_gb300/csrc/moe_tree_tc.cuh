@@ -15,9 +15,10 @@
 //    own maximum, sum and O, and are joined at the item's end.
 // A reference m moves only when a score passes it by 2^8 (O is then scaled).
 //
-// One CTA an SM: a warp copies the cache's blocks, eight turn codes into f16
-// tiles (K of the next tile while this one's softmax runs, V once the last
-// tile's second product is done), one thread issues the products.
+// One CTA an SM: a warp copies the cache's blocks, eight bring the queries and
+// turn codes into f16 tiles (K of tile t + 1 while tile t's softmax runs, then
+// V of tile t once the second product of tile t - 1 is done), one thread
+// issues the products.
 #pragma once
 #include "moe_tc.cuh"
 #include "moe_tree_attn.cuh"
@@ -41,8 +42,8 @@ struct TtcShape {
     static constexpr int PANEL = MOE_TTC_TOKENS * 128;     // 64 dimensions of 128 tokens (rows)
     static constexpr int K_AT = 0, V_AT = 2 * PANEL, Q_AT = 4 * PANEL;  // Q: [M tile][2 panels]
     static constexpr int RAW_AT = Q_AT + 4 * PANEL;
-    // after the raw stages: barriers, rows' multipliers, the second group's references and sums, the scan and the list
-    static constexpr int SMALL = 256 + 4 * 256 + 2 * 4 * 128 + 32 * 8;
+    // after the raw stages: barriers, rows' multipliers, the groups' references and sums, the scan and the list
+    static constexpr int SMALL = 256 + 4 * 4 * 256 + 4 * 128 * 8 + 32 * 8;
 };
 
 // descriptor of a tile whose M (N) side is contiguous: 128-byte rows of 64
@@ -54,6 +55,18 @@ __device__ __forceinline__ uint64_t mn_desc(const void *tile)
     return ((addr >> 4) & 0x3FFFull) | ((uint64_t)(MOE_TTC_TOKENS * 128 / 16) << 16) | ((1024ull >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
 }
+
+// a place in a ring and its phase, without a division
+struct TtcRing {
+    int slot = 0, phase = 0;
+    __device__ __forceinline__ void next(int n)
+    {
+        if (++slot == n) {
+            slot = 0;
+            ++phase;
+        }
+    }
+};
 
 // the softmax warps' own barrier
 __device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(MOE_TTC_SOFT * 32) : "memory"); }
@@ -99,13 +112,14 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
     uint8_t *sk = smem + T::K_AT, *sv = smem + T::V_AT, *sq = smem + T::Q_AT;
     uint8_t *raw = smem + T::RAW_AT, *small = raw + (size_t)stages * T::STAGE;
     uint64_t *bars = reinterpret_cast<uint64_t *>(small);
-    uint64_t *raw_full = bars, *raw_free = bars + 4, *k_full = bars + 8, *v_full = bars + 9, *k_done = bars + 10,
-             *v_done = bars + 11, *q_full = bars + 12, *s_full = bars + 13, *p_full = bars + 15, *o_done = bars + 17;  // s_full, p_full [2]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
+    uint64_t *raw_full = bars, *raw_free = bars + 4, *q_full = bars + 8;  // [4] each; q_full of item i at i % 4
+    uint64_t *k_full = bars + 12, *v_full = bars + 13, *k_done = bars + 14, *v_done = bars + 15, *o_done = bars + 16,
+             *o_free = bars + 17, *s_full = bars + 18, *p_full = bars + 20;  // s_full, p_full [2]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 22);
     uint32_t *gone = tmem_slot + 1;  // [8] blocks of tile t that are not there, at t % 8: kept longer than its stage
-    float *mul = reinterpret_cast<float *>(small + 256);  // [256] rows' multipliers
-    float *ref2 = mul + 256, *sum2 = ref2 + 128;          // the second group's
-    long long *scan = reinterpret_cast<long long *>(sum2 + 128), *cum = scan + 32;  // cum [batch + 1]
+    float *mul = reinterpret_cast<float *>(small + 256);  // [4][256] multipliers of the rows of item i, at i % 4
+    float2 *stat = reinterpret_cast<float2 *>(mul + 1024);  // [2][2][128] (reference, sum) of item i, at i % 2, by group
+    long long *scan = reinterpret_cast<long long *>(stat + 512), *cum = scan + 32;  // cum [batch + 1]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t *status = a.ctrl + MOE_CTRL_STATUS;
 
@@ -118,8 +132,10 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
         mbar_init(v_full, MOE_TTC_CODE);
         mbar_init(k_done, 1);
         mbar_init(v_done, 1);
-        mbar_init(q_full, MOE_TTC_SOFT);
+        for (int i = 0; i < 4; ++i)
+            mbar_init(q_full + i, MOE_TTC_CODE);
         mbar_init(o_done, 1);
+        mbar_init(o_free, MOE_TTC_SOFT);
         for (int x = 0; x < 2; ++x) {
             mbar_init(s_full + x, 1);
             mbar_init(p_full + x, MOE_TTC_SOFT / 2);
@@ -174,8 +190,16 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
     pdl_launch_dependents();
     if (tiles == 0 && tid == 0)
         a.cuts[blockIdx.x].runs = 0;
-    auto wait = [&](uint64_t *bar, int phase) { return mbar_wait(bar, (uint32_t)phase & 1u, status, a.wait_ns); };
-    auto item_at = [&](int t) { return tree_item<ROWS, MOE_TTC_TOKENS>(a, cum, lo + t); };
+    auto wait = [&](uint64_t *bar, int phase) {
+        return tree_wait(bar, (uint32_t)phase & 1u, status, a.wait_ns);
+    };
+    // to the item that begins at tile t of this run (t = 0: the one it is in)
+    auto to_item = [&](int t, TreeItem &it) {
+        if (t == 0)
+            it = tree_item<ROWS, MOE_TTC_TOKENS>(a, cum, lo);
+        else
+            tree_next<ROWS, MOE_TTC_TOKENS>(a, cum, it);
+    };
     // the item's tiles of this run end before tile:
     auto item_end = [&](const TreeItem &it) { return (int)(min(hi, it.lo + it.units) - lo); };
     auto wide = [&](const TreeItem &it) { return it.n * a.group - it.block * ROWS > 128; };  // a group an M tile
@@ -186,9 +210,10 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
         bool ok = true;
         int t = 0, end = 0;
         TreeItem it{};
-        for (; t < tiles; ++t) {
+        TtcRing ring;
+        for (; t < tiles; ++t, ring.next(stages)) {
             if (t == end) {
-                it = item_at(t);
+                to_item(t, it);
                 end = item_end(it);
             }
             const int blk = (int)(lo + t - it.lo) * 8 + lane, per_page = a.k.page / 16;
@@ -201,9 +226,9 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                     src = a.pages + (((size_t)page * a.k.heads + it.head) * per_page + blk % per_page) * T::BLOCK;
             }
             const uint32_t got = __ballot_sync(0xFFFFFFFFu, src != nullptr);
-            const int s = t % stages;
+            const int s = ring.slot;
             if (t >= stages)
-                ok = __all_sync(0xFFFFFFFFu, wait(raw_free + s, t / stages - 1));
+                ok = __all_sync(0xFFFFFFFFu, wait(raw_free + s, ring.phase - 1));
             if (!ok)
                 break;
             if (lane == 0) {
@@ -223,48 +248,62 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
             const uint64_t kd = sw128_desc(sk), vd = mn_desc(sv);
             bool ok = true;
             // by group, a bit each: parity of the products S begun; whether O of the last is still to come; whether
-            // that is the item's first
-            uint32_t jobs = 0, open = 0, fresh = 0;
-            int open_tile = -1, begin = 0, end = 0, items = 0;
-            bool two = false;
+            // that is the group's first of its item; whether the item has had one
+            uint32_t jobs = 0, open = 0, fresh = 0, begun = 0;
+            int open_tile = -1, end = 0, item = -1, of[2];  // of: the item of a group's last S
+            bool two = false, closing = false;              // closing: the open tile is its item's last
+            TreeItem it{};
             auto first = [&](int x, int m) {  // S of group x from M tile m
                 const uint64_t qd = sw128_desc(sq + m * 2 * T::PANEL);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)  // 16 dimensions: 32 bytes, then the next panel
-                    mma_f16(tmem + S_COL + x * 128, qd + (k / 4) * (T::PANEL / 16) + (k % 4) * 2,
-                            kd + (k / 4) * (T::PANEL / 16) + (k % 4) * 2, id_s, k > 0);
+                for (int k = 0; k < 8; ++k) {  // 16 dimensions: 32 bytes, then the next panel
+                    const int off = (k >> 2) * (T::PANEL / 16) + (k & 3) * 2;
+                    mma_f16(tmem + S_COL + x * 128, qd + off, kd + off, id_s, k > 0);
+                }
                 mma_commit(s_full + x);
                 jobs ^= 1u << x;
                 open |= 1u << x;
+                fresh = (fresh & ~(1u << x)) | (~begun & 1u << x);
+                begun |= 1u << x;
+                (x ? of[1] : of[0]) = item;
             };
             auto second = [&](int x) {  // O of group x += P V of the open tile
                 if (!(open >> x & 1) || !ok)
                     return;
-                ok = wait(v_full, open_tile) && wait(p_full + x, (int)(jobs >> x & 1) - 1);
+                const bool begins = fresh >> x & 1;
+                const int i = x ? of[1] : of[0];
+                ok = wait(v_full, open_tile) && wait(p_full + x, (int)(jobs >> x & 1) - 1) &&
+                     (!begins || i == 0 || wait(o_free, i - 1));  // the last item's O has been read
                 if (!ok)
                     return;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < 8; ++k)  // 16 tokens: 8 columns of P, 2048 bytes of V
-                    mma_f16_ts(tmem + O_COL + x * 128, tmem + S_COL + x * 128 + k * 8, vd + k * 128, id_o, !(fresh >> x & 1) || k > 0);
-                fresh &= ~(1u << x);
+                    mma_f16_ts(tmem + O_COL + x * 128, tmem + S_COL + x * 128 + k * 8, vd + k * 128, id_o, !begins || k > 0);
                 open &= ~(1u << x);
             };
+            auto close = [&]() {  // after the last second product of the open tile
+                mma_commit(v_done);
+                if (closing)
+                    mma_commit(o_done);
+                closing = false;
+                open_tile = -1;
+            };
             for (int t = 0; t < tiles && ok; ++t) {
-                if (t == end) {  // a new item: the softmax warps finish the last before they bring its queries
-                    second(0);
-                    second(1);
-                    if (t > 0) {
-                        mma_commit(v_done);
-                        mma_commit(o_done);
-                    }
-                    open_tile = -1;
-                    begin = t;
-                    const TreeItem it = item_at(t);
+                if (t == end) {
+                    const bool was = two;
+                    to_item(t, it);
                     end = item_end(it);
                     two = wide(it);
-                    fresh = 3;
-                    ok = ok && wait(q_full, items++);
+                    closing = t > 0;
+                    if (t > 0 && (was || two)) {  // both groups are needed (were in use)
+                        second(0);
+                        second(1);
+                        close();
+                    }
+                    ++item;
+                    begun = 0;
+                    ok = ok && wait(q_full + (item & 3), item >> 2);
                 }
                 // two M tiles: O of the last tile frees the S that the next product writes; else the groups' S are
                 // taken in turn, and O of the last tile comes after S of this one
@@ -272,7 +311,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                     for (int x = 0; x < 2; ++x) {
                         second(x);
                         if (x == 1 && open_tile >= 0)
-                            mma_commit(v_done);
+                            close();
                         ok = ok && wait(k_full, t);
                         if (!ok)
                             break;
@@ -285,12 +324,11 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                     if (!ok)
                         break;
                     tc_fence_after();
-                    const int x = (t - begin) & 1;
-                    first(x, 0);
+                    first(t & 1, 0);
                     mma_commit(k_done);
                     if (open_tile >= 0) {
-                        second(x ^ 1);
-                        mma_commit(v_done);
+                        second(t & 1 ^ 1);
+                        close();
                     }
                 }
                 open_tile = t;
@@ -298,9 +336,9 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
             second(0);
             second(1);
             if (tiles > 0 && ok) {
-                mma_commit(v_done);
-                mma_commit(o_done);
-                wait(o_done, items - 1);
+                closing = true;
+                close();
+                wait(o_done, item);
             }
         }
     } else if (warp >= MOE_TTC_SOFT) {
@@ -316,19 +354,49 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                                    v_row + (1 - odd) * 128 + ((((g & 3) * 2) ^ (2 * t4) ^ (1 - odd)) << 4)};
         constexpr int KP = FMT == MOE_KV_Q8 ? 4 : 2;  // 16-byte pieces of a block's K (V) codes a lane
         bool ok = true;
-        int end = 0;
+        TtcRing k_ring, v_ring;
+        int end = 0, item = -1, left = 0;  // left: tokens of the item from this warp's block of the last K tile on
         TreeItem it{};
-        for (int t = 0; t < tiles; ++t) {
-            if (t == end) {
-                it = item_at(t);
+        auto keys = [&](int t) {  // K of tile t, and before an item's first the queries
+            const bool begins = t == end;
+            if (begins) {
+                to_item(t, it);
                 end = item_end(it);
+                ++item;
             }
-            const int s = t % stages, left = it.len - (int)(lo + t - it.lo) * MOE_TTC_TOKENS - w * 16;  // of this block
-            ok = ok && wait(raw_full + s, t / stages);
+            left = it.len - (int)(lo + t - it.lo) * MOE_TTC_TOKENS - w * 16;
+            const int s = k_ring.slot;
+            if (t > 0)  // K and Q have been read
+                ok = ok && wait(k_done, t - 1);
+            if (begins) {
+                const int rows = it.n * a.group - it.block * ROWS;
+                for (int r = (tid >> 1) & 127; r < (rows > 128 ? ROWS : 128); r += 128) {  // a row a pair of threads
+                    const bool live = r < rows;
+                    const int rr = it.block * ROWS + (live ? r : 0);
+                    uint32_t q[32];
+                    const float c = tree_row<64, 2>(a, live, it.first + rr / a.group, it.head * a.group + rr % a.group,
+                                                    (tid & 1) * 64, q);
+                    if ((tid & 1) == 0)
+                        mul[(item & 3) * 256 + r] = c;
+                    uint8_t *p = sq + ((r >> 7) * 2 + (tid & 1)) * T::PANEL + (r & 127) * 128;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4 *>(p + ((k ^ (r & 7)) << 4)) =
+                            make_uint4(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(q_full + (item & 3));
+            }
+            ok = ok && wait(raw_full + s, k_ring.phase);
+            k_ring.next(stages);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok)
+                return;
             const uint8_t *b = raw + (size_t)s * T::STAGE + w * T::BLOCK;
             uint4 v[KP];
-            uint32_t sc[4], mn[4];
-            __syncwarp();
+            uint32_t sc[2], mn[2];
 #pragma unroll
             for (int i = 0; i < KP; ++i)
                 v[i] = *reinterpret_cast<const uint4 *>(b + (FMT == MOE_KV_Q8 ? i ^ turn : i) * 512 + lane * 16);
@@ -343,10 +411,6 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                     mn[nb] = dup_hi(dm);
                 }
             }
-            if (t > 0)
-                ok = ok && wait(k_done, t - 1);
-            if (!__all_sync(0xFFFFFFFFu, ok))
-                break;
 #pragma unroll
             for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
@@ -365,12 +429,18 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(k_full);
+        };
+        auto values = [&](int t, int left) {  // V of tile t
+            const int s = v_ring.slot;
+            v_ring.next(stages);
             const bool there = !(*reinterpret_cast<volatile uint32_t *>(gone + (t & 7)) >> w & 1);
-            const uint8_t *vb = b + T::HALF;
-            const __half *p = reinterpret_cast<const __half *>(vb + 16 * T::RB) + (g >> 1) * 16;
+            const uint8_t *b = raw + (size_t)s * T::STAGE + w * T::BLOCK + T::HALF;
+            const __half *p = reinterpret_cast<const __half *>(b + 16 * T::RB) + (g >> 1) * 16;
+            uint4 v[KP];
+            uint32_t sc[4], mn[4];
 #pragma unroll
             for (int i = 0; i < KP; ++i)
-                v[i] = *reinterpret_cast<const uint4 *>(vb + (FMT == MOE_KV_Q8 ? i ^ odd : i) * 512 + lane * 16);
+                v[i] = *reinterpret_cast<const uint4 *>(b + (FMT == MOE_KV_Q8 ? i ^ odd : i) * 512 + lane * 16);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int tok = (i >> 1) * 8 + 2 * t4 + ((i & 1) ^ odd);
@@ -383,9 +453,10 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
             if (lane == 0)  // the stage is in registers
                 mbar_arrive(raw_free + s);
             if (t > 0)
-                ok = wait(v_done, t - 1);
-            if (!__all_sync(0xFFFFFFFFu, ok))
-                break;
+                ok = ok && wait(v_done, t - 1);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok)
+                return;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t h[8];
@@ -402,6 +473,23 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(v_full);
+        };
+        // K of tile t and V of tile t - 1. With two M tiles V first: the second products come before the first ones
+        // of the next tile; else K first: S of the next tile is wanted while the softmax of the last two goes on.
+        bool two = false;
+        for (int t = 0, here = 0; t <= tiles && ok; ++t) {
+            const int last = here;
+            const bool values_first = two;
+#pragma unroll 1
+            for (int step = 0; step < 2; ++step)
+                if ((step == 0) == values_first) {
+                    if (t > 0 && ok)
+                        values(t - 1, last);
+                } else if (t < tiles && ok) {
+                    keys(t);
+                    here = left;
+                    two = wide(it);
+                }
         }
     } else {
         // ---------------- softmax: group x, row `row` of its M tile. Loops over columns stay loops: the four roles
@@ -410,41 +498,25 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t s_at = lanes + S_COL + x * 128, o_at = lanes + O_COL + x * 128;
         bool ok = true;
-        int jobs = 0, items = 0;
-        for (int t = 0; t < tiles;) {
-            // every warp goes through every item's barriers, a failed wait or not
-            const TreeItem it = item_at(t);
+        int jobs = 0, item = 0;
+        TreeItem it{};
+        for (int t = 0; t < tiles; ++item) {
+            // every warp goes through every item's barrier, a failed wait or not
+            to_item(t, it);
             const int end = item_end(it), rows = it.n * a.group - it.block * ROWS;
             const bool two = wide(it);
-            for (int r = tid >> 1; r < (two ? ROWS : 128); r += MOE_TTC_SOFT * 16) {  // the queries: a row a pair of threads
-                const bool live = r < rows;
-                const int rr = it.block * ROWS + (live ? r : 0);
-                uint32_t q[32];
-                const float c = tree_row<64, 2>(a, live, it.first + rr / a.group, it.head * a.group + rr % a.group,
-                                                (tid & 1) * 64, q);
-                if ((tid & 1) == 0)
-                    mul[r] = c;
-                uint8_t *p = sq + ((r >> 7) * 2 + (tid & 1)) * T::PANEL + (r & 127) * 128;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    *reinterpret_cast<uint4 *>(p + ((k ^ (r & 7)) << 4)) =
-                        make_uint4(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]);
-            }
-            fence_proxy_async_smem();
-            soft_sync();
-            if (lane == 0)
-                mbar_arrive(q_full);
             const int local = two ? x * 128 + row : row, at = it.block * ROWS + local;  // this thread's row
             const bool live = local < rows;
             const int node = live ? at / a.group : 0;
-            const float c = mul[local];
             // the drafted tokens that it sees
             const unsigned long long mask = !live ? 0 : (a.mask ? a.mask[it.first + node] : (2ull << node) - 1) &
                                                          (it.n < 64 ? (1ull << it.n) - 1 : ~0ull);
             const int prefix = it.len - it.n;
+            ok = ok && wait(q_full + (item & 3), item >> 2);
+            const float c = mul[(item & 3) * 256 + local];
             float m = -INFINITY, l = 0.0f;
             bool fresh = true;
-            for (int u = t + (two ? 0 : x); u < end; u += two ? 1 : 2) {
+            for (int u = t + (two ? 0 : (t ^ x) & 1); u < end; u += two ? 1 : 2) {
                 ok = ok && wait(s_full + x, jobs++);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
@@ -454,29 +526,38 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 const int first = (int)(lo + u - it.lo) * MOE_TTC_TOKENS;
                 const uint32_t out = *reinterpret_cast<volatile uint32_t *>(gone + (u & 7));
                 const bool masked = first + MOE_TTC_TOKENS > prefix || out;
-                auto scores = [&](int k, float (&s)[32]) {
-                    tmem_ld32(s_at + k, s);
+                // 64 scores from column k: the latency of a load is that of 40 columns' work
+                auto scores = [&](int k, uint32_t (&s)[64]) {
+                    uint32_t(&lo32)[32] = reinterpret_cast<uint32_t(&)[32]>(s[0]);
+                    uint32_t(&hi32)[32] = reinterpret_cast<uint32_t(&)[32]>(s[32]);
+                    tmem_ld32_begin(s_at + k, lo32);
+                    tmem_ld32_begin(s_at + k + 32, hi32);
+                    tmem_ld32_end(lo32);
+                    tmem_ld32_end(hi32);
                     if (masked) {  // bit i: token first + k + i is seen
                         const int off = prefix - (first + k);
-                        uint32_t vis = off >= 32  ? 0xFFFFFFFFu
-                                       : off >= 0 ? ((1u << off) - 1) | (uint32_t)(mask << off)
-                                       : off > -64 ? (uint32_t)(mask >> -off) : 0u;
-                        vis &= (out >> (k / 16) & 1 ? 0u : 0xFFFFu) | (out >> (k / 16 + 1) & 1 ? 0u : 0xFFFF0000u);
+                        unsigned long long vis = off >= 64  ? ~0ull
+                                                 : off >= 0 ? ((1ull << off) - 1) | mask << off
+                                                 : off > -64 ? mask >> -off
+                                                             : 0ull;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            s[i] = vis >> i & 1 ? s[i] : -INFINITY;
+                        for (int i = 0; i < 4; ++i)
+                            vis &= out >> (k / 16 + i) & 1 ? ~(0xFFFFull << (16 * i)) : ~0ull;
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            s[i] = vis >> i & 1 ? s[i] : 0xFF800000u;
                     }
                 };
-                float top = -INFINITY;
+                float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                for (int k = 0; k < 128; k += 32) {
-                    float s[32];
+                for (int k = 0; k < 128; k += 64) {
+                    uint32_t s[64];
                     scores(k, s);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        top = fmaxf(top, s[i]);
+                    for (int i = 0; i < 64; ++i)
+                        top4[i & 3] = fmaxf(top4[i & 3], __uint_as_float(s[i]));
                 }
-                top *= c;
+                const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * c;
                 const bool moves = top > m + MOE_TREE_SLACK;
                 if (__any_sync(0xFFFFFFFFu, moves)) {
                     const float f = moves ? ex2(m - top) : 1.0f;
@@ -497,23 +578,28 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 }
                 const float off = m == -INFINITY ? 0.0f : MOE_TREE_LIFT - m;
                 const F2 c2(c, c), off2(off, off);
-                F2 sum(0.0f, 0.0f);
+                F2 sum(0.0f, 0.0f), sum1(0.0f, 0.0f);
 #pragma unroll 1
-                for (int k = 0; k < 128; k += 32) {
-                    float s[32];
+                for (int k = 0; k < 128; k += 64) {
+                    uint32_t s[64];
                     scores(k, s);
-                    uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float e0, e1;
-                        fma2(F2(s[i], s[i + 1]), c2, off2).get(e0, e1);
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
-                        sum = add2(sum, F2(e0, e1));
-                        w[i / 2] = pack_h2(e0, e1);
+                    for (int h = 0; h < 64; h += 32) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float e0, e1;
+                            fma2(F2(__uint_as_float(s[h + i]), __uint_as_float(s[h + i + 1])), c2, off2).get(e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            F2 &to = i & 2 ? sum1 : sum;
+                            to = add2(to, F2(e0, e1));
+                            w[i / 2] = pack_h2(e0, e1);
+                        }
+                        tmem_st16(s_at + (k + h) / 2, w);  // P over the columns that have been read
                     }
-                    tmem_st16(s_at + k / 2, w);
                 }
+                sum = add2(sum, sum1);
                 float s0, s1;
                 sum.get(s0, s1);
                 l += s0 + s1;
@@ -524,83 +610,80 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 if (lane == 0)
                     mbar_arrive(p_full + x);
             }
-            // ---- the item's end: all its products are in
-            ok = ok && wait(o_done, items++);
+            // ---- the item's end. Two M tiles: each group its rows. Else both have the same rows (a lane of tensor
+            // memory is the same row in either's O), and each writes half of the dimensions of their sum
+            float f0 = 1.0f, f1 = 0.0f;  // factors of this group's O and of the other's
+            if (!two) {
+                float2 *mine = stat + ((item & 1) * 2) * 128 + row;
+                mine[x * 128] = make_float2(m, l);
+                soft_sync();
+                const float2 other = mine[(x ^ 1) * 128];
+                const float up = fmaxf(m, other.x);
+                f0 = m == -INFINITY ? 1.0f : ex2(m - up);  // sums of NaN stay
+                f1 = other.x == -INFINITY ? 1.0f : ex2(other.x - up);
+                l = l * f0 + other.y * f1;
+                m = up;
+            }
+            ok = ok && wait(o_done, item);
             __syncwarp();
             tc_fence_after();
-            // piece k of row `row` of the second group's O, in the queries' place
-            auto spot = [&](int k) { return reinterpret_cast<float4 *>(sq + row * 512 + ((k ^ (row & 31)) << 4)); };
-            if (!two && x == 1) {
-                ref2[row] = m;
-                sum2[row] = l;
-                if (!fresh)
-#pragma unroll 1
-                    for (int k = 0; k < 128; k += 16) {
-                        float o[16];
-                        tmem_ld16(o_at + k, o);
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4)
-                            *spot((k + i) / 4) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                    }
-            }
-            soft_sync();
             const bool whole = lo + t == it.lo && lo + end == it.lo + it.units;
-            if (two || x == 0) {
-                const bool join = !two && end - t > 1;
-                float f0 = 1.0f, f1 = 0.0f;
-                if (join) {
-                    const float m1 = ref2[row], up = fmaxf(m, m1);
-                    f0 = m == -INFINITY ? 1.0f : ex2(m - up);  // sums of NaN stay
-                    f1 = m1 == -INFINITY ? 1.0f : ex2(m1 - up);
-                    l = l * f0 + sum2[row] * f1;
-                    m = up;
-                }
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                float *part = a.part + ((size_t)blockIdx.x * 2 + (t == 0 ? 0 : 1)) * ROWS * (D + 2);
-                uint16_t *to = a.out + (it.first + node) * a.o_tok + (it.head * a.group + (live ? at % a.group : 0)) * a.o_head;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            float *part = a.part + ((size_t)blockIdx.x * 2 + (t == 0 ? 0 : 1)) * ROWS * (D + 2);
+            uint16_t *to = a.out + (it.first + node) * a.o_tok + (it.head * a.group + (live ? at % a.group : 0)) * a.o_head;
+            const bool own = !fresh, others = !two && (end - t > 1 || fresh);  // of one tile only one group has an O
+            const int k0 = two ? 0 : x * 64, k1 = two ? 128 : k0 + 64;
 #pragma unroll 1
-                for (int k = 0; k < 128; k += 16) {
-                    float o[16];
+            for (int k = k0; k < k1; k += 16) {
+                float o[16];
+                if (own) {
                     tmem_ld16(o_at + k, o);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        if (join) {
-                            const float4 v = *spot((k + i) / 4);
-                            o[i] = fmaf(v.x, f1, o[i] * f0);
-                            o[i + 1] = fmaf(v.y, f1, o[i + 1] * f0);
-                            o[i + 2] = fmaf(v.z, f1, o[i + 2] * f0);
-                            o[i + 3] = fmaf(v.w, f1, o[i + 3] * f0);
-                        }
-                        if (live && !whole)
-                            *reinterpret_cast<float4 *>(part + local * D + k + i) =
-                                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                    }
-                    if (live && whole) {
-                        uint32_t w[8];
+                    for (int i = 0; i < 16; ++i)
+                        o[i] *= f0;
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const __nv_bfloat162 v = __floats2bfloat162_rn(o[i] * inv, o[i + 1] * inv);
-                            w[i / 2] = *reinterpret_cast<const uint32_t *>(&v);
-                        }
-                        if (a.o_wide) {
-                            *reinterpret_cast<uint4 *>(to + k) = make_uint4(w[0], w[1], w[2], w[3]);
-                            *reinterpret_cast<uint4 *>(to + k + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                        } else {
+                    for (int i = 0; i < 16; ++i)
+                        o[i] = 0.0f;
+                }
+                if (others) {
+                    float v[16];
+                    tmem_ld16(lanes + O_COL + (x ^ 1) * 128 + k, v);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                to[k + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-                        }
-                    }
+                    for (int i = 0; i < 16; ++i)
+                        o[i] = fmaf(v[i], f1, o[i]);
                 }
                 if (live && !whole) {
-                    part[ROWS * D + local] = m;
-                    part[ROWS * D + ROWS + local] = l;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<float4 *>(part + local * D + k + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                } else if (live) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(o[i] * inv, o[i + 1] * inv);
+                        w[i / 2] = *reinterpret_cast<const uint32_t *>(&v);
+                    }
+                    if (a.o_wide) {
+                        *reinterpret_cast<uint4 *>(to + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(to + k + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            to[k + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+                    }
                 }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(o_free);
+            if (live && !whole && (two || x == 0)) {
+                part[ROWS * D + local] = m;
+                part[ROWS * D + ROWS + local] = l;
             }
             if (end == tiles && tid == 0)
                 tree_cut(a, it, lo, run);
-            tc_fence_before();
-            soft_sync();  // the queries' place and the small arrays are free
             t = end;
         }
     }
