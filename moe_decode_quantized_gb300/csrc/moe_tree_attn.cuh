@@ -58,7 +58,7 @@ struct TreeArgs {
     int min_units;            // fewest units of a run
     uint32_t *ctrl;
     TreeCut *cuts;     // [grid] the item that starts in the run and leaves it
-    float *part;              // [grid][2] partials: rows of head size, then references, then sums
+    float *part;              // [grid][2] partials: [head size / 4][rows][4], then the rows' references, then sums
     unsigned long long wait_ns;
 };
 
@@ -335,7 +335,7 @@ template <int D>
 __global__ void __launch_bounds__(MOE_TREE_JOIN_THREADS) moe_tree_join_kernel(const __grid_constant__ TreeArgs a, const int rows)
 {
     constexpr int NT = MOE_TREE_JOIN_THREADS, R = MOE_TREE_JOIN_ROWS, P = MOE_TREE_JOIN_PARTS;
-    constexpr int COLS = D / 4, STEP = NT / COLS, PER = R / STEP;  // a thread: four dimensions of PER rows
+    constexpr int COLS = D / 4, PER = COLS * R / NT;  // a thread: four dimensions of a row, PER times
     __shared__ float weight[P][R], top[R], sum[R];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(MOE_TREE_JOIN_THREADS) moe_tree_join_kernel(co
 #pragma unroll
     for (int k = 0; k < PER; ++k)
         o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int d = tid % COLS * 4, r1 = tid / COLS;  // rows r1, r1 + STEP, ..
+    const int r = tid % R, c1 = tid / R;  // pieces of four dimensions c1, c1 + NT / R, .. of row r
     for (int p0 = 0; p0 <= c.runs; p0 += P) {
         const int n = min(P, c.runs + 1 - p0);
         if (p0 > 0) {  // the next weights
@@ -384,29 +384,27 @@ __global__ void __launch_bounds__(MOE_TREE_JOIN_THREADS) moe_tree_join_kernel(co
             __syncthreads();
         }
 #pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float *src = part(p0 + i) + r0 * D + d;
+        for (int i = 0; i < n && r < live; ++i) {
+            const float4 *src = reinterpret_cast<const float4 *>(part(p0 + i)) + r0 + r;
+            const float f = weight[i][r];
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
-                const int r = r1 + k * STEP;
-                if (r < live) {
-                    const float4 v = *reinterpret_cast<const float4 *>(src + r * D);
-                    const float f = weight[i][r];
-                    o[k].x = fmaf(v.x, f, o[k].x);
-                    o[k].y = fmaf(v.y, f, o[k].y);
-                    o[k].z = fmaf(v.z, f, o[k].z);
-                    o[k].w = fmaf(v.w, f, o[k].w);
-                }
+                const float4 v = src[(c1 + k * (NT / R)) * rows];
+                o[k].x = fmaf(v.x, f, o[k].x);
+                o[k].y = fmaf(v.y, f, o[k].y);
+                o[k].z = fmaf(v.z, f, o[k].z);
+                o[k].w = fmaf(v.w, f, o[k].w);
             }
         }
     }
+    if (r >= live)
+        return;
+    const int rr = c.block * rows + r0 + r;
+    const float inv = sum[r] == 0.0f ? 0.0f : 1.0f / sum[r];
+    uint16_t *row = a.out + (c.first + rr / a.group) * a.o_tok + (c.head * a.group + rr % a.group) * a.o_head;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-        const int r = r1 + k * STEP, rr = c.block * rows + r0 + r;
-        if (r >= live)
-            continue;
-        const float inv = sum[r] == 0.0f ? 0.0f : 1.0f / sum[r];
-        uint16_t *to = a.out + (c.first + rr / a.group) * a.o_tok + (c.head * a.group + rr % a.group) * a.o_head + d;
+        uint16_t *to = row + (c1 + k * (NT / R)) * 4;
         const __nv_bfloat162 x = __floats2bfloat162_rn(o[k].x * inv, o[k].y * inv);
         const __nv_bfloat162 y = __floats2bfloat162_rn(o[k].z * inv, o[k].w * inv);
         const uint32_t w0 = *reinterpret_cast<const uint32_t *>(&x), w1 = *reinterpret_cast<const uint32_t *>(&y);
@@ -851,12 +849,11 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const int row = mt * 16 + r * 8 + g;
-                        float *p = part + row * D + t4 * (D / 4);
+                        float4 *p = reinterpret_cast<float4 *>(part) + t4 * (D / 16) * T::ROWS + row;
 #pragma unroll
                         for (int e = 0; e < D / 4; e += 4) {  // column 2 t4 of block j is dimension 2 t4 D / 8 + j
                             const int c = 2 * r + e / (D / 8), j = e % (D / 8);
-                            *reinterpret_cast<float4 *>(p + e) =
-                                make_float4(o[mt][j][c], o[mt][j + 1][c], o[mt][j + 2][c], o[mt][j + 3][c]);
+                            p[e / 4 * T::ROWS] = make_float4(o[mt][j][c], o[mt][j + 1][c], o[mt][j + 2][c], o[mt][j + 3][c]);
                         }
                         if (t4 == 0) {
                             part[T::ROWS * D + row] = m[mt][r];

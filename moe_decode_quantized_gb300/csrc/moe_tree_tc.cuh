@@ -68,6 +68,14 @@ struct TtcRing {
     }
 };
 
+// the largest of three (a NaN counts for nothing)
+__device__ __forceinline__ float max3(float x, float y, float z)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
 // the softmax warps' own barrier
 __device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(MOE_TTC_SOFT * 32) : "memory"); }
 
@@ -526,36 +534,38 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 const int first = (int)(lo + u - it.lo) * MOE_TTC_TOKENS;
                 const uint32_t out = *reinterpret_cast<volatile uint32_t *>(gone + (u & 7));
                 const bool masked = first + MOE_TTC_TOKENS > prefix || out;
-                // 64 scores from column k: the latency of a load is that of 40 columns' work
-                auto scores = [&](int k, uint32_t (&s)[64]) {
-                    uint32_t(&lo32)[32] = reinterpret_cast<uint32_t(&)[32]>(s[0]);
-                    uint32_t(&hi32)[32] = reinterpret_cast<uint32_t(&)[32]>(s[32]);
-                    tmem_ld32_begin(s_at + k, lo32);
-                    tmem_ld32_begin(s_at + k + 32, hi32);
-                    tmem_ld32_end(lo32);
-                    tmem_ld32_end(hi32);
-                    if (masked) {  // bit i: token first + k + i is seen
+                if (masked)  // the scores of tokens that are not seen to -inf, so that the passes below stay short
+#pragma unroll 1
+                    for (int k = 0; k < 128; k += 16) {  // bit i: token first + k + i is seen
                         const int off = prefix - (first + k);
-                        unsigned long long vis = off >= 64  ? ~0ull
-                                                 : off >= 0 ? ((1ull << off) - 1) | mask << off
-                                                 : off > -64 ? mask >> -off
-                                                             : 0ull;
+                        uint32_t vis = off >= 16   ? 0xFFFFu
+                                       : off >= 0  ? ((1u << off) - 1) | (uint32_t)(mask << off)
+                                       : off > -64 ? (uint32_t)(mask >> -off)
+                                                   : 0u;
+                        vis = out >> (k / 16) & 1 ? 0u : vis;
+                        float v[16];
+                        uint32_t w[16];
+                        tmem_ld16(s_at + k, v);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            vis &= out >> (k / 16 + i) & 1 ? ~(0xFFFFull << (16 * i)) : ~0ull;
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            s[i] = vis >> i & 1 ? s[i] : 0xFF800000u;
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = vis >> i & 1 ? __float_as_uint(v[i]) : 0xFF800000u;
+                        tmem_st16(s_at + k, w);
+                        tmem_st_wait();
                     }
-                };
+                // a load takes as long as the work on some 40 columns: two of 32 at a time
                 float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
                 for (int k = 0; k < 128; k += 64) {
-                    uint32_t s[64];
-                    scores(k, s);
+                    uint32_t s[2][32];
+                    tmem_ld32_begin(s_at + k, s[0]);
+                    tmem_ld32_begin(s_at + k + 32, s[1]);
+                    tmem_ld32_end(s[0]);
+                    tmem_ld32_end(s[1]);
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        top4[i & 3] = fmaxf(top4[i & 3], __uint_as_float(s[i]));
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            top4[i >> 1 & 3] = max3(top4[i >> 1 & 3], __uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1]));
                 }
                 const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * c;
                 const bool moves = top > m + MOE_TREE_SLACK;
@@ -563,7 +573,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                     const float f = moves ? ex2(m - top) : 1.0f;
                     m = moves ? top : m;
                     l *= f;
-                    if (!fresh) {  // S is there, so the last tile's O is too
+                    if (!fresh)  // S is there, so the last tile's O is too
 #pragma unroll 1
                         for (int k = 0; k < 128; k += 16) {
                             float o[16];
@@ -574,29 +584,31 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                                 w[i] = __float_as_uint(o[i] * f);
                             tmem_st16(o_at + k, w);
                         }
-                    }
                 }
                 const float off = m == -INFINITY ? 0.0f : MOE_TREE_LIFT - m;
                 const F2 c2(c, c), off2(off, off);
                 F2 sum(0.0f, 0.0f), sum1(0.0f, 0.0f);
 #pragma unroll 1
                 for (int k = 0; k < 128; k += 64) {
-                    uint32_t s[64];
-                    scores(k, s);
+                    uint32_t s[2][32];
+                    tmem_ld32_begin(s_at + k, s[0]);
+                    tmem_ld32_begin(s_at + k + 32, s[1]);
+                    tmem_ld32_end(s[0]);
+                    tmem_ld32_end(s[1]);
 #pragma unroll
-                    for (int h = 0; h < 64; h += 32) {
+                    for (int h = 0; h < 2; ++h) {
                         uint32_t w[16];
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
                             float e0, e1;
-                            fma2(F2(__uint_as_float(s[h + i]), __uint_as_float(s[h + i + 1])), c2, off2).get(e0, e1);
+                            fma2(F2(__uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1])), c2, off2).get(e0, e1);
                             e0 = ex2(e0);
                             e1 = ex2(e1);
                             F2 &to = i & 2 ? sum1 : sum;
                             to = add2(to, F2(e0, e1));
                             w[i / 2] = pack_h2(e0, e1);
                         }
-                        tmem_st16(s_at + (k + h) / 2, w);  // P over the columns that have been read
+                        tmem_st16(s_at + k / 2 + 16 * h, w);  // P over the columns that have been read
                     }
                 }
                 sum = add2(sum, sum1);
@@ -656,7 +668,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 if (live && !whole) {
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
-                        *reinterpret_cast<float4 *>(part + local * D + k + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        reinterpret_cast<float4 *>(part)[(k + i) / 4 * ROWS + local] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 } else if (live) {
                     uint32_t w[8];
 #pragma unroll
