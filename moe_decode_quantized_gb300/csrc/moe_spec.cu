@@ -197,21 +197,30 @@ int tree_device(TreeDevice **out)
     return MOE_OK;
 }
 
-// the second kernel of a call: a CTA a run and 16 rows of its row block
-int tree_join(const TreeArgs &a, int grid, int rows, cudaStream_t s)
+// the second kernel of a call: a CTA a run and 16 rows of its row block. items:
+// about how many there are; the runs that each spans decide on the instance
+// (one sequence of 8000 tokens, 8 items of 57 parts: 37 us with the small one,
+// 24 with the large; 512 items: 288 and 281 us the other way round)
+template <int D>
+TreeKernel join_kernel(bool deep)
 {
+    return deep ? moe_tree_join_kernel<D, 512, 16> : moe_tree_join_kernel<D, 256, D == 64 ? 2 : 4>;
+}
+
+int tree_join(const TreeArgs &a, int grid, int rows, long long items, cudaStream_t s)
+{
+    const bool deep = grid / items >= 8;
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3(grid, rows / MOE_TREE_JOIN_ROWS);
-    lc.blockDim = dim3(MOE_TREE_JOIN_THREADS);
+    lc.blockDim = dim3(deep ? 512 : 256);
     lc.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = at;
     lc.numAttrs = 1;
-    const TreeKernel kernel = a.k.dim == 64    ? moe_tree_join_kernel<64>
-                              : a.k.dim == 128 ? moe_tree_join_kernel<128>
-                                               : moe_tree_join_kernel<256>;
+    const TreeKernel kernel = a.k.dim == 64 ? join_kernel<64>(deep) : a.k.dim == 128 ? join_kernel<128>(deep)
+                                                                                      : join_kernel<256>(deep);
     SPEC_CUDA_OK(cudaLaunchKernelEx(&lc, kernel, a, rows));
     return MOE_OK;
 }
@@ -396,7 +405,10 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     if ((rc = tree_device(&dev)))
         return rc;
     const int rows = (n_tokens + batch - 1) / batch * a.group;
-    if (a.k.dim == 128 && rows > 16) {
+    // The tensor-core kernel from where the warps' own products cost more than its longer steps: 8-bit caches above
+    // 32 rows (8 sequences of 8000 tokens: 32 rows 52 us by warps, 65 us by it; 16 of 4000: 64 rows 176 and 79 us),
+    // 4-bit ones, whose codes cost a warp more a byte, above 16 (16 of up to 16000: 32 rows 143 and 120 us)
+    if (a.k.dim == 128 && rows > (a.k.fmt == MOE_KV_Q8 ? 32 : 16)) {
         const TtcInstance &t = dev->tc[a.k.fmt == MOE_KV_Q8 ? 0 : 1];
         const size_t used = t.fixed + 8 * ((size_t)batch + 1);
         const int stages = (int)std::min<size_t>(4, (dev->optin - used) / t.stage);
@@ -404,7 +416,8 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
         const int grid = std::min(dev->sms, MOE_TTC_MAX_GRID);
         t.kernel<<<grid, MOE_TTC_THREADS, used + stages * t.stage, (cudaStream_t)stream>>>(a, stages);
         SPEC_CUDA_OK(cudaGetLastError());
-        return tree_join(a, grid, MOE_TTC_ROWS, (cudaStream_t)stream);
+        return tree_join(a, grid, MOE_TTC_ROWS, (long long)batch * a.k.heads * ((rows + MOE_TTC_ROWS - 1) / MOE_TTC_ROWS),
+                         (cudaStream_t)stream);
     }
     const TreeInstance &t = dev->inst[tree_choose(a.k.fmt, a.k.dim, rows)];
     // as many CTAs an SM as the registers allow while each ring keeps three stages
@@ -421,7 +434,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     const int grid = std::min(dev->sms * ctas, MOE_TREE_MAX_GRID);
     t.kernel<<<grid, MOE_TREE_THREADS, used + stages * t.stage, (cudaStream_t)stream>>>(a, stages);
     SPEC_CUDA_OK(cudaGetLastError());
-    return tree_join(a, grid, t.rows, (cudaStream_t)stream);
+    return tree_join(a, grid, t.rows, (long long)batch * a.k.heads * ((rows + t.rows - 1) / t.rows), (cudaStream_t)stream);
 }
 
 int moe_spec_verify_workspace_bytes(int batch, int n_rows, size_t *bytes)

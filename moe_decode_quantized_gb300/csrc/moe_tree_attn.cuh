@@ -164,6 +164,14 @@ __device__ __forceinline__ void tree_sequence(const TreeArgs &a, int b, int &fir
     }
 }
 
+// x / y (x >= 0, y > 0), by a 32-bit division where both fit
+__device__ __forceinline__ long long tree_div(long long x, long long y)
+{
+    if ((unsigned long long)(x | y) >> 32 == 0)
+        return (uint32_t)x / (uint32_t)y;
+    return x / y;
+}
+
 // one item: the units [lo, lo + units) of the list
 struct TreeItem {
     int b, head, block, first, n, len, units;
@@ -192,7 +200,7 @@ __device__ __forceinline__ TreeItem tree_item(const TreeArgs &a, const long long
     it.n = a.q_start[x + 1] - it.first;
     it.len = a.kv_len[x];
     it.units = (it.len + TOKENS - 1) / TOKENS;
-    const int at = (int)((u - cum[x]) / it.units), blocks = tree_blocks<ROWS>(it.n, a.group);
+    const int at = (int)tree_div(u - cum[x], it.units), blocks = tree_blocks<ROWS>(it.n, a.group);
     it.head = at / blocks;
     it.block = at % blocks;
     it.lo = cum[x] + (long long)at * it.units;
@@ -321,21 +329,24 @@ __device__ __forceinline__ void tree_store(const TreeArgs &a, const TreeItem &it
 // the run's last item, if it starts in the run and goes on after it
 __device__ __forceinline__ void tree_cut(const TreeArgs &a, const TreeItem &it, long long lo, long long run)
 {
-    const long long p0 = it.lo / run, p1 = (it.lo + it.units - 1) / run;
+    const long long p0 = tree_div(it.lo, run), p1 = tree_div(it.lo + it.units - 1, run);
     a.cuts[blockIdx.x] = {it.first, it.n, it.head, it.block, p0 == blockIdx.x ? (int)(p1 - p0) : 0, it.lo == lo};
 }
 
 #define MOE_TREE_JOIN_ROWS 16
-#define MOE_TREE_JOIN_THREADS 256
-#define MOE_TREE_JOIN_PARTS 64  // whose weights are held at once
+#define MOE_TREE_JOIN_PARTS 128  // whose weights are held at once
 
-// Joins the partials of cut items: CTA (run, 16 rows of the row block). Bound
-// by latency: a round of loads for the weights, then one for every four parts.
-template <int D>
-__global__ void __launch_bounds__(MOE_TREE_JOIN_THREADS) moe_tree_join_kernel(const __grid_constant__ TreeArgs a, const int rows)
+// Joins the partials of cut items: CTA (run, 16 rows of the row block), with
+// LOADS loads of 16 bytes in flight a thread. Bound by latency: a round of
+// loads for the weights, then one for each LOADS (or so) parts. Two instances
+// are used: small ones that all fit beside one another where the items are
+// many and of few parts (a run's end each), and large ones for few items of
+// many parts.
+template <int D, int NT, int LOADS>
+__global__ void __launch_bounds__(NT) moe_tree_join_kernel(const __grid_constant__ TreeArgs a, const int rows)
 {
-    constexpr int NT = MOE_TREE_JOIN_THREADS, R = MOE_TREE_JOIN_ROWS, P = MOE_TREE_JOIN_PARTS;
-    constexpr int COLS = D / 4, PER = COLS * R / NT;  // a thread: four dimensions of a row, PER times
+    constexpr int R = MOE_TREE_JOIN_ROWS, P = MOE_TREE_JOIN_PARTS;
+    constexpr int COLS = D / 4, PER = COLS * R > NT ? COLS * R / NT : 1;  // a thread: four dimensions of a row, PER times
     __shared__ float weight[P][R], top[R], sum[R];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
@@ -372,6 +383,7 @@ __global__ void __launch_bounds__(MOE_TREE_JOIN_THREADS) moe_tree_join_kernel(co
     for (int k = 0; k < PER; ++k)
         o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const int r = tid % R, c1 = tid / R;  // pieces of four dimensions c1, c1 + NT / R, .. of row r
+    const bool mine = r < live && c1 < COLS;
     for (int p0 = 0; p0 <= c.runs; p0 += P) {
         const int n = min(P, c.runs + 1 - p0);
         if (p0 > 0) {  // the next weights
@@ -383,21 +395,29 @@ __global__ void __launch_bounds__(MOE_TREE_JOIN_THREADS) moe_tree_join_kernel(co
                 }
             __syncthreads();
         }
-#pragma unroll 4
-        for (int i = 0; i < n && r < live; ++i) {
-            const float4 *src = reinterpret_cast<const float4 *>(part(p0 + i)) + r0 + r;
-            const float f = weight[i][r];
+        constexpr int U = LOADS / PER;
+        for (int i0 = 0; i0 < n && mine; i0 += U) {
+            float4 v[U][PER];
 #pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                const float4 v = src[(c1 + k * (NT / R)) * rows];
-                o[k].x = fmaf(v.x, f, o[k].x);
-                o[k].y = fmaf(v.y, f, o[k].y);
-                o[k].z = fmaf(v.z, f, o[k].z);
-                o[k].w = fmaf(v.w, f, o[k].w);
+            for (int i = 0; i < U; ++i)
+#pragma unroll
+                for (int k = 0; k < PER; ++k)
+                    v[i][k] = i0 + i < n ? reinterpret_cast<const float4 *>(part(p0 + i0 + i))[(c1 + k * (NT / R)) * rows + r0 + r]
+                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const float f = i0 + i < n ? weight[i0 + i][r] : 0.0f;
+#pragma unroll
+                for (int k = 0; k < PER; ++k) {
+                    o[k].x = fmaf(v[i][k].x, f, o[k].x);
+                    o[k].y = fmaf(v[i][k].y, f, o[k].y);
+                    o[k].z = fmaf(v[i][k].z, f, o[k].z);
+                    o[k].w = fmaf(v[i][k].w, f, o[k].w);
+                }
             }
         }
     }
-    if (r >= live)
+    if (!mine)
         return;
     const int rr = c.block * rows + r0 + r;
     const float inv = sum[r] == 0.0f ? 0.0f : 1.0f / sum[r];
@@ -475,7 +495,7 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
         __syncthreads();
     }
     const long long total = cum[a.batch];
-    const long long run = max((total + gridDim.x - 1) / (long long)gridDim.x, (long long)a.min_units);
+    const long long run = max(tree_div(total + gridDim.x - 1, gridDim.x), (long long)a.min_units);
     const long long lo = run * blockIdx.x, hi = min(lo + run, total);
     pdl_launch_dependents();
     if (lo >= hi) {
@@ -530,25 +550,25 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
     for (long long u = lo; u < hi;) {
         const TreeItem it = tree_item<T::ROWS, MOE_KV_BLOCK>(a, cum, u);
         const long long end = min(hi, it.lo + it.units);
-        // query fragments: k step ks of lane (g, t4) is dimensions t4 D / 4 + 4 ks .. + 3 of rows g and g + 8
-        for (int mt = warp; mt < MT; mt += MOE_TREE_WARPS) {
-            uint32_t x[2][D / 8];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int at = mt * 16 + s * 8 + g, r = it.block * T::ROWS + at;
-                const bool live = r < it.n * a.group;
-                const int i = live ? r / a.group : 0;
-                const float mul = tree_row<D / 4, 4>(a, live, it.first + i, it.head * a.group + (live ? r % a.group : 0),
-                                                     t4 * (D / 4), x[s]);
-                if (t4 == 0) {
-                    cmul[at] = mul;
-                    masks[at] = !live ? 0 : a.mask ? a.mask[it.first + i] : (2ull << i) - 1;
-                }
+        // query fragments: k step ks of lane (g, t4) is dimensions t4 D / 4 + 4 ks .. + 3 of rows g and g + 8; here
+        // eight threads have a row between them
+#pragma unroll 1
+        for (int mt = 0; mt < MT; ++mt) {
+            const int at = mt * 16 + (tid >> 3), part = tid & 7, r = it.block * T::ROWS + at;
+            const bool live = r < it.n * a.group;
+            const int i = live ? r / a.group : 0;
+            uint32_t x[D / 16];
+            const float mul = tree_row<D / 8, 8>(a, live, it.first + i, it.head * a.group + (live ? r - i * a.group : 0),
+                                                 part * (D / 8), x);
+            if (part == 0) {
+                cmul[at] = mul;
+                masks[at] = !live ? 0 : a.mask ? a.mask[it.first + i] : (2ull << i) - 1;
             }
+            uint32_t *to = reinterpret_cast<uint32_t *>(
+                qf + (mt * T::KS + (part & 1) * (D / 32)) * 32 + (at & 7) * 4 + (part >> 1)) + (at >> 3 & 1);
 #pragma unroll
-            for (int ks = 0; ks < T::KS; ++ks)
-                qf[(mt * T::KS + ks) * 32 + lane] = make_uint4(x[0][2 * ks], x[1][2 * ks], x[0][2 * ks + 1],
-                                                               x[1][2 * ks + 1]);
+            for (int e = 0; e < D / 16; ++e)
+                to[(e >> 1) * 128 + (e & 1) * 2] = x[e];
         }
         __syncthreads();
         uint4 qr[T::QREG ? MT : 1][T::QREG ? T::KS : 1];
@@ -579,7 +599,7 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
         int first = (int)(lo + warp + (long long)done * MOE_TREE_WARPS - it.lo) * 16;
         for (; done < last; ++done, first += 16 * MOE_TREE_WARPS) {
             if (ok)
-                ok = __all_sync(0xFFFFFFFFu, tree_wait(bar + stage, phase, a.ctrl + MOE_CTRL_STATUS, a.wait_ns));
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar + stage, phase, a.ctrl + MOE_CTRL_STATUS, a.wait_ns));
             const uint8_t *blk = ring + stage * T::BLOCK;
             const bool gone = (done >= batch ? bad >> (done - batch) : bad_before >> (done - batch + 32)) & 1;
             const bool masked = gone || first + 16 > prefix;

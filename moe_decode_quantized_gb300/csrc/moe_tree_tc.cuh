@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
     }
     const uint32_t tmem = *tmem_slot;
     const long long total = cum[a.batch];
-    const long long run = max((total + gridDim.x - 1) / (long long)gridDim.x, (long long)a.min_units);
+    const long long run = max(tree_div(total + gridDim.x - 1, gridDim.x), (long long)a.min_units);
     const long long lo = min(run * blockIdx.x, total), hi = min(lo + run, total);
     const int tiles = (int)(hi - lo);
     pdl_launch_dependents();
