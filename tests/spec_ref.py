@@ -26,7 +26,7 @@ def quantise(x, fmt):
     """rows [..., D] -> codes uint8 [..., D], d f16 [..., D / 32], m f16 or None, values float64 [..., D]."""
     g = np.clip(np.nan_to_num(np.asarray(x, np.float64), nan=0.0, posinf=LIMIT, neginf=-LIMIT), -LIMIT, LIMIT)
     shape = g.shape
-    g = g.reshape(shape[:-1] + (-1, 32))
+    g = g.reshape(shape[:-1] + (shape[-1] // 32, 32))
     if fmt == Q8:
         d = f16_towards(np.abs(g).max(-1) / 127.0, True)
         f = d.astype(np.float64)[..., None]

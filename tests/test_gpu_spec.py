@@ -268,6 +268,45 @@ def test_large_and_equal_scores(k_scale):
     s.check(s.run())
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("group,rows", [(4, 1), (8, 8), (8, 40)])
+def test_one_long_sequence(fmt, group, rows):
+    """One head of one sequence over all CTAs: more partials than are weighed at once."""
+    s = Sequences(fmt, 128, 1, group, 128, [40011], [rows], rows, "tree")
+    s.check(s.run())
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_large_groups(dim):
+    s = Sequences(moe.MOE_KV_Q8, dim, 1, 64, 32, [300, 5, 77], [5, 1, 2], dim, "tree")
+    s.check(s.run())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("batch,ctx,rows", [(300, 20, 9), (40, 500, 30), (3, 3000, 64)])
+def test_many_and_few_items_of_many_rows(fmt, batch, ctx, rows):
+    """Row blocks of one and of two M tiles, in runs that cut few items and in runs of many whole ones, mixed."""
+    rng = np.random.default_rng(batch)
+    s = Sequences(fmt, 128, 2, 8, 16, [int(c) for c in rng.integers(0, ctx, batch)],
+                  [int(n) for n in rng.integers(0, rows + 1, batch)], batch, "tree")
+    out = s.run()
+    s.check(out, set(rng.integers(0, batch, 12).tolist()) | {0, batch - 1})
+    assert torch.isfinite(out).all()
+
+
+def test_strides_of_many_rows():
+    s = Sequences(moe.MOE_KV_Q8, 128, 2, 4, 32, [900, 5, 64], [64, 33, 40], 17, "tree")
+    ws = s.workspace()
+    want = s.run(ws)
+    s.check(want)
+    n, heads, dim = s.q.shape
+    odd = torch.zeros((n, heads, dim + 1), dtype=torch.bfloat16, device="cuda")
+    odd[:, :, 1:] = s.q
+    got = torch.zeros((heads, n, dim + 3), dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    s.run(ws, odd[:, :, 1:], got[:, :, 3:])
+    assert torch.equal(got[:, :, 3:], want) and (got[:, :, :3] == 0).all()
+
+
 def test_strides_streams_and_repeats():
     """q and out as views (a fused projection's output; heads first), another stream, and the same bits each time on a
     workspace that other calls used."""
@@ -466,6 +505,14 @@ def test_verify(kind, shape, drafts, batch, nodes, vocab):
     assert status == 0
 
 
+@pytest.mark.parametrize("kind,batch,vocab", [("f32", 20, 100003), ("bf16", 24, 131072), ("f32", 1, 1 << 22)])
+@pytest.mark.parametrize("drafts", [True, False])
+def test_verify_large_trees(kind, batch, vocab, drafts):
+    """More logits than are gone through ahead: rows as the walk reaches them."""
+    status, _ = check_verify(verify_case(batch, 24 if batch > 1 else 6, vocab, kind, "tree", drafts, vocab % 97))
+    assert status == 0
+
+
 @pytest.mark.parametrize("vocab", [1, 2, 7, 8, 9, 31, 1023, 8193, 131072])
 def test_verify_vocabularies(vocab):
     for drafts in (True, False):
@@ -569,3 +616,40 @@ def test_verify_follows_the_targets_distribution():
         seen = np.bincount(first, minlength=vocab)
         assert ((seen - batch * p) ** 2 / (batch * p)).sum() < 51.0
         assert 0.2 * batch < sum(c > 0 for c in n_acc) < batch
+
+
+# ------------------------------------------------------------------ together
+
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "speculative_decode.py")
+    spec = importlib.util.spec_from_file_location("speculative_decode", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_example_decodes_what_single_tokens_decode(fmt):
+    """Greedy decoding with drafted trees: every token is the largest logit of the plain decode of the tokens before it
+    (one token a step, another model object and cache), up to the rounding of the logits."""
+    ex = _example()
+    prompt, count = [3, 1, 4, 1, 5, 9, 2, 6, 5, 3, 5], 40
+    out, rounds = ex.generate(ex.Model(seed=4, kv_format=fmt), prompt, count)
+    assert rounds < len(out)  # some drafts were accepted
+    plain = ex.Model(seed=4, kv_format=fmt)
+    tokens = prompt + out
+    for i, t in enumerate(tokens[:-1]):
+        logits = plain.rows(torch.tensor([t], dtype=torch.int32, device="cuda"), i, None)[0]
+        if i >= len(prompt) - 1:
+            # bf16 activations: a few roundings of 2^-8 of logits of unit size times 4
+            assert logits[tokens[i + 1]] >= logits.max() - 0.15, i
+
+
+def test_example_samples():
+    ex = _example()
+    out, rounds = ex.generate(ex.Model(seed=5), [7, 7], 24, temperature=1.0)
+    assert len(out) >= 24 and all(0 <= t < 512 for t in out)
+    again, _ = ex.generate(ex.Model(seed=5), [7, 7], 24, temperature=1.0)
+    assert out == again
