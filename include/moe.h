@@ -505,8 +505,8 @@ int moe_kv_page_bytes(const moe_kv_cache *cache, size_t *bytes);
  * head h is k_dev + t * k_token_stride + h * k_head_stride (bf16, strides in
  * elements, so views of a fused projection's output can be passed), written
  * to slot slots_dev[t] (i32; -1: the token is skipped; the caller passes a
- * slot at most once). Rows that start on 16-byte boundaries with strides that
- * are multiples of 8 take the wider loads. *status_dev (NULL, or a device
+ * slot at most once). Rows that all start on 32-byte (16-byte) boundaries are
+ * loaded that wide, others slower. *status_dev (NULL, or a device
  * word) receives MOE_WS_INDEX for a slot outside the cache (skipped) and
  * MOE_WS_NONFINITE. */
 int moe_kv_append(const moe_kv_cache *cache, const void *k_dev, int64_t k_token_stride, int64_t k_head_stride,

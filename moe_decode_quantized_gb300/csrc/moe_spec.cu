@@ -62,15 +62,10 @@ int check_cache(const moe_kv_cache *c, KvDims &k)
 
 // ---- the cache's kernels
 
-using KvKernel = void (*)(KvArgs);
+// KvArgs::per_page
+unsigned long long kv_per_page(const KvDims &k) { return ((1ull << 36) + k.page / 16 - 1) / (k.page / 16); }
 
-template <int FMT, int D>
-KvKernel kv_append_kernel(int align)
-{
-    return align >= 32   ? moe_kv_append_kernel<FMT, D, 32>
-           : align >= 16 ? moe_kv_append_kernel<FMT, D, 16>
-                         : moe_kv_append_kernel<FMT, D, 2>;
-}
+using KvKernel = void (*)(KvArgs);
 
 template <int FMT, int D>
 KvKernel kv_read_kernel(bool f32, bool wide)
@@ -257,6 +252,7 @@ int moe_kv_append(const moe_kv_cache *cache, const void *k_dev, int64_t k_token_
         return MOE_OK;
     a.pages = static_cast<uint8_t *>(cache->pages);
     a.n_slots = cache->n_pages * cache->page_size;
+    a.per_page = kv_per_page(a.k);
     a.src[0] = static_cast<const uint16_t *>(k_dev);
     a.src[1] = static_cast<const uint16_t *>(v_dev);
     a.tok_stride[0] = k_token_stride;
@@ -271,15 +267,18 @@ int moe_kv_append(const moe_kv_cache *cache, const void *k_dev, int64_t k_token_
                           (k_token_stride | k_head_stride | v_token_stride | v_head_stride) * 2 % align == 0))
         align = align == 32 ? 16 : 2;
     KvKernel kernel = nullptr;
-    int most = 0;  // warps a head: the more of K's and V's
+    int per = 0;  // tokens of a warp
     with_kv(a.k, [&](auto f, auto d) {
-        constexpr int D = decltype(d)::value, TK = kv_append_tokens<D, false>();
-        kernel = kv_append_kernel<decltype(f)::value, D>(align);
-        most = std::max((n_tokens + TK - 1) / TK, (n_tokens + 7) / 8 * 2);
+        constexpr int F = decltype(f)::value, D = decltype(d)::value;
+        kernel = align == 32   ? moe_kv_append_kernel<F, D, 32>
+                 : align == 16 ? moe_kv_append_kernel<F, D, 16>
+                               : moe_kv_append_kernel<F, D, 2>;
+        per = align == 2 ? kv_append_tokens<D, 2>() : kv_append_tokens<D, 16>();
         return 0;
     });
-    const int warps = std::min(MOE_KV_THREADS / 32, most);
-    kernel<<<dim3((most + warps - 1) / warps, 2 * a.k.heads), warps * 32, 0, (cudaStream_t)stream>>>(a);
+    const long long all = ((long long)n_tokens + per - 1) / per;  // warps a head
+    const int warps = (int)std::min<long long>(MOE_KV_THREADS / 32, all);
+    kernel<<<dim3((unsigned)((all + warps - 1) / warps), 2 * a.k.heads), warps * 32, 0, (cudaStream_t)stream>>>(a);
     SPEC_CUDA_OK(cudaGetLastError());
     return MOE_OK;
 }
@@ -301,6 +300,7 @@ int moe_kv_read(const moe_kv_cache *cache, const int32_t *slots_dev, int n_token
         return MOE_OK;
     a.pages = static_cast<uint8_t *>(cache->pages);
     a.n_slots = cache->n_pages * cache->page_size;
+    a.per_page = kv_per_page(a.k);
     a.slots = slots_dev;
     a.out[0] = k_out_dev;
     a.out[1] = v_out_dev;
@@ -315,7 +315,7 @@ int moe_kv_read(const moe_kv_cache *cache, const int32_t *slots_dev, int n_token
         per = std::max(kv_read_threads<F, D, false>(), kv_read_threads<F, D, true>());
         return 0;
     });
-    const long long threads = (n_tokens + 7) / 8 * (long long)per;
+    const long long threads = (n_tokens + 7ll) / 8 * per;
     const dim3 grid((unsigned)((threads + MOE_KV_THREADS - 1) / MOE_KV_THREADS), 2 * a.k.heads);
     kernel<<<grid, MOE_KV_THREADS, 0, (cudaStream_t)stream>>>(a);
     SPEC_CUDA_OK(cudaGetLastError());
