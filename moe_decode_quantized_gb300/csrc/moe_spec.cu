@@ -102,7 +102,10 @@ VerifyKernel verify_kernel(bool f32, bool wide, bool ahead)
     return ahead ? verify_kernel<true>(f32, wide) : verify_kernel<false>(f32, wide);
 }
 
-#define MOE_VERIFY_AHEAD_BYTES (48u << 20)
+// The rows ahead pay where the walk would go through most of them: chains (4 rows of 32000: 6.7 us, in the walk 11.5;
+// 48 x 8 of 131072: 36 and 49), and trees of few bytes (8 rows of 128000: 10 and 15 us; 24 of 100003 in f32, 9.6 MB:
+// 13.5 and 14.8; 48 rows 14.6 and 16.6). Larger trees: 96 rows 16.5 and 13.4, 384 (154 MB) 39 and 18.
+#define MOE_VERIFY_AHEAD_BYTES (20u << 20)
 
 // ---- tree attention: instances and their launch shape
 
@@ -410,7 +413,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     // 4-bit ones, whose codes cost a warp more a byte, above 16 (16 of up to 16000: 32 rows 143 and 120 us)
     if (a.k.dim == 128 && rows > (a.k.fmt == MOE_KV_Q8 ? 32 : 16)) {
         const TtcInstance &t = dev->tc[a.k.fmt == MOE_KV_Q8 ? 0 : 1];
-        const size_t used = t.fixed + 8 * ((size_t)batch + 1);
+        const size_t used = t.fixed + 12 * ((size_t)batch + 1);
         const int stages = (int)std::min<size_t>(4, (dev->optin - used) / t.stage);
         a.min_units = 2;
         const int grid = std::min(dev->sms, MOE_TTC_MAX_GRID);
@@ -421,7 +424,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     }
     const TreeInstance &t = dev->inst[tree_choose(a.k.fmt, a.k.dim, rows)];
     // as many CTAs an SM as the registers allow while each ring keeps three stages
-    const size_t list = 8 * ((size_t)batch + 1), used = t.fixed + list;
+    const size_t list = 12 * ((size_t)batch + 1), used = t.fixed + list;
     int ctas = t.ctas, stages;
     for (;; --ctas) {
         const size_t room = std::min(dev->optin, dev->per_sm / ctas - 1024);
@@ -499,7 +502,8 @@ int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stri
     const bool wide = aligned(logits_dev, 16) && logits_stride % (f32 ? 4 : 8) == 0 &&
                       (!draft_dev || (aligned(draft_dev, 16) && draft_stride % 4 == 0)) &&
                       (!noise_dev || (aligned(noise_dev, 16) && noise_stride % 4 == 0));
-    // a cluster of CTAs a sequence: as many as are on the GPU together (three an SM), with 2048 values a CTA at least
+    // a cluster of CTAs a sequence: as many as are on the GPU together (three an SM; 512 sequences of 32000: 49 us, with
+    // eight CTAs each 76), with 2048 values a CTA at least (48 sequences of 131072: 36 us, with one CTA each 95)
     const int ranks = std::max(1, std::min({MOE_VERIFY_MAX_CLUSTER, 456 / batch, vocab / 2048}));
     a.slice = ((vocab + ranks - 1) / ranks + 7) / 8 * 8;
     // all rows ahead where that is little, else as the walk reaches them
@@ -507,8 +511,9 @@ int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stri
     const bool ahead = n_rows > 0 && (all <= MOE_VERIFY_AHEAD_BYTES || !parents_dev);
     if (ahead) {
         a.batch = batch;
-        // parts of 16384 values, of 2048 where the rows are few
-        a.splits = std::max(1, std::min({MOE_VERIFY_MAX_SPLITS, vocab / 2048, std::max(1216 / n_rows, vocab / 16384)}));
+        // parts of 16384 values, of down to 2048 where the rows are few (4 rows of 32000: 6.7 us, as two parts 8.7; 384
+        // of 131072: 36 us, in parts of 2048 107)
+        a.splits = std::max(1, std::min({MOE_VERIFY_MAX_SPLITS, vocab / 2048, std::max(608 / n_rows, vocab / 16384)}));
         a.split = ((vocab + a.splits - 1) / a.splits + 7) / 8 * 8;
         a.stats = reinterpret_cast<VerifySlice *>(static_cast<char *>(ws_dev) + SPEC_CTRL_BYTES);
         const auto rows = f32 ? (wide ? moe_verify_rows_kernel<true, true> : moe_verify_rows_kernel<true, false>)

@@ -26,7 +26,7 @@ namespace moe {
 
 #define MOE_TREE_WARPS 4
 #define MOE_TREE_THREADS (MOE_TREE_WARPS * 32)
-#define MOE_TREE_MAX_BATCH 1024
+#define MOE_TREE_COST 24  // of an item, beside its units
 // the weights are 2^(s - m + 7): m moves when a score passes it by 8, so a
 // weight stays below 2^15, and f16 holds weights of 2^-31 of the largest
 #define MOE_TREE_SLACK 8.0f
@@ -172,6 +172,26 @@ __device__ __forceinline__ long long tree_div(long long x, long long y)
     return x / y;
 }
 
+// zeros for the query rows of a sequence that does not hold
+template <int D>
+__device__ __forceinline__ void tree_zero(const TreeArgs &a, int first, int rows)
+{
+    const int heads = a.k.heads * a.group;
+    for (int r = 0; r < rows * heads; ++r) {
+        uint16_t *p = a.out + (first + r / heads) * a.o_tok + r % heads * a.o_head;
+        for (int d = 0; d < D; ++d)
+            p[d] = 0;
+    }
+}
+
+// The list is cut by cost: an item costs its units and COST more (its queries
+// are brought, its warps joined), so that no CTA gets many short items (8
+// sequences, one without a context, 20 rows a head: 90 us without, 74, 52, 46,
+// 45 with a cost of 8, 16, 24, 32; 64 sequences of 1 to 300 tokens 47 and 22 us;
+// 64 of 4000 to 24000 275, with 32 278; the tensor-core kernel's tiles of 128
+// tokens: 120 us without, 112 with 2, 117 with 6). cum [batch + 1] and items [batch + 1] are the units and the items before each
+// sequence; a place in the list of costs is turned into a unit by tree_place.
+
 // one item: the units [lo, lo + units) of the list
 struct TreeItem {
     int b, head, block, first, n, len, units;
@@ -207,6 +227,87 @@ __device__ __forceinline__ TreeItem tree_item(const TreeArgs &a, const long long
     return it;
 }
 
+// the first unit at or after place w of the list of costs (an item's units come before the rest of its cost)
+template <int ROWS, int TOKENS, int COST>
+__device__ __forceinline__ long long tree_place(const TreeArgs &a, const long long *cum, const int *items, long long w)
+{
+    int x = 0, y = a.batch;
+    while (y - x > 1) {
+        const int z = (x + y) / 2;
+        if (cum[z] + (long long)COST * items[z] <= w)
+            x = z;
+        else
+            y = z;
+    }
+    const int here = items[x + 1] - items[x];
+    if (here == 0)
+        return cum[x];
+    const int units = (a.kv_len[x] + TOKENS - 1) / TOKENS;
+    const long long off = w - cum[x] - (long long)COST * items[x], at = min(tree_div(off, units + COST), (long long)here - 1);
+    return cum[x] + at * units + min(off - at * (units + COST), (long long)units);
+}
+
+// Fills cum and items (scan, count: a word a warp) and gives this CTA's units
+// [lo, hi) and the cost of a run; zeros for rows of sequences that do not hold
+template <int D, int ROWS, int TOKENS, int COST, int NT>
+__device__ __forceinline__ void tree_list(const TreeArgs &a, long long *cum, int *items, long long *scan, int *count,
+                                          long long &lo, long long &hi, long long &run)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (a.batch + NT - 1) / NT;
+    long long mine = 0;
+    int own = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b >= a.batch)
+            break;
+        int first, n, len, rows;
+        tree_sequence(a, b, first, n, len, rows);
+        cum[b] = mine;
+        items[b] = own;
+        const int here = n > 0 ? tree_blocks<ROWS>(n, a.group) * a.k.heads : 0;
+        mine += (long long)((len + TOKENS - 1) / TOKENS) * here;
+        own += here;
+        if (n == 0 && rows > 0 && blockIdx.x == (unsigned)(b % gridDim.x))
+            tree_zero<D>(a, first, rows);
+    }
+    long long incl = mine;
+    int got = own;
+    for (int m = 1; m < 32; m *= 2) {
+        const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+        const int u = __shfl_up_sync(0xFFFFFFFFu, got, m);
+        if (lane >= m) {
+            incl += v;
+            got += u;
+        }
+    }
+    if (lane == 31) {
+        scan[warp] = incl;
+        count[warp] = got;
+    }
+    __syncthreads();
+    long long before = incl - mine;
+    int ahead = got - own;
+    for (int w = 0; w < warp; ++w) {
+        before += scan[w];
+        ahead += count[w];
+    }
+    for (int i = 0; i < per; ++i)
+        if (tid * per + i < a.batch) {
+            cum[tid * per + i] += before;
+            items[tid * per + i] += ahead;
+        }
+    if (tid == NT - 1) {
+        cum[a.batch] = before + mine;
+        items[a.batch] = ahead + own;
+    }
+    __syncthreads();
+    const long long total = cum[a.batch] + (long long)COST * items[a.batch];
+    run = max(tree_div(total + gridDim.x - 1, gridDim.x), (long long)a.min_units);
+    const long long w = run * blockIdx.x;
+    lo = w < total ? tree_place<ROWS, TOKENS, COST>(a, cum, items, w) : cum[a.batch];
+    hi = w + run < total ? tree_place<ROWS, TOKENS, COST>(a, cum, items, w + run) : cum[a.batch];
+}
+
 // the item after `it` in the list (there is one)
 template <int ROWS, int TOKENS>
 __device__ __forceinline__ void tree_next(const TreeArgs &a, const long long *cum, TreeItem &it)
@@ -225,18 +326,6 @@ __device__ __forceinline__ void tree_next(const TreeArgs &a, const long long *cu
     it.n = a.q_start[it.b + 1] - it.first;
     it.len = a.kv_len[it.b];
     it.units = (it.len + TOKENS - 1) / TOKENS;
-}
-
-// zeros for the query rows of a sequence that does not hold
-template <int D>
-__device__ __forceinline__ void tree_zero(const TreeArgs &a, int first, int rows)
-{
-    const int heads = a.k.heads * a.group;
-    for (int r = 0; r < rows * heads; ++r) {
-        uint16_t *p = a.out + (first + r / heads) * a.o_tok + r % heads * a.o_head;
-        for (int d = 0; d < D; ++d)
-            p[d] = 0;
-    }
 }
 
 // COUNT values (from dimension d0) of a query row that LANES neighbouring
@@ -327,9 +416,12 @@ __device__ __forceinline__ void tree_store(const TreeArgs &a, const TreeItem &it
 }
 
 // the run's last item, if it starts in the run and goes on after it
-__device__ __forceinline__ void tree_cut(const TreeArgs &a, const TreeItem &it, long long lo, long long run)
+template <int ROWS, int COST>
+__device__ __forceinline__ void tree_cut(const TreeArgs &a, const TreeItem &it, const int *items, long long lo, long long run)
 {
-    const long long p0 = tree_div(it.lo, run), p1 = tree_div(it.lo + it.units - 1, run);
+    const int ordinal = items[it.b] + it.head * tree_blocks<ROWS>(it.n, a.group) + it.block;
+    const long long w = it.lo + (long long)COST * ordinal;  // where it begins in the list of costs
+    const long long p0 = tree_div(w, run), p1 = tree_div(w + it.units - 1, run);
     a.cuts[blockIdx.x] = {it.first, it.n, it.head, it.block, p0 == blockIdx.x ? (int)(p1 - p0) : 0, it.lo == lo};
 }
 
@@ -452,6 +544,8 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
     uint4 *qf = reinterpret_cast<uint4 *>(smem + T::HEAD);                         // [mt][ks][lane]
     float4 *merge = reinterpret_cast<float4 *>(smem + T::HEAD + T::QBYTES);        // [2][regs / 4][lane]
     long long *cum = reinterpret_cast<long long *>(smem + T::FIXED + (size_t)MOE_TREE_WARPS * stages * T::BLOCK);  // [batch + 1]
+    int *items = reinterpret_cast<int *>(cum + a.batch + 1);                       // [batch + 1]
+    int *count = reinterpret_cast<int *>(scan + MOE_TREE_WARPS);                   // [warps]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     uint8_t *ring = smem + T::FIXED + (size_t)warp * stages * T::BLOCK;
     uint64_t *bar = bars + warp * 8;
@@ -460,43 +554,8 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
             mbar_init(bar + s, 1);
         fence_barrier_init();
     }
-    // the list: units before each sequence
-    {
-        const int per = (a.batch + MOE_TREE_THREADS - 1) / MOE_TREE_THREADS;
-        long long mine = 0;
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b >= a.batch)
-                break;
-            int first, n, len, rows;
-            tree_sequence(a, b, first, n, len, rows);
-            cum[b] = mine;
-            mine += (long long)((len + 15) / 16) * (n > 0 ? tree_blocks<T::ROWS>(n, a.group) * a.k.heads : 0);
-            if (n == 0 && rows > 0 && blockIdx.x == (unsigned)(b % gridDim.x))  // what does not hold gives zeros
-                tree_zero<D>(a, first, rows);
-        }
-        long long incl = mine;
-        for (int m = 1; m < 32; m *= 2) {
-            const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, m);
-            if (lane >= m)
-                incl += v;
-        }
-        if (lane == 31)
-            scan[warp] = incl;
-        __syncthreads();
-        long long before = incl - mine;
-        for (int w = 0; w < warp; ++w)
-            before += scan[w];
-        for (int i = 0; i < per; ++i)
-            if (tid * per + i < a.batch)
-                cum[tid * per + i] += before;
-        if (tid == MOE_TREE_THREADS - 1)
-            cum[a.batch] = before + mine;
-        __syncthreads();
-    }
-    const long long total = cum[a.batch];
-    const long long run = max(tree_div(total + gridDim.x - 1, gridDim.x), (long long)a.min_units);
-    const long long lo = run * blockIdx.x, hi = min(lo + run, total);
+    long long lo, hi, run;
+    tree_list<D, T::ROWS, MOE_KV_BLOCK, MOE_TREE_COST, MOE_TREE_THREADS>(a, cum, items, scan, count, lo, hi, run);
     pdl_launch_dependents();
     if (lo >= hi) {
         if (tid == 0)
@@ -883,7 +942,7 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
             }
         }
         if (end == hi && tid == 0)
-            tree_cut(a, it, lo, run);
+            tree_cut<T::ROWS, MOE_TREE_COST>(a, it, items, lo, run);
         u = end;
     }
     if (!ok)  // a copy did not arrive in time: wait for those in flight (bounded) before the memory is given back

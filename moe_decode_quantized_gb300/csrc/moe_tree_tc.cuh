@@ -27,6 +27,7 @@ namespace moe {
 
 #define MOE_TTC_TOKENS 128
 #define MOE_TTC_ROWS 256  // of a row block: two M tiles
+#define MOE_TTC_COST 2    // of an item, beside its tiles (moe_tree_attn.cuh)
 #define MOE_TTC_SOFT 8    // softmax warps
 #define MOE_TTC_CODE 8    // warps that turn codes into f16
 #define MOE_TTC_THREADS ((MOE_TTC_SOFT + MOE_TTC_CODE + 2) * 32)
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
     float *mul = reinterpret_cast<float *>(small + 256);  // [4][256] multipliers of the rows of item i, at i % 4
     float2 *stat = reinterpret_cast<float2 *>(mul + 1024);  // [2][2][128] (reference, sum) of item i, at i % 2, by group
     long long *scan = reinterpret_cast<long long *>(stat + 512), *cum = scan + 32;  // cum [batch + 1]
+    int *count = reinterpret_cast<int *>(scan + 20), *items = reinterpret_cast<int *>(cum + a.batch + 1);  // items [batch + 1]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t *status = a.ctrl + MOE_CTRL_STATUS;
 
@@ -152,48 +154,11 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
     }
     if (warp == 0)
         tmem_alloc(tmem_slot, 512);
-    // the list: tiles before each sequence
-    {
-        constexpr int NT = MOE_TTC_THREADS;
-        const int per = (a.batch + NT - 1) / NT;
-        long long mine = 0;
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b >= a.batch)
-                break;
-            int first, n, len, rows;
-            tree_sequence(a, b, first, n, len, rows);
-            cum[b] = mine;
-            mine += (long long)((len + MOE_TTC_TOKENS - 1) / MOE_TTC_TOKENS) *
-                    (n > 0 ? tree_blocks<ROWS>(n, a.group) * a.k.heads : 0);
-            if (n == 0 && rows > 0 && blockIdx.x == (unsigned)(b % gridDim.x))
-                tree_zero<D>(a, first, rows);
-        }
-        long long incl = mine;
-        for (int m = 1; m < 32; m *= 2) {
-            const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, m);
-            if (lane >= m)
-                incl += v;
-        }
-        if (lane == 31)
-            scan[warp] = incl;
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        long long before = incl - mine;
-        for (int w = 0; w < warp; ++w)
-            before += scan[w];
-        for (int i = 0; i < per; ++i)
-            if (tid * per + i < a.batch)
-                cum[tid * per + i] += before;
-        if (tid == NT - 1)
-            cum[a.batch] = before + mine;
-        __syncthreads();
-    }
+    long long lo, hi, run;
+    tc_fence_before();
+    tree_list<D, ROWS, MOE_TTC_TOKENS, MOE_TTC_COST, MOE_TTC_THREADS>(a, cum, items, scan, count, lo, hi, run);
+    tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const long long total = cum[a.batch];
-    const long long run = max(tree_div(total + gridDim.x - 1, gridDim.x), (long long)a.min_units);
-    const long long lo = min(run * blockIdx.x, total), hi = min(lo + run, total);
     const int tiles = (int)(hi - lo);
     pdl_launch_dependents();
     if (tiles == 0 && tid == 0)
@@ -695,7 +660,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 part[ROWS * D + ROWS + local] = l;
             }
             if (end == tiles && tid == 0)
-                tree_cut(a, it, lo, run);
+                tree_cut<ROWS, MOE_TTC_COST>(a, it, items, lo, run);
             t = end;
         }
     }
