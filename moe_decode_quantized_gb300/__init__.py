@@ -520,19 +520,22 @@ class KvCache:
         object.__setattr__(self, "_ref", None)
 
     def __post_init__(self):
-        self.n_pages = 0
-        per = kv_page_bytes(self)
-        if self.pages is not None:
-            size = self.pages.numel() * self.pages.element_size()
-            if size % per:
-                raise ValueError(f"pages holds {size} bytes, not a multiple of a page's {per}")
-            self.n_pages = size // per
+        self.ref()
+
+    @property
+    def n_pages(self) -> int:
+        if self.pages is None:
+            return 0
+        per, size = kv_page_bytes(self), self.pages.numel() * self.pages.element_size()
+        if size % per:
+            raise ValueError(f"pages holds {size} bytes, not a multiple of a page's {per}")
+        return size // per
 
     def ref(self):
         """The C struct by reference, made again after a field was set."""
         if self._ref is None:
-            c = _lib.MoeKvCache(_ptr(self.pages), self.n_pages, self.head_dim, self.n_kv_heads, self.page_size,
-                                self.format)
+            n_pages = self.n_pages
+            c = _lib.MoeKvCache(_ptr(self.pages), n_pages, self.head_dim, self.n_kv_heads, self.page_size, self.format)
             object.__setattr__(self, "_ref", C.byref(c))
         return self._ref
 

@@ -131,13 +131,20 @@ TreeInstance tree_instance()
 
 std::mutex g_tree_mu;
 
-// the instance for (format, head size) with at least `rows` rows a block where there is one, else the largest
+// The instance for (format, head size) with at least `rows` rows a block where there is one, else the largest: a block
+// of the cache is then turned into numbers once (64 sequences of 12000 tokens, Q8, 32 rows of 128: 378 us, as two row
+// blocks 525; of 16000, 64 rows of 64: 511 us, as two 622, as four 819). Heads of 256 leave registers for 16 rows.
 int tree_choose(int fmt, int dim, int rows)
 {
     const int mt = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;
-    const int first = dim == 64 ? 0 : dim == 128 ? 3 : 5, most = dim == 64 ? 2 : dim == 128 ? 1 : 0;
-    return (fmt == MOE_KV_Q8 ? 0 : 6) + first + std::min(mt, most);
+    if (dim == 256)
+        return fmt == MOE_KV_Q8 ? 5 : 10;
+    if (fmt == MOE_KV_Q8)
+        return dim == 64 ? mt : 3 + std::min(mt, 1);
+    return dim == 64 ? 6 + mt : 9;
 }
+
+#define MOE_TREE_INSTANCES 11
 
 // the tensor-core kernels' instances, by format
 struct TtcInstance {
@@ -155,7 +162,7 @@ TtcInstance ttc_instance()
 struct TreeDevice {
     int sms = 0;
     size_t per_sm = 0, optin = 0;  // shared memory
-    TreeInstance inst[12];
+    TreeInstance inst[MOE_TREE_INSTANCES];
     TtcInstance tc[2];
 };
 
@@ -169,16 +176,16 @@ int tree_device(TreeDevice **out)
     std::lock_guard<std::mutex> lk(g_tree_mu);
     TreeDevice &D = dev[d];
     if (!D.sms) {
-        const TreeInstance all[12] = {
+        const TreeInstance all[MOE_TREE_INSTANCES] = {
             tree_instance<MOE_KV_Q8, 64, 1>(),  tree_instance<MOE_KV_Q8, 64, 2>(),  tree_instance<MOE_KV_Q8, 64, 4>(),
             tree_instance<MOE_KV_Q8, 128, 1>(), tree_instance<MOE_KV_Q8, 128, 2>(), tree_instance<MOE_KV_Q8, 256, 1>(),
             tree_instance<MOE_KV_Q4, 64, 1>(),  tree_instance<MOE_KV_Q4, 64, 2>(),  tree_instance<MOE_KV_Q4, 64, 4>(),
-            tree_instance<MOE_KV_Q4, 128, 1>(), tree_instance<MOE_KV_Q4, 128, 2>(), tree_instance<MOE_KV_Q4, 256, 1>()};
+            tree_instance<MOE_KV_Q4, 128, 1>(), tree_instance<MOE_KV_Q4, 256, 1>()};
         int n = 0, per_sm = 0, optin = 0;
         SPEC_CUDA_OK(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d));
         SPEC_CUDA_OK(cudaDeviceGetAttribute(&per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, d));
         SPEC_CUDA_OK(cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, d));
-        for (int i = 0; i < 12; ++i) {
+        for (int i = 0; i < MOE_TREE_INSTANCES; ++i) {
             SPEC_CUDA_OK(cudaFuncSetAttribute(all[i].kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
             D.inst[i] = all[i];
         }
@@ -398,7 +405,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     a.scale = scale;
     a.q_wide = aligned(q_dev, 16) && (q_token_stride | q_head_stride) % 8 == 0;
     a.o_wide = aligned(out_dev, 16) && (out_token_stride | out_head_stride) % 8 == 0;
-    a.min_units = 2 * MOE_TREE_WARPS;
+    a.min_units = 2 * MOE_TREE_WARPS;  // (a sequence of 511 tokens: 12.3 us, with twice that 13.3; of 8000: 24.7, 22.8)
     a.ctrl = static_cast<uint32_t *>(ws_dev);
     a.cuts = reinterpret_cast<TreeCut *>(a.ctrl + SPEC_CTRL_BYTES / 4);
     a.part = reinterpret_cast<float *>(a.cuts + MOE_TREE_MAX_GRID);
@@ -409,8 +416,8 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
         return rc;
     const int rows = (n_tokens + batch - 1) / batch * a.group;
     // The tensor-core kernel from where the warps' own products cost more than its longer steps: 8-bit caches above
-    // 32 rows (8 sequences of 8000 tokens: 32 rows 52 us by warps, 65 us by it; 16 of 4000: 64 rows 176 and 79 us),
-    // 4-bit ones, whose codes cost a warp more a byte, above 16 (16 of up to 16000: 32 rows 143 and 120 us)
+    // 32 rows (64 sequences of 12000 tokens: 32 rows 378 us by warps, 582 us by it; 16 of 4000: 64 rows 176 and 79 us),
+    // 4-bit ones, whose codes cost a warp more a byte, above 16 (16 of up to 16000: 32 rows 143 and 112 us)
     if (a.k.dim == 128 && rows > (a.k.fmt == MOE_KV_Q8 ? 32 : 16)) {
         const TtcInstance &t = dev->tc[a.k.fmt == MOE_KV_Q8 ? 0 : 1];
         const size_t used = t.fixed + 12 * ((size_t)batch + 1);
@@ -423,7 +430,8 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
                          (cudaStream_t)stream);
     }
     const TreeInstance &t = dev->inst[tree_choose(a.k.fmt, a.k.dim, rows)];
-    // as many CTAs an SM as the registers allow while each ring keeps three stages
+    // as many CTAs an SM as the registers allow while each ring keeps three stages (64 sequences of 4000 to 24000
+    // tokens: three CTAs 276 us, two 346, one 562)
     const size_t list = 12 * ((size_t)batch + 1), used = t.fixed + list;
     int ctas = t.ctas, stages;
     for (;; --ctas) {

@@ -126,6 +126,40 @@ def test_append_of_extreme_values(fmt):
         assert status.item() == bits
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_append_rounds_as_the_quotient(fmt, dim):
+    """Numbers of few bits, whose quotients often lie halfway between two codes, at many magnitudes and odd scales."""
+    rng = np.random.default_rng(dim)
+    x = rng.integers(-255, 256, (512, 2, dim)) * 2.0 ** rng.integers(-20, 8, (512, 2, 1))
+    x[::3] = np.round(x[::3] / 2) * 2 + 1  # odd multiples of half a step
+    x[::4, :, ::32] = 31.75 * 2.0 ** rng.integers(-6, 6, (128, 2, 1))
+    rows = torch.from_numpy(x.astype(np.float32)).bfloat16()
+    cache = make_cache(fmt, dim, 2, 16, 33)
+    slots = torch.arange(512, dtype=torch.int32, device="cuda") + 16
+    moe.kv_append(cache, rows.cuda(), rows.cuda(), slots)
+    ko, vo = (torch.empty((512, 2, dim), dtype=torch.float32, device="cuda") for _ in range(2))
+    moe.kv_read(cache, slots, ko, vo)
+    want = spec_ref.quantise(f64(rows), fmt)[3].astype(np.float32).astype(np.float64)
+    assert np.array_equal(f64(ko), want) and np.array_equal(f64(vo), want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("off", [16, 8, 1])
+def test_append_of_rows_at_any_boundary(fmt, dim, off):
+    """Rows on 32-byte, 16-byte and 2-byte boundaries give the same bytes."""
+    rng = np.random.default_rng(off)
+    k, v = bf16_rows(rng, (45, 3, dim)).cuda(), bf16_rows(rng, (45, 3, dim)).cuda()
+    slots = torch.from_numpy(rng.permutation(96)[:45].astype(np.int32)).cuda()
+    want, got = make_cache(fmt, dim, 3, 48, 2), make_cache(fmt, dim, 3, 48, 2)
+    moe.kv_append(want, k, v, slots)
+    wide = torch.zeros((45, 3, dim + off), dtype=torch.bfloat16, device="cuda")
+    wide[:, :, off:] = k
+    moe.kv_append(got, wide[:, :, off:], v, slots)
+    assert torch.equal(want.pages, got.pages)
+
+
 def test_slots_outside_the_cache():
     cache = make_cache(moe.MOE_KV_Q8, 64, 2, 16, 2)
     x = torch.randn((4, 2, 64), device="cuda").bfloat16()
@@ -259,6 +293,19 @@ def test_many_sequences():
     ctx = [int(c) for c in rng.integers(0, 400, 200)]
     s = Sequences(moe.MOE_KV_Q8, 64, 2, 2, 16, ctx, [int(n) for n in rng.integers(0, 4, 200)], 9, "tree")
     s.check(s.run())
+
+
+@pytest.mark.parametrize("fmt,dim,group,nodes", [(moe.MOE_KV_Q8, 128, 4, 1), (moe.MOE_KV_Q8, 64, 2, 12),
+                                                 (moe.MOE_KV_Q4, 128, 8, 20), (moe.MOE_KV_Q8, 256, 1, 3)])
+@pytest.mark.parametrize("order", ["short first", "long first", "among"])
+def test_short_items_beside_long_ones(fmt, dim, group, nodes, order):
+    """Runs that begin and end in the part of an item's cost that is no unit, empty runs, items of one unit."""
+    ctx = [0, 1, 3, 20, 0, 7] * 12
+    ctx = {"short first": ctx + [9000], "long first": [9000] + ctx, "among": ctx[:30] + [9000, 0, 5000] + ctx[30:]}[order]
+    s = Sequences(fmt, dim, 2, group, 64, ctx, [nodes if i % 5 else 0 for i in range(len(ctx))], dim + nodes, "tree")
+    out = s.run()
+    s.check(out)
+    assert torch.equal(out, s.run())
 
 
 @pytest.mark.parametrize("k_scale", [0.0, 40.0, 3000.0])

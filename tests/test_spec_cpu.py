@@ -39,6 +39,18 @@ def test_page_bytes(fmt, dim):
         moe.KvCache(torch.empty(moe.kv_page_bytes(c) + 1, dtype=torch.uint8), dim, 3, 48, fmt)
 
 
+def test_pages_set_later_are_counted():
+    c = moe.KvCache(None, 64, 2, 16)
+    per = moe.kv_page_bytes(c)
+    assert c.n_pages == 0
+    for n in (5, 2):
+        c.pages = torch.empty(n * per, dtype=torch.uint8)
+        assert c.n_pages == n and c.ref()._obj.n_pages == n
+    c.pages = torch.empty(per + 1, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="not a multiple"):
+        c.ref()
+
+
 @pytest.mark.parametrize("field,value,code,text", [
     ("head_dim", 96, -2, "head_dim"), ("head_dim", 0, -1, "head_dim"), ("n_kv_heads", 0, -1, "n_kv_heads"),
     ("n_kv_heads", 257, -2, "n_kv_heads"), ("page_size", 24, -2, "page_size"), ("page_size", 2048, -2, "page_size"),
