@@ -137,14 +137,11 @@ std::mutex g_tree_mu;
 int tree_choose(int fmt, int dim, int rows)
 {
     const int mt = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;
-    if (dim == 256)
-        return fmt == MOE_KV_Q8 ? 5 : 10;
-    if (fmt == MOE_KV_Q8)
-        return dim == 64 ? mt : 3 + std::min(mt, 1);
-    return dim == 64 ? 6 + mt : 9;
+    const int first = dim == 64 ? 0 : dim == 128 ? 3 : 5, most = dim == 64 ? 2 : dim == 128 ? 1 : 0;
+    return (fmt == MOE_KV_Q8 ? 0 : 6) + first + std::min(mt, most);
 }
 
-#define MOE_TREE_INSTANCES 11
+#define MOE_TREE_INSTANCES 12
 
 // the tensor-core kernels' instances, by format
 struct TtcInstance {
@@ -180,7 +177,7 @@ int tree_device(TreeDevice **out)
             tree_instance<MOE_KV_Q8, 64, 1>(),  tree_instance<MOE_KV_Q8, 64, 2>(),  tree_instance<MOE_KV_Q8, 64, 4>(),
             tree_instance<MOE_KV_Q8, 128, 1>(), tree_instance<MOE_KV_Q8, 128, 2>(), tree_instance<MOE_KV_Q8, 256, 1>(),
             tree_instance<MOE_KV_Q4, 64, 1>(),  tree_instance<MOE_KV_Q4, 64, 2>(),  tree_instance<MOE_KV_Q4, 64, 4>(),
-            tree_instance<MOE_KV_Q4, 128, 1>(), tree_instance<MOE_KV_Q4, 256, 1>()};
+            tree_instance<MOE_KV_Q4, 128, 1>(), tree_instance<MOE_KV_Q4, 128, 2>(), tree_instance<MOE_KV_Q4, 256, 1>()};
         int n = 0, per_sm = 0, optin = 0;
         SPEC_CUDA_OK(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d));
         SPEC_CUDA_OK(cudaDeviceGetAttribute(&per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, d));
@@ -415,10 +412,10 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     if ((rc = tree_device(&dev)))
         return rc;
     const int rows = (n_tokens + batch - 1) / batch * a.group;
-    // The tensor-core kernel from where the warps' own products cost more than its longer steps: 8-bit caches above
-    // 32 rows (64 sequences of 12000 tokens: 32 rows 378 us by warps, 582 us by it; 16 of 4000: 64 rows 176 and 79 us),
-    // 4-bit ones, whose codes cost a warp more a byte, above 16 (16 of up to 16000: 32 rows 143 and 112 us)
-    if (a.k.dim == 128 && rows > (a.k.fmt == MOE_KV_Q8 ? 32 : 16)) {
+    // The tensor-core kernel from where the warps' own products cost more than its longer steps (64 sequences of 12000
+    // tokens, Q8, 32 rows: 385 us by warps, 582 us by it; 16 of up to 16000, Q4, 32 rows: 89 and 112 us; 16 of 4000, 48
+    // rows in Q8 84 and 68 us, 64 in Q4 92 and 67 us)
+    if (a.k.dim == 128 && rows > 32) {
         const TtcInstance &t = dev->tc[a.k.fmt == MOE_KV_Q8 ? 0 : 1];
         const size_t used = t.fixed + 12 * ((size_t)batch + 1);
         const int stages = (int)std::min<size_t>(4, (dev->optin - used) / t.stage);

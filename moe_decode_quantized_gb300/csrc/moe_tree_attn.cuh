@@ -194,7 +194,8 @@ __device__ __forceinline__ void tree_zero(const TreeArgs &a, int first, int rows
 // sequences, one without a context, 20 rows a head: 90 us without, 74, 52, 46,
 // 45 with a cost of 8, 16, 24, 32; 64 sequences of 1 to 300 tokens 47 and 22 us;
 // 64 of 4000 to 24000 275, with 32 278; the tensor-core kernel's tiles of 128
-// tokens: 120 us without, 112 with 2, 117 with 6). cum [batch + 1] and items [batch + 1] are the units and the items before each
+// tokens, 64 trees of up to 16 rows over 1 to 2000: 106 us without, 92 with 2, 96
+// with 6). cum [batch + 1] and items [batch + 1] are the units and the items before each
 // sequence; a place in the list of costs is turned into a unit by tree_place.
 
 // one item: the units [lo, lo + units) of the list

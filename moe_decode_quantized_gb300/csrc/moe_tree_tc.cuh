@@ -1,4 +1,4 @@
-// moe_tree_tc.cuh -- tree attention for more than 16 query rows a kv head, on
+// moe_tree_tc.cuh -- tree attention for more than 32 query rows a kv head, on
 // the 5th-generation tensor cores: the same sums, list of work and partials
 // as moe_tree_attn.cuh, in tiles of 128 tokens and up to 128 rows an M tile.
 //
@@ -21,8 +21,8 @@
 // issues the products.
 //
 // 61 rows of 8 heads over 100003 tokens take 118 us, 850 TFLOP/s of products
-// (43 % of the measured peak), 16 trees of up to 8 rows of 4 heads over up to
-// 16000 tokens in Q4 112 us. A tile of two M tiles takes some 4400 clocks: the
+// (43 % of the measured peak), 16 chains of 16 rows of 4 heads over 4000 tokens
+// 68 us. A tile of two M tiles takes some 4400 clocks: the
 // products 3300, in order and waiting once a tile for the K that takes the last
 // one's place, beside a softmax of 1950 clocks an M tile. Tiles of one M tile
 // take 3000 to 3300, bound by the turning of codes, which no more rows share. A
