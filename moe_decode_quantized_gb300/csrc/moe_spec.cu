@@ -199,31 +199,36 @@ int tree_device(TreeDevice **out)
     return MOE_OK;
 }
 
-// the second kernel of a call: a CTA a run and 16 rows of its row block. items:
-// about how many there are; the runs that each spans decide on the instance
-// (one sequence of 8000 tokens, 8 items of 57 parts: 37 us with the small one,
-// 24 with the large; 512 items: 288 and 281 us the other way round)
+// The second kernel of a call. items: about how many there are; the runs that
+// each may span decide on the instance (one sequence of 8000 tokens, 8 items of
+// 57 parts: 23 us with the small one, 17 with the large; 2 items of 228: 66 and
+// 34; 8 of 5 parts: 11.6 and 12.1; two row blocks of 4 heads over 152 runs: 118
+// and 120, 16 items over 152 runs: 28 and 33). The large one's CTAs, four an SM,
+// go through several runs each.
+using JoinKernel = void (*)(TreeArgs, int, int);
+
 template <int D>
-TreeKernel join_kernel(bool deep)
+JoinKernel join_kernel(bool deep)
 {
-    return deep ? moe_tree_join_kernel<D, 512, 16> : moe_tree_join_kernel<D, 256, D == 64 ? 2 : 4>;
+    return deep ? moe_tree_join_kernel<D, 256, 8, 8> : moe_tree_join_kernel<D, 256, D / 4, D == 64 ? 2 : 4>;
 }
 
-int tree_join(const TreeArgs &a, int grid, int rows, long long items, cudaStream_t s)
+int tree_join(const TreeArgs &a, const TreeDevice &dev, int runs, int rows, long long items, cudaStream_t s)
 {
-    const bool deep = grid / items >= 8;
+    const bool deep = runs / items >= 24;
+    const int blocks = rows / MOE_TREE_JOIN_ROWS, slices = deep ? a.k.dim / 32 : 1;
     cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3(grid, rows / MOE_TREE_JOIN_ROWS);
-    lc.blockDim = dim3(deep ? 512 : 256);
+    lc.gridDim = dim3(deep ? std::max(1, std::min(runs, 4 * dev.sms / (blocks * slices))) : runs, blocks, slices);
+    lc.blockDim = dim3(256);
     lc.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = at;
     lc.numAttrs = 1;
-    const TreeKernel kernel = a.k.dim == 64 ? join_kernel<64>(deep) : a.k.dim == 128 ? join_kernel<128>(deep)
+    const JoinKernel kernel = a.k.dim == 64 ? join_kernel<64>(deep) : a.k.dim == 128 ? join_kernel<128>(deep)
                                                                                       : join_kernel<256>(deep);
-    SPEC_CUDA_OK(cudaLaunchKernelEx(&lc, kernel, a, rows));
+    SPEC_CUDA_OK(cudaLaunchKernelEx(&lc, kernel, a, rows, runs));
     return MOE_OK;
 }
 
@@ -423,7 +428,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
         const int grid = std::min(dev->sms, MOE_TTC_MAX_GRID);
         t.kernel<<<grid, MOE_TTC_THREADS, used + stages * t.stage, (cudaStream_t)stream>>>(a, stages);
         SPEC_CUDA_OK(cudaGetLastError());
-        return tree_join(a, grid, MOE_TTC_ROWS, (long long)batch * a.k.heads * ((rows + MOE_TTC_ROWS - 1) / MOE_TTC_ROWS),
+        return tree_join(a, *dev, grid, MOE_TTC_ROWS, (long long)batch * a.k.heads * ((rows + MOE_TTC_ROWS - 1) / MOE_TTC_ROWS),
                          (cudaStream_t)stream);
     }
     const TreeInstance &t = dev->inst[tree_choose(a.k.fmt, a.k.dim, rows)];
@@ -442,7 +447,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     const int grid = std::min(dev->sms * ctas, MOE_TREE_MAX_GRID);
     t.kernel<<<grid, MOE_TREE_THREADS, used + stages * t.stage, (cudaStream_t)stream>>>(a, stages);
     SPEC_CUDA_OK(cudaGetLastError());
-    return tree_join(a, grid, t.rows, (long long)batch * a.k.heads * ((rows + t.rows - 1) / t.rows), (cudaStream_t)stream);
+    return tree_join(a, *dev, grid, t.rows, (long long)batch * a.k.heads * ((rows + t.rows - 1) / t.rows), (cudaStream_t)stream);
 }
 
 int moe_spec_verify_workspace_bytes(int batch, int n_rows, size_t *bytes)

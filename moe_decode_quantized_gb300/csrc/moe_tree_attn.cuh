@@ -434,105 +434,147 @@ __device__ __forceinline__ void tree_cut(const TreeArgs &a, const TreeItem &it, 
 #define MOE_TREE_JOIN_ROWS 16
 #define MOE_TREE_JOIN_PARTS 128  // whose weights are held at once
 
-// Joins the partials of cut items: CTA (run, 16 rows of the row block), with
-// LOADS loads of 16 bytes in flight a thread. Bound by latency: a round of
-// loads for the weights, then one for each LOADS (or so) parts. Two instances
-// are used: small ones that all fit beside one another where the items are
-// many and of few parts (a run's end each), and large ones for few items of
-// many parts.
-template <int D, int NT, int LOADS>
-__global__ void __launch_bounds__(NT) moe_tree_join_kernel(const __grid_constant__ TreeArgs a, const int rows)
+// Joins the partials of cut items: CTA (runs, 16 rows of the row block, CS
+// pieces of four dimensions), LOADS loads of 16 bytes in flight a thread. Where
+// an item has fewer (row, piece)s than the CTA threads, groups of threads take
+// its parts in turn and are added in order. Bound by latency: a round of loads
+// for the weights, then one for each LOADS parts of a group. Two instances are
+// used: small ones, whose CTAs take all dimensions, where the items are many and
+// of few parts (a run's end each), and large ones for few items of many parts.
+template <int D, int NT, int CS, int LOADS>
+__global__ void __launch_bounds__(NT) moe_tree_join_kernel(const __grid_constant__ TreeArgs a, const int rows, const int runs)
 {
-    constexpr int R = MOE_TREE_JOIN_ROWS, P = MOE_TREE_JOIN_PARTS;
-    constexpr int COLS = D / 4, PER = COLS * R > NT ? COLS * R / NT : 1;  // a thread: four dimensions of a row, PER times
+    constexpr int R = MOE_TREE_JOIN_ROWS, P = MOE_TREE_JOIN_PARTS, J = P / 32;
+    constexpr int PER = CS * R > NT ? CS * R / NT : 1, U = LOADS / PER;  // (row, piece)s of a thread; parts at once
     __shared__ float weight[P][R], top[R], sum[R];
+    __shared__ float4 group_sum[NT];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_wait();
-    const TreeCut c = a.cuts[blockIdx.x];
-    const int r0 = blockIdx.y * R, live = min(R, c.n * a.group - c.block * rows - r0);
-    if (c.runs == 0 || live <= 0)
-        return;
-    // part i: of the first run the second slot, unless the item begins with the run
+    const int r0 = blockIdx.y * R, first_piece = blockIdx.z * CS;
     const size_t size = (size_t)rows * (D + 2);
-    const float *base = a.part + (size_t)blockIdx.x * 2 * size;
-    auto part = [&](int i) { return base + (i == 0 && !c.whole_run ? size : 2 * i * size); };
-    for (int r = warp; r < live; r += NT / 32) {
-        float m = -INFINITY, l = 0.0f;
-        for (int i = lane; i <= c.runs; i += 32)
-            m = fmaxf(m, part(i)[rows * D + r0 + r]);
+    pdl_wait();
+    for (int begin = blockIdx.x; begin < runs; begin += 32 * gridDim.x) {
+        const int look = begin + lane * gridDim.x;  // every warp looks at the same 32 runs
+        uint32_t found = gridDim.x >= runs ? 1u : __ballot_sync(0xFFFFFFFFu, look < runs && a.cuts[min(look, runs - 1)].runs != 0);
+        for (; found; found &= found - 1) {
+            const int at = begin + (__ffs(found) - 1) * gridDim.x;
+            const TreeCut c = a.cuts[at];
+            const int live = min(R, c.n * a.group - c.block * rows - r0);
+            if (c.runs == 0 || live <= 0)
+                continue;
+            // part i: of the first run the second slot, unless the item begins with the run
+            const float *base = a.part + (size_t)at * 2 * size;
+            auto part = [&](int i) { return base + (i == 0 && !c.whole_run ? size : 2 * i * size); };
+            __syncthreads();  // the last item's numbers have been read
+            for (int r = warp; r < live; r += NT / 32) {
+                float v[J], s[J], m = -INFINITY, l = 0.0f;
 #pragma unroll
-        for (int x = 16; x; x /= 2)
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-        for (int i = lane; i <= c.runs; i += 32) {
-            const float v = part(i)[rows * D + r0 + r], f = v == -INFINITY ? 1.0f : ex2(v - m);  // a NaN sum stays
-            l += part(i)[rows * (D + 1) + r0 + r] * f;
-            if (i < P)
-                weight[i][r] = f;
-        }
-        l = warp_sum(l);
-        if (lane == 0) {
-            top[r] = m;
-            sum[r] = l;
-        }
-    }
-    __syncthreads();
-    float4 o[PER];
-#pragma unroll
-    for (int k = 0; k < PER; ++k)
-        o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int r = tid % R, c1 = tid / R;  // pieces of four dimensions c1, c1 + NT / R, .. of row r
-    const bool mine = r < live && c1 < COLS;
-    for (int p0 = 0; p0 <= c.runs; p0 += P) {
-        const int n = min(P, c.runs + 1 - p0);
-        if (p0 > 0) {  // the next weights
-            __syncthreads();
-            for (int x = tid; x < n * R; x += NT)
-                if (x % R < live) {
-                    const float v = part(p0 + x / R)[rows * D + r0 + x % R];
-                    weight[x / R][x % R] = v == -INFINITY ? 1.0f : ex2(v - top[x % R]);
+                for (int j = 0; j < J; ++j) {
+                    const bool there = lane + 32 * j <= c.runs;
+                    v[j] = there ? part(lane + 32 * j)[rows * D + r0 + r] : -INFINITY;
+                    s[j] = there ? part(lane + 32 * j)[rows * (D + 1) + r0 + r] : 0.0f;
                 }
-            __syncthreads();
-        }
-        constexpr int U = LOADS / PER;
-        for (int i0 = 0; i0 < n && mine; i0 += U) {
-            float4 v[U][PER];
 #pragma unroll
-            for (int i = 0; i < U; ++i)
+                for (int j = 0; j < J; ++j)
+                    m = fmaxf(m, v[j]);
+                for (int i = lane + P; i <= c.runs; i += 32)
+                    m = fmaxf(m, part(i)[rows * D + r0 + r]);
 #pragma unroll
-                for (int k = 0; k < PER; ++k)
-                    v[i][k] = i0 + i < n ? reinterpret_cast<const float4 *>(part(p0 + i0 + i))[(c1 + k * (NT / R)) * rows + r0 + r]
-                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int x = 16; x; x /= 2)
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+                auto factor = [&](float v) { return v == -INFINITY ? 1.0f : ex2(v - m); };  // a NaN sum stays
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const float f = i0 + i < n ? weight[i0 + i][r] : 0.0f;
-#pragma unroll
-                for (int k = 0; k < PER; ++k) {
-                    o[k].x = fmaf(v[i][k].x, f, o[k].x);
-                    o[k].y = fmaf(v[i][k].y, f, o[k].y);
-                    o[k].z = fmaf(v[i][k].z, f, o[k].z);
-                    o[k].w = fmaf(v[i][k].w, f, o[k].w);
+                for (int j = 0; j < J; ++j) {
+                    const float f = factor(v[j]);
+                    l += s[j] * f;
+                    weight[lane + 32 * j][r] = f;
+                }
+                for (int i = lane + P; i <= c.runs; i += 32)
+                    l += part(i)[rows * (D + 1) + r0 + r] * factor(part(i)[rows * D + r0 + r]);
+                l = warp_sum(l);
+                if (lane == 0) {
+                    top[r] = m;
+                    sum[r] = l;
                 }
             }
-        }
-    }
-    if (!mine)
-        return;
-    const int rr = c.block * rows + r0 + r;
-    const float inv = sum[r] == 0.0f ? 0.0f : 1.0f / sum[r];
-    uint16_t *row = a.out + (c.first + rr / a.group) * a.o_tok + (c.head * a.group + rr % a.group) * a.o_head;
+            __syncthreads();
+            float4 o[PER];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        uint16_t *to = row + (c1 + k * (NT / R)) * 4;
-        const __nv_bfloat162 x = __floats2bfloat162_rn(o[k].x * inv, o[k].y * inv);
-        const __nv_bfloat162 y = __floats2bfloat162_rn(o[k].z * inv, o[k].w * inv);
-        const uint32_t w0 = *reinterpret_cast<const uint32_t *>(&x), w1 = *reinterpret_cast<const uint32_t *>(&y);
-        if (a.o_wide) {
-            *reinterpret_cast<uint2 *>(to) = make_uint2(w0, w1);
-        } else {
-            to[0] = (uint16_t)w0;
-            to[1] = (uint16_t)(w0 >> 16);
-            to[2] = (uint16_t)w1;
-            to[3] = (uint16_t)(w1 >> 16);
+            for (int k = 0; k < PER; ++k)
+                o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const int pairs = live * CS, groups = max(1, NT / pairs), group = groups > 1 ? tid / pairs : 0;
+            const int x0 = tid - group * pairs;  // pairs x0, x0 + NT, ..: row x % live, piece first_piece + x / live
+            int row[PER], place[PER];
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int x = group < groups && x0 + k * NT < pairs ? x0 + k * NT : -1;
+                row[k] = x < 0 ? -1 : x % live;
+                place[k] = x < 0 ? 0 : (first_piece + x / live) * rows + r0 + row[k];
+            }
+            for (int p0 = 0; p0 <= c.runs; p0 += P) {
+                const int n = min(P, c.runs + 1 - p0);
+                if (p0 > 0) {  // the next weights
+                    __syncthreads();
+                    for (int x = tid; x < n * R; x += NT)
+                        if (x % R < live) {
+                            const float v = part(p0 + x / R)[rows * D + r0 + x % R];
+                            weight[x / R][x % R] = v == -INFINITY ? 1.0f : ex2(v - top[x % R]);
+                        }
+                    __syncthreads();
+                }
+                for (int i0 = group; i0 < n && row[0] >= 0; i0 += groups * U) {
+                    float4 v[U][PER];
+#pragma unroll
+                    for (int i = 0; i < U; ++i)
+#pragma unroll
+                        for (int k = 0; k < PER; ++k) {
+                            const int p = i0 + i * groups;
+                            v[i][k] = p < n && row[k] >= 0 ? reinterpret_cast<const float4 *>(part(p0 + p))[place[k]]
+                                                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        }
+#pragma unroll
+                    for (int i = 0; i < U; ++i)
+#pragma unroll
+                        for (int k = 0; k < PER; ++k) {
+                            const int p = i0 + i * groups;
+                            const float f = p < n && row[k] >= 0 ? weight[p][row[k]] : 0.0f;
+                            o[k].x = fmaf(v[i][k].x, f, o[k].x);
+                            o[k].y = fmaf(v[i][k].y, f, o[k].y);
+                            o[k].z = fmaf(v[i][k].z, f, o[k].z);
+                            o[k].w = fmaf(v[i][k].w, f, o[k].w);
+                        }
+                }
+            }
+            if (groups > 1) {
+                group_sum[tid] = o[0];
+                __syncthreads();
+                for (int g = 1; g < groups && group == 0; ++g) {  // (group 0: x0 < pairs)
+                    const float4 v = group_sum[g * pairs + x0];
+                    o[0].x += v.x;
+                    o[0].y += v.y;
+                    o[0].z += v.z;
+                    o[0].w += v.w;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                if (group > 0 || row[k] < 0)
+                    continue;
+                const int rr = c.block * rows + r0 + row[k];
+                const float inv = sum[row[k]] == 0.0f ? 0.0f : 1.0f / sum[row[k]];
+                uint16_t *to = a.out + (c.first + rr / a.group) * a.o_tok + (c.head * a.group + rr % a.group) * a.o_head +
+                               (first_piece + (x0 + k * NT) / live) * 4;
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(o[k].x * inv, o[k].y * inv);
+                const __nv_bfloat162 hi = __floats2bfloat162_rn(o[k].z * inv, o[k].w * inv);
+                const uint32_t w0 = *reinterpret_cast<const uint32_t *>(&lo), w1 = *reinterpret_cast<const uint32_t *>(&hi);
+                if (a.o_wide) {
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(w0, w1);
+                } else {
+                    to[0] = (uint16_t)w0;
+                    to[1] = (uint16_t)(w0 >> 16);
+                    to[2] = (uint16_t)w1;
+                    to[3] = (uint16_t)(w1 >> 16);
+                }
+            }
         }
     }
 }
