@@ -308,6 +308,15 @@ def test_short_items_beside_long_ones(fmt, dim, group, nodes, order):
     assert torch.equal(out, s.run())
 
 
+@pytest.mark.parametrize("fmt,dim,group,nodes", [(moe.MOE_KV_Q8, 128, 2, 1), (moe.MOE_KV_Q8, 128, 64, 2),
+                                                 (moe.MOE_KV_Q4, 128, 16, 4), (moe.MOE_KV_Q4, 256, 1, 2),
+                                                 (moe.MOE_KV_Q8, 64, 16, 3)])
+def test_the_largest_batch(fmt, dim, group, nodes):
+    rng = np.random.default_rng(nodes)
+    s = Sequences(fmt, dim, 1, group, 16, [int(c) for c in rng.integers(0, 60, 1024)], [nodes] * 1024, dim + nodes, "tree")
+    s.check(s.run(), set(rng.integers(0, 1024, 40).tolist()) | {0, 1023})
+
+
 @pytest.mark.parametrize("k_scale", [0.0, 40.0, 3000.0])
 def test_large_and_equal_scores(k_scale):
     """Weights that are all alike, and scores of hundreds and thousands, where one token takes the whole weight."""
