@@ -309,9 +309,10 @@ __device__ __forceinline__ void tree_list(const TreeArgs &a, long long *cum, int
     __syncthreads();
     const long long total = cum[a.batch] + (long long)COST * items[a.batch];
     run = max(tree_div(total + gridDim.x - 1, gridDim.x), (long long)a.min_units);
-    const long long w = run * blockIdx.x;
-    lo = w < total ? tree_place<ROWS, TOKENS, COST>(a, cum, items, w) : cum[a.batch];
-    hi = w + run < total ? tree_place<ROWS, TOKENS, COST>(a, cum, items, w + run) : cum[a.batch];
+    const long long w = run * blockIdx.x + (lane & 1 ? run : 0);  // even lanes the begin, odd ones the end
+    const long long place = w < total ? tree_place<ROWS, TOKENS, COST>(a, cum, items, w) : cum[a.batch];
+    lo = __shfl_sync(0xFFFFFFFFu, place, 0);
+    hi = __shfl_sync(0xFFFFFFFFu, place, 1);
 }
 
 // the item after `it` in the list (there is one)
