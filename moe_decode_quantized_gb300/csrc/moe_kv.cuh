@@ -278,6 +278,7 @@ template <int FMT, int D, int ALIGN>
 __global__ void __launch_bounds__(MOE_KV_THREADS) moe_kv_append_kernel(const KvArgs a)
 {
     constexpr int PIECES = D / kv_append_values<D, ALIGN>();
+    pdl_wait();
     const int lane = threadIdx.x & 31, head = blockIdx.y >> 1;
     const int token = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kv_append_tokens<D, ALIGN>() +
                       lane / PIECES;
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(MOE_KV_THREADS) moe_kv_read_kernel(const KvArg
     constexpr int NK = kv_read_threads<FMT, D, false>(), NV = kv_read_threads<FMT, D, true>();
     const int head = blockIdx.y >> 1;
     const int lane = threadIdx.x & 31;
+    pdl_wait();
     if ((blockIdx.y & 1) == 0) {
         const int tile = blockIdx.x * (MOE_KV_THREADS / NK) + threadIdx.x / NK;
         kv_read_piece<FMT, D, false, F32, WIDE>(a, tile * 8 + kv_tile_token(false, lane, 0), head, lane,

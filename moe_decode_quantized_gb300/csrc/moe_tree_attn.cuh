@@ -604,6 +604,7 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
         fence_barrier_init();
     }
     long long lo, hi, run;
+    pdl_wait();
     tree_list<D, T::ROWS, MOE_KV_BLOCK, MOE_TREE_COST, MOE_TREE_THREADS>(a, cum, items, scan, count, lo, hi, run);
     pdl_launch_dependents();
     if (lo >= hi) {

@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
         }
         fence_barrier_init();
     }
+    pdl_wait();  // before tensor memory is taken: the last kernel may still need it
     if (warp == 0)
         tmem_alloc(tmem_slot, 512);
     long long lo, hi, run;

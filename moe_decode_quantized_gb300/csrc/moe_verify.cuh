@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(MOE_VERIFY_STAT_THREADS) moe_verify_rows_kerne
     constexpr int NT = MOE_VERIFY_STAT_THREADS, NW = NT / 32;
     __shared__ VerifySlice warps[NW];
     __shared__ int seq;
-    pdl_launch_dependents();
+    pdl_wait();
+    pdl_launch_dependents();  // (after the wait: the walk reads the inputs before it waits for the rows)
     const int row = blockIdx.x / a.splits, part = blockIdx.x % a.splits;
     const int lo = min(part * a.split, a.vocab), hi = min(lo + a.split, a.vocab);
     using View = VerifyView<F32, WIDE, NT>;
@@ -326,6 +327,8 @@ __global__ void __launch_bounds__(MOE_VERIFY_THREADS, 3) moe_verify_kernel(const
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
     const int b = blockIdx.x / ranks;
+    if constexpr (!AHEAD)
+        pdl_wait();
     const int first = a.q_start[b], n = a.q_start[b + 1] - first;
     if (first < 0 || n < 1 || n > MOE_MAX_DRAFT || first > a.rows - n) {  // the whole cluster
         if (rank == 0 && tid == 0) {
