@@ -20,7 +20,7 @@
 // products, the weights as the A fragments of o += P V. 16 rows cost 64 such
 // products a unit of 128 dimensions, and 598 TFLOP/s of them were measured:
 // bound by the copies while the rows are few (64 sequences of 4000 to 24000
-// tokens, one row of 4 heads: 276 us, 93 % of the copy rate), by the turning of
+// tokens, one row of 4 heads: 271 us, 95 % of the copy rate), by the turning of
 // codes and the products from some 16 rows on (64 of 12000, 32 rows: 378 us, 67
 // %), by latency for short contexts (one sequence of 511 tokens: 11 us, of which
 // the second kernel is 3).
