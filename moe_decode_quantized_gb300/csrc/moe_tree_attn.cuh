@@ -12,18 +12,17 @@
 // into runs of equal cost, one a CTA, so ragged lengths cost nothing; a run that cuts
 // an item leaves a partial (o, m, l) in the workspace, and a second kernel,
 // launched behind the first so that it starts the moment that one ends, joins
-// the partials of each cut item in the order of the runs.
+// the partials of each cut item in a fixed order.
 //
 // A warp takes every fourth unit of its CTA's run through a ring of its own
 // (one bulk copy a unit), and everything stays in registers: codes to f16 B
 // fragments (the cache's byte order is the fragments'), S = Q K^T by 16x8x16
-// products, the weights as the A fragments of o += P V. 16 rows cost 64 such
+// products, the weights as the A fragments of o += P V. 16 rows cost 32 such
 // products a unit of 128 dimensions, and 598 TFLOP/s of them were measured:
 // bound by the copies while the rows are few (64 sequences of 4000 to 24000
 // tokens, one row of 4 heads: 271 us, 95 % of the copy rate), by the turning of
 // codes and the products from some 16 rows on (64 of 12000, 32 rows: 378 us, 67
-// %), by latency for short contexts (one sequence of 511 tokens: 11 us, of which
-// the second kernel is 3).
+// %), by latency for short contexts (one sequence of 511 tokens: 11.5 us).
 #pragma once
 #include "moe_kv.cuh"
 
