@@ -107,6 +107,9 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// the two halves of a barrier that orders no memory: every CTA of the cluster has started
+__device__ __forceinline__ void cluster_started_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_started_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st_cluster(const void *p, uint32_t rank, uint32_t v)
 {
     uint32_t at;
@@ -339,6 +342,7 @@ __global__ void __launch_bounds__(MOE_VERIFY_THREADS, 3) moe_verify_kernel(const
         }
         return;
     }
+    cluster_started_arrive();
     bool greedy;
     const float c = verify_scale(a, b, greedy);
     const int lo = min((int)rank * a.slice, a.vocab), hi = min(lo + a.slice, a.vocab);
@@ -361,7 +365,11 @@ __global__ void __launch_bounds__(MOE_VERIFY_THREADS, 3) moe_verify_kernel(const
         }
     }
 
-    // all slices' results to all CTAs of the cluster: one barrier, buffers in turn
+    // A CTA's shared memory may be written once the CTA has started: a barrier of the whole cluster before the first
+    // exchange (one that returned above did so with its whole cluster, and takes no part).
+    cluster_started_wait();
+    // All slices' results to all CTAs of the cluster: one barrier, buffers in turn. A buffer is written again two
+    // exchanges later, behind the barrier between, at which every CTA arrives after its last read of it.
     int turn = 0;
     auto exchange = [&](VerifySlice v, bool row) -> const VerifySlice * {
         v = warp_slice(v, row, c);

@@ -1,0 +1,57 @@
+"""Edges of the speculative-decoding operators on the GPU, beside test_gpu_spec.py: what
+clusters, waits, extreme scales and values, hidden tokens and empty calls come to. The same
+plain 64-bit implementations (spec_ref.py) and, where nothing else is said, the same
+tolerances."""
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import moe_decode_quantized_gb300 as moe
+
+import spec_ref
+import test_gpu_spec as base
+
+pytestmark = pytest.mark.gpu
+
+
+def verify_rows(sizes, vocab, kind, shape, drafts, seed, temps=(0.7, 1.0)):
+    """A case of base.verify_case's form with the given numbers of rows."""
+    rng, pick = np.random.default_rng(seed), random.Random(seed)
+    rows, batch = sum(sizes), len(sizes)
+    logits = torch.from_numpy((rng.standard_normal((rows, vocab), dtype=np.float32) * 2.5))
+    logits = logits.bfloat16() if kind == "bf16" else logits
+    case = {"tokens": [], "parents": [] if shape == "tree" else None, "u": [], "logits": logits.cuda(),
+            "temp": [temps[b % len(temps)] for b in range(batch)], "noise": rng.exponential(size=(batch, vocab)) + 1e-12}
+    l, at, draft = logits.float().numpy(), 0, np.zeros((rows, vocab) if drafts else (1, 1), np.float32)
+    for b, n in enumerate(sizes):
+        parents = [-1] + [pick.randint(max(0, j - 3), j - 1) if shape == "tree" else j - 1 for j in range(1, n)]
+        tokens, t = [0], case["temp"][b] or 0.5
+        for j in range(1, n):
+            z = l[at + parents[j]] / np.float32(t) + rng.standard_normal(vocab, dtype=np.float32) * np.float32(0.5)
+            p = np.exp(z - z.max(), dtype=np.float32)
+            p /= p.sum()
+            if drafts:
+                draft[at + j] = p
+            tokens.append(min(int(np.searchsorted(np.cumsum(p, dtype=np.float64), rng.random())), vocab - 1))
+        case["tokens"].append(np.array(tokens))
+        case["u"].append(rng.random(n))
+        if shape == "tree":
+            case["parents"].append(np.array(parents))
+        at += n
+    case["draft"] = torch.from_numpy(draft).cuda() if drafts else None
+    return case
+
+
+@pytest.mark.parametrize("ranks", range(2, 9))
+@pytest.mark.parametrize("sizes,shape", [([5, 3, 7], "chain"), ([24] * 56, "tree")])
+def test_verify_clusters_of_short_slices(ranks, sizes, shape):
+    """Clusters of every size with the shortest slices, whose CTAs exchange their first results soonest after they
+    start: rows ahead (the chains) and rows as the walk reaches them (the trees: more than 20 MB of logits)."""
+    case = verify_rows(sizes, 2048 * ranks + 3, "f32", shape, shape == "chain", ranks)
+    status, _ = base.check_verify(case)
+    assert status == 0
+    want = base.verify(case)[:3]
+    for _ in range(3):
+        assert base.verify(case)[:3] == want
