@@ -21,7 +21,7 @@
 //    other. Only what is needed is read, which for a large tree is a small
 //    part, but a path of k nodes is k + 1 passes in turn.
 // Bound by the latency of the passes for one sequence (a chain of 3 drafts over
-// 32000: 6.6 us), by the reads for many (48 chains of 7 over 131072: 36 us, 157
+// 32000: 7.2 us), by the reads for many (48 chains of 7 over 131072: 38 us, 157
 // MB with the draft rows that the residuals take; 16 trees of 12 to 24 rows over
 // 100003 in f32: 18 us, bound by the passes in turn).
 #pragma once
@@ -260,7 +260,7 @@ __device__ __forceinline__ VerifySlice warp_slice(VerifySlice v, bool row, float
 }
 
 // All rows ahead: CTA (row, part). Bound by the reads (384 rows of 131072 in
-// bf16 are 101 MB: about 20 of the 36 us of such a call).
+// bf16 are 101 MB: about 20 of the 38 us of such a call).
 template <bool F32, bool WIDE>
 __global__ void __launch_bounds__(MOE_VERIFY_STAT_THREADS) moe_verify_rows_kernel(const VerifyArgs a)
 {
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(MOE_VERIFY_STAT_THREADS) moe_verify_rows_kerne
     __shared__ VerifySlice warps[NW];
     __shared__ int seq;
     pdl_wait();
-    pdl_launch_dependents();  // (after the wait: the walk reads the inputs before it waits for the rows)
+    pdl_launch_dependents();
     const int row = blockIdx.x / a.splits, part = blockIdx.x % a.splits;
     const int lo = min(part * a.split, a.vocab), hi = min(lo + a.split, a.vocab);
     using View = VerifyView<F32, WIDE, NT>;
@@ -330,8 +330,11 @@ __global__ void __launch_bounds__(MOE_VERIFY_THREADS, 3) moe_verify_kernel(const
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
     const int b = blockIdx.x / ranks;
-    if constexpr (!AHEAD)
-        pdl_wait();
+    // Before anything is read or written, the refusal below included: what earlier kernels wrote is promised to be
+    // seen only behind it, and a call of refused sequences alone would end beside its rows kernel without it. (With the
+    // tokens and drafts read ahead of it, a chain of 3 drafts over 32000 took 6.6 us, now 7.2, 48 chains over 131072
+    // 36.3 us, now 38.2.)
+    pdl_wait();
     const int first = a.q_start[b], n = a.q_start[b + 1] - first;
     if (first < 0 || n < 1 || n > MOE_MAX_DRAFT || first > a.rows - n) {  // the whole cluster
         if (rank == 0 && tid == 0) {
@@ -351,17 +354,18 @@ __global__ void __launch_bounds__(MOE_VERIFY_THREADS, 3) moe_verify_kernel(const
     using View = VerifyView<F32, WIDE, NT>;
     const View view{a, hi};
     auto weight = [&](float l, float top) { return verify_weight(l, top, c); };
-    if (tid < n) {
-        const int x = a.tokens[first + tid], up = a.parents ? a.parents[first + tid] : tid - 1;
+    // by the last warps, while the first ones bring the rows' results
+    if (const int i = tid - (NT - MOE_MAX_DRAFT); i >= 0 && i < n) {
+        const int x = a.tokens[first + i], up = a.parents ? a.parents[first + i] : i - 1;
         const bool in = x >= 0 && x < a.vocab;
-        if (tid > 0 && !in && rank == 0)
+        if (i > 0 && !in && rank == 0)
             atomicOr(a.ctrl + MOE_CTRL_STATUS, (uint32_t)MOE_WS_INDEX);
-        token[tid] = x;
-        parent[tid] = tid > 0 && in && up < tid ? up : -1;  // -1: never a candidate
-        uniform[tid] = a.uniforms && !greedy ? a.uniforms[first + tid] : 0.5f;
-        if (tid > 0 && in && up >= 0 && up < tid) {
-            draft_x[tid] = a.draft ? a.draft[(first + tid) * a.draft_stride + x] : 1.0f;
-            logit_x[tid] = View::clean(view.logit(first + up, x));
+        token[i] = x;
+        parent[i] = i > 0 && in && up < i ? up : -1;  // -1: never a candidate
+        uniform[i] = a.uniforms && !greedy ? a.uniforms[first + i] : 0.5f;
+        if (i > 0 && in && up >= 0 && up < i) {
+            draft_x[i] = a.draft ? a.draft[(first + i) * a.draft_stride + x] : 1.0f;
+            logit_x[i] = View::clean(view.logit(first + up, x));
         }
     }
 
@@ -395,7 +399,6 @@ __global__ void __launch_bounds__(MOE_VERIFY_THREADS, 3) moe_verify_kernel(const
     };
     // the rows' results ahead, a warp a row
     if constexpr (AHEAD) {
-        pdl_wait();
         for (int r = warp; r < n; r += NW) {
             VerifySlice v{-INFINITY, 0.0f, a.vocab};
             for (int k = lane; k < a.splits; k += 32) {

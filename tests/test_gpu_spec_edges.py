@@ -55,3 +55,22 @@ def test_verify_clusters_of_short_slices(ranks, sizes, shape):
     want = base.verify(case)[:3]
     for _ in range(3):
         assert base.verify(case)[:3] == want
+
+
+def test_verify_of_refused_sequences_is_over_before_the_next_kernel():
+    """Sequences of too many rows are refused at once, but the call ends only when its reads of the logits have: what
+    the stream writes over them next is not seen (NaN would be flagged)."""
+    rows, vocab = 70, 131072
+    logits = torch.zeros((2 * rows, vocab), device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    starts, tokens = torch.tensor([0, rows, 2 * rows], **i32), torch.zeros(2 * rows, **i32)
+    u, noise = torch.full((2 * rows,), 0.5, device="cuda"), torch.ones((2, vocab), device="cuda")
+    n_acc, nxt, path = torch.full((2,), 9, **i32), torch.full((2,), 9, **i32), torch.full((2 * rows,), 9, **i32)
+    ws = torch.empty(moe.spec_verify_workspace_bytes(2, 2 * rows), dtype=torch.uint8, device="cuda")
+    moe.workspace_init(ws)
+    for _ in range(20):
+        moe.spec_verify(logits, starts, tokens, None, None, None, u, noise, n_acc, path, nxt, ws)
+        logits.fill_(float("nan"))
+        assert moe.read_status(ws) == moe.MOE_WS_INDEX
+        assert n_acc.tolist() == [0, 0] and nxt.tolist() == [-1, -1]
+        logits.zero_()
