@@ -382,7 +382,9 @@ __device__ __forceinline__ float tree_row(const TreeArgs &a, bool live, int toke
         const float f0 = bf16_lo(x[i]) * up0 * up1 * sign, f1 = bf16_hi(x[i]) * up0 * up1 * sign;
         x[i] = odd ? 0x7E007E00u : pack_h2(f0, f1);
     }
-    return sign == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f / up0 / up1;
+    // not below 2^-126: there the exponents of all scores (below 2^38) vanish as they should, and -inf, of a token that
+    // is not seen, is not multiplied by 0
+    return sign == 0.0f ? 1.0f : fmaxf(fabsf(a.scale) * 1.4426950408889634f / up0 / up1, 1.17549435e-38f);
 }
 
 // writes a row block: o[mt][j] of this lane divided by the rows' sums

@@ -35,10 +35,10 @@ def verify_rows(sizes, vocab, kind, shape, drafts, seed, temps=(0.7, 1.0)):
             if drafts:
                 draft[at + j] = p
             tokens.append(min(int(np.searchsorted(np.cumsum(p, dtype=np.float64), rng.random())), vocab - 1))
-        case["tokens"].append(np.array(tokens))
+        case["tokens"].append(np.array(tokens[:n], dtype=np.int64))
         case["u"].append(rng.random(n))
         if shape == "tree":
-            case["parents"].append(np.array(parents))
+            case["parents"].append(np.array(parents[:n], dtype=np.int64))
         at += n
     case["draft"] = torch.from_numpy(draft).cuda() if drafts else None
     return case
@@ -74,3 +74,20 @@ def test_verify_of_refused_sequences_is_over_before_the_next_kernel():
         assert moe.read_status(ws) == moe.MOE_WS_INDEX
         assert n_acc.tolist() == [0, 0] and nxt.tolist() == [-1, -1]
         logits.zero_()
+
+
+# (format, head size, heads of a kv head, rows of a sequence): the warp kernel's instances, then the tensor-core kernel's
+# with one M tile and with two
+SHAPES = [(moe.MOE_KV_Q8, 64, 2, 3), (moe.MOE_KV_Q4, 64, 16, 4), (moe.MOE_KV_Q8, 128, 4, 1), (moe.MOE_KV_Q4, 128, 4, 8),
+          (moe.MOE_KV_Q8, 256, 1, 3), (moe.MOE_KV_Q4, 128, 8, 12), (moe.MOE_KV_Q8, 128, 8, 40)]
+
+
+@pytest.mark.parametrize("fmt,dim,group,rows", SHAPES)
+@pytest.mark.parametrize("scale", [1.0 / 32, 1.0 / 128, -1.0 / 128, 1e-38])
+def test_queries_of_subnormal_numbers(fmt, dim, group, rows, scale):
+    """Scores that vanish against 1, times a scale that takes their multiplier below f32: the mean of the seen values,
+    and masked tokens stay masked."""
+    s = base.Sequences(fmt, dim, 2, group, 16, [300, 20, 0], [rows, rows, rows], 31, "any")
+    s.scale = scale
+    s.q = (torch.randint(-1, 2, s.q.shape, device="cuda").float() * 2.0 ** -133).bfloat16()
+    s.check(s.run())
