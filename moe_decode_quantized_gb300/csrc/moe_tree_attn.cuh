@@ -382,9 +382,11 @@ __device__ __forceinline__ float tree_row(const TreeArgs &a, bool live, int toke
         const float f0 = bf16_lo(x[i]) * up0 * up1 * sign, f1 = bf16_hi(x[i]) * up0 * up1 * sign;
         x[i] = odd ? 0x7E007E00u : pack_h2(f0, f1);
     }
-    // not below 2^-126: there the exponents of all scores (below 2^38) vanish as they should, and -inf, of a token that
-    // is not seen, is not multiplied by 0
-    return sign == 0.0f ? 1.0f : fmaxf(fabsf(a.scale) * 1.4426950408889634f / up0 / up1, 1.17549435e-38f);
+    // Not below 2^-126: there the exponents of all scores (below 2^38) vanish as they should, and -inf, of a token that
+    // is not seen, is not multiplied by 0. Not above 2^88: the exponents stay finite, and scores that differ, by 2^-48
+    // at least (a product of two of f16's smallest numbers), still do by 2^40.
+    return sign == 0.0f ? 1.0f
+                        : fminf(fmaxf(fabsf(a.scale) * 1.4426950408889634f / up0 / up1, 1.17549435e-38f), 3.0948501e26f);
 }
 
 // writes a row block: o[mt][j] of this lane divided by the rows' sums
@@ -688,13 +690,15 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
 #pragma unroll
                 for (int ks = 0; ks < T::KS; ++ks)
                     qr[mt][ks] = qf[(mt * T::KS + ks) * 32 + lane];
-        float c[MT][2], m[MT][2], l[MT][2], o[MT][T::NB][4];
+        // z: minus the row's reference, as a score: where the scores' sums begin. So an exponent is the multiple of a
+        // difference, as exact as the scores however large they are. The bits 0: there is no reference yet.
+        float c[MT][2], z[MT][2], l[MT][2], o[MT][T::NB][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 c[mt][s] = cmul[mt * 16 + s * 8 + g];
-                m[mt][s] = -INFINITY;
+                z[mt][s] = 0.0f;
                 l[mt][s] = 0.0f;
             }
 #pragma unroll
@@ -722,7 +726,7 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
                 for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        s[mt][nb][i] = 0.0f;
+                        s[mt][nb][i] = z[mt][i / 2];
             {
                 uint32_t kw[2 * T::WK];
 #pragma unroll
@@ -789,8 +793,8 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
                     float v = fmaxf(fmaxf(s[mt][0][2 * r], s[mt][0][2 * r + 1]), fmaxf(s[mt][1][2 * r], s[mt][1][2 * r + 1]));
                     v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
                     v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
-                    top[mt][r] = v * c[mt][r];
-                    moves |= top[mt][r] > m[mt][r] + MOE_TREE_SLACK;
+                    top[mt][r] = v;
+                    moves |= v * c[mt][r] > (__float_as_uint(z[mt][r]) ? MOE_TREE_SLACK : -INFINITY);
                 }
             if (__any_sync(0xFFFFFFFFu, moves)) {
 #pragma unroll
@@ -798,10 +802,18 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
                     float keep[2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const bool up = top[mt][r] > m[mt][r] + MOE_TREE_SLACK;
-                        keep[r] = up ? ex2(m[mt][r] - top[mt][r]) : 1.0f;
-                        m[mt][r] = up ? top[mt][r] : m[mt][r];
+                        const float by = top[mt][r] * c[mt][r];
+                        const bool none = __float_as_uint(z[mt][r]) == 0;
+                        const bool up = by > (none ? -INFINITY : MOE_TREE_SLACK);
+                        const float less = up ? top[mt][r] : 0.0f;
+                        keep[r] = up && !none ? ex2(-by) : 1.0f;
+                        z[mt][r] = up ? -(top[mt][r] + (0.0f - z[mt][r])) : z[mt][r];  // (never +0)
                         l[mt][r] *= keep[r];
+#pragma unroll
+                        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                            for (int i = 2 * r; i < 2 * r + 2; ++i)
+                                s[mt][nb][i] -= less;
                     }
 #pragma unroll
                     for (int j = 0; j < T::NB; ++j) {
@@ -817,12 +829,11 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
                 float e[2][4];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float off = m[mt][r] == -INFINITY ? 0.0f : MOE_TREE_LIFT - m[mt][r];
 #pragma unroll
                     for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
                         for (int i = 2 * r; i < 2 * r + 2; ++i)
-                            e[nb][i] = ex2(fmaf(s[mt][nb][i], c[mt][r], off));
+                            e[nb][i] = ex2(fmaf(s[mt][nb][i], c[mt][r], MOE_TREE_LIFT));
                     l[mt][r] += (e[0][2 * r] + e[0][2 * r + 1]) + (e[1][2 * r] + e[1][2 * r + 1]);
                 }
                 p[mt] = make_uint4(pack_h2(e[0][0], e[0][1]), pack_h2(e[0][2], e[0][3]), pack_h2(e[1][0], e[1][1]),
@@ -910,8 +921,9 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
             for (int r = 0; r < 2; ++r) {
                 l[mt][r] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][r], 1);
                 l[mt][r] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][r], 2);
+                z[mt][r] = __float_as_uint(z[mt][r]) ? -z[mt][r] : -INFINITY;  // the reference itself from here on
                 if (t4 == 0) {
-                    wm[warp * T::ROWS + mt * 16 + r * 8 + g] = m[mt][r];
+                    wm[warp * T::ROWS + mt * 16 + r * 8 + g] = z[mt][r];
                     wl[warp * T::ROWS + mt * 16 + r * 8 + g] = l[mt][r];
                 }
             }
@@ -926,10 +938,10 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
                     up = fmaxf(up, wm[w * T::ROWS + row]);
                 for (int w = 0; w < MOE_TREE_WARPS; ++w) {
                     const float v = wm[w * T::ROWS + row];
-                    sum += wl[w * T::ROWS + row] * (v == -INFINITY ? 1.0f : ex2(v - up));  // a NaN sum stays
+                    sum += wl[w * T::ROWS + row] * (v == -INFINITY ? 1.0f : ex2((v - up) * c[mt][r]));  // a NaN sum stays
                 }
-                const float keep = m[mt][r] == -INFINITY ? 1.0f : ex2(m[mt][r] - up);
-                m[mt][r] = up;
+                const float keep = z[mt][r] == -INFINITY ? 1.0f : ex2((z[mt][r] - up) * c[mt][r]);
+                z[mt][r] = up;
                 l[mt][r] = sum;
 #pragma unroll
                 for (int j = 0; j < T::NB; ++j) {
@@ -986,7 +998,7 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
                             p[e / 4 * T::ROWS] = make_float4(o[mt][j][c], o[mt][j + 1][c], o[mt][j + 2][c], o[mt][j + 3][c]);
                         }
                         if (t4 == 0) {
-                            part[T::ROWS * D + row] = m[mt][r];
+                            part[T::ROWS * D + row] = z[mt][r] * c[mt][r];  // as an exponent of 2
                             part[T::ROWS * D + T::ROWS + row] = l[mt][r];
                         }
                     }

@@ -76,6 +76,19 @@ def test_verify_of_refused_sequences_is_over_before_the_next_kernel():
         logits.zero_()
 
 
+def refill(s, keys, values, skip=(), fill=0xFF):
+    """The cache of a base.Sequences anew: `fill` in every byte, then the rows keys[b], values[b] [tokens, heads, dim]
+    (bf16) but those of the places (sequence, token) in `skip`."""
+    s.cache.pages.fill_(fill)
+    table, page, slots = s.table.cpu().numpy(), s.cache.page_size, []
+    for b, n in enumerate(s.lens):
+        slots += [-1 if (b, j) in skip else int(table[b, j // page]) * page + j % page for j in range(n)]
+    moe.kv_append(s.cache, torch.cat(keys).cuda(), torch.cat(values).cuda(),
+                  torch.tensor(slots, dtype=torch.int32, device="cuda"))
+    s.k = [spec_ref.quantise(base.f64(x), s.cache.format)[3] for x in keys]
+    s.v = [spec_ref.quantise(base.f64(x), s.cache.format)[3] for x in values]
+
+
 # (format, head size, heads of a kv head, rows of a sequence): the warp kernel's instances, then the tensor-core kernel's
 # with one M tile and with two
 SHAPES = [(moe.MOE_KV_Q8, 64, 2, 3), (moe.MOE_KV_Q4, 64, 16, 4), (moe.MOE_KV_Q8, 128, 4, 1), (moe.MOE_KV_Q4, 128, 4, 8),
@@ -91,3 +104,48 @@ def test_queries_of_subnormal_numbers(fmt, dim, group, rows, scale):
     s.scale = scale
     s.q = (torch.randint(-1, 2, s.q.shape, device="cuda").float() * 2.0 ** -133).bfloat16()
     s.check(s.run())
+
+
+def check_winners(fmt, dim, group, rows, scale, size):
+    """Queries along single dimensions, for each of which two tokens far apart have equal keys four times as large as
+    all others: their mean comes back, however large the scores."""
+    s = base.Sequences(fmt, dim, 2, group, 16, [700], [rows], 32, "any")
+    rng = np.random.default_rng(dim)
+    t = s.lens[0]
+    k = rng.uniform(-2, 2, (t, 2, dim))
+    first, second = rng.integers(0, 300, dim), rng.integers(400, 700, dim)
+    k[first, :, np.arange(dim)] = 8.0
+    k[second, :, np.arange(dim)] = 8.0
+    k[:, :, ::32] = 8.0 * 15 / 16  # the groups' ends, so that both keys have the same scale (and minimum)
+    k[:, :, 1::32] = -8.0
+    k[:, :, 2::32] = 8.0
+    v = rng.standard_normal((t, 2, dim)) + 0.25
+    k, v = (torch.from_numpy(x.astype(np.float32)).bfloat16() for x in (k, v))
+    refill(s, [k], [v])
+    at = rng.choice([d for d in range(dim) if d % 32 > 2], s.q.shape[:2])
+    q = torch.zeros(s.q.shape)
+    q.scatter_(2, torch.from_numpy(at)[..., None], size if scale > 0 else -size)
+    s.q, s.scale = q.bfloat16().cuda(), scale
+    got = base.f64(s.run())
+    for i in range(rows):
+        for h in range(2 * group):
+            d = at[i, h]
+            pair = s.v[0][[first[d], second[d]], h // group]
+            ref = pair.mean(0)
+            # V rounded to f16 (2^-11 of each), one rounding to bf16, f32 sums
+            bound = (2.0 ** -11 + 2.0 ** -14) * np.abs(pair).mean(0) + 2.0 ** -8 * np.abs(ref) + 1e-6
+            assert (np.abs(got[i, h] - ref) <= bound).all(), (i, h, got[i, h, :4], ref[:4])
+
+
+@pytest.mark.parametrize("fmt,dim,group,rows", SHAPES)
+@pytest.mark.parametrize("scale,size", [(3e38, 1.0), (-3e38, 1.0), (0.09, 2.0 ** 127), (3e38, 2.0 ** 127)])
+def test_scores_beyond_f32(fmt, dim, group, rows, scale, size):
+    check_winners(fmt, dim, group, rows, scale, size)
+
+
+@pytest.mark.parametrize("fmt,dim,group,rows", SHAPES)
+@pytest.mark.parametrize("scale,size", [(1.0, 2.0 ** 16), (0.7, 2.0 ** 20), (1.0, 2.0 ** 24), (-0.7, 2.0 ** 27),
+                                        (0.11, 2.0 ** 33), (1.0, 2.0 ** 60)])
+def test_scores_of_many_digits(fmt, dim, group, rows, scale, size):
+    """A score's multiple of log2(e) has more digits than f32 from some 2^24 on."""
+    check_winners(fmt, dim, group, rows, scale, size)
