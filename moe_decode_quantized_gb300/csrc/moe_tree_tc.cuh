@@ -37,10 +37,6 @@ namespace moe {
 #define MOE_TTC_TOKENS 128
 #define MOE_TTC_ROWS 256  // of a row block: two M tiles
 #define MOE_TTC_COST 2    // of an item, beside its tiles (moe_tree_attn.cuh)
-// From here on a reference in f32 may be half a step (2^-1 and more) off the
-// exponent that it stands for, a product that is not rounded: the exponents of
-// an item with such a reference are rounded products too, less the reference.
-#define MOE_TTC_FAR 16777216.0f
 #define MOE_TTC_SOFT 8    // softmax warps
 #define MOE_TTC_CODE 8    // warps that turn codes into f16
 #define MOE_TTC_THREADS ((MOE_TTC_SOFT + MOE_TTC_CODE + 2) * 32)
@@ -501,8 +497,8 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
             const int prefix = it.len - it.n;
             ok = ok && wait(q_full + (item & 3), item >> 2);
             const float c = mul[(item & 3) * 256 + local];
-            float m = -INFINITY, l = 0.0f;
-            bool fresh = true, far = false;  // far: a row's reference is MOE_TTC_FAR or more
+            float m = -INFINITY, l = 0.0f;  // m: the reference as a score, so that exponents are multiples of differences
+            bool fresh = true;
             for (int u = t + (two ? 0 : (t ^ x) & 1); u < end; u += two ? 1 : 2) {
                 ok = ok && wait(s_full + x, jobs++);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -546,13 +542,12 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                         for (int i = 0; i < 32; i += 2)
                             top4[i >> 1 & 3] = max3(top4[i >> 1 & 3], __uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1]));
                 }
-                const float top = __fmul_rn(fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])), c);
-                const bool moves = top > m + MOE_TREE_SLACK;
+                const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                const bool moves = (top - m) * c > MOE_TREE_SLACK;
                 if (__any_sync(0xFFFFFFFFu, moves)) {
-                    const float f = moves ? ex2(m - top) : 1.0f;
+                    const float f = moves ? ex2((m - top) * c) : 1.0f;
                     m = moves ? top : m;
                     l *= f;
-                    far = far || __any_sync(0xFFFFFFFFu, moves && fabsf(m) >= MOE_TTC_FAR);
                     if (!fresh)  // S is there, so the last tile's O is too
 #pragma unroll 1
                         for (int k = 0; k < 128; k += 16) {
@@ -565,21 +560,8 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                             tmem_st16(o_at + k, w);
                         }
                 }
-                const float ref = m == -INFINITY ? 0.0f : m, off = far ? MOE_TREE_LIFT : MOE_TREE_LIFT - ref;
-                if (far)  // the scores to rounded exponents less the reference
-#pragma unroll 1
-                    for (int k = 0; k < 128; k += 16) {
-                        float v[16];
-                        uint32_t w[16];
-                        tmem_ld16(s_at + k, v);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            w[i] = __float_as_uint(__fmul_rn(v[i], c) - ref);
-                        tmem_st16(s_at + k, w);
-                        tmem_st_wait();
-                    }
-                const float by = far ? 1.0f : c;
-                const F2 c2(by, by), off2(off, off);
+                const float ref = m == -INFINITY ? 0.0f : -m;
+                const F2 ref2(ref, ref), c2(c, c), lift2(MOE_TREE_LIFT, MOE_TREE_LIFT);
                 F2 sum(0.0f, 0.0f), sum1(0.0f, 0.0f);
 #pragma unroll 1
                 for (int k = 0; k < 128; k += 64) {
@@ -594,7 +576,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
                             float e0, e1;
-                            fma2(F2(__uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1])), c2, off2).get(e0, e1);
+                            fma2(add2(F2(__uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1])), ref2), c2, lift2).get(e0, e1);
                             e0 = ex2(e0);
                             e1 = ex2(e1);
                             F2 &to = i & 2 ? sum1 : sum;
@@ -624,8 +606,8 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 soft_sync();
                 const float2 other = mine[(x ^ 1) * 128];
                 const float up = fmaxf(m, other.x);
-                f0 = m == -INFINITY ? 1.0f : ex2(m - up);  // sums of NaN stay
-                f1 = other.x == -INFINITY ? 1.0f : ex2(other.x - up);
+                f0 = m == -INFINITY ? 1.0f : ex2((m - up) * c);  // sums of NaN stay
+                f1 = other.x == -INFINITY ? 1.0f : ex2((other.x - up) * c);
                 l = l * f0 + other.y * f1;
                 m = up;
             }
@@ -684,7 +666,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
             if (lane == 0)
                 mbar_arrive(o_free);
             if (live && !whole && (two || x == 0)) {
-                part[ROWS * D + local] = m;
+                part[ROWS * D + local] = m * c;  // as an exponent of 2
                 part[ROWS * D + ROWS + local] = l;
             }
             if (end == tiles && tid == 0)

@@ -149,3 +149,33 @@ def test_scores_beyond_f32(fmt, dim, group, rows, scale, size):
 def test_scores_of_many_digits(fmt, dim, group, rows, scale, size):
     """A score's multiple of log2(e) has more digits than f32 from some 2^24 on."""
     check_winners(fmt, dim, group, rows, scale, size)
+
+
+@pytest.mark.parametrize("fmt,dim,group,rows", SHAPES)
+def test_near_scores_of_many_digits(fmt, dim, group, rows):
+    """Scores of some 2^26 that differ by 4, 8, ..: f32 holds them, and the weights are e^-4, e^-8, .. of the largest."""
+    s = base.Sequences(fmt, dim, 2, group, 16, [700], [rows], 34, "any")
+    rng = np.random.default_rng(dim)
+    t = s.lens[0]
+    k = np.zeros((t, 2, dim))
+    k[:, :, ::32] = 15.0  # steps of 1 from 0 to 15
+    k[:, :, 1::32] = rng.integers(0, 8, (t, 2, dim // 32))
+    if fmt == moe.MOE_KV_Q8:
+        k[:, :, ::32] = 127.0
+    v = rng.standard_normal((t, 2, dim)) + 0.25
+    k, v = (torch.from_numpy(x.astype(np.float32)).bfloat16() for x in (k, v))
+    refill(s, [k], [v])
+    assert np.array_equal(s.k[0], base.f64(k))  # held exactly
+    q = torch.zeros(s.q.shape)
+    q[:, :, 0] = 2.0 ** (22 if fmt == moe.MOE_KV_Q4 else 19)  # the large part of the score, the same for all
+    q[:, :, 1] = 4.0
+    s.q, s.scale = q.bfloat16().cuda(), 1.0
+    got = base.f64(s.run())
+    for i in range(rows):
+        seen = [j for j in range(t) if j < 700 or s.masks[i] >> (j - 700) & 1]
+        for h in range(2 * group):
+            w = np.exp(4.0 * (s.k[0][seen, h // group, 1] - 7.0))
+            w /= w.sum()
+            ref, size = w @ s.v[0][seen, h // group], w @ np.abs(s.v[0][seen, h // group])
+            # V and the weights rounded to f16 (2^-11 each), exponentials and sums in f32 (2^-14), one rounding to bf16
+            assert (np.abs(got[i, h] - ref) <= (2.0 ** -10 + 2.0 ** -14) * size + 2.0 ** -8 * np.abs(ref) + 1e-6).all()
