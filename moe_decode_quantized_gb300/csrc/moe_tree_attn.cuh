@@ -855,11 +855,18 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
                     if (FMT == MOE_KV_Q4)
                         vm[x] = h2(vs[T::GR * 8 + at2 + 4 * x]);
                 }
-                if (masked) {  // bytes past the length (of no page) are anything: as values they are 0
+                if (masked) {  // bytes past the length, of no page or of a token that no row sees are anything: 0 as values
+                    unsigned long long seen = ~0ull;
+                    if (a.mask) {
+                        seen = masks[lane & (T::ROWS - 1)] | (T::ROWS > 32 ? masks[lane + T::ROWS - 32] : 0);
+                        seen = __reduce_or_sync(0xFFFFFFFFu, (uint32_t)seen) |
+                               (unsigned long long)__reduce_or_sync(0xFFFFFFFFu, (uint32_t)(seen >> 32)) << 32;
+                    }
+                    auto in = [&](int j) { return j < it.len && (j < prefix || seen >> (j - prefix) & 1); };
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const int j = first + 8 * x + 2 * t4;
-                        const uint32_t keep = gone ? 0u : (j < it.len ? 0xFFFFu : 0u) | (j + 1 < it.len ? 0xFFFF0000u : 0u);
+                        const uint32_t keep = gone ? 0u : (in(j) ? 0xFFFFu : 0u) | (in(j + 1) ? 0xFFFF0000u : 0u);
                         vd[x] = h2(h2(vd[x]) & keep);
                         if (FMT == MOE_KV_Q4)
                             vm[x] = h2(h2(vm[x]) & keep);

@@ -432,6 +432,19 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 if (FMT == MOE_KV_Q4)
                     mn[i] = in ? h2(__half2half2(p[T::GR * 16 + tok])) : 0u;
             }
+            // A token that no row sees may never have been written: whatever its bytes, its values are numbers (they are
+            // multiplied by weights of 0). Bounds past what the cache's writer makes: 472.5 (Q8); a minimum of +-60000
+            // and a scale of (60000 - minimum) / 15, rounded up (Q4).
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                __half2 most = h2(0x5FFF5FFFu);  // 511.75
+                if (FMT == MOE_KV_Q4) {
+                    const __half2 m = __hmax2(__hmin2(h2(mn[i]), h2(0x7B557B55u)), h2(0xFB55FB55u));  // +-60064
+                    mn[i] = h2(m);
+                    most = __hfma2(m, __float2half2_rn(-1.0f / 15), __float2half2_rn(4364.0f));
+                }
+                sc[i] = h2(__hmax2(__hmin2(h2(sc[i]), most), h2(0u)));
+            }
             __syncwarp();
             if (lane == 0)  // the stage is in registers
                 mbar_arrive(raw_free + s);

@@ -179,3 +179,38 @@ def test_near_scores_of_many_digits(fmt, dim, group, rows):
             ref, size = w @ s.v[0][seen, h // group], w @ np.abs(s.v[0][seen, h // group])
             # V and the weights rounded to f16 (2^-11 each), exponentials and sums in f32 (2^-14), one rounding to bf16
             assert (np.abs(got[i, h] - ref) <= (2.0 ** -10 + 2.0 ** -14) * size + 2.0 ** -8 * np.abs(ref) + 1e-6).all()
+
+
+@pytest.mark.parametrize("fmt,dim,group,rows", [x for x in SHAPES if x[3] > 1])
+@pytest.mark.parametrize("fill", [0xFF, 0x7B])
+def test_slots_never_written_that_no_row_sees(fmt, dim, group, rows, fill):
+    """Drafted tokens that were left out of the cache (slot -1) and that every mask leaves out: their bytes, scales of
+    NaN or too large for f16, reach no row. One lies beside seen tokens, one at the end, one sequence sees none."""
+    s = base.Sequences(fmt, dim, 2, group, 16, [300, 13, 0], [rows, rows, rows], 33, "any")
+    rng = np.random.default_rng(rows)
+    kv = [[torch.from_numpy(rng.standard_normal((t, 2, dim)).astype(np.float32)).bfloat16() for t in s.lens]
+          for _ in range(2)]
+    hidden = [{rows // 2, rows - 1}, {0}, set(range(rows))]
+    s.masks = [m & ~sum(1 << j for j in hidden[i // rows]) for i, m in enumerate(s.masks)]
+    s.mask = torch.tensor([m - (1 << 64) if m >> 63 else m for m in s.masks], dtype=torch.int64, device="cuda")
+    refill(s, *kv, {(b, s.lens[b] - rows + j) for b in range(3) for j in hidden[b]}, fill)
+    out = s.run()
+    s.check(out)
+    assert (out[2 * rows:] == 0).all()
+
+
+@pytest.mark.parametrize("fmt,dim,group,rows", SHAPES)
+def test_values_at_the_ends_of_the_range(fmt, dim, group, rows):
+    """The largest scales (and minima) that the cache's writer makes: values up to 60000 of either sign or of both."""
+    s = base.Sequences(fmt, dim, 2, group, 16, [300, 13], [rows, rows], 35, "any")
+    rng = np.random.default_rng(rows)
+    k = [torch.from_numpy(rng.standard_normal((t, 2, dim)).astype(np.float32)).bfloat16() for t in s.lens]
+    v = []
+    for t in s.lens:
+        x = rng.uniform(-1, 1, (t, 2, dim)) * 6.2e4
+        x[::3] = np.abs(x[::3])
+        x[1::3] = -np.abs(x[1::3])
+        x[::5] = np.sign(x[::5]) * 6.2e4
+        v.append(torch.from_numpy(x.astype(np.float32)).bfloat16())
+    refill(s, k, v)
+    s.check(s.run())
