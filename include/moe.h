@@ -575,7 +575,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
  * (-1 where the last row has no finite logit, or no rows). A logit of NaN or
  * +infinity counts as -infinity and sets MOE_WS_NONFINITE, a token outside the
  * vocabulary is passed over and sets MOE_WS_INDEX. ws_dev: initialised once.
- * batch 0 .. 65535, vocab 1 .. 2^24. */
+ * batch 0 .. 65535, vocab 1 .. 2^24; n_rows 0: the rows' arguments may be NULL. */
 int moe_spec_verify_workspace_bytes(int batch, int n_rows, size_t *bytes);
 int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stride, const int32_t *q_start_dev,
                     const int32_t *tokens_dev, const int32_t *parents_dev, const float *draft_dev,

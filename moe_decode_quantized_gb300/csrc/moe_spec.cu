@@ -482,9 +482,10 @@ int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stri
         return host_fail(vocab < 1 ? MOE_EINVAL : MOE_EUNSUPPORTED, "moe_spec_verify: vocab (%d) of 1 .. 2^24", vocab);
     if (batch == 0)
         return MOE_OK;
-    if (!logits_dev || !q_start_dev || !tokens_dev || !n_accepted_dev || !path_dev || !next_token_dev || !ws_dev)
+    if (!q_start_dev || !n_accepted_dev || !next_token_dev || !ws_dev ||
+        (n_rows > 0 && (!logits_dev || !tokens_dev || !path_dev)))
         return host_fail(MOE_EINVAL, "moe_spec_verify: NULL argument");
-    if ((uniforms_dev == nullptr) != (noise_dev == nullptr))
+    if (n_rows > 0 && (uniforms_dev == nullptr) != (noise_dev == nullptr))
         return host_fail(MOE_EINVAL, "moe_spec_verify: uniforms and noise go together");
     if (!aligned(logits_dev, logits_type == MOE_F32 ? 4 : 2) || !aligned(q_start_dev, 4) || !aligned(tokens_dev, 4) ||
         !aligned(parents_dev, 4) || !aligned(draft_dev, 4) || !aligned(temperature_dev, 4) || !aligned(uniforms_dev, 4) ||

@@ -214,3 +214,25 @@ def test_values_at_the_ends_of_the_range(fmt, dim, group, rows):
         v.append(torch.from_numpy(x.astype(np.float32)).bfloat16())
     refill(s, k, v)
     s.check(s.run())
+
+
+def test_verify_of_no_rows():
+    """A step in which no sequence has rows, and sequences without rows among others."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for drafts in (True, False):
+        n_acc, nxt = torch.full((3,), 9, **i32), torch.full((3,), 9, **i32)
+        empty, ws = torch.empty(0, **i32), torch.empty(moe.spec_verify_workspace_bytes(3, 0), dtype=torch.uint8, device="cuda")
+        moe.workspace_init(ws)
+        draft = torch.empty((0, 100), device="cuda") if drafts else None
+        moe.spec_verify(torch.empty((0, 100), device="cuda"), torch.zeros(4, **i32), empty, empty, draft, None,
+                        torch.empty(0, device="cuda"), torch.ones((3, 100), device="cuda"), n_acc, empty, nxt, ws)
+        assert moe.read_status(ws) == 0 and n_acc.tolist() == [0, 0, 0] and nxt.tolist() == [-1, -1, -1]
+    case = verify_rows([0, 3, 0, 0, 5, 0], 333, "f32", "tree", True, 5)
+    n_acc, path, nxt, status, _ = base.verify(case)
+    alone = verify_rows([0, 3, 0, 0, 5, 0], 333, "f32", "tree", True, 5)
+    for x in ("tokens", "parents", "u"):
+        alone[x] = [alone[x][1], alone[x][4]]
+    alone["temp"], alone["noise"] = [alone["temp"][1], alone["temp"][4]], alone["noise"][[1, 4]]
+    want = base.verify(alone)
+    assert status == 0 and [n_acc[1], n_acc[4]] == want[0] and path == want[1] and [nxt[1], nxt[4]] == want[2]
+    assert [n_acc[b] for b in (0, 2, 3, 5)] == [0] * 4 and [nxt[b] for b in (0, 2, 3, 5)] == [-1] * 4
