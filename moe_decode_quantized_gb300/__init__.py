@@ -532,11 +532,14 @@ class KvCache:
         return size // per
 
     def ref(self):
-        """The C struct by reference, made again after a field was set."""
-        if self._ref is None:
+        """The C struct by reference, made again after a field was set or the pages tensor got other memory."""
+        pages = self.pages
+        at = None if pages is None else (pages.data_ptr(), pages.numel())
+        if self._ref is None or at != self._at:
             n_pages = self.n_pages
-            c = _lib.MoeKvCache(_ptr(self.pages), n_pages, self.head_dim, self.n_kv_heads, self.page_size, self.format)
+            c = _lib.MoeKvCache(_ptr(pages), n_pages, self.head_dim, self.n_kv_heads, self.page_size, self.format)
             object.__setattr__(self, "_ref", C.byref(c))
+            object.__setattr__(self, "_at", at)
         return self._ref
 
 
