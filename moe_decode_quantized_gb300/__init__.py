@@ -467,7 +467,7 @@ def _on(rt, stream):
 
 
 def _dev(t, name, dtype, n):
-    """Device address of a contiguous tensor of at least n values; None stays NULL."""
+    """Address of a contiguous tensor of at least n values; None stays NULL."""
     if t is None:
         return None
     if t.dtype is not dtype:
@@ -477,6 +477,13 @@ def _dev(t, name, dtype, n):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _refuse_host(**tensors):
+    """Refuses the first host tensor: its address means nothing to the kernels."""
+    for name, t in tensors.items():
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name} must be on the GPU, not on {t.device}")
 
 
 def _matrix(t, name, dtype, rows, columns):
@@ -558,8 +565,11 @@ def kv_append(cache: KvCache, k, v, slots, status=None, stream=None):
     n, heads = k.shape[0], cache.n_kv_heads
     if n != v.shape[0]:
         raise ValueError("k and v must have the same number of tokens")
-    rc = rt.lib.moe_kv_append(cache.ref(), *_heads(rt, cache, k, "k", heads), *_heads(rt, cache, v, "v", heads),
-                              _dev(slots, "slots", rt.i32, n), n, _dev(status, "status", rt.i32, 1), _on(rt, stream))
+    args = (cache.ref(), *_heads(rt, cache, k, "k", heads), *_heads(rt, cache, v, "v", heads),
+            _dev(slots, "slots", rt.i32, n), n, _dev(status, "status", rt.i32, 1), _on(rt, stream))
+    if not (k.is_cuda and v.is_cuda and slots.is_cuda and cache.pages.is_cuda and (status is None or status.is_cuda)):
+        _refuse_host(pages=cache.pages, k=k, v=v, slots=slots, status=status)
+    rc = rt.lib.moe_kv_append(*args)
     if rc:
         _check(rc)
 
@@ -571,9 +581,13 @@ def kv_read(cache: KvCache, slots, k_out, v_out, status=None, stream=None):
     if kind is not rt.bf16 and kind is not rt.f32:
         raise ValueError(f"k_out must be bfloat16 or float32, not {kind}")
     size = n * cache.n_kv_heads * cache.head_dim
-    rc = rt.lib.moe_kv_read(cache.ref(), _dev(slots, "slots", rt.i32, n), n, _dev(k_out, "k_out", kind, size),
-                            _dev(v_out, "v_out", kind, size), MOE_F32 if kind is rt.f32 else MOE_BF16,
-                            _dev(status, "status", rt.i32, 1), _on(rt, stream))
+    args = (cache.ref(), _dev(slots, "slots", rt.i32, n), n, _dev(k_out, "k_out", kind, size),
+            _dev(v_out, "v_out", kind, size), MOE_F32 if kind is rt.f32 else MOE_BF16,
+            _dev(status, "status", rt.i32, 1), _on(rt, stream))
+    if not (slots.is_cuda and k_out.is_cuda and v_out.is_cuda and cache.pages.is_cuda and
+            (status is None or status.is_cuda)):
+        _refuse_host(pages=cache.pages, slots=slots, k_out=k_out, v_out=v_out, status=status)
+    rc = rt.lib.moe_kv_read(*args)
     if rc:
         _check(rc)
 
@@ -597,11 +611,14 @@ def tree_attention(cache: KvCache, q, out, q_start, kv_len, table, mask, scale: 
     if mask is not None and mask.dtype not in rt.bits:
         raise ValueError(f"mask must be int64, not {mask.dtype}")
     tp, ts = _matrix(table, "table", rt.i32, batch, table.shape[-1])
-    rc = rt.lib.moe_tree_attention(cache.ref(), *_heads(rt, cache, q, "q", heads), *_heads(rt, cache, out, "out", heads),
-                                   heads, _dev(q_start, "q_start", rt.i32, batch + 1),
-                                   _dev(kv_len, "kv_len", rt.i32, batch), tp, ts, table.shape[1],
-                                   None if mask is None else _dev(mask, "mask", mask.dtype, n), batch, n, scale,
-                                   ws.data_ptr(), ws.numel() * ws.element_size(), _on(rt, stream))
+    args = (cache.ref(), *_heads(rt, cache, q, "q", heads), *_heads(rt, cache, out, "out", heads),
+            heads, _dev(q_start, "q_start", rt.i32, batch + 1), _dev(kv_len, "kv_len", rt.i32, batch), tp, ts,
+            table.shape[1], None if mask is None else _dev(mask, "mask", mask.dtype, n), batch, n, scale,
+            ws.data_ptr(), ws.numel() * ws.element_size(), _on(rt, stream))
+    if not (q.is_cuda and out.is_cuda and q_start.is_cuda and kv_len.is_cuda and table.is_cuda and ws.is_cuda and
+            cache.pages.is_cuda and (mask is None or mask.is_cuda)):
+        _refuse_host(pages=cache.pages, q=q, out=out, q_start=q_start, kv_len=kv_len, table=table, mask=mask, ws=ws)
+    rc = rt.lib.moe_tree_attention(*args)
     if rc:
         _check(rc)
 
@@ -627,11 +644,18 @@ def spec_verify(logits, q_start, tokens, parents, draft, temperature, uniforms, 
     lp, ls = _matrix(logits, "logits", kind, rows, vocab)
     dp, ds = _matrix(draft, "draft", f32, rows, vocab)
     np_, ns = _matrix(noise, "noise", f32, batch, vocab)
-    rc = rt.lib.moe_spec_verify(lp, MOE_F32 if kind is f32 else MOE_BF16, ls, _dev(q_start, "q_start", i32, batch + 1),
-                                _dev(tokens, "tokens", i32, rows), _dev(parents, "parents", i32, rows), dp, ds,
-                                _dev(temperature, "temperature", f32, batch), _dev(uniforms, "uniforms", f32, rows),
-                                np_, ns, batch, rows, vocab, _dev(n_accepted, "n_accepted", i32, batch),
-                                _dev(path, "path", i32, rows), _dev(next_token, "next_token", i32, batch),
-                                ws.data_ptr(), ws.numel() * ws.element_size(), _on(rt, stream))
+    args = (lp, MOE_F32 if kind is f32 else MOE_BF16, ls, _dev(q_start, "q_start", i32, batch + 1),
+            _dev(tokens, "tokens", i32, rows), _dev(parents, "parents", i32, rows), dp, ds,
+            _dev(temperature, "temperature", f32, batch), _dev(uniforms, "uniforms", f32, rows),
+            np_, ns, batch, rows, vocab, _dev(n_accepted, "n_accepted", i32, batch),
+            _dev(path, "path", i32, rows), _dev(next_token, "next_token", i32, batch),
+            ws.data_ptr(), ws.numel() * ws.element_size(), _on(rt, stream))
+    if not (logits.is_cuda and q_start.is_cuda and tokens.is_cuda and n_accepted.is_cuda and path.is_cuda and
+            next_token.is_cuda and ws.is_cuda and (parents is None or parents.is_cuda) and
+            (draft is None or draft.is_cuda) and (temperature is None or temperature.is_cuda) and
+            (uniforms is None or uniforms.is_cuda) and (noise is None or noise.is_cuda)):
+        _refuse_host(logits=logits, q_start=q_start, tokens=tokens, parents=parents, draft=draft, temperature=temperature,
+                 uniforms=uniforms, noise=noise, n_accepted=n_accepted, path=path, next_token=next_token, ws=ws)
+    rc = rt.lib.moe_spec_verify(*args)
     if rc:
         _check(rc)

@@ -236,3 +236,24 @@ def test_verify_of_no_rows():
     want = base.verify(alone)
     assert status == 0 and [n_acc[1], n_acc[4]] == want[0] and path == want[1] and [nxt[1], nxt[4]] == want[2]
     assert [n_acc[b] for b in (0, 2, 3, 5)] == [0] * 4 and [nxt[b] for b in (0, 2, 3, 5)] == [-1] * 4
+
+
+def test_one_host_tensor_among_device_ones_is_refused():
+    s = base.Sequences(moe.MOE_KV_Q8, 64, 1, 2, 16, [5], [2], 36)
+    ws, slots = s.workspace(), torch.zeros(2, dtype=torch.int32, device="cuda")
+    x = torch.zeros((2, 1, 64), dtype=torch.bfloat16, device="cuda")
+    good = dict(cache=s.cache, q=s.q, out=torch.empty_like(s.q), q_start=s.q_start, kv_len=s.kv_len, table=s.table,
+                mask=s.mask, scale=s.scale, ws=ws)
+    for name in ("q", "out", "q_start", "kv_len", "table", "mask", "ws"):
+        with pytest.raises(ValueError, match=f"{name} must be on the GPU"):
+            moe.tree_attention(**{**good, name: good[name].cpu()})
+    moe.tree_attention(**good)
+    for name, bad in (("k", (x.cpu(), x, slots)), ("v", (x, x.cpu(), slots)), ("slots", (x, x, slots.cpu()))):
+        with pytest.raises(ValueError, match=f"{name} must be on the GPU"):
+            moe.kv_append(s.cache, *bad)
+    with pytest.raises(ValueError, match="status must be on the GPU"):
+        moe.kv_append(s.cache, x, x, slots, torch.zeros(1, dtype=torch.int32))
+    case = verify_rows([2], 100, "f32", "chain", True, 1)
+    for name in ("logits", "draft"):
+        with pytest.raises(ValueError, match=f"{name} must be on the GPU"):
+            base.verify({**case, name: case[name].cpu()})

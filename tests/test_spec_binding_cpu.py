@@ -24,3 +24,22 @@ def test_pages_that_get_other_memory_are_followed():
     c.pages.resize_(per + 1)
     with pytest.raises(ValueError, match="not a multiple"):
         c.ref()
+
+
+def test_host_tensors_are_refused():
+    """In calls that are right but for where their tensors are. (Without the refusal these would launch nothing here:
+    there is no device.)"""
+    c, i32 = _cache(), dict(dtype=torch.int32)
+    k, s = torch.zeros((3, 2, 64), dtype=torch.bfloat16), torch.zeros(3, **i32)
+    with pytest.raises(ValueError, match="pages must be on the GPU"):
+        moe.kv_append(c, k, k, s, stream=0)
+    with pytest.raises(ValueError, match="pages must be on the GPU"):
+        moe.kv_read(c, s, k.clone(), k.clone(), stream=0)
+    q, ws = torch.zeros((3, 4, 64), dtype=torch.bfloat16), torch.zeros(256, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="on the GPU"):
+        moe.tree_attention(c, q, q.clone(), torch.tensor([0, 3], **i32), s[:1], torch.zeros((1, 2), **i32), None, 1.0, ws,
+                           stream=0)
+    l = torch.zeros((3, 7))
+    with pytest.raises(ValueError, match="logits must be on the GPU"):
+        moe.spec_verify(l, torch.tensor([0, 3], **i32), s, None, None, None, l[:, 0].contiguous(), l[:1], s[:1].clone(),
+                        s.clone(), s[:1].clone(), ws, stream=0)
