@@ -479,6 +479,13 @@ def _dev(t, name, dtype, n):
     return t.data_ptr()
 
 
+def _bytes(ws):
+    """Address and size of a workspace tensor."""
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _refuse_host(**tensors):
     """Refuses the first host tensor: its address means nothing to the kernels."""
     for name, t in tensors.items():
@@ -614,7 +621,7 @@ def tree_attention(cache: KvCache, q, out, q_start, kv_len, table, mask, scale: 
     args = (cache.ref(), *_heads(rt, cache, q, "q", heads), *_heads(rt, cache, out, "out", heads),
             heads, _dev(q_start, "q_start", rt.i32, batch + 1), _dev(kv_len, "kv_len", rt.i32, batch), tp, ts,
             table.shape[1], None if mask is None else _dev(mask, "mask", mask.dtype, n), batch, n, scale,
-            ws.data_ptr(), ws.numel() * ws.element_size(), _on(rt, stream))
+            *_bytes(ws), _on(rt, stream))
     if not (q.is_cuda and out.is_cuda and q_start.is_cuda and kv_len.is_cuda and table.is_cuda and ws.is_cuda and
             cache.pages.is_cuda and (mask is None or mask.is_cuda)):
         _refuse_host(pages=cache.pages, q=q, out=out, q_start=q_start, kv_len=kv_len, table=table, mask=mask, ws=ws)
@@ -649,7 +656,7 @@ def spec_verify(logits, q_start, tokens, parents, draft, temperature, uniforms, 
             _dev(temperature, "temperature", f32, batch), _dev(uniforms, "uniforms", f32, rows),
             np_, ns, batch, rows, vocab, _dev(n_accepted, "n_accepted", i32, batch),
             _dev(path, "path", i32, rows), _dev(next_token, "next_token", i32, batch),
-            ws.data_ptr(), ws.numel() * ws.element_size(), _on(rt, stream))
+            *_bytes(ws), _on(rt, stream))
     if not (logits.is_cuda and q_start.is_cuda and tokens.is_cuda and n_accepted.is_cuda and path.is_cuda and
             next_token.is_cuda and ws.is_cuda and (parents is None or parents.is_cuda) and
             (draft is None or draft.is_cuda) and (temperature is None or temperature.is_cuda) and

@@ -43,3 +43,16 @@ def test_host_tensors_are_refused():
     with pytest.raises(ValueError, match="logits must be on the GPU"):
         moe.spec_verify(l, torch.tensor([0, 3], **i32), s, None, None, None, l[:, 0].contiguous(), l[:1], s[:1].clone(),
                         s.clone(), s[:1].clone(), ws, stream=0)
+
+
+def test_a_strided_workspace_is_refused():
+    """Its bytes are fewer than those between its first and last: the kernels would write past it or into others'."""
+    c, i32 = _cache(), dict(dtype=torch.int32)
+    q, ws, s = torch.zeros((3, 4, 64), dtype=torch.bfloat16), torch.zeros((256, 2), dtype=torch.uint8)[:, 0], torch.zeros(3, **i32)
+    with pytest.raises(ValueError, match="ws must be contiguous"):
+        moe.tree_attention(c, q, q.clone(), torch.tensor([0, 3], **i32), s[:1], torch.zeros((1, 2), **i32), None, 1.0, ws,
+                           stream=0)
+    l = torch.zeros((3, 7))
+    with pytest.raises(ValueError, match="ws must be contiguous"):
+        moe.spec_verify(l, torch.tensor([0, 3], **i32), s, None, None, None, l[:, 0].contiguous(), l[:1], s[:1].clone(),
+                        s.clone(), s[:1].clone(), ws, stream=0)
