@@ -30,6 +30,7 @@ namespace moe {
 
 #define MOE_TREE_WARPS 4
 #define MOE_TREE_THREADS (MOE_TREE_WARPS * 32)
+#define MOE_TREE_DRAIN_NS 1000000ull  // a wait for what is in flight after another wait ran out: at least this long
 #define MOE_TREE_COST 24  // of an item, beside its units
 // the weights are 2^(s - m + 7): m moves when a score passes it by 8, so a
 // weight stays below 2^15, and f16 holds weights of 2^-31 of the largest
@@ -1017,7 +1018,7 @@ __global__ void __launch_bounds__(MOE_TREE_THREADS, TreeShape<FMT, D, MT>::CTAS)
     }
     if (!ok)  // a copy did not arrive in time: wait for those in flight (bounded) before the memory is given back
         for (int k = max(0, asked - stages); k < asked; ++k)
-            mbar_wait(bar + k % stages, (uint32_t)(k / stages) & 1u, a.ctrl + MOE_CTRL_STATUS, a.wait_ns);
+            mbar_wait(bar + k % stages, (uint32_t)(k / stages) & 1u, a.ctrl + MOE_CTRL_STATUS, max(a.wait_ns, MOE_TREE_DRAIN_NS));
 }
 
 }  // namespace moe

@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
     uint64_t *k_full = bars + 12, *v_full = bars + 13, *k_done = bars + 14, *v_done = bars + 15, *o_done = bars + 16,
              *o_free = bars + 17, *s_full = bars + 18, *p_full = bars + 20;  // s_full, p_full [2]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 22);
+    uint64_t *drained = bars + 28;  // after a wait that ran out
     uint32_t *gone = tmem_slot + 1;  // [8] blocks of tile t that are not there, at t % 8: kept longer than its stage
     float *mul = reinterpret_cast<float *>(small + 256);  // [4][256] multipliers of the rows of item i, at i % 4
     float2 *stat = reinterpret_cast<float2 *>(mul + 1024);  // [2][2][128] (reference, sum) of item i, at i % 2, by group
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
         mbar_init(v_done, 1);
         for (int i = 0; i < 4; ++i)
             mbar_init(q_full + i, MOE_TTC_CODE);
+        mbar_init(drained, 1);
         mbar_init(o_done, 1);
         mbar_init(o_free, MOE_TTC_SOFT);
         for (int x = 0; x < 2; ++x) {
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 bulk_g2s(raw + (size_t)s * T::STAGE + lane * T::BLOCK, src, T::BLOCK, raw_full + s, policy);
         }
         for (int k = max(0, t - stages); k < t; ++k)  // nothing in flight when the memory is given back
-            wait(raw_full + k % stages, k / stages);
+            tree_wait(raw_full + k % stages, (uint32_t)(k / stages) & 1u, status, max(a.wait_ns, MOE_TREE_DRAIN_NS));
     } else if (warp == MOE_TTC_SOFT + MOE_TTC_CODE + 1) {
         // ---------------- the products
         if (lane == 0) {
@@ -321,7 +323,11 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
             if (tiles > 0 && ok) {
                 closing = true;
                 close();
-                wait(o_done, item);
+                ok = wait(o_done, item);
+            }
+            if (!ok) {  // products may be in flight: they end before tensor and shared memory are given back
+                mma_commit(drained);
+                tree_wait(drained, 0, status, max(a.wait_ns, MOE_TREE_DRAIN_NS));
             }
         }
     } else if (warp >= MOE_TTC_SOFT) {
