@@ -257,3 +257,186 @@ def test_one_host_tensor_among_device_ones_is_refused():
     for name in ("logits", "draft"):
         with pytest.raises(ValueError, match=f"{name} must be on the GPU"):
             base.verify({**case, name: case[name].cpu()})
+
+
+# ------------------------------------------------------------------ every part of a long item
+
+LONG = [(4, 1), (8, 4), (8, 8), (8, 40)]  # heads of a kv head and rows over 40011 tokens: the join of some 300 and 150 parts
+
+
+@pytest.mark.parametrize("fmt", base.FMTS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group,rows", LONG)
+def test_every_token_of_a_long_sequence_counts(fmt, dim, group, rows):
+    """Equal weights, and a dimension for each stretch of tokens: one that lost (or counted twice) as few as 16 tokens
+    would be off by 2 % or more."""
+    s = base.Sequences(fmt, dim, 1, group, 128, [40011], [rows], rows, "chain")
+    t = s.lens[0]
+    stretch = min(-(-t // dim), 700)
+    for first in range(0, t, stretch * dim):
+        v = torch.zeros((t, 1, dim))
+        part = torch.arange(first, min(t, first + stretch * dim))
+        v[part, 0, (part - first) // stretch] = 1.0
+        refill(s, [torch.zeros((t, 1, dim)).bfloat16()], [v.bfloat16()])
+        got = base.f64(s.run())
+        for i in range(rows):
+            ref = s.v[0][:t - rows + i + 1, 0].mean(0)
+            # V and the weights rounded to f16 (2^-11 each), sums in f32 (2^-14), one rounding to bf16
+            bound = (2.0 ** -10 + 2.0 ** -14 + 2.0 ** -8) * np.abs(ref)
+            assert (np.abs(got[i] - ref) <= bound).all(), (i, np.abs(got[i] - ref).max(), ref.max())
+    assert 16 / stretch > 2 * (2.0 ** -10 + 2.0 ** -14 + 2.0 ** -8)  # what the test can see
+
+
+@pytest.mark.parametrize("fmt", base.FMTS)
+@pytest.mark.parametrize("dim,group,rows", [(128, 4, 1), (128, 8, 8), (128, 8, 40), (64, 16, 4), (256, 4, 3)])
+def test_a_winning_token_anywhere_in_a_long_sequence(fmt, dim, group, rows):
+    """Tokens whose keys are the queries' own random signs, beside and at the places where runs of 128 tokens (and tiles
+    of the tensor-core kernel) meet: each query row gets its token's value back, in whichever part it lies."""
+    s = base.Sequences(fmt, dim, 1, group, 128, [40011], [rows], rows, "chain")
+    t, rng = s.lens[0], np.random.default_rng(rows)
+    places = np.unique(np.concatenate([np.arange(0, 40011, 128), np.arange(127, 40011, 128), [40010]]))
+    signs = rng.choice([-1.0, 1.0], (len(places), dim))
+    k, v = rng.standard_normal((t, 1, dim)) * 0.1, rng.standard_normal((t, 1, dim)) + 0.25
+    k[places, 0] = signs
+    refill(s, *([torch.from_numpy(x.astype(np.float32)).bfloat16()] for x in (k, v)))
+    s.scale = 1.0
+    cross = signs @ signs.T - 2 * dim * np.eye(len(places))
+    gain = 64.0 / (dim - cross.max())  # the next best token has a weight of e^-60 or less (of the quantised keys)
+    ws = s.workspace()
+    for first in range(0, len(places), rows * group):
+        at = np.resize(np.arange(first, min(len(places), first + rows * group)), (rows, group))
+        s.q = torch.from_numpy(signs[at] * gain).to(torch.bfloat16).cuda()
+        got, ref = base.f64(s.run(ws)), s.v[0][places[at], 0]
+        assert (np.abs(got - ref) <= (2.0 ** -11 + 2.0 ** -14 + 2.0 ** -8) * np.abs(ref) + 1e-6).all(), first
+
+
+@pytest.mark.parametrize("fmt,dim,group,rows", SHAPES)
+@pytest.mark.parametrize("scale,size", [(1.0, 2.0 ** 3), (0.7, 2.0 ** 5), (-1.0, 2.0 ** 7), (1.0, 2.0 ** 10)])
+def test_scores_of_hundreds_and_thousands(fmt, dim, group, rows, scale, size):
+    check_winners(fmt, dim, group, rows, scale, size)
+
+
+# ------------------------------------------------------------------ the tensor-core kernel's own paths
+
+# heads of 128: a row block of two M tiles, and of one
+MANY = [(moe.MOE_KV_Q8, 8, 61), (moe.MOE_KV_Q4, 8, 61), (moe.MOE_KV_Q8, 4, 16), (moe.MOE_KV_Q4, 4, 16)]
+
+
+@pytest.mark.parametrize("fmt,group,rows", MANY)
+def test_many_rows_in_a_graph(fmt, group, rows):
+    """A captured call follows the lengths, and gives the same bits each time."""
+    s = base.Sequences(fmt, 128, 2, group, 32, [700, 90, 1500], [rows, rows - 3, rows], 41, "tree")
+    ws, out = s.workspace(), torch.empty_like(s.q)
+    want = s.run(ws).clone()
+    s.check(want)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        moe.tree_attention(s.cache, s.q, out, s.q_start, s.kv_len, s.table, s.mask, s.scale, ws)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    s.kv_len.copy_(torch.tensor([300, 80, 1001], dtype=torch.int32))
+    g.replay()
+    torch.cuda.synchronize()
+    got = out.clone()
+    assert torch.equal(got, s.run(ws)) and not torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fmt,group,rows", MANY)
+def test_many_rows_one_of_them_nan(fmt, group, rows):
+    """Within one run and across runs and groups: the row is NaN, the others keep their bits."""
+    s = base.Sequences(fmt, 128, 2, group, 32, [50, 3000], [rows, rows], 42, "tree")
+    want = s.run()
+    at = [(1, 1), (rows - 1, 0), (rows, 2 * group - 1), (rows + rows // 2, 3)]
+    for n, (i, h) in enumerate(at):
+        s.q[i, h, 7 * n] = float("nan") if n % 2 else -float("inf")
+    got = s.run()
+    for i, h in at:
+        assert torch.isnan(got[i, h]).all()
+        got[i, h] = want[i, h]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fmt,group,rows", MANY)
+def test_many_rows_lengths_and_pages_outside(fmt, group, rows):
+    s = base.Sequences(fmt, 128, 1, group, 16, [400, 20, 300], [rows] * 3, 43, "tree")
+    want, ws = s.run(), s.workspace()
+
+    def status():
+        out = torch.full_like(s.q, 5.0)
+        moe.tree_attention(s.cache, s.q, out, s.q_start, s.kv_len, s.table, s.mask, s.scale, ws)
+        st = moe.read_status(ws)
+        moe.workspace_init(ws)
+        return st, out
+
+    keep = s.kv_len.clone()
+    for bad in (1, -3, 10 ** 6):  # fewer tokens than query rows; negative; more than the table has pages for
+        s.kv_len[1] = bad
+        st, out = status()
+        assert st == moe.MOE_WS_INDEX
+        assert torch.equal(out[:rows], want[:rows]) and torch.equal(out[2 * rows:], want[2 * rows:])
+        assert (out[rows:2 * rows] == 0).all()
+    s.kv_len.copy_(keep)
+    # blocks of a tile that are not there: one, two in different tiles, the tile's first and last, a whole tile of eight
+    for pages in ([0], [3, 17], [8, 15], list(range(8, 16)), [24]):
+        old = s.table[0].clone()
+        for n, p in enumerate(pages):
+            s.table[0, p] = (-1, s.cache.n_pages, 1 << 30)[n % 3]
+        st, out = status()
+        s.table[0] = old
+        assert st == moe.MOE_WS_INDEX and torch.equal(out[rows:], want[rows:])
+        kept = [j for j in range(400 + rows) if j // 16 not in pages]  # pages of the context alone
+        ref, bound = spec_ref.attention(base.f64(s.q[:rows]), s.k[0][kept], s.v[0][kept], rows, group, s.scale,
+                                        s.masks[:rows])
+        assert (np.abs(base.f64(out[:rows]) - ref) <= bound).all(), pages
+    assert torch.equal(s.run(ws), want)
+
+
+@pytest.mark.parametrize("fmt,group,rows", MANY)
+def test_many_rows_masked_values_do_not_reach_a_row(fmt, group, rows):
+    """A drafted token that no row sees, with a key and value as large as the cache holds; one that only a few see."""
+    s = base.Sequences(fmt, 128, 1, group, 64, [137], [rows], 44, "any")
+    s.masks = [m & ~(1 << 2) for m in s.masks]
+    s.mask = torch.tensor([m - (1 << 64) if m >> 63 else m for m in s.masks], dtype=torch.int64, device="cuda")
+    want = s.run()
+    s.check(want)
+    big = torch.full((1, 1, 128), 6.0e4, device="cuda").bfloat16()
+
+    def put(node):
+        j = 137 + node
+        slot = int(s.table[0, j // 64]) * 64 + j % 64
+        moe.kv_append(s.cache, big, -big, torch.tensor([slot], dtype=torch.int32, device="cuda"))
+
+    put(2)
+    assert torch.equal(s.run(), want)
+    put(5)
+    blind = [i for i in range(rows) if not s.masks[i] >> 5 & 1]
+    assert blind and torch.equal(s.run()[blind], want[blind])
+
+
+# ------------------------------------------------------------------ one sequence's verification
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", ["chain", "tree"])
+@pytest.mark.parametrize("drafts", [True, False])
+@pytest.mark.parametrize("nodes,vocab", [(4, 32000), (8, 131072), (2, 2048), (12, 5003)])
+def test_verify_one_sequence(kind, shape, drafts, nodes, vocab):
+    """All rows of one sequence, over seeds in which drafts are accepted and rejected."""
+    accepted = rejected = sure = 0
+    for seed in range(8):
+        case = verify_rows([nodes], vocab, kind, shape, drafts, seed, temps=(0.5 if seed % 2 else 1.0,))
+        n_acc, path, nxt, status, _ = base.verify(case)
+        want, last, margin = spec_ref.verify(
+            base.f64(case["logits"]), case["tokens"][0], None if shape == "chain" else case["parents"][0],
+            None if not drafts else case["draft"].cpu().numpy(), case["temp"][0],
+            np.float32(case["u"][0]).astype(np.float64), np.float32(case["noise"][0]).astype(np.float64))
+        assert status == 0
+        if margin > base.MARGIN:
+            sure += 1
+            assert n_acc == [len(want)] and nxt == [last] and path == want + [-1] * (nodes - len(want)), seed
+            accepted += len(want)
+            rejected += len(want) < nodes - 1
+    assert sure >= 7 and rejected > 0 and accepted > 0
