@@ -525,9 +525,9 @@ int moe_kv_read(const moe_kv_cache *cache, const int32_t *slots_dev, int n_token
 
 /* Attention of drafted tokens. Sequence b has the query rows (tokens)
  * q_start_dev[b] .. q_start_dev[b + 1] - 1 (i32 [batch + 1], at most
- * MOE_MAX_DRAFT rows each, n_tokens in all) and kv_len_dev[b] (i32) tokens in
- * the cache, its query rows' own keys and values among them as the last ones;
- * token j of it is in slot j % page_size of page
+ * MOE_MAX_DRAFT rows each, n_tokens in all) and kv_len_dev[b] (i32, at most
+ * 2^31 - 256) tokens in the cache, its query rows' own keys and values among
+ * them as the last ones; token j of it is in slot j % page_size of page
  * table_dev[b * table_stride + j / page_size] (i32, table_pages entries a
  * sequence). Query row i of the sequence sees the tokens before the sequence's
  * query rows, and of those row j when bit j of mask_dev[q_start + i] (u64) is

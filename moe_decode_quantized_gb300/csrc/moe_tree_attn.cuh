@@ -30,6 +30,7 @@ namespace moe {
 
 #define MOE_TREE_WARPS 4
 #define MOE_TREE_THREADS (MOE_TREE_WARPS * 32)
+#define MOE_TREE_MAX_LEN 0x7FFFFF00
 #define MOE_TREE_DRAIN_NS 1000000ull  // a wait for what is in flight after another wait ran out: at least this long
 #define MOE_TREE_COST 24  // of an item, beside its units
 // the weights are 2^(s - m + 7): m moves when a score passes it by 8, so a
@@ -162,7 +163,8 @@ __device__ __forceinline__ void tree_sequence(const TreeArgs &a, int b, int &fir
     len = a.kv_len[b];
     const bool held = first >= 0 && n >= 0 && n <= MOE_MAX_DRAFT && first <= a.tokens - n;
     rows = held ? n : 0;
-    if (!held || len < n || len > (long long)a.table_pages * a.k.page) {
+    // (whole tiles past a length of MOE_TREE_MAX_LEN or less end below 2^31)
+    if (!held || len < n || len > min((long long)a.table_pages * a.k.page, (long long)MOE_TREE_MAX_LEN)) {
         if (!held || n > 0)
             atomicOr(a.ctrl + MOE_CTRL_STATUS, (uint32_t)MOE_WS_INDEX);
         n = 0;

@@ -440,3 +440,20 @@ def test_verify_one_sequence(kind, shape, drafts, nodes, vocab):
             accepted += len(want)
             rejected += len(want) < nodes - 1
     assert sure >= 7 and rejected > 0 and accepted > 0
+
+
+@pytest.mark.parametrize("group,rows", [(2, 2), (8, 61)])
+@pytest.mark.parametrize("length", [(1 << 31) - 1, (1 << 31) - 255])
+def test_lengths_whose_tiles_would_pass_31_bits(group, rows, length):
+    """In a table that has room for them: refused, the other sequences as ever. (As numbers of blocks and tiles
+    they would be negative.)"""
+    s = base.Sequences(moe.MOE_KV_Q8, 128, 1, group, 1024, [400, 20, 300], [rows] * 3, 45, "tree")
+    ws = s.workspace()
+    table = torch.zeros((3, 1 << 21), dtype=torch.int32, device="cuda")
+    table[:, :s.table.shape[1]] = s.table
+    s.kv_len[1] = length
+    out = torch.full_like(s.q, 5.0)
+    moe.tree_attention(s.cache, s.q, out, s.q_start, s.kv_len, table, s.mask, s.scale, ws)
+    assert moe.read_status(ws) == moe.MOE_WS_INDEX
+    s.check(out, {0, 2})  # (in other runs than beside a third sequence: other last bits)
+    assert (out[rows:2 * rows] == 0).all()
