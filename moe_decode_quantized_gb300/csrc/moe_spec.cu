@@ -407,7 +407,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     a.kv_len = kv_len_dev;
     a.table = table_dev;
     a.table_stride = table_stride;
-    a.table_pages = table_pages;
+    a.max_len = (int)std::min((long long)table_pages * a.k.page, (long long)MOE_TREE_MAX_LEN);
     a.mask = reinterpret_cast<const unsigned long long *>(mask_dev);
     a.batch = batch;
     a.tokens = n_tokens;

@@ -30,7 +30,7 @@ namespace moe {
 
 #define MOE_TREE_WARPS 4
 #define MOE_TREE_THREADS (MOE_TREE_WARPS * 32)
-#define MOE_TREE_MAX_LEN 0x7FFFFF00
+#define MOE_TREE_MAX_LEN 0x7FFFFF00   // tokens of a sequence: whole tiles past them end below 2^31
 #define MOE_TREE_DRAIN_NS 1000000ull  // a wait for what is in flight after another wait ran out: at least this long
 #define MOE_TREE_COST 24  // of an item, beside its units
 // the weights are 2^(s - m + 7): m moves when a score passes it by 8, so a
@@ -56,7 +56,7 @@ struct TreeArgs {
     const int32_t *kv_len;    // [batch]
     const int32_t *table;     // [batch, table_stride]
     long long table_stride;
-    int table_pages;          // pages a sequence can have
+    int max_len;              // tokens that a sequence can have
     const unsigned long long *mask;  // [tokens] or NULL: causal
     int batch, tokens, group;
     float scale;
@@ -163,20 +163,22 @@ __device__ __forceinline__ void tree_sequence(const TreeArgs &a, int b, int &fir
     len = a.kv_len[b];
     const bool held = first >= 0 && n >= 0 && n <= MOE_MAX_DRAFT && first <= a.tokens - n;
     rows = held ? n : 0;
-    // (whole tiles past a length of MOE_TREE_MAX_LEN or less end below 2^31)
-    if (!held || len < n || len > min((long long)a.table_pages * a.k.page, (long long)MOE_TREE_MAX_LEN)) {
+    if (!held || len < n || len > a.max_len) {
         if (!held || n > 0)
             atomicOr(a.ctrl + MOE_CTRL_STATUS, (uint32_t)MOE_WS_INDEX);
         n = 0;
     }
 }
 
+// (out of line: it is rarely needed, and the kernels' roles share the instruction cache)
+__device__ __noinline__ long long tree_div_long(long long x, long long y) { return x / y; }
+
 // x / y (x >= 0, y > 0), by a 32-bit division where both fit
 __device__ __forceinline__ long long tree_div(long long x, long long y)
 {
     if ((unsigned long long)(x | y) >> 32 == 0)
         return (uint32_t)x / (uint32_t)y;
-    return x / y;
+    return tree_div_long(x, y);
 }
 
 // zeros for the query rows of a sequence that does not hold

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
                 bulk_g2s(raw + (size_t)s * T::STAGE + lane * T::BLOCK, src, T::BLOCK, raw_full + s, policy);
         }
         for (int k = max(0, t - stages); k < t; ++k)  // nothing in flight when the memory is given back
-            tree_wait(raw_full + k % stages, (uint32_t)(k / stages) & 1u, status, max(a.wait_ns, MOE_TREE_DRAIN_NS));
+            tree_wait_on(raw_full + k % stages, (uint32_t)(k / stages) & 1u, status, max(a.wait_ns, MOE_TREE_DRAIN_NS));
     } else if (warp == MOE_TTC_SOFT + MOE_TTC_CODE + 1) {
         // ---------------- the products
         if (lane == 0) {
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(MOE_TTC_THREADS, 1) moe_tree_tc_kernel(const _
             }
             if (!ok) {  // products may be in flight: they end before tensor and shared memory are given back
                 mma_commit(drained);
-                tree_wait(drained, 0, status, max(a.wait_ns, MOE_TREE_DRAIN_NS));
+                tree_wait_on(drained, 0, status, max(a.wait_ns, MOE_TREE_DRAIN_NS));
             }
         }
     } else if (warp >= MOE_TTC_SOFT) {
