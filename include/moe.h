@@ -534,9 +534,12 @@ int moe_kv_read(const moe_kv_cache *cache, const int32_t *slots_dev, int n_token
  * set; mask_dev NULL: rows 0 .. i (a chain). A single token: one row, mask_dev
  * NULL. Per query head h, kv head h / (n_q_heads / n_kv_heads):
  *   out = sum_j softmax_j(scale q . K_j | j seen) V_j,
- * a row that sees nothing gives 0. Products of f16 roundings of the cache's
- * values (2^-12 relative) and of the query's bf16 values scaled by a power of
- * two, f32 sums; the softmax in f32, its weights rounded to f16 for the second
+ * a row that sees nothing gives 0, and a drafted token that no row of its
+ * sequence sees need not be in the cache. Products of f16 roundings of the
+ * cache's values (2^-11 relative) and of the query's bf16 values times the
+ * power of two that brings the row's largest into [2^13, 2^14) (exact down to
+ * 2^-30 of the largest, below that within 2^-25 of the scaled value), f32 sums;
+ * the softmax in f32, its weights rounded to f16 (2^-11) for the second
  * product. q, out bf16, row stride *_token_stride and head stride
  * *_head_stride in elements, dimensions contiguous. n_q_heads a multiple of
  * n_kv_heads, at most 64 a kv head. ws_dev: moe_tree_attention_workspace_bytes

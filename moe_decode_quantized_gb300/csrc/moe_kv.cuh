@@ -146,7 +146,8 @@ __host__ __device__ constexpr int kv_append_tokens() { return 32 * kv_append_val
 // piece N. The scale is rounded up and the minimum down to f16, so that no
 // code is clipped: |x - value| <= scale / 2 over the whole range. ALIGN: 32,
 // 16 or 2, what rows and strides are multiples of in bytes (65536 tokens in Q8:
-// 64, 69 and 117 us).
+// 64, 69 and 117 us; views at odd boundaries are rare, so no wider loads are
+// shifted for them).
 template <int FMT, int D, bool VALUE, int ALIGN>
 __device__ __forceinline__ void kv_append_piece(const KvArgs &a, int token, int head, int piece)
 {

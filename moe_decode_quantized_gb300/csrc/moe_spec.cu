@@ -24,7 +24,7 @@ namespace {
     } while (0)
 
 // Launches behind the stream's last kernel while that still runs (the kernels wait for its end before they touch
-// memory): one token over 511, call after call, 11.8 us a call, launched the plain way 14.3.
+// memory): one token over 511, call after call, 12.0 us a call, launched the plain way 16.4.
 template <typename... A>
 cudaError_t launch(void (*kernel)(A...), dim3 grid, int threads, size_t shared, moe_stream_t stream, A... args)
 {
@@ -120,9 +120,9 @@ VerifyKernel verify_kernel(bool f32, bool wide, bool ahead)
     return ahead ? verify_kernel<true>(f32, wide) : verify_kernel<false>(f32, wide);
 }
 
-// The rows ahead pay where the walk would go through most of them: chains (4 rows of 32000: 6.7 us, in the walk 11.5;
-// 48 x 8 of 131072: 36 and 49), and trees of few bytes (8 rows of 128000: 10 and 15 us; 24 of 100003 in f32, 9.6 MB:
-// 13.5 and 14.8; 48 rows 14.6 and 16.6). Larger trees: 96 rows 16.5 and 13.4, 384 (154 MB) 39 and 18.
+// The rows ahead pay where the walk would go through most of them: chains (4 rows of 32000: 7.2 us, in the walk 11.5;
+// 48 x 8 of 131072: 38 and 50), and trees of few bytes (8 rows of 128000: 11 and 15 us; 24 of 100003 in f32, 9.6 MB:
+// 14.2 and 14.8; 48 rows 15.4 and 16.4). Larger trees: 96 rows 17.2 and 13.4, 384 (154 MB) 40 and 18.5.
 #define MOE_VERIFY_AHEAD_BYTES (20u << 20)
 
 // ---- tree attention: instances and their launch shape
@@ -150,8 +150,8 @@ TreeInstance tree_instance()
 std::mutex g_tree_mu;
 
 // The instance for (format, head size) with at least `rows` rows a block where there is one, else the largest: a block
-// of the cache is then turned into numbers once (64 sequences of 12000 tokens, Q8, 32 rows of 128: 378 us, as two row
-// blocks 525; of 16000, 64 rows of 64: 511 us, as two 622, as four 819). Heads of 256 leave registers for 16 rows.
+// of the cache is then turned into numbers once (64 sequences of 12000 tokens, Q8, 32 rows of 128: 386 us, as two row
+// blocks 502; of 16000, 64 rows of 64: 497 us, as two 631, as four 790). Heads of 256 leave registers for 16 rows.
 int tree_choose(int fmt, int dim, int rows)
 {
     const int mt = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;
@@ -219,10 +219,11 @@ int tree_device(TreeDevice **out)
 
 // The second kernel of a call. items: about how many there are; the runs that
 // each may span decide on the instance (one sequence of 8000 tokens, 8 items of
-// 57 parts: 23 us with the small one, 17 with the large; 2 items of 228: 66 and
-// 34; 8 of 5 parts: 11.6 and 12.1; two row blocks of 4 heads over 152 runs: 118
-// and 120, 16 items over 152 runs: 28 and 33). The large one's CTAs, four an SM,
-// go through several runs each.
+// 57 parts: 21.5 us with the small one, 15.7 with the large; 2 items of 228: 65
+// and 33; 8 of 19, heads of 256: 17.7 and 15.9; two row blocks of 4 heads over 152
+// runs: 124 and 125, 16 items over 152 runs: 24.5 and 30.8; one sequence of 511,
+// whose 8 items have 4 parts and could have had 57: 11.2 and 11.7). The large
+// one's CTAs, four an SM, go through several runs each.
 using JoinKernel = void (*)(TreeArgs, int, int);
 
 template <int D>
@@ -415,7 +416,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     a.scale = scale;
     a.q_wide = aligned(q_dev, 16) && (q_token_stride | q_head_stride) % 8 == 0;
     a.o_wide = aligned(out_dev, 16) && (out_token_stride | out_head_stride) % 8 == 0;
-    a.min_units = 2 * MOE_TREE_WARPS;  // (a sequence of 511 tokens: 12.3 us, with twice that 13.3; of 8000: 24.7, 22.8)
+    a.min_units = 2 * MOE_TREE_WARPS;  // (a sequence of 511 tokens: 11.7 us, with twice that 13.0; of 8000: 15.7, 16.3)
     a.ctrl = static_cast<uint32_t *>(ws_dev);
     a.cuts = reinterpret_cast<TreeCut *>(a.ctrl + SPEC_CTRL_BYTES / 4);
     a.part = reinterpret_cast<float *>(a.cuts + MOE_TREE_MAX_GRID);
@@ -426,8 +427,8 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
         return rc;
     const int rows = (n_tokens + batch - 1) / batch * a.group;
     // The tensor-core kernel from where the warps' own products cost more than its longer steps (64 sequences of 12000
-    // tokens, Q8, 32 rows: 385 us by warps, 582 us by it; 16 of up to 16000, Q4, 32 rows: 89 and 112 us; 16 of 4000, 48
-    // rows in Q8 84 and 68 us, 64 in Q4 92 and 67 us)
+    // tokens, Q8, 32 rows: 386 us by warps, 586 us by it; 16 of up to 16000, Q4, 32 rows: 90 and 117 us; 16 of 4000, 48
+    // rows in Q8 84 and 68 us, 64 in Q4 92 and 69 us)
     if (a.k.dim == 128 && rows > 32) {
         const TtcInstance &t = dev->tc[a.k.fmt == MOE_KV_Q8 ? 0 : 1];
         const size_t used = t.fixed + 12 * ((size_t)batch + 1);
@@ -440,7 +441,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     }
     const TreeInstance &t = dev->inst[tree_choose(a.k.fmt, a.k.dim, rows)];
     // as many CTAs an SM as the registers allow while each ring keeps three stages (64 sequences of 4000 to 24000
-    // tokens: three CTAs 276 us, two 346, one 562)
+    // tokens: three CTAs 264 us, two 324, one 511)
     const size_t list = 12 * ((size_t)batch + 1), used = t.fixed + list;
     int ctas = t.ctas, stages;
     for (;; --ctas) {
@@ -519,8 +520,8 @@ int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stri
     const bool wide = aligned(logits_dev, 16) && logits_stride % (f32 ? 4 : 8) == 0 &&
                       (!draft_dev || (aligned(draft_dev, 16) && draft_stride % 4 == 0)) &&
                       (!noise_dev || (aligned(noise_dev, 16) && noise_stride % 4 == 0));
-    // a cluster of CTAs a sequence: as many as are on the GPU together (three an SM; 512 sequences of 32000: 49 us, with
-    // eight CTAs each 76), with 2048 values a CTA at least (48 sequences of 131072: 36 us, with one CTA each 95)
+    // a cluster of CTAs a sequence: as many as are on the GPU together (three an SM; 512 chains of 3 drafts over 32000: 63
+    // us, with eight CTAs each 93), with 2048 values a CTA at least (48 of 7 over 131072: 38 us, with one CTA each 99)
     const int ranks = std::max(1, std::min({MOE_VERIFY_MAX_CLUSTER, 456 / batch, vocab / 2048}));
     a.slice = ((vocab + ranks - 1) / ranks + 7) / 8 * 8;
     // all rows ahead where that is little, else as the walk reaches them
@@ -528,8 +529,8 @@ int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stri
     const bool ahead = n_rows > 0 && (all <= MOE_VERIFY_AHEAD_BYTES || !parents_dev);
     if (ahead) {
         a.batch = batch;
-        // parts of 16384 values, of down to 2048 where the rows are few (4 rows of 32000: 6.7 us, as two parts 8.7; 384
-        // of 131072: 36 us, in parts of 2048 107)
+        // parts of 16384 values, of down to 2048 where the rows are few (4 rows of 32000: 7.2 us, as two parts 9.0; 384
+        // of 131072: 38 us, in parts of 2048 109)
         a.splits = std::max(1, std::min({MOE_VERIFY_MAX_SPLITS, vocab / 2048, std::max(608 / n_rows, vocab / 16384)}));
         a.split = ((vocab + a.splits - 1) / a.splits + 7) / 8 * 8;
         a.stats = reinterpret_cast<VerifySlice *>(static_cast<char *>(ws_dev) + SPEC_CTRL_BYTES);

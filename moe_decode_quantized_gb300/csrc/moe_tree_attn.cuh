@@ -20,9 +20,10 @@
 // products, the weights as the A fragments of o += P V. 16 rows cost 32 such
 // products a unit of 128 dimensions, and 598 TFLOP/s of them were measured:
 // bound by the copies while the rows are few (64 sequences of 4000 to 24000
-// tokens, one row of 4 heads: 271 us, 95 % of the copy rate), by the turning of
-// codes and the products from some 16 rows on (64 of 12000, 32 rows: 378 us, 67
-// %), by latency for short contexts (one sequence of 511 tokens: 11.5 us).
+// tokens, one row of 4 heads: 264 us, 97 % of the copy rate), by the turning of
+// codes and the products from some 16 rows on (64 of 12000, 32 rows: 386 us, 65
+// %) and, in 4 bits, from the first (the former case 339 us, 45 % of the rate), by
+// latency for short contexts (one sequence of 511 tokens: 11.7 us).
 #pragma once
 #include "moe_kv.cuh"
 
@@ -82,7 +83,8 @@ struct TreeShape {
     static constexpr int WV = RB / 32;      // words of a lane's eighth of a V row
     static constexpr int ROWS = 16 * MT;
     static constexpr int OREGS = MT * NB * 4;
-    static constexpr int CTAS = OREGS <= 32 ? 4 : OREGS <= 64 ? 3 : 2;  // an SM, by registers
+    // CTAs an SM, by registers (heads of 64 with two and four tiles spill 44 and 28 bytes a thread within them)
+    static constexpr int CTAS = OREGS <= 32 ? 4 : OREGS <= 64 ? 3 : 2;
     static constexpr bool QREG = OREGS + MT * KS * 4 <= 96;  // query fragments kept in registers
     static constexpr int PART = ROWS * D + 2 * ROWS;         // floats of a partial
     static constexpr int BARS = 8 * 8 * MOE_TREE_WARPS;      // room for 8 stages' barriers
@@ -195,11 +197,11 @@ __device__ __forceinline__ void tree_zero(const TreeArgs &a, int first, int rows
 
 // The list is cut by cost: an item costs its units and COST more (its queries
 // are brought, its warps joined), so that no CTA gets many short items (8
-// sequences, one without a context, 20 rows a head: 90 us without, 74, 52, 46,
-// 45 with a cost of 8, 16, 24, 32; 64 sequences of 1 to 300 tokens 47 and 22 us;
-// 64 of 4000 to 24000 275, with 32 278; the tensor-core kernel's tiles of 128
-// tokens, 64 trees of up to 16 rows over 1 to 2000: 106 us without, 92 with 2, 96
-// with 6). cum [batch + 1] and items [batch + 1] are the units and the items before each
+// sequences of 8000, one without a context, up to 20 rows a head: 68 us without,
+// 43, 37, 37, 37 with a cost of 8, 16, 24, 32; 64 sequences of 1 to 300 tokens 48
+// and 21 us; 64 of 4000 to 24000 270 without, 264 with 24, 266 with 32; the
+// tensor-core kernel's tiles of 128 tokens, 64 trees of up to 16 rows over 1 to
+// 2000: 110 us without, 97 with 2, 98 with 6). cum [batch + 1] and items [batch + 1] are the units and the items before each
 // sequence; a place in the list of costs is turned into a unit by tree_place.
 
 // one item: the units [lo, lo + units) of the list
@@ -341,8 +343,9 @@ __device__ __forceinline__ void tree_next(const TreeArgs &a, const long long *cu
 
 // COUNT values (from dimension d0) of a query row that LANES neighbouring
 // lanes hold between them, as f16 pairs: the row times the power of two that
-// brings its largest magnitude below 2^14, so that f16 holds bf16's values
-// exactly (and the scale's sign). Returns what turns the row's scores into
+// brings its largest magnitude into [2^13, 2^14) (and the scale's sign). f16
+// then holds bf16's values exactly down to 2^-17, 2^-30 of the largest; smaller
+// ones lose bits to its subnormal numbers, 2^-25 at most. Returns what turns the row's scores into
 // exponents of 2. A row with a NaN or an infinity becomes a row of NaN; a row
 // that is not live (and every row for scale 0) one of zeros.
 template <int COUNT, int LANES>

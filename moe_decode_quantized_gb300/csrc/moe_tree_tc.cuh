@@ -20,14 +20,14 @@
 // V of tile t once the second product of tile t - 1 is done), one thread
 // issues the products.
 //
-// 61 rows of 8 heads over 100003 tokens take 118 us, 850 TFLOP/s of products
-// (43 % of the measured peak), 16 chains of 16 rows of 4 heads over 4000 tokens
-// 68 us. A tile of two M tiles takes some 4400 clocks: the
+// 61 rows of 8 heads over 100003 tokens take 123 us, 810 TFLOP/s of products
+// (41 % of the measured peak), 16 chains of 16 rows of 4 heads over 4000 tokens
+// 68 us. A tile of two M tiles takes some 4500 clocks: the
 // products 3300, in order and waiting once a tile for the K that takes the last
-// one's place, beside a softmax of 1950 clocks an M tile. Tiles of one M tile
-// take 3000 to 3300, bound by the turning of codes, which no more rows share. A
-// second place for K, at the price of halves of raw stages, was measured at 131
-// and 133 us and left out.
+// one's place, beside a softmax of some 2000 clocks an M tile. Tiles of one M
+// tile take 3000 to 3300, bound by the turning of codes, which no more rows
+// share. A second place for K, at the price of halves of raw stages, was measured
+// at 131 and 133 us where one place took 123 and left out.
 #pragma once
 #include "moe_tc.cuh"
 #include "moe_tree_attn.cuh"
