@@ -66,6 +66,7 @@ typedef struct CUstream_st *moe_stream_t; /* == cudaStream_t */
 #define MOE_WS_TRIPLE 4    /* moe_slot_table_set met a triple outside the table */
 #define MOE_WS_INDEX 8     /* a slot, page, length or token read on the device lay outside its table */
 #define MOE_WS_NONFINITE 16 /* a value to be quantised or a logit was NaN or infinite                */
+#define MOE_WS_PAGES 32    /* the pool had no free page left for an entry      */
 
 /* Layer configuration ([moe_v41] struct MoeV41Cfg). norm_topk_prob is 0/1. */
 typedef struct {
@@ -586,6 +587,200 @@ int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stri
                     const float *noise_dev, int64_t noise_stride, int batch, int n_rows, int vocab,
                     int32_t *n_accepted_dev, int32_t *path_dev, int32_t *next_token_dev, void *ws_dev,
                     size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions, attention with keys and values from one shared latent
+ * vector a token, and the care of a cache's pages. The pages that the rest of
+ * this header cites have no counterpart of these calls: they are what surrounds
+ * the layer step in a layer of this kind. All calls only enqueue on `stream`;
+ * status words (NULL, or a device word) receive MOE_WS_* bits. */
+
+/* Frequencies of rotary positions: pair i of dim / 2 turns by f_i = base^(-2i /
+ * dim) radians a position, scaled for contexts longer than the model's own by
+ *   MOE_ROPE_PLAIN   nothing;
+ *   MOE_ROPE_LINEAR  f_i / factor;
+ *   MOE_ROPE_BASE    the base times factor^(dim / (dim - 2)) (dim > 2);
+ *   MOE_ROPE_PARTS   f_i (k + (1 - k) / factor), k = clamp((r - slow) / (fast -
+ *                    slow), 0, 1) with r = original f_i / 2 pi the pair's turns
+ *                    in `original` positions, and the magnitude 0.1 ln(factor) + 1
+ *                    (else 1) for both results of a turn. */
+#define MOE_ROPE_PLAIN 0
+#define MOE_ROPE_LINEAR 1
+#define MOE_ROPE_BASE 2
+#define MOE_ROPE_PARTS 3
+typedef struct {
+    int32_t dim, scaling;
+    double base, factor, original, slow, fast;
+} moe_rope_cfg;
+
+/* Host: table_host[i] (dim / 2 of them) = f_i / 2 pi, the part of a turn that a
+ * position adds, times 2^64 and rounded, so that position p stands at p *
+ * table[i] mod 2^64 of a turn, exactly, for any int32 p. Copied to the device by
+ * the caller. dim even, 2 .. 1024; base, factor >= 1 (f_i of less than a turn);
+ * 0 <= slow < fast, original > 0 for MOE_ROPE_PARTS. *magnitude_host may be NULL. */
+int moe_rope_table(const moe_rope_cfg *cfg, uint64_t *table_host, float *magnitude_host);
+
+/* Which dimensions are a pair: i and i + rope_dim / 2, or 2i and 2i + 1. */
+#define MOE_ROPE_HALF 0
+#define MOE_ROPE_INTERLEAVED 1
+
+/* Rotary positions on part of each head: of x [tokens, heads, head_dim] (type
+ * MOE_BF16 or MOE_F32; token and head strides in elements, dimensions
+ * contiguous), dimensions offset .. offset + rope_dim - 1 of each row, in pairs
+ * (a, b) with angle t of the row's position (positions_dev i32 [tokens], any
+ * sign) and the pair (table_dev u64 [rope_dim / 2]):
+ *   a' = magnitude (a cos t - b sin t), b' = magnitude (a sin t + b cos t);
+ * transposed != 0: -t, the gradient's way back (with magnitude 1 also the
+ * inverse). In f32, the angle's turn rounded once to 2^-32, results rounded once.
+ * Other dimensions are copied. out may be x with the same strides (in place:
+ * other dimensions are not touched); it must not overlap x in another way.
+ * head_dim 1 .. 1024, rope_dim even, 2 .. head_dim - offset. Rows that start on
+ * 16-byte boundaries, with offset and half a rope_dim (MOE_ROPE_INTERLEAVED: a
+ * rope_dim) of whole 16-byte pieces, are moved in such pieces, others value by
+ * value. tokens or heads 0: nothing is launched. */
+int moe_rope(const void *x_dev, int64_t x_token_stride, int64_t x_head_stride, void *out_dev,
+             int64_t out_token_stride, int64_t out_head_stride, int type, int tokens, int heads, int head_dim,
+             int offset, int rope_dim, int layout, const int32_t *positions_dev, const uint64_t *table_dev,
+             float magnitude, int transposed, moe_stream_t stream);
+
+/* A cache of one layer's latent vectors: n_pages pages of page_size rows
+ * (tokens), a row latent_dim + rope_dim bf16 values, the latent vector and the
+ * part of the key that turns; slot s is row s. pages: device memory, 16-byte
+ * aligned, n_pages * moe_latent_page_bytes bytes. latent_dim 128, 256 or 512;
+ * rope_dim a multiple of 8 from 8 to 64; page_size a multiple of 16 up to 1024;
+ * n_pages * page_size below 2^31. */
+typedef struct {
+    void *pages;
+    int64_t n_pages;
+    int32_t latent_dim, rope_dim, page_size;
+} moe_latent_cache;
+
+/* Bytes of one page (pages and n_pages of the struct are not looked at). */
+int moe_latent_page_bytes(const moe_latent_cache *cache, size_t *bytes);
+
+/* Writes n_tokens rows: latent vector c_dev + t * c_stride and key part kr_dev
+ * + t * kr_stride (bf16, strides in elements) to slot slots_dev[t] (i32; -1: the
+ * token is skipped; the caller passes a slot at most once; a slot outside the
+ * cache is skipped and sets MOE_WS_INDEX). positions_dev i32 [n_tokens] and
+ * table_dev u64 [rope_dim / 2]: the key part is turned as by moe_rope with
+ * `layout` and `magnitude` on its way; both NULL: written as it is. */
+int moe_latent_append(const moe_latent_cache *cache, const void *c_dev, int64_t c_stride, const void *kr_dev,
+                      int64_t kr_stride, const int32_t *slots_dev, int n_tokens, const int32_t *positions_dev,
+                      const uint64_t *table_dev, int layout, float magnitude, uint32_t *status_dev,
+                      moe_stream_t stream);
+
+/* Reads rows back (for the expanded form, another pool or a check): c_out_dev
+ * [n_tokens, latent_dim], kr_out_dev [n_tokens, rope_dim] bf16, row strides in
+ * elements; slot -1 (or one outside the cache, which sets MOE_WS_INDEX) gives
+ * zeros. */
+int moe_latent_read(const moe_latent_cache *cache, const int32_t *slots_dev, int n_tokens, void *c_out_dev,
+                    int64_t c_stride, void *kr_out_dev, int64_t kr_stride, uint32_t *status_dev,
+                    moe_stream_t stream);
+
+/* Latent attention, absorbed form: one token, a chain or a tree of drafted
+ * tokens a sequence, all heads over the sequence's shared rows of the cache.
+ * Sequences, lengths, page table and masks are as for moe_tree_attention
+ * (q_start, kv_len, table, mask; at most MOE_MAX_DRAFT rows a sequence). For row
+ * i and head h, over the tokens j that row i sees:
+ *   out[i, h] = sum_j softmax_j(scale (q[i, h] . c_j + qr[i, h] . kr_j)) c_j,
+ * q, out [n_tokens, heads, latent_dim], qr [n_tokens, heads, rope_dim] bf16 with
+ * token and head strides in elements: q is the query times the keys'
+ * up-projection, out goes through the values' one. A row that sees nothing gives
+ * 0; a drafted token that no row of its sequence sees need not be in the cache,
+ * and a NaN or infinity in a token's row reaches only query rows that see the token. bf16
+ * products in f32 sums, the softmax in f32, its weights rounded to bf16 (2^-8)
+ * for the second product and added up as rounded. heads 1 .. 128, batch 0 ..
+ * 1024. ws_dev: moe_latent_attention_workspace_bytes bytes, initialised once
+ * (moe_workspace_init); moe_read_status gives MOE_WS_INDEX where lengths (the
+ * sequence's rows are 0), or a page (its tokens are not seen) lay outside. */
+int moe_latent_attention_workspace_bytes(const moe_latent_cache *cache, int heads, int batch, int n_tokens,
+                                         size_t *bytes);
+int moe_latent_attention(const moe_latent_cache *cache, const void *q_dev, int64_t q_token_stride,
+                         int64_t q_head_stride, const void *qr_dev, int64_t qr_token_stride, int64_t qr_head_stride,
+                         void *out_dev, int64_t out_token_stride, int64_t out_head_stride, int heads,
+                         const int32_t *q_start_dev, const int32_t *kv_len_dev, const int32_t *table_dev,
+                         int64_t table_stride, int table_pages, const uint64_t *mask_dev, int batch, int n_tokens,
+                         float scale, void *ws_dev, size_t ws_bytes, moe_stream_t stream);
+
+/* Latent attention, expanded form, for prompts: sequence b has the query rows
+ * q_start_dev[b] .. q_start_dev[b + 1] - 1 (i32 [batch + 1]) and the tokens
+ * kv_start_dev[b] .. kv_start_dev[b + 1] - 1 of k, kr and v, its query rows the
+ * last of them (earlier parts of the prompt come before). Row i of n over t
+ * tokens sees tokens 0 .. t - n + i (causal != 0) or all:
+ *   out[i, h] = sum_j softmax_j(scale (q[i, h] . [k[j, h] | kr[j]])) v[j, h],
+ * q [q_tokens, heads, nope_dim + rope_dim], k, v [kv_tokens, heads, nope_dim],
+ * kr [kv_tokens, rope_dim], out [q_tokens, heads, nope_dim], all bf16, strides
+ * in elements. A row that sees nothing gives 0 (a causal one of a sequence with
+ * fewer tokens than rows); a NaN or infinity in a token that a row does not see
+ * does not reach it. Products as for moe_latent_attention. nope_dim 64 or 128,
+ * rope_dim a multiple of 8 from 8 to 64, heads 1 .. 1024, batch 0 .. 1024. k, kr
+ * and v must start on 16-byte boundaries and have strides of multiples of 8.
+ * *status_dev receives MOE_WS_INDEX where q_start or kv_start fall or lie
+ * outside q_tokens or kv_tokens (the sequence's rows within q_tokens are 0), and
+ * MOE_WS_TIMEOUT. */
+int moe_latent_prompt_attention(const void *q_dev, int64_t q_token_stride, int64_t q_head_stride, const void *k_dev,
+                                int64_t k_token_stride, int64_t k_head_stride, const void *kr_dev, int64_t kr_stride,
+                                const void *v_dev, int64_t v_token_stride, int64_t v_head_stride, void *out_dev,
+                                int64_t out_token_stride, int64_t out_head_stride, int heads, int nope_dim,
+                                int rope_dim, const int32_t *q_start_dev, const int32_t *kv_start_dev, int batch,
+                                int q_tokens, int kv_tokens, int causal, float scale, uint32_t *status_dev,
+                                moe_stream_t stream);
+
+/* The care of pages, on the device, so that a captured step can do it. A pool
+ * counts for each page how many table entries hold it (refs_dev i32 [n_pages],
+ * 0: free; all 0 at first); a table has a row a sequence (i32 [rows, stride],
+ * table_pages entries a row; -1: none). One pool and table serve the caches of
+ * all layers. New pages are the lowest free ones, in order of rows and entries;
+ * where none is left the entry stays -1 and MOE_WS_PAGES is set. An entry, row
+ * or length outside its bounds is passed over and sets MOE_WS_INDEX. Calls on
+ * one pool must be ordered. n_pages 1 .. 2^24, rows 1 .. 1024. */
+typedef struct {
+    int32_t *refs;
+    int64_t n_pages;
+    int32_t page_size;
+} moe_page_pool;
+
+/* Gives each row a page for every entry below ceil(len_dev[row] / page_size)
+ * that is -1. */
+int moe_pages_grow(const moe_page_pool *pool, int32_t *table_dev, int64_t table_stride, int table_pages, int rows,
+                   const int32_t *len_dev, uint32_t *status_dev, moe_stream_t stream);
+
+/* Row target_dev[i] becomes a fork of row source_dev[i] (i < n): it shares the
+ * len / page_size full pages of len = kv_len_dev[source] tokens, and gets a page
+ * of its own for the rest, if any; its other entries become -1 (what it held
+ * must have been freed). copies_dev i32 [n, 2] = (page to copy from, page to copy
+ * to) for moe_pages_copy, or (-1, -1). A row may be forked many times; a target
+ * that comes twice (after its first), or a source that is also a target, is
+ * passed over and sets MOE_WS_INDEX. n 0 .. 1024. */
+int moe_pages_fork(const moe_page_pool *pool, int32_t *table_dev, int64_t table_stride, int table_pages, int rows,
+                   const int32_t *kv_len_dev, const int32_t *source_dev, const int32_t *target_dev, int n,
+                   int32_t *copies_dev, uint32_t *status_dev, moe_stream_t stream);
+
+/* Gives back all entries of rows rows_dev[i] (i < n; a row that comes twice is
+ * freed once): they become -1, and pages that no entry holds any more are free. */
+int moe_pages_free(const moe_page_pool *pool, int32_t *table_dev, int64_t table_stride, int table_pages, int rows,
+                   const int32_t *rows_dev, int n, uint32_t *status_dev, moe_stream_t stream);
+
+/* Moves the pages held to the front of the pool: with L pages held, the held
+ * pages from L on go, in order, to the free ones below L. copies_dev i32
+ * [max_copies, 2] receives (from, to), then (-1, -1); *n_copies_dev their number;
+ * refs_out_dev [n_pages] and table_out_dev (strides and rows as table) the pool's
+ * counts and the table afterwards (they may be refs and table themselves). The
+ * pages' contents are then moved by moe_pages_copy, for each cache. max_copies
+ * n_pages / 2 at least. */
+int moe_pages_compact(const moe_page_pool *pool, const int32_t *table_dev, int64_t table_stride, int table_pages,
+                      int rows, int32_t *refs_out_dev, int32_t *table_out_dev, int32_t *copies_dev, int max_copies,
+                      int32_t *n_copies_dev, uint32_t *status_dev, moe_stream_t stream);
+
+/* Copies pages of `layers` caches (of any kind: pages of page_bytes bytes, layer
+ * l's at pages_dev + l * layer_stride, n_pages of them): from copies_dev[i, 0]
+ * to copies_dev[i, 1], i < n or, where n_copies_dev is not NULL, below that count
+ * too. A negative pair is passed over; one outside the cache too, and sets
+ * MOE_WS_INDEX. No page may be copied to twice, or be copied both from and to.
+ * pages_dev, layer_stride and page_bytes multiples of 16. */
+int moe_pages_copy(void *pages_dev, int64_t layer_stride, int layers, int64_t n_pages, int64_t page_bytes,
+                   const int32_t *copies_dev, int n, const int32_t *n_copies_dev, uint32_t *status_dev,
+                   moe_stream_t stream);
 
 /* Last error message of the calling thread ("" if none). */
 const char *moe_last_error(void);

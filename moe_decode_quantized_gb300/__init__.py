@@ -23,11 +23,18 @@ MOE_WS_PLAN = 2
 MOE_WS_TRIPLE = 4
 MOE_WS_INDEX = 8
 MOE_WS_NONFINITE = 16
+MOE_WS_PAGES = 32
 MOE_KV_Q8 = 0
 MOE_KV_Q4 = 1
 MOE_MAX_DRAFT = 64
 MOE_BF16 = 0
 MOE_F32 = 1
+MOE_ROPE_PLAIN = 0
+MOE_ROPE_LINEAR = 1
+MOE_ROPE_BASE = 2
+MOE_ROPE_PARTS = 3
+MOE_ROPE_HALF = 0
+MOE_ROPE_INTERLEAVED = 1
 MOE_SHARED_BF16 = 0
 MOE_SHARED_KQUANT = 1
 MOE_GRAPH_SNAPSHOTS = 1
@@ -42,7 +49,10 @@ __all__ = ["Config", "Arena", "Layer", "MoeError", "header_words", "workspace_by
            "expert_step_unreleased", "gemm_bf16", "prefill_workspace_bytes", "prefill_step", "prefill_step_profiled", "prefill_status", "graph_snapshot_bytes", "HostSource",
            "ExpertCache", "slot_table_set", "dedupe_triples", "parse_header", "Graph",
            "KvCache", "kv_page_bytes", "kv_append", "kv_read", "tree_attention_workspace_bytes", "tree_attention",
-           "spec_verify_workspace_bytes", "spec_verify"]
+           "spec_verify_workspace_bytes", "spec_verify",
+           "rope_table", "rope", "LatentCache", "latent_page_bytes", "latent_append", "latent_read",
+           "latent_attention_workspace_bytes", "latent_attention", "latent_prompt_attention",
+           "PagePool", "pages_grow", "pages_fork", "pages_free", "pages_compact", "pages_copy"]
 
 
 class MoeError(RuntimeError):
@@ -664,5 +674,318 @@ def spec_verify(logits, q_start, tokens, parents, draft, temperature, uniforms, 
         _refuse_host(logits=logits, q_start=q_start, tokens=tokens, parents=parents, draft=draft, temperature=temperature,
                  uniforms=uniforms, noise=noise, n_accepted=n_accepted, path=path, next_token=next_token, ws=ws)
     rc = rt.lib.moe_spec_verify(*args)
+    if rc:
+        _check(rc)
+
+
+# ------------------------------------------------------------------ positions, latent attention, pages
+
+
+def _on_gpu(**tensors):
+    """Refuses the first tensor that is on the host, or on another GPU than the first of them."""
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on the GPU, not on {t.device}")
+        if device is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the arguments before it on {device}")
+        device = t.device
+
+
+def _rows3(t, name, kinds, heads, dim):
+    """Address, token stride and head stride of rows [tokens, heads, dim] with contiguous dimensions."""
+    if t.dtype not in kinds:
+        raise ValueError(f"{name} must be {kinds[0]}, not {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], not {list(shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1 and dim > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr(), st, sh
+
+
+def _rows2(t, name, kinds, rows, dim):
+    """Address and row stride of rows [at least `rows`, dim] with contiguous dimensions."""
+    if t.dtype not in kinds:
+        raise ValueError(f"{name} must be {kinds[0]}, not {t.dtype}")
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != dim:
+        raise ValueError(f"{name} must be [{rows}, {dim}], not {list(t.shape)}")
+    if t.stride(1) != 1 and dim > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr(), t.stride(0)
+
+
+def _distinct(t, name):
+    """Refuses an output whose rows share memory (an expanded tensor)."""
+    if any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
+        raise ValueError(f"{name} is an output: its rows must not share memory")
+
+
+def rope_table(dim: int, base: float = 10000.0, scaling: int = MOE_ROPE_PLAIN, factor: float = 1.0,
+               original: float = 4096.0, slow: float = 1.0, fast: float = 32.0):
+    """-> (frequencies uint64 numpy [dim / 2], magnitude): the part of a turn that a position adds, times 2^64
+    (include/moe.h, moe_rope_table). On the device: torch.from_numpy(table.view(numpy.int64)).cuda()."""
+    table = np.zeros(max(int(dim), 2) // 2, np.uint64)
+    magnitude = C.c_float(1.0)
+    cfg = _lib.MoeRopeCfg(dim, scaling, base, factor, original, slow, fast)
+    _check(_lib.moe().moe_rope_table(C.byref(cfg), C.c_void_p(table.ctypes.data), C.byref(magnitude)))
+    return table, magnitude.value
+
+
+def rope(x, out, positions, table, offset: int = 0, layout: int = MOE_ROPE_HALF, magnitude: float = 1.0,
+         transposed: bool = False, stream=None):
+    """Rotary positions on dimensions offset .. offset + 2 * table.numel() - 1 of each head (include/moe.h, moe_rope):
+    x, out bf16 or f32 [tokens, heads, head_dim], any strides of the first two (out may be x), positions int32
+    [tokens], table int64 (rope_table's). transposed: turned back, as a gradient is."""
+    rt = _runtime()
+    kind = x.dtype
+    if kind is not rt.bf16 and kind is not rt.f32:
+        raise ValueError(f"x must be bfloat16 or float32, not {kind}")
+    if x.dim() != 3 or out.shape != x.shape:
+        raise ValueError(f"x and out must both be [tokens, heads, head_dim], not {list(x.shape)} and {list(out.shape)}")
+    tokens, heads, dim = x.shape
+    if table.dtype not in rt.bits:
+        raise ValueError(f"table must be int64, not {table.dtype}")
+    _distinct(out, "out")
+    args = (*_rows3(x, "x", (kind,), heads, dim), *_rows3(out, "out", (kind,), heads, dim),
+            MOE_F32 if kind is rt.f32 else MOE_BF16, tokens, heads, dim, offset, 2 * table.numel(), layout,
+            _dev(positions, "positions", rt.i32, tokens), _dev(table, "table", table.dtype, 1), magnitude, int(transposed),
+            _on(rt, stream))
+    _on_gpu(x=x, out=out, positions=positions, table=table)
+    rc = rt.lib.moe_rope(*args)
+    if rc:
+        _check(rc)
+
+
+@dataclass
+class LatentCache:
+    """A paged cache of latent vectors (include/moe.h, moe_latent_cache). pages: device tensor of whole pages
+    (latent_page_bytes each), rows of latent_dim + rope_dim bf16 values."""
+    pages: object
+    latent_dim: int
+    rope_dim: int
+    page_size: int = 64
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_ref", None)
+
+    def __post_init__(self):
+        self.ref()
+
+    @property
+    def n_pages(self) -> int:
+        if self.pages is None:
+            return 0
+        per, size = latent_page_bytes(self), self.pages.numel() * self.pages.element_size()
+        if size % per:
+            raise ValueError(f"pages holds {size} bytes, not a multiple of a page's {per}")
+        return size // per
+
+    def ref(self):
+        """The C struct by reference, made again after a field was set or the pages tensor got other memory."""
+        pages = self.pages
+        at = None if pages is None else (pages.data_ptr(), pages.numel())
+        if self._ref is None or at != self._at:
+            c = _lib.MoeLatentCache(_ptr(pages), self.n_pages, self.latent_dim, self.rope_dim, self.page_size)
+            object.__setattr__(self, "_ref", C.byref(c))
+            object.__setattr__(self, "_at", at)
+        return self._ref
+
+
+def latent_page_bytes(cache: LatentCache) -> int:
+    b = C.c_size_t(0)
+    c = _lib.MoeLatentCache(None, 0, cache.latent_dim, cache.rope_dim, cache.page_size)
+    _check(_lib.moe().moe_latent_page_bytes(C.byref(c), C.byref(b)))
+    return b.value
+
+
+def latent_append(cache: LatentCache, c, k_rope, slots, positions=None, table=None, layout: int = MOE_ROPE_HALF,
+                  magnitude: float = 1.0, status=None, stream=None):
+    """Write rows into slots (int32 [tokens], -1: skipped): latent vectors c [tokens, latent_dim] and key parts k_rope
+    [tokens, rope_dim] (bf16, any row strides), the latter turned by positions (int32 [tokens]) and table (rope_table's)
+    where they are given. status: None, or a device word (int32) that receives MOE_WS_* bits."""
+    rt = _runtime()
+    n = c.shape[0]
+    if n != k_rope.shape[0]:
+        raise ValueError("c and k_rope must have the same number of tokens")
+    if table is not None and (table.dtype not in rt.bits or 2 * table.numel() != cache.rope_dim):
+        raise ValueError(f"table must be int64 of {cache.rope_dim // 2} values, not {table.dtype} of {table.numel()}")
+    args = (cache.ref(), *_rows2(c, "c", rt.rows, n, cache.latent_dim),
+            *_rows2(k_rope, "k_rope", rt.rows, n, cache.rope_dim), _dev(slots, "slots", rt.i32, n), n,
+            _dev(positions, "positions", rt.i32, n), None if table is None else _dev(table, "table", table.dtype, 1),
+            layout, magnitude, _dev(status, "status", rt.i32, 1), _on(rt, stream))
+    _on_gpu(pages=cache.pages, c=c, k_rope=k_rope, slots=slots, positions=positions, table=table, status=status)
+    rc = rt.lib.moe_latent_append(*args)
+    if rc:
+        _check(rc)
+
+
+def latent_read(cache: LatentCache, slots, c_out, k_rope_out, status=None, stream=None):
+    """Rows of the cache: c_out [tokens, latent_dim], k_rope_out [tokens, rope_dim], bf16, any row strides."""
+    rt = _runtime()
+    n = slots.numel()
+    for t, name in ((c_out, "c_out"), (k_rope_out, "k_rope_out")):
+        _distinct(t, name)
+    args = (cache.ref(), _dev(slots, "slots", rt.i32, n), n, *_rows2(c_out, "c_out", rt.rows, n, cache.latent_dim),
+            *_rows2(k_rope_out, "k_rope_out", rt.rows, n, cache.rope_dim), _dev(status, "status", rt.i32, 1),
+            _on(rt, stream))
+    _on_gpu(pages=cache.pages, slots=slots, c_out=c_out, k_rope_out=k_rope_out, status=status)
+    rc = rt.lib.moe_latent_read(*args)
+    if rc:
+        _check(rc)
+
+
+def latent_attention_workspace_bytes(cache: LatentCache, heads: int, batch: int, n_tokens: int) -> int:
+    b = C.c_size_t(0)
+    _check(_lib.moe().moe_latent_attention_workspace_bytes(cache.ref(), heads, batch, n_tokens, C.byref(b)))
+    return b.value
+
+
+def latent_attention(cache: LatentCache, q, q_rope, out, q_start, kv_len, table, mask, scale: float, ws, stream=None):
+    """Latent attention in absorbed form (include/moe.h, moe_latent_attention): q, out bf16 [tokens, heads, latent_dim],
+    q_rope bf16 [tokens, heads, rope_dim]; the others as for tree_attention."""
+    rt = _runtime()
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError("q must be [tokens, heads, latent_dim] and out have its shape")
+    n, heads = q.shape[:2]
+    if q_rope.shape[0] != n:
+        raise ValueError("q and q_rope must have the same number of tokens")
+    batch = kv_len.numel()
+    if mask is not None and mask.dtype not in rt.bits:
+        raise ValueError(f"mask must be int64, not {mask.dtype}")
+    _distinct(out, "out")
+    tp, ts = _matrix(table, "table", rt.i32, batch, table.shape[-1])
+    args = (cache.ref(), *_rows3(q, "q", rt.rows, heads, cache.latent_dim),
+            *_rows3(q_rope, "q_rope", rt.rows, heads, cache.rope_dim), *_rows3(out, "out", rt.rows, heads, cache.latent_dim),
+            heads, _dev(q_start, "q_start", rt.i32, batch + 1), _dev(kv_len, "kv_len", rt.i32, batch), tp, ts,
+            table.shape[1], None if mask is None else _dev(mask, "mask", mask.dtype, n), batch, n, scale,
+            *_bytes(ws), _on(rt, stream))
+    _on_gpu(pages=cache.pages, q=q, q_rope=q_rope, out=out, q_start=q_start, kv_len=kv_len, table=table, mask=mask, ws=ws)
+    rc = rt.lib.moe_latent_attention(*args)
+    if rc:
+        _check(rc)
+
+
+def latent_prompt_attention(q, k, k_rope, v, out, q_start, kv_start, causal: bool, scale: float, status=None, stream=None):
+    """Latent attention in expanded form, for prompts (include/moe.h, moe_latent_prompt_attention): q bf16 [q tokens,
+    heads, nope + rope], k, v [kv tokens, heads, nope], k_rope [kv tokens, rope], out [q tokens, heads, nope], any token
+    and head strides; q_start, kv_start int32 [batch + 1]."""
+    rt = _runtime()
+    if q.dim() != 3 or k.dim() != 3 or k_rope.dim() != 2:
+        raise ValueError("q and k must be [tokens, heads, dims], k_rope [tokens, dims]")
+    n, heads, t, nope, rope_dim = q.shape[0], q.shape[1], k.shape[0], k.shape[2], k_rope.shape[1]
+    if v.shape != k.shape or k_rope.shape[0] != t:
+        raise ValueError("k, v and k_rope must have the same number of tokens, v k's shape")
+    if out.shape[0] != n:
+        raise ValueError("out must have q's number of tokens")
+    batch = q_start.numel() - 1
+    _distinct(out, "out")
+    args = (*_rows3(q, "q", rt.rows, heads, nope + rope_dim), *_rows3(k, "k", rt.rows, heads, nope),
+            *_rows2(k_rope, "k_rope", rt.rows, t, rope_dim), *_rows3(v, "v", rt.rows, heads, nope),
+            *_rows3(out, "out", rt.rows, heads, nope), heads, nope, rope_dim,
+            _dev(q_start, "q_start", rt.i32, max(batch + 1, 1)), _dev(kv_start, "kv_start", rt.i32, max(batch + 1, 1)),
+            max(batch, 0), n, t, int(bool(causal)), scale, _dev(status, "status", rt.i32, 1), _on(rt, stream))
+    _on_gpu(q=q, k=k, k_rope=k_rope, v=v, out=out, q_start=q_start, kv_start=kv_start, status=status)
+    rc = rt.lib.moe_latent_prompt_attention(*args)
+    if rc:
+        _check(rc)
+
+
+@dataclass
+class PagePool:
+    """A pool of pages (include/moe.h, moe_page_pool). refs: int32 device tensor, how many table entries hold each page."""
+    refs: object
+    page_size: int = 64
+
+    def c(self) -> _lib.MoePagePool:
+        if self.refs.dtype is not _runtime().i32:
+            raise ValueError(f"refs must be int32, not {self.refs.dtype}")
+        return _lib.MoePagePool(_ptr(self.refs), self.refs.numel(), self.page_size)
+
+
+def _pool_table(rt, pool, table, name="table"):
+    if table.dim() != 2:
+        raise ValueError(f"{name} must be [rows, pages], not {list(table.shape)}")
+    rows, pages = table.shape
+    _distinct(table, name)
+    p, stride = _matrix(table, name, rt.i32, rows, pages)
+    return C.byref(pool.c()), p, stride, pages, rows
+
+
+def pages_grow(pool: PagePool, table, lengths, status=None, stream=None):
+    """Give each row of the table (int32 [rows, pages], -1: none) the pages that lengths (int32 [rows]) tokens need
+    (include/moe.h, moe_pages_grow)."""
+    rt = _runtime()
+    args = (*_pool_table(rt, pool, table), _dev(lengths, "lengths", rt.i32, table.shape[0]),
+            _dev(status, "status", rt.i32, 1), _on(rt, stream))
+    _on_gpu(refs=pool.refs, table=table, lengths=lengths, status=status)
+    rc = rt.lib.moe_pages_grow(*args)
+    if rc:
+        _check(rc)
+
+
+def pages_fork(pool: PagePool, table, kv_len, source, target, copies, status=None, stream=None):
+    """Row target[i] of the table becomes a fork of row source[i] (include/moe.h, moe_pages_fork): full pages shared, a
+    part-filled last one to be copied as copies [n, 2] (int32) says (pages_copy). kv_len int32 [rows]."""
+    rt = _runtime()
+    n = source.numel()
+    args = (*_pool_table(rt, pool, table), _dev(kv_len, "kv_len", rt.i32, table.shape[0]),
+            _dev(source, "source", rt.i32, n), _dev(target, "target", rt.i32, n), n,
+            _dev(copies, "copies", rt.i32, 2 * n), _dev(status, "status", rt.i32, 1), _on(rt, stream))
+    _on_gpu(refs=pool.refs, table=table, kv_len=kv_len, source=source, target=target, copies=copies, status=status)
+    rc = rt.lib.moe_pages_fork(*args)
+    if rc:
+        _check(rc)
+
+
+def pages_free(pool: PagePool, table, rows, status=None, stream=None):
+    """Give back the pages of the table's rows `rows` (int32); their entries become -1."""
+    rt = _runtime()
+    args = (*_pool_table(rt, pool, table), _dev(rows, "rows", rt.i32, 0), rows.numel(),
+            _dev(status, "status", rt.i32, 1), _on(rt, stream))
+    _on_gpu(refs=pool.refs, table=table, rows=rows, status=status)
+    rc = rt.lib.moe_pages_free(*args)
+    if rc:
+        _check(rc)
+
+
+def pages_compact(pool: PagePool, table, refs_out, table_out, copies, n_copies, status=None, stream=None):
+    """Move the pages held to the pool's front (include/moe.h, moe_pages_compact): counts and table afterwards in
+    refs_out and table_out (which may be pool.refs and table), the moves in copies [at least n_pages / 2, 2] and
+    n_copies [1] (int32) for pages_copy."""
+    rt = _runtime()
+    if table_out.shape != table.shape or table_out.stride() != table.stride():
+        raise ValueError("table_out must have the table's shape and strides")
+    head = _pool_table(rt, pool, table)
+    args = (*head, _dev(refs_out, "refs_out", rt.i32, pool.refs.numel()), _pool_table(rt, pool, table_out, "table_out")[1],
+            _dev(copies, "copies", rt.i32, 2), copies.numel() // 2, _dev(n_copies, "n_copies", rt.i32, 1),
+            _dev(status, "status", rt.i32, 1), _on(rt, stream))
+    _on_gpu(refs=pool.refs, table=table, refs_out=refs_out, table_out=table_out, copies=copies, n_copies=n_copies,
+            status=status)
+    rc = rt.lib.moe_pages_compact(*args)
+    if rc:
+        _check(rc)
+
+
+def pages_copy(pages, copies, n_copies=None, status=None, stream=None):
+    """Copy pages as copies [n, 2] (int32: from, to) says, n_copies [1] of them where it is given, in every layer of
+    pages [layers, n_pages, ...] (each layer contiguous; include/moe.h, moe_pages_copy)."""
+    rt = _runtime()
+    if pages.dim() < 3:
+        raise ValueError(f"pages must be [layers, n_pages, ...], not {list(pages.shape)}")
+    layers, n_pages = pages.shape[:2]
+    size = pages.element_size()
+    if layers and not pages[0].is_contiguous():
+        raise ValueError("each layer of pages must be contiguous")
+    _distinct(pages, "pages")
+    per = pages[0, 0].numel() * size if layers and n_pages else 0
+    args = (pages.data_ptr(), pages.stride(0) * size, layers, n_pages, per, _dev(copies, "copies", rt.i32, 0),
+            copies.numel() // 2, _dev(n_copies, "n_copies", rt.i32, 1), _dev(status, "status", rt.i32, 1), _on(rt, stream))
+    _on_gpu(pages=pages, copies=copies, n_copies=n_copies, status=status)
+    rc = rt.lib.moe_pages_copy(*args)
     if rc:
         _check(rc)

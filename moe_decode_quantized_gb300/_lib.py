@@ -41,6 +41,19 @@ class MoeKvCache(C.Structure):
                 ("page_size", I32), ("format", I32)]
 
 
+class MoeRopeCfg(C.Structure):
+    _fields_ = [("dim", I32), ("scaling", I32), ("base", C.c_double), ("factor", C.c_double), ("original", C.c_double),
+                ("slow", C.c_double), ("fast", C.c_double)]
+
+
+class MoeLatentCache(C.Structure):
+    _fields_ = [("pages", P), ("n_pages", C.c_int64), ("latent_dim", I32), ("rope_dim", I32), ("page_size", I32)]
+
+
+class MoePagePool(C.Structure):
+    _fields_ = [("refs", P), ("n_pages", C.c_int64), ("page_size", I32)]
+
+
 class MoeWsView(C.Structure):
     _fields_ = [("logits", P), ("plan_w", P), ("plan_rows", P), ("ptrs", P), ("g", P), ("u", P),
                 ("gs", P), ("us", P), ("down", P), ("sd", P), ("acc", P), ("status", P)]
@@ -111,6 +124,25 @@ MOE_SYMBOLS = {
     "moe_spec_verify_workspace_bytes": (C.c_int, [C.c_int, C.c_int, C.POINTER(SZ)]),
     "moe_spec_verify": (C.c_int, [P, C.c_int, I64, P, P, P, P, I64, P, P, P, I64, C.c_int, C.c_int, C.c_int, P, P,
                                   P, P, SZ, P]),
+    "moe_rope_table": (C.c_int, [C.POINTER(MoeRopeCfg), P, C.POINTER(C.c_float)]),
+    "moe_rope": (C.c_int, [P, I64, I64, P, I64, I64, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, P, P,
+                           C.c_float, C.c_int, P]),
+    "moe_latent_page_bytes": (C.c_int, [C.POINTER(MoeLatentCache), C.POINTER(SZ)]),
+    "moe_latent_append": (C.c_int, [C.POINTER(MoeLatentCache), P, I64, P, I64, P, C.c_int, P, P, C.c_int, C.c_float, P,
+                                    P]),
+    "moe_latent_read": (C.c_int, [C.POINTER(MoeLatentCache), P, C.c_int, P, I64, P, I64, P, P]),
+    "moe_latent_attention_workspace_bytes": (C.c_int, [C.POINTER(MoeLatentCache), C.c_int, C.c_int, C.c_int,
+                                                       C.POINTER(SZ)]),
+    "moe_latent_attention": (C.c_int, [C.POINTER(MoeLatentCache), P, I64, I64, P, I64, I64, P, I64, I64, C.c_int, P, P, P,
+                                       I64, C.c_int, P, C.c_int, C.c_int, C.c_float, P, SZ, P]),
+    "moe_latent_prompt_attention": (C.c_int, [P, I64, I64, P, I64, I64, P, I64, P, I64, I64, P, I64, I64, C.c_int,
+                                              C.c_int, C.c_int, P, P, C.c_int, C.c_int, C.c_int, C.c_int, C.c_float, P,
+                                              P]),
+    "moe_pages_grow": (C.c_int, [C.POINTER(MoePagePool), P, I64, C.c_int, C.c_int, P, P, P]),
+    "moe_pages_fork": (C.c_int, [C.POINTER(MoePagePool), P, I64, C.c_int, C.c_int, P, P, P, C.c_int, P, P, P]),
+    "moe_pages_free": (C.c_int, [C.POINTER(MoePagePool), P, I64, C.c_int, C.c_int, P, C.c_int, P, P]),
+    "moe_pages_compact": (C.c_int, [C.POINTER(MoePagePool), P, I64, C.c_int, C.c_int, P, P, P, C.c_int, P, P, P]),
+    "moe_pages_copy": (C.c_int, [P, I64, C.c_int, I64, I64, P, C.c_int, P, P, P]),
     "moe_last_error": (C.c_char_p, []),
 }
 

@@ -1,6 +1,6 @@
 """Builds the in-tree CUDA libraries for sm_103a with nvcc.
 
-libmoe.so        the engine (csrc/moe_abi.cu, csrc/moe_spec.cu and the kernels
+libmoe.so        the engine (csrc/moe_abi.cu, moe_spec.cu, moe_latent.cu, moe_pages.cu and the kernels
                  they include)
 libmoe_synth.so  the device twin of the synthetic-input generator
 
@@ -44,7 +44,7 @@ def _stale(out: str, deps) -> bool:
 def targets():
     hdrs = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     return [
-        (LIBMOE, [os.path.join(CSRC, f) for f in ("moe_abi.cu", "moe_spec.cu")], hdrs),
+        (LIBMOE, [os.path.join(CSRC, f) for f in ("moe_abi.cu", "moe_spec.cu", "moe_latent.cu", "moe_pages.cu")], hdrs),
         (LIBSYNTH, [os.path.join(CSRC, "moe_synth.cu")], [os.path.join(INCLUDE, "moe_synth.h")]),
     ]
 

@@ -1,0 +1,382 @@
+// moe_latent.cu -- the entry points of libmoe.so for rotary positions, the cache
+// of latent vectors and attention over it (declared and documented in
+// include/moe.h). Argument checks, workspace layout and launches.
+#include <math.h>
+
+#include <algorithm>
+
+#include "moe_latent_attn.cuh"
+#include "moe_launch.cuh"
+
+using namespace moe;
+
+namespace {
+
+#define LATENT_CTRL_BYTES 256  // control words: the status is word MOE_CTRL_STATUS
+
+int check_shape(const moe_latent_cache *c)
+{
+    if (!c)
+        return host_fail(MOE_EINVAL, "cache is NULL");
+    if (c->latent_dim < 1 || c->rope_dim < 1 || c->page_size < 1)
+        return host_fail(MOE_EINVAL, "latent_dim (%d), rope_dim (%d) and page_size (%d) must be positive", c->latent_dim,
+                         c->rope_dim, c->page_size);
+    if ((c->latent_dim != 128 && c->latent_dim != 256 && c->latent_dim != 512) || c->rope_dim % 8 || c->rope_dim > 64 ||
+        c->page_size % 16 || c->page_size > 1024)
+        return host_fail(MOE_EUNSUPPORTED, "latent_dim (%d) of 128, 256 or 512, rope_dim (%d) a multiple of 8 up to 64, "
+                         "page_size (%d) a multiple of 16 up to 1024", c->latent_dim, c->rope_dim, c->page_size);
+    return MOE_OK;
+}
+
+int check_cache(const moe_latent_cache *c)
+{
+    const int rc = check_shape(c);
+    if (rc)
+        return rc;
+    if (!c->pages || !aligned(c->pages, 16))
+        return host_fail(MOE_EINVAL, "the cache's pages are NULL or not 16-byte aligned");
+    if (c->n_pages < 1 || c->n_pages > 0x7FFFFFFFll / c->page_size)
+        return host_fail(MOE_EINVAL, "n_pages (%lld) must be positive and n_pages * page_size below 2^31",
+                         (long long)c->n_pages);
+    return MOE_OK;
+}
+
+bool wide_rows(const void *p, int64_t s0, int64_t s1) { return aligned(p, 16) && (s0 | s1) % 8 == 0; }
+
+// rows of the latent cache, in or out
+int latent_rows(bool read, LatentRows &a, const moe_latent_cache *cache, moe_stream_t stream)
+{
+    a.pages = static_cast<uint16_t *>(cache->pages);
+    a.n_slots = cache->n_pages * cache->page_size;
+    a.latent = cache->latent_dim;
+    a.rope = cache->rope_dim;
+    a.c_wide = wide_rows(a.c, a.c_stride, 0);
+    a.kr_wide = wide_rows(a.kr, a.kr_stride, 0);
+    const long long pieces = (long long)a.tokens * (a.latent / 8);
+    const dim3 grid((unsigned)((pieces + MOE_LATENT_THREADS - 1) / MOE_LATENT_THREADS), 2);
+    MOE_CUDA_OK(launch(read ? moe_latent_rows_kernel<true> : moe_latent_rows_kernel<false>, grid, MOE_LATENT_THREADS, 0,
+                       stream, a));
+    return MOE_OK;
+}
+
+using RopeKernel = void (*)(RopeArgs);
+
+template <bool F32, bool WIDE>
+RopeKernel rope_kernel(bool inter)
+{
+    return inter ? moe_rope_kernel<F32, WIDE, true> : moe_rope_kernel<F32, WIDE, false>;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_rope_table(const moe_rope_cfg *cfg, uint64_t *table_host, float *magnitude_host)
+{
+    if (!cfg || !table_host)
+        return host_fail(MOE_EINVAL, "moe_rope_table: NULL argument");
+    const int dim = cfg->dim;
+    if (dim < 2 || dim % 2)
+        return host_fail(MOE_EINVAL, "moe_rope_table: dim (%d) must be even and positive", dim);
+    if (dim > 1024)
+        return host_fail(MOE_EUNSUPPORTED, "moe_rope_table: dim (%d) <= 1024", dim);
+    if (cfg->scaling < MOE_ROPE_PLAIN || cfg->scaling > MOE_ROPE_PARTS)
+        return host_fail(MOE_EINVAL, "moe_rope_table: scaling %d", cfg->scaling);
+    const bool scaled = cfg->scaling != MOE_ROPE_PLAIN, parts = cfg->scaling == MOE_ROPE_PARTS;
+    if (!(cfg->base >= 1.0 && cfg->base < 1e30) || (scaled && !(cfg->factor >= 1.0 && cfg->factor < 1e30)))
+        return host_fail(MOE_EINVAL, "moe_rope_table: base (%g) and factor (%g) must be at least 1 and finite", cfg->base,
+                         cfg->factor);
+    if (cfg->scaling == MOE_ROPE_BASE && dim == 2)
+        return host_fail(MOE_EINVAL, "moe_rope_table: dim 2 has no base to scale");
+    if (parts && !(cfg->slow >= 0.0 && cfg->fast > cfg->slow && cfg->fast < 1e30 && cfg->original > 0.0 &&
+                   cfg->original < 1e30))
+        return host_fail(MOE_EINVAL, "moe_rope_table: 0 <= slow (%g) < fast (%g) and original (%g) > 0", cfg->slow,
+                         cfg->fast, cfg->original);
+    const double turn = 6.283185307179586476925286766559;
+    const double base = cfg->scaling == MOE_ROPE_BASE ? cfg->base * pow(cfg->factor, (double)dim / (dim - 2)) : cfg->base;
+    for (int i = 0; i < dim / 2; ++i) {
+        double f = pow(base, -2.0 * i / dim);
+        if (cfg->scaling == MOE_ROPE_LINEAR)
+            f /= cfg->factor;
+        if (parts) {
+            const double r = cfg->original * f / turn;
+            const double k = std::min(std::max((r - cfg->slow) / (cfg->fast - cfg->slow), 0.0), 1.0);
+            f *= k + (1.0 - k) / cfg->factor;
+        }
+        table_host[i] = (uint64_t)rint(f / turn * 18446744073709551616.0);  // below 2^62: f is 1 at most
+    }
+    if (magnitude_host)
+        *magnitude_host = parts ? (float)(0.1 * log(cfg->factor) + 1.0) : 1.0f;
+    return MOE_OK;
+}
+
+int moe_rope(const void *x_dev, int64_t x_token_stride, int64_t x_head_stride, void *out_dev, int64_t out_token_stride,
+             int64_t out_head_stride, int type, int tokens, int heads, int head_dim, int offset, int rope_dim, int layout,
+             const int32_t *positions_dev, const uint64_t *table_dev, float magnitude, int transposed, moe_stream_t stream)
+{
+    if (type != MOE_BF16 && type != MOE_F32)
+        return host_fail(MOE_EINVAL, "moe_rope: type %d", type);
+    if (layout != MOE_ROPE_HALF && layout != MOE_ROPE_INTERLEAVED)
+        return host_fail(MOE_EINVAL, "moe_rope: layout %d", layout);
+    if (tokens < 0 || heads < 0 || head_dim < 1 || offset < 0 || rope_dim < 2 || rope_dim % 2 || rope_dim > head_dim ||
+        offset > head_dim - rope_dim)
+        return host_fail(MOE_EINVAL, "moe_rope: tokens (%d) and heads (%d) must not be negative, rope_dim (%d) even, from 2 "
+                         "to head_dim (%d) - offset (%d)", tokens, heads, rope_dim, head_dim, offset);
+    if (head_dim > 1024 || heads > 65536)
+        return host_fail(MOE_EUNSUPPORTED, "moe_rope: head_dim (%d) <= 1024, heads (%d) <= 65536", head_dim, heads);
+    if (!(magnitude >= -3.0e38f && magnitude <= 3.0e38f))
+        return host_fail(MOE_EINVAL, "moe_rope: magnitude must be finite");
+    if (tokens == 0 || heads == 0)
+        return MOE_OK;
+    if (!x_dev || !out_dev || !positions_dev || !table_dev)
+        return host_fail(MOE_EINVAL, "moe_rope: NULL argument");
+    const bool f32 = type == MOE_F32;
+    const int size = f32 ? 4 : 2;
+    if (!aligned(x_dev, size) || !aligned(out_dev, size) || !aligned(positions_dev, 4) || !aligned(table_dev, 8))
+        return host_fail(MOE_EINVAL, "moe_rope: an argument is not aligned to its type");
+    const bool in_place = x_dev == out_dev;
+    if (in_place && ((tokens > 1 && x_token_stride != out_token_stride) || (heads > 1 && x_head_stride != out_head_stride)))
+        return host_fail(MOE_EINVAL, "moe_rope: in place, the strides of x and out must be the same");
+    const bool inter = layout == MOE_ROPE_INTERLEAVED;
+    const int v = 16 / size;
+    const bool wide = aligned(x_dev, 16) && aligned(out_dev, 16) && head_dim % v == 0 && offset % v == 0 &&
+                      (inter ? rope_dim : rope_dim / 2) % v == 0 &&
+                      (x_token_stride | x_head_stride | out_token_stride | out_head_stride) % v == 0;
+    RopeArgs a{};
+    a.x = x_dev;
+    a.out = out_dev;
+    a.x_tok = x_token_stride;
+    a.x_head = x_head_stride;
+    a.o_tok = out_token_stride;
+    a.o_head = out_head_stride;
+    a.tokens = tokens;
+    a.heads = heads;
+    a.dim = head_dim;
+    a.offset = offset;
+    a.rope = rope_dim;
+    a.positions = positions_dev;
+    a.table = reinterpret_cast<const unsigned long long *>(table_dev);
+    a.magnitude = magnitude;
+    a.sign = transposed ? -1.0f : 1.0f;
+    a.turned = wide ? (inter ? rope_dim : rope_dim / 2) / v : rope_dim / 2;
+    a.items = a.turned + (in_place ? 0 : (head_dim - rope_dim) / (wide ? v : 1));
+    a.heads_cta = std::min(heads, MOE_ROPE_HEADS);
+    // a CTA some 2048 pieces, and every SM a few CTAs
+    const long long per = (long long)a.heads_cta * a.items;
+    a.tokens_cta = (int)std::max(1ll, std::min({2048 / per, tokens / 608ll, MOE_ROPE_SMEM / (4ll * rope_dim)}));
+    const dim3 grid((unsigned)((tokens + a.tokens_cta - 1) / a.tokens_cta),
+                    (unsigned)((heads + a.heads_cta - 1) / a.heads_cta));
+    const RopeKernel kernel = f32 ? (wide ? rope_kernel<true, true>(inter) : rope_kernel<true, false>(inter))
+                                  : (wide ? rope_kernel<false, true>(inter) : rope_kernel<false, false>(inter));
+    MOE_CUDA_OK(launch(kernel, grid, MOE_ROPE_THREADS, (size_t)a.tokens_cta * rope_dim * 4, stream, a));
+    return MOE_OK;
+}
+
+int moe_latent_page_bytes(const moe_latent_cache *cache, size_t *bytes)
+{
+    const int rc = check_shape(cache);
+    if (rc)
+        return rc;
+    if (!bytes)
+        return host_fail(MOE_EINVAL, "bytes is NULL");
+    *bytes = (size_t)cache->page_size * (cache->latent_dim + cache->rope_dim) * 2;
+    return MOE_OK;
+}
+
+int moe_latent_append(const moe_latent_cache *cache, const void *c_dev, int64_t c_stride, const void *kr_dev,
+                      int64_t kr_stride, const int32_t *slots_dev, int n_tokens, const int32_t *positions_dev,
+                      const uint64_t *table_dev, int layout, float magnitude, uint32_t *status_dev, moe_stream_t stream)
+{
+    const int rc = check_cache(cache);
+    if (rc)
+        return rc;
+    if (n_tokens < 0 || (n_tokens > 0 && (!c_dev || !kr_dev || !slots_dev)))
+        return host_fail(MOE_EINVAL, "moe_latent_append: NULL argument or n_tokens (%d) < 0", n_tokens);
+    if ((positions_dev == nullptr) != (table_dev == nullptr))
+        return host_fail(MOE_EINVAL, "moe_latent_append: positions and table go together");
+    if (layout != MOE_ROPE_HALF && layout != MOE_ROPE_INTERLEAVED)
+        return host_fail(MOE_EINVAL, "moe_latent_append: layout %d", layout);
+    if (!(magnitude >= -3.0e38f && magnitude <= 3.0e38f))
+        return host_fail(MOE_EINVAL, "moe_latent_append: magnitude must be finite");
+    if (!aligned(c_dev, 2) || !aligned(kr_dev, 2) || !aligned(slots_dev, 4) || !aligned(positions_dev, 4) ||
+        !aligned(table_dev, 8) || !aligned(status_dev, 4))
+        return host_fail(MOE_EINVAL, "moe_latent_append: an argument is not aligned to its type");
+    if (n_tokens == 0)
+        return MOE_OK;
+    LatentRows a{};
+    a.c = static_cast<uint16_t *>(const_cast<void *>(c_dev));
+    a.kr = static_cast<uint16_t *>(const_cast<void *>(kr_dev));
+    a.c_stride = c_stride;
+    a.kr_stride = kr_stride;
+    a.slots = slots_dev;
+    a.tokens = n_tokens;
+    a.positions = positions_dev;
+    a.table = reinterpret_cast<const unsigned long long *>(table_dev);
+    a.layout = layout;
+    a.magnitude = magnitude;
+    a.status = status_dev;
+    return latent_rows(false, a, cache, stream);
+}
+
+int moe_latent_read(const moe_latent_cache *cache, const int32_t *slots_dev, int n_tokens, void *c_out_dev,
+                    int64_t c_stride, void *kr_out_dev, int64_t kr_stride, uint32_t *status_dev, moe_stream_t stream)
+{
+    const int rc = check_cache(cache);
+    if (rc)
+        return rc;
+    if (n_tokens < 0 || (n_tokens > 0 && (!c_out_dev || !kr_out_dev || !slots_dev)))
+        return host_fail(MOE_EINVAL, "moe_latent_read: NULL argument or n_tokens (%d) < 0", n_tokens);
+    if (!aligned(c_out_dev, 2) || !aligned(kr_out_dev, 2) || !aligned(slots_dev, 4) || !aligned(status_dev, 4))
+        return host_fail(MOE_EINVAL, "moe_latent_read: an argument is not aligned to its type");
+    if (n_tokens > 1 && (c_stride < cache->latent_dim || kr_stride < cache->rope_dim))
+        return host_fail(MOE_EINVAL, "moe_latent_read: a row stride is below the row's length");
+    if (n_tokens == 0)
+        return MOE_OK;
+    LatentRows a{};
+    a.c = static_cast<uint16_t *>(c_out_dev);
+    a.kr = static_cast<uint16_t *>(kr_out_dev);
+    a.c_stride = c_stride;
+    a.kr_stride = kr_stride;
+    a.slots = slots_dev;
+    a.tokens = n_tokens;
+    a.status = status_dev;
+    return latent_rows(true, a, cache, stream);
+}
+
+static int latent_ws(const moe_latent_cache *cache, int heads, int batch, int n_tokens, size_t &bytes)
+{
+    const int rc = check_shape(cache);
+    if (rc)
+        return rc;
+    if (heads < 1 || batch < 0 || n_tokens < 0)
+        return host_fail(MOE_EINVAL, "heads (%d) must be positive, batch (%d) and n_tokens (%d) not negative", heads, batch,
+                         n_tokens);
+    if (heads > 128 || batch > 1024 || n_tokens > batch * MOE_MAX_DRAFT)
+        return host_fail(MOE_EUNSUPPORTED, "heads (%d) <= 128, batch (%d) <= 1024, n_tokens (%d) <= %d a sequence", heads,
+                         batch, n_tokens, MOE_MAX_DRAFT);
+    bytes = LATENT_CTRL_BYTES;
+    return MOE_OK;
+}
+
+int moe_latent_attention_workspace_bytes(const moe_latent_cache *cache, int heads, int batch, int n_tokens, size_t *bytes)
+{
+    if (!bytes)
+        return host_fail(MOE_EINVAL, "bytes is NULL");
+    return latent_ws(cache, heads, batch, n_tokens, *bytes);
+}
+
+int moe_latent_attention(const moe_latent_cache *cache, const void *q_dev, int64_t q_token_stride, int64_t q_head_stride,
+                         const void *qr_dev, int64_t qr_token_stride, int64_t qr_head_stride, void *out_dev,
+                         int64_t out_token_stride, int64_t out_head_stride, int heads, const int32_t *q_start_dev,
+                         const int32_t *kv_len_dev, const int32_t *table_dev, int64_t table_stride, int table_pages,
+                         const uint64_t *mask_dev, int batch, int n_tokens, float scale, void *ws_dev, size_t ws_bytes,
+                         moe_stream_t stream)
+{
+    int rc = check_cache(cache);
+    if (rc)
+        return rc;
+    size_t need;
+    if ((rc = latent_ws(cache, heads, batch, n_tokens, need)))
+        return rc;
+    if (batch == 0 || n_tokens == 0)
+        return MOE_OK;
+    if (!q_dev || !qr_dev || !out_dev || !q_start_dev || !kv_len_dev || !table_dev || !ws_dev)
+        return host_fail(MOE_EINVAL, "moe_latent_attention: NULL argument");
+    if (!aligned(q_dev, 2) || !aligned(qr_dev, 2) || !aligned(out_dev, 2) || !aligned(q_start_dev, 4) ||
+        !aligned(kv_len_dev, 4) || !aligned(table_dev, 4) || !aligned(mask_dev, 8) || !aligned(ws_dev, 256))
+        return host_fail(MOE_EINVAL, "moe_latent_attention: an argument is not aligned to its type, or ws_dev not to 256 "
+                         "bytes");
+    if (ws_bytes < need)
+        return host_fail(MOE_EINVAL, "moe_latent_attention: the workspace holds %zu bytes, %zu are needed", ws_bytes, need);
+    if (table_pages < 1 || (batch > 1 && table_stride < table_pages) || !(scale >= -3.0e38f && scale <= 3.0e38f))
+        return host_fail(MOE_EINVAL, "moe_latent_attention: table_pages (%d) must be positive and at most table_stride "
+                         "(%lld), scale finite", table_pages, (long long)table_stride);
+    LatentArgs a{};
+    TreeArgs &t = a.t;
+    t.k = {cache->latent_dim, 1, cache->page_size, 0};
+    t.pages = static_cast<const uint8_t *>(cache->pages);
+    t.n_pages = (int)cache->n_pages;
+    t.q = static_cast<const uint16_t *>(q_dev);
+    t.q_tok = q_token_stride;
+    t.q_head = q_head_stride;
+    a.qr = static_cast<const uint16_t *>(qr_dev);
+    a.qr_tok = qr_token_stride;
+    a.qr_head = qr_head_stride;
+    a.rope = cache->rope_dim;
+    t.out = static_cast<uint16_t *>(out_dev);
+    t.o_tok = out_token_stride;
+    t.o_head = out_head_stride;
+    t.q_start = q_start_dev;
+    t.kv_len = kv_len_dev;
+    t.table = table_dev;
+    t.table_stride = table_stride;
+    t.max_len = (int)std::min((long long)table_pages * t.k.page, (long long)MOE_TREE_MAX_LEN);
+    t.mask = reinterpret_cast<const unsigned long long *>(mask_dev);
+    t.batch = batch;
+    t.tokens = n_tokens;
+    t.group = heads;
+    t.scale = scale;
+    t.ctrl = static_cast<uint32_t *>(ws_dev);
+    t.wait_ns = host_wait_ns();
+    MOE_CUDA_OK(launch(moe_latent_row_kernel, dim3((unsigned)n_tokens, (unsigned)heads), MOE_ROW_THREADS, 0, stream, a));
+    return MOE_OK;
+}
+
+int moe_latent_prompt_attention(const void *q_dev, int64_t q_token_stride, int64_t q_head_stride, const void *k_dev,
+                                int64_t k_token_stride, int64_t k_head_stride, const void *kr_dev, int64_t kr_stride,
+                                const void *v_dev, int64_t v_token_stride, int64_t v_head_stride, void *out_dev,
+                                int64_t out_token_stride, int64_t out_head_stride, int heads, int nope_dim, int rope_dim,
+                                const int32_t *q_start_dev, const int32_t *kv_start_dev, int batch, int q_tokens,
+                                int kv_tokens, int causal, float scale, uint32_t *status_dev, moe_stream_t stream)
+{
+    if (heads < 1 || nope_dim < 1 || rope_dim < 1 || batch < 0 || q_tokens < 0 || kv_tokens < 0)
+        return host_fail(MOE_EINVAL, "moe_latent_prompt_attention: heads (%d), nope_dim (%d) and rope_dim (%d) must be "
+                         "positive, batch (%d), q_tokens (%d) and kv_tokens (%d) not negative", heads, nope_dim, rope_dim,
+                         batch, q_tokens, kv_tokens);
+    if ((nope_dim != 64 && nope_dim != 128) || rope_dim % 8 || rope_dim > 64 || heads > 1024 || batch > 1024)
+        return host_fail(MOE_EUNSUPPORTED, "moe_latent_prompt_attention: nope_dim (%d) of 64 or 128, rope_dim (%d) a "
+                         "multiple of 8 up to 64, heads (%d) and batch (%d) <= 1024", nope_dim, rope_dim, heads, batch);
+    if (!(scale >= -3.0e38f && scale <= 3.0e38f))
+        return host_fail(MOE_EINVAL, "moe_latent_prompt_attention: scale must be finite");
+    if (batch == 0 || q_tokens == 0)
+        return MOE_OK;
+    if (!q_dev || !out_dev || !q_start_dev || !kv_start_dev || (kv_tokens > 0 && (!k_dev || !kr_dev || !v_dev)))
+        return host_fail(MOE_EINVAL, "moe_latent_prompt_attention: NULL argument");
+    if (!aligned(q_dev, 2) || !aligned(out_dev, 2) || !aligned(q_start_dev, 4) || !aligned(kv_start_dev, 4) ||
+        !aligned(status_dev, 4))
+        return host_fail(MOE_EINVAL, "moe_latent_prompt_attention: an argument is not aligned to its type");
+    if (!aligned(k_dev, 16) || !aligned(kr_dev, 16) || !aligned(v_dev, 16) ||
+        (k_token_stride | k_head_stride | kr_stride | v_token_stride | v_head_stride) % 8)
+        return host_fail(MOE_EINVAL, "moe_latent_prompt_attention: k, kr and v must start on 16-byte boundaries and have "
+                         "strides of multiples of 8");
+    PromptArgs a{};
+    a.q = static_cast<const uint16_t *>(q_dev);
+    a.k = static_cast<const uint16_t *>(k_dev);
+    a.kr = static_cast<const uint16_t *>(kr_dev);
+    a.v = static_cast<const uint16_t *>(v_dev);
+    a.out = static_cast<uint16_t *>(out_dev);
+    a.q_tok = q_token_stride;
+    a.q_head = q_head_stride;
+    a.k_tok = k_token_stride;
+    a.k_head = k_head_stride;
+    a.kr_tok = kr_stride;
+    a.v_tok = v_token_stride;
+    a.v_head = v_head_stride;
+    a.o_tok = out_token_stride;
+    a.o_head = out_head_stride;
+    a.q_start = q_start_dev;
+    a.kv_start = kv_start_dev;
+    a.batch = batch;
+    a.heads = heads;
+    a.nope = nope_dim;
+    a.rope = rope_dim;
+    a.q_tokens = q_tokens;
+    a.kv_tokens = kv_tokens;
+    a.causal = causal;
+    a.scale = scale;
+    a.status = status_dev;
+    MOE_CUDA_OK(launch(moe_prompt_row_kernel, dim3((unsigned)q_tokens, (unsigned)heads), MOE_ROW_THREADS, 0, stream, a));
+    return MOE_OK;
+}
+
+}  // extern "C"

@@ -7,6 +7,7 @@
 
 #include "moe_common.cuh"
 #include "moe_host.cuh"
+#include "moe_launch.cuh"
 #include "moe_kv.cuh"
 #include "moe_tree_attn.cuh"
 #include "moe_tree_tc.cuh"
@@ -15,33 +16,6 @@
 using namespace moe;
 
 namespace {
-
-#define SPEC_CUDA_OK(expr)                                                                              \
-    do {                                                                                                \
-        cudaError_t e_ = (expr);                                                                        \
-        if (e_ != cudaSuccess)                                                                          \
-            return host_fail(MOE_ECUDA, "%s: %s (%s)", #expr, cudaGetErrorString(e_), cudaGetErrorName(e_)); \
-    } while (0)
-
-// Launches behind the stream's last kernel while that still runs (the kernels wait for its end before they touch
-// memory): one token over 511, call after call, 12.0 us a call, launched the plain way 16.4.
-template <typename... A>
-cudaError_t launch(void (*kernel)(A...), dim3 grid, int threads, size_t shared, moe_stream_t stream, A... args)
-{
-    cudaLaunchConfig_t lc{};
-    lc.gridDim = grid;
-    lc.blockDim = dim3((unsigned)threads);
-    lc.dynamicSmemBytes = shared;
-    lc.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, kernel, args...);
-}
-
-bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 #define SPEC_CTRL_BYTES 256  // control words: the status is word MOE_CTRL_STATUS
 
@@ -185,7 +159,7 @@ int tree_device(TreeDevice **out)
 {
     static TreeDevice dev[MOE_TREE_MAX_DEVICES];
     int d = 0;
-    SPEC_CUDA_OK(cudaGetDevice(&d));
+    MOE_CUDA_OK(cudaGetDevice(&d));
     if (d < 0 || d >= MOE_TREE_MAX_DEVICES)
         return host_fail(MOE_EUNSUPPORTED, "device ordinal %d", d);
     std::lock_guard<std::mutex> lk(g_tree_mu);
@@ -197,16 +171,16 @@ int tree_device(TreeDevice **out)
             tree_instance<MOE_KV_Q4, 64, 1>(),  tree_instance<MOE_KV_Q4, 64, 2>(),  tree_instance<MOE_KV_Q4, 64, 4>(),
             tree_instance<MOE_KV_Q4, 128, 1>(), tree_instance<MOE_KV_Q4, 128, 2>(), tree_instance<MOE_KV_Q4, 256, 1>()};
         int n = 0, per_sm = 0, optin = 0;
-        SPEC_CUDA_OK(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d));
-        SPEC_CUDA_OK(cudaDeviceGetAttribute(&per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, d));
-        SPEC_CUDA_OK(cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, d));
+        MOE_CUDA_OK(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d));
+        MOE_CUDA_OK(cudaDeviceGetAttribute(&per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, d));
+        MOE_CUDA_OK(cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, d));
         for (int i = 0; i < MOE_TREE_INSTANCES; ++i) {
-            SPEC_CUDA_OK(cudaFuncSetAttribute(all[i].kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
+            MOE_CUDA_OK(cudaFuncSetAttribute(all[i].kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
             D.inst[i] = all[i];
         }
         const TtcInstance tc[2] = {ttc_instance<MOE_KV_Q8>(), ttc_instance<MOE_KV_Q4>()};
         for (int i = 0; i < 2; ++i) {
-            SPEC_CUDA_OK(cudaFuncSetAttribute(tc[i].kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
+            MOE_CUDA_OK(cudaFuncSetAttribute(tc[i].kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
             D.tc[i] = tc[i];
         }
         D.per_sm = per_sm;
@@ -239,7 +213,7 @@ int tree_join(const TreeArgs &a, const TreeDevice &dev, int runs, int rows, long
     const dim3 grid(deep ? std::max(1, std::min(runs, 4 * dev.sms / (blocks * slices))) : runs, blocks, slices);
     const JoinKernel kernel = a.k.dim == 64 ? join_kernel<64>(deep) : a.k.dim == 128 ? join_kernel<128>(deep)
                                                                                       : join_kernel<256>(deep);
-    SPEC_CUDA_OK(launch(kernel, grid, 256, 0, stream, a, rows, runs));
+    MOE_CUDA_OK(launch(kernel, grid, 256, 0, stream, a, rows, runs));
     return MOE_OK;
 }
 
@@ -301,7 +275,7 @@ int moe_kv_append(const moe_kv_cache *cache, const void *k_dev, int64_t k_token_
     });
     const long long all = ((long long)n_tokens + per - 1) / per;  // warps a head
     const int warps = (int)std::min<long long>(MOE_KV_THREADS / 32, all);
-    SPEC_CUDA_OK(launch(kernel, dim3((unsigned)((all + warps - 1) / warps), 2 * a.k.heads), warps * 32, 0, stream, a));
+    MOE_CUDA_OK(launch(kernel, dim3((unsigned)((all + warps - 1) / warps), 2 * a.k.heads), warps * 32, 0, stream, a));
     return MOE_OK;
 }
 
@@ -339,7 +313,7 @@ int moe_kv_read(const moe_kv_cache *cache, const int32_t *slots_dev, int n_token
     });
     const long long threads = (n_tokens + 7ll) / 8 * per;
     const dim3 grid((unsigned)((threads + MOE_KV_THREADS - 1) / MOE_KV_THREADS), 2 * a.k.heads);
-    SPEC_CUDA_OK(launch(kernel, grid, MOE_KV_THREADS, 0, stream, a));
+    MOE_CUDA_OK(launch(kernel, grid, MOE_KV_THREADS, 0, stream, a));
     return MOE_OK;
 }
 
@@ -435,7 +409,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
         const int stages = (int)std::min<size_t>(4, (dev->optin - used) / t.stage);
         a.min_units = 2;
         const int grid = std::min(dev->sms, MOE_TTC_MAX_GRID);
-        SPEC_CUDA_OK(launch(t.kernel, dim3(grid), MOE_TTC_THREADS, used + stages * t.stage, stream, a, stages));
+        MOE_CUDA_OK(launch(t.kernel, dim3(grid), MOE_TTC_THREADS, used + stages * t.stage, stream, a, stages));
         return tree_join(a, *dev, grid, MOE_TTC_ROWS, (long long)batch * a.k.heads * ((rows + MOE_TTC_ROWS - 1) / MOE_TTC_ROWS),
                          stream);
     }
@@ -453,7 +427,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     if (stages < 2)
         return host_fail(MOE_EUNSUPPORTED, "moe_tree_attention: %zu bytes of shared memory do not fit", used + 2 * t.stage);
     const int grid = std::min(dev->sms * ctas, MOE_TREE_MAX_GRID);
-    SPEC_CUDA_OK(launch(t.kernel, dim3(grid), MOE_TREE_THREADS, used + stages * t.stage, stream, a, stages));
+    MOE_CUDA_OK(launch(t.kernel, dim3(grid), MOE_TREE_THREADS, used + stages * t.stage, stream, a, stages));
     return tree_join(a, *dev, grid, t.rows, (long long)batch * a.k.heads * ((rows + t.rows - 1) / t.rows), stream);
 }
 
@@ -536,7 +510,7 @@ int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stri
         a.stats = reinterpret_cast<VerifySlice *>(static_cast<char *>(ws_dev) + SPEC_CTRL_BYTES);
         const auto rows = f32 ? (wide ? moe_verify_rows_kernel<true, true> : moe_verify_rows_kernel<true, false>)
                               : (wide ? moe_verify_rows_kernel<false, true> : moe_verify_rows_kernel<false, false>);
-        SPEC_CUDA_OK(launch(rows, dim3((unsigned)n_rows * a.splits), MOE_VERIFY_STAT_THREADS, 0, stream, a));
+        MOE_CUDA_OK(launch(rows, dim3((unsigned)n_rows * a.splits), MOE_VERIFY_STAT_THREADS, 0, stream, a));
     }
     const auto kernel = verify_kernel(f32, wide, ahead);
     cudaLaunchConfig_t lc{};
@@ -551,7 +525,7 @@ int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stri
     at[1].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = at;
     lc.numAttrs = 2;
-    SPEC_CUDA_OK(cudaLaunchKernelEx(&lc, kernel, a));
+    MOE_CUDA_OK(cudaLaunchKernelEx(&lc, kernel, a));
     return MOE_OK;
 }
 

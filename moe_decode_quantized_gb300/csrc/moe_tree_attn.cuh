@@ -126,7 +126,7 @@ __device__ __forceinline__ bool tree_poll(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
-__device__ __noinline__ bool tree_wait_on(uint64_t *bar, uint32_t parity, uint32_t *status, unsigned long long wait_ns)
+static __device__ __noinline__ bool tree_wait_on(uint64_t *bar, uint32_t parity, uint32_t *status, unsigned long long wait_ns)
 {
     const uint64_t t0 = globaltimer();
     do {
@@ -173,7 +173,7 @@ __device__ __forceinline__ void tree_sequence(const TreeArgs &a, int b, int &fir
 }
 
 // (out of line: it is rarely needed, and the kernels' roles share the instruction cache)
-__device__ __noinline__ long long tree_div_long(long long x, long long y) { return x / y; }
+static __device__ __noinline__ long long tree_div_long(long long x, long long y) { return x / y; }
 
 // x / y (x >= 0, y > 0), by a 32-bit division where both fit
 __device__ __forceinline__ long long tree_div(long long x, long long y)
