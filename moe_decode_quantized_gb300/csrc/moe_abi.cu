@@ -806,7 +806,7 @@ struct HostSource {
 
 }  // namespace
 
-// the message and the wait bound for the library's other translation units
+// the message, the wait bound and tensor maps for the library's other translation units
 int moe::host_fail(int code, const char *fmt, ...)
 {
     va_list ap;
@@ -817,6 +817,25 @@ int moe::host_fail(int code, const char *fmt, ...)
 }
 
 unsigned long long moe::host_wait_ns() { return g_wait_ns.load(); }
+
+int moe::host_map_bf16(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                       const uint32_t *box)
+{
+    EncodeTiledFn fn;
+    const int rc = encode_tiled(&fn);
+    if (rc)
+        return rc;
+    const cuuint32_t es[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base),
+                          reinterpret_cast<const cuuint64_t *>(dims), reinterpret_cast<const cuuint64_t *>(strides),
+                          reinterpret_cast<const cuuint32_t *>(box), es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(MOE_ECUDA, "cuTensorMapEncodeTiled (%d-D, %llu x %llu) failed: %d", rank, (unsigned long long)dims[1],
+                    (unsigned long long)dims[0], (int)r);
+    return MOE_OK;
+}
 
 // ==================================================================== C ABI
 

@@ -4,8 +4,10 @@
 #include <math.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "moe_latent_attn.cuh"
+#include "moe_latent_tc.cuh"
 #include "moe_launch.cuh"
 
 using namespace moe;
@@ -57,6 +59,76 @@ int latent_rows(bool read, LatentRows &a, const moe_latent_cache *cache, moe_str
     MOE_CUDA_OK(launch(read ? moe_latent_rows_kernel<true> : moe_latent_rows_kernel<false>, grid, MOE_LATENT_THREADS, 0,
                        stream, a));
     return MOE_OK;
+}
+
+// ---- absorbed attention: instances, maps of the cache, the join of cut items
+
+#define MOE_LTC_MAX_PAIRS 80  // the workspace holds two partials each
+#define MOE_LATENT_MAX_DEVICES 64
+
+std::mutex g_latent_mu;
+
+struct LatentInstance {
+    void (*kernel)(LatentArgs, int);
+    size_t fixed, stage;  // bytes of shared memory beside the ring and the list; of a stage
+    void (*join[2])(TreeArgs, int, int);  // for many items, for few long ones
+};
+
+template <int L>
+LatentInstance latent_instance()
+{
+    using T = LtcShape<L>;
+    return {moe_latent_tc_kernel<L>, 1024 + (size_t)T::RING_AT + T::SMALL, (size_t)T::STAGE,
+            {moe_tree_join_kernel<L, 256, 32, 4>, moe_tree_join_kernel<L, 256, 8, 8>}};
+}
+
+struct LatentDevice {
+    int pairs = 0;
+    size_t optin = 0;
+    LatentInstance inst[3];
+};
+
+int latent_device(LatentDevice **out)
+{
+    static LatentDevice dev[MOE_LATENT_MAX_DEVICES];
+    int d = 0;
+    MOE_CUDA_OK(cudaGetDevice(&d));
+    if (d < 0 || d >= MOE_LATENT_MAX_DEVICES)
+        return host_fail(MOE_EUNSUPPORTED, "device ordinal %d", d);
+    std::lock_guard<std::mutex> lk(g_latent_mu);
+    LatentDevice &D = dev[d];
+    if (!D.pairs) {
+        int n = 0, optin = 0;
+        MOE_CUDA_OK(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d));
+        MOE_CUDA_OK(cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, d));
+        const LatentInstance all[3] = {latent_instance<128>(), latent_instance<256>(), latent_instance<512>()};
+        for (int i = 0; i < 3; ++i) {
+            MOE_CUDA_OK(cudaFuncSetAttribute(all[i].kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
+            D.inst[i] = all[i];
+        }
+        D.optin = optin;
+        D.pairs = std::min(n / 2, MOE_LTC_MAX_PAIRS);
+    }
+    *out = &D;
+    return MOE_OK;
+}
+
+// the cache's rows as tensor maps: boxes of 32 tokens and all chunks of 64 dimensions where pages are of whole 32
+// tokens, else of 16 tokens and a chunk
+int latent_maps(const moe_latent_cache *c, LatentArgs &a)
+{
+    const uint64_t row = 2ull * (c->latent_dim + c->rope_dim), slots = (uint64_t)c->n_pages * c->page_size;
+    const uint32_t chunks = c->latent_dim / 64, tokens = a.big ? 32 : 16;
+    const uint64_t dims[3] = {64, slots, chunks}, strides[2] = {row, 128};
+    const uint64_t rope_dims[2] = {(uint64_t)c->rope_dim, slots};
+    const uint32_t keys[3] = {64, tokens, a.big ? chunks : 1}, values[3] = {64, tokens, a.big ? chunks / 2 : 1};
+    const uint32_t ropes[2] = {64, tokens};
+    int rc = host_map_bf16(&a.keys, c->pages, 3, dims, strides, keys);
+    if (!rc)
+        rc = host_map_bf16(&a.values, c->pages, 3, dims, strides, values);
+    if (!rc)
+        rc = host_map_bf16(&a.ropes, static_cast<const char *>(c->pages) + 2 * c->latent_dim, 2, rope_dims, strides, ropes);
+    return rc;
 }
 
 using RopeKernel = void (*)(RopeArgs);
@@ -254,7 +326,9 @@ static int latent_ws(const moe_latent_cache *cache, int heads, int batch, int n_
     if (heads > 128 || batch > 1024 || n_tokens > batch * MOE_MAX_DRAFT)
         return host_fail(MOE_EUNSUPPORTED, "heads (%d) <= 128, batch (%d) <= 1024, n_tokens (%d) <= %d a sequence", heads,
                          batch, n_tokens, MOE_MAX_DRAFT);
-    bytes = LATENT_CTRL_BYTES;
+    // control words, cuts, and two partials of a row block a run
+    bytes = LATENT_CTRL_BYTES + sizeof(TreeCut) * MOE_LTC_MAX_PAIRS +
+            (size_t)MOE_LTC_MAX_PAIRS * 2 * MOE_LTC_ROWS * 4 * (cache->latent_dim + 2);
     return MOE_OK;
 }
 
@@ -316,9 +390,46 @@ int moe_latent_attention(const moe_latent_cache *cache, const void *q_dev, int64
     t.tokens = n_tokens;
     t.group = heads;
     t.scale = scale;
+    t.q_wide = wide_rows(q_dev, q_token_stride, q_head_stride);
+    a.qr_wide = wide_rows(qr_dev, qr_token_stride, qr_head_stride);
+    t.o_wide = wide_rows(out_dev, out_token_stride, out_head_stride);
+    t.min_units = 1;
     t.ctrl = static_cast<uint32_t *>(ws_dev);
+    t.cuts = reinterpret_cast<TreeCut *>(t.ctrl + LATENT_CTRL_BYTES / 4);
+    t.part = reinterpret_cast<float *>(t.cuts + MOE_LTC_MAX_PAIRS);
     t.wait_ns = host_wait_ns();
-    MOE_CUDA_OK(launch(moe_latent_row_kernel, dim3((unsigned)n_tokens, (unsigned)heads), MOE_ROW_THREADS, 0, stream, a));
+    a.big = t.k.page % 32 == 0;
+    if ((rc = latent_maps(cache, a)))
+        return rc;
+    LatentDevice *dev;
+    if ((rc = latent_device(&dev)))
+        return rc;
+    const int latent = cache->latent_dim;
+    const LatentInstance &inst = dev->inst[latent == 128 ? 0 : latent == 256 ? 1 : 2];
+    const size_t used = inst.fixed + 12 * ((size_t)batch + 1);
+    const int stages = (int)std::min<size_t>(MOE_LTC_MAX_STAGES, (dev->optin - used) / inst.stage);
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3((unsigned)dev->pairs * 2);
+    lc.blockDim = dim3(MOE_LTC_THREADS);
+    lc.dynamicSmemBytes = used + stages * inst.stage;
+    lc.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = 2;
+    MOE_CUDA_OK(cudaLaunchKernelEx(&lc, inst.kernel, a, stages));
+    // the join: the runs that each item may span decide on the instance (moe_spec.cu has the figures)
+    const int rows = (n_tokens + batch - 1) / batch * heads, runs = dev->pairs;
+    const long long items = (long long)batch * ((rows + MOE_LTC_ROWS - 1) / MOE_LTC_ROWS);
+    const bool deep = runs / items >= 24;
+    const int blocks = std::min((rows + MOE_TREE_JOIN_ROWS - 1) / MOE_TREE_JOIN_ROWS, MOE_LTC_ROWS / MOE_TREE_JOIN_ROWS);
+    const dim3 grid((unsigned)runs, (unsigned)(batch == 1 ? blocks : MOE_LTC_ROWS / MOE_TREE_JOIN_ROWS),
+                    (unsigned)(deep ? latent / 32 : latent / 128));
+    MOE_CUDA_OK(launch(inst.join[deep], grid, 256, 0, stream, t, MOE_LTC_ROWS, runs));
     return MOE_OK;
 }
 

@@ -1,24 +1,16 @@
-// moe_latent_attn.cuh -- latent attention: absorbed form over the paged cache,
-// expanded form over a prompt's keys and values.
+// moe_latent_attn.cuh -- latent attention in expanded form, over a prompt's keys
+// and values.
 //
 // A CTA works on one query row of one head: tiles of 32 tokens, a score by a warp
 // at a time, one pass with a running maximum and sum, a thread a few dimensions
 // of the output.
 #pragma once
 #include "moe_latent.cuh"
-#include "moe_tree_attn.cuh"
 
 namespace moe {
 
 #define MOE_ROW_THREADS 128
 #define MOE_ROW_TILE 32
-
-struct LatentArgs {
-    TreeArgs t;  // k.heads 1, k.dim the latent vector's, group the heads; q the query's latent part
-    const uint16_t *qr;
-    long long qr_tok, qr_head;
-    int rope;
-};
 
 struct PromptArgs {
     const uint16_t *q, *k, *kr, *v;
@@ -70,53 +62,6 @@ __device__ __forceinline__ void row_attention(const float *qs, int dims, int vdi
     }
     for (int i = 0, d = tid; d < vdims; d += MOE_ROW_THREADS, ++i)
         out(d, l == 0.0f ? 0.0f : o[i] / l);
-}
-
-__global__ void __launch_bounds__(MOE_ROW_THREADS) moe_latent_row_kernel(const __grid_constant__ LatentArgs a)
-{
-    __shared__ float qs[576];
-    __shared__ int which;
-    pdl_wait();
-    const TreeArgs &t = a.t;
-    const int token = blockIdx.x, head = blockIdx.y, latent = t.k.dim, row = latent + a.rope;
-    if (threadIdx.x == 0)
-        which = -1;
-    __syncthreads();
-    for (int b = threadIdx.x; b < t.batch; b += MOE_ROW_THREADS)
-        if (t.q_start[b] <= token && token < t.q_start[b + 1])
-            which = b;
-    __syncthreads();
-    const int b = which;
-    if (b < 0)
-        return;
-    int first, n, len, rows;
-    tree_sequence(t, b, first, n, len, rows);
-    if (rows == 0)
-        return;
-    uint16_t *out = t.out + token * t.o_tok + head * t.o_head;
-    if (n == 0) {
-        for (int d = threadIdx.x; d < latent; d += MOE_ROW_THREADS)
-            out[d] = 0;
-        return;
-    }
-    for (int d = threadIdx.x; d < row; d += MOE_ROW_THREADS)
-        qs[d] = bf16_to_f32(d < latent ? t.q[token * t.q_tok + head * t.q_head + d]
-                                       : a.qr[token * a.qr_tok + head * a.qr_head + d - latent]);
-    const int prefix = len - n, node = token - first;
-    const unsigned long long mask = t.mask ? t.mask[token] : (2ull << node) - 1;
-    const uint16_t *pages = reinterpret_cast<const uint16_t *>(t.pages);
-    auto at = [&](int j) {
-        const int page = t.table[b * t.table_stride + j / t.k.page];
-        if (page < 0 || page >= t.n_pages) {
-            atomicOr(t.ctrl + MOE_CTRL_STATUS, (uint32_t)MOE_WS_INDEX);
-            return (const uint16_t *)nullptr;
-        }
-        return pages + ((long long)page * t.k.page + j % t.k.page) * row;
-    };
-    auto value = [&](int j, int d) { return bf16_to_f32(at(j)[d]); };
-    auto seen = [&](int j) { return (j < prefix || mask >> (j - prefix) & 1) && at(j) != nullptr; };
-    row_attention(qs, row, latent, len, t.scale, value, value, seen,
-                  [&](int d, float x) { out[d] = (uint16_t)pack_bf2(x, x); });
 }
 
 __global__ void __launch_bounds__(MOE_ROW_THREADS) moe_prompt_row_kernel(const __grid_constant__ PromptArgs a)

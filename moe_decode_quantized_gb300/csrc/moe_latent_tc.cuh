@@ -1,0 +1,576 @@
+// moe_latent_tc.cuh -- latent attention in absorbed form on the 5th-generation
+// tensor cores: for the rows (query token, head) of a sequence
+//   S = Q C^T + QR KR^T,   O += P C,   P = 2^(c (S - m)),
+// over the sequence's shared rows [C | KR] of the paged cache, in one pass, with
+// a running reference m and sum of weights for each row.
+//
+// O of 128 rows and 512 dimensions would fill a CTA's tensor memory, so a pair of
+// CTAs (cta_group::2) shares a block of 128 rows: each has 64 of them, all tokens
+// and all dimensions of the result in tensor memory, and half of what both
+// multiply with. Tiles of 64 tokens: for S each CTA brings its 32 tokens' rows
+// whole; for O it needs all 64 tokens but only its half of the dimensions, which
+// it has of its own tokens already, and the other tokens' are brought, from the
+// L2, to where its own tokens' other half has stood once S is there. A tile so
+// takes no more shared memory than its rows, and every row comes from memory
+// once. In a row of tensor memory (lane), lanes 0 to 63 are the pair's 64 rows
+// with the first half of S's tokens (O's dimensions), lanes 64 to 127 the same
+// rows with the second.
+//
+// Items, runs and partials are those of moe_tree_attn.cuh, a run a pair.
+#pragma once
+#include "moe_latent.cuh"
+#include "moe_tc.cuh"
+#include "moe_tree_attn.cuh"
+
+namespace moe {
+
+#define MOE_LTC_TOKENS 64
+#define MOE_LTC_ROWS 128   // of a pair
+#define MOE_LTC_COST 3     // of an item, beside its tiles
+#define MOE_LTC_SOFT 4     // softmax warps
+#define MOE_LTC_THREADS ((MOE_LTC_SOFT + 4) * 32)
+#define MOE_LTC_MAX_STAGES 8
+#define MOE_LTC_CHUNK 4096  // 64 dimensions of 32 tokens
+#define MOE_LTC_SLACK 8.0f  // m moves when an exponent passes it by this
+
+struct LatentArgs {
+    TreeArgs t;  // k.heads 1, k.dim the latent vector's, group the heads; q the query's latent part
+    const uint16_t *qr;
+    long long qr_tok, qr_head;
+    int rope, qr_wide;
+    int big;  // boxes of 32 tokens and of all chunks; else of 16 tokens and one
+    CUtensorMap keys, values, ropes;  // the cache's rows [64, slots, chunks]; the same; their turning part [rope, slots]
+};
+
+template <int L>
+struct LtcShape {
+    static constexpr int CHUNKS = L / 64;        // of the latent vector; one more is the turning part
+    static constexpr int HALF = L / 128;         // chunks of the dimensions that a CTA's part of O has
+    static constexpr int STAGE = (CHUNKS + 1) * MOE_LTC_CHUNK;
+    static constexpr int Q_CHUNK = 8192;         // 64 dimensions of 64 rows
+    static constexpr int P_AT = (CHUNKS + 1) * Q_CHUNK;
+    static constexpr int P_BYTES = 8192;         // 64 tokens of 64 rows; two
+    static constexpr int RING_AT = P_AT + 2 * P_BYTES;
+    static constexpr int N = L < 256 ? L : 256;  // dimensions of one product
+    static constexpr int O_COLS = L / 2;
+    // barriers; maxima [2][2][64], sums [2][64]; gone [16]; the scan and the list
+    static constexpr int SMALL = 512 + 6 * 64 * 4 + 64 + 32 * 8;
+};
+
+// ---- pairs of CTAs
+
+__device__ __forceinline__ uint32_t cta_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void pair_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// an arrival at the barrier of the pair's first CTA (what it tells of is read by the tensor core alone, and has passed
+// fence.proxy.async or has come by an asynchronous copy)
+__device__ __forceinline__ void arrive_first(uint64_t *bar)
+{
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
+                 " mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+// D[tmem] (+)= A[smem] . B[smem]: M rows over the pair, each CTA's shared memory holding half of A's rows and half of
+// B's columns at the same places. By a whole warp, one lane of which issues it: with the operands the same in every
+// lane they are kept in uniform registers (36 products of 64 tokens and two commits: 970 clocks; by a lane that works
+// alone, whose operands are moved there each time, 1680)
+__device__ __forceinline__ void mma2_f16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xFFFFFFFF;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// the barrier in both CTAs completes (one arrival) once the products that this warp issued before have
+__device__ __forceinline__ void mma2_commit(uint64_t *bar)
+{
+    asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xFFFFFFFF;\n"
+                 " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
+                     smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem2_alloc(uint32_t *dst, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem2_dealloc(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// descriptor of a tile whose N side is contiguous: rows (one a k) of 64 elements, 8 rows 1024 bytes apart, the next 64
+// elements `next` bytes
+__device__ __forceinline__ uint64_t mn128_desc(const void *tile, uint32_t next)
+{
+    const uint64_t addr = smem_u32(tile);
+    return ((addr >> 4) & 0x3FFFull) | ((uint64_t)(next >> 4) << 16) | ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// bit pairs whose exponent is all ones (NaN, infinities) to 0
+__device__ __forceinline__ uint32_t finite_bf2(uint32_t w)
+{
+    return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
+}
+
+template <int L>
+__global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const __grid_constant__ LatentArgs a, const int stages)
+{
+    using T = LtcShape<L>;
+    constexpr int ROWS = MOE_LTC_ROWS, TOKENS = MOE_LTC_TOKENS;
+    constexpr uint32_t O_COL = 64;  // of tensor memory: S (two of 32 columns), O
+    extern __shared__ __align__(1024) uint8_t smem_any[];
+    uint8_t *smem = smem_any + (-smem_u32(smem_any) & 1023u);  // the swizzle goes by address bits
+    uint8_t *sq = smem, *sp = smem + T::P_AT, *ring = smem + T::RING_AT, *small = ring + (size_t)stages * T::STAGE;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(small);
+    uint64_t *full = bars, *peer_full = bars + 8, *empty = bars + 16, *v_full = bars + 24;  // [stages]
+    uint64_t *s_full = bars + 32, *p_full = bars + 34, *pv_done = bars + 36;                // [2]
+    uint64_t *q_full = bars + 38, *o_free = bars + 39, *drained = bars + 40, *peer_v = bars + 41;  // peer_v [stages]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 49);
+    float *top_of = reinterpret_cast<float *>(small + 512), *sum_of = top_of + 256;  // [2][2][64], [2][64]
+    uint32_t *gone = reinterpret_cast<uint32_t *>(sum_of + 128);  // [16] 16-token groups of tile t that are not there, at t % 16
+    long long *scan = reinterpret_cast<long long *>(gone + 16), *cum = scan + 32;  // cum [batch + 1]
+    int *count = reinterpret_cast<int *>(scan + 20), *items = reinterpret_cast<int *>(cum + a.t.batch + 1);  // items [batch + 1]
+    const TreeArgs &t = a.t;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cta_rank();
+    const unsigned pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    uint32_t *status = t.ctrl + MOE_CTRL_STATUS;
+
+    if (tid == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(peer_full + s, 1);
+            mbar_init(empty + s, 1);
+            mbar_init(v_full + s, 1);
+            mbar_init(peer_v + s, 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(s_full + x, 1);
+            mbar_init(p_full + x, 2 * MOE_LTC_SOFT);
+            mbar_init(pv_done + x, 1);
+        }
+        mbar_init(q_full, 2 * MOE_LTC_SOFT);
+        mbar_init(o_free, 2 * MOE_LTC_SOFT);
+        mbar_init(drained, 1);
+        fence_barrier_init();
+    }
+    pdl_wait();  // before tensor memory is taken: the last kernel may still need it
+    if (warp == 0)
+        tmem2_alloc(tmem_slot, 512);
+    long long lo, hi, run;
+    tc_fence_before();
+    tree_list<L, ROWS, TOKENS, MOE_LTC_COST, MOE_LTC_THREADS>(t, cum, items, scan, count, lo, hi, run, pair, pairs);
+    pair_sync();  // the barriers of both CTAs stand
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int tiles = (int)(hi - lo);
+    pdl_launch_dependents();
+    if (tiles == 0 && tid == 0 && rank == 0)
+        t.cuts[pair].runs = 0;
+    auto wait = [&](uint64_t *bar, int phase) {
+        return tree_poll(bar, (uint32_t)phase & 1u) || tree_wait_on(bar, (uint32_t)phase & 1u, status, t.wait_ns);
+    };
+    auto drain = [&](uint64_t *bar, int phase) { tree_wait_on(bar, (uint32_t)phase & 1u, status, max(t.wait_ns, MOE_TREE_DRAIN_NS)); };
+    auto to_item = [&](int u, TreeItem &it) {
+        if (u == 0)
+            it = tree_item<ROWS, TOKENS>(t, cum, lo);
+        else
+            tree_next<ROWS, TOKENS>(t, cum, it);
+    };
+    auto item_end = [&](const TreeItem &it) { return (int)(min(hi, it.lo + it.units) - lo); };
+    // lane i < 4: the slot of the i-th 16 tokens of tile u, and where there is none one past the pool, which reads as zeros
+    const int no_slot = t.n_pages * t.k.page;
+    auto find = [&](const TreeItem &it, int u, bool tell) {
+        const int j = (int)(lo + u - it.lo) * TOKENS + (lane & 3) * 16;
+        int slot = no_slot;
+        if (j < it.len) {
+            const int at = j / t.k.page, page = t.table[it.b * t.table_stride + at];
+            if (page >= 0 && page < t.n_pages)
+                slot = page * t.k.page + (j - at * t.k.page);
+            else if (tell && lane < 4)
+                atomicOr(status, (uint32_t)MOE_WS_INDEX);
+        }
+        return slot;
+    };
+    // copies of chunks `first` on (`n` of them) of the tokens' half h of a tile to `to`
+    auto copy = [&](const CUtensorMap *map, uint8_t *to, int first, int n, int slots, int h, uint64_t *bar) {
+        const int s0 = __shfl_sync(0xFFFFFFFFu, slots, 2 * h), s1 = __shfl_sync(0xFFFFFFFFu, slots, 2 * h + 1);
+        if (a.big) {
+            if (lane == 0)
+                tma_load_3d(to, map, 0, s0, first, bar);
+        } else {
+            for (int i = lane; i < 2 * n; i += 32)
+                tma_load_3d(to + (i >> 1) * MOE_LTC_CHUNK + (i & 1) * 2048, map, 0, i & 1 ? s1 : s0, first + (i >> 1), bar);
+        }
+    };
+
+    if (warp == MOE_LTC_SOFT) {
+        // ---------------- this CTA's half of each tile's tokens, whole rows
+        bool ok = true;
+        int u = 0, end = 0;
+        TreeItem it{};
+        for (; u < tiles; ++u) {
+            if (u == end) {
+                to_item(u, it);
+                end = item_end(it);
+            }
+            const int s = u % stages, slots = find(it, u, rank == 0);
+            const uint32_t out = __ballot_sync(0xFFFFFFFFu, slots == no_slot) & 15u;
+            if (u >= stages)
+                ok = __all_sync(0xFFFFFFFFu, wait(empty + s, u / stages - 1));
+            if (!ok)
+                break;
+            uint8_t *to = ring + (size_t)s * T::STAGE;
+            if (lane == 0) {
+                gone[u & 15] = out;
+                mbar_arrive_expect_tx(full + s, T::STAGE);
+            }
+            __syncwarp();
+            copy(&a.keys, to, 0, T::CHUNKS, slots, rank, full + s);
+            const int s0 = __shfl_sync(0xFFFFFFFFu, slots, 2 * rank), s1 = __shfl_sync(0xFFFFFFFFu, slots, 2 * rank + 1);
+            if (lane == 0)
+                tma_load_2d(to + T::CHUNKS * MOE_LTC_CHUNK, &a.ropes, 0, s0, full + s);
+            if (lane == 1 && !a.big)
+                tma_load_2d(to + T::CHUNKS * MOE_LTC_CHUNK + 2048, &a.ropes, 0, s1, full + s);
+        }
+        for (int k = max(0, u - stages); k < u; ++k) {  // nothing in flight, nothing to arrive when the CTA ends
+            drain(full + k % stages, k / stages);
+            if (ok)
+                drain(empty + k % stages, k / stages);
+        }
+    } else if (warp == MOE_LTC_SOFT + 2) {
+        // ---------------- the other tokens' values, once the tile's S is there
+        bool ok = true;
+        int u = 0, end = 0;
+        TreeItem it{};
+        for (; u < tiles; ++u) {
+            if (u == end) {
+                to_item(u, it);
+                end = item_end(it);
+            }
+            const int s = u % stages, slots = find(it, u, false), other = 1 - (int)rank;
+            ok = __all_sync(0xFFFFFFFFu, wait(s_full + (u & 1), u >> 1));
+            if (!ok)
+                break;
+            if (lane == 0)
+                mbar_arrive_expect_tx(v_full + s, T::HALF * MOE_LTC_CHUNK);
+            __syncwarp();
+            copy(&a.values, ring + (size_t)s * T::STAGE + other * T::HALF * MOE_LTC_CHUNK, (int)rank * T::HALF, T::HALF, slots,
+                 other, v_full + s);
+        }
+        for (int k = max(0, u - stages); k < u; ++k)
+            drain(v_full + k % stages, k / stages);
+    } else if (rank == 1 ? warp == MOE_LTC_SOFT + 1 || warp == MOE_LTC_SOFT + 3 : warp == MOE_LTC_SOFT + 3) {
+        // ---------------- tells the first CTA that this one's rows (values) are there
+        uint64_t *here = warp == MOE_LTC_SOFT + 1 ? full : v_full, *there = warp == MOE_LTC_SOFT + 1 ? peer_full : peer_v;
+        if (lane == 0 && rank == 1)
+            for (int u = 0; u < tiles && wait(here + u % stages, u / stages); ++u)
+                arrive_first(there + u % stages);
+    } else if (warp == MOE_LTC_SOFT + 1) {
+        // ---------------- the products, by the whole warp
+        constexpr uint32_t id_s = mma_idesc(ROWS, TOKENS, true), id_o = mma_idesc(ROWS, T::N, true) | (1u << 16);
+        const uint64_t qd = sw128_desc(sq), pd = sw128_desc(sp), rd = sw128_desc(ring), vd = mn128_desc(ring, MOE_LTC_CHUNK);
+        const uint32_t tm = __reduce_max_sync(0xFFFFFFFFu, tmem);
+        const int n = __reduce_max_sync(0xFFFFFFFFu, tiles);
+        bool ok = true;
+        int end = 0, item = -1, s = 0, phase = 0;  // s, phase: place of tile u in the ring
+        int s1 = 0, phase1 = 0;                    // of tile u - 1
+        bool begins = false;                       // tile u - 1: its item's first
+        TreeItem it{};
+        auto all = [&](bool v) { return __all_sync(0xFFFFFFFFu, v) != 0; };
+        auto second = [&](int u, int of) {  // O += P V of tile u, of item `of`
+            const int x = u & 1;
+            ok = ok && all(wait(v_full + s1, phase1)) && all(wait(peer_v + s1, phase1)) && all(wait(p_full + x, u >> 1)) &&
+                 (!begins || of == 0 || all(wait(o_free, of - 1)));
+            if (!ok)
+                return;
+            tc_fence_after();
+            const uint64_t v = vd + (uint32_t)(s1 * T::STAGE) / 16, p = pd + (uint32_t)(x * T::P_BYTES) / 16;
+#pragma unroll
+            for (int d = 0; d < L / T::N; ++d)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // 16 tokens: 32 bytes of P, 2048 of V
+                    mma2_f16(tm + O_COL + d * (T::N / 2), p + k * 2,
+                             v + (((k >> 1) * T::HALF + d * (T::N / 128)) * MOE_LTC_CHUNK + (k & 1) * 2048) / 16, id_o,
+                             !begins || k > 0);
+            mma2_commit(empty + s1);
+            mma2_commit(pv_done + x);
+        };
+        for (int u = 0; u < n && ok; ++u) {
+            const bool first = all(u == end);
+            if (first) {
+                to_item(u, it);
+                end = item_end(it);
+                ++item;
+                if (u > 0)  // before the next item's queries are waited for
+                    second(u - 1, item - 1);
+                ok = ok && all(wait(q_full, item));
+            }
+            ok = ok && all(wait(full + s, phase)) && all(wait(peer_full + s, phase));
+            if (!ok)
+                break;
+            tc_fence_after();
+            const uint64_t k = rd + (uint32_t)(s * T::STAGE) / 16;
+#pragma unroll
+            for (int d = 0; d <= T::CHUNKS; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mma2_f16(tm + (u & 1) * 32, qd + (d * T::Q_CHUNK + i * 32) / 16, k + (d * MOE_LTC_CHUNK + i * 32) / 16,
+                             id_s, d + i > 0);
+            mma2_commit(s_full + (u & 1));
+            if (u > 0 && !first)
+                second(u - 1, item);
+            begins = first;
+            s1 = s;
+            phase1 = phase;
+            if (++s == stages) {
+                s = 0;
+                ++phase;
+            }
+        }
+        if (n > 0 && ok)
+            second(n - 1, item);
+        if (!ok) {  // products may be in flight: they end before tensor and shared memory are given back
+            mma2_commit(drained);
+            drain(drained, 0);
+        }
+    } else {
+        // ---------------- softmax: row `row` of this CTA's, tokens (dimensions of O) of half `half`. No loop is left
+        // early: the warps of a pair meet at barriers.
+        const int row = tid & 63, half = tid >> 6, mine = (int)rank * 64 + row;
+        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        auto meet = [&]() { asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + (warp & 1)) : "memory"); };
+        const float sign = t.scale < 0.0f ? -1.0f : 1.0f;
+        const float scaled = fminf(fabsf(t.scale) * 1.4426950408889634f, 3.0e38f);
+        const bool flat = scaled == 0.0f;  // all scores alike: the queries are taken as zeros
+        const float c = flat ? 1.0f : scaled;
+        bool ok = true;
+        int item = 0;
+        TreeItem it{};
+        for (int u = 0; u < tiles; ++item) {
+            to_item(u, it);
+            const int end = item_end(it), at = it.block * ROWS + mine, rows = it.n * t.group;
+            const bool live = at < rows;
+            // ---- queries: the last item's S have been made (this warp has seen the last)
+            {
+                const int first = it.block * ROWS + (int)rank * 64, here = min(64, rows - first);
+                const uint32_t flip = sign < 0.0f ? 0x80008000u : 0u;
+                for (int r0 = warp; r0 < here; r0 += 4 * MOE_LTC_SOFT) {
+                    constexpr int PER = (T::CHUNKS + 3) / 4 + 1;  // 16-byte pieces of a lane in a row
+                    uint4 v[4][PER];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + i * MOE_LTC_SOFT;
+                        const int rr = first + r, token = it.first + rr / t.group, head = rr % t.group;
+#pragma unroll
+                        for (int p = 0; p < PER; ++p) {
+                            v[i][p] = make_uint4(0, 0, 0, 0);
+                            if (r >= here || flat)
+                                continue;
+                            const int piece = p * 32 + lane;
+                            if (p + 1 < PER) {
+                                if (piece < T::CHUNKS * 8)
+                                    v[i][p] = latent_get(t.q + token * t.q_tok + head * t.q_head + piece * 8, t.q_wide);
+                            } else if (lane < a.rope / 8) {
+                                v[i][p] = latent_get(a.qr + token * a.qr_tok + head * a.qr_head + lane * 8, a.qr_wide);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + i * MOE_LTC_SOFT;
+                        if (r >= here)
+                            break;
+#pragma unroll
+                        for (int p = 0; p < PER; ++p) {
+                            const int piece = p + 1 < PER ? p * 32 + lane : T::CHUNKS * 8 + lane;
+                            if (p + 1 < PER ? piece < T::CHUNKS * 8 : lane < 8) {
+                                const uint4 w = v[i][p];
+                                *reinterpret_cast<uint4 *>(sq + (piece >> 3) * T::Q_CHUNK + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) =
+                                    make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip);
+                            }
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    arrive_first(q_full);
+            }
+            const int node = live ? at / t.group : 0;
+            // the drafted tokens that it sees
+            const unsigned long long mask = !live ? 0 : (t.mask ? t.mask[it.first + node] : (2ull << node) - 1) &
+                                                         (it.n < 64 ? (1ull << it.n) - 1 : ~0ull);
+            const int prefix = it.len - it.n;
+            float m = -INFINITY, l = 0.0f;
+            bool fresh = true;
+            for (; u < end; ++u) {
+                const int x = u & 1, s = u % stages;
+                ok = ok && wait(s_full + x, u >> 1);
+                __syncwarp();
+                tc_fence_after();
+                const int first = (int)(lo + u - it.lo) * TOKENS;
+                const uint32_t out = *reinterpret_cast<volatile uint32_t *>(gone + (u & 15));
+                float v[32];
+                tmem_ld32(lanes + x * 32, v);
+                const bool masked = first + TOKENS > prefix || out;
+                if (masked) {
+                    const int off = prefix - (first + half * 32);
+                    uint32_t vis = off >= 32  ? ~0u
+                                   : off >= 0 ? ((1u << off) - 1) | (uint32_t)(mask << off)
+                                   : off > -64 ? (uint32_t)(mask >> -off)
+                                               : 0u;
+                    vis &= (out >> (2 * half) & 1 ? 0u : 0xFFFFu) | (out >> (2 * half + 1) & 1 ? 0u : 0xFFFF0000u);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = vis >> i & 1 ? v[i] : -INFINITY;
+                }
+                float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 32; i += 2)
+                    top4[i >> 1 & 3] = max3(top4[i >> 1 & 3], v[i], v[i + 1]);
+                float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                float *tops = top_of + x * 128;
+                tops[half * 64 + row] = top;
+                meet();
+                top = fmaxf(top, tops[(half ^ 1) * 64 + row]);
+                const bool moves = (top - m) * c > MOE_LTC_SLACK;
+                if (__any_sync(0xFFFFFFFFu, moves)) {
+                    const float f = moves ? ex2((m - top) * c) : 1.0f;
+                    m = moves ? top : m;
+                    l *= f;
+                    if (!fresh) {
+                        ok = ok && wait(pv_done + (x ^ 1), (u - 1) >> 1);  // O of the last tile is there
+                        __syncwarp();
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int k = 0; k < T::O_COLS; k += 16) {
+                            float o[16];
+                            uint32_t w[16];
+                            tmem_ld16(lanes + O_COL + k, o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                w[i] = __float_as_uint(o[i] * f);
+                            tmem_st16(lanes + O_COL + k, w);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.0f : -m;
+                const F2 ref2(ref, ref), c2(c, c);
+                uint32_t w[16];
+                F2 sum(0.0f, 0.0f), sum1(0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    float e0, e1;
+                    mul2(add2(F2(v[i], v[i + 1]), ref2), c2).get(e0, e1);
+                    const uint32_t p = pack_bf2(ex2(e0), ex2(e1));
+                    w[i / 2] = p;
+                    F2 &to = i & 2 ? sum1 : sum;
+                    to = add2(to, F2(bf16_lo(p), bf16_hi(p)));  // as rounded
+                }
+                sum = add2(sum, sum1);
+                float l0, l1;
+                sum.get(l0, l1);
+                l += l0 + l1;
+                fresh = false;
+                if (u > 1)  // P of the last tile but one has been read
+                    ok = ok && wait(pv_done + x, (u - 2) >> 1);
+                uint8_t *p = sp + x * T::P_BYTES + row * 128;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(p + (((half * 4 + i) ^ (row & 7)) << 4)) =
+                        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                if (first + TOKENS > prefix) {
+                    ok = ok && wait(v_full + s, u / stages);
+                    // Values past the length are anything, and those of drafted tokens need not be numbers, which must not
+                    // reach rows that do not see them: zeros in their place (a row that sees one has a NaN among its scores)
+                    uint8_t *values = ring + (size_t)s * T::STAGE;
+                    for (int i = tid; i < 64 * T::HALF * 8; i += MOE_LTC_SOFT * 32) {
+                        const int token = i / (T::HALF * 8), piece = i % (T::HALF * 8);
+                        if (first + token < prefix)
+                            continue;
+                        uint4 *q = reinterpret_cast<uint4 *>(values + ((token >> 5) * T::HALF + piece / 8) * MOE_LTC_CHUNK +
+                                                             (token & 31) * 128 + (piece & 7) * 16);
+                        uint4 y = make_uint4(0, 0, 0, 0);
+                        if (first + token < it.len) {
+                            y = *q;
+                            y = make_uint4(finite_bf2(y.x), finite_bf2(y.y), finite_bf2(y.z), finite_bf2(y.w));
+                        }
+                        *q = y;
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    arrive_first(p_full + x);
+            }
+            // ---- the item's end
+            sum_of[half * 64 + row] = l;
+            ok = ok && wait(pv_done + ((end - 1) & 1), (end - 1) >> 1);
+            meet();
+            __syncwarp();
+            l += sum_of[(half ^ 1) * 64 + row];
+            tc_fence_after();
+            const bool whole = it.lo >= lo && it.lo + it.units <= hi;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            float *part = t.part + ((size_t)pair * 2 + (it.lo <= lo ? 0 : 1)) * ROWS * (L + 2);
+            uint16_t *to = t.out + (it.first + node) * t.o_tok + (live ? at % t.group : 0) * t.o_head + half * (L / 2);
+#pragma unroll 1
+            for (int k = 0; k < T::O_COLS; k += 16) {
+                float o[16];
+                tmem_ld16(lanes + O_COL + k, o);
+                if (live && !whole) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        reinterpret_cast<float4 *>(part)[(half * (L / 2) + k + i) / 4 * ROWS + mine] =
+                            make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                } else if (live) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2)
+                        w[i / 2] = pack_bf2(o[i] * inv, o[i + 1] * inv);
+                    latent_put(to + k, make_uint4(w[0], w[1], w[2], w[3]), t.o_wide);
+                    latent_put(to + k + 8, make_uint4(w[4], w[5], w[6], w[7]), t.o_wide);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                arrive_first(o_free);
+            if (live && !whole && half == 0) {
+                part[ROWS * L + mine] = m * c;  // as an exponent of 2
+                part[ROWS * L + ROWS + mine] = l;
+            }
+            if (end == tiles && tid == 0 && rank == 0)
+                tree_cut<ROWS, MOE_LTC_COST>(t, it, items, lo, run, pair);
+            meet();  // the sums have been read
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    pair_sync();
+    if (warp == 0)
+        tmem2_dealloc(tmem, 512);
+    pair_sync();
+}
+
+}  // namespace moe

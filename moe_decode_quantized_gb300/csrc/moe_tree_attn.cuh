@@ -183,6 +183,14 @@ __device__ __forceinline__ long long tree_div(long long x, long long y)
     return tree_div_long(x, y);
 }
 
+// the largest of three (a NaN counts for nothing)
+__device__ __forceinline__ float max3(float x, float y, float z)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
 // zeros for the query rows of a sequence that does not hold
 template <int D>
 __device__ __forceinline__ void tree_zero(const TreeArgs &a, int first, int rows)
@@ -259,11 +267,12 @@ __device__ __forceinline__ long long tree_place(const TreeArgs &a, const long lo
     return cum[x] + at * units + min(off - at * (units + COST), (long long)units);
 }
 
-// Fills cum and items (scan, count: a word a warp) and gives this CTA's units
+// Fills cum and items (scan, count: a word a warp) and gives this CTA's (worker's) units
 // [lo, hi) and the cost of a run; zeros for rows of sequences that do not hold
 template <int D, int ROWS, int TOKENS, int COST, int NT>
 __device__ __forceinline__ void tree_list(const TreeArgs &a, long long *cum, int *items, long long *scan, int *count,
-                                          long long &lo, long long &hi, long long &run)
+                                          long long &lo, long long &hi, long long &run, unsigned worker = blockIdx.x,
+                                          unsigned workers = gridDim.x)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (a.batch + NT - 1) / NT;
     long long mine = 0;
@@ -279,7 +288,7 @@ __device__ __forceinline__ void tree_list(const TreeArgs &a, long long *cum, int
         const int here = n > 0 ? tree_blocks<ROWS>(n, a.group) * a.k.heads : 0;
         mine += (long long)((len + TOKENS - 1) / TOKENS) * here;
         own += here;
-        if (n == 0 && rows > 0 && blockIdx.x == (unsigned)(b % gridDim.x))
+        if (n == 0 && rows > 0 && worker == (unsigned)b % workers)
             tree_zero<D>(a, first, rows);
     }
     long long incl = mine;
@@ -314,8 +323,8 @@ __device__ __forceinline__ void tree_list(const TreeArgs &a, long long *cum, int
     }
     __syncthreads();
     const long long total = cum[a.batch] + (long long)COST * items[a.batch];
-    run = max(tree_div(total + gridDim.x - 1, gridDim.x), (long long)a.min_units);
-    const long long w = run * blockIdx.x + (lane & 1 ? run : 0);  // even lanes the begin, odd ones the end
+    run = max(tree_div(total + workers - 1, workers), (long long)a.min_units);
+    const long long w = run * worker + (lane & 1 ? run : 0);  // even lanes the begin, odd ones the end
     const long long place = w < total ? tree_place<ROWS, TOKENS, COST>(a, cum, items, w) : cum[a.batch];
     lo = __shfl_sync(0xFFFFFFFFu, place, 0);
     hi = __shfl_sync(0xFFFFFFFFu, place, 1);
@@ -435,12 +444,13 @@ __device__ __forceinline__ void tree_store(const TreeArgs &a, const TreeItem &it
 
 // the run's last item, if it starts in the run and goes on after it
 template <int ROWS, int COST>
-__device__ __forceinline__ void tree_cut(const TreeArgs &a, const TreeItem &it, const int *items, long long lo, long long run)
+__device__ __forceinline__ void tree_cut(const TreeArgs &a, const TreeItem &it, const int *items, long long lo, long long run,
+                                         unsigned worker = blockIdx.x)
 {
     const int ordinal = items[it.b] + it.head * tree_blocks<ROWS>(it.n, a.group) + it.block;
     const long long w = it.lo + (long long)COST * ordinal;  // where it begins in the list of costs
     const long long p0 = tree_div(w, run), p1 = tree_div(w + it.units - 1, run);
-    a.cuts[blockIdx.x] = {it.first, it.n, it.head, it.block, p0 == blockIdx.x ? (int)(p1 - p0) : 0, it.lo == lo};
+    a.cuts[worker] = {it.first, it.n, it.head, it.block, p0 == worker ? (int)(p1 - p0) : 0, it.lo == lo};
 }
 
 #define MOE_TREE_JOIN_ROWS 16

@@ -78,14 +78,6 @@ struct TtcRing {
     }
 };
 
-// the largest of three (a NaN counts for nothing)
-__device__ __forceinline__ float max3(float x, float y, float z)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-    return r;
-}
-
 // the softmax warps' own barrier
 __device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(MOE_TTC_SOFT * 32) : "memory"); }
 
