@@ -78,7 +78,7 @@ template <int L>
 LatentInstance latent_instance()
 {
     using T = LtcShape<L>;
-    return {moe_latent_tc_kernel<L>, 1024 + (size_t)T::RING_AT + T::SMALL, (size_t)T::STAGE,
+    return {moe_latent_tc_kernel<L>, (size_t)T::RING_AT + T::SMALL, (size_t)T::STAGE,
             {moe_tree_join_kernel<L, 256, 32, 4>, moe_tree_join_kernel<L, 256, 8, 8>}};
 }
 

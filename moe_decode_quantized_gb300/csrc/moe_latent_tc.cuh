@@ -49,12 +49,12 @@ struct LtcShape {
     static constexpr int STAGE = (CHUNKS + 1) * MOE_LTC_CHUNK;
     static constexpr int Q_CHUNK = 8192;         // 64 dimensions of 64 rows
     static constexpr int P_AT = (CHUNKS + 1) * Q_CHUNK;
-    static constexpr int P_BYTES = 8192;         // 64 tokens of 64 rows; two
-    static constexpr int RING_AT = P_AT + 2 * P_BYTES;
+    static constexpr int P_BYTES = 8192;         // 64 tokens of 64 rows
+    static constexpr int RING_AT = P_AT + P_BYTES;
     static constexpr int N = L < 256 ? L : 256;  // dimensions of one product
     static constexpr int O_COLS = L / 2;
-    // barriers; maxima [2][2][64], sums [2][64]; gone [16]; the scan and the list
-    static constexpr int SMALL = 512 + 6 * 64 * 4 + 64 + 32 * 8;
+    // barriers; maxima [2][2][64]; gone [16]; the scan, then the list
+    static constexpr int SMALL = 320 + 4 * 64 * 4 + 64 + 32 * 8;
 };
 
 // ---- pairs of CTAs
@@ -78,6 +78,33 @@ __device__ __forceinline__ void arrive_first(uint64_t *bar)
     asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
                  " mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar))
                  : "memory");
+}
+
+// the address of the barrier at `bar` in CTA `of` of the pair
+__device__ __forceinline__ uint32_t pair_bar(uint64_t *bar, uint32_t of)
+{
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(bar)), "r"(of));
+    return at;
+}
+
+// tma_load_3d (2d) into this CTA, counted by a barrier of either of the pair
+__device__ __forceinline__ void pair_load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void pair_load_2d(void *dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
 }
 
 // D[tmem] (+)= A[smem] . B[smem]: M rows over the pair, each CTA's shared memory holding half of A's rows and half of
@@ -136,15 +163,14 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
     constexpr int ROWS = MOE_LTC_ROWS, TOKENS = MOE_LTC_TOKENS;
     constexpr uint32_t O_COL = 64;  // of tensor memory: S (two of 32 columns), O
     extern __shared__ __align__(1024) uint8_t smem_any[];
-    uint8_t *smem = smem_any + (-smem_u32(smem_any) & 1023u);  // the swizzle goes by address bits
-    uint8_t *sq = smem, *sp = smem + T::P_AT, *ring = smem + T::RING_AT, *small = ring + (size_t)stages * T::STAGE;
+    uint8_t *sq = smem_any, *sp = smem_any + T::P_AT, *ring = smem_any + T::RING_AT, *small = ring + (size_t)stages * T::STAGE;
     uint64_t *bars = reinterpret_cast<uint64_t *>(small);
-    uint64_t *full = bars, *peer_full = bars + 8, *empty = bars + 16, *v_full = bars + 24;  // [stages]
-    uint64_t *s_full = bars + 32, *p_full = bars + 34, *pv_done = bars + 36;                // [2]
-    uint64_t *q_full = bars + 38, *o_free = bars + 39, *drained = bars + 40, *peer_v = bars + 41;  // peer_v [stages]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 49);
-    float *top_of = reinterpret_cast<float *>(small + 512), *sum_of = top_of + 256;  // [2][2][64], [2][64]
-    uint32_t *gone = reinterpret_cast<uint32_t *>(sum_of + 128);  // [16] 16-token groups of tile t that are not there, at t % 16
+    uint64_t *full = bars, *empty = bars + 8, *v_full = bars + 16;             // [stages]
+    uint64_t *s_full = bars + 24, *p_full = bars + 26, *pv_done = bars + 28;   // [2]
+    uint64_t *q_full = bars + 30, *o_free = bars + 31, *v_here = bars + 32, *drained = bars + 34;  // v_here [2], drained [3]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 37);
+    float *top_of = reinterpret_cast<float *>(small + 320);  // [2][2][64]
+    uint32_t *gone = reinterpret_cast<uint32_t *>(top_of + 256);  // [16] 16-token groups of tile t that are not there, at t % 16
     long long *scan = reinterpret_cast<long long *>(gone + 16), *cum = scan + 32;  // cum [batch + 1]
     int *count = reinterpret_cast<int *>(scan + 20), *items = reinterpret_cast<int *>(cum + a.t.batch + 1);  // items [batch + 1]
     const TreeArgs &t = a.t;
@@ -156,19 +182,19 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
     if (tid == 0) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(full + s, 1);
-            mbar_init(peer_full + s, 1);
             mbar_init(empty + s, 1);
             mbar_init(v_full + s, 1);
-            mbar_init(peer_v + s, 1);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(s_full + x, 1);
             mbar_init(p_full + x, 2 * MOE_LTC_SOFT);
             mbar_init(pv_done + x, 1);
+            mbar_init(v_here + x, 1);
         }
         mbar_init(q_full, 2 * MOE_LTC_SOFT);
         mbar_init(o_free, 2 * MOE_LTC_SOFT);
-        mbar_init(drained, 1);
+        for (int i = 0; i < 3; ++i)
+            mbar_init(drained + i, 1);
         fence_barrier_init();
     }
     pdl_wait();  // before tensor memory is taken: the last kernel may still need it
@@ -209,17 +235,19 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
         }
         return slot;
     };
-    // copies of chunks `first` on (`n` of them) of the tokens' half h of a tile to `to`
-    auto copy = [&](const CUtensorMap *map, uint8_t *to, int first, int n, int slots, int h, uint64_t *bar) {
+    // copies of chunks `first` on (`n` of them) of the tokens' half h of a tile to `to`, counted by `bar` (pair_bar)
+    auto copy = [&](const CUtensorMap *map, uint8_t *to, int first, int n, int slots, int h, uint32_t bar) {
         const int s0 = __shfl_sync(0xFFFFFFFFu, slots, 2 * h), s1 = __shfl_sync(0xFFFFFFFFu, slots, 2 * h + 1);
         if (a.big) {
             if (lane == 0)
-                tma_load_3d(to, map, 0, s0, first, bar);
+                pair_load_3d(to, map, 0, s0, first, bar);
         } else {
             for (int i = lane; i < 2 * n; i += 32)
-                tma_load_3d(to + (i >> 1) * MOE_LTC_CHUNK + (i & 1) * 2048, map, 0, i & 1 ? s1 : s0, first + (i >> 1), bar);
+                pair_load_3d(to + (i >> 1) * MOE_LTC_CHUNK + (i & 1) * 2048, map, 0, i & 1 ? s1 : s0, first + (i >> 1), bar);
         }
     };
+    // a tile whose tokens not all rows see, or not all of which are there
+    auto special = [&](const TreeItem &it, int u) { return (int)(lo + u - it.lo) * TOKENS + TOKENS > it.len - it.n; };
 
     if (warp == MOE_LTC_SOFT) {
         // ---------------- this CTA's half of each tile's tokens, whole rows
@@ -240,21 +268,20 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             uint8_t *to = ring + (size_t)s * T::STAGE;
             if (lane == 0) {
                 gone[u & 15] = out;
-                mbar_arrive_expect_tx(full + s, T::STAGE);
+                if (rank == 0)  // both CTAs' copies (the other's may come before this)
+                    mbar_arrive_expect_tx(full + s, 2 * T::STAGE);
             }
             __syncwarp();
-            copy(&a.keys, to, 0, T::CHUNKS, slots, rank, full + s);
+            const uint32_t bar = pair_bar(full + s, 0);
+            copy(&a.keys, to, 0, T::CHUNKS, slots, rank, bar);
             const int s0 = __shfl_sync(0xFFFFFFFFu, slots, 2 * rank), s1 = __shfl_sync(0xFFFFFFFFu, slots, 2 * rank + 1);
             if (lane == 0)
-                tma_load_2d(to + T::CHUNKS * MOE_LTC_CHUNK, &a.ropes, 0, s0, full + s);
+                pair_load_2d(to + T::CHUNKS * MOE_LTC_CHUNK, &a.ropes, 0, s0, bar);
             if (lane == 1 && !a.big)
-                tma_load_2d(to + T::CHUNKS * MOE_LTC_CHUNK + 2048, &a.ropes, 0, s1, full + s);
+                pair_load_2d(to + T::CHUNKS * MOE_LTC_CHUNK + 2048, &a.ropes, 0, s1, bar);
         }
-        for (int k = max(0, u - stages); k < u; ++k) {  // nothing in flight, nothing to arrive when the CTA ends
-            drain(full + k % stages, k / stages);
-            if (ok)
-                drain(empty + k % stages, k / stages);
-        }
+        for (int k = max(0, u - stages); k < u; ++k)  // nothing in flight, nothing to arrive when the CTA ends
+            drain(ok ? empty + k % stages : rank == 0 ? full + k % stages : drained + 2, ok || rank == 0 ? k / stages : 0);
     } else if (warp == MOE_LTC_SOFT + 2) {
         // ---------------- the other tokens' values, once the tile's S is there
         bool ok = true;
@@ -269,89 +296,76 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             ok = __all_sync(0xFFFFFFFFu, wait(s_full + (u & 1), u >> 1));
             if (!ok)
                 break;
-            if (lane == 0)
-                mbar_arrive_expect_tx(v_full + s, T::HALF * MOE_LTC_CHUNK);
+            // counted by the first CTA's barrier, but in a tile that the softmax warps look through by their own CTA's
+            const bool own = special(it, u);
+            if (lane == 0 && (rank == 0 || own))
+                mbar_arrive_expect_tx(rank == 0 ? v_full + s : v_here + (u & 1), (own ? 1 : 2) * T::HALF * MOE_LTC_CHUNK);
             __syncwarp();
             copy(&a.values, ring + (size_t)s * T::STAGE + other * T::HALF * MOE_LTC_CHUNK, (int)rank * T::HALF, T::HALF, slots,
-                 other, v_full + s);
+                 other, own && rank == 1 ? pair_bar(v_here + (u & 1), 1) : pair_bar(v_full + s, 0));
         }
-        for (int k = max(0, u - stages); k < u; ++k)
-            drain(v_full + k % stages, k / stages);
-    } else if (rank == 1 ? warp == MOE_LTC_SOFT + 1 || warp == MOE_LTC_SOFT + 3 : warp == MOE_LTC_SOFT + 3) {
-        // ---------------- tells the first CTA that this one's rows (values) are there
-        uint64_t *here = warp == MOE_LTC_SOFT + 1 ? full : v_full, *there = warp == MOE_LTC_SOFT + 1 ? peer_full : peer_v;
-        if (lane == 0 && rank == 1)
-            for (int u = 0; u < tiles && wait(here + u % stages, u / stages); ++u)
-                arrive_first(there + u % stages);
-    } else if (warp == MOE_LTC_SOFT + 1) {
-        // ---------------- the products, by the whole warp
+        for (int k = max(0, u - stages); k < u && !ok; ++k)
+            drain(rank == 0 ? v_full + k % stages : drained + 2, rank == 0 ? k / stages : 0);
+    } else if (warp >= MOE_LTC_SOFT && rank == 0) {
+        // ---------------- the products: a warp those of S, another those of O, so that one's waits pass under the
+        // other's products
+        const bool scores = warp == MOE_LTC_SOFT + 1;
         constexpr uint32_t id_s = mma_idesc(ROWS, TOKENS, true), id_o = mma_idesc(ROWS, T::N, true) | (1u << 16);
         const uint64_t qd = sw128_desc(sq), pd = sw128_desc(sp), rd = sw128_desc(ring), vd = mn128_desc(ring, MOE_LTC_CHUNK);
-        const uint32_t tm = __reduce_max_sync(0xFFFFFFFFu, tmem);
+        const uint32_t tm = __reduce_max_sync(0xFFFFFFFFu, tmem);  // (what the loops need is the same in all lanes)
         const int n = __reduce_max_sync(0xFFFFFFFFu, tiles);
         bool ok = true;
-        int end = 0, item = -1, s = 0, phase = 0;  // s, phase: place of tile u in the ring
-        int s1 = 0, phase1 = 0;                    // of tile u - 1
-        bool begins = false;                       // tile u - 1: its item's first
+        int end = 0, item = -1, s = 0, phase = 0;
         TreeItem it{};
         auto all = [&](bool v) { return __all_sync(0xFFFFFFFFu, v) != 0; };
-        auto second = [&](int u, int of) {  // O += P V of tile u, of item `of`
+        for (int u = 0; u < n; ++u) {
             const int x = u & 1;
-            ok = ok && all(wait(v_full + s1, phase1)) && all(wait(peer_v + s1, phase1)) && all(wait(p_full + x, u >> 1)) &&
-                 (!begins || of == 0 || all(wait(o_free, of - 1)));
-            if (!ok)
-                return;
-            tc_fence_after();
-            const uint64_t v = vd + (uint32_t)(s1 * T::STAGE) / 16, p = pd + (uint32_t)(x * T::P_BYTES) / 16;
-#pragma unroll
-            for (int d = 0; d < L / T::N; ++d)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)  // 16 tokens: 32 bytes of P, 2048 of V
-                    mma2_f16(tm + O_COL + d * (T::N / 2), p + k * 2,
-                             v + (((k >> 1) * T::HALF + d * (T::N / 128)) * MOE_LTC_CHUNK + (k & 1) * 2048) / 16, id_o,
-                             !begins || k > 0);
-            mma2_commit(empty + s1);
-            mma2_commit(pv_done + x);
-        };
-        for (int u = 0; u < n && ok; ++u) {
             const bool first = all(u == end);
             if (first) {
                 to_item(u, it);
                 end = item_end(it);
                 ++item;
-                if (u > 0)  // before the next item's queries are waited for
-                    second(u - 1, item - 1);
-                ok = ok && all(wait(q_full, item));
+                ok = ok && (scores ? all(wait(q_full, item)) : item == 0 || all(wait(o_free, item - 1)));
             }
-            ok = ok && all(wait(full + s, phase)) && all(wait(peer_full + s, phase));
-            if (!ok)
-                break;
-            tc_fence_after();
-            const uint64_t k = rd + (uint32_t)(s * T::STAGE) / 16;
+            if (scores) {  // S of tile u, in the place of the last but one, which has been read
+                ok = ok && all(wait(full + s, phase)) && (u < 2 || all(wait(p_full + x, (u >> 1) - 1)));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint64_t k = rd + (uint32_t)(s * T::STAGE) / 16;
 #pragma unroll
-            for (int d = 0; d <= T::CHUNKS; ++d)
+                for (int d = 0; d <= T::CHUNKS; ++d)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mma2_f16(tm + (u & 1) * 32, qd + (d * T::Q_CHUNK + i * 32) / 16, k + (d * MOE_LTC_CHUNK + i * 32) / 16,
-                             id_s, d + i > 0);
-            mma2_commit(s_full + (u & 1));
-            if (u > 0 && !first)
-                second(u - 1, item);
-            begins = first;
-            s1 = s;
-            phase1 = phase;
+                    for (int i = 0; i < 4; ++i)
+                        mma2_f16(tm + x * 32, qd + (d * T::Q_CHUNK + i * 32) / 16, k + (d * MOE_LTC_CHUNK + i * 32) / 16, id_s,
+                                 d + i > 0);
+                mma2_commit(s_full + x);
+            } else {  // O += P V
+                ok = ok && all(wait(v_full + s, phase)) && all(wait(p_full + x, u >> 1));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint64_t v = vd + (uint32_t)(s * T::STAGE) / 16, p = pd;
+#pragma unroll
+                for (int d = 0; d < L / T::N; ++d)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)  // 16 tokens: 32 bytes of P, 2048 of V
+                        mma2_f16(tm + O_COL + d * (T::N / 2), p + k * 2,
+                                 v + (((k >> 1) * T::HALF + d * (T::N / 128)) * MOE_LTC_CHUNK + (k & 1) * 2048) / 16, id_o,
+                                 !first || k > 0);
+                mma2_commit(empty + s);
+                mma2_commit(pv_done + x);
+            }
             if (++s == stages) {
                 s = 0;
                 ++phase;
             }
         }
-        if (n > 0 && ok)
-            second(n - 1, item);
         if (!ok) {  // products may be in flight: they end before tensor and shared memory are given back
-            mma2_commit(drained);
-            drain(drained, 0);
+            mma2_commit(drained + scores);
+            drain(drained + scores, 0);
         }
-    } else {
+    } else if (warp < MOE_LTC_SOFT) {
         // ---------------- softmax: row `row` of this CTA's, tokens (dimensions of O) of half `half`. No loop is left
         // early: the warps of a pair meet at barriers.
         const int row = tid & 63, half = tid >> 6, mine = (int)rank * 64 + row;
@@ -363,6 +377,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
         const float c = flat ? 1.0f : scaled;
         bool ok = true;
         int item = 0;
+        uint32_t seen = 0;  // by x, a bit each: parity of the tiles looked through
         TreeItem it{};
         for (int u = 0; u < tiles; ++item) {
             to_item(u, it);
@@ -491,15 +506,16 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 sum.get(l0, l1);
                 l += l0 + l1;
                 fresh = false;
-                if (u > 1)  // P of the last tile but one has been read
-                    ok = ok && wait(pv_done + x, (u - 2) >> 1);
-                uint8_t *p = sp + x * T::P_BYTES + row * 128;
+                if (u > 0)  // P of the last tile has been read
+                    ok = ok && wait(pv_done + (x ^ 1), (u - 1) >> 1);
+                uint8_t *p = sp + row * 128;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     *reinterpret_cast<uint4 *>(p + (((half * 4 + i) ^ (row & 7)) << 4)) =
                         make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                if (first + TOKENS > prefix) {
-                    ok = ok && wait(v_full + s, u / stages);
+                if (special(it, u)) {
+                    ok = ok && (rank == 0 ? wait(v_full + s, u / stages) : wait(v_here + x, (int)(seen >> x & 1)));
+                    seen ^= 1u << x;
                     // Values past the length are anything, and those of drafted tokens need not be numbers, which must not
                     // reach rows that do not see them: zeros in their place (a row that sees one has a NaN among its scores)
                     uint8_t *values = ring + (size_t)s * T::STAGE;
@@ -524,11 +540,12 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                     arrive_first(p_full + x);
             }
             // ---- the item's end
-            sum_of[half * 64 + row] = l;
+            float *sums = top_of + (end & 1) * 128;  // (the maxima that the last tile has not used)
+            sums[half * 64 + row] = l;
             ok = ok && wait(pv_done + ((end - 1) & 1), (end - 1) >> 1);
             meet();
             __syncwarp();
-            l += sum_of[(half ^ 1) * 64 + row];
+            l += sums[(half ^ 1) * 64 + row];
             tc_fence_after();
             const bool whole = it.lo >= lo && it.lo + it.units <= hi;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
