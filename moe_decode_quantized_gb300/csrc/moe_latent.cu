@@ -71,7 +71,7 @@ std::mutex g_latent_mu;
 struct LatentInstance {
     void (*kernel)(LatentArgs, int);
     size_t fixed, stage;  // bytes of shared memory beside the ring and the list; of a stage
-    void (*join[2])(TreeArgs, int, int);  // for many items, for few long ones
+    void (*join)(TreeArgs), (*join_long)(TreeArgs, int, int);  // of many items, of few long ones
 };
 
 template <int L>
@@ -79,7 +79,7 @@ LatentInstance latent_instance()
 {
     using T = LtcShape<L>;
     return {moe_latent_tc_kernel<L>, (size_t)T::RING_AT + T::SMALL, (size_t)T::STAGE,
-            {moe_tree_join_kernel<L, 256, 32, 4>, moe_tree_join_kernel<L, 256, 8, 8>}};
+            moe_latent_join_kernel<L>, moe_tree_join_kernel<L, 256, 8, 8>};
 }
 
 struct LatentDevice {
@@ -422,14 +422,17 @@ int moe_latent_attention(const moe_latent_cache *cache, const void *q_dev, int64
     lc.attrs = at;
     lc.numAttrs = 2;
     MOE_CUDA_OK(cudaLaunchKernelEx(&lc, inst.kernel, a, stages));
-    // the join: the runs that each item may span decide on the instance (moe_spec.cu has the figures)
+    // the join, by the parts that each item may have
     const int rows = (n_tokens + batch - 1) / batch * heads, runs = dev->pairs;
     const long long items = (long long)batch * ((rows + MOE_LTC_ROWS - 1) / MOE_LTC_ROWS);
-    const bool deep = runs / items >= 24;
-    const int blocks = std::min((rows + MOE_TREE_JOIN_ROWS - 1) / MOE_TREE_JOIN_ROWS, MOE_LTC_ROWS / MOE_TREE_JOIN_ROWS);
-    const dim3 grid((unsigned)runs, (unsigned)(batch == 1 ? blocks : MOE_LTC_ROWS / MOE_TREE_JOIN_ROWS),
-                    (unsigned)(deep ? latent / 32 : latent / 128));
-    MOE_CUDA_OK(launch(inst.join[deep], grid, 256, 0, stream, t, MOE_LTC_ROWS, runs));
+    if (runs / items >= 24) {
+        const int blocks = std::min((rows + MOE_TREE_JOIN_ROWS - 1) / MOE_TREE_JOIN_ROWS, MOE_LTC_ROWS / MOE_TREE_JOIN_ROWS);
+        const dim3 grid((unsigned)runs, (unsigned)(batch == 1 ? blocks : MOE_LTC_ROWS / MOE_TREE_JOIN_ROWS),
+                        (unsigned)(latent / 32));
+        MOE_CUDA_OK(launch(inst.join_long, grid, 256, 0, stream, t, MOE_LTC_ROWS, runs));
+    } else {
+        MOE_CUDA_OK(launch(inst.join, dim3((unsigned)runs, (unsigned)(latent / 32)), MOE_LTC_JOIN_THREADS, 0, stream, t));
+    }
     return MOE_OK;
 }
 

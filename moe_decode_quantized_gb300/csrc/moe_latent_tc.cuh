@@ -28,7 +28,7 @@ namespace moe {
 #define MOE_LTC_ROWS 128   // of a pair
 #define MOE_LTC_COST 3     // of an item, beside its tiles
 #define MOE_LTC_SOFT 4     // softmax warps
-#define MOE_LTC_THREADS ((MOE_LTC_SOFT + 4) * 32)
+#define MOE_LTC_THREADS ((MOE_LTC_SOFT + 5) * 32)
 #define MOE_LTC_MAX_STAGES 8
 #define MOE_LTC_CHUNK 4096  // 64 dimensions of 32 tokens
 #define MOE_LTC_SLACK 8.0f  // m moves when an exponent passes it by this
@@ -54,7 +54,7 @@ struct LtcShape {
     static constexpr int N = L < 256 ? L : 256;  // dimensions of one product
     static constexpr int O_COLS = L / 2;
     // barriers; maxima [2][2][64]; gone [16]; the scan, then the list
-    static constexpr int SMALL = 320 + 4 * 64 * 4 + 64 + 32 * 8;
+    static constexpr int SMALL = 384 + 4 * 64 * 4 + 64 + 32 * 8;
 };
 
 // ---- pairs of CTAs
@@ -165,11 +165,11 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
     extern __shared__ __align__(1024) uint8_t smem_any[];
     uint8_t *sq = smem_any, *sp = smem_any + T::P_AT, *ring = smem_any + T::RING_AT, *small = ring + (size_t)stages * T::STAGE;
     uint64_t *bars = reinterpret_cast<uint64_t *>(small);
-    uint64_t *full = bars, *empty = bars + 8, *v_full = bars + 16;             // [stages]
-    uint64_t *s_full = bars + 24, *p_full = bars + 26, *pv_done = bars + 28;   // [2]
-    uint64_t *q_full = bars + 30, *o_free = bars + 31, *v_here = bars + 32, *drained = bars + 34;  // v_here [2], drained [3]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 37);
-    float *top_of = reinterpret_cast<float *>(small + 320);  // [2][2][64]
+    uint64_t *full = bars, *empty = bars + 8, *v_full = bars + 16, *s_full = bars + 24;  // [stages]
+    uint64_t *p_full = bars + 32, *pv_done = bars + 34, *v_here = bars + 36;             // [2]
+    uint64_t *q_full = bars + 38, *o_free = bars + 39, *drained = bars + 40;             // drained [4]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 44);
+    float *top_of = reinterpret_cast<float *>(small + 384);  // [2][2][64]
     uint32_t *gone = reinterpret_cast<uint32_t *>(top_of + 256);  // [16] 16-token groups of tile t that are not there, at t % 16
     long long *scan = reinterpret_cast<long long *>(gone + 16), *cum = scan + 32;  // cum [batch + 1]
     int *count = reinterpret_cast<int *>(scan + 20), *items = reinterpret_cast<int *>(cum + a.t.batch + 1);  // items [batch + 1]
@@ -184,16 +184,16 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
             mbar_init(v_full + s, 1);
+            mbar_init(s_full + s, 1);
         }
         for (int x = 0; x < 2; ++x) {
-            mbar_init(s_full + x, 1);
             mbar_init(p_full + x, 2 * MOE_LTC_SOFT);
             mbar_init(pv_done + x, 1);
             mbar_init(v_here + x, 1);
         }
         mbar_init(q_full, 2 * MOE_LTC_SOFT);
         mbar_init(o_free, 2 * MOE_LTC_SOFT);
-        for (int i = 0; i < 3; ++i)
+        for (int i = 0; i < 4; ++i)
             mbar_init(drained + i, 1);
         fence_barrier_init();
     }
@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 pair_load_2d(to + T::CHUNKS * MOE_LTC_CHUNK + 2048, &a.ropes, 0, s1, bar);
         }
         for (int k = max(0, u - stages); k < u; ++k)  // nothing in flight, nothing to arrive when the CTA ends
-            drain(ok ? empty + k % stages : rank == 0 ? full + k % stages : drained + 2, ok || rank == 0 ? k / stages : 0);
-    } else if (warp == MOE_LTC_SOFT + 2) {
+            drain(ok ? empty + k % stages : rank == 0 ? full + k % stages : drained + 3, ok || rank == 0 ? k / stages : 0);
+    } else if (warp == MOE_LTC_SOFT + 4) {
         // ---------------- the other tokens' values, once the tile's S is there
         bool ok = true;
         int u = 0, end = 0;
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 end = item_end(it);
             }
             const int s = u % stages, slots = find(it, u, false), other = 1 - (int)rank;
-            ok = __all_sync(0xFFFFFFFFu, wait(s_full + (u & 1), u >> 1));
+            ok = __all_sync(0xFFFFFFFFu, wait(s_full + s, u / stages));
             if (!ok)
                 break;
             // counted by the first CTA's barrier, but in a tile that the softmax warps look through by their own CTA's
@@ -305,11 +305,12 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                  other, own && rank == 1 ? pair_bar(v_here + (u & 1), 1) : pair_bar(v_full + s, 0));
         }
         for (int k = max(0, u - stages); k < u && !ok; ++k)
-            drain(rank == 0 ? v_full + k % stages : drained + 2, rank == 0 ? k / stages : 0);
+            drain(rank == 0 ? v_full + k % stages : drained + 3, rank == 0 ? k / stages : 0);
     } else if (warp >= MOE_LTC_SOFT && rank == 0) {
-        // ---------------- the products: a warp those of S, another those of O, so that one's waits pass under the
-        // other's products
-        const bool scores = warp == MOE_LTC_SOFT + 1;
+        // ---------------- the products: two warps those of S, a tile each in turn, another those of O, so that one's
+        // waits pass under the others' products
+        const int role = warp - MOE_LTC_SOFT - 1;
+        const bool scores = role != 2;
         constexpr uint32_t id_s = mma_idesc(ROWS, TOKENS, true), id_o = mma_idesc(ROWS, T::N, true) | (1u << 16);
         const uint64_t qd = sw128_desc(sq), pd = sw128_desc(sp), rd = sw128_desc(ring), vd = mn128_desc(ring, MOE_LTC_CHUNK);
         const uint32_t tm = __reduce_max_sync(0xFFFFFFFFu, tmem);  // (what the loops need is the same in all lanes)
@@ -327,8 +328,10 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 ++item;
                 ok = ok && (scores ? all(wait(q_full, item)) : item == 0 || all(wait(o_free, item - 1)));
             }
-            if (scores) {  // S of tile u, in the place of the last but one, which has been read
-                ok = ok && all(wait(full + s, phase)) && (u < 2 || all(wait(p_full + x, (u >> 1) - 1)));
+            if (scores && x == (role != 0)) {
+                // S of tile u, in the place of the last but one, which has been read (and first that wait: then the tile
+                // before has had its turn, and no phase of `full` is passed over)
+                ok = ok && (u < 2 || all(wait(p_full + x, (u >> 1) - 1))) && all(wait(full + s, phase));
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -339,8 +342,8 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                     for (int i = 0; i < 4; ++i)
                         mma2_f16(tm + x * 32, qd + (d * T::Q_CHUNK + i * 32) / 16, k + (d * MOE_LTC_CHUNK + i * 32) / 16, id_s,
                                  d + i > 0);
-                mma2_commit(s_full + x);
-            } else {  // O += P V
+                mma2_commit(s_full + s);  // (by stages, so that the values' copies may lag)
+            } else if (!scores) {  // O += P V
                 ok = ok && all(wait(v_full + s, phase)) && all(wait(p_full + x, u >> 1));
                 if (!ok)
                     break;
@@ -362,8 +365,8 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             }
         }
         if (!ok) {  // products may be in flight: they end before tensor and shared memory are given back
-            mma2_commit(drained + scores);
-            drain(drained + scores, 0);
+            mma2_commit(drained + role);
+            drain(drained + role, 0);
         }
     } else if (warp < MOE_LTC_SOFT) {
         // ---------------- softmax: row `row` of this CTA's, tokens (dimensions of O) of half `half`. No loop is left
@@ -373,7 +376,8 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
         auto meet = [&]() { asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + (warp & 1)) : "memory"); };
         const float sign = t.scale < 0.0f ? -1.0f : 1.0f;
         const float scaled = fminf(fabsf(t.scale) * 1.4426950408889634f, 3.0e38f);
-        const bool flat = scaled == 0.0f;  // all scores alike: the queries are taken as zeros
+        const bool flat = scaled == 0.0f;  // all scores alike
+        const float turn = flat ? 0.0f : sign;
         const float c = flat ? 1.0f : scaled;
         bool ok = true;
         int item = 0;
@@ -386,44 +390,26 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             // ---- queries: the last item's S have been made (this warp has seen the last)
             {
                 const int first = it.block * ROWS + (int)rank * 64, here = min(64, rows - first);
-                const uint32_t flip = sign < 0.0f ? 0x80008000u : 0u;
-                for (int r0 = warp; r0 < here; r0 += 4 * MOE_LTC_SOFT) {
-                    constexpr int PER = (T::CHUNKS + 3) / 4 + 1;  // 16-byte pieces of a lane in a row
-                    uint4 v[4][PER];
+                for (int r = warp; r < here; r += MOE_LTC_SOFT) {
+                    const int token = it.first + (first + r) / t.group, head = (first + r) % t.group;
+                    const uint16_t *q = t.q + token * t.q_tok + head * t.q_head, *qr = a.qr + token * a.qr_tok + head * a.qr_head;
+                    uint8_t *to = sq + r * 128;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r0 + i * MOE_LTC_SOFT;
-                        const int rr = first + r, token = it.first + rr / t.group, head = rr % t.group;
-#pragma unroll
-                        for (int p = 0; p < PER; ++p) {
-                            v[i][p] = make_uint4(0, 0, 0, 0);
-                            if (r >= here || flat)
-                                continue;
-                            const int piece = p * 32 + lane;
-                            if (p + 1 < PER) {
-                                if (piece < T::CHUNKS * 8)
-                                    v[i][p] = latent_get(t.q + token * t.q_tok + head * t.q_head + piece * 8, t.q_wide);
-                            } else if (lane < a.rope / 8) {
-                                v[i][p] = latent_get(a.qr + token * a.qr_tok + head * a.qr_head + lane * 8, a.qr_wide);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r0 + i * MOE_LTC_SOFT;
-                        if (r >= here)
-                            break;
-#pragma unroll
-                        for (int p = 0; p < PER; ++p) {
-                            const int piece = p + 1 < PER ? p * 32 + lane : T::CHUNKS * 8 + lane;
-                            if (p + 1 < PER ? piece < T::CHUNKS * 8 : lane < 8) {
-                                const uint4 w = v[i][p];
-                                *reinterpret_cast<uint4 *>(sq + (piece >> 3) * T::Q_CHUNK + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) =
-                                    make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip);
-                            }
-                        }
+                    for (int i = lane; i < T::CHUNKS * 8 + 8; i += 32) {
+                        const bool turning = i >= T::CHUNKS * 8;
+                        const int k = turning ? i - T::CHUNKS * 8 : i;
+                        uint4 *at = reinterpret_cast<uint4 *>(to + (i >> 3) * T::Q_CHUNK + (((i & 7) ^ (r & 7)) << 4));
+                        if (turning && k >= a.rope / 8)
+                            *at = make_uint4(0, 0, 0, 0);
+                        else if (turning ? a.qr_wide : t.q_wide)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(at)),
+                                         "l"((turning ? qr : q) + k * 8)
+                                         : "memory");
+                        else
+                            *at = latent_get((turning ? qr : q) + k * 8, false);
                     }
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
@@ -438,13 +424,17 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             bool fresh = true;
             for (; u < end; ++u) {
                 const int x = u & 1, s = u % stages;
-                ok = ok && wait(s_full + x, u >> 1);
+                ok = ok && wait(s_full + s, u / stages);
                 __syncwarp();
                 tc_fence_after();
                 const int first = (int)(lo + u - it.lo) * TOKENS;
                 const uint32_t out = *reinterpret_cast<volatile uint32_t *>(gone + (u & 15));
                 float v[32];
                 tmem_ld32(lanes + x * 32, v);
+                if (turn != 1.0f)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] *= turn;
                 const bool masked = first + TOKENS > prefix || out;
                 if (masked) {
                     const int off = prefix - (first + half * 32);
@@ -588,6 +578,69 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
     if (warp == 0)
         tmem2_dealloc(tmem, 512);
     pair_sync();
+}
+
+// Joins the partials of cut items of few parts, in order: a thread a row and 16 dimensions (a sector of the output), the
+// rows of a warp side by side in the partials; CTA (run, 32 dimensions). moe_tree_join_kernel, whose threads share an
+// item's parts, takes those of many.
+#define MOE_LTC_JOIN_THREADS 256
+template <int L>
+__global__ void __launch_bounds__(MOE_LTC_JOIN_THREADS) moe_latent_join_kernel(const __grid_constant__ TreeArgs a)
+{
+    constexpr int ROWS = MOE_LTC_ROWS, U = 4;  // parts in flight
+    const int r = threadIdx.x % ROWS, d = (blockIdx.y * (MOE_LTC_JOIN_THREADS / ROWS) + threadIdx.x / ROWS) * 16;
+    constexpr size_t SIZE = (size_t)ROWS * (L + 2);
+    pdl_wait();
+    const TreeCut c = a.cuts[blockIdx.x];
+    const int rr = c.block * ROWS + r;
+    if (c.runs == 0 || rr >= c.n * a.group)
+        return;
+    // part i: of the first run the second slot, unless the item begins with the run
+    const float *base = a.part + (size_t)blockIdx.x * 2 * SIZE;
+    auto part = [&](int i) { return base + (i == 0 && !c.whole_run ? SIZE : 2 * i * SIZE); };
+    float m = -INFINITY;
+    for (int i = 0; i <= c.runs; ++i)
+        m = fmaxf(m, part(i)[ROWS * L + r]);
+    float4 o[4];
+    float l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = 0; i0 <= c.runs; i0 += U) {
+        float4 v[U][4];
+        float f[U], w[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (i0 + i <= c.runs) {
+                const float *p = part(i0 + i);
+                f[i] = p[ROWS * L + r];
+                w[i] = p[ROWS * L + ROWS + r];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[i][k] = reinterpret_cast<const float4 *>(p)[(d / 4 + k) * ROWS + r];
+            }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (i0 + i <= c.runs) {
+                const float x = f[i] == -INFINITY ? 1.0f : ex2(f[i] - m);  // a NaN sum stays
+                l += w[i] * x;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    o[k].x = fmaf(v[i][k].x, x, o[k].x);
+                    o[k].y = fmaf(v[i][k].y, x, o[k].y);
+                    o[k].z = fmaf(v[i][k].z, x, o[k].z);
+                    o[k].w = fmaf(v[i][k].w, x, o[k].w);
+                }
+            }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t *to = a.out + (c.first + rr / a.group) * a.o_tok + rr % a.group * a.o_head + d;
+#pragma unroll
+    for (int k = 0; k < 4; k += 2)
+        latent_put(to + 4 * k,
+                   make_uint4(pack_bf2(o[k].x * inv, o[k].y * inv), pack_bf2(o[k].z * inv, o[k].w * inv),
+                              pack_bf2(o[k + 1].x * inv, o[k + 1].y * inv), pack_bf2(o[k + 1].z * inv, o[k + 1].w * inv)),
+                   a.o_wide);
 }
 
 }  // namespace moe
