@@ -6,9 +6,9 @@
 #include <algorithm>
 #include <mutex>
 
-#include "moe_latent_attn.cuh"
 #include "moe_latent_tc.cuh"
 #include "moe_launch.cuh"
+#include "moe_prompt.cuh"
 
 using namespace moe;
 
@@ -129,6 +129,39 @@ int latent_maps(const moe_latent_cache *c, LatentArgs &a)
     if (!rc)
         rc = host_map_bf16(&a.ropes, static_cast<const char *>(c->pages) + 2 * c->latent_dim, 2, rope_dims, strides, ropes);
     return rc;
+}
+
+// ---- expanded attention
+
+#define MOE_PROMPT_SMALL 512  // bytes of shared memory beside the queries and the ring
+
+// rows [tokens, heads, dims] as a tensor map: boxes of `box` tokens of one head and 64 dimensions
+int prompt_map(CUtensorMap *m, const void *base, int64_t token_stride, int64_t head_stride, int tokens, int heads, int dims,
+               uint32_t box)
+{
+    const bool one = heads == 1 || head_stride == 0;
+    const uint64_t size[3] = {(uint64_t)dims, one ? 1ull : (uint64_t)heads, (uint64_t)tokens};
+    const uint64_t strides[2] = {one ? 16ull : 2 * (uint64_t)head_stride, tokens == 1 ? 16ull : 2 * (uint64_t)token_stride};
+    const uint32_t boxes[3] = {64, 1, box};
+    return host_map_bf16(m, base, 3, size, strides, boxes);
+}
+
+// shared memory of the kernel, asked for once a device
+int prompt_device()
+{
+    static bool done[MOE_LATENT_MAX_DEVICES];
+    int d = 0, optin = 0;
+    MOE_CUDA_OK(cudaGetDevice(&d));
+    if (d < 0 || d >= MOE_LATENT_MAX_DEVICES)
+        return host_fail(MOE_EUNSUPPORTED, "device ordinal %d", d);
+    std::lock_guard<std::mutex> lk(g_latent_mu);
+    if (!done[d]) {
+        MOE_CUDA_OK(cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, d));
+        MOE_CUDA_OK(cudaFuncSetAttribute(moe_prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
+        MOE_CUDA_OK(cudaFuncSetAttribute(moe_prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
+        done[d] = true;
+    }
+    return MOE_OK;
 }
 
 using RopeKernel = void (*)(RopeArgs);
@@ -450,6 +483,9 @@ int moe_latent_prompt_attention(const void *q_dev, int64_t q_token_stride, int64
     if ((nope_dim != 64 && nope_dim != 128) || rope_dim % 8 || rope_dim > 64 || heads > 1024 || batch > 1024)
         return host_fail(MOE_EUNSUPPORTED, "moe_latent_prompt_attention: nope_dim (%d) of 64 or 128, rope_dim (%d) a "
                          "multiple of 8 up to 64, heads (%d) and batch (%d) <= 1024", nope_dim, rope_dim, heads, batch);
+    if (q_tokens > 1 << 23 || kv_tokens > 1 << 30)
+        return host_fail(MOE_EUNSUPPORTED, "moe_latent_prompt_attention: q_tokens (%d) <= 2^23, kv_tokens (%d) <= 2^30", q_tokens,
+                         kv_tokens);
     if (!(scale >= -3.0e38f && scale <= 3.0e38f))
         return host_fail(MOE_EINVAL, "moe_latent_prompt_attention: scale must be finite");
     if (batch == 0 || q_tokens == 0)
@@ -463,17 +499,16 @@ int moe_latent_prompt_attention(const void *q_dev, int64_t q_token_stride, int64
         (k_token_stride | k_head_stride | kr_stride | v_token_stride | v_head_stride) % 8)
         return host_fail(MOE_EINVAL, "moe_latent_prompt_attention: k, kr and v must start on 16-byte boundaries and have "
                          "strides of multiples of 8");
+    if (kv_tokens > 1 && (k_token_stride < 1 || kr_stride < 1 || v_token_stride < 1))
+        return host_fail(MOE_EINVAL, "moe_latent_prompt_attention: k's, kr's and v's token strides must be positive");
+    if (heads > 1 && (k_head_stride < 0 || v_head_stride < 0))
+        return host_fail(MOE_EINVAL, "moe_latent_prompt_attention: k's and v's head strides must not be negative");
     PromptArgs a{};
     a.q = static_cast<const uint16_t *>(q_dev);
-    a.k = static_cast<const uint16_t *>(k_dev);
-    a.kr = static_cast<const uint16_t *>(kr_dev);
     a.v = static_cast<const uint16_t *>(v_dev);
     a.out = static_cast<uint16_t *>(out_dev);
     a.q_tok = q_token_stride;
     a.q_head = q_head_stride;
-    a.k_tok = k_token_stride;
-    a.k_head = k_head_stride;
-    a.kr_tok = kr_stride;
     a.v_tok = v_token_stride;
     a.v_head = v_head_stride;
     a.o_tok = out_token_stride;
@@ -481,15 +516,32 @@ int moe_latent_prompt_attention(const void *q_dev, int64_t q_token_stride, int64
     a.q_start = q_start_dev;
     a.kv_start = kv_start_dev;
     a.batch = batch;
-    a.heads = heads;
-    a.nope = nope_dim;
     a.rope = rope_dim;
     a.q_tokens = q_tokens;
     a.kv_tokens = kv_tokens;
     a.causal = causal;
+    a.q_wide = wide_rows(q_dev, q_token_stride, q_head_stride);
+    a.o_wide = wide_rows(out_dev, out_token_stride, out_head_stride);
+    a.one_k = heads == 1 || k_head_stride == 0;
+    a.one_v = heads == 1 || v_head_stride == 0;
     a.scale = scale;
     a.status = status_dev;
-    MOE_CUDA_OK(launch(moe_prompt_row_kernel, dim3((unsigned)q_tokens, (unsigned)heads), MOE_ROW_THREADS, 0, stream, a));
+    a.wait_ns = host_wait_ns();
+    int rc = MOE_OK;
+    if (kv_tokens > 0) {
+        const uint64_t dims[2] = {(uint64_t)rope_dim, (uint64_t)kv_tokens}, strides[1] = {kv_tokens == 1 ? 16ull : 2 * (uint64_t)kr_stride};
+        const uint32_t box[2] = {64, MOE_PROMPT_TOKENS};
+        if ((rc = prompt_map(&a.keys, k_dev, k_token_stride, k_head_stride, kv_tokens, heads, nope_dim, MOE_PROMPT_TOKENS)) ||
+            (rc = prompt_map(&a.values, v_dev, v_token_stride, v_head_stride, kv_tokens, heads, nope_dim,
+                             MOE_PROMPT_TOKENS / (nope_dim / 64))) ||
+            (rc = host_map_bf16(&a.ropes, kr_dev, 2, dims, strides, box)))
+            return rc;
+    }
+    if ((rc = prompt_device()))
+        return rc;
+    const size_t shared = (2 * (nope_dim / 64 + 1) + MOE_PROMPT_PLACES) * (size_t)MOE_PROMPT_PLACE + MOE_PROMPT_SMALL;
+    const dim3 grid((unsigned)heads, (unsigned)(q_tokens / MOE_PROMPT_ROWS + batch));
+    MOE_CUDA_OK(launch(nope_dim == 64 ? moe_prompt_kernel<64> : moe_prompt_kernel<128>, grid, MOE_PROMPT_THREADS, shared, stream, a));
     return MOE_OK;
 }
 

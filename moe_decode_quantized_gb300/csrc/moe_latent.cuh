@@ -46,6 +46,12 @@ __device__ __forceinline__ void latent_put(uint16_t *p, const uint4 &v, bool wid
     }
 }
 
+// bf16 values whose exponent is all ones (NaN, infinities) to 0
+__device__ __forceinline__ uint32_t finite_bf2(uint32_t w)
+{
+    return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
+}
+
 // the row of the token's slot; nullptr where there is none
 __device__ __forceinline__ uint16_t *latent_row(const LatentRows &a, int token)
 {

@@ -150,12 +150,6 @@ __device__ __forceinline__ uint64_t mn128_desc(const void *tile, uint32_t next)
     return ((addr >> 4) & 0x3FFFull) | ((uint64_t)(next >> 4) << 16) | ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// bit pairs whose exponent is all ones (NaN, infinities) to 0
-__device__ __forceinline__ uint32_t finite_bf2(uint32_t w)
-{
-    return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
-}
-
 template <int L>
 __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const __grid_constant__ LatentArgs a, const int stages)
 {
@@ -167,8 +161,8 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
     uint64_t *bars = reinterpret_cast<uint64_t *>(small);
     uint64_t *full = bars, *empty = bars + 8, *v_full = bars + 16, *s_full = bars + 24;  // [stages]
     uint64_t *p_full = bars + 32, *pv_done = bars + 34, *v_here = bars + 36;             // [2]
-    uint64_t *q_full = bars + 38, *o_free = bars + 39, *drained = bars + 40;             // drained [4]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 44);
+    uint64_t *q_full = bars + 38, *o_free = bars + 40, *drained = bars + 41;             // q_full [2], by items; drained [4]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 45);
     float *top_of = reinterpret_cast<float *>(small + 384);  // [2][2][64]
     uint32_t *gone = reinterpret_cast<uint32_t *>(top_of + 256);  // [16] 16-token groups of tile t that are not there, at t % 16
     long long *scan = reinterpret_cast<long long *>(gone + 16), *cum = scan + 32;  // cum [batch + 1]
@@ -190,8 +184,8 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             mbar_init(p_full + x, 2 * MOE_LTC_SOFT);
             mbar_init(pv_done + x, 1);
             mbar_init(v_here + x, 1);
+            mbar_init(q_full + x, 2 * MOE_LTC_SOFT);
         }
-        mbar_init(q_full, 2 * MOE_LTC_SOFT);
         mbar_init(o_free, 2 * MOE_LTC_SOFT);
         for (int i = 0; i < 4; ++i)
             mbar_init(drained + i, 1);
@@ -326,7 +320,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 to_item(u, it);
                 end = item_end(it);
                 ++item;
-                ok = ok && (scores ? all(wait(q_full, item)) : item == 0 || all(wait(o_free, item - 1)));
+                ok = ok && (scores ? all(wait(q_full + (item & 1), item >> 1)) : item == 0 || all(wait(o_free, item - 1)));
             }
             if (scores && x == (role != 0)) {
                 // S of tile u, in the place of the last but one, which has been read (and first that wait: then the tile
@@ -413,7 +407,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    arrive_first(q_full);
+                    arrive_first(q_full + (item & 1));
             }
             const int node = live ? at / t.group : 0;
             // the drafted tokens that it sees

@@ -1,0 +1,503 @@
+// moe_prompt.cuh -- latent attention in expanded form, for prompts, on the
+// 5th-generation tensor cores: a CTA takes 256 query rows of one head of a
+// sequence, in two M tiles of 128, over tiles of 128 tokens,
+//   S = [Q | QR] [K | KR]^T,   O += P V,   P = 2^(c (S - m)),
+// in one pass with a running reference m and sum of weights a row.
+//
+// S, P and O are in tensor memory, a row a lane, so that a row's maximum and sum
+// are one thread's; P (bf16) takes its S's place and is the second product's A
+// operand from there. One M tile's softmax passes under the other's products.
+// Keys and values come by TMA through a ring of eight 16 KB places: K (and the
+// part that all heads share) in chunks of 64 dimensions of 128 tokens, V in
+// chunks of 64 tokens of all dimensions, read with the dimensions contiguous.
+// One thread each issues S's and O's products.
+//
+// Tokens that not all rows see (of the causal edge, past the sequence's end) may
+// hold anything: their scores are taken out, their values that are not finite
+// are zeros in the product, and are added at the end to the rows that see them.
+#pragma once
+#include "moe_latent.cuh"
+#include "moe_tc.cuh"
+#include "moe_tree_attn.cuh"
+
+namespace moe {
+
+#define MOE_PROMPT_ROWS 256
+#define MOE_PROMPT_TOKENS 128
+#define MOE_PROMPT_SOFT 8   // softmax warps
+#define MOE_PROMPT_CLEAN 4  // warps that look through values
+#define MOE_PROMPT_THREADS ((MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN + 3) * 32)
+#define MOE_PROMPT_PLACE 16384
+#define MOE_PROMPT_PLACES 8
+#define MOE_PROMPT_SLACK 8.0f  // m moves when an exponent passes it by this
+
+struct PromptArgs {
+    const uint16_t *q, *v;
+    uint16_t *out;
+    long long q_tok, q_head, v_tok, v_head, o_tok, o_head;
+    const int32_t *q_start, *kv_start;
+    int batch, rope, q_tokens, kv_tokens, causal, q_wide, o_wide;
+    int one_k, one_v;  // heads share their keys (values)
+    float scale;
+    uint32_t *status;
+    unsigned long long wait_ns;
+    CUtensorMap keys, ropes, values;  // [D, heads, tokens], [rope, tokens], [D, heads, tokens]
+};
+
+__device__ uint32_t prompt_unasked;  // the status of calls that ask for none
+
+// tcgen05.mma by a whole warp, one lane of which issues it (see moe_latent_tc.cuh's)
+__device__ __forceinline__ void mma1_f16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xFFFFFFFF;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma1_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xFFFFFFFF;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma1_commit(uint64_t *bar)
+{
+    asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xFFFFFFFF;\n"
+                 " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+// block `at` of the call's row blocks, those of the sequences in order (of a sequence whose starts do not hold, of its
+// rows that lie in the call); q1 <= q0: there is no such block
+struct PromptBlock {
+    int q0, q1, row, k0, t, n;  // query rows [q0, q1) of the call, the first's place in the sequence; tokens [k0, k0 + t)
+    bool held;
+};
+
+// whether a sequence's starts hold
+__device__ __forceinline__ bool prompt_held(const PromptArgs &a, int b)
+{
+    const int q0 = a.q_start[b], q1 = a.q_start[b + 1], k0 = a.kv_start[b], k1 = a.kv_start[b + 1];
+    return q0 >= 0 && q1 >= q0 && q1 <= a.q_tokens && k0 >= 0 && k1 >= k0 && k1 <= a.kv_tokens;
+}
+
+// whole CTA: found [3] and scan [33] in shared memory
+__device__ __forceinline__ PromptBlock prompt_block(const PromptArgs &a, int at, int *scan, int *found, uint32_t *status)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = MOE_PROMPT_THREADS;
+    if (tid == 0)
+        found[0] = -1;
+    const int per = (a.batch + nt - 1) / nt;
+    auto rows = [&](int b, int &q0) {  // rows of a sequence that lie in the call
+        q0 = max(a.q_start[b], 0);
+        return max(min(a.q_start[b + 1], a.q_tokens) - q0, 0);
+    };
+    int mine = 0, q0;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b >= a.batch)
+            break;
+        mine += (rows(b, q0) + MOE_PROMPT_ROWS - 1) / MOE_PROMPT_ROWS;
+        if (blockIdx.x == 0 && blockIdx.y == 0 && !prompt_held(a, b))
+            atomicOr(status, (uint32_t)MOE_WS_INDEX);
+    }
+    int incl = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+        incl += lane >= m ? u : 0;
+    }
+    if (lane == 31)
+        scan[warp] = incl;
+    __syncthreads();
+    int before = incl - mine;
+    for (int w = 0; w < warp; ++w)
+        before += scan[w];
+    if (at >= before && at < before + mine)
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b >= a.batch)
+                break;
+            const int n = rows(b, q0), blocks = (n + MOE_PROMPT_ROWS - 1) / MOE_PROMPT_ROWS;
+            if (at < before + blocks) {
+                found[0] = b;
+                found[1] = q0 + (at - before) * MOE_PROMPT_ROWS;
+                found[2] = q0 + n;
+                break;
+            }
+            before += blocks;
+        }
+    __syncthreads();
+    PromptBlock r{};
+    const int b = found[0];
+    if (b < 0)
+        return r;
+    const int s0 = a.q_start[b], s1 = a.q_start[b + 1];
+    r.k0 = a.kv_start[b];
+    r.t = a.kv_start[b + 1] - r.k0;
+    r.n = s1 - s0;
+    r.q0 = found[1];
+    r.q1 = min(found[1] + MOE_PROMPT_ROWS, found[2]);
+    r.row = r.q0 - s0;
+    r.held = prompt_held(a, b);
+    return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const __grid_constant__ PromptArgs a)
+{
+    constexpr int KC = D / 64 + 1;   // places of a tile's K
+    constexpr int VC = D / 64;       // and of its V: VT tokens each
+    constexpr int VT = MOE_PROMPT_TOKENS / VC;
+    constexpr uint32_t S_COL = 0, O_COL = 256;  // of tensor memory: S (and P) of the M tiles, O of the two
+    constexpr int TOKENS = MOE_PROMPT_TOKENS, PLACE = MOE_PROMPT_PLACE, Q_TILE = KC * PLACE;
+    extern __shared__ __align__(1024) uint8_t smem_prompt[];
+    uint8_t *sq = smem_prompt, *ring = smem_prompt + 2 * Q_TILE, *small = ring + MOE_PROMPT_PLACES * PLACE;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(small);
+    uint64_t *k_full = bars, *v_full = bars + 2, *k_free = bars + 4, *v_free = bars + 6;  // [2], by tiles
+    uint64_t *s_full = bars + 8, *p_full = bars + 10, *pv_done = bars + 12;               // [2], by M tile
+    uint64_t *v_edge = bars + 14, *v_clean = bars + 17;  // [3] values of the tiles that are looked through: there, and fit
+    uint64_t *q_full = bars + 20, *drained = bars + 21;  // drained [2]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 23);
+    uint32_t *bad = tmem_slot + 1;  // [3][4] tokens of the tiles that are looked through with values that are not finite
+    int *scan = reinterpret_cast<int *>(bad + 12), *found = scan + 33;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.x;
+    uint32_t *status = a.status ? a.status : &prompt_unasked;
+
+    if (tid == 0) {
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(k_full + x, 1);
+            mbar_init(v_full + x, 1);
+            mbar_init(k_free + x, 1);
+            mbar_init(v_free + x, 1);
+            mbar_init(s_full + x, 1);
+            mbar_init(p_full + x, MOE_PROMPT_SOFT / 2);
+            mbar_init(pv_done + x, 1);
+            mbar_init(drained + x, 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(v_edge + i, 1);
+            mbar_init(v_clean + i, MOE_PROMPT_CLEAN);
+        }
+        mbar_init(q_full, MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN);
+        fence_barrier_init();
+    }
+    if (tid < 12)
+        bad[tid] = 0;
+    pdl_wait();  // before tensor memory is taken: the last kernel may still need it
+    // (the last blocks first: a sequence's later rows see more)
+    const PromptBlock b = prompt_block(a, gridDim.y - 1 - blockIdx.y, scan, found, status);
+    if (b.q1 <= b.q0)
+        return;
+    if (!b.held) {
+        for (int i = tid; i < (b.q1 - b.q0) * D; i += MOE_PROMPT_THREADS)
+            a.out[(b.q0 + i / D) * a.o_tok + head * a.o_head + i % D] = 0;
+        return;
+    }
+    if (warp == 0)
+        tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_launch_dependents();
+    const int rows = b.q1 - b.q0;
+    // tokens that row i of the block sees
+    auto sees = [&](int i) { return a.causal ? max(0, min(b.t, b.t - b.n + b.row + i + 1)) : b.t; };
+    // tiles of each M tile, and the first that not all rows see whole
+    const int tiles0 = (sees(min(rows, 128) - 1) + TOKENS - 1) / TOKENS, tiles1 = rows > 128 ? (sees(rows - 1) + TOKENS - 1) / TOKENS : 0;
+    const int tiles = max(tiles0, tiles1), edge = sees(0) / TOKENS;
+    auto wait = [&](uint64_t *bar, int phase) {
+        return tree_poll(bar, (uint32_t)phase & 1u) || tree_wait_on(bar, (uint32_t)phase & 1u, status, a.wait_ns);
+    };
+    auto drain = [&](uint64_t *bar, int phase) { tree_wait_on(bar, (uint32_t)phase & 1u, status, max(a.wait_ns, MOE_TREE_DRAIN_NS)); };
+    auto place = [&](int i) { return ring + (i & (MOE_PROMPT_PLACES - 1)) * PLACE; };
+
+    if (warp < MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN && tiles > 0) {
+        // ---------------- the queries
+        constexpr int PIECES = D / 8 + 8;
+        for (int i = tid; i < rows * PIECES; i += (MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN) * 32) {
+            const int r = i / PIECES, k = i % PIECES;
+            uint4 *at = reinterpret_cast<uint4 *>(sq + (r >> 7) * Q_TILE + (k >> 3) * PLACE + (r & 127) * 128 + (((k & 7) ^ (r & 7)) << 4));
+            const uint16_t *from = a.q + (long long)(b.q0 + r) * a.q_tok + head * a.q_head + k * 8;
+            if (k >= D / 8 + a.rope / 8)
+                *at = make_uint4(0, 0, 0, 0);
+            else if (a.q_wide)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(at)), "l"(from) : "memory");
+            else
+                *at = latent_get(from, false);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(q_full);
+    }
+
+    if (warp == MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN) {
+        // ---------------- the copies: K of tile u once V of tile u - 2 is done with, V of it once K of tile u - 1 is
+        if (lane == 0) {
+            bool ok = true;
+            int u = 0, half = 0;  // half: K of tile u has been asked for
+            for (; u < tiles; ++u) {
+                const int x = u & 1, at = u * (KC + VC), token = b.k0 + u * TOKENS;
+                half = 0;
+                ok = u < 2 || wait(v_free + x, (u >> 1) - 1);
+                if (!ok)
+                    break;
+                mbar_arrive_expect_tx(k_full + x, KC * PLACE);
+#pragma unroll
+                for (int d = 0; d < D / 64; ++d)
+                    tma_load_3d(place(at + d), &a.keys, d * 64, a.one_k ? 0 : head, token, k_full + x);
+                tma_load_2d(place(at + D / 64), &a.ropes, 0, token, k_full + x);
+                half = 1;
+                ok = u < 1 || wait(k_free + (x ^ 1), (u - 1) >> 1);
+                if (!ok)
+                    break;
+                uint64_t *v_bar = u < edge ? v_full + x : v_edge + (u - edge);
+                mbar_arrive_expect_tx(v_bar, VC * PLACE);
+#pragma unroll
+                for (int i = 0; i < VC; ++i)
+#pragma unroll
+                    for (int d = 0; d < D / 64; ++d)
+                        tma_load_3d(place(at + KC + i) + d * VT * 128, &a.values, d * 64, a.one_v ? 0 : head, token + i * VT, v_bar);
+            }
+            // nothing in flight when the CTA ends
+            for (int k = max(0, u - 2); k < u; ++k) {
+                drain(k_full + (k & 1), k >> 1);
+                drain(k < edge ? v_full + (k & 1) : v_edge + (k - edge), k < edge ? k >> 1 : 0);
+            }
+            if (!ok && half)
+                drain(k_full + (u & 1), u >> 1);
+        }
+    } else if (warp > MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN) {
+        // ---------------- the products: a warp S's, one O's
+        const bool scores = warp == MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN + 1;
+        constexpr uint32_t id_s = mma_idesc(128, TOKENS, true), id_o = mma_idesc(128, D, true) | (1u << 16);
+        const uint32_t tm = __reduce_max_sync(0xFFFFFFFFu, tmem);  // (what the loops need is the same in all lanes)
+        const int n = __reduce_max_sync(0xFFFFFFFFu, tiles), n0 = __reduce_max_sync(0xFFFFFFFFu, tiles0),
+                  n1 = __reduce_max_sync(0xFFFFFFFFu, tiles1), e = __reduce_max_sync(0xFFFFFFFFu, edge);
+        const uint64_t qd = sw128_desc(sq), kd = sw128_desc(ring);
+        // V: rows (one a token) of 64 dimensions, 8 rows 1024 bytes apart, the next 64 dimensions VT rows
+        const uint64_t vd = kd & ~(0x3FFFull << 16) | (uint64_t)(VT * 128 / 16) << 16;
+        auto all = [&](bool v) { return __all_sync(0xFFFFFFFFu, v) != 0; };
+        auto off = [&](int i) { return (uint32_t)((i & (MOE_PROMPT_PLACES - 1)) * PLACE) / 16; };
+        bool ok = n == 0 || !scores || all(wait(q_full, 0));
+        for (int u = 0; u < n && ok; ++u) {
+            const int x = u & 1, at = u * (KC + VC);
+            if (scores) {
+                ok = all(wait(k_full + x, u >> 1));
+#pragma unroll 1
+                for (int g = 0; g < 2; ++g) {
+                    if (u >= (g ? n1 : n0) || !ok)
+                        continue;
+                    ok = u == 0 || all(wait(pv_done + g, u - 1));  // P, in S's place, has been read
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int d = 0; d < KC; ++d)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma1_f16(tm + S_COL + g * 128, qd + (uint32_t)(g * Q_TILE + d * PLACE + k * 32) / 16,
+                                     kd + off(at + d) + k * 2, id_s, d + k > 0);
+                    mma1_commit(s_full + g);
+                }
+                mma1_commit(k_free + x);
+            } else {
+                ok = all(u < e ? wait(v_full + x, u >> 1) : wait(v_clean + (u - e), 0));
+#pragma unroll 1
+                for (int g = 0; g < 2; ++g) {
+                    if (u >= (g ? n1 : n0) || !ok)
+                        continue;
+                    ok = all(wait(p_full + g, u));
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)  // 16 tokens: 8 columns of P, 2048 bytes of V
+                        mma1_f16_ts(tm + O_COL + g * 128, tm + S_COL + g * 128 + k * 8,
+                                    vd + off(at + KC + k * 16 / VT) + (uint32_t)(k * 16 % VT * 128) / 16, id_o, u > 0 || k > 0);
+                    mma1_commit(pv_done + g);
+                }
+                mma1_commit(v_free + x);
+            }
+        }
+        if (n > 0) {  // what has been issued ends before tensor and shared memory are given back
+            mma1_commit(drained + scores);
+            drain(drained + scores, 0);
+        }
+    } else if (warp >= MOE_PROMPT_SOFT) {
+        // ---------------- values of tiles that not all rows see: those past the end zeros, those that are not finite
+        // zeros and noted
+        bool ok = true;
+        for (int u = edge; u < tiles; ++u) {
+            ok = ok && wait(v_edge + (u - edge), 0);
+            __syncwarp();
+            const int at = u * (KC + VC) + KC;
+            for (int i = tid - MOE_PROMPT_SOFT * 32; i < TOKENS * D / 8; i += MOE_PROMPT_CLEAN * 32) {
+                const int token = i / (D / 8), piece = i % (D / 8);
+                uint4 *p = reinterpret_cast<uint4 *>(place(at + token / VT) + (piece >> 3) * VT * 128 + token % VT * 128 + (piece & 7) * 16);
+                if (u * TOKENS + token >= b.t) {
+                    *p = make_uint4(0, 0, 0, 0);
+                    continue;
+                }
+                const uint4 v = *p, w = make_uint4(finite_bf2(v.x), finite_bf2(v.y), finite_bf2(v.z), finite_bf2(v.w));
+                if (v.x != w.x || v.y != w.y || v.z != w.z || v.w != w.w) {
+                    *p = w;
+                    atomicOr(bad + (u - edge) * 4 + (token >> 5), 1u << (token & 31));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(v_clean + (u - edge));
+        }
+    } else {
+        // ---------------- softmax: M tile g, row `row` of it
+        const int g = warp >> 2, row = (warp & 3) * 32 + lane, mine = g * 128 + row, n = g ? tiles1 : tiles0;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_at = lanes + S_COL + g * 128, o_at = lanes + O_COL + g * 128;
+        const bool live = mine < rows;
+        const int most = live ? sees(mine) : 0;
+        const float scaled = fminf(fabsf(a.scale) * 1.4426950408889634f, 3.0e38f);
+        const bool flat = scaled == 0.0f;  // all scores alike
+        const float c = flat ? 1.0f : scaled, turn = flat ? 0.0f : a.scale < 0.0f ? -1.0f : 1.0f;
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int u = 0; u < n; ++u) {
+            ok = ok && wait(s_full + g, u);
+            __syncwarp();
+            tc_fence_after();
+            if (u >= edge || turn != 1.0f) {  // the scores of tokens that are not seen to -inf, so that the passes below stay short
+                const int vis = most - u * TOKENS;
+#pragma unroll 1
+                for (int k = 0; k < TOKENS; k += 16) {
+                    float v[16];
+                    uint32_t w[16];
+                    tmem_ld16(s_at + k, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[i] = k + i < vis ? __float_as_uint(v[i] * turn) : 0xFF800000u;
+                    tmem_st16(s_at + k, w);
+                    tmem_st_wait();
+                }
+            }
+            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int k = 0; k < TOKENS; k += 64) {
+                uint32_t s[2][32];
+                tmem_ld32_begin(s_at + k, s[0]);
+                tmem_ld32_begin(s_at + k + 32, s[1]);
+                tmem_ld32_end(s[0]);
+                tmem_ld32_end(s[1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        top4[i >> 1 & 3] = max3(top4[i >> 1 & 3], __uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1]));
+            }
+            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+            const bool moves = (top - m) * c > MOE_PROMPT_SLACK;
+            if (__any_sync(0xFFFFFFFFu, moves)) {
+                const float f = moves ? ex2((m - top) * c) : 1.0f;
+                m = moves ? top : m;
+                l *= f;
+                if (u > 0)  // S is there, so the last tile's O is too
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 16) {
+                        float o[16];
+                        uint32_t w[16];
+                        tmem_ld16(o_at + k, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = __float_as_uint(o[i] * f);
+                        tmem_st16(o_at + k, w);
+                    }
+            }
+            const float ref = m == -INFINITY ? 0.0f : -m;
+            const F2 ref2(ref, ref), c2(c, c);
+            F2 sum(0.0f, 0.0f), sum1(0.0f, 0.0f);
+#pragma unroll 1
+            for (int k = 0; k < TOKENS; k += 64) {
+                uint32_t s[2][32];
+                tmem_ld32_begin(s_at + k, s[0]);
+                tmem_ld32_begin(s_at + k + 32, s[1]);
+                tmem_ld32_end(s[0]);
+                tmem_ld32_end(s[1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float e0, e1;
+                        mul2(add2(F2(__uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1])), ref2), c2).get(e0, e1);
+                        const uint32_t p = pack_bf2(ex2(e0), ex2(e1));
+                        F2 &to = i & 2 ? sum1 : sum;
+                        to = add2(to, F2(bf16_lo(p), bf16_hi(p)));  // as rounded
+                        w[i / 2] = p;
+                    }
+                    tmem_st16(s_at + k / 2 + 16 * h, w);  // P over the columns that have been read
+                }
+            }
+            sum = add2(sum, sum1);
+            float l0, l1;
+            sum.get(l0, l1);
+            l += l0 + l1;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(p_full + g);
+        }
+        // ---- the end
+        if (n > 0)
+            ok = ok && wait(pv_done + g, n - 1);
+        __syncwarp();
+        tc_fence_after();
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t *to = a.out + (long long)(b.q0 + mine) * a.o_tok + head * a.o_head;
+#pragma unroll 1
+        for (int k = 0; k < D && mine - lane < rows; k += 16) {
+            float o[16];
+            if (n > 0) {
+                tmem_ld16(o_at + k, o);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[i] = 0.0f;
+            }
+#pragma unroll 1
+            for (int w = 0; w < 12; ++w)  // values that are not finite, of tokens that the row sees
+                for (uint32_t set = *reinterpret_cast<volatile uint32_t *>(bad + w); set; set &= set - 1) {
+                    const int token = (edge + w / 4) * TOKENS + (w & 3) * 32 + __ffs(set) - 1;
+                    if (token >= most)
+                        continue;
+                    const uint16_t *v = a.v + (long long)(b.k0 + token) * a.v_tok + head * a.v_head + k;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if ((v[i] & 0x7F80u) == 0x7F80u)
+                            o[i] += bf16_to_f32(v[i]);
+                }
+            if (!live)
+                continue;
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2)
+                w[i / 2] = pack_bf2(o[i] * inv, o[i + 1] * inv);
+            latent_put(to + k, make_uint4(w[0], w[1], w[2], w[3]), a.o_wide);
+            latent_put(to + k + 8, make_uint4(w[4], w[5], w[6], w[7]), a.o_wide);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0)
+        tmem_dealloc(tmem, 512);
+}
+
+}  // namespace moe
