@@ -461,6 +461,8 @@ class _Runtime:
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         device, current = torch.cuda.current_device, torch.cuda.current_stream
         self.stream = (lambda: raw(device())) if raw is not None else (lambda: current().cuda_stream)
+        self.raw = raw if raw is not None else (lambda d: current().cuda_stream)
+        self.device = getattr(torch._C, "_cuda_getDevice", device)
 
 
 def _runtime():
@@ -682,16 +684,25 @@ def spec_verify(logits, q_start, tokens, parents, draft, temperature, uniforms, 
 
 
 def _on_gpu(**tensors):
-    """Refuses the first tensor that is on the host, or on another GPU than the first of them."""
-    device = None
+    """Refuses the first tensor that is on the host, or on another GPU than the current one."""
+    import torch
     for name, t in tensors.items():
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be on the GPU, not on {t.device}")
-        if device is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the arguments before it on {device}")
-        device = t.device
+        if t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, which is not the current device")
+
+
+def _here(rt, stream, d):
+    """The stream's handle; whether device d (a tensor's get_device, -1 on the host) is the current one."""
+    if d < 0:
+        return 0, False
+    now = rt.device()
+    if stream is None:
+        return rt.raw(now), d == now
+    return (stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)), d == now
 
 
 def _rows3(t, name, kinds, heads, dim):
@@ -711,16 +722,18 @@ def _rows2(t, name, kinds, rows, dim):
     """Address and row stride of rows [at least `rows`, dim] with contiguous dimensions."""
     if t.dtype not in kinds:
         raise ValueError(f"{name} must be {kinds[0]}, not {t.dtype}")
-    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != dim:
-        raise ValueError(f"{name} must be [{rows}, {dim}], not {list(t.shape)}")
-    if t.stride(1) != 1 and dim > 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < rows or shape[1] != dim:
+        raise ValueError(f"{name} must be [{rows}, {dim}], not {list(shape)}")
+    sr, sd = t.stride()
+    if sd != 1 and dim > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), sr
 
 
 def _distinct(t, name):
     """Refuses an output whose rows share memory (an expanded tensor)."""
-    if any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
+    if 0 in t.stride() and any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
         raise ValueError(f"{name} is an output: its rows must not share memory")
 
 
@@ -740,21 +753,36 @@ def rope(x, out, positions, table, offset: int = 0, layout: int = MOE_ROPE_HALF,
     """Rotary positions on dimensions offset .. offset + 2 * table.numel() - 1 of each head (include/moe.h, moe_rope):
     x, out bf16 or f32 [tokens, heads, head_dim], any strides of the first two (out may be x), positions int32
     [tokens], table int64 (rope_table's). transposed: turned back, as a gradient is."""
-    rt = _runtime()
+    rt = _rt or _runtime()
     kind = x.dtype
-    if kind is not rt.bf16 and kind is not rt.f32:
+    if kind is rt.bf16:
+        code = MOE_BF16
+    elif kind is rt.f32:
+        code = MOE_F32
+    else:
         raise ValueError(f"x must be bfloat16 or float32, not {kind}")
-    if x.dim() != 3 or out.shape != x.shape:
+    shape = x.shape
+    if len(shape) != 3 or out.shape != shape:
         raise ValueError(f"x and out must both be [tokens, heads, head_dim], not {list(x.shape)} and {list(out.shape)}")
-    tokens, heads, dim = x.shape
-    if table.dtype not in rt.bits:
-        raise ValueError(f"table must be int64, not {table.dtype}")
-    _distinct(out, "out")
-    args = (*_rows3(x, "x", (kind,), heads, dim), *_rows3(out, "out", (kind,), heads, dim),
-            MOE_F32 if kind is rt.f32 else MOE_BF16, tokens, heads, dim, offset, 2 * table.numel(), layout,
-            _dev(positions, "positions", rt.i32, tokens), _dev(table, "table", table.dtype, 1), magnitude, int(transposed),
-            _on(rt, stream))
-    _on_gpu(x=x, out=out, positions=positions, table=table)
+    if out.dtype is not kind:
+        raise ValueError(f"out must be {kind}, not {out.dtype}")
+    tokens, heads, dim = shape
+    bits = table.dtype
+    if bits not in rt.bits:
+        raise ValueError(f"table must be int64, not {bits}")
+    xt, xh, xd = x.stride()
+    ot, oh, od = out.stride()
+    if (xd != 1 or od != 1) and dim > 1:
+        raise ValueError("the last dimension of x and out must be contiguous")
+    if ot == 0 or oh == 0:
+        _distinct(out, "out")
+    pairs = table.numel()
+    d = x.get_device()
+    on, here = _here(rt, stream, d)
+    args = (x.data_ptr(), xt, xh, out.data_ptr(), ot, oh, code, tokens, heads, dim, offset, 2 * pairs, layout,
+            _dev(positions, "positions", rt.i32, tokens), _dev(table, "table", bits, 1), magnitude, 1 if transposed else 0, on)
+    if not (here and out.get_device() == d and positions.get_device() == d and table.get_device() == d):
+        _on_gpu(x=x, out=out, positions=positions, table=table)
     rc = rt.lib.moe_rope(*args)
     if rc:
         _check(rc)
@@ -814,11 +842,16 @@ def latent_append(cache: LatentCache, c, k_rope, slots, positions=None, table=No
         raise ValueError("c and k_rope must have the same number of tokens")
     if table is not None and (table.dtype not in rt.bits or 2 * table.numel() != cache.rope_dim):
         raise ValueError(f"table must be int64 of {cache.rope_dim // 2} values, not {table.dtype} of {table.numel()}")
+    d = c.get_device()
+    on, here = _here(rt, stream, d)
     args = (cache.ref(), *_rows2(c, "c", rt.rows, n, cache.latent_dim),
             *_rows2(k_rope, "k_rope", rt.rows, n, cache.rope_dim), _dev(slots, "slots", rt.i32, n), n,
             _dev(positions, "positions", rt.i32, n), None if table is None else _dev(table, "table", table.dtype, 1),
-            layout, magnitude, _dev(status, "status", rt.i32, 1), _on(rt, stream))
-    _on_gpu(pages=cache.pages, c=c, k_rope=k_rope, slots=slots, positions=positions, table=table, status=status)
+            layout, magnitude, _dev(status, "status", rt.i32, 1), on)
+    if not (here and cache.pages.get_device() == d and k_rope.get_device() == d and slots.get_device() == d and
+            (positions is None or positions.get_device() == d) and (table is None or table.get_device() == d) and
+            (status is None or status.get_device() == d)):
+        _on_gpu(pages=cache.pages, c=c, k_rope=k_rope, slots=slots, positions=positions, table=table, status=status)
     rc = rt.lib.moe_latent_append(*args)
     if rc:
         _check(rc)
@@ -830,10 +863,13 @@ def latent_read(cache: LatentCache, slots, c_out, k_rope_out, status=None, strea
     n = slots.numel()
     for t, name in ((c_out, "c_out"), (k_rope_out, "k_rope_out")):
         _distinct(t, name)
+    d = c_out.get_device()
+    on, here = _here(rt, stream, d)
     args = (cache.ref(), _dev(slots, "slots", rt.i32, n), n, *_rows2(c_out, "c_out", rt.rows, n, cache.latent_dim),
-            *_rows2(k_rope_out, "k_rope_out", rt.rows, n, cache.rope_dim), _dev(status, "status", rt.i32, 1),
-            _on(rt, stream))
-    _on_gpu(pages=cache.pages, slots=slots, c_out=c_out, k_rope_out=k_rope_out, status=status)
+            *_rows2(k_rope_out, "k_rope_out", rt.rows, n, cache.rope_dim), _dev(status, "status", rt.i32, 1), on)
+    if not (here and cache.pages.get_device() == d and k_rope_out.get_device() == d and slots.get_device() == d and
+            (status is None or status.get_device() == d)):
+        _on_gpu(pages=cache.pages, slots=slots, c_out=c_out, k_rope_out=k_rope_out, status=status)
     rc = rt.lib.moe_latent_read(*args)
     if rc:
         _check(rc)
@@ -859,12 +895,18 @@ def latent_attention(cache: LatentCache, q, q_rope, out, q_start, kv_len, table,
         raise ValueError(f"mask must be int64, not {mask.dtype}")
     _distinct(out, "out")
     tp, ts = _matrix(table, "table", rt.i32, batch, table.shape[-1])
+    d = q.get_device()
+    on, here = _here(rt, stream, d)
     args = (cache.ref(), *_rows3(q, "q", rt.rows, heads, cache.latent_dim),
             *_rows3(q_rope, "q_rope", rt.rows, heads, cache.rope_dim), *_rows3(out, "out", rt.rows, heads, cache.latent_dim),
             heads, _dev(q_start, "q_start", rt.i32, batch + 1), _dev(kv_len, "kv_len", rt.i32, batch), tp, ts,
             table.shape[1], None if mask is None else _dev(mask, "mask", mask.dtype, n), batch, n, scale,
-            *_bytes(ws), _on(rt, stream))
-    _on_gpu(pages=cache.pages, q=q, q_rope=q_rope, out=out, q_start=q_start, kv_len=kv_len, table=table, mask=mask, ws=ws)
+            *_bytes(ws), on)
+    if not (here and cache.pages.get_device() == d and q_rope.get_device() == d and out.get_device() == d and
+            q_start.get_device() == d and kv_len.get_device() == d and table.get_device() == d and ws.get_device() == d and
+            (mask is None or mask.get_device() == d)):
+        _on_gpu(pages=cache.pages, q=q, q_rope=q_rope, out=out, q_start=q_start, kv_len=kv_len, table=table,
+                mask=mask, ws=ws)
     rc = rt.lib.moe_latent_attention(*args)
     if rc:
         _check(rc)
@@ -884,12 +926,16 @@ def latent_prompt_attention(q, k, k_rope, v, out, q_start, kv_start, causal: boo
         raise ValueError("out must have q's number of tokens")
     batch = q_start.numel() - 1
     _distinct(out, "out")
+    d = q.get_device()
+    on, here = _here(rt, stream, d)
     args = (*_rows3(q, "q", rt.rows, heads, nope + rope_dim), *_rows3(k, "k", rt.rows, heads, nope),
             *_rows2(k_rope, "k_rope", rt.rows, t, rope_dim), *_rows3(v, "v", rt.rows, heads, nope),
             *_rows3(out, "out", rt.rows, heads, nope), heads, nope, rope_dim,
             _dev(q_start, "q_start", rt.i32, max(batch + 1, 1)), _dev(kv_start, "kv_start", rt.i32, max(batch + 1, 1)),
-            max(batch, 0), n, t, int(bool(causal)), scale, _dev(status, "status", rt.i32, 1), _on(rt, stream))
-    _on_gpu(q=q, k=k, k_rope=k_rope, v=v, out=out, q_start=q_start, kv_start=kv_start, status=status)
+            max(batch, 0), n, t, int(bool(causal)), scale, _dev(status, "status", rt.i32, 1), on)
+    if not (here and k.get_device() == d and k_rope.get_device() == d and v.get_device() == d and out.get_device() == d and
+            q_start.get_device() == d and kv_start.get_device() == d and (status is None or status.get_device() == d)):
+        _on_gpu(q=q, k=k, k_rope=k_rope, v=v, out=out, q_start=q_start, kv_start=kv_start, status=status)
     rc = rt.lib.moe_latent_prompt_attention(*args)
     if rc:
         _check(rc)
@@ -901,28 +947,44 @@ class PagePool:
     refs: object
     page_size: int = 64
 
-    def c(self) -> _lib.MoePagePool:
-        if self.refs.dtype is not _runtime().i32:
-            raise ValueError(f"refs must be int32, not {self.refs.dtype}")
-        return _lib.MoePagePool(_ptr(self.refs), self.refs.numel(), self.page_size)
+    def ref(self):
+        """The C struct by reference, made again after a field was set or the refs tensor got other memory."""
+        refs = self.refs
+        at = (refs.data_ptr(), refs.numel(), self.page_size)
+        kept = self.__dict__.get("_kept")
+        if kept is None or kept[0] != at:
+            if refs.dtype is not _runtime().i32:
+                raise ValueError(f"refs must be int32, not {refs.dtype}")
+            kept = self.__dict__["_kept"] = (at, C.byref(_lib.MoePagePool(_ptr(refs), at[1], at[2])))
+        return kept[1]
 
 
 def _pool_table(rt, pool, table, name="table"):
-    if table.dim() != 2:
-        raise ValueError(f"{name} must be [rows, pages], not {list(table.shape)}")
-    rows, pages = table.shape
-    _distinct(table, name)
-    p, stride = _matrix(table, name, rt.i32, rows, pages)
-    return C.byref(pool.c()), p, stride, pages, rows
+    """The pool; address, row stride, entries a row and rows of a table."""
+    if table.dtype is not rt.i32:
+        raise ValueError(f"{name} must be int32, not {table.dtype}")
+    shape = table.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be [rows, pages], not {list(shape)}")
+    sr, se = table.stride()
+    if se != 1 and shape[1] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if sr == 0:
+        _distinct(table, name)
+    return pool.ref(), table.data_ptr(), sr, shape[1], shape[0]
 
 
 def pages_grow(pool: PagePool, table, lengths, status=None, stream=None):
     """Give each row of the table (int32 [rows, pages], -1: none) the pages that lengths (int32 [rows]) tokens need
     (include/moe.h, moe_pages_grow)."""
-    rt = _runtime()
-    args = (*_pool_table(rt, pool, table), _dev(lengths, "lengths", rt.i32, table.shape[0]),
-            _dev(status, "status", rt.i32, 1), _on(rt, stream))
-    _on_gpu(refs=pool.refs, table=table, lengths=lengths, status=status)
+    rt = _rt or _runtime()
+    head = _pool_table(rt, pool, table)
+    d = table.get_device()
+    on, here = _here(rt, stream, d)
+    args = (*head, _dev(lengths, "lengths", rt.i32, head[4]), _dev(status, "status", rt.i32, 1), on)
+    if not (here and pool.refs.get_device() == d and lengths.get_device() == d and
+            (status is None or status.get_device() == d)):
+        _on_gpu(refs=pool.refs, table=table, lengths=lengths, status=status)
     rc = rt.lib.moe_pages_grow(*args)
     if rc:
         _check(rc)
@@ -931,12 +993,17 @@ def pages_grow(pool: PagePool, table, lengths, status=None, stream=None):
 def pages_fork(pool: PagePool, table, kv_len, source, target, copies, status=None, stream=None):
     """Row target[i] of the table becomes a fork of row source[i] (include/moe.h, moe_pages_fork): full pages shared, a
     part-filled last one to be copied as copies [n, 2] (int32) says (pages_copy). kv_len int32 [rows]."""
-    rt = _runtime()
+    rt = _rt or _runtime()
     n = source.numel()
-    args = (*_pool_table(rt, pool, table), _dev(kv_len, "kv_len", rt.i32, table.shape[0]),
-            _dev(source, "source", rt.i32, n), _dev(target, "target", rt.i32, n), n,
-            _dev(copies, "copies", rt.i32, 2 * n), _dev(status, "status", rt.i32, 1), _on(rt, stream))
-    _on_gpu(refs=pool.refs, table=table, kv_len=kv_len, source=source, target=target, copies=copies, status=status)
+    head = _pool_table(rt, pool, table)
+    d = table.get_device()
+    on, here = _here(rt, stream, d)
+    args = (*head, _dev(kv_len, "kv_len", rt.i32, head[4]), _dev(source, "source", rt.i32, n),
+            _dev(target, "target", rt.i32, n), n, _dev(copies, "copies", rt.i32, 2 * n), _dev(status, "status", rt.i32, 1), on)
+    if not (here and pool.refs.get_device() == d and kv_len.get_device() == d and source.get_device() == d and
+            target.get_device() == d and copies.get_device() == d and (status is None or status.get_device() == d)):
+        _on_gpu(refs=pool.refs, table=table, kv_len=kv_len, source=source, target=target, copies=copies,
+                status=status)
     rc = rt.lib.moe_pages_fork(*args)
     if rc:
         _check(rc)
@@ -944,10 +1011,12 @@ def pages_fork(pool: PagePool, table, kv_len, source, target, copies, status=Non
 
 def pages_free(pool: PagePool, table, rows, status=None, stream=None):
     """Give back the pages of the table's rows `rows` (int32); their entries become -1."""
-    rt = _runtime()
-    args = (*_pool_table(rt, pool, table), _dev(rows, "rows", rt.i32, 0), rows.numel(),
-            _dev(status, "status", rt.i32, 1), _on(rt, stream))
-    _on_gpu(refs=pool.refs, table=table, rows=rows, status=status)
+    rt = _rt or _runtime()
+    d = table.get_device()
+    on, here = _here(rt, stream, d)
+    args = (*_pool_table(rt, pool, table), _dev(rows, "rows", rt.i32, 0), rows.numel(), _dev(status, "status", rt.i32, 1), on)
+    if not (here and pool.refs.get_device() == d and rows.get_device() == d and (status is None or status.get_device() == d)):
+        _on_gpu(refs=pool.refs, table=table, rows=rows, status=status)
     rc = rt.lib.moe_pages_free(*args)
     if rc:
         _check(rc)
@@ -974,18 +1043,27 @@ def pages_compact(pool: PagePool, table, refs_out, table_out, copies, n_copies, 
 def pages_copy(pages, copies, n_copies=None, status=None, stream=None):
     """Copy pages as copies [n, 2] (int32: from, to) says, n_copies [1] of them where it is given, in every layer of
     pages [layers, n_pages, ...] (each layer contiguous; include/moe.h, moe_pages_copy)."""
-    rt = _runtime()
-    if pages.dim() < 3:
+    rt = _rt or _runtime()
+    shape, strides = pages.shape, pages.stride()
+    if len(shape) < 3:
         raise ValueError(f"pages must be [layers, n_pages, ...], not {list(pages.shape)}")
-    layers, n_pages = pages.shape[:2]
-    size = pages.element_size()
-    if layers and not pages[0].is_contiguous():
+    layers, n_pages = shape[:2]
+    per = 1
+    for n, st in zip(reversed(shape[2:]), reversed(strides[2:])):
+        if n != 1 and st != per:
+            raise ValueError("each layer of pages must be contiguous")
+        per *= n
+    if n_pages > 1 and strides[1] != per:
         raise ValueError("each layer of pages must be contiguous")
-    _distinct(pages, "pages")
-    per = pages[0, 0].numel() * size if layers and n_pages else 0
-    args = (pages.data_ptr(), pages.stride(0) * size, layers, n_pages, per, _dev(copies, "copies", rt.i32, 0),
-            copies.numel() // 2, _dev(n_copies, "n_copies", rt.i32, 1), _dev(status, "status", rt.i32, 1), _on(rt, stream))
-    _on_gpu(pages=pages, copies=copies, n_copies=n_copies, status=status)
+    if strides[0] == 0 and layers > 1:
+        raise ValueError("pages is an output: its layers must not share memory")
+    size, d = pages.element_size(), pages.get_device()
+    on, here = _here(rt, stream, d)
+    args = (pages.data_ptr(), strides[0] * size, layers, n_pages, per * size, _dev(copies, "copies", rt.i32, 0),
+            copies.numel() // 2, _dev(n_copies, "n_copies", rt.i32, 1), _dev(status, "status", rt.i32, 1), on)
+    if not (here and copies.get_device() == d and (n_copies is None or n_copies.get_device() == d) and
+            (status is None or status.get_device() == d)):
+        _on_gpu(pages=pages, copies=copies, n_copies=n_copies, status=status)
     rc = rt.lib.moe_pages_copy(*args)
     if rc:
         _check(rc)
