@@ -520,8 +520,11 @@ int moe_latent_prompt_attention(const void *q_dev, int64_t q_token_stride, int64
     a.q_tokens = q_tokens;
     a.kv_tokens = kv_tokens;
     a.causal = causal;
-    a.q_wide = wide_rows(q_dev, q_token_stride, q_head_stride);
-    a.o_wide = wide_rows(out_dev, out_token_stride, out_head_stride);
+    // (TMA takes the queries where it can)
+    a.q_wide = wide_rows(q_dev, q_token_stride, q_head_stride) && (q_tokens == 1 || q_token_stride > 0) &&
+               (heads == 1 || q_head_stride > 0);
+    a.o_wide = !wide_rows(out_dev, out_token_stride, out_head_stride) ? 0
+               : aligned(out_dev, 32) && (out_token_stride | out_head_stride) % 16 == 0 ? 2 : 1;
     a.one_k = heads == 1 || k_head_stride == 0;
     a.one_v = heads == 1 || v_head_stride == 0;
     a.scale = scale;
@@ -537,6 +540,8 @@ int moe_latent_prompt_attention(const void *q_dev, int64_t q_token_stride, int64
             (rc = host_map_bf16(&a.ropes, kr_dev, 2, dims, strides, box)))
             return rc;
     }
+    if (a.q_wide && (rc = prompt_map(&a.queries, q_dev, q_token_stride, q_head_stride, q_tokens, heads, nope_dim + rope_dim, 128)))
+        return rc;
     if ((rc = prompt_device()))
         return rc;
     const size_t shared = (2 * (nope_dim / 64 + 1) + MOE_PROMPT_PLACES) * (size_t)MOE_PROMPT_PLACE + MOE_PROMPT_SMALL;

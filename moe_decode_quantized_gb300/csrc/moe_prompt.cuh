@@ -10,7 +10,6 @@
 // Keys and values come by TMA through a ring of eight 16 KB places: K (and the
 // part that all heads share) in chunks of 64 dimensions of 128 tokens, V in
 // chunks of 64 tokens of all dimensions, read with the dimensions contiguous.
-// One thread each issues S's and O's products.
 //
 // Tokens that not all rows see (of the causal edge, past the sequence's end) may
 // hold anything: their scores are taken out, their values that are not finite
@@ -25,8 +24,7 @@ namespace moe {
 #define MOE_PROMPT_ROWS 256
 #define MOE_PROMPT_TOKENS 128
 #define MOE_PROMPT_SOFT 8   // softmax warps
-#define MOE_PROMPT_CLEAN 4  // warps that look through values
-#define MOE_PROMPT_THREADS ((MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN + 3) * 32)
+#define MOE_PROMPT_THREADS ((MOE_PROMPT_SOFT + 2) * 32)
 #define MOE_PROMPT_PLACE 16384
 #define MOE_PROMPT_PLACES 8
 #define MOE_PROMPT_SLACK 8.0f  // m moves when an exponent passes it by this
@@ -41,7 +39,7 @@ struct PromptArgs {
     float scale;
     uint32_t *status;
     unsigned long long wait_ns;
-    CUtensorMap keys, ropes, values;  // [D, heads, tokens], [rope, tokens], [D, heads, tokens]
+    CUtensorMap queries, keys, ropes, values;  // [D + rope, heads, rows], [D, heads, tokens], [rope, tokens], [D, heads, tokens]
 };
 
 __device__ uint32_t prompt_unasked;  // the status of calls that ask for none
@@ -148,6 +146,31 @@ __device__ __forceinline__ PromptBlock prompt_block(const PromptArgs &a, int at,
     return r;
 }
 
+// 32 bytes, a sector, at once
+__device__ __forceinline__ void put8(uint16_t *p, const uint32_t (&w)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// adds the values that are not finite, of the noted tokens that a row sees (the first `most`), to 16 dimensions from k on
+// (rarely needed: out of line)
+static __device__ __noinline__ void prompt_add(const PromptArgs &a, float (&o)[16], const uint32_t *bad, int edge, int most, int k0,
+                                               int head, int k)
+{
+    for (int w = 0; w < 12; ++w)
+        for (uint32_t set = *reinterpret_cast<const volatile uint32_t *>(bad + w); set; set &= set - 1) {
+            const int token = (edge + w / 4) * MOE_PROMPT_TOKENS + (w & 3) * 32 + __ffs(set) - 1;
+            if (token >= most)
+                continue;
+            const uint16_t *v = a.v + (long long)(k0 + token) * a.v_tok + head * a.v_head + k;
+            for (int i = 0; i < 16; ++i)
+                if ((v[i] & 0x7F80u) == 0x7F80u)
+                    o[i] += bf16_to_f32(v[i]);
+        }
+}
+
 template <int D>
 __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const __grid_constant__ PromptArgs a)
 {
@@ -160,10 +183,10 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
     uint8_t *sq = smem_prompt, *ring = smem_prompt + 2 * Q_TILE, *small = ring + MOE_PROMPT_PLACES * PLACE;
     uint64_t *bars = reinterpret_cast<uint64_t *>(small);
     uint64_t *k_full = bars, *v_full = bars + 2, *k_free = bars + 4, *v_free = bars + 6;  // [2], by tiles
-    uint64_t *s_full = bars + 8, *p_full = bars + 10, *pv_done = bars + 12;               // [2], by M tile
+    uint64_t *s_full = bars + 8, *p_full = bars + 10, *o_full = bars + 12;                // [2], by M tile
     uint64_t *v_edge = bars + 14, *v_clean = bars + 17;  // [3] values of the tiles that are looked through: there, and fit
-    uint64_t *q_full = bars + 20, *drained = bars + 21;  // drained [2]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 23);
+    uint64_t *q_full = bars + 20, *drained = bars + 21;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 22);
     uint32_t *bad = tmem_slot + 1;  // [3][4] tokens of the tiles that are looked through with values that are not finite
     int *scan = reinterpret_cast<int *>(bad + 12), *found = scan + 33;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.x;
@@ -177,14 +200,12 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
             mbar_init(v_free + x, 1);
             mbar_init(s_full + x, 1);
             mbar_init(p_full + x, MOE_PROMPT_SOFT / 2);
-            mbar_init(pv_done + x, 1);
-            mbar_init(drained + x, 1);
+            mbar_init(o_full + x, 1);
         }
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 3; ++i)
             mbar_init(v_edge + i, 1);
-            mbar_init(v_clean + i, MOE_PROMPT_CLEAN);
-        }
-        mbar_init(q_full, MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN);
+        mbar_init(q_full, a.q_wide ? 1 : MOE_PROMPT_SOFT);
+        mbar_init(drained, 1);
         fence_barrier_init();
     }
     if (tid < 12)
@@ -199,6 +220,17 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
             a.out[(b.q0 + i / D) * a.o_tok + head * a.o_head + i % D] = 0;
         return;
     }
+    const int rows = b.q1 - b.q0;
+    // tokens that row i of the block sees
+    auto sees = [&](int i) { return a.causal ? max(0, min(b.t, b.t - b.n + b.row + i + 1)) : b.t; };
+    // tiles of each M tile, and the first that not all rows see whole
+    const int tiles0 = (sees(min(rows, 128) - 1) + TOKENS - 1) / TOKENS, tiles1 = rows > 128 ? (sees(rows - 1) + TOKENS - 1) / TOKENS : 0;
+    const int tiles = max(tiles0, tiles1), edge = sees(0) / TOKENS;
+    if (tid == 0) {
+        for (int i = 0; i < 3; ++i)  // the warps of the M tiles that the tile is for
+            mbar_init(v_clean + i, max(1, (edge + i < tiles0 ? MOE_PROMPT_SOFT / 2 : 0) + (edge + i < tiles1 ? MOE_PROMPT_SOFT / 2 : 0)));
+        fence_barrier_init();
+    }
     if (warp == 0)
         tmem_alloc(tmem_slot, 512);
     tc_fence_before();
@@ -206,44 +238,39 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_launch_dependents();
-    const int rows = b.q1 - b.q0;
-    // tokens that row i of the block sees
-    auto sees = [&](int i) { return a.causal ? max(0, min(b.t, b.t - b.n + b.row + i + 1)) : b.t; };
-    // tiles of each M tile, and the first that not all rows see whole
-    const int tiles0 = (sees(min(rows, 128) - 1) + TOKENS - 1) / TOKENS, tiles1 = rows > 128 ? (sees(rows - 1) + TOKENS - 1) / TOKENS : 0;
-    const int tiles = max(tiles0, tiles1), edge = sees(0) / TOKENS;
+    // (a poll that does not hold the warp first: 15 clocks where the phase is complete, one that may 69)
     auto wait = [&](uint64_t *bar, int phase) {
-        return tree_poll(bar, (uint32_t)phase & 1u) || tree_wait_on(bar, (uint32_t)phase & 1u, status, a.wait_ns);
+        return mbar_try_wait(bar, (uint32_t)phase & 1u) || tree_wait_on(bar, (uint32_t)phase & 1u, status, a.wait_ns);
     };
     auto drain = [&](uint64_t *bar, int phase) { tree_wait_on(bar, (uint32_t)phase & 1u, status, max(a.wait_ns, MOE_TREE_DRAIN_NS)); };
     auto place = [&](int i) { return ring + (i & (MOE_PROMPT_PLACES - 1)) * PLACE; };
 
-    if (warp < MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN && tiles > 0) {
-        // ---------------- the queries
+    if (warp < MOE_PROMPT_SOFT && tiles > 0 && !a.q_wide) {
+        // ---------------- queries that TMA does not take
         constexpr int PIECES = D / 8 + 8;
-        for (int i = tid; i < rows * PIECES; i += (MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN) * 32) {
+        for (int i = tid; i < rows * PIECES; i += MOE_PROMPT_SOFT * 32) {
             const int r = i / PIECES, k = i % PIECES;
-            uint4 *at = reinterpret_cast<uint4 *>(sq + (r >> 7) * Q_TILE + (k >> 3) * PLACE + (r & 127) * 128 + (((k & 7) ^ (r & 7)) << 4));
-            const uint16_t *from = a.q + (long long)(b.q0 + r) * a.q_tok + head * a.q_head + k * 8;
-            if (k >= D / 8 + a.rope / 8)
-                *at = make_uint4(0, 0, 0, 0);
-            else if (a.q_wide)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(at)), "l"(from) : "memory");
-            else
-                *at = latent_get(from, false);
+            *reinterpret_cast<uint4 *>(sq + (r >> 7) * Q_TILE + (k >> 3) * PLACE + (r & 127) * 128 + (((k & 7) ^ (r & 7)) << 4)) =
+                k < D / 8 + a.rope / 8 ? latent_get(a.q + (long long)(b.q0 + r) * a.q_tok + head * a.q_head + k * 8, false)
+                                       : make_uint4(0, 0, 0, 0);
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
             mbar_arrive(q_full);
     }
 
-    if (warp == MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN) {
+    if (warp == MOE_PROMPT_SOFT) {
         // ---------------- the copies: K of tile u once V of tile u - 2 is done with, V of it once K of tile u - 1 is
         if (lane == 0) {
             bool ok = true;
             int u = 0, half = 0;  // half: K of tile u has been asked for
+            if (a.q_wide && tiles > 0) {
+                const int m = rows > 128 ? 2 : 1;
+                mbar_arrive_expect_tx(q_full, m * Q_TILE);
+                for (int i = 0; i < m * KC; ++i)
+                    tma_load_3d(sq + i * PLACE, &a.queries, i % KC * 64, head, b.q0 + i / KC * 128, q_full);
+            }
             for (; u < tiles; ++u) {
                 const int x = u & 1, at = u * (KC + VC), token = b.k0 + u * TOKENS;
                 half = 0;
@@ -268,6 +295,8 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
                         tma_load_3d(place(at + KC + i) + d * VT * 128, &a.values, d * 64, a.one_v ? 0 : head, token + i * VT, v_bar);
             }
             // nothing in flight when the CTA ends
+            if (a.q_wide && tiles > 0)
+                drain(q_full, 0);
             for (int k = max(0, u - 2); k < u; ++k) {
                 drain(k_full + (k & 1), k >> 1);
                 drain(k < edge ? v_full + (k & 1) : v_edge + (k - edge), k < edge ? k >> 1 : 0);
@@ -275,9 +304,9 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
             if (!ok && half)
                 drain(k_full + (u & 1), u >> 1);
         }
-    } else if (warp > MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN) {
-        // ---------------- the products: a warp S's, one O's
-        const bool scores = warp == MOE_PROMPT_SOFT + MOE_PROMPT_CLEAN + 1;
+    } else if (warp == MOE_PROMPT_SOFT + 1) {
+        // ---------------- the products, in order: for each M tile in turn, O with the last tile's P, then S of this one in
+        // P's place, so that one's products pass under the other's softmax
         constexpr uint32_t id_s = mma_idesc(128, TOKENS, true), id_o = mma_idesc(128, D, true) | (1u << 16);
         const uint32_t tm = __reduce_max_sync(0xFFFFFFFFu, tmem);  // (what the loops need is the same in all lanes)
         const int n = __reduce_max_sync(0xFFFFFFFFu, tiles), n0 = __reduce_max_sync(0xFFFFFFFFu, tiles0),
@@ -287,19 +316,36 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
         const uint64_t vd = kd & ~(0x3FFFull << 16) | (uint64_t)(VT * 128 / 16) << 16;
         auto all = [&](bool v) { return __all_sync(0xFFFFFFFFu, v) != 0; };
         auto off = [&](int i) { return (uint32_t)((i & (MOE_PROMPT_PLACES - 1)) * PLACE) / 16; };
-        bool ok = n == 0 || !scores || all(wait(q_full, 0));
-        for (int u = 0; u < n && ok; ++u) {
-            const int x = u & 1, at = u * (KC + VC);
-            if (scores) {
-                ok = all(wait(k_full + x, u >> 1));
+        bool ok = n == 0 || all(wait(q_full, 0));
+        for (int u = 0; u <= n && ok && n > 0; ++u) {
+            const int at = u * (KC + VC), x = u & 1;
+            ok = u == 0 || all(u - 1 < e ? wait(v_full + (x ^ 1), (u - 1) >> 1) : wait(v_clean + (u - 1 - e), 0));
+            bool keys = false;
 #pragma unroll 1
-                for (int g = 0; g < 2; ++g) {
-                    if (u >= (g ? n1 : n0) || !ok)
-                        continue;
-                    ok = u == 0 || all(wait(pv_done + g, u - 1));  // P, in S's place, has been read
+            for (int g = 0; g < 2 && ok; ++g) {
+                const int last = g ? n1 : n0;
+                if (u > 0 && u <= last) {
+                    ok = all(wait(p_full + g, u - 1));
                     if (!ok)
                         break;
                     tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)  // 16 tokens: 8 columns of P, 2048 bytes of V
+                        mma1_f16_ts(tm + O_COL + g * 128, tm + S_COL + g * 128 + k * 8,
+                                    vd + off(at - VC + k * 16 / VT) + (uint32_t)(k * 16 % VT * 128) / 16, id_o, u > 1 || k > 0);
+                    if (u == last)
+                        mma1_commit(o_full + g);
+                    if (g || u > n1)  // the last M tile's: before S's products, so that the copies wait no longer
+                        mma1_commit(v_free + (x ^ 1));
+                }
+                if (u < last) {
+                    if (!keys) {
+                        ok = all(wait(k_full + x, u >> 1));
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        keys = true;
+                    }
 #pragma unroll
                     for (int d = 0; d < KC; ++d)
 #pragma unroll
@@ -308,55 +354,13 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
                                      kd + off(at + d) + k * 2, id_s, d + k > 0);
                     mma1_commit(s_full + g);
                 }
-                mma1_commit(k_free + x);
-            } else {
-                ok = all(u < e ? wait(v_full + x, u >> 1) : wait(v_clean + (u - e), 0));
-#pragma unroll 1
-                for (int g = 0; g < 2; ++g) {
-                    if (u >= (g ? n1 : n0) || !ok)
-                        continue;
-                    ok = all(wait(p_full + g, u));
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)  // 16 tokens: 8 columns of P, 2048 bytes of V
-                        mma1_f16_ts(tm + O_COL + g * 128, tm + S_COL + g * 128 + k * 8,
-                                    vd + off(at + KC + k * 16 / VT) + (uint32_t)(k * 16 % VT * 128) / 16, id_o, u > 0 || k > 0);
-                    mma1_commit(pv_done + g);
-                }
-                mma1_commit(v_free + x);
             }
+            if (u < n)
+                mma1_commit(k_free + x);
         }
         if (n > 0) {  // what has been issued ends before tensor and shared memory are given back
-            mma1_commit(drained + scores);
-            drain(drained + scores, 0);
-        }
-    } else if (warp >= MOE_PROMPT_SOFT) {
-        // ---------------- values of tiles that not all rows see: those past the end zeros, those that are not finite
-        // zeros and noted
-        bool ok = true;
-        for (int u = edge; u < tiles; ++u) {
-            ok = ok && wait(v_edge + (u - edge), 0);
-            __syncwarp();
-            const int at = u * (KC + VC) + KC;
-            for (int i = tid - MOE_PROMPT_SOFT * 32; i < TOKENS * D / 8; i += MOE_PROMPT_CLEAN * 32) {
-                const int token = i / (D / 8), piece = i % (D / 8);
-                uint4 *p = reinterpret_cast<uint4 *>(place(at + token / VT) + (piece >> 3) * VT * 128 + token % VT * 128 + (piece & 7) * 16);
-                if (u * TOKENS + token >= b.t) {
-                    *p = make_uint4(0, 0, 0, 0);
-                    continue;
-                }
-                const uint4 v = *p, w = make_uint4(finite_bf2(v.x), finite_bf2(v.y), finite_bf2(v.z), finite_bf2(v.w));
-                if (v.x != w.x || v.y != w.y || v.z != w.z || v.w != w.w) {
-                    *p = w;
-                    atomicOr(bad + (u - edge) * 4 + (token >> 5), 1u << (token & 31));
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(v_clean + (u - edge));
+            mma1_commit(drained);
+            drain(drained, 0);
         }
     } else {
         // ---------------- softmax: M tile g, row `row` of it
@@ -371,6 +375,29 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int u = 0; u < n; ++u) {
+            if (u >= edge) {
+                // values of a tile that not all rows see: those past the end zeros, those that are not finite zeros and
+                // noted; each M tile that the tile is for looks through its part
+                ok = ok && wait(v_edge + (u - edge), 0);
+                __syncwarp();
+                const int at = u * (KC + VC) + KC, other = g ? tiles0 : tiles1, step = u < other ? 256 : 128;
+#pragma unroll 2
+                for (int i = u < other ? tid : tid & 127; i < TOKENS * D / 8; i += step) {
+                    const int token = i / (D / 8), piece = i % (D / 8);
+                    uint4 *p = reinterpret_cast<uint4 *>(place(at + token / VT) + (piece >> 3) * VT * 128 + token % VT * 128 + (piece & 7) * 16);
+                    const uint4 v = *p, w = u * TOKENS + token >= b.t ? make_uint4(0, 0, 0, 0)
+                                                                      : make_uint4(finite_bf2(v.x), finite_bf2(v.y), finite_bf2(v.z), finite_bf2(v.w));
+                    if (v.x != w.x || v.y != w.y || v.z != w.z || v.w != w.w) {
+                        *p = w;
+                        if (u * TOKENS + token < b.t)
+                            atomicOr(bad + (u - edge) * 4 + (token >> 5), 1u << (token & 31));
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(v_clean + (u - edge));
+            }
             ok = ok && wait(s_full + g, u);
             __syncwarp();
             tc_fence_after();
@@ -445,23 +472,26 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
                     tmem_st16(s_at + k / 2 + 16 * h, w);  // P over the columns that have been read
                 }
             }
-            sum = add2(sum, sum1);
-            float l0, l1;
-            sum.get(l0, l1);
-            l += l0 + l1;
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(p_full + g);
+            sum = add2(sum, sum1);
+            float l0, l1;
+            sum.get(l0, l1);
+            l += l0 + l1;
         }
         // ---- the end
         if (n > 0)
-            ok = ok && wait(pv_done + g, n - 1);
+            ok = ok && wait(o_full + g, 0);
         __syncwarp();
         tc_fence_after();
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         uint16_t *to = a.out + (long long)(b.q0 + mine) * a.o_tok + head * a.o_head;
+        uint32_t any = 0;  // values that are not finite
+        for (int w = 0; w < 12; ++w)
+            any |= *reinterpret_cast<volatile uint32_t *>(bad + w);
 #pragma unroll 1
         for (int k = 0; k < D && mine - lane < rows; k += 16) {
             float o[16];
@@ -472,26 +502,20 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
                 for (int i = 0; i < 16; ++i)
                     o[i] = 0.0f;
             }
-#pragma unroll 1
-            for (int w = 0; w < 12; ++w)  // values that are not finite, of tokens that the row sees
-                for (uint32_t set = *reinterpret_cast<volatile uint32_t *>(bad + w); set; set &= set - 1) {
-                    const int token = (edge + w / 4) * TOKENS + (w & 3) * 32 + __ffs(set) - 1;
-                    if (token >= most)
-                        continue;
-                    const uint16_t *v = a.v + (long long)(b.k0 + token) * a.v_tok + head * a.v_head + k;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if ((v[i] & 0x7F80u) == 0x7F80u)
-                            o[i] += bf16_to_f32(v[i]);
-                }
+            if (any)
+                prompt_add(a, o, bad, edge, most, b.k0, head, k);
             if (!live)
                 continue;
             uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 16; i += 2)
                 w[i / 2] = pack_bf2(o[i] * inv, o[i + 1] * inv);
-            latent_put(to + k, make_uint4(w[0], w[1], w[2], w[3]), a.o_wide);
-            latent_put(to + k + 8, make_uint4(w[4], w[5], w[6], w[7]), a.o_wide);
+            if (a.o_wide == 2) {
+                put8(to + k, w);
+            } else {
+                latent_put(to + k, make_uint4(w[0], w[1], w[2], w[3]), a.o_wide);
+                latent_put(to + k + 8, make_uint4(w[4], w[5], w[6], w[7]), a.o_wide);
+            }
         }
     }
     tc_fence_before();
