@@ -204,9 +204,11 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
     pdl_launch_dependents();
     if (tiles == 0 && tid == 0 && rank == 0)
         t.cuts[pair].runs = 0;
-    // (a poll that does not hold the warp first: 15 clocks where the phase is complete, one that may 69)
+    // (a poll that does not hold the warp first: 15 clocks where the phase is complete, one that may 69; and the clock,
+    // which takes longer than most waits, last)
     auto wait = [&](uint64_t *bar, int phase) {
-        return mbar_try_wait(bar, (uint32_t)phase & 1u) || tree_wait_on(bar, (uint32_t)phase & 1u, status, t.wait_ns);
+        return mbar_try_wait(bar, (uint32_t)phase & 1u) || tree_poll(bar, (uint32_t)phase & 1u) ||
+               tree_wait_on(bar, (uint32_t)phase & 1u, status, t.wait_ns);
     };
     auto drain = [&](uint64_t *bar, int phase) { tree_wait_on(bar, (uint32_t)phase & 1u, status, max(t.wait_ns, MOE_TREE_DRAIN_NS)); };
     auto to_item = [&](int u, TreeItem &it) {

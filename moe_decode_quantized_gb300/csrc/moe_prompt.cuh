@@ -238,9 +238,11 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_launch_dependents();
-    // (a poll that does not hold the warp first: 15 clocks where the phase is complete, one that may 69)
+    // (a poll that does not hold the warp first: 15 clocks where the phase is complete, one that may 69; and the clock,
+    // which takes longer than most waits, last)
     auto wait = [&](uint64_t *bar, int phase) {
-        return mbar_try_wait(bar, (uint32_t)phase & 1u) || tree_wait_on(bar, (uint32_t)phase & 1u, status, a.wait_ns);
+        return mbar_try_wait(bar, (uint32_t)phase & 1u) || tree_poll(bar, (uint32_t)phase & 1u) ||
+               tree_wait_on(bar, (uint32_t)phase & 1u, status, a.wait_ns);
     };
     auto drain = [&](uint64_t *bar, int phase) { tree_wait_on(bar, (uint32_t)phase & 1u, status, max(a.wait_ns, MOE_TREE_DRAIN_NS)); };
     auto place = [&](int i) { return ring + (i & (MOE_PROMPT_PLACES - 1)) * PLACE; };
