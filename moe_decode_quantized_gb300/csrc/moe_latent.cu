@@ -55,7 +55,7 @@ int latent_rows(bool read, LatentRows &a, const moe_latent_cache *cache, moe_str
     a.c_wide = wide_rows(a.c, a.c_stride, 0);
     a.kr_wide = wide_rows(a.kr, a.kr_stride, 0);
     const long long pieces = (long long)a.tokens * (a.latent / 8);
-    const dim3 grid((unsigned)((pieces + MOE_LATENT_THREADS - 1) / MOE_LATENT_THREADS), 2);
+    const dim3 grid((unsigned)((pieces + MOE_LATENT_PIECES * MOE_LATENT_THREADS - 1) / (MOE_LATENT_PIECES * MOE_LATENT_THREADS)), 2);
     MOE_CUDA_OK(launch(read ? moe_latent_rows_kernel<true> : moe_latent_rows_kernel<false>, grid, MOE_LATENT_THREADS, 0,
                        stream, a));
     return MOE_OK;

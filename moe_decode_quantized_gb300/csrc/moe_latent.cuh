@@ -63,49 +63,75 @@ __device__ __forceinline__ uint16_t *latent_row(const LatentRows &a, int token)
     return nullptr;
 }
 
+#define MOE_LATENT_PIECES 4  // of a thread, in flight together
+
+// One piece of a key part on its way into the cache: turned
+__device__ __forceinline__ uint4 latent_turned(const LatentRows &a, int token, int piece, const uint16_t *row, uint4 v)
+{
+    const int p = a.positions[token];
+    float f[8];
+    piece_get<false>(v, f);
+    if (a.layout == MOE_ROPE_INTERLEAVED) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            rope_apply(f[2 * k], f[2 * k + 1], rope_turn(p, a.table[piece * 4 + k], a.magnitude, 1.0f));
+    } else {  // the other of each pair, which another thread writes, is read too
+        const int half = a.rope / 2;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int d = piece * 8 + k, i2 = d < half ? d : d - half;
+            const float2 cs = rope_turn(p, a.table[i2], a.magnitude, 1.0f);
+            const float o = bf16_to_f32(row[d < half ? d + half : i2]);
+            f[k] = d < half ? f[k] * cs.x - o * cs.y : o * cs.y + f[k] * cs.x;
+        }
+    }
+    return piece_put<false>(f);
+}
+
 // blockIdx.y 0: the latent vectors' pieces; 1: the key parts'
 template <bool READ>
 __global__ void __launch_bounds__(MOE_LATENT_THREADS) moe_latent_rows_kernel(const __grid_constant__ LatentRows a)
 {
+    constexpr int U = MOE_LATENT_PIECES;
     pdl_wait();
-    const long long i = (long long)blockIdx.x * MOE_LATENT_THREADS + threadIdx.x;
     const bool key = blockIdx.y != 0;
-    const int per = (key ? a.rope : a.latent) / 8;
-    const int token = (int)(i / per), piece = (int)(i - (long long)token * per);
-    if (token >= a.tokens)
-        return;
-    uint16_t *row = latent_row(a, token);
-    uint16_t *other = key ? a.kr + token * a.kr_stride : a.c + token * a.c_stride;
+    const int shift = key ? 0 : 31 - __clz(a.latent / 8), per = key ? a.rope / 8 : a.latent / 8;  // latent_dim is a power of two
     const bool wide = key ? a.kr_wide : a.c_wide;
-    if (READ) {
-        const uint4 v = row ? *reinterpret_cast<const uint4 *>(row + (key ? a.latent : 0) + piece * 8) : make_uint4(0, 0, 0, 0);
-        latent_put(other + piece * 8, v, wide);
-        return;
+    const long long stride = key ? a.kr_stride : a.c_stride, first = (long long)blockIdx.x * (U * MOE_LATENT_THREADS) + threadIdx.x;
+    uint16_t *rows[U], *others[U];
+    uint4 v[U];
+    int tokens[U], pieces[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const long long i = first + u * MOE_LATENT_THREADS;
+        tokens[u] = (int)(key ? i / per : i >> shift);
+        pieces[u] = (int)(i - (long long)tokens[u] * per);
+        rows[u] = nullptr;
+        if (i < (long long)a.tokens * per)
+            rows[u] = latent_row(a, tokens[u]);
+        else
+            tokens[u] = -1;
     }
-    if (!row)
-        return;
-    uint4 v = latent_get(other + piece * 8, wide);
-    if (key && a.positions) {
-        const int p = a.positions[token];
-        float f[8];
-        piece_get<false>(v, f);
-        if (a.layout == MOE_ROPE_INTERLEAVED) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                rope_apply(f[2 * k], f[2 * k + 1], rope_turn(p, a.table[piece * 4 + k], a.magnitude, 1.0f));
-        } else {  // the other of each pair, which another thread writes, is read too
-            const int half = a.rope / 2;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int d = piece * 8 + k, i2 = d < half ? d : d - half;
-                const float2 cs = rope_turn(p, a.table[i2], a.magnitude, 1.0f);
-                const float o = bf16_to_f32(other[d < half ? d + half : i2]);
-                f[k] = d < half ? f[k] * cs.x - o * cs.y : o * cs.y + f[k] * cs.x;
-            }
+    for (int u = 0; u < U; ++u) {
+        others[u] = (key ? a.kr : a.c) + max(tokens[u], 0) * stride;
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (rows[u]) {
+            rows[u] += (key ? a.latent : 0) + pieces[u] * 8;
+            v[u] = READ ? *reinterpret_cast<const uint4 *>(rows[u]) : latent_get(others[u] + pieces[u] * 8, wide);
         }
-        v = piece_put<false>(f);
     }
-    *reinterpret_cast<uint4 *>(row + (key ? a.latent : 0) + piece * 8) = v;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (READ) {
+            if (tokens[u] >= 0)
+                latent_put(others[u] + pieces[u] * 8, v[u], wide);
+        } else if (rows[u]) {
+            if (key && a.positions)
+                v[u] = latent_turned(a, tokens[u], pieces[u], others[u], v[u]);
+            *reinterpret_cast<uint4 *>(rows[u]) = v[u];
+        }
+    }
 }
 
 }  // namespace moe

@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 tops[half * 64 + row] = top;
                 meet();
                 top = fmaxf(top, tops[(half ^ 1) * 64 + row]);
-                const bool moves = (top - m) * c > MOE_LTC_SLACK;
+                const bool moves = live && (top - m) * c > MOE_LTC_SLACK;  // (rows that are none hold anything)
                 if (__any_sync(0xFFFFFFFFu, moves)) {
                     const float f = moves ? ex2((m - top) * c) : 1.0f;
                     m = moves ? top : m;

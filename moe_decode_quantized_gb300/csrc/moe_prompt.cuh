@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
                         top4[i >> 1 & 3] = max3(top4[i >> 1 & 3], __uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1]));
             }
             const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-            const bool moves = (top - m) * c > MOE_PROMPT_SLACK;
+            const bool moves = live && (top - m) * c > MOE_PROMPT_SLACK;  // (rows that are none hold anything)
             if (__any_sync(0xFFFFFFFFu, moves)) {
                 const float f = moves ? ex2((m - top) * c) : 1.0f;
                 m = moves ? top : m;
