@@ -539,21 +539,21 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             float *part = t.part + ((size_t)pair * 2 + (it.lo <= lo ? 0 : 1)) * ROWS * (L + 2);
             uint16_t *to = t.out + (it.first + node) * t.o_tok + (live ? at % t.group : 0) * t.o_head + half * (L / 2);
 #pragma unroll 1
-            for (int k = 0; k < T::O_COLS; k += 16) {
-                float o[16];
-                tmem_ld16(lanes + O_COL + k, o);
+            for (int k = 0; k < T::O_COLS; k += 32) {
+                float o[32];
+                tmem_ld32(lanes + O_COL + k, o);
                 if (live && !whole) {
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4)
+                    for (int i = 0; i < 32; i += 4)
                         reinterpret_cast<float4 *>(part)[(half * (L / 2) + k + i) / 4 * ROWS + mine] =
                             make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 } else if (live) {
-                    uint32_t w[8];
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2)
-                        w[i / 2] = pack_bf2(o[i] * inv, o[i + 1] * inv);
-                    latent_put(to + k, make_uint4(w[0], w[1], w[2], w[3]), t.o_wide);
-                    latent_put(to + k + 8, make_uint4(w[4], w[5], w[6], w[7]), t.o_wide);
+                    for (int i = 0; i < 32; i += 8)
+                        latent_put(to + k + i,
+                                   make_uint4(pack_bf2(o[i] * inv, o[i + 1] * inv), pack_bf2(o[i + 2] * inv, o[i + 3] * inv),
+                                              pack_bf2(o[i + 4] * inv, o[i + 5] * inv), pack_bf2(o[i + 6] * inv, o[i + 7] * inv)),
+                                   t.o_wide);
                 }
             }
             tc_fence_before();
@@ -596,8 +596,15 @@ __global__ void __launch_bounds__(MOE_LTC_JOIN_THREADS) moe_latent_join_kernel(c
     const float *base = a.part + (size_t)blockIdx.x * 2 * SIZE;
     auto part = [&](int i) { return base + (i == 0 && !c.whole_run ? SIZE : 2 * i * SIZE); };
     float m = -INFINITY;
-    for (int i = 0; i <= c.runs; ++i)
-        m = fmaxf(m, part(i)[ROWS * L + r]);
+    for (int i0 = 0; i0 <= c.runs; i0 += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = i0 + i <= c.runs ? part(i0 + i)[ROWS * L + r] : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            m = fmaxf(m, v[i]);
+    }
     float4 o[4];
     float l = 0.0f;
 #pragma unroll
