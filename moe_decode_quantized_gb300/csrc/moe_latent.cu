@@ -432,6 +432,7 @@ int moe_latent_attention(const moe_latent_cache *cache, const void *q_dev, int64
     t.part = reinterpret_cast<float *>(t.cuts + MOE_LTC_MAX_PAIRS);
     t.wait_ns = host_wait_ns();
     a.big = t.k.page % 32 == 0;
+    a.per_page = ((1ull << 36) + t.k.page / 16 - 1) / (t.k.page / 16);
     if ((rc = latent_maps(cache, a)))
         return rc;
     LatentDevice *dev;

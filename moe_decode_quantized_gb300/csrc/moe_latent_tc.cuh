@@ -39,6 +39,7 @@ struct LatentArgs {
     long long qr_tok, qr_head;
     int rope, qr_wide;
     int big;  // boxes of 32 tokens and of all chunks; else of 16 tokens and one
+    unsigned long long per_page;  // 2^36 / (page / 16), rounded up: x / (page / 16) = x per_page >> 36 below 2^27
     CUtensorMap keys, values, ropes;  // the cache's rows [64, slots, chunks]; the same; their turning part [rope, slots]
 };
 
@@ -218,19 +219,24 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             tree_next<ROWS, TOKENS>(t, cum, it);
     };
     auto item_end = [&](const TreeItem &it) { return (int)(min(hi, it.lo + it.units) - lo); };
-    // lane i < 4: the slot of the i-th 16 tokens of tile u, and where there is none one past the pool, which reads as zeros
-    const int no_slot = t.n_pages * t.k.page;
-    auto find = [&](const TreeItem &it, int u, bool tell) {
-        const int j = (int)(lo + u - it.lo) * TOKENS + (lane & 3) * 16;
-        int slot = no_slot;
-        if (j < it.len) {
-            const int at = j / t.k.page, page = t.table[it.b * t.table_stride + at];
-            if (page >= 0 && page < t.n_pages)
-                slot = page * t.k.page + (j - at * t.k.page);
-            else if (tell && lane < 4)
-                atomicOr(status, (uint32_t)MOE_WS_INDEX);
-        }
-        return slot;
+    // lane i < 4: where the i-th 16 tokens of tile u are, in two steps, so that the table's entry can come under a wait: the
+    // entry (block -1: past the length), then the slot; where there is none, one past the pool, which reads as zeros
+    const int no_slot = t.n_pages * t.k.page, page_blocks = t.k.page / 16;
+    struct Place {
+        int page, block;
+    };
+    auto look = [&](const TreeItem &it, int u) {
+        const int blk = (int)(lo + u - it.lo) * (TOKENS / 16) + (lane & 3);
+        const int at = (int)((unsigned long long)(unsigned)blk * a.per_page >> 36);
+        const bool in = blk * 16 < it.len;
+        return Place{in ? t.table[it.b * t.table_stride + at] : -1, in ? blk - at * page_blocks : -1};
+    };
+    auto find = [&](const Place &p, bool tell) {
+        if (p.page >= 0 && p.page < t.n_pages)
+            return p.page * t.k.page + p.block * 16;
+        if (tell && lane < 4 && p.block >= 0)
+            atomicOr(status, (uint32_t)MOE_WS_INDEX);
+        return no_slot;
     };
     // copies of chunks `first` on (`n` of them) of the tokens' half h of a tile to `to`, counted by `bar` (pair_bar)
     auto copy = [&](const CUtensorMap *map, uint8_t *to, int first, int n, int slots, int h, uint32_t bar) {
@@ -249,17 +255,26 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
     if (warp == MOE_LTC_SOFT) {
         // ---------------- this CTA's half of each tile's tokens, whole rows
         bool ok = true;
-        int u = 0, end = 0;
+        int u = 0, end = 0, s = 0, phase = 0;
         TreeItem it{};
-        for (; u < tiles; ++u) {
-            if (u == end) {
-                to_item(u, it);
-                end = item_end(it);
+        Place next{};
+        auto look_on = [&](int v) {
+            if (v < tiles) {
+                if (v == end) {
+                    to_item(v, it);
+                    end = item_end(it);
+                }
+                next = look(it, v);
             }
-            const int s = u % stages, slots = find(it, u, rank == 0);
+        };
+        look_on(0);
+        for (; u < tiles; ++u) {
+            const Place now = next;
+            look_on(u + 1);
+            const int slots = find(now, rank == 0);
             const uint32_t out = __ballot_sync(0xFFFFFFFFu, slots == no_slot) & 15u;
             if (u >= stages)
-                ok = __all_sync(0xFFFFFFFFu, wait(empty + s, u / stages - 1));
+                ok = __all_sync(0xFFFFFFFFu, wait(empty + s, phase - 1));
             if (!ok)
                 break;
             uint8_t *to = ring + (size_t)s * T::STAGE;
@@ -276,33 +291,53 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 pair_load_2d(to + T::CHUNKS * MOE_LTC_CHUNK, &a.ropes, 0, s0, bar);
             if (lane == 1 && !a.big)
                 pair_load_2d(to + T::CHUNKS * MOE_LTC_CHUNK + 2048, &a.ropes, 0, s1, bar);
+            if (++s == stages) {
+                s = 0;
+                ++phase;
+            }
         }
         for (int k = max(0, u - stages); k < u; ++k)  // nothing in flight, nothing to arrive when the CTA ends
             drain(ok ? empty + k % stages : rank == 0 ? full + k % stages : drained + 3, ok || rank == 0 ? k / stages : 0);
     } else if (warp == MOE_LTC_SOFT + 4) {
         // ---------------- the other tokens' values, once the tile's S is there
         bool ok = true;
-        int u = 0, end = 0;
+        int u = 0, end = 0, s = 0, phase = 0;
+        const int other = 1 - (int)rank;
+        uint32_t sent = 0;  // of v_here: phases begun, by x, a bit each for some and for their parity
         TreeItem it{};
         for (; u < tiles; ++u) {
             if (u == end) {
                 to_item(u, it);
                 end = item_end(it);
             }
-            const int s = u % stages, slots = find(it, u, false), other = 1 - (int)rank;
-            ok = __all_sync(0xFFFFFFFFu, wait(s_full + s, u / stages));
+            const Place p = look(it, u);
+            ok = __all_sync(0xFFFFFFFFu, wait(s_full + s, phase));
             if (!ok)
                 break;
+            const int slots = find(p, false);
             // counted by the first CTA's barrier, but in a tile that the softmax warps look through by their own CTA's
             const bool own = special(it, u);
             if (lane == 0 && (rank == 0 || own))
                 mbar_arrive_expect_tx(rank == 0 ? v_full + s : v_here + (u & 1), (own ? 1 : 2) * T::HALF * MOE_LTC_CHUNK);
+            if (own && rank == 1)
+                sent = (sent | 1u << (u & 1)) ^ 4u << (u & 1);
             __syncwarp();
             copy(&a.values, ring + (size_t)s * T::STAGE + other * T::HALF * MOE_LTC_CHUNK, (int)rank * T::HALF, T::HALF, slots,
                  other, own && rank == 1 ? pair_bar(v_here + (u & 1), 1) : pair_bar(v_full + s, 0));
+            if (++s == stages) {
+                s = 0;
+                ++phase;
+            }
         }
-        for (int k = max(0, u - stages); k < u && !ok; ++k)
-            drain(rank == 0 ? v_full + k % stages : drained + 3, rank == 0 ? k / stages : 0);
+        for (int k = max(0, u - stages); k < u; ++k) {
+            if (rank == 0)
+                drain(v_full + k % stages, k / stages);
+            else if (!ok)
+                drain(drained + 3, 0);
+        }
+        for (int x = 0; x < 2; ++x)
+            if (sent >> x & 1)
+                drain(v_here + x, (int)(sent >> (2 + x) & 1) - 1);
     } else if (warp >= MOE_LTC_SOFT && rank == 0) {
         // ---------------- the products: two warps those of S, a tile each in turn, another those of O, so that one's
         // waits pass under the others' products
@@ -361,7 +396,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 ++phase;
             }
         }
-        if (!ok) {  // products may be in flight: they end before tensor and shared memory are given back
+        if (n > 0) {  // what has been issued ends before tensor and shared memory are given back
             mma2_commit(drained + role);
             drain(drained + role, 0);
         }
@@ -377,7 +412,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
         const float turn = flat ? 0.0f : sign;
         const float c = flat ? 1.0f : scaled;
         bool ok = true;
-        int item = 0;
+        int item = 0, s = 0, phase = 0;  // s, phase: the tile's stage and its phase
         uint32_t seen = 0;  // by x, a bit each: parity of the tiles looked through
         TreeItem it{};
         for (int u = 0; u < tiles; ++item) {
@@ -420,8 +455,8 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             float m = -INFINITY, l = 0.0f;
             bool fresh = true;
             for (; u < end; ++u) {
-                const int x = u & 1, s = u % stages;
-                ok = ok && wait(s_full + s, u / stages);
+                const int x = u & 1;
+                ok = ok && wait(s_full + s, phase);
                 __syncwarp();
                 tc_fence_after();
                 const int first = (int)(lo + u - it.lo) * TOKENS;
@@ -501,7 +536,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                     *reinterpret_cast<uint4 *>(p + (((half * 4 + i) ^ (row & 7)) << 4)) =
                         make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 if (special(it, u)) {
-                    ok = ok && (rank == 0 ? wait(v_full + s, u / stages) : wait(v_here + x, (int)(seen >> x & 1)));
+                    ok = ok && (rank == 0 ? wait(v_full + s, phase) : wait(v_here + x, (int)(seen >> x & 1)));
                     seen ^= 1u << x;
                     // Values past the length are anything, and those of drafted tokens need not be numbers, which must not
                     // reach rows that do not see them: zeros in their place (a row that sees one has a NaN among its scores)
@@ -525,6 +560,10 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 __syncwarp();
                 if (lane == 0)
                     arrive_first(p_full + x);
+                if (++s == stages) {
+                    s = 0;
+                    ++phase;
+                }
             }
             // ---- the item's end
             float *sums = top_of + (end & 1) * 128;  // (the maxima that the last tile has not used)

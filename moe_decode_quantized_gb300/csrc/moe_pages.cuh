@@ -304,24 +304,31 @@ __global__ void __launch_bounds__(MOE_PAGES_THREADS) moe_pages_compact_kernel(co
         a.refs_out[p] = 0;
 }
 
+#define MOE_PAGES_MOVES 8192  // moves whose sources are searched in shared memory
+
 // the table's entries after the moves: those that moved are found among the copies, which ascend
 __global__ void __launch_bounds__(256) moe_pages_remap_kernel(const __grid_constant__ PagesArgs a)
 {
+    __shared__ int from[MOE_PAGES_MOVES];
     pdl_wait();
     const int moved = *a.n_copies, r = blockIdx.y;
+    const bool near = moved <= MOE_PAGES_MOVES;  // (one round of loads instead of one for each step of a search)
+    for (int i = threadIdx.x; near && i < moved; i += 256)
+        from[i] = a.copies[2 * i];
+    __syncthreads();
     for (int j = blockIdx.x * 256 + threadIdx.x; j < a.table_pages; j += gridDim.x * 256) {
         int page = a.table[r * a.stride + j];
         if (page >= a.n_pages)
             pages_flag(a, MOE_WS_INDEX);
-        int x = 0, y = moved;
+        int x = 0, y = page < 0 ? 0 : moved;
         while (x < y) {
             const int z = (x + y) / 2;
-            if (a.copies[2 * z] < page)
+            if ((near ? from[z] : a.copies[2 * z]) < page)
                 x = z + 1;
             else
                 y = z;
         }
-        if (x < moved && a.copies[2 * x] == page)
+        if (page >= 0 && x < moved && a.copies[2 * x] == page)
             page = a.copies[2 * x + 1];
         a.table_out[r * a.stride + j] = page;
     }
