@@ -639,3 +639,119 @@ def test_both_forms_agree():
     # most: a score of about 1 moves by a few 2^-8, and so does a weight; values of unit size, averaged
     assert (short - full.float()).abs().max() <= 8 * ref.BF16 * 1.5
     assert (short - full.float()).square().mean().sqrt() <= ref.BF16
+
+
+# ------------------------------------------------------------------ more of what a caller can do
+
+def test_batch_that_leaves_three_stages():
+    n = 300
+    lens = [1 + 37 * b % 400 for b in range(n)]
+    c = Case(512, 64, 3, 16, [1] * n, lens, seed=41)
+    c.run(0.06)
+    c.check(0.06)
+
+
+def test_most_rows_a_sequence():
+    c = Case(512, 64, 128, 64, [64], [200], seed=42)
+    c.run(0.06)
+    got = c.out[:, ::17]
+    k = c.rows[0].double()[:, None]
+    q = torch.cat([c.q, c.qr], -1)[:, ::17].double().cpu()
+    near(got, *ref.attention(q, k, k[..., :512], c.sees(0), 0.06))
+
+
+def test_an_item_of_many_runs_beside_short_ones():
+    lens = [30000] + [3] * 20
+    c = Case(256, 64, 16, 64, [1] * 21, lens, seed=43)
+    c.run(0.02)
+    c.check(0.02)
+    assert moe.read_status(c.ws) == 0
+
+
+@pytest.mark.parametrize("layout", ["heads", "shared", "odd"])
+def test_prompts_of_other_layouts(layout):
+    """Head-major tensors; keys and values that all heads share (expanded); queries that TMA does not take."""
+    p = Prompt(128, 64, 3, [130, 40], [200, 40], seed=44)
+    if layout == "heads":
+        p.q, p.k, p.v = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (p.q, p.k, p.v))
+        p.out = torch.empty((3, 170, 128), dtype=BF, device="cuda").transpose(0, 1)
+    elif layout == "shared":
+        p.k, p.v = (x[:, :1].contiguous().expand(-1, 3, -1) for x in (p.k, p.v))
+    else:
+        big = torch.zeros((170, 3, 193), dtype=BF, device="cuda")
+        big[..., 1:] = p.q
+        p.q = big[..., 1:]
+    p.run(0.09)
+    p.check(0.09)
+
+
+def test_values_of_seen_tokens_that_are_not_finite():
+    """In the tiles that are looked through and in those that are not: in their own dimensions, of the rows that see them."""
+    p = Prompt(128, 64, 1, [300], [300], seed=45)
+    p.v[10, 0, 5] = float("inf")
+    p.v[150, 0, 7] = float("nan")
+    p.v[290, 0, 9] = -float("inf")
+    p.run(0.05)
+    out = p.out[:, 0].double().cpu()
+    assert (out[10:, 5] == math.inf).all() and torch.isfinite(out[:10]).all()
+    assert torch.isnan(out[150:, 7]).all() and torch.isfinite(out[:150, 7]).all()
+    assert (out[290:, 9] == -math.inf).all() and torch.isfinite(out[:290, 9]).all()
+    assert torch.isfinite(out[:, [0, 1, 2, 3, 4, 6, 8] + list(range(10, 128))]).all()
+
+
+def test_rope_and_rows_in_a_graph():
+    g = torch.Generator().manual_seed(46)
+    x, c = torch.randn((9, 4, 64), generator=g).bfloat16().cuda(), torch.randn((9, 144), generator=g).bfloat16().cuda()
+    cache, table = make_cache(128, 16, 16, 3, 0.0), table_of(16)
+    pos, slots = i32(list(range(9))), i32(list(range(20, 29)))
+    out, co, ko = torch.empty_like(x), torch.empty((9, 128), dtype=BF, device="cuda"), torch.empty((9, 16), dtype=BF, device="cuda")
+
+    def step():
+        moe.rope(x, out, pos, table[0], offset=48)
+        moe.latent_append(cache, c[:, :128], c[:, 128:], slots, pos, table[0])
+        moe.latent_read(cache, slots, co, ko)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for first in (100, 70000):
+        pos.copy_(i32(list(range(first, first + 9))))
+        graph.replay()
+        part = x[..., 48:].double().cpu()
+        near(out[..., 48:], ref.turned(part, pos.tolist(), table[1], 0), ref.turned_bound(part, 0, 1.0, True))
+        part = c[:, None, 128:].double().cpu()
+        near(ko[:, None], ref.turned(part, pos.tolist(), table[1], 0), ref.turned_bound(part, 0, 1.0, True))
+        assert torch.equal(co, c[:, :128])
+
+
+def test_example_decodes_samples():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "latent_decode.py")
+    spec = importlib.util.spec_from_file_location("latent_decode", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    prompts = [[3, 1, 4, 1, 5, 9, 2, 6] * 5, [2, 7, 1, 8]]
+    model = ex.Model()
+    out = ex.generate(model, prompts, 3, 20)
+    assert [len(o) for o in out] == [20] * 6 and len({tuple(o) for o in out[:3]}) > 1
+    # what six forked, grown and compacted rows hold: the prompt's tokens and 19 more
+    counts = [-(-(len(p) + 19) // 16) for p in prompts for _ in range(3)]
+    assert [(r >= 0).sum().item() for r in model.table[2:8]] == counts
+    held = int((model.pool.refs > 0).sum())
+    assert held == sum(counts) - 2 * (40 // 16)  # two full pages of the first prompt are shared by its three samples
+    assert model.pool.refs.sum().item() == sum(counts)
+    # the tokens so far as a prompt, anew: its last logits against those of the step that made the last token
+    again = ex.Model()
+    for b, p in ((0, 0), (4, 1)):
+        fresh = ex.Model()
+        logits = fresh.prompts([prompts[p] + out[b][:-1]])
+        again.prompts([prompts[p]])
+        for j, t in enumerate(out[b][:-1]):
+            last = again.step([0], [len(prompts[p]) + j], [t])
+        moe.pages_free(again.pool, again.table, i32([0]))
+        # both forms round to bf16 some twenty times on the way, 2^-8 each of values of the size of the logits' inputs; the
+        # logits are 4 times sums of 256 products
+        assert (logits - last).abs().max() <= 20 * ref.BF16 * 4 and torch.corrcoef(torch.stack([logits[0], last[0]]))[0, 1] > 0.99
