@@ -44,22 +44,23 @@ struct PromptArgs {
 
 __device__ uint32_t prompt_unasked;  // the status of calls that ask for none
 
-// tcgen05.mma by a whole warp, one lane of which issues it (see moe_latent_tc.cuh's)
-__device__ __forceinline__ void mma1_f16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate)
+// tcgen05.mma by a whole warp, one lane of which issues it (see moe_latent_tc.cuh's). Descriptors as the low word, where
+// the address is, and the high one, which stays.
+__device__ __forceinline__ void mma1_f16(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate)
 {
     asm volatile(
-        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xFFFFFFFF;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n .reg .pred p, e;\n .reg .b64 a, b;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n setp.ne.b32 p, %5, 0;\n"
+        " elect.sync _|e, 0xFFFFFFFF;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(tmem_d),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
 
-__device__ __forceinline__ void mma1_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc, bool accumulate)
+__device__ __forceinline__ void mma1_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate)
 {
     asm volatile(
-        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xFFFFFFFF;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
-        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n .reg .pred p, e;\n .reg .b64 b;\n mov.b64 b, {%2, %3};\n setp.ne.b32 p, %5, 0;\n"
+        " elect.sync _|e, 0xFFFFFFFF;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(tmem_d),
+        "r"(tmem_a), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
 
@@ -313,19 +314,22 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
         const uint32_t tm = __reduce_max_sync(0xFFFFFFFFu, tmem);  // (what the loops need is the same in all lanes)
         const int n = __reduce_max_sync(0xFFFFFFFFu, tiles), n0 = __reduce_max_sync(0xFFFFFFFFu, tiles0),
                   n1 = __reduce_max_sync(0xFFFFFFFFu, tiles1), e = __reduce_max_sync(0xFFFFFFFFu, edge);
-        const uint64_t qd = sw128_desc(sq), kd = sw128_desc(ring);
+        const uint64_t desc = sw128_desc(ring);
+        const uint32_t hi = (uint32_t)(desc >> 32), kd = (uint32_t)desc, qd = (uint32_t)sw128_desc(sq);
         // V: rows (one a token) of 64 dimensions, 8 rows 1024 bytes apart, the next 64 dimensions VT rows
-        const uint64_t vd = kd & ~(0x3FFFull << 16) | (uint64_t)(VT * 128 / 16) << 16;
+        const uint32_t vd = kd & ~(0x3FFFu << 16) | (uint32_t)(VT * 128 / 16) << 16;
         auto all = [&](bool v) { return __all_sync(0xFFFFFFFFu, v) != 0; };
         auto off = [&](int i) { return (uint32_t)((i & (MOE_PROMPT_PLACES - 1)) * PLACE) / 16; };
         bool ok = n == 0 || all(wait(q_full, 0));
         for (int u = 0; u <= n && ok && n > 0; ++u) {
-            const int at = u * (KC + VC), x = u & 1;
+            const int x = u & 1;
             ok = u == 0 || all(u - 1 < e ? wait(v_full + (x ^ 1), (u - 1) >> 1) : wait(v_clean + (u - 1 - e), 0));
             bool keys = false;
 #pragma unroll 1
             for (int g = 0; g < 2 && ok; ++g) {
                 const int last = g ? n1 : n0;
+                int at = u * (KC + VC);
+                asm volatile("" : "+r"(at));  // (addresses are made as the products go: ahead of them all, they hold them up)
                 if (u > 0 && u <= last) {
                     ok = all(wait(p_full + g, u - 1));
                     if (!ok)
@@ -334,7 +338,8 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
 #pragma unroll
                     for (int k = 0; k < 8; ++k)  // 16 tokens: 8 columns of P, 2048 bytes of V
                         mma1_f16_ts(tm + O_COL + g * 128, tm + S_COL + g * 128 + k * 8,
-                                    vd + off(at - VC + k * 16 / VT) + (uint32_t)(k * 16 % VT * 128) / 16, id_o, u > 1 || k > 0);
+                                    vd + off(at - VC + k * 16 / VT) + (uint32_t)(k * 16 % VT * 128) / 16, hi, id_o,
+                                    u > 1 || k > 0);
                     if (u == last)
                         mma1_commit(o_full + g);
                     if (g || u > n1)  // the last M tile's: before S's products, so that the copies wait no longer
@@ -353,7 +358,7 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             mma1_f16(tm + S_COL + g * 128, qd + (uint32_t)(g * Q_TILE + d * PLACE + k * 32) / 16,
-                                     kd + off(at + d) + k * 2, id_s, d + k > 0);
+                                     kd + off(at + d) + k * 2, hi, id_s, d + k > 0);
                     mma1_commit(s_full + g);
                 }
             }
