@@ -26,7 +26,8 @@ namespace moe {
 
 #define MOE_LTC_TOKENS 64
 #define MOE_LTC_ROWS 128   // of a pair
-#define MOE_LTC_COST 3     // of an item, beside its tiles
+#define MOE_LTC_COST 8     // of an item, beside its tiles (16 trees over 1000 to 16000 tokens: 80 us with 5, 78 with 8, 80 with 12;
+                           // 200 sequences of 1 to 2000, 64 heads: 95, 90 and 92)
 #define MOE_LTC_SOFT 4     // softmax warps
 #define MOE_LTC_THREADS ((MOE_LTC_SOFT + 5) * 32)
 #define MOE_LTC_MAX_STAGES 8
@@ -414,39 +415,45 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
         bool ok = true;
         int item = 0, s = 0, phase = 0;  // s, phase: the tile's stage and its phase
         uint32_t seen = 0;  // by x, a bit each: parity of the tiles looked through
-        TreeItem it{};
-        for (int u = 0; u < tiles; ++item) {
-            to_item(u, it);
+        // an item's queries, once the last item's S have been made (this warp has seen the last): asked for, and there
+        auto ask = [&](const TreeItem &i) {
+            const int first = i.block * ROWS + (int)rank * 64, here = min(64, i.n * t.group - first);
+            for (int r = warp; r < here; r += MOE_LTC_SOFT) {
+                const int token = i.first + (first + r) / t.group, head = (first + r) % t.group;
+                const uint16_t *q = t.q + token * t.q_tok + head * t.q_head, *qr = a.qr + token * a.qr_tok + head * a.qr_head;
+                uint8_t *to = sq + r * 128;
+#pragma unroll
+                for (int i = lane; i < T::CHUNKS * 8 + 8; i += 32) {
+                    const bool turning = i >= T::CHUNKS * 8;
+                    const int k = turning ? i - T::CHUNKS * 8 : i;
+                    uint4 *at = reinterpret_cast<uint4 *>(to + (i >> 3) * T::Q_CHUNK + (((i & 7) ^ (r & 7)) << 4));
+                    if (turning && k >= a.rope / 8)
+                        *at = make_uint4(0, 0, 0, 0);
+                    else if (turning ? a.qr_wide : t.q_wide)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(at)),
+                                     "l"((turning ? qr : q) + k * 8)
+                                     : "memory");
+                    else
+                        *at = latent_get((turning ? qr : q) + k * 8, false);
+                }
+            }
+        };
+        auto there = [&](int i) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                arrive_first(q_full + (i & 1));
+        };
+        TreeItem it{}, following{};
+        if (tiles > 0) {
+            to_item(0, it);
+            ask(it);
+            there(0);
+        }
+        for (int u = 0; u < tiles; ++item, it = following) {
             const int end = item_end(it), at = it.block * ROWS + mine, rows = it.n * t.group;
             const bool live = at < rows;
-            // ---- queries: the last item's S have been made (this warp has seen the last)
-            {
-                const int first = it.block * ROWS + (int)rank * 64, here = min(64, rows - first);
-                for (int r = warp; r < here; r += MOE_LTC_SOFT) {
-                    const int token = it.first + (first + r) / t.group, head = (first + r) % t.group;
-                    const uint16_t *q = t.q + token * t.q_tok + head * t.q_head, *qr = a.qr + token * a.qr_tok + head * a.qr_head;
-                    uint8_t *to = sq + r * 128;
-#pragma unroll
-                    for (int i = lane; i < T::CHUNKS * 8 + 8; i += 32) {
-                        const bool turning = i >= T::CHUNKS * 8;
-                        const int k = turning ? i - T::CHUNKS * 8 : i;
-                        uint4 *at = reinterpret_cast<uint4 *>(to + (i >> 3) * T::Q_CHUNK + (((i & 7) ^ (r & 7)) << 4));
-                        if (turning && k >= a.rope / 8)
-                            *at = make_uint4(0, 0, 0, 0);
-                        else if (turning ? a.qr_wide : t.q_wide)
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(at)),
-                                         "l"((turning ? qr : q) + k * 8)
-                                         : "memory");
-                        else
-                            *at = latent_get((turning ? qr : q) + k * 8, false);
-                    }
-                }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    arrive_first(q_full + (item & 1));
-            }
             const int node = live ? at / t.group : 0;
             // the drafted tokens that it sees
             const unsigned long long mask = !live ? 0 : (t.mask ? t.mask[it.first + node] : (2ull << node) - 1) &
@@ -565,10 +572,17 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                     ++phase;
                 }
             }
-            // ---- the item's end
+            // ---- the item's end. The next one's queries first, so that its S are made under it
+            following = it;
+            if (u < tiles) {
+                to_item(u, following);
+                ask(following);
+            }
             float *sums = top_of + (end & 1) * 128;  // (the maxima that the last tile has not used)
             sums[half * 64 + row] = l;
             ok = ok && wait(pv_done + ((end - 1) & 1), (end - 1) >> 1);
+            if (u < tiles)
+                there(item + 1);
             meet();
             __syncwarp();
             l += sums[(half ^ 1) * 64 + row];
