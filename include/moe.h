@@ -645,7 +645,8 @@ int moe_rope(const void *x_dev, int64_t x_token_stride, int64_t x_head_stride, v
 
 /* A cache of one layer's latent vectors: n_pages pages of page_size rows
  * (tokens), a row latent_dim + rope_dim bf16 values, the latent vector and the
- * part of the key that turns; slot s is row s. pages: device memory, 16-byte
+ * part of the key that turns; slot s is row s, token s % page_size of page s /
+ * page_size. pages: device memory, 16-byte
  * aligned, n_pages * moe_latent_page_bytes bytes. latent_dim 128, 256 or 512;
  * rope_dim a multiple of 8 from 8 to 64; page_size a multiple of 16 up to 1024;
  * n_pages * page_size below 2^31. */
@@ -713,8 +714,11 @@ int moe_latent_attention(const moe_latent_cache *cache, const void *q_dev, int64
  * in elements. A row that sees nothing gives 0 (a causal one of a sequence with
  * fewer tokens than rows); a NaN or infinity in a token that a row does not see
  * does not reach it. Products as for moe_latent_attention. nope_dim 64 or 128,
- * rope_dim a multiple of 8 from 8 to 64, heads 1 .. 1024, batch 0 .. 1024. k, kr
- * and v must start on 16-byte boundaries and have strides of multiples of 8.
+ * rope_dim a multiple of 8 from 8 to 64, heads 1 .. 1024, batch 0 .. 1024,
+ * q_tokens up to 2^23, kv_tokens up to 2^30. k, kr and v must start on 16-byte
+ * boundaries and have strides of multiples of 8, those of tokens positive, those
+ * of heads positive or 0 (keys, values that all heads share). Rows that no
+ * sequence has are not written.
  * *status_dev receives MOE_WS_INDEX where q_start or kv_start fall or lie
  * outside q_tokens or kv_tokens (the sequence's rows within q_tokens are 0), and
  * MOE_WS_TIMEOUT. */
@@ -740,8 +744,9 @@ typedef struct {
     int32_t page_size;
 } moe_page_pool;
 
-/* Gives each row a page for every entry below ceil(len_dev[row] / page_size)
- * that is -1. */
+/* Gives each row a page for every entry from its first -1 on and below
+ * ceil(len_dev[row] / page_size) (i32 [rows]; a row's pages come before its -1
+ * entries, as these calls leave them). */
 int moe_pages_grow(const moe_page_pool *pool, int32_t *table_dev, int64_t table_stride, int table_pages, int rows,
                    const int32_t *len_dev, uint32_t *status_dev, moe_stream_t stream);
 
