@@ -782,7 +782,8 @@ int moe_pages_compact(const moe_page_pool *pool, const int32_t *table_dev, int64
  * to copies_dev[i, 1], i < n or, where n_copies_dev is not NULL, below that count
  * too. A negative pair is passed over; one outside the cache too, and sets
  * MOE_WS_INDEX. No page may be copied to twice, or be copied both from and to.
- * pages_dev, layer_stride and page_bytes multiples of 16. */
+ * pages_dev, layer_stride (n_pages * page_bytes at least) and page_bytes multiples
+ * of 16. */
 int moe_pages_copy(void *pages_dev, int64_t layer_stride, int layers, int64_t n_pages, int64_t page_bytes,
                    const int32_t *copies_dev, int n, const int32_t *n_copies_dev, uint32_t *status_dev,
                    moe_stream_t stream);

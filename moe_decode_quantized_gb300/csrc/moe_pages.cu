@@ -140,10 +140,11 @@ int moe_pages_copy(void *pages_dev, int64_t layer_stride, int layers, int64_t n_
         return host_fail(MOE_EINVAL, "moe_pages_copy: NULL argument");
     if (!aligned(pages_dev, 16) || page_bytes % 16 || (layers > 1 && layer_stride % 16))
         return host_fail(MOE_EINVAL, "moe_pages_copy: pages, layer_stride and page_bytes must be multiples of 16");
-    if (layers > 1 && layer_stride < 0)
-        return host_fail(MOE_EINVAL, "moe_pages_copy: layer_stride (%lld) < 0", (long long)layer_stride);
     if (page_bytes > 1ll << 32)
         return host_fail(MOE_EUNSUPPORTED, "moe_pages_copy: page_bytes (%lld) <= 2^32", (long long)page_bytes);
+    if (layers > 1 && (layer_stride < 0 || layer_stride / page_bytes < n_pages))
+        return host_fail(MOE_EINVAL, "moe_pages_copy: layer_stride (%lld) is below n_pages (%lld) pages of %lld bytes",
+                         (long long)layer_stride, (long long)n_pages, (long long)page_bytes);
     if (!aligned(copies_dev, 4) || !aligned(n_copies_dev, 4) || !aligned(status_dev, 4))
         return host_fail(MOE_EINVAL, "moe_pages_copy: an argument is not aligned to its type");
     CopyArgs a{};

@@ -216,7 +216,8 @@ def test_pages_copy_refusals():
         return L.moe_pages_copy(pages, stride, layers, n_pages, per, copies, n, None, None, None)
 
     for kw in (dict(n=-1), dict(layers=-1), dict(n_pages=0), dict(per=0), dict(pages=None), dict(copies=None), dict(pages=ADDR + 8),
-               dict(per=24), dict(stride=8), dict(stride=-16), dict(copies=ADDR + 2)):
+               dict(per=24), dict(stride=8), dict(stride=-16), dict(copies=ADDR + 2),
+               dict(stride=4 * 4096 - 16), dict(stride=4096), dict(stride=0)):  # layers that overlap
         assert copy(**kw) == -1, kw
     assert copy(per=(1 << 32) + 16) == -2
     assert copy(n=0, pages=None) == 0 and copy(layers=0, pages=None) == 0
