@@ -54,8 +54,9 @@ int latent_rows(bool read, LatentRows &a, const moe_latent_cache *cache, moe_str
     a.rope = cache->rope_dim;
     a.c_wide = wide_rows(a.c, a.c_stride, 0);
     a.kr_wide = wide_rows(a.kr, a.kr_stride, 0);
-    const long long pieces = (long long)a.tokens * (a.latent / 8);
-    const dim3 grid((unsigned)((pieces + MOE_LATENT_PIECES * MOE_LATENT_THREADS - 1) / (MOE_LATENT_PIECES * MOE_LATENT_THREADS)), 2);
+    const long long per = MOE_LATENT_PIECES * MOE_LATENT_THREADS, n = a.tokens;
+    a.c_blocks = (unsigned)((n * (a.latent / 8) + per - 1) / per);
+    const dim3 grid(a.c_blocks + (unsigned)((n * (a.rope / 8) + per - 1) / per));
     MOE_CUDA_OK(launch(read ? moe_latent_rows_kernel<true> : moe_latent_rows_kernel<false>, grid, MOE_LATENT_THREADS, 0,
                        stream, a));
     return MOE_OK;
@@ -266,7 +267,8 @@ int moe_rope(const void *x_dev, int64_t x_token_stride, int64_t x_head_stride, v
     a.turned = wide ? (inter ? rope_dim : rope_dim / 2) / v : rope_dim / 2;
     a.items = a.turned + (in_place ? 0 : (head_dim - rope_dim) / (wide ? v : 1));
     a.heads_cta = std::min(heads, MOE_ROPE_HEADS);
-    // a CTA some 2048 pieces, and every SM a few CTAs
+    // a CTA some 2048 pieces (16384 tokens of 32 heads in bf16 and 4099 of 12 in f32: 67.2 and 10.9 us; 1024: 75.9 and 14.2;
+    // 4096: 67.1 and 12.0), and every SM a few CTAs
     const long long per = (long long)a.heads_cta * a.items;
     a.tokens_cta = (int)std::max(1ll, std::min({2048 / per, tokens / 608ll, MOE_ROPE_SMEM / (4ll * rope_dim)}));
     const dim3 grid((unsigned)((tokens + a.tokens_cta - 1) / a.tokens_cta),
