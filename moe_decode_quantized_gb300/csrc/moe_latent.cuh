@@ -1,9 +1,8 @@
 // moe_latent.cuh -- the paged cache of latent vectors: rows written (the key's
 // turning part rotated on its way) and read back. A row is latent_dim + rope_dim
 // bf16 values, moved in pieces of 16 bytes: bound by bytes, and by the wait for
-// a slot before a row can be moved. Hence four pieces a thread in flight: 65536
-// rows of 512 + 64 values are written and read back in 56.4 us, 45 at the copy
-// rate.
+// a slot before a row can be moved: 65536 rows of 512 + 64 values are written and
+// read back in 54.3 us, 45 at the copy rate.
 #pragma once
 #include "moe_rope.cuh"
 
@@ -67,7 +66,7 @@ __device__ __forceinline__ uint16_t *latent_row(const LatentRows &a, int token)
     return nullptr;
 }
 
-#define MOE_LATENT_PIECES 4  // of a thread, in flight together
+#define MOE_LATENT_PIECES 2  // of a thread, in flight together (the calls above with 1: 60.9 us, 4: 55.8, 8: 72.4)
 
 // One piece of a key part on its way into the cache: turned
 __device__ __forceinline__ uint4 latent_turned(const LatentRows &a, int token, int piece, const uint16_t *row, uint4 v)
