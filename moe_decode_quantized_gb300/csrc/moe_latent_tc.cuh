@@ -17,6 +17,16 @@
 // rows with the second.
 //
 // Items, runs and partials are those of moe_tree_attn.cuh, a run a pair.
+//
+// Bound by products and by bytes nearly alike at 128 heads (242 FLOP a byte), by
+// bytes below that, by two launches' latency for one short sequence. One token of
+// 64 sequences over 4000 to 24000 tokens, latent vectors of 512: 128 heads 194 us
+// (139 at the copy rate, 117 at the products'), 16 heads 180 (5.2 TB/s: the tiles take as long, rows or not); 16
+// trees of 8 rows, 32 heads, over up to 16000: 78; one sequence of 511: 14.7. A
+// tile of 128 rows takes some 1900 clocks, of which its products need 1160: its
+// second product waits for its softmax, and two S beside O's columns are what
+// tensor memory has room for. Tiles of 64 tokens leave room for four stages,
+// which is what the copies' latency needs; 8 softmax warps gained nothing over 4.
 #pragma once
 #include "moe_latent.cuh"
 #include "moe_tc.cuh"
