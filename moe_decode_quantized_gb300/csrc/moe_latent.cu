@@ -268,7 +268,8 @@ int moe_rope(const void *x_dev, int64_t x_token_stride, int64_t x_head_stride, v
     a.items = a.turned + (in_place ? 0 : (head_dim - rope_dim) / (wide ? v : 1));
     a.heads_cta = std::min(heads, MOE_ROPE_HEADS);
     // a CTA some 2048 pieces (16384 tokens of 32 heads in bf16 and 4099 of 12 in f32: 67.2 and 10.9 us; 1024: 75.9 and 14.2;
-    // 4096: 67.1 and 12.0), and every SM a few CTAs
+    // 4096: 67.1 and 12.0), but four CTAs an SM first (8 tokens of 40 heads in a graph 2.1 us, else 4.7; 2000 of one head 2.1
+    // and 5.3)
     const long long per = (long long)a.heads_cta * a.items;
     a.tokens_cta = (int)std::max(1ll, std::min({2048 / per, tokens / 608ll, MOE_ROPE_SMEM / (4ll * rope_dim)}));
     const dim3 grid((unsigned)((tokens + a.tokens_cta - 1) / a.tokens_cta),
@@ -549,7 +550,10 @@ int moe_latent_prompt_attention(const void *q_dev, int64_t q_token_stride, int64
     if ((rc = prompt_device()))
         return rc;
     const size_t shared = (2 * (nope_dim / 64 + 1) + MOE_PROMPT_PLACES) * (size_t)MOE_PROMPT_PLACE + MOE_PROMPT_SMALL;
-    const dim3 grid((unsigned)heads, (unsigned)(q_tokens / MOE_PROMPT_ROWS + batch));
+    // one M tile a CTA where the SMs are enough for that (512 rows of 32 heads after 16000 tokens: 216 us, with two a CTA 252;
+    // 1024 of 16 after 8000: 125 and 145); beyond, two pass faster than one after the other
+    a.block = (long long)heads * ((q_tokens + 127) / 128) <= 152 ? MOE_PROMPT_ROWS / 2 : MOE_PROMPT_ROWS;
+    const dim3 grid((unsigned)heads, (unsigned)(q_tokens / a.block + batch));
     MOE_CUDA_OK(launch(nope_dim == 64 ? moe_prompt_kernel<64> : moe_prompt_kernel<128>, grid, MOE_PROMPT_THREADS, shared, stream, a));
     return MOE_OK;
 }

@@ -699,6 +699,30 @@ def test_values_of_seen_tokens_that_are_not_finite():
     assert torch.isfinite(out[:, [0, 1, 2, 3, 4, 6, 8] + list(range(10, 128))]).all()
 
 
+@pytest.mark.parametrize("nope,rope", [(128, 64), (64, 24)])
+@pytest.mark.parametrize("heads,q,kv", [(31, [300, 2, 255], [300, 700, 400]), (31, [513], [640]), (52, [129, 131], [130, 128])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_of_many_heads(nope, rope, heads, q, kv, causal):
+    """Too many for a CTA to every 128 rows: one to 256."""
+    p = Prompt(nope, rope, heads, q, kv, causal, seed=sum(kv) + heads)
+    p.out.fill_(9.0)
+    p.run(0.09)
+    p.check(0.09)
+
+
+def test_values_that_are_not_finite_in_prompts_of_many_heads():
+    p = Prompt(128, 64, 52, [300], [300], seed=47)
+    p.v[10, :, 5] = float("inf")
+    p.v[150, :, 7] = float("nan")
+    p.v[290, :, 9] = -float("inf")
+    p.run(0.05)
+    out = p.out.double().cpu()
+    assert (out[10:, :, 5] == math.inf).all() and torch.isfinite(out[:10]).all()
+    assert torch.isnan(out[150:, :, 7]).all() and torch.isfinite(out[:150, :, 7]).all()
+    assert (out[290:, :, 9] == -math.inf).all() and torch.isfinite(out[:290, :, 9]).all()
+    assert torch.isfinite(out[..., [0, 1, 2, 3, 4, 6, 8] + list(range(10, 128))]).all()
+
+
 def test_rope_and_rows_in_a_graph():
     g = torch.Generator().manual_seed(46)
     x, c = torch.randn((9, 4, 64), generator=g).bfloat16().cuda(), torch.randn((9, 144), generator=g).bfloat16().cuda()
