@@ -550,11 +550,31 @@ int moe_latent_prompt_attention(const void *q_dev, int64_t q_token_stride, int64
     if ((rc = prompt_device()))
         return rc;
     const size_t shared = (2 * (nope_dim / 64 + 1) + MOE_PROMPT_PLACES) * (size_t)MOE_PROMPT_PLACE + MOE_PROMPT_SMALL;
-    // one M tile a CTA where the SMs are enough for that (512 rows of 32 heads after 16000 tokens: 216 us, with two a CTA 252;
-    // 1024 of 16 after 8000: 125 and 145); beyond, two pass faster than one after the other
-    a.block = (long long)heads * ((q_tokens + 127) / 128) <= 152 ? MOE_PROMPT_ROWS / 2 : MOE_PROMPT_ROWS;
-    const dim3 grid((unsigned)heads, (unsigned)(q_tokens / a.block + batch));
-    MOE_CUDA_OK(launch(nope_dim == 64 ? moe_prompt_kernel<64> : moe_prompt_kernel<128>, grid, MOE_PROMPT_THREADS, shared, stream, a));
+    // Where blocks are few, clusters share each one's tokens, as many CTAs as run at once (128 rows of 4 heads after 30000
+    // tokens: 63 us, by a CTA a block 385; 512 of 32 after 16000: 139 and 252); but parts of two tiles at least, and of 6
+    // where a CTA to every 128 rows does instead (512 rows of 16 heads, no tokens before: 15 us, shared out 19; 2048 of 8: 34
+    // and 30.5): so too where the SMs are enough for that alone (1024 rows of 16: 22 us, 26 with 256 a CTA).
+    const long long blocks = (long long)heads * std::max((q_tokens + MOE_PROMPT_ROWS - 1) / MOE_PROMPT_ROWS, std::min(batch, q_tokens));
+    const int least = (q_tokens <= (long long)batch * (MOE_PROMPT_ROWS / 2) ? 2 : 6) * MOE_PROMPT_TOKENS;
+    a.split = 1;
+    while (blocks * a.split * 2 <= 152 && a.split * 2 <= std::min(MOE_PROMPT_SPLIT, nope_dim / 16) &&
+           kv_tokens >= (long long)batch * a.split * 2 * least)
+        a.split *= 2;
+    a.block = a.split == 1 && (long long)heads * ((q_tokens + 127) / 128) <= 152 ? MOE_PROMPT_ROWS / 2 : MOE_PROMPT_ROWS;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3((unsigned)(heads * a.split), (unsigned)(q_tokens / a.block + batch));
+    lc.blockDim = dim3(MOE_PROMPT_THREADS);
+    lc.dynamicSmemBytes = shared;
+    lc.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = a.split;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    lc.attrs = at;
+    lc.numAttrs = a.split > 1 ? 2 : 1;
+    MOE_CUDA_OK(cudaLaunchKernelEx(&lc, nope_dim == 64 ? moe_prompt_kernel<64> : moe_prompt_kernel<128>, a));
     return MOE_OK;
 }
 

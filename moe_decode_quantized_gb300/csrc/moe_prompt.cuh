@@ -16,6 +16,9 @@
 // hold anything: their scores are taken out, their values that are not finite
 // are zeros in the product, and are added at the end to the rows that see them.
 //
+// Where blocks are few, a cluster of CTAs shares one's tokens; their O, references
+// and sums meet in shared memory, each CTA adding up some dimensions, in order.
+//
 // Bound by products. 8192 tokens of 32 heads, 128 + 64 dimensions, causal: 494 us,
 // 1.39 PFLOP/s (74 % of the rate that was measured for large products). One warp issues all
 // products, in the order in which their operands come to be: by two, one an M
@@ -26,6 +29,7 @@
 #include "moe_latent.cuh"
 #include "moe_tc.cuh"
 #include "moe_tree_attn.cuh"
+#include "moe_verify.cuh"
 
 namespace moe {
 
@@ -35,6 +39,7 @@ namespace moe {
 #define MOE_PROMPT_THREADS ((MOE_PROMPT_SOFT + 2) * 32)
 #define MOE_PROMPT_PLACE 16384
 #define MOE_PROMPT_PLACES 8
+#define MOE_PROMPT_SPLIT 8     // CTAs that share a block's tokens at most
 #define MOE_PROMPT_SLACK 8.0f  // m moves when an exponent passes it by this
 
 struct PromptArgs {
@@ -45,6 +50,7 @@ struct PromptArgs {
     int batch, rope, q_tokens, kv_tokens, causal, q_wide, o_wide;
     int one_k, one_v;  // heads share their keys (values)
     int block;         // query rows of a CTA: MOE_PROMPT_ROWS, or half
+    int split;         // CTAs (a cluster) that share a block's tokens
     float scale;
     uint32_t *status;
     unsigned long long wait_ns;
@@ -181,6 +187,48 @@ static __device__ __noinline__ void prompt_add(const PromptArgs &a, float (&o)[1
         }
 }
 
+// 16 dimensions of an output row
+__device__ __forceinline__ void prompt_put(uint16_t *to, const float (&o)[16], float by, int o_wide)
+{
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 16; i += 2)
+        w[i / 2] = pack_bf2(o[i] * by, o[i + 1] * by);
+    if (o_wide == 2) {
+        put8(to, w);
+    } else {
+        latent_put(to, make_uint4(w[0], w[1], w[2], w[3]), o_wide);
+        latent_put(to + 8, make_uint4(w[4], w[5], w[6], w[7]), o_wide);
+    }
+}
+
+// a part's share of a sum: what is not finite stays, whatever its weight
+__device__ __forceinline__ float prompt_part(float o, float by)
+{
+    return by > 0.0f || fabsf(o) <= 3.402823466e38f ? o * by : o;
+}
+
+// shared memory of CTA `of` of the cluster, at the place of p
+__device__ __forceinline__ float4 peer_get4(const void *p, int of)
+{
+    float4 v;
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}\n"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(smem_u32(p)), "r"(of)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float2 peer_get2(const void *p, int of)
+{
+    float2 v;
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %2, %3;\n ld.shared::cluster.v2.f32 {%0, %1}, [a];\n}\n"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(smem_u32(p)), "r"(of)
+                 : "memory");
+    return v;
+}
+
 template <int D>
 __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const __grid_constant__ PromptArgs a)
 {
@@ -199,7 +247,8 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 22);
     uint32_t *bad = tmem_slot + 1;  // [3][4] tokens of the tiles that are looked through with values that are not finite
     int *scan = reinterpret_cast<int *>(bad + 12), *found = scan + 33;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, split = a.split;
+    const int head = blockIdx.x / split, part = blockIdx.x - head * split;  // (split CTAs are a cluster)
     uint32_t *status = a.status ? a.status : &prompt_unasked;
 
     if (tid == 0) {
@@ -222,7 +271,7 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
         bad[tid] = 0;
     pdl_wait();  // before tensor memory is taken: the last kernel may still need it
     // (the last blocks first: a sequence's later rows see more)
-    const PromptBlock b = prompt_block(a, gridDim.y - 1 - blockIdx.y, scan, found, status);
+    PromptBlock b = prompt_block(a, gridDim.y - 1 - blockIdx.y, scan, found, status);
     if (b.q1 <= b.q0)
         return;
     if (!b.held) {
@@ -231,8 +280,16 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
         return;
     }
     const int rows = b.q1 - b.q0;
-    // tokens that row i of the block sees
-    auto sees = [&](int i) { return a.causal ? max(0, min(b.t, b.t - b.n + b.row + i + 1)) : b.t; };
+    // tokens that row i of the block sees, of this CTA's part of them
+    int from = 0, len = b.t;
+    auto sees = [&](int i) { return max(0, min(len, (a.causal ? min(b.t, b.t - b.n + b.row + i + 1) : b.t) - from)); };
+    if (split > 1) {
+        const int all = (sees(rows - 1) + TOKENS - 1) / TOKENS, end = all * (part + 1) / split;
+        const int begin = all * part / split * TOKENS;
+        len = max(0, min(b.t, end * TOKENS) - begin);
+        from = begin;
+    }
+    b.k0 += from;
     // tiles of each M tile, and the first that not all rows see whole
     const int tiles0 = (sees(min(rows, 128) - 1) + TOKENS - 1) / TOKENS, tiles1 = rows > 128 ? (sees(rows - 1) + TOKENS - 1) / TOKENS : 0;
     const int tiles = max(tiles0, tiles1), edge = sees(0) / TOKENS;
@@ -255,8 +312,18 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
                tree_wait_on(bar, (uint32_t)phase & 1u, status, a.wait_ns);
     };
     auto drain = [&](uint64_t *bar, int phase) { tree_wait_on(bar, (uint32_t)phase & 1u, status, max(a.wait_ns, MOE_TREE_DRAIN_NS)); };
+    auto get_o = [&](float (&o)[16], uint32_t at, int n) {
+        if (n > 0) {
+            tmem_ld16(at, o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                o[i] = 0.0f;
+        }
+    };
     auto place = [&](int i) { return ring + (i & (MOE_PROMPT_PLACES - 1)) * PLACE; };
 
+    float m_end = -INFINITY, l_end = 0.0f;
     if (warp < MOE_PROMPT_SOFT && tiles > 0 && !a.q_wide) {
         // ---------------- queries that TMA does not take
         constexpr int PIECES = D / 8 + 8;
@@ -401,11 +468,11 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
                 for (int i = u < other ? tid : tid & 127; i < TOKENS * D / 8; i += step) {
                     const int token = i / (D / 8), piece = i % (D / 8);
                     uint4 *p = reinterpret_cast<uint4 *>(place(at + token / VT) + (piece >> 3) * VT * 128 + token % VT * 128 + (piece & 7) * 16);
-                    const uint4 v = *p, w = u * TOKENS + token >= b.t ? make_uint4(0, 0, 0, 0)
+                    const uint4 v = *p, w = u * TOKENS + token >= len ? make_uint4(0, 0, 0, 0)
                                                                       : make_uint4(finite_bf2(v.x), finite_bf2(v.y), finite_bf2(v.z), finite_bf2(v.w));
                     if (v.x != w.x || v.y != w.y || v.z != w.z || v.w != w.w) {
                         *p = w;
-                        if (u * TOKENS + token < b.t)
+                        if (u * TOKENS + token < len)
                             atomicOr(bad + (u - edge) * 4 + (token >> 5), 1u << (token & 31));
                     }
                 }
@@ -503,36 +570,93 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
             ok = ok && wait(o_full + g, 0);
         __syncwarp();
         tc_fence_after();
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint16_t *to = a.out + (long long)(b.q0 + mine) * a.o_tok + head * a.o_head;
-        uint32_t any = 0;  // values that are not finite
-        for (int w = 0; w < 12; ++w)
-            any |= *reinterpret_cast<volatile uint32_t *>(bad + w);
+        m_end = m;
+        l_end = l;
+        if (split == 1) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            uint16_t *to = a.out + (long long)(b.q0 + mine) * a.o_tok + head * a.o_head;
+            uint32_t any = 0;  // values that are not finite
+            for (int w = 0; w < 12; ++w)
+                any |= *reinterpret_cast<volatile uint32_t *>(bad + w);
 #pragma unroll 1
-        for (int k = 0; k < D && mine - lane < rows; k += 16) {
-            float o[16];
-            if (n > 0) {
-                tmem_ld16(o_at + k, o);
-            } else {
+            for (int k = 0; k < D && mine - lane < rows; k += 16) {
+                float o[16];
+                get_o(o, o_at + k, n);
+                if (any)
+                    prompt_add(a, o, bad, edge, most, b.k0, head, k);
+                if (live)
+                    prompt_put(to + k, o, inv, a.o_wide);
+            }
+        }
+    }
+    if (split > 1) {
+        // ---------------- the parts of a block joined: each CTA's O, references and sums into its shared memory, where
+        // products and copies have ended; then each CTA some dimensions of all rows, the parts in order
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        float4 *kept = reinterpret_cast<float4 *>(smem_prompt);  // [D / 4][256]
+        float2 *ends = reinterpret_cast<float2 *>(smem_prompt + 256 * D * 4);
+        const int row = tid & 255;
+        const bool live = warp < MOE_PROMPT_SOFT && row < rows;
+        if (warp < MOE_PROMPT_SOFT && row - lane < rows) {
+            const int g = warp >> 2, n = g ? tiles1 : tiles0, most = live ? sees(row) : 0;
+            const uint32_t o_at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + O_COL + g * 128;
+            uint32_t any = 0;
+            for (int w = 0; w < 12; ++w)
+                any |= *reinterpret_cast<volatile uint32_t *>(bad + w);
+#pragma unroll 1
+            for (int k = 0; k < D; k += 16) {
+                float o[16];
+                get_o(o, o_at + k, n);
+                if (any)
+                    prompt_add(a, o, bad, edge, most, b.k0, head, k);
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    kept[(k + i) / 4 * 256 + row] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
+            ends[row] = make_float2(m_end, l_end);
+        }
+        __syncwarp();
+        cluster_sync();
+        if (live) {
+            const float scaled = fminf(fabsf(a.scale) * 1.4426950408889634f, 3.0e38f), c = scaled == 0.0f ? 1.0f : scaled;
+            float m = -INFINITY, l = 0.0f, by[MOE_PROMPT_SPLIT];
+#pragma unroll
+            for (int i = 0; i < MOE_PROMPT_SPLIT; ++i)
+                if (i < split)
+                    m = fmaxf(m, peer_get2(ends + row, i).x);
+#pragma unroll
+            for (int i = 0; i < MOE_PROMPT_SPLIT; ++i)
+                if (i < split) {
+                    const float2 e = peer_get2(ends + row, i);
+                    by[i] = e.x == -INFINITY ? 1.0f : ex2((e.x - m) * c);  // a NaN sum stays
+                    l += e.y * by[i];
+                }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            uint16_t *to = a.out + (long long)(b.q0 + row) * a.o_tok + head * a.o_head;
+#pragma unroll 1
+            for (int k = D / split * part; k < D / split * (part + 1); k += 16) {
+                float o[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     o[i] = 0.0f;
-            }
-            if (any)
-                prompt_add(a, o, bad, edge, most, b.k0, head, k);
-            if (!live)
-                continue;
-            uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 16; i += 2)
-                w[i / 2] = pack_bf2(o[i] * inv, o[i + 1] * inv);
-            if (a.o_wide == 2) {
-                put8(to + k, w);
-            } else {
-                latent_put(to + k, make_uint4(w[0], w[1], w[2], w[3]), a.o_wide);
-                latent_put(to + k + 8, make_uint4(w[4], w[5], w[6], w[7]), a.o_wide);
+                for (int x = 0; x < MOE_PROMPT_SPLIT; ++x)
+                    if (x < split)
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 v = peer_get4(kept + (k + i) / 4 * 256 + row, x);
+                            o[i] += prompt_part(v.x, by[x]);
+                            o[i + 1] += prompt_part(v.y, by[x]);
+                            o[i + 2] += prompt_part(v.z, by[x]);
+                            o[i + 3] += prompt_part(v.w, by[x]);
+                        }
+                prompt_put(to + k, o, inv, a.o_wide);
             }
         }
+        __syncwarp();
+        cluster_sync();  // (no CTA's shared memory goes while it is read)
     }
     tc_fence_before();
     __syncthreads();

@@ -723,6 +723,57 @@ def test_values_that_are_not_finite_in_prompts_of_many_heads():
     assert torch.isfinite(out[..., [0, 1, 2, 3, 4, 6, 8] + list(range(10, 128))]).all()
 
 
+@pytest.mark.parametrize("nope,rope", [(128, 64), (64, 40)])
+@pytest.mark.parametrize("heads,q,kv", [(1, [40], [5000]), (2, [1, 300, 0], [3000, 2001, 600]), (9, [513], [4097]),
+                                        (1, [3200], [3200]), (3, [128, 90], [1030, 60])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_whose_tokens_are_shared_out(nope, rope, heads, q, kv, causal):
+    """Few blocks of rows: several CTAs to each, a part of its tokens each (none, for rows that see few)."""
+    p = Prompt(nope, rope, heads, q, kv, causal, seed=sum(kv) + heads)
+    p.out.fill_(9.0)
+    p.run(0.09)
+    p.check(0.09)
+
+
+def test_shared_out_tokens_that_are_not_finite():
+    p = Prompt(128, 64, 1, [300], [4000], seed=48)
+    p.v[10, 0, 5] = float("inf")
+    p.v[3850, 0, 7] = float("nan")
+    p.v[3990, 0, 9] = -float("inf")
+    p.run(0.05)
+    out = p.out[:, 0].double().cpu()  # row i sees tokens 0 .. 3700 + i
+    assert (out[:, 5] == math.inf).all()
+    assert torch.isnan(out[150:, 7]).all() and torch.isfinite(out[:150, 7]).all()
+    assert (out[290:, 9] == -math.inf).all() and torch.isfinite(out[:290, 9]).all()
+    assert torch.isfinite(out[:, [0, 1, 2, 3, 4, 6, 8] + list(range(10, 128))]).all()
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 30.0])
+def test_shared_out_scales(scale):
+    """Scores far apart, so that parts weigh nothing beside others."""
+    p = Prompt(64, 64, 2, [140, 3], [2000, 3000], seed=49)
+    p.run(scale)
+    p.check(scale)
+
+
+def test_shared_out_tokens_in_a_graph():
+    p = Prompt(128, 64, 2, [200, 80], [3000, 1080], seed=50)
+    p.run(0.1)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            p.run(0.1)
+    p.q.neg_()
+    p.n, p.t = [100, 180], [180, 3900]
+    p.q_start.copy_(i32([0, 100, 280]))
+    p.kv_start.copy_(i32([0, 180, 4080]))
+    for _ in range(3):
+        p.out.fill_(5.0)
+        g.replay()
+        p.check(0.1)
+
+
 def test_rope_and_rows_in_a_graph():
     g = torch.Generator().manual_seed(46)
     x, c = torch.randn((9, 4, 64), generator=g).bfloat16().cuda(), torch.randn((9, 144), generator=g).bfloat16().cuda()
