@@ -718,7 +718,9 @@ int moe_latent_attention(const moe_latent_cache *cache, const void *q_dev, int64
  * q_tokens up to 2^23, kv_tokens up to 2^30. k, kr and v must start on 16-byte
  * boundaries and have strides of multiples of 8, those of tokens positive, those
  * of heads positive or 0 (keys, values that all heads share). Rows that no
- * sequence has are not written.
+ * sequence has are not written. The order in which a row's products are added up
+ * goes by heads, batch, q_tokens, kv_tokens and nope_dim, never by timing: the
+ * same call gives the same bits, another batch around a sequence need not.
  * *status_dev receives MOE_WS_INDEX where q_start or kv_start fall or lie
  * outside q_tokens or kv_tokens (the sequence's rows within q_tokens are 0), and
  * MOE_WS_TIMEOUT. */
