@@ -721,9 +721,10 @@ int moe_latent_attention(const moe_latent_cache *cache, const void *q_dev, int64
  * sequence has are not written. The order in which a row's products are added up
  * goes by heads, batch, q_tokens, kv_tokens and nope_dim, never by timing: the
  * same call gives the same bits, another batch around a sequence need not.
- * *status_dev receives MOE_WS_INDEX where q_start or kv_start fall or lie
- * outside q_tokens or kv_tokens (the sequence's rows within q_tokens are 0), and
- * MOE_WS_TIMEOUT. */
+ * *status_dev receives MOE_WS_INDEX where a sequence's q_start or kv_start fall
+ * or lie outside q_tokens or kv_tokens, or its q_start lies before an earlier
+ * sequence's (its rows within q_tokens are 0, but those that are a sequence's
+ * whose starts hold), and MOE_WS_TIMEOUT. */
 int moe_latent_prompt_attention(const void *q_dev, int64_t q_token_stride, int64_t q_head_stride, const void *k_dev,
                                 int64_t k_token_stride, int64_t k_head_stride, const void *kr_dev, int64_t kr_stride,
                                 const void *v_dev, int64_t v_token_stride, int64_t v_head_stride, void *out_dev,

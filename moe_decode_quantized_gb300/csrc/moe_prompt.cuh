@@ -86,39 +86,75 @@ __device__ __forceinline__ void mma1_commit(uint64_t *bar)
                  : "memory");
 }
 
-// block `at` of the call's row blocks, those of the sequences in order (of a sequence whose starts do not hold, of its
-// rows that lie in the call); q1 <= q0: there is no such block
+// block `at` of the call's row blocks, those of the sequences that hold, in order; q1 <= q0: there is no such block
 struct PromptBlock {
     int q0, q1, row, k0, t, n;  // query rows [q0, q1) of the call, the first's place in the sequence; tokens [k0, k0 + t)
-    bool held;
 };
 
-// whether a sequence's starts hold
+// whether a sequence's own starts hold
 __device__ __forceinline__ bool prompt_held(const PromptArgs &a, int b)
 {
     const int q0 = a.q_start[b], q1 = a.q_start[b + 1], k0 = a.kv_start[b], k1 = a.kv_start[b + 1];
     return q0 >= 0 && q1 >= q0 && q1 <= a.q_tokens && k0 >= 0 && k1 >= k0 && k1 <= a.kv_tokens;
 }
 
-// whole CTA: found [3] and scan [33] in shared memory
-__device__ __forceinline__ PromptBlock prompt_block(const PromptArgs &a, int at, int *scan, int *found, uint32_t *status)
+// Where not all starts hold (rarely: out of line). By the whole CTA: of the sequences whose own starts hold, those that
+// begin before an earlier one do not hold either, so that no row is two sequences'; the sequences that hold as bits [32];
+// and zeros in the rows of the others that none of these has, those of this CTA's share.
+template <int D>
+static __device__ __noinline__ void prompt_sort_out(const PromptArgs &a, uint32_t *held, int head, bool clears)
+{
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int b = tid; b < 1024; b += MOE_PROMPT_THREADS) {  // (whole warps)
+        bool ok = b < a.batch && prompt_held(a, b);
+        for (int i = 0; i < b && ok; ++i)
+            ok = a.q_start[i] <= a.q_start[b];
+        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, ok);
+        if (lane == 0)
+            held[b >> 5] = bits;
+    }
+    __syncthreads();
+    constexpr int WARPS = MOE_PROMPT_THREADS / 32;
+    for (int r = blockIdx.y * WARPS + (tid >> 5); clears && r < a.q_tokens; r += gridDim.y * WARPS) {
+        bool other = false, own = false;
+        for (int b = lane; b < a.batch; b += 32)
+            if (a.q_start[b] <= r && r < a.q_start[b + 1])
+                (held[b >> 5] >> (b & 31) & 1 ? own : other) = true;
+        if (__any_sync(0xFFFFFFFFu, other) && !__any_sync(0xFFFFFFFFu, own))
+            for (int d = lane; d < D; d += 32)
+                a.out[(long long)r * a.o_tok + head * a.o_head + d] = 0;
+    }
+}
+
+// whole CTA: found [3], scan [33] and held [32] in shared memory; clears: whether it takes part in prompt_sort_out's zeros
+template <int D>
+__device__ __forceinline__ PromptBlock prompt_block(const PromptArgs &a, int at, int *scan, int *found, uint32_t *held,
+                                                    uint32_t *status, int head, bool clears)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = MOE_PROMPT_THREADS;
     if (tid == 0)
         found[0] = -1;
     const int per = (a.batch + nt - 1) / nt;
-    auto rows = [&](int b, int &q0) {  // rows of a sequence that lie in the call
-        q0 = max(a.q_start[b], 0);
-        return max(min(a.q_start[b + 1], a.q_tokens) - q0, 0);
-    };
-    int mine = 0, q0;
+    int mine = 0;
+    bool odd = false;
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         if (b >= a.batch)
             break;
-        mine += (rows(b, q0) + a.block - 1) / a.block;
-        if (blockIdx.x == 0 && blockIdx.y == 0 && !prompt_held(a, b))
+        if (prompt_held(a, b))
+            mine += (a.q_start[b + 1] - a.q_start[b] + a.block - 1) / a.block;
+        else
+            odd = true;
+    }
+    const bool all = !__syncthreads_or(odd);  // (then the starts do not fall)
+    auto holds = [&](int b) { return all || (held[b >> 5] >> (b & 31) & 1); };
+    if (!all) {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0)
             atomicOr(status, (uint32_t)MOE_WS_INDEX);
+        prompt_sort_out<D>(a, held, head, clears);
+        mine = 0;
+        for (int b = tid * per; b < min(tid * per + per, a.batch); ++b)
+            mine += holds(b) ? (a.q_start[b + 1] - a.q_start[b] + a.block - 1) / a.block : 0;
     }
     int incl = mine;
 #pragma unroll
@@ -137,11 +173,11 @@ __device__ __forceinline__ PromptBlock prompt_block(const PromptArgs &a, int at,
             const int b = tid * per + i;
             if (b >= a.batch)
                 break;
-            const int n = rows(b, q0), blocks = (n + a.block - 1) / a.block;
+            const int q0 = a.q_start[b], q1 = a.q_start[b + 1], blocks = holds(b) ? (q1 - q0 + a.block - 1) / a.block : 0;
             if (at < before + blocks) {
                 found[0] = b;
                 found[1] = q0 + (at - before) * a.block;
-                found[2] = q0 + n;
+                found[2] = q1;
                 break;
             }
             before += blocks;
@@ -151,14 +187,12 @@ __device__ __forceinline__ PromptBlock prompt_block(const PromptArgs &a, int at,
     const int b = found[0];
     if (b < 0)
         return r;
-    const int s0 = a.q_start[b], s1 = a.q_start[b + 1];
     r.k0 = a.kv_start[b];
     r.t = a.kv_start[b + 1] - r.k0;
-    r.n = s1 - s0;
+    r.n = found[2] - a.q_start[b];
     r.q0 = found[1];
     r.q1 = min(found[1] + a.block, found[2]);
-    r.row = r.q0 - s0;
-    r.held = prompt_held(a, b);
+    r.row = r.q0 - a.q_start[b];
     return r;
 }
 
@@ -247,6 +281,7 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 22);
     uint32_t *bad = tmem_slot + 1;  // [3][4] tokens of the tiles that are looked through with values that are not finite
     int *scan = reinterpret_cast<int *>(bad + 12), *found = scan + 33;
+    uint32_t *held = reinterpret_cast<uint32_t *>(found + 3);  // [32]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, split = a.split;
     const int head = blockIdx.x / split, part = blockIdx.x - head * split;  // (split CTAs are a cluster)
     uint32_t *status = a.status ? a.status : &prompt_unasked;
@@ -271,14 +306,9 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
         bad[tid] = 0;
     pdl_wait();  // before tensor memory is taken: the last kernel may still need it
     // (the last blocks first: a sequence's later rows see more)
-    PromptBlock b = prompt_block(a, gridDim.y - 1 - blockIdx.y, scan, found, status);
+    PromptBlock b = prompt_block<D>(a, gridDim.y - 1 - blockIdx.y, scan, found, held, status, head, part == 0);
     if (b.q1 <= b.q0)
         return;
-    if (!b.held) {
-        for (int i = tid; i < (b.q1 - b.q0) * D; i += MOE_PROMPT_THREADS)
-            a.out[(b.q0 + i / D) * a.o_tok + head * a.o_head + i % D] = 0;
-        return;
-    }
     const int rows = b.q1 - b.q0;
     // tokens that row i of the block sees, of this CTA's part of them
     int from = 0, len = b.t;
