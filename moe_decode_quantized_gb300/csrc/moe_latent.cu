@@ -425,7 +425,10 @@ int moe_latent_attention(const moe_latent_cache *cache, const void *q_dev, int64
     t.batch = batch;
     t.tokens = n_tokens;
     t.group = heads;
-    t.scale = scale;
+    // exponents of 2 are scores (of the scale's sign) times join_c; where the scale is too small for that, all alike
+    const float c = std::min(fabsf(scale) * 1.4426950408889634f, 3.0e38f);
+    t.scale = c == 0.0f ? 0.0f : scale;
+    t.join_c = c == 0.0f ? 1.0f : c;
     t.q_wide = wide_rows(q_dev, q_token_stride, q_head_stride);
     a.qr_wide = wide_rows(qr_dev, qr_token_stride, qr_head_stride);
     t.o_wide = wide_rows(out_dev, out_token_stride, out_head_stride);

@@ -417,11 +417,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
         const int row = tid & 63, half = tid >> 6, mine = (int)rank * 64 + row;
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         auto meet = [&]() { asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + (warp & 1)) : "memory"); };
-        const float sign = t.scale < 0.0f ? -1.0f : 1.0f;
-        const float scaled = fminf(fabsf(t.scale) * 1.4426950408889634f, 3.0e38f);
-        const bool flat = scaled == 0.0f;  // all scores alike
-        const float turn = flat ? 0.0f : sign;
-        const float c = flat ? 1.0f : scaled;
+        const float c = t.join_c, turn = t.scale == 0.0f ? 0.0f : t.scale < 0.0f ? -1.0f : 1.0f;
         bool ok = true;
         int item = 0, s = 0, phase = 0;  // s, phase: the tile's stage and its phase
         uint32_t seen = 0;  // by x, a bit each: parity of the tiles looked through
@@ -624,7 +620,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             if (lane == 0)
                 arrive_first(o_free);
             if (live && !whole && half == 0) {
-                part[ROWS * L + mine] = m * c;  // as an exponent of 2
+                part[ROWS * L + mine] = m;  // (not as an exponent: m c may pass f32 where differences times c need not)
                 part[ROWS * L + ROWS + mine] = l;
             }
             if (end == tiles && tid == 0 && rank == 0)
@@ -689,7 +685,7 @@ __global__ void __launch_bounds__(MOE_LTC_JOIN_THREADS) moe_latent_join_kernel(c
 #pragma unroll
         for (int i = 0; i < U; ++i)
             if (i0 + i <= c.runs) {
-                const float x = f[i] == -INFINITY ? 1.0f : ex2(f[i] - m);  // a NaN sum stays
+                const float x = f[i] == -INFINITY ? 1.0f : ex2((f[i] - m) * a.join_c);  // a NaN sum stays
                 l += w[i] * x;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {

@@ -388,6 +388,7 @@ int moe_tree_attention(const moe_kv_cache *cache, const void *q_dev, int64_t q_t
     a.tokens = n_tokens;
     a.group = n_q_heads / a.k.heads;
     a.scale = scale;
+    a.join_c = 1.0f;  // (references are kept as exponents: rows have multipliers of their own)
     a.q_wide = aligned(q_dev, 16) && (q_token_stride | q_head_stride) % 8 == 0;
     a.o_wide = aligned(out_dev, 16) && (out_token_stride | out_head_stride) % 8 == 0;
     a.min_units = 2 * MOE_TREE_WARPS;  // (a sequence of 511 tokens: 11.7 us, with twice that 13.0; of 8000: 15.7, 16.3)

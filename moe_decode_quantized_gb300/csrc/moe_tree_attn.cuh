@@ -66,6 +66,7 @@ struct TreeArgs {
     uint32_t *ctrl;
     TreeCut *cuts;     // [grid] the item that starts in the run and leaves it
     float *part;              // [grid][2] partials: [head size / 4][rows][4], then the rows' references, then sums
+    float join_c;             // what turns differences of the references into exponents of 2
     unsigned long long wait_ns;
 };
 
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(NT) moe_tree_join_kernel(const __grid_constant
 #pragma unroll
                 for (int x = 16; x; x /= 2)
                     m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-                auto factor = [&](float v) { return v == -INFINITY ? 1.0f : ex2(v - m); };  // a NaN sum stays
+                auto factor = [&](float v) { return v == -INFINITY ? 1.0f : ex2((v - m) * a.join_c); };  // a NaN sum stays
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
                     const float f = factor(v[j]);
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(NT) moe_tree_join_kernel(const __grid_constant
                     for (int x = tid; x < n * R; x += NT)
                         if (x % R < live) {
                             const float v = part(p0 + x / R)[rows * D + r0 + x % R];
-                            weight[x / R][x % R] = v == -INFINITY ? 1.0f : ex2(v - top[x % R]);
+                            weight[x / R][x % R] = v == -INFINITY ? 1.0f : ex2((v - top[x % R]) * a.join_c);
                         }
                     __syncthreads();
                 }

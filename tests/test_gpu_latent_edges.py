@@ -48,3 +48,59 @@ def test_prompt_query_starts_that_do_not_hold(starts, rows, heads, kv):
                                                           p.v[k0:k0 + t, cut].double().cpu(), sees, 0.1))
     out = p.out.cpu()
     assert (out[zero] == 0).all() and (out[~zero & ~some] == 9).all()
+
+
+# ------------------------------------------------------------------ absorbed form: scores that are exact in f32
+
+class Exact(base.Case):
+    """Queries and rows of multiples of 1/8 in eight dimensions, zeros in the queries' others: every product is a multiple of
+    1/64 and every sum is below 2^8, so that scores have no error in f32 in any order."""
+
+    def __init__(self, *a, **kw):
+        super().__init__(*a, **kw)
+        g = torch.Generator().manual_seed(1)
+        self.rows = [(torch.randint(-24, 25, r.shape, generator=g) / 8).bfloat16() for r in self.rows]
+        self.write()
+        self.q.zero_()
+        self.qr.zero_()
+        for x, n in ((self.q, 5), (self.qr, 3)):
+            x[..., :n] = (torch.randint(-24, 25, (*x.shape[:2], n), generator=g) / 8).to(x)
+
+    def check_exact(self, scale):
+        first = 0
+        for b, n in enumerate(self.sizes):
+            k = self.rows[b].double()
+            q = torch.cat([self.q[first:first + n], self.qr[first:first + n]], -1).double().cpu()
+            s = torch.einsum("nhd,td->nht", q, k).mul(math.copysign(1, scale)).masked_fill(~self.sees(b)[:, None], -math.inf)
+            p = torch.exp((s - s.amax(-1, keepdim=True)) * abs(scale))
+            p /= p.sum(-1, keepdim=True)
+            v = k[:, :self.latent]
+            o = p @ v
+            # exponents and exponentials in f32 2^-14 in all (an exponent that weighs is below 2^5: 2^-18 of it and less),
+            # weights rounded to bf16 and added up as rounded, sums 2^-14, one rounding to bf16
+            far = torch.einsum("nht,nhtd->nhd", p, (v - o[..., None, :]).abs())
+            bound = 1.01 * ref.BF16 * far + 2.0 ** -13 * (p @ v.abs())
+            bound = bound * (1 + ref.BF16) + ref.BF16 * o.abs() + 1e-30
+            assert (bound.mean() < 0.05 * o.abs().mean()), "a bound that zeros would pass"
+            base.near(self.out[first:first + n], o, bound)
+            first += n
+
+
+@pytest.mark.parametrize("scale", [30.0, -30.0, 2.0, 1e4, 1e36, -1e37, 3e38])
+@pytest.mark.parametrize("latent,heads,sizes,lens", [(512, 6, [1, 4], [517, 200]), (512, 16, [1], [3001]), (128, 3, [2, 1], [2500, 1]),
+                                                     (256, 128, [1], [700])])
+def test_scores_far_apart(latent, heads, sizes, lens, scale):
+    """Items that are cut into runs and joined, and items that are not: the same whatever the scale, although a score times
+    it passes what f32 holds."""
+    c = Exact(latent, 64, heads, 32, sizes, lens, seed=sum(lens))
+    c.run(scale)
+    c.check_exact(scale)
+    assert moe.read_status(c.ws) == 0
+
+
+@pytest.mark.parametrize("scale", [30.0, 1e36, -3e38])
+def test_scores_far_apart_of_many_runs(scale):
+    """Joined by the kernel that takes items of many parts."""
+    c = Exact(512, 64, 16, 64, [1], [40000], seed=3)
+    c.run(scale)
+    c.check_exact(scale)
