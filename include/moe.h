@@ -686,10 +686,12 @@ int moe_latent_read(const moe_latent_cache *cache, const int32_t *slots_dev, int
  *   out[i, h] = sum_j softmax_j(scale (q[i, h] . c_j + qr[i, h] . kr_j)) c_j,
  * q, out [n_tokens, heads, latent_dim], qr [n_tokens, heads, rope_dim] bf16 with
  * token and head strides in elements: q is the query times the keys'
- * up-projection, out goes through the values' one. A row that sees nothing gives
- * 0; a drafted token that no row of its sequence sees need not be in the cache,
- * and a NaN or infinity in a token's row reaches only query rows that see the token. bf16
- * products in f32 sums, the softmax in f32, its weights rounded to bf16 (2^-8)
+ * up-projection, out goes through the values' one. A row that sees nothing, or
+ * nothing but scores of -inf, gives 0; a drafted token that no row of its
+ * sequence sees need not be in the cache, and a NaN or infinity in a token's row
+ * reaches only query rows that see the token: all of the row where the token's
+ * score is NaN or +inf, and where it is -inf the token's dimensions that are not
+ * finite, as NaN. bf16 products in f32 sums, the softmax in f32, its weights rounded to bf16 (2^-8)
  * for the second product and added up as rounded. heads 1 .. 128, batch 0 ..
  * 1024. ws_dev: moe_latent_attention_workspace_bytes bytes, initialised once
  * (moe_workspace_init); moe_read_status gives MOE_WS_INDEX where lengths (the

@@ -162,6 +162,30 @@ __device__ __forceinline__ uint64_t mn128_desc(const void *tile, uint32_t next)
     return ((addr >> 4) & 0x3FFFull) | ((uint64_t)(next >> 4) << 16) | ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// NaN in the dimensions d .. d + n - 1 of a row's results in which a drafted token (of those after the sequence b's first
+// `prefix`) that the row sees (mask) holds a value that is not finite: in part, pieces of four `step` apart, or in out
+// (rarely needed: out of line)
+static __device__ __noinline__ void latent_odd(const LatentArgs &a, int b, int prefix, unsigned long long mask, int d, int n,
+                                               float *part, int step, uint16_t *out)
+{
+    const TreeArgs &t = a.t;
+    for (; mask; mask &= mask - 1) {
+        const int token = prefix + __ffsll((long long)mask) - 1, page = t.table[b * t.table_stride + token / t.k.page];
+        if (page < 0 || page >= t.n_pages)
+            continue;
+        const uint16_t *row = reinterpret_cast<const uint16_t *>(t.pages) +
+                              ((long long)page * t.k.page + token % t.k.page) * (t.k.dim + a.rope) + d;
+        for (int i = 0; i < n; ++i) {
+            if ((row[i] & 0x7F80u) != 0x7F80u)
+                continue;
+            if (part)
+                part[(size_t)(i / 4) * step + i % 4] = NAN;
+            else
+                out[i] = 0x7FFF;
+        }
+    }
+}
+
 template <int L>
 __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const __grid_constant__ LatentArgs a, const int stages)
 {
@@ -466,7 +490,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                                                          (it.n < 64 ? (1ull << it.n) - 1 : ~0ull);
             const int prefix = it.len - it.n;
             float m = -INFINITY, l = 0.0f;
-            bool fresh = true;
+            bool fresh = true, odd = false;  // odd: a token that it sees in a masked tile has a score of -inf
             for (; u < end; ++u) {
                 const int x = u & 1;
                 ok = ok && wait(s_full + s, phase);
@@ -489,8 +513,10 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                                                : 0u;
                     vis &= (out >> (2 * half) & 1 ? 0u : 0xFFFFu) | (out >> (2 * half + 1) & 1 ? 0u : 0xFFFF0000u);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
+                    for (int i = 0; i < 32; ++i) {
+                        odd |= vis >> i & 1 && v[i] == -INFINITY;
                         v[i] = vis >> i & 1 ? v[i] : -INFINITY;
+                    }
                 }
                 float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -552,7 +578,8 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                     ok = ok && (rank == 0 ? wait(v_full + s, phase) : wait(v_here + x, (int)(seen >> x & 1)));
                     seen ^= 1u << x;
                     // Values past the length are anything, and those of drafted tokens need not be numbers, which must not
-                    // reach rows that do not see them: zeros in their place (a row that sees one has a NaN among its scores)
+                    // reach rows that do not see them: zeros in their place. A row that sees one of them scores it NaN or
+                    // +inf, which makes the row NaN, or -inf, which is seen to at the item's end.
                     uint8_t *values = ring + (size_t)s * T::STAGE;
                     for (int i = tid; i < 64 * T::HALF * 8; i += MOE_LTC_SOFT * 32) {
                         const int token = i / (T::HALF * 8), piece = i % (T::HALF * 8);
@@ -585,13 +612,15 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 ask(following);
             }
             float *sums = top_of + (end & 1) * 128;  // (the maxima that the last tile has not used)
-            sums[half * 64 + row] = l;
+            sums[half * 64 + row] = odd ? -l : l;  // (sums are not negative)
             ok = ok && wait(pv_done + ((end - 1) & 1), (end - 1) >> 1);
             if (u < tiles)
                 there(item + 1);
             meet();
             __syncwarp();
-            l += sums[(half ^ 1) * 64 + row];
+            const float theirs = sums[(half ^ 1) * 64 + row];
+            odd |= __float_as_int(theirs) < 0;
+            l += fabsf(theirs);
             tc_fence_after();
             const bool whole = it.lo >= lo && it.lo + it.units <= hi;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -619,6 +648,9 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             __syncwarp();
             if (lane == 0)
                 arrive_first(o_free);
+            if (live && odd)  // a weight of 0 times a value that is not finite
+                latent_odd(a, it.b, prefix, mask, half * (L / 2), L / 2,
+                           whole ? nullptr : part + ((size_t)half * (L / 8) * ROWS + mine) * 4, 4 * ROWS, to);
             if (live && !whole && half == 0) {
                 part[ROWS * L + mine] = m;  // (not as an exponent: m c may pass f32 where differences times c need not)
                 part[ROWS * L + ROWS + mine] = l;

@@ -104,3 +104,45 @@ def test_scores_far_apart_of_many_runs(scale):
     c = Exact(512, 64, 16, 64, [1], [40000], seed=3)
     c.run(scale)
     c.check_exact(scale)
+
+
+# ------------------------------------------------------------------ absorbed form: infinities that are seen
+
+@pytest.mark.parametrize("what", [math.inf, -math.inf])
+@pytest.mark.parametrize("latent,heads,lens,scale", [(512, 20, [150, 40], 0.05), (512, 20, [150, 40], -0.05),
+                                                     (128, 3, [4000, 40], 0.05), (256, 70, [70, 6], 0.05)])
+@pytest.mark.parametrize("dims", [[100], [3, 127], [0, 64], "rope"])
+def test_infinities_of_drafted_tokens_that_a_row_sees(latent, heads, lens, scale, dims, what):
+    """A score of -inf is a weight of 0, and 0 times an infinity no number: in the token's dimensions that are infinite the
+    row is NaN, in the others as without the token. A score of +inf or NaN: all of the row."""
+    masks = [1, 3, 5, 9, 11]  # node 3 is seen by rows 3 and 4, node 1 by rows 1 and 4
+    c = base.Case(latent, 64, heads, 16, [5, 2], lens, masks + [1, 3], seed=8)
+    at = lens[0] - 5 + 3
+    place = [latent + 9] if dims == "rope" else dims
+    c.rows[0][at, place] = what
+    c.write()
+    c.run(scale)
+    q = torch.cat([c.q, c.qr], -1).double().cpu()
+    k, first = c.rows[0].double(), 0
+    score = scale * (q[:, :, place] * what).sum(-1)  # what is finite does not matter beside it
+    low = 0
+    for i in range(5):
+        sees = c.sees(0)[i:i + 1]
+        for h in range(heads):
+            got = c.out[i, h].double().cpu()
+            if sees[0, at] and score[i, h] != -math.inf:
+                assert torch.isnan(got).all()
+                continue
+            without = sees.clone()
+            without[0, at] = False
+            want, bound = ref.attention(q[i:i + 1, h:h + 1], k[:, None], k[:, None, :latent], without, scale)
+            want = want[0, 0]
+            if sees[0, at]:
+                low += 1
+                if dims != "rope":
+                    want[place] = math.nan
+                    assert torch.isnan(got[place]).all()
+            base.near(got, want, bound[0, 0])
+    assert low > 0 or heads < 20
+    q1, k1 = q[5:], c.rows[1].double()[:, None]
+    base.near(c.out[5:], *ref.attention(q1, k1, k1[..., :latent], c.sees(1), scale))
