@@ -317,6 +317,8 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 gone[u & 15] = out;
                 if (rank == 0)  // both CTAs' copies (the other's may come before this)
                     mbar_arrive_expect_tx(full + s, 2 * T::STAGE);
+                else  // no copies are counted here: it tells this CTA's softmax warps of `gone`
+                    mbar_arrive(full + s);
             }
             __syncwarp();
             const uint32_t bar = pair_bar(full + s, 0);
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             bool fresh = true, odd = false;  // odd: a token that it sees in a masked tile has a score of -inf
             for (; u < end; ++u) {
                 const int x = u & 1;
-                ok = ok && wait(s_full + s, phase);
+                ok = ok && wait(s_full + s, phase) && wait(full + s, phase);  // (the second has passed: `gone` is seen by it)
                 __syncwarp();
                 tc_fence_after();
                 const int first = (int)(lo + u - it.lo) * TOKENS;

@@ -146,3 +146,30 @@ def test_infinities_of_drafted_tokens_that_a_row_sees(latent, heads, lens, scale
     assert low > 0 or heads < 20
     q1, k1 = q[5:], c.rows[1].double()[:, None]
     base.near(c.out[5:], *ref.attention(q1, k1, k1[..., :latent], c.sees(1), scale))
+
+
+# ------------------------------------------------------------------ absorbed form: pages that are not there
+
+@pytest.mark.parametrize("latent,heads,page,sizes,lens", [(128, 20, 16, [1], [20000]), (512, 70, 16, [3, 1], [9000, 700]),
+                                                          (256, 128, 16, [1] * 4, [3000, 2000, 64, 16]), (128, 4, 48, [2], [30001])])
+def test_pages_that_are_not_there_in_every_tile(latent, heads, page, sizes, lens):
+    """Which of a tile's tokens are there differs from tile to tile: every tile takes its own."""
+    c = base.Case(latent, 64, heads, page, sizes, lens, seed=17)
+    for b, n in enumerate(lens):
+        pages = -(-n // page)
+        gone = torch.rand(pages, generator=torch.Generator().manual_seed(b)) < 0.4
+        c.table[b, :pages][gone.cuda()] = c.cache.n_pages + 5
+        c.rows[b] = torch.where(gone[torch.arange(n) // page, None], math.nan, c.rows[b])
+    c.run(0.05)
+    assert moe.read_status(c.ws) == moe.MOE_WS_INDEX
+    once = c.out.clone()
+    first = 0
+    for b, n in enumerate(sizes):
+        k = c.rows[b].double()[:, None]
+        sees = c.sees(b) & ~torch.isnan(c.rows[b][:, 0])
+        q = torch.cat([c.q[first:first + n], c.qr[first:first + n]], -1)[:, ::5].double().cpu()
+        base.near(c.out[first:first + n, ::5], *ref.attention(q, k, k[..., :latent], sees, 0.05))
+        first += n
+    for _ in range(50):
+        c.run(0.05)
+        assert torch.equal(c.out, once)
