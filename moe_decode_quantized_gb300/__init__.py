@@ -950,11 +950,13 @@ class PagePool:
     def ref(self):
         """The C struct by reference, made again after a field was set or the refs tensor got other memory."""
         refs = self.refs
+        if refs.dtype is not _runtime().i32:
+            raise ValueError(f"refs must be int32, not {refs.dtype}")
+        if not refs.is_contiguous():
+            raise ValueError("refs must be contiguous")
         at = (refs.data_ptr(), refs.numel(), self.page_size)
         kept = self.__dict__.get("_kept")
         if kept is None or kept[0] != at:
-            if refs.dtype is not _runtime().i32:
-                raise ValueError(f"refs must be int32, not {refs.dtype}")
             kept = self.__dict__["_kept"] = (at, C.byref(_lib.MoePagePool(_ptr(refs), at[1], at[2])))
         return kept[1]
 

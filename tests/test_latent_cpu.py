@@ -290,3 +290,17 @@ def test_the_binding_checks_what_it_is_given():
             (lambda: moe.pages_copy(z(2, 4, 32), i(2, 2), stream=0), "on the GPU")]:
         with pytest.raises(ValueError, match=text):
             call()
+
+
+def test_a_pool_looks_at_its_counts_at_each_call():
+    """Other tensors at the address and of the size that were taken before: refused as they would be at first."""
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    counts, table = i(200), torch.full((4, 8), -1, dtype=torch.int32)
+    pool = moe.PagePool(counts[:100], 16)
+    for refs, text in [(counts[:100], "on the GPU"), (counts[::2], "refs must be contiguous"), (counts[:100], "on the GPU"),
+                       (counts[:100].view(torch.float32), "refs must be int32"),
+                       (counts.view(torch.int16)[:100], "refs must be int32"), (counts[:99], "on the GPU")]:
+        pool.refs = refs
+        for call in (lambda: moe.pages_grow(pool, table, i(4), stream=0), lambda: moe.pages_free(pool, table, i(2), stream=0)):
+            with pytest.raises(ValueError, match=text):
+                call()
