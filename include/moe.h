@@ -631,7 +631,9 @@ int moe_rope_table(const moe_rope_cfg *cfg, uint64_t *table_host, float *magnitu
  * sign) and the pair (table_dev u64 [rope_dim / 2]):
  *   a' = magnitude (a cos t - b sin t), b' = magnitude (a sin t + b cos t);
  * transposed != 0: -t, the gradient's way back (with magnitude 1 also the
- * inverse). In f32, the angle's turn rounded once to 2^-32, results rounded once.
+ * inverse). In f32: the angle, from half a turn back to half a turn on, rounded
+ * to 2^-32 of a turn and then to f32 (an error of 2^-26 + 2^-33 of a turn at most,
+ * near half a turn; less with the angle), results rounded once.
  * Other dimensions are copied. out may be x with the same strides (in place:
  * other dimensions are not touched); it must not overlap x in another way.
  * head_dim 1 .. 1024, rope_dim even, 2 .. head_dim - offset. Rows that start on

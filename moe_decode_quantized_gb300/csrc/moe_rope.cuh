@@ -4,8 +4,10 @@
 // b' = m (a sin t + b cos t). The table holds f, the part of a turn a position
 // adds, times 2^64, so that p f modulo whole turns is the low half of one 64-bit
 // product: exact for every position, where a product in f32 would be off by
-// radians from position 10^6 on. The turn is rounded to 2^-32 and goes through
-// sincospif.
+// radians from position 10^6 on. The turn is rounded to 2^-32, then to f32 (by
+// 2^-26 at most, near half a turn), and goes through sincospif. (With whole quarter
+// turns taken off before, 2^-28 at most: 65536 rows written and read back 55.7 us
+// for 55.1.)
 //
 // A CTA takes a few tokens: the sines and cosines of its (token, pair)s once into
 // shared memory, then every head's rows, in pieces of 16 bytes where alignment

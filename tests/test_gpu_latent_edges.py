@@ -173,3 +173,30 @@ def test_pages_that_are_not_there_in_every_tile(latent, heads, page, sizes, lens
     for _ in range(50):
         c.run(0.05)
         assert torch.equal(c.out, once)
+
+
+# ------------------------------------------------------------------ rotary positions
+
+@pytest.mark.parametrize("layout", [moe.MOE_ROPE_HALF, moe.MOE_ROPE_INTERLEAVED])
+def test_angles_next_to_quarter_turns(layout):
+    """Small sines and cosines there are as near as documented: 2^-26 + 2^-33 of a turn for the angle's two roundings, and
+    sine and cosine within an ulp, 2^-23, which is doubled for this plain form."""
+    table, ints, _ = base.table_of(2)
+    f, found = ints[0], []
+    for p in range(1, 400000):
+        t = p * f % 2 ** 64
+        q = (t + 2 ** 61) >> 62
+        rest = t - (q << 62)
+        if 0 < abs(rest) < 2 ** 58:  # 1/64 of a turn
+            found.append((p if p % 3 else -p, q % 4, rest))
+    found = found[::7]
+    assert {q for _, q, _ in found} == {0, 1, 2, 3} and len(found) > 1000
+    x = torch.zeros((len(found), 1, 2), device="cuda")
+    x[..., 0] = 1.0
+    out = torch.empty_like(x)
+    moe.rope(x, out, i32([p for p, _, _ in found]), table, layout=layout)
+    for (c, s), (p, q, rest) in zip(out[:, 0].double().cpu().tolist(), found):
+        small = math.sin(2 * math.pi * (rest / 2.0 ** 64)) * (-1 if q > 1 else 1)
+        value = s if q % 2 == 0 else -c  # sine, -cosine, sine, -cosine from the nearest quarter turn
+        small = -small if p < 0 and q % 2 == 0 else small
+        assert abs(value - small) <= 2 * math.pi * (2.0 ** -26 + 2.0 ** -33) + abs(small) * 2.0 ** -22, (p, q, rest)
