@@ -272,7 +272,7 @@ int moe_rope(const void *x_dev, int64_t x_token_stride, int64_t x_head_stride, v
     // and 5.3)
     const long long per = (long long)a.heads_cta * a.items;
     a.tokens_cta = (int)std::max(1ll, std::min({2048 / per, tokens / 608ll, MOE_ROPE_SMEM / (4ll * rope_dim)}));
-    const dim3 grid((unsigned)((tokens + a.tokens_cta - 1) / a.tokens_cta),
+    const dim3 grid((unsigned)(((long long)tokens + a.tokens_cta - 1) / a.tokens_cta),
                     (unsigned)((heads + a.heads_cta - 1) / a.heads_cta));
     const RopeKernel kernel = f32 ? (wide ? rope_kernel<true, true>(inter) : rope_kernel<true, false>(inter))
                                   : (wide ? rope_kernel<false, true>(inter) : rope_kernel<false, false>(inter));

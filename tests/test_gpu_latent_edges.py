@@ -200,3 +200,20 @@ def test_angles_next_to_quarter_turns(layout):
         value = s if q % 2 == 0 else -c  # sine, -cosine, sine, -cosine from the nearest quarter turn
         small = -small if p < 0 and q % 2 == 0 else small
         assert abs(value - small) <= 2 * math.pi * (2.0 ** -26 + 2.0 ** -33) + abs(small) * 2.0 ** -22, (p, q, rest)
+
+
+def test_the_most_tokens():
+    """2^31 - 1 of one pair, in place: 26 GB with their positions."""
+    n = 2 ** 31 - 1
+    table, ints, _ = base.table_of(2)
+    x = torch.zeros((n, 1, 2), dtype=BF, device="cuda")
+    x[..., 0] = 1.0
+    positions = torch.arange(n, dtype=torch.int32, device="cuda")
+    moe.rope(x, x, positions, table)
+    for at in (0, 2047, 2048, n // 2, n - 2049, n - 1):
+        want = torch.zeros((1, 1, 2), dtype=torch.float64)
+        want[..., 0] = 1.0
+        base.near(x[at:at + 1], ref.turned(want, [at], ints, ref.HALF), ref.turned_bound(want, ref.HALF, 1.0, True))
+    for at in range(0, n, n // 4):  # everywhere a turn of length 1, by roundings of 2^-8 each
+        part = x[at:at + 10 ** 7].float()
+        assert (part.square().sum(-1) - 1).abs().max() < 4 * ref.BF16
