@@ -753,7 +753,7 @@ typedef struct {
 
 /* Gives each row a page for every entry from its first -1 on and below
  * ceil(len_dev[row] / page_size) (i32 [rows]; a row's pages come before its -1
- * entries, as these calls leave them). */
+ * entries, as these calls leave them). rows * table_pages below 2^31. */
 int moe_pages_grow(const moe_page_pool *pool, int32_t *table_dev, int64_t table_stride, int table_pages, int rows,
                    const int32_t *len_dev, uint32_t *status_dev, moe_stream_t stream);
 

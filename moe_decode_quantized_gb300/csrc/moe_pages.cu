@@ -50,6 +50,8 @@ int moe_pages_grow(const moe_page_pool *pool, int32_t *table_dev, int64_t table_
     const int rc = check_pool(pool, "moe_pages_grow", table_dev, table_stride, table_pages, rows, status_dev, a);
     if (rc || rows == 0)
         return rc;
+    if ((long long)rows * table_pages > 0x7FFFFFFFll)  // (the entries that lengths may ask for are counted in 32 bits)
+        return host_fail(MOE_EUNSUPPORTED, "moe_pages_grow: rows (%d) * table_pages (%d) < 2^31", rows, table_pages);
     if (!len_dev || !aligned(len_dev, 4))
         return host_fail(MOE_EINVAL, "moe_pages_grow: the lengths are NULL or not aligned to their type");
     a.len = len_dev;

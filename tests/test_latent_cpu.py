@@ -304,3 +304,12 @@ def test_a_pool_looks_at_its_counts_at_each_call():
         for call in (lambda: moe.pages_grow(pool, table, i(4), stream=0), lambda: moe.pages_free(pool, table, i(2), stream=0)):
             with pytest.raises(ValueError, match=text):
                 call()
+
+
+def test_grow_refuses_tables_whose_entries_pass_31_bits():
+    """Their sum over the rows is counted in 32 bits: a thousand rows of 2^21 entries asked for at once had got none."""
+    L = _lib.moe()
+    grow = lambda rows, pages: L.moe_pages_grow(_pool(), ADDR, 1 << 24, pages, rows, None, None, None)  # noqa: E731
+    _refused(grow(1024, 1 << 21), -2, "2^31")
+    _refused(grow(128, 1 << 24), -2, "2^31")
+    _refused(grow(1024, (1 << 21) - 1), -1, "lengths")  # (the next check)
