@@ -147,21 +147,57 @@ int prompt_map(CUtensorMap *m, const void *base, int64_t token_stride, int64_t h
     return host_map_bf16(m, base, 3, size, strides, boxes);
 }
 
-// shared memory of the kernel, asked for once a device
-int prompt_device()
+struct PromptDevice {
+    int sms = 0;
+    int clusters[2][4];  // [nope_dim 64, 128][i]: clusters of 2^i CTAs that run at once (i 1 to 3)
+};
+
+size_t prompt_shared(int nope_dim) { return (2 * (nope_dim / 64 + 1) + MOE_PROMPT_PLACES) * (size_t)MOE_PROMPT_PLACE + MOE_PROMPT_SMALL; }
+
+// the kernel's launch: clusters of `split` CTAs
+struct PromptLaunch {
+    cudaLaunchConfig_t lc{};
+    cudaLaunchAttribute at[2];
+    PromptLaunch(dim3 grid, int nope_dim, int split, moe_stream_t stream)
+    {
+        lc.gridDim = grid;
+        lc.blockDim = dim3(MOE_PROMPT_THREADS);
+        lc.dynamicSmemBytes = prompt_shared(nope_dim);
+        lc.stream = (cudaStream_t)stream;
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = split;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        lc.attrs = at;
+        lc.numAttrs = split > 1 ? 2 : 1;
+    }
+};
+
+// shared memory of the kernel, and what of it runs at once, asked for once a device
+int prompt_device(PromptDevice **out)
 {
-    static bool done[MOE_LATENT_MAX_DEVICES];
-    int d = 0, optin = 0;
+    static PromptDevice dev[MOE_LATENT_MAX_DEVICES];
+    int d = 0, optin = 0, sms = 0;
     MOE_CUDA_OK(cudaGetDevice(&d));
     if (d < 0 || d >= MOE_LATENT_MAX_DEVICES)
         return host_fail(MOE_EUNSUPPORTED, "device ordinal %d", d);
     std::lock_guard<std::mutex> lk(g_latent_mu);
-    if (!done[d]) {
+    PromptDevice &D = dev[d];
+    if (!D.sms) {
         MOE_CUDA_OK(cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, d));
-        MOE_CUDA_OK(cudaFuncSetAttribute(moe_prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
-        MOE_CUDA_OK(cudaFuncSetAttribute(moe_prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
-        done[d] = true;
+        MOE_CUDA_OK(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d));
+        for (int k = 0; k < 2; ++k) {
+            const auto kernel = k ? moe_prompt_kernel<128> : moe_prompt_kernel<64>;
+            MOE_CUDA_OK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin));
+            for (int i = 1; i < 4; ++i) {
+                PromptLaunch l(dim3(1u << i), 64 << k, 1 << i, nullptr);
+                MOE_CUDA_OK(cudaOccupancyMaxActiveClusters(&D.clusters[k][i], kernel, &l.lc));
+            }
+        }
+        D.sms = sms;
     }
+    *out = &D;
     return MOE_OK;
 }
 
@@ -550,34 +586,24 @@ int moe_latent_prompt_attention(const void *q_dev, int64_t q_token_stride, int64
     }
     if (a.q_wide && (rc = prompt_map(&a.queries, q_dev, q_token_stride, q_head_stride, q_tokens, heads, nope_dim + rope_dim, 128)))
         return rc;
-    if ((rc = prompt_device()))
+    PromptDevice *dev;
+    if ((rc = prompt_device(&dev)))
         return rc;
-    const size_t shared = (2 * (nope_dim / 64 + 1) + MOE_PROMPT_PLACES) * (size_t)MOE_PROMPT_PLACE + MOE_PROMPT_SMALL;
-    // Where blocks are few, clusters share each one's tokens, as many CTAs as run at once (128 rows of 4 heads after 30000
-    // tokens: 63 us, by a CTA a block 385; 512 of 32 after 16000: 139 and 252); but parts of two tiles at least, and of 6
+    // Where blocks are few, clusters share each one's tokens, as far as the clusters run at once (128 rows of 4 heads after 30000
+    // tokens: 63 us, by a CTA a block 385; 512 of 32 after 16000: 139 and 252; 128 of 19 after 8000 by clusters of 4: 39.5 us, by
+    // 19 of 8, some of which wait for others' end, 54); but parts of two tiles at least, and of 6
     // where a CTA to every 128 rows does instead (512 rows of 16 heads, no tokens before: 15 us, shared out 19; 2048 of 8: 34
     // and 30.5): so too where the SMs are enough for that alone (1024 rows of 16: 22 us, 26 with 256 a CTA).
     const long long blocks = (long long)heads * std::max((q_tokens + MOE_PROMPT_ROWS - 1) / MOE_PROMPT_ROWS, std::min(batch, q_tokens));
     const int least = (q_tokens <= (long long)batch * (MOE_PROMPT_ROWS / 2) ? 2 : 6) * MOE_PROMPT_TOKENS;
     a.split = 1;
-    while (blocks * a.split * 2 <= 152 && a.split * 2 <= std::min(MOE_PROMPT_SPLIT, nope_dim / 16) &&
-           kv_tokens >= (long long)batch * a.split * 2 * least)
+    for (int i = 1; a.split * 2 <= std::min(MOE_PROMPT_SPLIT, nope_dim / 16) && blocks <= dev->clusters[nope_dim / 128][i] &&
+                    kv_tokens >= (long long)batch * a.split * 2 * least;
+         ++i)
         a.split *= 2;
-    a.block = a.split == 1 && (long long)heads * ((q_tokens + 127) / 128) <= 152 ? MOE_PROMPT_ROWS / 2 : MOE_PROMPT_ROWS;
-    cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3((unsigned)(heads * a.split), (unsigned)(q_tokens / a.block + batch));
-    lc.blockDim = dim3(MOE_PROMPT_THREADS);
-    lc.dynamicSmemBytes = shared;
-    lc.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = a.split;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    lc.attrs = at;
-    lc.numAttrs = a.split > 1 ? 2 : 1;
-    MOE_CUDA_OK(cudaLaunchKernelEx(&lc, nope_dim == 64 ? moe_prompt_kernel<64> : moe_prompt_kernel<128>, a));
+    a.block = a.split == 1 && (long long)heads * ((q_tokens + 127) / 128) <= dev->sms ? MOE_PROMPT_ROWS / 2 : MOE_PROMPT_ROWS;
+    const PromptLaunch l(dim3((unsigned)(heads * a.split), (unsigned)(q_tokens / a.block + batch)), nope_dim, a.split, stream);
+    MOE_CUDA_OK(cudaLaunchKernelEx(&l.lc, nope_dim == 64 ? moe_prompt_kernel<64> : moe_prompt_kernel<128>, a));
     return MOE_OK;
 }
 

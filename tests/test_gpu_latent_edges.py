@@ -50,6 +50,39 @@ def test_prompt_query_starts_that_do_not_hold(starts, rows, heads, kv):
     assert (out[zero] == 0).all() and (out[~zero & ~some] == 9).all()
 
 
+# ------------------------------------------------------------------ expanded form: layouts in each plan
+
+@pytest.mark.parametrize("nope,rope", [(128, 64), (64, 40)])
+@pytest.mark.parametrize("heads,q,kv", [(3, [130, 40], [200, 40]),      # a CTA to every 128 rows
+                                        (52, [129, 131], [130, 128]),   # to every 256
+                                        (3, [140, 60], [2100, 1100]), (19, [100], [4000]), (37, [90], [3000])])  # clusters
+@pytest.mark.parametrize("layout", ["plain", "heads", "shared", "odd", "by 8"])
+def test_prompts_of_other_layouts_in_each_plan(nope, rope, heads, q, kv, layout):
+    """Results written 32 bytes at a time (plain, head-major), 16 (rows 8 values apart) and value by value (the others);
+    keys and values of all heads; queries that TMA does not take."""
+    p = base.Prompt(nope, rope, heads, q, kv, seed=heads + nope)
+    n = sum(q)
+    p.out = torch.full((n, heads, nope + (8 if layout == "by 8" else 5 if layout in ("shared", "odd") else 0)), 9.0, dtype=BF,
+                       device="cuda")
+    if layout == "heads":
+        p.q, p.k, p.v = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (p.q, p.k, p.v))
+        p.out = torch.empty((heads, n, nope), dtype=BF, device="cuda").transpose(0, 1)
+    elif layout == "shared":
+        p.k, p.v = (x[:, :1].contiguous().expand(-1, heads, -1) for x in (p.k, p.v))
+    elif layout == "odd":
+        big = torch.zeros((n, heads, nope + rope + 1), dtype=BF, device="cuda")
+        big[..., 1:] = p.q
+        p.q = big[..., 1:]
+    whole, p.out = p.out, p.out[..., :nope]
+    p.run(0.09)
+    if layout not in ("plain", "heads"):
+        assert (whole[..., nope:] == 9).all()
+    cut = slice(0, heads, max(1, heads // 4))
+    p.q, p.k, p.v, p.out = (x[:, cut] for x in (p.q, p.k, p.v, p.out))
+    p.heads = p.q.shape[1]
+    p.check(0.09)
+
+
 # ------------------------------------------------------------------ absorbed form: scores that are exact in f32
 
 class Exact(base.Case):
