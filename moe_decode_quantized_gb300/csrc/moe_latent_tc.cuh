@@ -162,6 +162,21 @@ __device__ __forceinline__ uint64_t mn128_desc(const void *tile, uint32_t next)
     return ((addr >> 4) & 0x3FFFull) | ((uint64_t)(next >> 4) << 16) | ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// The word at p once it is the tile's, which its upper 28 bits say. (Read before the wait for the tile's S, it mostly is. That
+// wait does not order it: in a pair's second CTA the barrier passes by way of the first. A wait for a barrier of the word's
+// own instead: latent vectors of 256 126 us for 121, of 128 115.4 for 112.7.)
+static __device__ __noinline__ uint32_t latent_gone(const uint32_t *p, uint32_t tile, uint32_t *status, unsigned long long wait_ns)
+{
+    const uint64_t t0 = globaltimer();
+    uint32_t v;
+    do
+        v = *reinterpret_cast<const volatile uint32_t *>(p);
+    while ((v ^ tile) >> 4 && globaltimer() - t0 <= wait_ns);
+    if ((v ^ tile) >> 4)
+        atomicOr(status, (uint32_t)MOE_WS_TIMEOUT);
+    return v;
+}
+
 // NaN in the dimensions d .. d + n - 1 of a row's results in which a drafted token (of those after the sequence b's first
 // `prefix`) that the row sees (mask) holds a value that is not finite: in part, pieces of four `step` apart, or in out
 // (rarely needed: out of line)
@@ -200,7 +215,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
     uint64_t *q_full = bars + 38, *o_free = bars + 40, *drained = bars + 41;             // q_full [2], by items; drained [4]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 45);
     float *top_of = reinterpret_cast<float *>(small + 384);  // [2][2][64]
-    uint32_t *gone = reinterpret_cast<uint32_t *>(top_of + 256);  // [16] 16-token groups of tile t that are not there, at t % 16
+    uint32_t *gone = reinterpret_cast<uint32_t *>(top_of + 256);  // [16] at t % 16: t, and tile t's 16-token groups that are not there
     long long *scan = reinterpret_cast<long long *>(gone + 16), *cum = scan + 32;  // cum [batch + 1]
     int *count = reinterpret_cast<int *>(scan + 20), *items = reinterpret_cast<int *>(cum + a.t.batch + 1);  // items [batch + 1]
     const TreeArgs &t = a.t;
@@ -227,6 +242,8 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             mbar_init(drained + i, 1);
         fence_barrier_init();
     }
+    if (tid < 16)
+        gone[tid] = ~0u;
     pdl_wait();  // before tensor memory is taken: the last kernel may still need it
     if (warp == 0)
         tmem2_alloc(tmem_slot, 512);
@@ -314,11 +331,9 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 break;
             uint8_t *to = ring + (size_t)s * T::STAGE;
             if (lane == 0) {
-                gone[u & 15] = out;
+                *reinterpret_cast<volatile uint32_t *>(gone + (u & 15)) = (uint32_t)u << 4 | out;
                 if (rank == 0)  // both CTAs' copies (the other's may come before this)
                     mbar_arrive_expect_tx(full + s, 2 * T::STAGE);
-                else  // no copies are counted here: it tells this CTA's softmax warps of `gone`
-                    mbar_arrive(full + s);
             }
             __syncwarp();
             const uint32_t bar = pair_bar(full + s, 0);
@@ -495,17 +510,22 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
             bool fresh = true, odd = false;  // odd: a token that it sees in a masked tile has a score of -inf
             for (; u < end; ++u) {
                 const int x = u & 1;
-                ok = ok && wait(s_full + s, phase) && wait(full + s, phase);  // (the second has passed: `gone` is seen by it)
+                uint32_t out = *reinterpret_cast<volatile uint32_t *>(gone + (u & 15));
+                ok = ok && wait(s_full + s, phase);
                 __syncwarp();
                 tc_fence_after();
                 const int first = (int)(lo + u - it.lo) * TOKENS;
-                const uint32_t out = *reinterpret_cast<volatile uint32_t *>(gone + (u & 15));
                 float v[32];
                 tmem_ld32(lanes + x * 32, v);
                 if (turn != 1.0f)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         v[i] *= turn;
+                if (ok && (out ^ (uint32_t)u << 4) >> 4) {
+                    out = latent_gone(gone + (u & 15), (uint32_t)u << 4, status, t.wait_ns);
+                    ok = (out ^ (uint32_t)u << 4) >> 4 == 0;
+                }
+                out &= 15u;
                 const bool masked = first + TOKENS > prefix || out;
                 if (masked) {
                     const int off = prefix - (first + half * 32);
