@@ -603,7 +603,11 @@ int moe_spec_verify(const void *logits_dev, int logits_type, int64_t logits_stri
  *   MOE_ROPE_PARTS   f_i (k + (1 - k) / factor), k = clamp((r - slow) / (fast -
  *                    slow), 0, 1) with r = original f_i / 2 pi the pair's turns
  *                    in `original` positions, and the magnitude 0.1 ln(factor) + 1
- *                    (else 1) for both results of a turn. */
+ *                    (else 1) for both results of a turn. The ramp is over a
+ *                    pair's turns. Code that ramps over its index i, between two
+ *                    whole indices, gives other frequencies to the pairs between
+ *                    them, and may use another magnitude: a caller that needs
+ *                    those fills the table and gives the magnitude itself. */
 #define MOE_ROPE_PLAIN 0
 #define MOE_ROPE_LINEAR 1
 #define MOE_ROPE_BASE 2
@@ -723,8 +727,9 @@ int moe_latent_attention(const moe_latent_cache *cache, const void *q_dev, int64
  * boundaries and have strides of multiples of 8, those of tokens positive, those
  * of heads positive or 0 (keys, values that all heads share). Rows that no
  * sequence has are not written. The order in which a row's products are added up
- * goes by heads, batch, q_tokens, kv_tokens and nope_dim, never by timing: the
- * same call gives the same bits, another batch around a sequence need not.
+ * goes by heads, batch, q_tokens, kv_tokens, nope_dim and the kind of GPU, never
+ * by timing: the same call gives the same bits, another batch around a sequence
+ * need not.
  * *status_dev receives MOE_WS_INDEX where a sequence's q_start or kv_start fall
  * or lie outside q_tokens or kv_tokens, or its q_start lies before an earlier
  * sequence's (its rows within q_tokens are 0, but those that are a sequence's
@@ -743,7 +748,8 @@ int moe_latent_prompt_attention(const void *q_dev, int64_t q_token_stride, int64
  * table_pages entries a row; -1: none). One pool and table serve the caches of
  * all layers. New pages are the lowest free ones, in order of rows and entries;
  * where none is left the entry stays -1 and MOE_WS_PAGES is set. An entry, row
- * or length outside its bounds is passed over and sets MOE_WS_INDEX. Calls on
+ * or length outside its bounds is passed over and sets MOE_WS_INDEX
+ * (moe_pages_grow does not look at the pages that a row holds). Calls on
  * one pool must be ordered. n_pages 1 .. 2^24, rows 1 .. 1024. */
 typedef struct {
     int32_t *refs;

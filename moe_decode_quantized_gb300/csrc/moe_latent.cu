@@ -593,7 +593,8 @@ int moe_latent_prompt_attention(const void *q_dev, int64_t q_token_stride, int64
     // tokens: 63 us, by a CTA a block 385; 512 of 32 after 16000: 139 and 252; 128 of 19 after 8000 by clusters of 4: 39.5 us, by
     // 19 of 8, some of which wait for others' end, 54); but parts of two tiles at least, and of 6
     // where a CTA to every 128 rows does instead (512 rows of 16 heads, no tokens before: 15 us, shared out 19; 2048 of 8: 34
-    // and 30.5): so too where the SMs are enough for that alone (1024 rows of 16: 22 us, 26 with 256 a CTA).
+    // and 30.5): so too where the SMs are enough for that alone (1024 rows of 16: 22 us, 26 with 256 a CTA). (How the rows
+    // are spread over the sequences is not known here: blocks that end short of 256 rows count for less than they are.)
     const long long blocks = (long long)heads * std::max((q_tokens + MOE_PROMPT_ROWS - 1) / MOE_PROMPT_ROWS, std::min(batch, q_tokens));
     const int least = (q_tokens <= (long long)batch * (MOE_PROMPT_ROWS / 2) ? 2 : 6) * MOE_PROMPT_TOKENS;
     a.split = 1;

@@ -22,11 +22,14 @@
 // bytes below that, by two launches' latency for one short sequence. One token of
 // 64 sequences over 4000 to 24000 tokens, latent vectors of 512: 128 heads 194 us
 // (139 at the copy rate, 117 at the products'), 16 heads 180 (5.2 TB/s: the tiles take as long, rows or not); 16
-// trees of 8 rows, 32 heads, over up to 16000: 78; one sequence of 511: 14.7. A
-// tile of 128 rows takes some 1900 clocks, of which its products need 1160: its
-// second product waits for its softmax, and two S beside O's columns are what
-// tensor memory has room for. Tiles of 64 tokens leave room for four stages,
-// which is what the copies' latency needs; 8 softmax warps gained nothing over 4.
+// trees of 8 rows, 32 heads, over up to 16000: 78; one sequence of 511: 14.0. A
+// tile of 128 rows takes some 1900 clocks, of which its products need 1160: there
+// is one buffer of P, so that a tile's softmax stores only when the product before
+// has read it, and that tile's product begins only then. The same chain bounds
+// latent vectors of 256 and 128 (64 heads 121 us, 76 at the copy rate; 32 heads
+// 112, 46), whatever their bytes. Of tensor memory's 512 columns O takes L / 2 and the two S
+// 64. Tiles of 64 tokens leave room for four stages at 512, which is what the
+// copies' latency needs; 8 softmax warps gained nothing over 4.
 #pragma once
 #include "moe_latent.cuh"
 #include "moe_tc.cuh"
@@ -579,6 +582,7 @@ __global__ void __launch_bounds__(MOE_LTC_THREADS, 1) moe_latent_tc_kernel(const
                 for (int i = 0; i < 32; i += 2) {
                     float e0, e1;
                     mul2(add2(F2(v[i], v[i + 1]), ref2), c2).get(e0, e1);
+                    // (bf16, by 2^-8 at most: the tensor core takes P only in the type of the values beside it)
                     const uint32_t p = pack_bf2(ex2(e0), ex2(e1));
                     w[i / 2] = p;
                     F2 &to = i & 2 ? sum1 : sum;

@@ -19,8 +19,10 @@
 // Where blocks are few, a cluster of CTAs shares one's tokens; their O, references
 // and sums meet in shared memory, each CTA adding up some dimensions, in order.
 //
-// Bound by products. 8192 tokens of 32 heads, 128 + 64 dimensions, causal: 494 us,
-// 1.39 PFLOP/s (74 % of the rate that was measured for large products). One warp issues all
+// Bound by products at 128 + 64 dimensions, and by the chain of an M tile's scores,
+// their softmax and the product with its weights at 64 + 64 (8192 tokens of 32
+// heads, causal: 494 us, 1.39 PFLOP/s, 74 % of the rate that was measured for large
+// products; and 430 to 455 us where products are 219). One warp issues all
 // products, in the order in which their operands come to be: by two, one an M
 // tile, 718 us, and 609 with turns between them. Heads vary fastest over the grid,
 // so that the CTAs that run together have rows of one length: with row blocks
@@ -577,6 +579,7 @@ __global__ void __launch_bounds__(MOE_PROMPT_THREADS, 1) moe_prompt_kernel(const
                     for (int i = 0; i < 32; i += 2) {
                         float e0, e1;
                         mul2(add2(F2(__uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1])), ref2), c2).get(e0, e1);
+                        // (bf16, by 2^-8 at most: the tensor core takes P only in the type of the values beside it)
                         const uint32_t p = pack_bf2(ex2(e0), ex2(e1));
                         F2 &to = i & 2 ? sum1 : sum;
                         to = add2(to, F2(bf16_lo(p), bf16_hi(p)));  // as rounded
