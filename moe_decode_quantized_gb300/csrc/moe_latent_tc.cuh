@@ -20,9 +20,9 @@
 //
 // Bound by products and by bytes nearly alike at 128 heads (242 FLOP a byte), by
 // bytes below that, by two launches' latency for one short sequence. One token of
-// 64 sequences over 4000 to 24000 tokens, latent vectors of 512: 128 heads 194 us
-// (139 at the copy rate, 117 at the products'), 16 heads 180 (5.2 TB/s: the tiles take as long, rows or not); 16
-// trees of 8 rows, 32 heads, over up to 16000: 78; one sequence of 511: 14.0. A
+// 64 sequences over 4000 to 24000 tokens, latent vectors of 512: 128 heads 191 us
+// (139 at the copy rate, 117 at the products'), 16 heads 177 (5.1 TB/s: the tiles take as long, rows or not); 16
+// trees of 8 rows, 32 heads, over up to 16000: 77; one sequence of 511: 14.0. A
 // tile of 128 rows takes some 1900 clocks, of which its products need 1160: there
 // is one buffer of P, so that a tile's softmax stores only when the product before
 // has read it, and that tile's product begins only then. The same chain bounds

@@ -21,7 +21,7 @@
 //
 // Bound by products at 128 + 64 dimensions, and by the chain of an M tile's scores,
 // their softmax and the product with its weights at 64 + 64 (8192 tokens of 32
-// heads, causal: 494 us, 1.39 PFLOP/s, 74 % of the rate that was measured for large
+// heads, causal: 491 us, 1.40 PFLOP/s, 74 % of the rate that was measured for large
 // products; and 430 to 455 us where products are 219). One warp issues all
 // products, in the order in which their operands come to be: by two, one an M
 // tile, 718 us, and 609 with turns between them. Heads vary fastest over the grid,
