@@ -785,7 +785,7 @@ int moe_pages_free(const moe_page_pool *pool, int32_t *table_dev, int64_t table_
  * refs_out_dev [n_pages] and table_out_dev (strides and rows as table) the pool's
  * counts and the table afterwards (they may be refs and table themselves). The
  * pages' contents are then moved by moe_pages_copy, for each cache. max_copies
- * n_pages / 2 at least. */
+ * n_pages / 2 at least, 2^30 at most. */
 int moe_pages_compact(const moe_page_pool *pool, const int32_t *table_dev, int64_t table_stride, int table_pages,
                       int rows, int32_t *refs_out_dev, int32_t *table_out_dev, int32_t *copies_dev, int max_copies,
                       int32_t *n_copies_dev, uint32_t *status_dev, moe_stream_t stream);
@@ -796,7 +796,7 @@ int moe_pages_compact(const moe_page_pool *pool, const int32_t *table_dev, int64
  * too. A negative pair is passed over; one outside the cache too, and sets
  * MOE_WS_INDEX. No page may be copied to twice, or be copied both from and to.
  * pages_dev, layer_stride (n_pages * page_bytes at least) and page_bytes multiples
- * of 16. */
+ * of 16; n 0 .. 2^30. */
 int moe_pages_copy(void *pages_dev, int64_t layer_stride, int layers, int64_t n_pages, int64_t page_bytes,
                    const int32_t *copies_dev, int n, const int32_t *n_copies_dev, uint32_t *status_dev,
                    moe_stream_t stream);

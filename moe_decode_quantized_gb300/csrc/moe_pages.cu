@@ -117,6 +117,8 @@ int moe_pages_compact(const moe_page_pool *pool, const int32_t *table_dev, int64
     if (max_copies < pool->n_pages / 2)
         return host_fail(MOE_EINVAL, "moe_pages_compact: max_copies (%d) must be n_pages / 2 (%lld) at least", max_copies,
                          (long long)pool->n_pages / 2);
+    if (max_copies > MOE_PAGES_MAX_COPIES)
+        return host_fail(MOE_EUNSUPPORTED, "moe_pages_compact: max_copies (%d) <= 2^30", max_copies);
     a.refs_out = refs_out_dev;
     a.table_out = table_out_dev;
     a.copies = copies_dev;
@@ -136,6 +138,8 @@ int moe_pages_copy(void *pages_dev, int64_t layer_stride, int layers, int64_t n_
     if (n < 0 || layers < 0 || n_pages < 1 || page_bytes < 1 || n_pages > 0x7FFFFFFF)
         return host_fail(MOE_EINVAL, "moe_pages_copy: n (%d) and layers (%d) must not be negative, n_pages (%lld) and "
                          "page_bytes (%lld) positive, n_pages below 2^31", n, layers, (long long)n_pages, (long long)page_bytes);
+    if (n > MOE_PAGES_MAX_COPIES)
+        return host_fail(MOE_EUNSUPPORTED, "moe_pages_copy: n (%d) <= 2^30", n);
     if (n == 0 || layers == 0)
         return MOE_OK;
     if (!pages_dev || !copies_dev)

@@ -16,6 +16,7 @@ namespace moe {
 
 #define MOE_PAGES_THREADS 1024
 #define MOE_PAGES_MAX_ROWS 1024
+#define MOE_PAGES_MAX_COPIES (1 << 30)          // pairs, whose numbers are counted in 31 bits
 #define MOE_PAGES_STEP (4 * MOE_PAGES_THREADS)  // counts of a step of the pass
 
 struct PagesArgs {

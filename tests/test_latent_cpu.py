@@ -313,3 +313,12 @@ def test_grow_refuses_tables_whose_entries_pass_31_bits():
     _refused(grow(1024, 1 << 21), -2, "2^31")
     _refused(grow(128, 1 << 24), -2, "2^31")
     _refused(grow(1024, (1 << 21) - 1), -1, "lengths")  # (the next check)
+
+
+def test_lists_of_copies_that_pass_31_bits_are_refused():
+    """A list's numbers are counted in 31 bits: of more than 2^30 pairs, those past them had been read and written before it."""
+    L = _lib.moe()
+    for n in (2 ** 30 + 1, 2 ** 31 - 1):
+        _refused(L.moe_pages_copy(ADDR, 1 << 20, 2, 4, 4096, ADDR, n, None, None, None), -2, "2^30")
+        _refused(L.moe_pages_compact(_pool(), ADDR, 8, 8, 4, ADDR, ADDR, ADDR, n, ADDR, None, None), -2, "2^30")
+    _refused(L.moe_pages_copy(None, 1 << 20, 2, 4, 4096, ADDR, 2 ** 30, None, None, None), -1, "NULL")  # (the next check)
