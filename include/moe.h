@@ -721,7 +721,8 @@ int moe_latent_attention(const moe_latent_cache *cache, const void *q_dev, int64
  * kr [kv_tokens, rope_dim], out [q_tokens, heads, nope_dim], all bf16, strides
  * in elements. A row that sees nothing gives 0 (a causal one of a sequence with
  * fewer tokens than rows); a NaN or infinity in a token that a row does not see
- * does not reach it. Products as for moe_latent_attention. nope_dim 64 or 128,
+ * does not reach it, and a row that sees an infinite value is infinite or NaN
+ * there, whatever its score. Products as for moe_latent_attention. nope_dim 64 or 128,
  * rope_dim a multiple of 8 from 8 to 64, heads 1 .. 1024, batch 0 .. 1024,
  * q_tokens up to 2^23, kv_tokens up to 2^30. k, kr and v must start on 16-byte
  * boundaries and have strides of multiples of 8, those of tokens positive, those

@@ -83,6 +83,34 @@ def test_prompts_of_other_layouts_in_each_plan(nope, rope, heads, q, kv, layout)
     p.check(0.09)
 
 
+# ------------------------------------------------------------------ expanded form: infinities that are seen
+
+@pytest.mark.parametrize("heads,q,kv", [(3, 130, 400), (52, 260, 390), (3, 140, 3100)])  # 128 rows a CTA, 256, clusters
+@pytest.mark.parametrize("back", [4, 135, 330])  # tokens from the end: of a tile that not all rows see, and not
+def test_infinities_of_tokens_that_a_row_sees(heads, q, kv, back):
+    """An infinite value whose token's score is -inf (a weight of 0), +inf or NaN: not finite in rows that see it. Rows that
+    do not are as without the token."""
+    p = base.Prompt(128, 64, heads, [q], [kv], seed=heads + back)
+    at = kv - back
+    p.kr[at, 7] = math.inf
+    p.v[at, :, 5] = -math.inf
+    p.run(0.09)
+    out, score = p.out.float().cpu(), p.q[:, :, 128 + 7].float().cpu() * math.inf
+    low = score == -math.inf
+    sees = torch.arange(kv - q, kv) >= at
+    assert not torch.isfinite(out[sees][..., 5]).any()
+    assert torch.isnan(out[sees][~low[sees]]).all()
+    others = [i for i in range(128) if i != 5]
+    assert torch.isfinite(out[sees][low[sees]][:, others]).all() and low[sees].any()
+    blind = (~sees).nonzero().flatten()[-3:]
+    cut = slice(0, heads, max(1, heads // 3))
+    if len(blind):
+        k = torch.cat([p.k, p.kr[:, None].expand(-1, heads, -1)], -1).double().cpu()
+        seen = torch.arange(kv) <= (kv - q + blind)[:, None]
+        base.near(p.out[blind.cuda()][:, cut], *ref.attention(p.q[blind.cuda()][:, cut].double().cpu(), k[:, cut],
+                                                              p.v[:, cut].double().cpu(), seen, 0.09))
+
+
 # ------------------------------------------------------------------ absorbed form: scores that are exact in f32
 
 class Exact(base.Case):
